@@ -76,6 +76,7 @@ typedef enum pa_dtype {
 #define PA_DEV_SMEM_ALIGN    128  /* pa_prefill: shared memory not 1024-byte aligned (nothing computed) */
 #define PA_DEV_RANGE         256  /* a value outside f16's finite range (|x| >= 65536, or infinite)
                                      reached an f16 operand; see the entry points that stage in f16 */
+#define PA_DEV_NO_BLOCKS     512  /* pa_plan_step: out of free blocks or token capacity */
 
 /* Human-readable name of a status. Never NULL. */
 const char *pa_status_string(pa_status status);
@@ -419,6 +420,156 @@ pa_status pa_prefill(void *out, const void *query, const void *key_cache, const 
                      int num_query_tokens, int max_query_len, float scale, pa_dtype dtype,
                      int window, void *workspace, size_t workspace_bytes, int32_t *device_status,
                      void *stream);
+
+/*
+ * The bookkeeping of one serving step on the GPU: what pa_bm_append_slots and
+ * pa_bm_fill_tables do for one token per sequence on the host, for any number
+ * of new tokens per sequence, from lengths that are already on the device
+ * ("PagedAttention por dentro", section "La tabla de páginas (block table)").
+ * Sequence b holds L_b = context_lens[b] tokens and brings T_b = new_lens[b].
+ *  block_tables      int32 [num_seqs][max_blocks_per_seq], in and out: entries
+ *                    of blocks that hold tokens are read; entries
+ *                    ceil(L_b / 16) .. ceil((L_b + T_b) / 16) - 1 are written
+ *  free_blocks       int32 [free_capacity], of which the first *num_free are
+ *                    free blocks, a stack: they are handed out from the end,
+ *                    sequence by sequence, a sequence's first new block first
+ *  num_free          device int32
+ *  context_lens_out  int32 [num_seqs]: L_b + T_b
+ *  query_start       int32 [num_seqs + 1]: where each sequence's tokens begin
+ *                    in the flat list (as pa_prefill takes it)
+ *  slot_mapping      int64 [token_capacity]: slot of every new token; -1 behind
+ *                    the last one (the cache writes skip those)
+ *  positions         int32 [token_capacity]: context position of every new
+ *                    token; 0 behind the last one
+ *  num_free_out      device int32: free blocks that are left (the first ones)
+ * Sequences are served in order.  The first one whose blocks or tokens do not
+ * fit and all after it bring nothing: their length stays, their query_start
+ * entries are the end of the list, and the call flags PA_DEV_NO_BLOCKS.  A
+ * sequence with a negative length or new length, or longer than its table, is
+ * passed over and flagged PA_DEV_BAD_CONTEXT_LEN.  *num_free outside
+ * [0, free_capacity] is clamped and flagged, a block id outside
+ * [0, num_blocks) gives slot -1; both flag PA_DEV_BAD_BLOCK_ID.
+ * Outputs may overlap neither inputs nor one another (PA_ERR_INVALID_ARG), so a
+ * captured step uses two sets of lengths and counts in turn.  Shared blocks are
+ * the host manager's business: a block about to be written is private.
+ * One kernel launch; all arrays are device memory.
+ */
+pa_status pa_plan_step(int32_t *block_tables, const int32_t *context_lens, const int32_t *new_lens,
+                       const int32_t *free_blocks, const int32_t *num_free,
+                       int32_t *context_lens_out, int32_t *query_start, int64_t *slot_mapping,
+                       int32_t *positions, int32_t *num_free_out, int num_seqs,
+                       int max_blocks_per_seq, int block_size, int num_blocks, int free_capacity,
+                       int token_capacity, int32_t *device_status, void *stream);
+
+/*
+ * Frequencies for rotary positions.  Pair i of rotary_dim / 2 turns by
+ * theta_i = base^(-2 i / rotary_dim) radians per position, changed for contexts
+ * longer than the trained ones by `scaling`:
+ *   PA_ROTARY_LINEAR    theta_i / factor (position interpolation)
+ *   PA_ROTARY_NTK       base * factor^(rotary_dim / (rotary_dim - 2)) as the base
+ *   PA_ROTARY_BY_PARTS  theta_i for pairs that turn more than beta_fast times
+ *                       over original_context positions, theta_i / factor for
+ *                       those that turn less than beta_slow times, a linear
+ *                       ramp between (YaRN, Peng et al. 2023); attention factor
+ *                       0.1 ln(factor) + 1 for a factor above 1
+ *  turns             host uint64 [rotary_dim / 2]: theta_i / (2 pi), as a
+ *                    64-bit fraction of a whole turn
+ *  attention_factor  host float: multiplies cos and sin (1 otherwise)
+ * Host only; no CUDA call.
+ */
+typedef enum pa_rotary_scaling {
+    PA_ROTARY_NONE = 0,
+    PA_ROTARY_LINEAR = 1,
+    PA_ROTARY_NTK = 2,
+    PA_ROTARY_BY_PARTS = 3
+} pa_rotary_scaling;
+pa_status pa_rotary_turns(uint64_t *turns, float *attention_factor, int rotary_dim, double base,
+                          pa_rotary_scaling scaling, double factor, double original_context,
+                          double beta_fast, double beta_slow);
+
+/*
+ * Rotary positions on the new tokens' queries and keys, and the cache write.
+ * Every token i's first rotary_dim elements of each query and key head are
+ * turned by its position's angles,
+ *   y0 = A (x0 cos - x1 sin), y1 = A (x1 cos + x0 sin),  A = attention_factor,
+ * where the pairs (x0, x1) are elements (j, j + rotary_dim / 2), or
+ * (2 j, 2 j + 1) when interleaved != 0; the rest is copied.  Queries go to
+ * query_out, keys and values to their slots.
+ *  query, key, value  device, dtype (f32 or bf16): head h of token i begins at
+ *                    i * stride + h * head_dim elements, so that slices of one
+ *                    projection output can be passed; 16-byte aligned, strides
+ *                    multiples of 16 bytes
+ *  query_out         as query; may be query itself (same stride).
+ *                    num_q_heads 0: keys and values only
+ *  positions         device int32 [num_tokens], any value
+ *  turns             device uint64 [rotary_dim / 2] (pa_rotary_turns).  The
+ *                    angle is the product modulo a whole turn in 64-bit
+ *                    integers: exact to 2^-32 of a turn at any position
+ *  rotary_dim        even, 0 .. head_dim (0: no rotation)
+ *  slot_mapping      device int64 [num_tokens]; negative = no cache write (the
+ *                    query is turned all the same); a slot past the pool is
+ *                    skipped and flagged PA_DEV_BAD_SLOT
+ *  cache_dtype       dtype: rows are stored as they are (k_scales and v_scales
+ *                    unused), or PA_DTYPE_FP8_E4M3: codes with one scale per
+ *                    block and KV head
+ *  k_scales, v_scales  device float [num_blocks][num_kv_heads], in and out
+ *  head_dim          at most 256; rows are whole 16-byte pieces
+ * Block scales.  A block's scale is the smallest power of two 2^e, e in
+ * [-32, 31], with amax <= 448 * 2^e over the rows written; the value of a code
+ * is code_value * scale.  When the lowest offset written in a block is above 0,
+ * the rows below it are the block's earlier tokens: the scale is then at least
+ * the old one, and if it grows those rows are re-encoded in place (exact apart
+ * from codes that become subnormal).  Writing a block's offset 0 starts it anew.
+ * Rows at or above the lowest written offset that are not written hold nothing.
+ * Codes round to nearest even; NaN stays NaN; a magnitude above 448 * 2^31
+ * saturates and the call flags PA_DEV_RANGE.
+ * The tokens of one block must lie within 32 consecutive entries of
+ * slot_mapping (chunks and decode steps in order do); a token of a block whose
+ * entries spread over 33 to 62 is dropped and flagged PA_DEV_BAD_SLOT, farther
+ * ones of one block race.  Of two tokens with one slot in a block-scaled pool
+ * the later one is stored, in other pools they race.
+ * Arithmetic: f32, rounded once.  One kernel launch.
+ */
+pa_status pa_rope_cache_write(void *query_out, const void *query, const void *key, const void *value,
+                              const int32_t *positions, const uint64_t *turns,
+                              float attention_factor, int rotary_dim, int interleaved,
+                              void *key_cache, void *value_cache, float *k_scales, float *v_scales,
+                              const int64_t *slot_mapping, int num_tokens, int num_q_heads,
+                              int num_kv_heads, int head_dim, int64_t query_out_stride,
+                              int64_t query_stride, int64_t key_stride, int64_t value_stride,
+                              int block_size, int num_blocks, pa_dtype dtype, pa_dtype cache_dtype,
+                              int32_t *device_status, void *stream);
+
+/*
+ * Paged decode attention over E4M3 pools with one scale per block and KV head
+ * ("KV cache: la memoria de trabajo que sostiene la inferencia LLM", section
+ * "Trucos para que el cuaderno sea más fino"), as pa_rope_cache_write fills
+ * them: the value of a code is code_value * scale of its block and KV head.
+ *  k_scales, v_scales  device float [num_blocks][num_kv_heads], 4-byte aligned.
+ *                    Any finite key scale; value scales lie in [2^-32, 2^31]
+ *                    (others are clamped and flagged PA_DEV_RANGE)
+ *  window            0 = the whole context; W > 0: the last W positions, as in
+ *                    pa_decode_sliding_window
+ *  workspace         at least pa_decode_block_fp8_workspace_bytes(...) bytes
+ * Everything else is as in pa_decode_fp8.  Supported: head_dim 128, any group
+ * (one of more than 8 query heads is split into parts of its largest divisor up
+ * to 8, which read the same tiles).
+ * Arithmetic: codes are widened exactly; the query is rounded to f16 once (as
+ * in pa_decode_fp8, with PA_DEV_RANGE); a value scale enters the exponent of
+ * its tokens' weights, which are rounded to f16 relative to the largest of
+ * them; sums are fp32.
+ */
+size_t pa_decode_block_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
+                                           int head_dim, int max_blocks_per_seq, int block_size,
+                                           int window, int partition_size);
+pa_status pa_decode_block_fp8(void *out, const void *query, const void *key_cache,
+                              const void *value_cache, const float *k_scales,
+                              const float *v_scales, const int32_t *block_tables,
+                              const int32_t *context_lens, int num_seqs, int num_q_heads,
+                              int num_kv_heads, int head_dim, int block_size,
+                              int max_blocks_per_seq, int num_blocks, float scale, int window,
+                              int partition_size, void *workspace, size_t workspace_bytes,
+                              int32_t *device_status, void *stream);
 
 /*
  * Swap of blocks between the pools and a staging buffer ("PagedAttention por

@@ -21,6 +21,7 @@ i32 = ctypes.c_int
 i64 = ctypes.c_int64
 u64 = ctypes.c_uint64
 f32 = ctypes.c_float
+f64 = ctypes.c_double
 sz = ctypes.c_size_t
 ptr_i32 = ctypes.POINTER(ctypes.c_int32)
 ptr_i64 = ctypes.POINTER(ctypes.c_int64)
@@ -54,6 +55,14 @@ SIGNATURES = {
     "pa_prefill_workspace_bytes": (sz, []),
     "pa_prefill": (i32, [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32,
                          f32, i32, i32, vp, sz, vp, vp]),
+    "pa_plan_step": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp,
+                           vp]),
+    "pa_rotary_turns": (i32, [vp, vp, i32, f64, i32, f64, f64, f64, f64]),
+    "pa_rope_cache_write": (i32, [vp, vp, vp, vp, vp, vp, f32, i32, i32, vp, vp, vp, vp, vp, i32, i32,
+                                  i32, i32, i64, i64, i64, i64, i32, i32, i32, i32, vp, vp]),
+    "pa_decode_block_fp8_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32, i32, i32]),
+    "pa_decode_block_fp8": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32,
+                                  f32, i32, i32, vp, sz, vp, vp]),
     "pa_swap_bytes": (sz, [i32, i32, i32, i32]),
     "pa_swap_out": (i32, [vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, vp, vp]),
     "pa_swap_in": (i32, [vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, vp, vp]),
@@ -111,6 +120,9 @@ PA_DEV_PREFIX_MISMATCH = 32
 PA_DEV_BAD_QUERY_LEN = 64
 PA_DEV_SMEM_ALIGN = 128
 PA_DEV_RANGE = 256
+PA_DEV_NO_BLOCKS = 512
+
+PA_ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 
 
 class PagedKVError(RuntimeError):

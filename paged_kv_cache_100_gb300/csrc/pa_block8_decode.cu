@@ -1,0 +1,597 @@
+// Paged decode attention over E4M3 pools with one scale per block of 16 tokens
+// and KV head ("KV cache: la memoria de trabajo que sostiene la inferencia LLM",
+// section "Trucos para que el cuaderno sea más fino": quantising the cache), one
+// query token per sequence.  The mathematics of the scales is in pa_block8.cuh.
+//
+// One CTA handles one (sequence, KV head, partition).  Each warp owns every
+// NW-th block of the partition and streams it through its own ring of STAGES
+// slots: a block's K and V tiles are 16 rows x 128 codes = 2 KiB each, one TMA
+// box (128-byte swizzle).  The group's query heads are the N columns of
+// mma.sync m16n8k16 tiles in transposed form, S^T[16 tokens x 8 heads] = K Q^T
+// and O^T[128 x 8 heads] += V^T P^T, so one pass over K/V serves the group; a
+// group of more than 8 heads is split over CTAs that follow one another and
+// find the tiles in L2.  Codes widen to f16 exactly.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "pa_block8.cuh"
+#include "pa_device.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+namespace {
+
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kD = 128;
+constexpr int kTileBytes = kBlockSize * kD;      // codes of one block of one KV head
+constexpr int kStageBytes = 2 * kTileBytes;      // K and V
+constexpr int kHeads = 8;                        // query heads of a CTA at most
+// a head's reference maximum moves only when a block exceeds it by more than
+// 2^8: the weights stay in [0, 256], which f16 holds
+constexpr float kLazyLog2 = 8.f;
+
+struct Block8Args {
+    void *out;
+    const void *query;
+    const int32_t *block_tables;
+    const int32_t *context_lens;
+    const float *k_scales;       // [num_blocks][num_kv_heads]
+    const float *v_scales;
+    float *part_o;               // [(b * Hq + h) * max_parts + part][128]
+    float2 *part_ml;             // (reference, sum)
+    int32_t *status;
+    int num_seqs, num_q_heads, num_kv_heads;
+    int heads;                   // query heads of a CTA
+    int splits;                  // CTAs of a (sequence, KV head, partition)
+    int max_blocks, num_blocks;
+    int part_blocks, max_parts;
+    int window;
+    float scale_log2;
+};
+
+// A block of the partition as the warps read it: where its tiles are, and its scales.
+struct __align__(16) Entry {
+    int row;                     // first pool row of the block's tile of this KV head
+    float ck;                    // key scale * softmax scale * log2(e)
+    float lv;                    // log2 of the value scale
+    float rv;                    // 1 / value scale
+};
+
+struct Span {
+    int L, start, blk0, nblk, nparts;
+};
+
+// Partition `part` of a context of `len` tokens; false when it lies past the end.
+__device__ __forceinline__ bool span_of(const Block8Args &a, int len, int part, bool say, Span &w) {
+    const int lmax = a.max_blocks * kBlockSize;
+    if (len < 0 || len > lmax) {
+        if (say) report(a.status, PA_DEV_BAD_CONTEXT_LEN);
+        len = len < 0 ? 0 : lmax;
+    }
+    w.L = len;
+    w.start = a.window > 0 && len > a.window ? len - a.window : 0;
+    const int first = w.start / kBlockSize, blocks = (len + kBlockSize - 1) / kBlockSize;
+    w.nparts = blocks <= first ? 1 : (blocks - first + a.part_blocks - 1) / a.part_blocks;
+    if (part >= w.nparts) return false;
+    w.blk0 = first + part * a.part_blocks;
+    w.nblk = max(min(w.blk0 + a.part_blocks, blocks) - w.blk0, 0);
+    return true;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+// byte offset of code `col` of tile row `row` (128-byte swizzle)
+__device__ __forceinline__ uint32_t code_at(int row, int col) {
+    return (uint32_t)(row * 128 + (((col >> 4) ^ (row & 7)) << 4) + (col & 15));
+}
+
+// One warp's attention state over its blocks: 8 query heads (columns; those
+// past the group have a zero query and are not stored).  Lane (g, t) = (lane /
+// 4, lane % 4) holds scores of tokens g and g + 8 for heads 2t and 2t + 1.
+//  * S^T: the contraction may visit the head dimension in any order as long as
+//    K and Q agree, so a lane reads 8 consecutive codes of rows g and g + 8 and
+//    the query's fragments are laid out to match.
+//  * O^T: the A operand needs two tokens of one head-dim element in a register,
+//    so a lane reads 4 codes of rows 2t, 2t + 1, 2t + 8, 2t + 9 and pairs them
+//    with byte permutes; m-tile 2c + j holds elements 32c + 4g + 2j (row g) and
+//    + 1 (row g + 8).
+struct Warp8 {
+    uint32_t qb[8][2];
+    float o[8][4];
+    float m0, m1, l0, l1;
+    int lane, g, t;
+    uint32_t koff[4], voff_a[4], voff_b[4];
+
+    __device__ __forceinline__ void init(const Block8Args &a, int b, int first_head, int lane_) {
+        lane = lane_;
+        g = lane >> 2;
+        t = lane & 3;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            koff[c] = code_at(g, 32 * c + 8 * t);
+            voff_a[c] = code_at(2 * t, 32 * c + 4 * g);
+            voff_b[c] = code_at(2 * t + 1, 32 * c + 4 * g);
+        }
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(
+            static_cast<const __nv_bfloat16 *>(a.query) + ((int64_t)b * a.num_q_heads + first_head + g) * kD);
+        const bool real = g < a.heads;
+        bool beyond = false;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int d = 32 * (k >> 1) + 8 * t + 4 * (k & 1);
+            const uint32_t w0 = real ? q[d / 2] : 0u, w1 = real ? q[d / 2 + 1] : 0u;
+            qb[k][0] = pack_f16x2(bf16lo(w0), bf16hi(w0));
+            qb[k][1] = pack_f16x2(bf16lo(w1), bf16hi(w1));
+            beyond |= bf16x2_beyond_f16(w0) | bf16x2_beyond_f16(w1);
+        }
+        if (beyond) report(a.status, PA_DEV_RANGE);      // the f16 query is not the query
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        m0 = m1 = -INFINITY;
+        l0 = l1 = 0.f;
+    }
+
+    // One block, of which the rows [nlo, nvalid) are attended (at least one).
+    __device__ __forceinline__ void block(uint32_t ktile, uint32_t vtile, int nlo, int nvalid, const Entry &e) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint2 r0 = lds64(ktile + koff[c]);
+            const uint2 r1 = lds64(ktile + koff[c] + 1024);      // row g + 8: same swizzle phase
+            uint32_t x[4];
+            e4m3x4_to_f16x2x2(r0.x, x[0], x[2]);
+            e4m3x4_to_f16x2x2(r1.x, x[1], x[3]);
+            mma_f16_16816(s, x, qb[2 * c][0], qb[2 * c][1]);
+            e4m3x4_to_f16x2x2(r0.y, x[0], x[2]);
+            e4m3x4_to_f16x2x2(r1.y, x[1], x[3]);
+            mma_f16_16816(s, x, qb[2 * c + 1][0], qb[2 * c + 1][1]);
+        }
+        const bool v0 = g >= nlo && g < nvalid, v1 = g + 8 >= nlo && g + 8 < nvalid;
+        s[0] = v0 ? fmaf(s[0], e.ck, e.lv) : -INFINITY;
+        s[1] = v0 ? fmaf(s[1], e.ck, e.lv) : -INFINITY;
+        s[2] = v1 ? fmaf(s[2], e.ck, e.lv) : -INFINITY;
+        s[3] = v1 ? fmaf(s[3], e.ck, e.lv) : -INFINITY;
+        float mx0 = fmaxf(s[0], s[2]), mx1 = fmaxf(s[1], s[3]);
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, k));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, k));
+        }
+        const bool need0 = mx0 > m0 + kLazyLog2, need1 = mx1 > m1 + kLazyLog2;
+        if (__any_sync(kFull, need0 || need1)) {
+            const float a0 = need0 ? exp2f(m0 - mx0) : 1.f;      // 0 while m0 is -inf
+            const float a1 = need1 ? exp2f(m1 - mx1) : 1.f;
+            m0 = need0 ? mx0 : m0;
+            m1 = need1 ? mx1 : m1;
+            l0 *= a0;
+            l1 *= a1;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                o[i][0] *= a0;
+                o[i][1] *= a1;
+                o[i][2] *= a0;
+                o[i][3] *= a1;
+            }
+        }
+        const float w0 = ex2_fast(s[0] - m0), w1 = ex2_fast(s[1] - m1);
+        const float w2 = ex2_fast(s[2] - m0), w3 = ex2_fast(s[3] - m1);
+        l0 = fmaf(w0 + w2, e.rv, l0);
+        l1 = fmaf(w1 + w3, e.rv, l1);
+        // the weights enter the second product as f16, rounded once: 11 bits
+        // move an output by at most 2^-11 of the largest value it weighs, where
+        // bf16's 8 bits would be as coarse as the output's own rounding
+        const uint32_t b0 = movmatrix_trans(pack_f16x2(w0, w1));
+        const uint32_t b1 = movmatrix_trans(pack_f16x2(w2, w3));
+        if (nlo > 0 || nvalid < kBlockSize) zero_rows(vtile, nlo, nvalid);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t wa = lds32(vtile + voff_a[c]), wb = lds32(vtile + voff_b[c]);
+            const uint32_t wc = lds32(vtile + voff_a[c] + 1024), wd = lds32(vtile + voff_b[c] + 1024);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t sel = j == 0 ? 0x5140u : 0x7362u;
+                uint32_t x[4];
+                e4m3x4_to_f16x2x2(__byte_perm(wa, wb, sel), x[0], x[1]);     // tokens 2t, 2t + 1
+                e4m3x4_to_f16x2x2(__byte_perm(wc, wd, sel), x[2], x[3]);     // tokens 2t + 8, 2t + 9
+                mma_f16_16816(o[2 * c + j], x, b0, b1);
+            }
+        }
+    }
+
+    // Rows that are not attended may hold any code, NaN among them, and would
+    // reach the sum as 0 * NaN.
+    __device__ __forceinline__ void zero_rows(uint32_t tile, int nlo, int nvalid) {
+        for (int i = lane; i < (kBlockSize - (nvalid - nlo)) * 8; i += 32) {
+            int r = i / 8;
+            r = r < nlo ? r : r - nlo + nvalid;
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(tile + (uint32_t)(r * 128 + (i % 8) * 16)),
+                         "r"(0u)
+                         : "memory");
+        }
+        __syncwarp();
+    }
+
+    // The state as acc[heads][128], m[heads], l[heads].
+    __device__ __forceinline__ void finish(int heads, float *acc, float *m, float *l) {
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) {
+            l0 += __shfl_xor_sync(kFull, l0, k);
+            l1 += __shfl_xor_sync(kFull, l1, k);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int h = 2 * t + e;
+            if (h >= heads) continue;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<float2 *>(acc + h * kD + 32 * (i >> 1) + 4 * g + 2 * (i & 1)) =
+                    make_float2(o[i][e], o[i][2 + e]);
+            if (g == 0) {
+                m[h] = e ? m1 : m0;
+                l[h] = e ? l1 : l0;
+            }
+        }
+    }
+};
+
+template <int NW, int STAGES>
+struct Shape {
+    static constexpr int kRing = NW * STAGES * kStageBytes;
+    static_assert(STAGES * kStageBytes >= kHeads * kD * 4, "a warp's state is merged over its ring");
+    static size_t smem(int part_blocks) {
+        return 1024 + kRing + (size_t)part_blocks * sizeof(Entry) + NW * STAGES * 8 + 2 * NW * kHeads * sizeof(float);
+    }
+};
+
+template <int NW, int STAGES>
+__global__ void __launch_bounds__(NW * 32)
+    pa_decode_block8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                            const Block8Args a) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // CTAs go partition by partition, so that the shorter last partitions (and
+    // the empty ones of short sequences) end the grid
+    const int axis = a.num_kv_heads * a.splits;
+    int idx = blockIdx.x;
+    const int part = idx / (a.num_seqs * axis);
+    idx -= part * a.num_seqs * axis;
+    const int b = idx / axis;
+    idx -= b * axis;
+    const int kvh = idx / a.splits;
+    const int first_head = kvh * a.heads * a.splits + (idx - kvh * a.splits) * a.heads;
+    Span w;
+    if (!span_of(a, a.context_lens[b], part, threadIdx.x == 0 && part == 0 && idx == 0, w)) return;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Entry *entries = reinterpret_cast<Entry *>(ring + Shape<NW, STAGES>::kRing);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(entries + a.part_blocks);
+    float *s_m = reinterpret_cast<float *>(bars + NW * STAGES);
+    float *s_l = s_m + NW * kHeads;
+    __shared__ int s_fail;
+    if (threadIdx.x == 0) {
+        s_fail = 0;
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+    }
+    const int32_t *table = a.block_tables + (int64_t)b * a.max_blocks + w.blk0;
+    for (int i = threadIdx.x; i < w.nblk; i += NW * 32) {
+        int phys = table[i];
+        if ((unsigned)phys >= (unsigned)a.num_blocks) {
+            report(a.status, PA_DEV_BAD_BLOCK_ID);
+            phys = 0;
+        }
+        const int64_t at = (int64_t)phys * a.num_kv_heads + kvh;
+        const float sv = value_scale(a.v_scales[at], a.status);
+        entries[i] = Entry{(int)(at * kBlockSize), a.k_scales[at] * a.scale_log2, log2_scale(sv), 1.f / sv};
+    }
+    uint64_t *my_bars = bars + warp * STAGES;
+    uint8_t *my_ring = ring + warp * STAGES * kStageBytes;
+    if (lane == 0) {
+#pragma unroll
+        for (int s = 0; s < STAGES; ++s) mbar_init(&my_bars[s], 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    Warp8 state;
+    state.init(a, b, first_head, lane);
+
+    const int count = w.nblk > warp ? (w.nblk - warp + NW - 1) / NW : 0;
+    const uint64_t policy = l2_policy_evict_first();     // tiles are read once: they leave L2 first
+    auto issue = [&](int it) {
+        const int s = it % STAGES;
+        const int row = entries[warp + it * NW].row;
+        uint8_t *kt = my_ring + s * kStageBytes;
+        mbar_arrive_expect_tx(&my_bars[s], kStageBytes);
+        tma_load_2d_hint(kt, &kmap, 0, row, &my_bars[s], policy);
+        tma_load_2d_hint(kt + kTileBytes, &vmap, 0, row, &my_bars[s], policy);
+    };
+    if (lane == 0)
+        for (int it = 0; it < STAGES && it < count; ++it) issue(it);
+    bool ok = true;
+    int it = 0;
+    for (; it < count; ++it) {
+        const int s = it % STAGES;
+        if (!__all_sync(kFull, mbar_wait_bounded(&my_bars[s], (it / STAGES) & 1))) {
+            ok = false;
+            break;
+        }
+        const int tok = (w.blk0 + warp + it * NW) * kBlockSize;
+        const uint32_t kt = smem_u32(my_ring + s * kStageBytes);
+        state.block(kt, kt + kTileBytes, max(0, w.start - tok), min(kBlockSize, w.L - tok), entries[warp + it * NW]);
+        __syncwarp();
+        if (lane == 0 && it + STAGES < count) {
+            fence_proxy_async_smem();
+            issue(it + STAGES);
+        }
+    }
+    if (!ok) {
+        // copies in flight get a bounded chance to land before the memory is given up
+        for (int k = it; k < count && k < it + STAGES; ++k)
+            (void)mbar_wait_bounded(&my_bars[k % STAGES], (k / STAGES) & 1);
+        if (lane == 0) {
+            report(a.status, PA_DEV_TIMEOUT);
+            s_fail = 1;
+        }
+    }
+    // the ring is idle: the warps' states are merged over it
+    float *acc = reinterpret_cast<float *>(my_ring);
+    state.finish(a.heads, acc, s_m + warp * kHeads, s_l + warp * kHeads);
+    __syncthreads();
+    if (s_fail) return;
+    const bool whole = w.nparts == 1;
+    for (int i = threadIdx.x; i < a.heads * kD; i += NW * 32) {
+        const int h = i / kD, d = i % kD;
+        float M = -INFINITY, O = 0.f, sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) M = fmaxf(M, s_m[k * kHeads + h]);
+#pragma unroll
+        for (int k = 0; k < NW; ++k) {
+            const float mk = s_m[k * kHeads + h];
+            const float f = mk == -INFINITY ? 0.f : exp2f(mk - M);
+            sum = fmaf(f, s_l[k * kHeads + h], sum);
+            O = fmaf(f, reinterpret_cast<const float *>(ring + k * STAGES * kStageBytes)[i], O);
+        }
+        const int64_t head = (int64_t)b * a.num_q_heads + first_head + h;
+        if (whole) {
+            // a NaN sum stays NaN; an empty context gives zeros
+            static_cast<__nv_bfloat16 *>(a.out)[head * kD + d] = __float2bfloat16_rn(sum == 0.f ? 0.f : O / sum);
+        } else {
+            const int64_t row = head * a.max_parts + part;
+            a.part_o[row * kD + d] = O;
+            if (d == 0) a.part_ml[row] = make_float2(M, sum);
+        }
+    }
+}
+
+// Merges the partitions of a (sequence, query head) row, one warp a row: a lane
+// owns four of the 128 columns, partials are read eight at a time so that their
+// latencies overlap.
+__global__ void __launch_bounds__(128) pa_merge_block8_kernel(const Block8Args a) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (row >= (int64_t)a.num_seqs * a.num_q_heads) return;
+    Span w;
+    span_of(a, a.context_lens[row / a.num_q_heads], 0, false, w);
+    if (w.nparts <= 1) return;
+    const float2 *ml = a.part_ml + row * a.max_parts;
+    const float4 *po = reinterpret_cast<const float4 *>(a.part_o + row * a.max_parts * kD);
+    float M = -INFINITY;
+    for (int p = lane; p < w.nparts; p += 32) M = fmaxf(M, ml[p].x);
+#pragma unroll
+    for (int k = 16; k >= 1; k >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, k));
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = 0; p0 < w.nparts; p0 += 8) {
+        float4 v[8];
+        float2 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const bool in = p0 + i < w.nparts;
+            v[i] = in ? po[(int64_t)(p0 + i) * 32 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[i] = in ? ml[p0 + i] : make_float2(-INFINITY, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float f = x[i].x == -INFINITY ? 0.f : exp2f(x[i].x - M);
+            sum = fmaf(f, x[i].y, sum);
+            acc.x = fmaf(f, v[i].x, acc.x);
+            acc.y = fmaf(f, v[i].y, acc.y);
+            acc.z = fmaf(f, v[i].z, acc.z);
+            acc.w = fmaf(f, v[i].w, acc.w);
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * kD + 4 * lane) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+int sms() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+        (void)cudaGetLastError();
+        return 152;
+    }
+    return n;
+}
+
+// Query heads of one CTA: the group, or its largest divisor up to 8.
+int heads_per_cta(int group) {
+    int h = std::min(group, kHeads);
+    while (group % h != 0) --h;
+    return h;
+}
+
+struct Plan {
+    int part_blocks, max_parts;
+};
+
+// Blocks a context can span and their partitions.  partition_size 0: the
+// longest of 4096 .. 128 tokens that gives four CTAs per SM.
+bool plan_of(int num_seqs, int axis, int max_blocks, int window, int partition_size, Plan *p) {
+    if (partition_size != 0 && (partition_size < kBlockSize || partition_size > kMaxPartition || partition_size % kBlockSize))
+        return false;
+    int span = max_blocks;
+    if (window > 0) span = std::min(span, (window - 1) / kBlockSize + 2);
+    int size = partition_size;
+    if (size == 0) {
+        const int64_t target = 4LL * sms();
+        for (size = 4096; size > 128; size /= 2) {
+            const int64_t parts = std::max(1, (span + size / kBlockSize - 1) / (size / kBlockSize));
+            if ((int64_t)num_seqs * axis * parts >= target) break;
+        }
+    }
+    p->part_blocks = size / kBlockSize;
+    p->max_parts = std::max(1, (span + p->part_blocks - 1) / p->part_blocks);
+    // blocks are spread evenly over the partitions of a full-length context
+    if (partition_size == 0) p->part_blocks = std::max(1, (span + p->max_parts - 1) / p->max_parts);
+    return true;
+}
+
+size_t rows_bytes(int64_t rows) { return ((size_t)rows * kD * sizeof(float) + 255) & ~size_t(255); }
+
+size_t workspace_of(int num_seqs, int num_q_heads, int max_parts) {
+    if (max_parts <= 1) return 0;
+    const int64_t rows = (int64_t)num_seqs * num_q_heads * max_parts;
+    return rows_bytes(rows) + (size_t)rows * sizeof(float2);
+}
+
+template <int NW, int STAGES>
+pa_status launch_decode(const Block8Args &a, const void *kc, const void *vc, int64_t rows, cudaStream_t st) {
+    CUtensorMap kmap, vmap;
+    if (!encode_block8_map(&kmap, kc, rows) || !encode_block8_map(&vmap, vc, rows))
+        return cuda_failure(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
+    const size_t smem = Shape<NW, STAGES>::smem(a.part_blocks);
+    auto kernel = pa_decode_block8_kernel<NW, STAGES>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return cuda_failure(e, "cudaFuncSetAttribute(block-scaled decode)");
+    const int64_t grid = (int64_t)a.num_seqs * a.num_kv_heads * a.splits * a.max_parts;
+    e = launch_chained(kernel, dim3((unsigned)grid), dim3(NW * 32), smem, st, kmap, vmap, a);
+    if (e != cudaSuccess) return cuda_failure(e, "pa_decode_block8_kernel launch");
+    count_launches(1);
+    return PA_OK;
+}
+
+}  // namespace
+
+bool encode_block8_map(CUtensorMap *map, const void *pool, int64_t rows) {
+    static PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    if (enc == nullptr) return false;
+    cuuint64_t dims[2] = {kD, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {kD};
+    cuuint32_t box[2] = {kD, kBlockSize};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(pool), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" size_t pa_decode_block_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                                      int max_blocks_per_seq, int block_size, int window,
+                                                      int partition_size) {
+    if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 || head_dim != kD ||
+        max_blocks_per_seq < 0 || max_blocks_per_seq > 0x7fffffff / kBlockSize || block_size != kBlockSize || window < 0)
+        return (size_t)-1;
+    const int group = num_q_heads / num_kv_heads;
+    Plan p;
+    if (!plan_of(num_seqs, num_kv_heads * (group / heads_per_cta(group)), max_blocks_per_seq, window, partition_size, &p))
+        return (size_t)-1;
+    return workspace_of(num_seqs, num_q_heads, p.max_parts);
+}
+
+extern "C" pa_status pa_decode_block_fp8(void *out, const void *query, const void *key_cache, const void *value_cache,
+                                         const float *k_scales, const float *v_scales, const int32_t *block_tables,
+                                         const int32_t *context_lens, int num_seqs, int num_q_heads, int num_kv_heads,
+                                         int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
+                                         float scale, int window, int partition_size, void *workspace,
+                                         size_t workspace_bytes, int32_t *device_status, void *stream) {
+    if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
+        block_size != kBlockSize || max_blocks_per_seq < 0 || max_blocks_per_seq > 0x7fffffff / kBlockSize ||
+        num_blocks <= 0 || window < 0 || !(scale == scale))
+        return PA_ERR_INVALID_ARG;
+    const int group = num_q_heads / num_kv_heads, heads = heads_per_cta(group), splits = group / heads;
+    Plan p;
+    if (!plan_of(num_seqs, num_kv_heads * splits, max_blocks_per_seq, window, partition_size, &p))
+        return PA_ERR_INVALID_ARG;
+    if (head_dim != kD) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PA_OK;
+    if (!out || !query || !key_cache || !value_cache || !k_scales || !v_scales || !context_lens ||
+        (!block_tables && max_blocks_per_seq > 0))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(query) || !aligned16(key_cache) || !aligned16(value_cache) ||
+        ((reinterpret_cast<uintptr_t>(k_scales) | reinterpret_cast<uintptr_t>(v_scales) |
+          reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens)) & 3u))
+        return PA_ERR_INVALID_ARG;
+    const int64_t rows = (int64_t)num_blocks * num_kv_heads * kBlockSize;
+    if (rows >= ((int64_t)1 << 31) ||
+        (int64_t)num_seqs * num_q_heads * p.max_parts >= ((int64_t)1 << 31))
+        return PA_ERR_UNSUPPORTED;
+    const size_t need = workspace_of(num_seqs, num_q_heads, p.max_parts);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace))) return PA_ERR_WORKSPACE;
+    Block8Args a = {};
+    a.out = out;
+    a.query = query;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    if (need > 0) {
+        a.part_o = static_cast<float *>(workspace);
+        a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) +
+                                               rows_bytes((int64_t)num_seqs * num_q_heads * p.max_parts));
+    }
+    a.status = device_status;
+    a.num_seqs = num_seqs;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.heads = heads;
+    a.splits = splits;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.part_blocks = p.part_blocks;
+    a.max_parts = p.max_parts;
+    a.window = window;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    pa_status s = launch_decode<4, 3>(a, key_cache, value_cache, rows, st);
+    if (s != PA_OK || p.max_parts <= 1) return s;
+    const int64_t merge = ((int64_t)num_seqs * num_q_heads + 3) / 4;
+    cudaError_t e = launch_chained(pa_merge_block8_kernel, dim3((unsigned)merge), dim3(128), 0, st, a);
+    if (e != cudaSuccess) return cuda_failure(e, "pa_merge_block8_kernel launch");
+    count_launches(1);
+    return PA_OK;
+}

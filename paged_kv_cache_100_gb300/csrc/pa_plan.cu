@@ -1,0 +1,270 @@
+// The bookkeeping of one serving step on the GPU: block tables, slots and
+// positions of the step's tokens from the request lengths ("PagedAttention por
+// dentro: bloques, tabla de páginas, evicción y el estado del arte del KV cache
+// en 2026", section "La tabla de páginas (block table)": a sequence holding N
+// tokens writes the next one into its last block while N mod 16 != 0, else into
+// a block taken from the pool).
+//
+// With L_b tokens held and T_b new ones, sequence b takes
+//   need_b = ceil((L_b + T_b) / 16) - ceil(L_b / 16)
+// blocks.  The sequences are served in order; b is served while the running
+// sums of need and T stay within the free blocks and the token capacity, so the
+// served ones are a prefix of the batch (apart from sequences that bring
+// nothing).  The sum of need before b is where b's blocks begin in the free
+// stack, the sum of T before b where its tokens begin in the flat list.
+//
+// One launch, no scratch memory: the two running sums are cheap (8 bytes per
+// sequence, from L2), so every CTA computes them for itself, kSeqs sequences at
+// a time, and then writes its own range of tokens, finding a token's sequence
+// by bisection among the kSeqs ends in shared memory.  A new block's table
+// entry is written by the thread of its first token.  The sequences' outputs
+// are written by one CTA for each group of kSeqs.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+namespace {
+
+constexpr int kPlanThreads = 256;
+constexpr int kPlanItems = 4;                       // sequences per thread and round
+constexpr int kSeqs = kPlanThreads * kPlanItems;    // sequences per round
+constexpr int kPlanWarps = kPlanThreads / 32;
+
+struct PlanArgs {
+    int32_t *block_tables;
+    const int32_t *context_lens;
+    const int32_t *new_lens;
+    const int32_t *free_blocks;
+    const int32_t *num_free;
+    int32_t *context_lens_out;
+    int32_t *query_start;
+    int64_t *slot_mapping;
+    int32_t *positions;
+    int32_t *num_free_out;
+    int32_t *status;
+    int num_seqs;
+    int max_blocks;
+    int num_blocks;
+    int free_capacity;
+    int token_capacity;
+    int tokens_per_cta;
+};
+
+__device__ __forceinline__ int blocks_of(int tokens) {
+    return (int)(((unsigned)tokens + (kBlockSize - 1)) / kBlockSize);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) pa_plan_step_kernel(const PlanArgs a) {
+    // ends, first blocks and held tokens of the round's sequences; a sequence
+    // that is not served ends where the served ones end
+    __shared__ int s_end[kSeqs], s_new[kSeqs], s_off[kSeqs], s_len[kSeqs];
+    __shared__ int64_t s_warp[2][kPlanWarps];
+    __shared__ int s_total[2], s_used[2];           // alternate between rounds
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int free = *a.num_free;
+    if (free < 0 || free > a.free_capacity) {
+        if (blockIdx.x == 0 && tid == 0) report(a.status, PA_DEV_BAD_BLOCK_ID);
+        free = free < 0 ? 0 : a.free_capacity;
+    }
+    const int t_lo = (int)min((int64_t)a.token_capacity, (int64_t)blockIdx.x * a.tokens_per_cta);
+    const int t_hi = (int)min((int64_t)a.token_capacity, (int64_t)t_lo + a.tokens_per_cta);
+    int64_t carry_need = 0, carry_new = 0;          // sums over the rounds before, served or not
+    int total = 0, used = 0;                        // tokens and blocks of the served sequences
+    if (tid < 2) s_total[tid] = s_used[tid] = 0;
+    if (blockIdx.x == 0 && tid == 0) a.query_start[0] = 0;
+    __syncthreads();
+    int round = 0;
+    for (int64_t base = 0; base < a.num_seqs; base += kSeqs, ++round) {
+        int len[kPlanItems], add[kPlanItems], need[kPlanItems];
+        int64_t sum_need = 0, sum_new = 0;
+#pragma unroll
+        for (int j = 0; j < kPlanItems; ++j) {
+            const int64_t b = base + tid * kPlanItems + j;
+            len[j] = b < a.num_seqs ? a.context_lens[b] : 0;
+            add[j] = b < a.num_seqs ? a.new_lens[b] : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < kPlanItems; ++j) {
+            if (len[j] < 0 || add[j] < 0 ||
+                (int64_t)len[j] + add[j] > (int64_t)a.max_blocks * kBlockSize) {
+                if (blockIdx.x == 0) report(a.status, PA_DEV_BAD_CONTEXT_LEN);
+                add[j] = 0;
+            }
+            need[j] = add[j] > 0 ? blocks_of(len[j] + add[j]) - blocks_of(len[j]) : 0;
+            sum_need += need[j];
+            sum_new += add[j];
+        }
+        // exclusive sums over the round's threads
+        int64_t at_need = sum_need, at_new = sum_new;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, at_need, o);
+            const int64_t y = __shfl_up_sync(0xffffffffu, at_new, o);
+            if (lane >= o) {
+                at_need += x;
+                at_new += y;
+            }
+        }
+        if (lane == 31) {
+            s_warp[0][warp] = at_need;
+            s_warp[1][warp] = at_new;
+        }
+        __syncthreads();
+        int64_t before_need = carry_need, before_new = carry_new;
+        for (int w = 0; w < kPlanWarps; ++w) {
+            const int64_t x = s_warp[0][w], y = s_warp[1][w];
+            if (w < warp) {
+                before_need += x;
+                before_new += y;
+            }
+            carry_need += x;
+            carry_new += y;
+        }
+        at_need += before_need - sum_need;
+        at_new += before_new - sum_new;
+        bool served[kPlanItems];
+        int last_new = 0, last_need = 0;
+        bool cut = false;
+#pragma unroll
+        for (int j = 0; j < kPlanItems; ++j) {
+            served[j] = at_need + need[j] <= free && at_new + add[j] <= a.token_capacity;
+            cut |= !served[j] && add[j] > 0;
+            const int k = tid * kPlanItems + j;
+            s_off[k] = served[j] ? (int)at_need : 0;
+            s_len[k] = len[j];
+            s_new[k] = served[j] ? add[j] : 0;
+            at_need += need[j];
+            at_new += add[j];
+            s_end[k] = served[j] ? (int)at_new : 0x7fffffff;
+            if (served[j]) {
+                last_new = (int)at_new;
+                last_need = (int)at_need;
+            }
+        }
+        if (cut && blockIdx.x == 0) report(a.status, PA_DEV_NO_BLOCKS);
+        // the sums never fall, so the served prefix's totals are their maxima
+        const int slot = round & 1;
+        last_new = __reduce_max_sync(0xffffffffu, last_new);
+        last_need = __reduce_max_sync(0xffffffffu, last_need);
+        if (lane == 0) {
+            atomicMax(&s_total[slot], last_new);
+            atomicMax(&s_used[slot], last_need);
+        }
+        __syncthreads();
+        const int total_before = total;
+        total = max(total, s_total[slot]);
+        used = max(used, s_used[slot]);
+        if (tid == 0) s_total[slot ^ 1] = s_used[slot ^ 1] = 0;
+        if (round % gridDim.x == blockIdx.x) {
+#pragma unroll
+            for (int j = 0; j < kPlanItems; ++j) {
+                const int64_t b = base + tid * kPlanItems + j;
+                if (b < a.num_seqs) {
+                    a.context_lens_out[b] = len[j] + (served[j] ? add[j] : 0);
+                    a.query_start[b + 1] = min(s_end[tid * kPlanItems + j], total);
+                }
+            }
+        }
+        for (int i = max(t_lo, total_before) + tid; i < min(t_hi, total); i += kPlanThreads) {
+            int k = 0;                               // the first sequence that ends behind token i
+#pragma unroll
+            for (int step = kSeqs / 2; step >= 1; step >>= 1)
+                if (s_end[k + step - 1] <= i) k += step;
+            const int pos = s_len[k] + i - (s_end[k] - s_new[k]);
+            const int blk = pos / kBlockSize;
+            int32_t *entry = a.block_tables + (base + k) * a.max_blocks + blk;
+            const int have = blocks_of(s_len[k]);
+            int32_t phys;
+            if (blk >= have) {
+                phys = a.free_blocks[free - 1 - (s_off[k] + blk - have)];
+                if (pos % kBlockSize == 0) *entry = phys;
+            } else {
+                phys = *entry;
+            }
+            const bool good = (unsigned)phys < (unsigned)a.num_blocks;
+            if (!good) report(a.status, PA_DEV_BAD_BLOCK_ID);
+            a.slot_mapping[i] = good ? (int64_t)phys * kBlockSize + pos % kBlockSize : -1;
+            a.positions[i] = pos;
+        }
+        __syncthreads();                             // the round's arrays are read
+    }
+    for (int i = max(t_lo, total) + tid; i < t_hi; i += kPlanThreads) {
+        a.slot_mapping[i] = -1;
+        a.positions[i] = 0;
+    }
+    if (blockIdx.x == 0 && tid == 0) *a.num_free_out = free - used;
+}
+
+bool overlap(const void *p, size_t n, const void *q, size_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
+    return n > 0 && m > 0 && x < y + m && y < x + n;
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" pa_status pa_plan_step(int32_t *block_tables, const int32_t *context_lens,
+                                  const int32_t *new_lens, const int32_t *free_blocks,
+                                  const int32_t *num_free, int32_t *context_lens_out,
+                                  int32_t *query_start, int64_t *slot_mapping, int32_t *positions,
+                                  int32_t *num_free_out, int num_seqs, int max_blocks_per_seq,
+                                  int block_size, int num_blocks, int free_capacity,
+                                  int token_capacity, int32_t *device_status, void *stream) {
+    if (num_seqs < 0 || max_blocks_per_seq < 0 || block_size != kBlockSize || num_blocks <= 0 ||
+        free_capacity < 0 || token_capacity < 0 || max_blocks_per_seq > 0x7fffffff / kBlockSize)
+        return PA_ERR_INVALID_ARG;
+    if (!query_start || !num_free || !num_free_out || (num_seqs > 0 && (!context_lens || !new_lens || !context_lens_out)) ||
+        (num_seqs > 0 && max_blocks_per_seq > 0 && !block_tables) || (free_capacity > 0 && !free_blocks) ||
+        (token_capacity > 0 && (!slot_mapping || !positions)))
+        return PA_ERR_INVALID_ARG;
+    const size_t n = (size_t)num_seqs, t = (size_t)token_capacity;
+    const struct { const void *p; size_t bytes, align; } out[6] = {
+        {block_tables, n * max_blocks_per_seq * 4, 4}, {context_lens_out, n * 4, 4},
+        {query_start, n * 4 + 4, 4}, {slot_mapping, t * 8, 8}, {positions, t * 4, 4}, {num_free_out, 4, 4}};
+    const struct { const void *p; size_t bytes; } in[4] = {
+        {context_lens, n * 4}, {new_lens, n * 4}, {free_blocks, (size_t)free_capacity * 4}, {num_free, 4}};
+    // every CTA reads all of the inputs while others write: nothing may overlap
+    for (int i = 0; i < 6; ++i) {
+        if (reinterpret_cast<uintptr_t>(out[i].p) % out[i].align) return PA_ERR_INVALID_ARG;
+        for (int j = 0; j < 4; ++j)
+            if (overlap(out[i].p, out[i].bytes, in[j].p, in[j].bytes)) return PA_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return PA_ERR_INVALID_ARG;
+    }
+    for (int j = 0; j < 4; ++j)
+        if (reinterpret_cast<uintptr_t>(in[j].p) & 3u) return PA_ERR_INVALID_ARG;
+    PlanArgs a;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.new_lens = new_lens;
+    a.free_blocks = free_blocks;
+    a.num_free = num_free;
+    a.context_lens_out = context_lens_out;
+    a.query_start = query_start;
+    a.slot_mapping = slot_mapping;
+    a.positions = positions;
+    a.num_free_out = num_free_out;
+    a.status = device_status;
+    a.num_seqs = num_seqs;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.free_capacity = free_capacity;
+    a.token_capacity = token_capacity;
+    // one token per thread up to 128 CTAs, then longer ranges
+    const int per_thread = std::max(1, (int)(((int64_t)token_capacity + 128 * kPlanThreads - 1) / (128 * kPlanThreads)));
+    a.tokens_per_cta = per_thread * kPlanThreads;
+    const int grid = std::max(1, (int)(((int64_t)token_capacity + a.tokens_per_cta - 1) / a.tokens_per_cta));
+    cudaError_t e = launch_chained(pa_plan_step_kernel, dim3((unsigned)grid), dim3(kPlanThreads), 0,
+                                   static_cast<cudaStream_t>(stream), a);
+    if (e != cudaSuccess) return cuda_failure(e, "pa_plan_step_kernel launch");
+    count_launches(1);
+    return PA_OK;
+}

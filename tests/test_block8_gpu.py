@@ -1,0 +1,189 @@
+"""pa_decode_block_fp8 and pa_prefill_block_fp8: attention over E4M3 pools with one scale per block
+and KV head, against 64-bit attention over the same values."""
+import numpy as np
+import pytest
+import torch
+
+from tests import block8_ref as R
+
+pytestmark = pytest.mark.gpu
+D = 128
+
+
+@pytest.fixture(scope="module")
+def pkv():
+    from paged_kv_cache_100_gb300.build import build
+    build()
+    import paged_kv_cache_100_gb300 as m
+    return m
+
+
+class Pool:
+    """Pools, tables and lengths of a batch; codes and scales of slots that hold no token are NaN
+    codes and absurd scales."""
+
+    def __init__(self, seed, lens, hkv, spread=1.5, width=None, poison=True):
+        g = self.g = torch.Generator().manual_seed(seed)
+        self.lens = np.asarray(lens, np.int32)
+        self.tables, self.blocks = R.tables_for(g, lens, width=width)
+        self.hkv = hkv
+        self.kc, self.ks = R.pools(g, self.blocks, hkv, D, spread)
+        self.vc, self.vs = R.pools(g, self.blocks, hkv, D, spread)
+        if poison:
+            live = np.zeros((self.blocks, 16), bool)
+            for b, n in enumerate(lens):
+                for p in range(int(n)):
+                    live[self.tables[b, p // 16], p % 16] = True
+            dead = torch.from_numpy(~live)
+            self.kc[dead[:, None].expand(-1, hkv, -1)] = 0x7F
+            self.vc[dead[:, None].expand(-1, hkv, -1)] = 0xFF
+            unused = dead.all(1)
+            for s in (self.ks, self.vs):
+                s[unused] = float("nan")
+
+    def device(self):
+        return [t.cuda() for t in (self.kc, self.vc, self.ks, self.vs)] + [
+            torch.from_numpy(self.tables).cuda(), torch.from_numpy(self.lens).cuda()]
+
+    def reference(self, q, rows, scale, window=0):
+        """q [rows][Hq][D] float64; rows: (sequence, last position) of each."""
+        group = q.shape[1] // self.hkv
+        kv, vv = R.decode_codes(self.kc), R.decode_codes(self.vc)
+        ks, vs = self.ks.double().numpy(), self.vs.double().numpy()
+        out, bound = np.zeros_like(q), np.zeros_like(q)
+        for i, (b, last) in enumerate(rows):
+            lo = max(0, last + 1 - window) if window else 0
+            for h in range(self.hkv):
+                j = slice(h * group, (h + 1) * group)
+                out[i, j], bound[i, j] = R.attention(q[i, j], kv[:, h], ks[:, h], vv[:, h], vs[:, h], self.tables[b],
+                                                     lo, last + 1, scale)
+        return out, bound
+
+
+def _check(got, ref, bound, what=""):
+    err = np.abs(got.double().cpu().numpy() - ref)
+    limit = bound + 2.0 ** -8 * (np.abs(ref) + bound)
+    assert (err <= limit).all(), (what, float(np.nanmax(err - limit)), np.argwhere(~(err <= limit))[:4].tolist())
+
+
+def _query(pool, rows, hq):
+    return torch.randn(rows, hq, D, generator=pool.g).to(torch.bfloat16)
+
+
+LENS = [1, 15, 16, 17, 0, 100, 513, 1100, 31]
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 8), (8, 4), (6, 2), (8, 2), (5, 1), (12, 2), (7, 1), (16, 2), (11, 1), (24, 2), (16, 1)])
+@pytest.mark.parametrize("partition", [0, 64, 16384])
+def test_decode_matches(pkv, hq, hkv, partition):
+    p = Pool(hq * 10 + hkv, LENS, hkv)
+    q = _query(p, len(LENS), hq)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = pkv.decode_block_fp8(q.cuda(), *p.device(), partition_size=partition, status=status)
+    ref, bound = p.reference(q.double().numpy(), [(b, n - 1) for b, n in enumerate(LENS)], D ** -0.5)
+    _check(out, ref, bound, f"{hq}/{hkv} P={partition}")
+    assert (out[4] == 0).all() and int(status.item()) == 0
+
+
+@pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 100, 513, 5000])
+@pytest.mark.parametrize("hq,hkv,partition", [(8, 8, 0), (16, 2, 0), (8, 2, 32)])
+def test_decode_window(pkv, window, hq, hkv, partition):
+    p = Pool(window, LENS, hkv)
+    q = _query(p, len(LENS), hq)
+    dev = p.device()
+    first = [max(0, n - window) // 16 for n in LENS]
+    for b, f in enumerate(first):                           # released blocks before the window
+        dev[4][b, :f] = -1
+    out = pkv.decode_block_fp8(q.cuda(), *dev, window=window, partition_size=partition)
+    ref, bound = p.reference(q.double().numpy(), [(b, n - 1) for b, n in enumerate(LENS)], D ** -0.5, window)
+    _check(out, ref, bound, f"W={window}")
+
+
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (8, 1)])
+def test_decode_scales_of_any_size(pkv, hq, hkv):
+    """Value scales over the whole range in one context, an outlier block, scales that are no powers
+    of two, tiny and negative key scales."""
+    lens = [700, 700, 700, 60]
+    p = Pool(3, lens, hkv, poison=False)
+    p.vs[:] = torch.exp2(torch.randint(-32, 32, p.vs.shape, generator=p.g).float())
+    t = p.tables
+    p.vs[t[1, :43]] = torch.rand(43, hkv, generator=p.g) + 0.3
+    p.vs[t[1, 20]] = 40000.0
+    p.ks[t[1, :43]] = torch.randn(43, hkv, generator=p.g) * 0.01
+    p.vs[t[2, :44]] = 2.0 ** -32
+    p.vs[t[3, :4]] = 2.0 ** 31
+    q = _query(p, len(lens), hq)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = pkv.decode_block_fp8(q.cuda(), *p.device(), status=status)
+    ref, bound = p.reference(q.double().numpy(), [(b, n - 1) for b, n in enumerate(lens)], D ** -0.5)
+    _check(out, ref, bound)
+    assert int(status.item()) == 0
+
+
+def test_decode_flags_bad_scales_tables_lengths_and_queries(pkv):
+    from paged_kv_cache_100_gb300 import _lib
+    lens = [40, 40]
+    for what, bit in (("scale", _lib.PA_DEV_RANGE), ("zero", _lib.PA_DEV_RANGE), ("query", _lib.PA_DEV_RANGE),
+                      ("table", _lib.PA_DEV_BAD_BLOCK_ID), ("length", _lib.PA_DEV_BAD_CONTEXT_LEN)):
+        p = Pool(5, lens, 2, poison=False)
+        q = _query(p, 2, 4)
+        if what == "scale":
+            p.vs[p.tables[1, 1]] = float("inf")
+        if what == "zero":
+            p.vs[p.tables[1, 1]] = 0.0
+        if what == "query":
+            q[1, 0, 0] = 70000.0
+        dev = p.device()
+        if what == "table":
+            dev[4][1, 1] = p.blocks
+        if what == "length":
+            dev[5][1] = 16 * 3 + 1
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = pkv.decode_block_fp8(q.cuda(), *dev, status=status)
+        assert int(status.item()) == bit, what
+        ref, bound = p.reference(q.double().numpy()[:1], [(0, 39)], D ** -0.5)
+        _check(out[:1], ref, bound, what)                   # the other sequence is not touched by it
+
+
+def test_decode_nan_code_reaches_the_output(pkv):
+    p = Pool(6, [33, 20, 20], 1, poison=False)
+    p.vc[p.tables[0, 1], 0, 3, 7] = 0x7F
+    p.kc[p.tables[2, 0], 0, 3, 7] = 0x7F
+    q = _query(p, 3, 2)
+    out = pkv.decode_block_fp8(q.cuda(), *p.device()).cpu()
+    assert torch.isnan(out[0, :, 7]).all() and torch.isfinite(out[0, :, :7]).all()
+    assert torch.isfinite(out[1]).all() and torch.isnan(out[2]).all()
+
+
+def test_decode_long_context_and_given_workspace(pkv):
+    lens = [20000, 3]
+    p = Pool(9, lens, 2, spread=0.7)
+    q = _query(p, 2, 4)
+    dev = p.device()
+    for P in (0, 512, 16384):
+        need = pkv.decode_block_fp8_workspace_bytes(2, 4, 2, D, p.tables.shape[1], P)
+        ws = torch.full((need + 64,), 0xAB, dtype=torch.uint8, device="cuda")
+        out = pkv.decode_block_fp8(q.cuda(), *dev, partition_size=P, workspace=ws[:need])
+        ref, bound = p.reference(q.double().numpy(), [(b, n - 1) for b, n in enumerate(lens)], D ** -0.5)
+        _check(out, ref, bound, f"P={P}")
+        assert (ws[need:] == 0xAB).all()
+
+
+def test_decode_graph_replay_and_streams(pkv):
+    p = Pool(11, [900, 1, 2000, 64], 4)
+    q = _query(p, 4, 16).cuda()
+    dev = p.device()
+    want = pkv.decode_block_fp8(q, *dev, partition_size=256)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = pkv.decode_block_fp8(q, *dev, partition_size=256, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = pkv.decode_block_fp8(q, *dev, partition_size=256)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)

@@ -1,0 +1,242 @@
+"""pa_rope_cache_write: rotary positions on queries and keys with the cache write, into f32, bf16
+and block-scaled E4M3 pools, against 64-bit implementations."""
+import numpy as np
+import pytest
+import torch
+
+from tests import block8_ref as R
+
+pytestmark = pytest.mark.gpu
+
+# cos and sin: the angle is held to 2^-24 of at most half a turn (pi 2^-24 < 2^-22 radians), sincospi
+# to 2 units of 2^-23; two products and a sum of f32 round 3 times 2^-24.  Per |x0| + |x1|:
+TURN = 2.0 ** -22 + 2.0 ** -22 + 3 * 2.0 ** -24
+HALF_STEP = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+
+
+@pytest.fixture(scope="module")
+def pkv():
+    from paged_kv_cache_100_gb300.build import build
+    build()
+    import paged_kv_cache_100_gb300 as m
+    return m
+
+
+def _inputs(seed, T, Hq, Hkv, D, dtype, blocks, far=False):
+    g = torch.Generator().manual_seed(seed)
+    qkv = torch.randn(T, Hq + 2 * Hkv, D, generator=g) * torch.exp2(torch.randn(T, Hq + 2 * Hkv, 1, generator=g))
+    qkv = qkv.to(dtype)
+    pos = torch.randint(0, 1 << 30 if far else 5000, (T,), generator=g, dtype=torch.int32)
+    slots = torch.randperm(blocks * 16, generator=g)[:T]
+    return g, qkv, pos, slots
+
+
+def _close(got, ref, mass, a, dtype, what):
+    err = np.abs(got.double().cpu().numpy() - ref)
+    bound = a * TURN * mass + HALF_STEP[dtype] * (np.abs(ref) + a * TURN * mass)
+    assert (err <= bound).all(), (what, float((err - bound).max()))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D,rot", [(64, 64), (128, 128), (128, 64), (128, 20), (64, 2), (256, 250), (96, 96), (80, 0), (8, 6)])
+def test_rows_match(pkv, D, rot, dtype, interleaved):
+    T, Hq, Hkv, blocks = 21, 5, 2, 4
+    g, qkv, pos, slots = _inputs(D + rot, T, Hq, Hkv, D, dtype, blocks)
+    slots[3] = -1
+    rope = pkv.rotary_plan(rot, interleaved=interleaved)
+    x = qkv.cuda()
+    kc = torch.randn(blocks, Hkv, 16, D, generator=g).to(dtype)
+    vc = torch.randn(blocks, Hkv, 16, D, generator=g).to(dtype)
+    kd, vd = kc.cuda(), vc.cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = pkv.rope_cache_write(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], pos.cuda(), rope, kd, vd, slots.cuda(),
+                               status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    cos, sin = R.rotary_angles(pos.numpy(), rot)
+    ref, mass = R.rotate(qkv.double().numpy(), cos, sin, interleaved)
+    _close(out, ref[:, :Hq], mass[:, :Hq], 1.0, dtype, "query")
+    want, wmass = kc.double().numpy(), np.zeros(kc.shape)
+    for i, s in enumerate(slots.tolist()):
+        if s >= 0:
+            want[s // 16, :, s % 16] = ref[i, Hq:Hq + Hkv]
+            wmass[s // 16, :, s % 16] = mass[i, Hq:Hq + Hkv]
+            vc[s // 16, :, s % 16] = qkv[i, Hq + Hkv:]
+    _close(kd, want, wmass, 1.0, dtype, "keys")
+    assert torch.equal(vd.cpu(), vc)
+    # the same call in place on contiguous queries
+    q = x[:, :Hq].contiguous()
+    same = pkv.rope_cache_write(q, x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], pos.cuda(), rope, kd, vd, slots.cuda(), query_out=q)
+    assert same is q and torch.equal(q, out)
+
+
+@pytest.mark.parametrize("scaling,factor", [("none", 1.0), ("linear", 4.0), ("ntk", 8.0), ("by_parts", 8.0)])
+def test_scaled_and_far_positions(pkv, scaling, factor):
+    T, H, D = 40, 3, 128
+    _, qkv, pos, slots = _inputs(5, T, H, 1, D, torch.float32, 8, far=True)
+    pos[:4] = torch.tensor([0, 1, 2 ** 31 - 1, 131071], dtype=torch.int32)
+    rope = pkv.rotary_plan(D, 500000.0, scaling=scaling, factor=factor)
+    x = qkv.cuda()
+    pool = torch.zeros(8, 1, 16, D, device="cuda")
+    out = pkv.rope_cache_write(x[:, :H], x[:, H:H + 1], x[:, H + 1:], pos.cuda(), rope, pool, torch.zeros_like(pool), slots.cuda())
+    # in whole turns, so that the reference's own angle is exact at far positions
+    turns = [int(t) % (1 << 64) for t in rope.turns.cpu().tolist()]
+    frac = np.array([[((int(p) * t) % (1 << 64)) / 2.0 ** 64 for t in turns] for p in pos.tolist()])
+    a = rope.attention_factor
+    near, _ = R.rotary_angles(np.ones(1), D, 500000.0, scaling, factor)
+    assert np.allclose(near[0], a * np.cos(2 * np.pi * np.array(turns) / 2.0 ** 64), atol=1e-7)
+    ref, mass = R.rotate(qkv.double().numpy(), a * np.cos(2 * np.pi * frac), a * np.sin(2 * np.pi * frac), False)
+    _close(out, ref[:, :H], mass[:, :H], a, torch.float32, scaling)
+
+
+def _chunks(rng, seqs, longest, spare=2):
+    """Slots of chunks that begin anywhere in a block; blocks in random order."""
+    lens = rng.integers(0, 40, seqs)
+    new = rng.integers(1, longest + 1, seqs)
+    first = lens // 16
+    need = -(-(lens + new) // 16) - first
+    perm = rng.permutation(int(need.sum()) + spare)
+    slots, pos, at = [], [], 0
+    for b in range(seqs):
+        for p in range(lens[b], lens[b] + new[b]):
+            slots.append(int(perm[at + p // 16 - first[b]]) * 16 + p % 16)
+            pos.append(p)
+        at += need[b]
+    return np.array(slots, np.int64), np.array(pos, np.int32), perm.size
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,rot,interleaved", [(128, 128, False), (128, 96, True), (64, 50, False), (256, 256, False), (16, 16, False)])
+@pytest.mark.parametrize("seqs,longest", [(1, 1), (5, 1), (4, 70), (40, 3)])
+def test_block_scaled_write(pkv, seqs, longest, D, rot, interleaved, dtype):
+    rng = np.random.default_rng(seqs * 1000 + longest + D)
+    slots, pos, blocks = _chunks(rng, seqs, longest)
+    T, Hq, Hkv = slots.size, 2, 3
+    g, qkv, _, _ = _inputs(seqs + D, T, Hq, Hkv, D, dtype, blocks + T)
+    kc, ks = R.pools(g, blocks, Hkv, D)
+    vc, vs = R.pools(g, blocks, Hkv, D)
+    qkv[T // 2, Hq:] = 0                                     # an all-zero row
+    if T > 3:
+        slots[T - 2] = -1
+    x, d = qkv.cuda(), lambda t: t.cuda()  # noqa: E731
+    kd, ksd, vd, vsd = d(kc), d(ks), d(vc), d(vs)
+    rope = pkv.rotary_plan(rot, interleaved=interleaved)
+    out = pkv.rope_cache_write(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], torch.from_numpy(pos).cuda(), rope,
+                               kd, vd, torch.from_numpy(slots).cuda(), k_scales=ksd, v_scales=vsd)
+    torch.cuda.synchronize()
+    cos, sin = R.rotary_angles(pos, rot)
+    ref, mass = R.rotate(qkv.double().numpy(), cos, sin, interleaved)
+    _close(out, ref[:, :Hq], mass[:, :Hq], 1.0, dtype, "query")
+    kv, vv = R.decode_codes(kc), R.decode_codes(vc)
+    kss, vss = ks.double().numpy().copy(), vs.double().numpy().copy()
+    R.write_blocks(qkv[:, Hq + Hkv:].double().numpy(), slots, vv, vss)
+    assert np.array_equal(vsd.cpu().double().numpy(), vss)
+    assert np.array_equal(R.decode_codes(vd), vv)            # values are not turned: every code is the same
+    R.write_blocks(ref[:, Hq:Hq + Hkv], slots, kv, kss)
+    assert np.array_equal(ksd.cpu().double().numpy(), kss)
+    got = R.decode_codes(kd)
+    # a key next to the border of two codes may take either: one step of the code, in few places
+    step = 2.0 ** (np.clip(np.floor(np.log2(np.maximum(np.abs(kv), 2.0 ** -9))), -6, 8) - 3)
+    assert (np.abs(got - kv) <= step * 1.001).all() and (got != kv).mean() < 1e-3
+
+
+def test_block_scaled_write_grows_a_block_token_by_token(pkv):
+    """Sixteen single-token writes with growing magnitudes: the scale grows, earlier rows follow."""
+    D, H = 128, 2
+    g = torch.Generator().manual_seed(8)
+    rows = (torch.randn(16, H, D, generator=g) * 2.0 ** torch.arange(-8, 8)[:, None, None]).to(torch.bfloat16)
+    kc = torch.full((3, H, 16, D), 0x7F, dtype=torch.uint8, device="cuda")      # stale codes, NaN among them
+    vc, ks, vs = kc.clone(), torch.full((3, H), 1e9, device="cuda"), torch.full((3, H), 1e9, device="cuda")
+    kv, kss = R.decode_codes(kc), ks.double().cpu().numpy()
+    for i in range(16):
+        pkv.rope_cache_write(None, rows[i:i + 1].cuda(), rows[i:i + 1].cuda(), None, None, kc, vc,
+                             torch.tensor([16 + i], device="cuda"), k_scales=ks, v_scales=vs)
+        R.write_blocks(rows[i:i + 1].double().numpy(), [16 + i], kv, kss)
+        assert np.array_equal(R.decode_codes(kc)[1, :, :i + 1], kv[1, :, :i + 1])
+        assert np.array_equal(ks.double().cpu().numpy(), kss) and torch.equal(ks, vs) and torch.equal(kc, vc)
+    assert (kc[0] == 0x7F).all() and (kc[2] == 0x7F).all()
+
+
+def test_block_scaled_write_special_values(pkv):
+    from paged_kv_cache_100_gb300 import _lib
+    D, H = 128, 1
+    rows = torch.zeros(4, H, D, dtype=torch.bfloat16)
+    rows[0, 0, :3] = torch.tensor([float("nan"), 1.0, -2.0])
+    rows[1, 0, :2] = torch.tensor([float("inf"), 5.0])
+    rows[2, 0, :2] = torch.tensor([1e-30, 3.0e-30])
+    rows[3, 0, :2] = torch.tensor([448.0, -448.0])
+    kc = torch.zeros(4, H, 16, D, dtype=torch.uint8, device="cuda")
+    vc, ks, vs = kc.clone(), torch.zeros(4, H, device="cuda"), torch.zeros(4, H, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    slots = torch.tensor([0, 16, 32, 48], device="cuda")
+    pkv.rope_cache_write(None, rows.cuda(), rows.cuda(), None, None, kc, vc, slots, k_scales=ks, v_scales=vs, status=status)
+    v = R.decode_codes(kc)[:, 0, 0]
+    s = ks.cpu().double().numpy()[:, 0]
+    assert np.isnan(v[0, 0]) and (v[0, 1:3] * s[0]).tolist() == [1.0, -2.0] and s[0] == 2.0 ** -7
+    assert v[1, 0] == 448 and s[1] == 2.0 ** 31 and int(status.item()) == _lib.PA_DEV_RANGE
+    assert (v[2] == 0).all() and s[2] == 2.0 ** -32
+    assert v[3, 0] == 448 and v[3, 1] == -448 and s[3] == 1.0
+
+
+def test_block_scaled_write_duplicates_holes_and_spread_blocks(pkv):
+    """Holes and repeated slots inside a block's run, a block whose entries lie too far apart, a
+    slot past the pool."""
+    from paged_kv_cache_100_gb300 import _lib
+    D, H, T = 128, 2, 45
+    g = torch.Generator().manual_seed(2)
+    rows = torch.randn(T, H, D, generator=g).to(torch.bfloat16)
+    slots = np.full(T, -1, np.int64)
+    slots[[0, 2, 5, 9]] = [20, 22, 21, 22]                   # block 1: offsets 4, 6, 5, and 6 again
+    slots[[3, 40]] = [48, 49]                                # block 3: 37 entries apart
+    slots[7] = 4 * 16 + 5                                    # past the pool
+    kc, ks = R.pools(g, 4, H, D)
+    kd, ksd = kc.cuda(), ks.cuda()
+    vd, vsd = kc.cuda(), ks.cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pkv.rope_cache_write(None, rows.cuda(), rows.cuda(), None, None, kd, vd, torch.from_numpy(slots).cuda(),
+                         k_scales=ksd, v_scales=vsd, status=status)
+    kv, kss = R.decode_codes(kc), ks.double().numpy().copy()
+    slots[40] = -1                                           # dropped
+    R.write_blocks(rows.double().numpy(), slots, kv, kss)
+    assert np.array_equal(R.decode_codes(kd), kv) and np.array_equal(ksd.cpu().double().numpy(), kss)
+    assert torch.equal(kd, vd) and torch.equal(ksd, vsd)
+    assert int(status.item()) == _lib.PA_DEV_BAD_SLOT
+
+
+def test_a_chosen_scale_is_kept_and_divided_by(pkv):
+    """A part-filled block whose scale is no power of two and large enough keeps it."""
+    D, H = 128, 1
+    g = torch.Generator().manual_seed(4)
+    rows = torch.randn(1, H, D, generator=g).to(torch.bfloat16)
+    kc, ks = R.pools(g, 2, H, D)
+    ks[1] = 0.1
+    kd, ksd, vd, vsd = kc.cuda(), ks.cuda(), kc.cuda(), ks.cuda()
+    pkv.rope_cache_write(None, rows.cuda(), rows.cuda(), None, None, kd, vd, torch.tensor([16 + 9], device="cuda"),
+                         k_scales=ksd, v_scales=vsd)
+    assert torch.equal(ksd.cpu(), ks)
+    want = kc.clone()
+    want[1, 0, 9] = (rows[0, 0].float() / torch.tensor(0.1)).to(torch.float8_e4m3fn).view(torch.uint8)
+    assert torch.equal(kd.cpu(), want)
+
+
+def test_large_batch_uses_many_tokens_per_block(pkv):
+    """Enough tokens that one thread block takes several; checked against small calls."""
+    rng = np.random.default_rng(1)
+    slots, pos, blocks = _chunks(rng, 30, 600)
+    T, Hq, Hkv, D = slots.size, 4, 2, 128
+    g, qkv, _, _ = _inputs(3, T, Hq, Hkv, D, torch.bfloat16, blocks + T)
+    x = qkv.cuda()
+    rope = pkv.rotary_plan(D)
+    kc, ks = R.pools(g, blocks, Hkv, D)
+    a, b = [[t.cuda() for t in (kc, ks, kc, ks)] for _ in range(2)]
+    p, s = torch.from_numpy(pos).cuda(), torch.from_numpy(slots).cuda()
+    run = lambda c, lo, hi: pkv.rope_cache_write(  # noqa: E731
+        x[lo:hi, :Hq], x[lo:hi, Hq:Hq + Hkv], x[lo:hi, Hq + Hkv:], p[lo:hi], rope, c[0], c[2], s[lo:hi],
+        k_scales=c[1], v_scales=c[3])
+    whole = run(a, 0, T)
+    ends = [0] + [i for i in range(1, T) if slots[i] // 16 != slots[i - 1] // 16] + [T]
+    parts = [run(b, lo, hi) for lo, hi in zip(ends, ends[1:])]
+    assert torch.equal(whole, torch.cat(parts))
+    for u, v in zip(a, b):
+        assert torch.equal(u, v)
