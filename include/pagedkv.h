@@ -572,6 +572,34 @@ pa_status pa_decode_block_fp8(void *out, const void *query, const void *key_cach
                               int32_t *device_status, void *stream);
 
 /*
+ * Chunked prefill attention over E4M3 pools with one scale per block and KV
+ * head, filled by pa_rope_cache_write: pa_prefill's semantics (query_start,
+ * context_lens, max_query_len, window, causal mask) with the pools and scales
+ * of pa_decode_block_fp8.
+ *  workspace         device scratch of at least
+ *                    pa_prefill_block_fp8_workspace_bytes() bytes, 16-byte
+ *                    aligned; calls that run at the same time need their own
+ * A sequence whose query_start entries fall, leave [0, num_query_tokens] or
+ * exceed its context length is not computed and flagged PA_DEV_BAD_CONTEXT_LEN.
+ * Supported: head_dim 128, group 1, 2, 4, 8 or 16.
+ * Arithmetic: both products on tcgen05 tensor cores, f16 operands and f32 sums.
+ * Codes are widened exactly; queries are converted to f16 (exact for |q| in
+ * [2^-14, 65504], others flag PA_DEV_RANGE); weights are rounded to f16 as in
+ * pa_decode_block_fp8.  A NaN value reaches every row of the 256-row tiles that
+ * process its position, also rows before it.
+ */
+size_t pa_prefill_block_fp8_workspace_bytes(void);
+pa_status pa_prefill_block_fp8(void *out, const void *query, const void *key_cache,
+                               const void *value_cache, const float *k_scales,
+                               const float *v_scales, const int32_t *block_tables,
+                               const int32_t *context_lens, const int32_t *query_start,
+                               int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                               int block_size, int max_blocks_per_seq, int num_blocks,
+                               int num_query_tokens, int max_query_len, float scale, int window,
+                               void *workspace, size_t workspace_bytes, int32_t *device_status,
+                               void *stream);
+
+/*
  * Swap of blocks between the pools and a staging buffer ("PagedAttention por
  * dentro", section "Evicción y preemption", strategy 2 "swap": the blocks of
  * a preempted sequence move to CPU memory, freeing device memory, and come

@@ -29,7 +29,7 @@ BLOCK_SIZE = 16
 
 __all__ = ["prefill", "swap_out", "swap_in", "decode", "decode_fp8", "decode_sliding_window", "decode_shared_prefix", "decode_shared_prefix_fp8", "shared_prefix_blocks", "decode_workspace_bytes", "decode_partition_size",
            "plan_step", "StepPlan", "rotary_plan", "RotaryPlan", "rope_cache_write", "decode_block_fp8",
-           "decode_block_fp8_workspace_bytes", "cache_write", "cache_write_fp8", "block_copy", "launch_count", "BlockManager",
+           "decode_block_fp8_workspace_bytes", "prefill_block_fp8", "cache_write", "cache_write_fp8", "block_copy", "launch_count", "BlockManager",
            "PagedKVError", "BLOCK_SIZE", "library_path"]
 
 
@@ -701,6 +701,41 @@ def decode_block_fp8(query, key_cache, value_cache, k_scales, v_scales, block_ta
             D ** -0.5 if scale is None else float(scale), int(window), int(partition_size), ws_ptr, ws_bytes,
             _status_ptr(status), _stream(stream, query))
     check(rc, "pa_decode_block_fp8")
+    return out
+
+
+def prefill_block_fp8(query, key_cache, value_cache, k_scales, v_scales, block_tables, context_lens, query_start,
+                      max_query_len=None, scale=None, *, window=0, out=None, workspace=None, status=None,
+                      stream=None):
+    """Chunked prefill over E4M3 pools with one scale per block and KV head
+    (``pa_prefill_block_fp8``); arguments as ``prefill``.  Returns ``out`` (bf16)."""
+    torch = _torch()
+    N, Hq, D = query.shape
+    B = context_lens.shape[0]
+    NB, Hkv, D = _block_fp8_pools(query, key_cache, value_cache, k_scales, v_scales, block_tables, B)
+    if query_start.shape != (B + 1,):
+        raise ValueError("query_start must be [num_seqs + 1]")
+    dev = _same_device(query, key_cache=key_cache, value_cache=value_cache, k_scales=k_scales,
+                       v_scales=v_scales, block_tables=block_tables, context_lens=context_lens,
+                       query_start=query_start, out=out, workspace=workspace, status=status)
+    with _on(dev, stream):
+        if max_query_len is None:
+            max_query_len = int((query_start[1:] - query_start[:-1]).max().item()) if B else 0
+        if out is None:
+            out = torch.empty(query.shape, dtype=query.dtype, device=query.device)
+        elif out.shape != query.shape or out.dtype != query.dtype:
+            raise ValueError("out must match query")
+        if workspace is None:
+            workspace = torch.empty(lib().pa_prefill_block_fp8_workspace_bytes(), dtype=torch.uint8, device=query.device)
+        rc = lib().pa_prefill_block_fp8(
+            _dev(out, "out"), _dev(query, "query"), _dev(key_cache, "key_cache"),
+            _dev(value_cache, "value_cache"), _dev(k_scales, "k_scales", torch.float32),
+            _dev(v_scales, "v_scales", torch.float32), _dev(block_tables, "block_tables", torch.int32),
+            _dev(context_lens, "context_lens", torch.int32), _dev(query_start, "query_start", torch.int32), B, Hq,
+            Hkv, D, BLOCK_SIZE, block_tables.shape[1], NB, N, int(max_query_len),
+            D ** -0.5 if scale is None else float(scale), int(window), _dev(workspace, "workspace"),
+            workspace.nbytes, _status_ptr(status), _stream(stream, query))
+    check(rc, "pa_prefill_block_fp8")
     return out
 
 

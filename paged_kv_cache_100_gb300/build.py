@@ -17,7 +17,7 @@ LIB = os.path.join(BUILD, "libpagedkv.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CU_SOURCES = ["pa_decode.cu", "pa_cache.cu", "pa_decode_noalloc.cu", "pa_prefill.cu", "pa_plan.cu",
-              "pa_rope.cu", "pa_block8_decode.cu"]
+              "pa_rope.cu", "pa_block8_decode.cu", "pa_block8_prefill.cu"]
 CPP_SOURCES = ["block_manager.cpp"]
 HEADERS = ["pa_device.cuh", "pa_internal.h", "pa_tc.cuh", "pa_block8.cuh"]
 

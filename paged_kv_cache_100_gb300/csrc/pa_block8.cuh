@@ -40,7 +40,8 @@ __device__ __forceinline__ float log2_scale(float x) {
 }
 
 // 2-D view of an E4M3 pool as [num_blocks * num_kv_heads * 16 rows][128 codes],
-// loaded as boxes of 16 rows with 128-byte swizzle.  Defined in pa_block8_decode.cu.
-bool encode_block8_map(CUtensorMap *map, const void *pool, int64_t rows);
+// loaded as boxes of 16 rows, with 128-byte swizzle or as they are.  Defined in
+// pa_block8_decode.cu.
+bool encode_block8_map(CUtensorMap *map, const void *pool, int64_t rows, bool swizzled);
 
 }  // namespace pa

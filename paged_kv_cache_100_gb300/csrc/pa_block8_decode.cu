@@ -480,7 +480,7 @@ size_t workspace_of(int num_seqs, int num_q_heads, int max_parts) {
 template <int NW, int STAGES>
 pa_status launch_decode(const Block8Args &a, const void *kc, const void *vc, int64_t rows, cudaStream_t st) {
     CUtensorMap kmap, vmap;
-    if (!encode_block8_map(&kmap, kc, rows) || !encode_block8_map(&vmap, vc, rows))
+    if (!encode_block8_map(&kmap, kc, rows, true) || !encode_block8_map(&vmap, vc, rows, true))
         return cuda_failure(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
     const size_t smem = Shape<NW, STAGES>::smem(a.part_blocks);
     auto kernel = pa_decode_block8_kernel<NW, STAGES>;
@@ -495,7 +495,7 @@ pa_status launch_decode(const Block8Args &a, const void *kc, const void *vc, int
 
 }  // namespace
 
-bool encode_block8_map(CUtensorMap *map, const void *pool, int64_t rows) {
+bool encode_block8_map(CUtensorMap *map, const void *pool, int64_t rows, bool swizzled) {
     static PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -512,8 +512,8 @@ bool encode_block8_map(CUtensorMap *map, const void *pool, int64_t rows) {
     cuuint32_t box[2] = {kD, kBlockSize};
     cuuint32_t estr[2] = {1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(pool), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace pa

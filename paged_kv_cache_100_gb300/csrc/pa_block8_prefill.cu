@@ -1,0 +1,917 @@
+// Chunked (paged) prefill attention over E4M3 pools with one scale per block of
+// 16 tokens and KV head, on 5th-generation tensor cores ("PagedAttention por
+// dentro", section "Chunked prefill integrado con paged KV"; "KV cache: la
+// memoria de trabajo que sostiene la inferencia LLM", section "Trucos para que
+// el cuaderno sea más fino").  The mathematics of the scales is in
+// pa_block8.cuh: a block's key scale multiplies its 16 columns of scores, the
+// logarithm of its value scale is added to them, and the sum of its weights is
+// divided by the value scale.
+//
+// One CTA computes two 128-row tiles (A, then B) of (token, query head of the
+// group) rows of one sequence and KV head over 128-position K/V tiles.  The
+// second operand of both products is the cache's codes widened to f16 (exact),
+// so queries and weights are f16 too (queries are exact for |q| in
+// [2^-14, 65504]; bf16 weights would be too coarse for the output).
+//   warp 0       TMA producer: both Q tiles, then the codes of each K/V step in
+//                half tiles of four blocks through a ring of kCodeStages;
+//   warp 1       MMA issuer, ping-pong between the tiles:
+//                  S_A(0) S_B(0) | PV_A(j) S_A(j+1) PV_B(j) S_B(j+1) | ...
+//                S = Q K^T and O += P V accumulate in tensor memory, P is read
+//                from tensor memory, written there over its own S;
+//   warps 2..9   softmax of tile A, warps 10..17 of tile B: two threads per row,
+//                64 of the 128 columns of S and O each, one pass over S per step
+//                against an integer reference that rises only when a chunk's
+//                weights would leave f16's range;
+//   warps 18..   widen: Q tiles in place (bf16 to f16), each half tile of codes
+//                into the f16 K or V tile, positions outside the item's range
+//                zeroed in V; they also stage the blocks' scales.
+// Persistent CTAs take items from a ticket counter; barrier phases are counted
+// across items, so an item's loads start under the end of the one before.
+// Every wait is bounded (about a second); one that gives up sets PA_DEV_TIMEOUT,
+// the CTA drains its tensor-core work and returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include <algorithm>
+#include <climits>
+#include <mutex>
+
+#include "pa_block8.cuh"
+#include "pa_device.cuh"
+#include "pa_internal.h"
+#include "pa_tc.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kRows = 128;               // rows per Q tile (M of every MMA)
+constexpr int kQT = 2;                   // Q tiles per CTA
+constexpr int kKv = 128;                 // positions per step (8 blocks)
+constexpr int kD = 128;                  // head_dim
+constexpr int kHalf = 16384;             // one 64-column swizzled region of a tile
+constexpr int kTile = 2 * kHalf;         // 128 rows x 256 bytes
+constexpr int kCols = 64;                // S / O columns per softmax thread (two per row)
+constexpr int kGroup = 2 * kRows;        // softmax threads per Q tile
+constexpr int kWidenWarp0 = 2 + kQT * kGroup / 32;
+constexpr int kWidenThreads = 64;
+constexpr int kThreads = kWidenWarp0 * 32 + kWidenThreads;
+constexpr int kStages = 2;               // f16 K tiles, f16 V tiles
+constexpr int kCodeStages = 3;           // half tiles of codes
+constexpr int kCodeRows = 64;            // positions of a half tile
+constexpr int kCodeBytes = kCodeRows * kD;
+constexpr int kScaleSlots = 4;
+constexpr float kChunkSumMax = 32768.f;  // largest weight sum of a 32-column chunk kept as computed
+constexpr size_t kWorkspaceBytes = 256;  // the ticket counter (rounded up)
+
+// shared memory map (offsets from the 1024-byte aligned dynamic base)
+constexpr int kOffQ = 0;
+constexpr int kOffK = kOffQ + kQT * kTile;
+constexpr int kOffV = kOffK + kStages * kTile;
+constexpr int kOffCode = kOffV + kStages * kTile;
+constexpr int kOffScale = kOffCode + kCodeStages * kCodeBytes;   // float4 [kScaleSlots][8]
+constexpr int kOffRed = kOffScale + kScaleSlots * 8 * 16;        // float [kQT][2 parities][2][128]
+constexpr int kPermMax = 64;
+constexpr int kOffPerm = kOffRed + kQT * 2 * 2 * kRows * 4;      // int [kPermMax]
+constexpr int kOffBar = kOffPerm + kPermMax * 4;
+
+constexpr int kQFull = 0, kQConv = 1, kQFree = 2, kDrain = 3, kCodeFull = 4, kCodeEmpty = kCodeFull + kCodeStages,
+              kKConv = kCodeEmpty + kCodeStages, kKEmpty = kKConv + kStages, kVConv = kKEmpty + kStages,
+              kVEmpty = kVConv + kStages, kSFull = kVEmpty + kStages, kPFull = kSFull + kQT, kPvDone = kPFull + kQT,
+              kOFree = kPvDone + kQT, kItemFull = kOFree + kQT, kItemEmpty = kItemFull + 2,
+              kScaleFull = kItemEmpty + 2, kNumBars = kScaleFull + kScaleSlots;
+constexpr int kOffMisc = kOffBar + kNumBars * 8;                 // TMEM slot, failure flag, item order, item queue [2]
+constexpr int kSmemBytes = kOffMisc + 32;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+constexpr uint32_t kTmemCols = 512;      // S_A, S_B, O_A, O_B
+__device__ __forceinline__ uint32_t col_s(int x) { return (uint32_t)(x * kKv); }
+__device__ __forceinline__ uint32_t col_o(int x) { return (uint32_t)(kQT * kKv + x * kD); }
+
+struct PrefillArgs {
+    void *out;
+    const int32_t *block_tables;
+    const int32_t *context_lens;
+    const int32_t *query_start;
+    const float *k_scales;
+    const float *v_scales;
+    int32_t *status;
+    int num_seqs, num_q_heads, num_kv_heads, group;
+    int max_blocks, num_blocks;
+    int num_query_tokens, max_query_len;
+    int window;
+    float scale_log2;
+    int n_mt;                            // pair tiles per (sequence, KV head)
+    int num_items;
+    unsigned int *work_counter;
+};
+
+__device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, volatile int *fail, int32_t *status) {
+    if (*fail) return false;
+    if (mbar_wait_bounded(bar, parity)) return true;
+    *fail = 1;
+    report(status, PA_DEV_TIMEOUT);
+    return false;
+}
+
+// A bounded wait whose outcome is the same for every lane of the warp (the
+// tensor-memory instructions after it are warp-wide).
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *fail, int32_t *status) {
+    return __all_sync(0xffffffffu, wait_or_fail(bar, parity, fail, status));
+}
+
+// pairs of floats for f32x2 arithmetic
+__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t x, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// 2^(a - b) for references a <= b that are integers or -inf: exact, 0 when a is
+// -inf or far below b.
+__device__ __forceinline__ float pow2_diff(float a, float b) {
+    if (a == b) return 1.f;
+    if (!(a > -INFINITY) || !(b - a < 256.f)) return 0.f;
+    return ldexpf(1.f, (int)(a - b));
+}
+
+// A block's scales as the softmax uses them: x = key scale * softmax scale *
+// log2(e), y = log2 of the value scale, z = 1 / value scale.
+//
+// Weights of the 32-column chunk of S at taddr (its first column is position kc,
+// its two blocks' scales e[0], e[1]) written over it as 16 f16 pairs.  A lane
+// whose first attempt summed past the limit (over) first raises its reference to
+// the next integer at or above the chunk's largest attended exponent.  Returns
+// (weights divided by the value scales, summed; reference).  Out of line, so
+// that the common path keeps its registers; called by all lanes of a warp.
+__device__ __noinline__ float2 chunk_weights_again(uint32_t taddr, const float4 *e, float ref, bool over, bool masked,
+                                                   int kc, int qpos, int wlo) {
+    uint32_t v[32];
+    tmem_ld32(taddr, v);
+    tmem_wait_ld();
+    if (over) {
+        float rmax = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (!masked || (kc + i <= qpos && kc + i >= wlo))
+                rmax = fmaxf(rmax, fmaf(__uint_as_float(v[i]), e[i >> 4].x, e[i >> 4].y));
+        const float nref = ceilf(rmax);
+        if (nref > ref) ref = nref;      // else scores that are not finite: as computed before
+    }
+    uint32_t pp[16];
+    float sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        float p0 = ex2_fast(fmaf(__uint_as_float(v[i]), e[i >> 4].x, e[i >> 4].y - ref));
+        float p1 = ex2_fast(fmaf(__uint_as_float(v[i + 1]), e[i >> 4].x, e[i >> 4].y - ref));
+        if (masked) {
+            if (!(kc + i <= qpos && kc + i >= wlo)) p0 = 0.f;
+            if (!(kc + i + 1 <= qpos && kc + i + 1 >= wlo)) p1 = 0.f;
+        }
+        sum[i >> 4] += p0 + p1;
+        pp[i >> 1] = pack_f16x2(p0, p1);
+    }
+    tmem_st16(taddr, pp);
+    return make_float2(fmaf(sum[0], e[0].z, sum[1] * e[1].z), ref);
+}
+
+// Scales the f16 weights of this thread's two 32-column chunks by f0 and f1.
+__device__ __noinline__ void scale_chunk_weights(uint32_t taddr, float f0, float f1) {
+#pragma unroll 1
+    for (int c = 0; c < 64; c += 32) {
+        const float f = c == 0 ? f0 : f1;
+        uint32_t w[32];
+        tmem_ld32(taddr + c, w);
+        tmem_wait_ld();
+        uint32_t q[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) q[i] = pack_f16x2(f16lo(w[i]) * f, f16hi(w[i]) * f);
+        tmem_st16(taddr + c, q);
+    }
+    tmem_wait_st();
+}
+
+// The two warps of a softmax group that hold the same 32 rows meet here.
+__device__ __forceinline__ void pair_sync(int x, int quarter) {
+    asm volatile("bar.sync %0, 64;" ::"r"(5 + 4 * x + quarter) : "memory");
+}
+
+// AND of `v` over the threads of softmax group x.
+__device__ __forceinline__ bool group_all(int x, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(3 + x), "n"(kGroup)
+        : "memory");
+    return r != 0;
+}
+
+// Two 128-row Q tiles of one sequence and KV head against a range of positions.
+struct Item {
+    int b, kvh;
+    int q0, T, C;       // first query row of the chunk, its tokens, context before it
+    int t0;             // first token of tile A
+    int kv_lo, kv_hi, blk_lo, blk_hi, n_tiles;
+    bool has_b;
+};
+
+__device__ __forceinline__ bool describe_item(const PrefillArgs &a, int item, bool by_length, bool say, const int *perm,
+                                              Item &d) {
+    const int tok_per_tile = kRows / a.group;
+    const int lmax = a.max_blocks * kBlockSize;
+    // by_length: every group's longest tile, then every group's next one, ...;
+    // else the tiles of a (sequence, KV head) together, longest first
+    const int groups = a.num_seqs * a.num_kv_heads;
+    const int x = by_length ? item / groups : item % a.n_mt;
+    const int rest = by_length ? item - x * groups : item / a.n_mt;
+    d.kvh = rest % a.num_kv_heads;
+    d.b = rest / a.num_kv_heads;
+    if (perm != nullptr) d.b = perm[d.b];
+    d.q0 = a.query_start[d.b];
+    const int end = a.query_start[d.b + 1];
+    const int L = a.context_lens[d.b];
+    const bool first = say && x == 0 && d.kvh == 0;
+    if (d.q0 < 0 || end < d.q0 || end > a.num_query_tokens || end - d.q0 > L || L > lmax) {
+        if (first) report(a.status, PA_DEV_BAD_CONTEXT_LEN);
+        return false;
+    }
+    d.T = end - d.q0;
+    if (first && d.T > a.max_query_len) report(a.status, PA_DEV_BAD_QUERY_LEN);
+    d.t0 = (a.n_mt - 1 - x) * kQT * tok_per_tile;
+    if (d.t0 >= d.T) return false;
+    d.C = L - d.T;
+    d.kv_hi = d.C + min(d.T, d.t0 + kQT * tok_per_tile);
+    d.kv_lo = a.window > 0 ? max(0, d.C + d.t0 + 1 - a.window) : 0;
+    d.blk_lo = d.kv_lo / kBlockSize;
+    d.blk_hi = (d.kv_hi + kBlockSize - 1) / kBlockSize;
+    d.has_b = d.t0 + tok_per_tile < d.T;
+    d.n_tiles = (d.blk_hi - d.blk_lo + 7) / 8;
+    return true;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    pa_prefill_block8_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                             const __grid_constant__ CUtensorMap vmap, const PrefillArgs a) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int tok_per_tile = kRows / a.group;
+
+    extern __shared__ __align__(1024) uint8_t base[];
+    if (smem_u32(base) & 1023u) {
+        if (threadIdx.x == 0) report(a.status, PA_DEV_SMEM_ALIGN);
+        return;
+    }
+    uint8_t *sQ = base + kOffQ, *sK = base + kOffK, *sV = base + kOffV, *sCode = base + kOffCode;
+    float4 *s_scale = reinterpret_cast<float4 *>(base + kOffScale);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(base + kOffBar);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(base + kOffMisc);
+    volatile int *fail = reinterpret_cast<volatile int *>(base + kOffMisc + 4);
+    volatile int *s_order = reinterpret_cast<volatile int *>(base + kOffMisc + 8);
+    volatile int *s_item = reinterpret_cast<volatile int *>(base + kOffMisc + 16);   // [2]
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kNumBars; ++i) {
+            int n = 1;
+            if (i == kQConv || (i >= kCodeEmpty && i < kCodeEmpty + kCodeStages) || (i >= kKConv && i < kKConv + kStages) ||
+                (i >= kVConv && i < kVConv + kStages))
+                n = kWidenThreads;
+            if ((i >= kPFull && i < kPFull + kQT) || (i >= kOFree && i < kOFree + kQT)) n = kGroup;
+            if (i >= kItemEmpty && i < kItemEmpty + 2) n = 1 + kQT * kGroup + kWidenThreads;
+            mbar_init(&bars[i], n);
+        }
+        *fail = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&qmap);
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+    }
+    if (warp == 2) {
+        // item order: longest first across all groups when the chunks bring more
+        // tokens than the contexts held before (causal tiles from short to long);
+        // else a group's tiles together, their K/V shared in L2
+        long long cached = 0, fresh = 0;
+        for (int i = lane; i < a.num_seqs; i += 32) {
+            const int T = a.query_start[i + 1] - a.query_start[i];
+            const int L = a.context_lens[i];
+            fresh += T > 0 ? T : 0;
+            cached += L - T > 0 ? L - T : 0;
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) {
+            cached += __shfl_xor_sync(0xffffffffu, cached, o);
+            fresh += __shfl_xor_sync(0xffffffffu, fresh, o);
+        }
+        if (lane == 0) *s_order = cached < fresh ? 1 : 0;
+        if (a.num_seqs <= kPermMax) {
+            // sequences longest context first, so that the call ends on short ones
+            int *perm = reinterpret_cast<int *>(base + kOffPerm);
+            for (int i = lane; i < a.num_seqs; i += 32) {
+                const int li = a.context_lens[i];
+                int r = 0;
+                for (int j = 0; j < a.num_seqs; ++j) {
+                    const int lj = a.context_lens[j];
+                    r += (lj > li) | ((lj == li) & (j < i));
+                }
+                perm[r] = i;
+            }
+        }
+    }
+    if (warp == 1) tmem_alloc(tslot, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    const bool by_length = *s_order != 0;
+    const int *perm = a.num_seqs <= kPermMax ? reinterpret_cast<const int *>(base + kOffPerm) : nullptr;
+
+    // the next item of a consumer role, -1 at the end (or after a wait gave up)
+    auto next_item = [&](int it) -> int {
+        const int slot = it & 1;
+        const int item = wait_or_fail(&bars[kItemFull + slot], (it >> 1) & 1, fail, a.status) ? s_item[slot] : -1;
+        mbar_arrive(&bars[kItemEmpty + slot]);
+        return item;
+    };
+
+    if (warp == 0) {
+        // ---------------- TMA producer (and item fetch) ----------------
+        if (lane == 0) {
+            int q_issued = -1;
+            uint32_t code = 0;                      // half tiles issued
+            bool ok = true;
+            for (int it = 0;; ++it) {
+                int item = -1;
+                Item d;
+                while (ok) {
+                    const int t = (int)atomicAdd(a.work_counter, 1u);
+                    if (t >= a.num_items) break;
+                    if (describe_item(a, t, by_length, true, perm, d)) {
+                        item = t;
+                        break;
+                    }
+                }
+                const int slot = it & 1;
+                if (it >= 2 && !wait_or_fail(&bars[kItemEmpty + slot], ((it >> 1) - 1) & 1, fail, a.status)) item = -1;
+                s_item[slot] = item;
+                mbar_arrive(&bars[kItemFull + slot]);
+                if (item < 0) break;
+                // Q once the last QK^T of the item before has run
+                if (it >= 1 && !wait_or_fail(&bars[kQFree], (it - 1) & 1, fail, a.status)) {
+                    ok = false;
+                    continue;
+                }
+                const int nq = d.has_b ? kQT : 1;
+                mbar_arrive_expect_tx(&bars[kQFull], nq * kTile);
+                for (int x = 0; x < nq; ++x) {
+                    const int row0 = d.q0 + d.t0 + x * tok_per_tile;
+                    tma_load_4d(sQ + x * kTile, &qmap, 0, 0, d.kvh, row0, &bars[kQFull]);
+                    tma_load_4d(sQ + x * kTile + kHalf, &qmap, 64, 0, d.kvh, row0, &bars[kQFull]);
+                }
+                q_issued = it;
+                const int32_t *trow = a.block_tables + (int64_t)d.b * a.max_blocks;
+                for (int j = 0; ok && j < d.n_tiles; ++j) {
+                    int rows[8];
+                    const int blk0 = d.blk_lo + 8 * j, nb = min(8, d.blk_hi - blk0);
+                    for (int i = 0; i < nb; ++i) {
+                        int phys = trow[blk0 + i];
+                        if ((unsigned)phys >= (unsigned)a.num_blocks) {
+                            report(a.status, PA_DEV_BAD_BLOCK_ID);
+                            phys = 0;
+                        }
+                        rows[i] = (phys * a.num_kv_heads + d.kvh) * kBlockSize;
+                    }
+                    // K's two halves, then V's
+                    for (int h = 0; h < 4; ++h, ++code) {
+                        const int s = code % kCodeStages;
+                        if (code >= kCodeStages &&
+                            !wait_or_fail(&bars[kCodeEmpty + s], ((code / kCodeStages) - 1) & 1, fail, a.status)) {
+                            ok = false;
+                            break;
+                        }
+                        const int first = (h & 1) * 4, n = max(0, min(4, nb - first));
+                        const CUtensorMap *map = h < 2 ? &kmap : &vmap;
+                        mbar_arrive_expect_tx(&bars[kCodeFull + s], n * kBlockSize * kD);
+                        for (int i = 0; i < n; ++i)
+                            tma_load_2d(sCode + s * kCodeBytes + i * kBlockSize * kD, map, 0, rows[first + i],
+                                        &bars[kCodeFull + s]);
+                    }
+                }
+            }
+            // no copy of ours may still be landing when the CTA leaves
+            if (q_issued >= 0) (void)mbar_wait_bounded(&bars[kQFull], q_issued & 1);
+            for (uint32_t j = code > kCodeStages ? code - kCodeStages : 0; j < code; ++j)
+                (void)mbar_wait_bounded(&bars[kCodeFull + j % kCodeStages], (j / kCodeStages) & 1);
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer ----------------
+        if (lane == 0) {
+            constexpr uint32_t idS = idesc_f16_f32(kRows, kKv, false);
+            constexpr uint32_t idPV = idesc_f16_f32(kRows, kD, true);
+            const uint32_t q_u = smem_u32(sQ), k_u = smem_u32(sK), v_u = smem_u32(sV);
+            uint32_t gstep = 0;
+            uint32_t pcount[kQT] = {0, 0};
+            bool ok = true;
+            auto issue_s = [&](int x, uint32_t gs) {
+                const uint32_t qb = q_u + x * kTile, kb = k_u + (gs % kStages) * kTile;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t o = (k >> 2) * kHalf + (k & 3) * 32;
+                    umma_bf16(tmem + col_s(x), sw128_desc(qb + o, 16, 1024), sw128_desc(kb + o, 16, 1024), idS,
+                              k > 0 ? 1u : 0u);
+                }
+                umma_commit(&bars[kSFull + x]);
+            };
+            // P of tokens [16 k, 16 k + 16): f16 pairs from column 32 (k / 2) + 8 (k % 2) of the S buffer
+            auto issue_pv = [&](int x, uint32_t gs, int j, int it) -> bool {
+                if (!wait_or_fail(&bars[kPFull + x], pcount[x] & 1, fail, a.status)) return false;
+                ++pcount[x];
+                // the first P.V of an item overwrites O: the item before must have read it out
+                if (j == 0 && it >= 1 && !wait_or_fail(&bars[kOFree + x], (it - 1) & 1, fail, a.status)) return false;
+                tc_fence_after();
+                const uint32_t vb = v_u + (gs % kStages) * kTile;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    umma_bf16_tmem_a(tmem + col_o(x), tmem + col_s(x) + 32 * (k >> 1) + 8 * (k & 1),
+                                     sw128_desc(vb + k * 2048, kHalf, 1024), idPV, (j > 0 || k > 0) ? 1u : 0u);
+                umma_commit(&bars[kPvDone + x]);
+                return true;
+            };
+            for (int it = 0; ok; ++it) {
+                const int item = next_item(it);
+                if (item < 0) break;
+                Item d;
+                describe_item(a, item, by_length, false, perm, d);
+                const int n = d.n_tiles;
+                if (!wait_or_fail(&bars[kQConv], it & 1, fail, a.status) ||
+                    !wait_or_fail(&bars[kKConv + gstep % kStages], (gstep / kStages) & 1, fail, a.status))
+                    break;
+                tc_fence_after();
+                issue_s(0, gstep);
+                if (d.has_b) issue_s(1, gstep);
+                umma_commit(&bars[kKEmpty + gstep % kStages]);
+                if (n == 1) umma_commit(&bars[kQFree]);
+                for (int j = 0; ok && j < n; ++j) {
+                    const uint32_t gs = gstep + j, gk = gs + 1;
+                    const bool more = j + 1 < n;
+                    if (!wait_or_fail(&bars[kVConv + gs % kStages], (gs / kStages) & 1, fail, a.status) ||
+                        !issue_pv(0, gs, j, it)) {
+                        ok = false;
+                        break;
+                    }
+                    if (more) {
+                        if (!wait_or_fail(&bars[kKConv + gk % kStages], (gk / kStages) & 1, fail, a.status)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        issue_s(0, gk);
+                    }
+                    if (d.has_b && !issue_pv(1, gs, j, it)) {
+                        ok = false;
+                        break;
+                    }
+                    umma_commit(&bars[kVEmpty + gs % kStages]);
+                    if (more) {
+                        if (d.has_b) issue_s(1, gk);
+                        umma_commit(&bars[kKEmpty + gk % kStages]);
+                        if (j + 2 == n) umma_commit(&bars[kQFree]);
+                    }
+                }
+                umma_commit(&bars[kDrain]);          // every MMA of the item has completed once it flips
+                gstep += n;
+            }
+        }
+    } else if (warp >= kWidenWarp0) {
+        // ---------------- widening ----------------
+        const int ct = threadIdx.x - kWidenWarp0 * 32;
+        uint32_t gstep = 0, code = 0;
+        bool ok = true, beyond = false;
+        for (int it = 0;; ++it) {
+            const int item = next_item(it);
+            if (item < 0) break;
+            Item d;
+            describe_item(a, item, by_length, false, perm, d);
+            if (!ok || !wait_or_fail(&bars[kQFull], it & 1, fail, a.status)) {
+                ok = false;
+                continue;
+            }
+            // the scales of the item's first step, one thread per block
+            const int32_t *trow = a.block_tables + (int64_t)d.b * a.max_blocks;
+            float ks = 0.f, vs = 1.f;
+            bool has = false;
+            auto fetch_scales = [&](int j) {
+                const int blk = d.blk_lo + 8 * j + ct;
+                has = ct < 8 && blk < d.blk_hi;
+                if (has) {
+                    int phys = trow[blk];
+                    phys = (unsigned)phys < (unsigned)a.num_blocks ? phys : 0;
+                    const int64_t at = (int64_t)phys * a.num_kv_heads + d.kvh;
+                    ks = a.k_scales[at];
+                    vs = a.v_scales[at];
+                }
+            };
+            fetch_scales(0);
+            uint4 *q = reinterpret_cast<uint4 *>(sQ);
+#pragma unroll 4
+            for (int c = ct; c < (d.has_b ? kQT : 1) * kTile / 16; c += kWidenThreads) {
+                const uint4 w = q[c];
+                beyond |= bf16x2_beyond_f16(w.x) | bf16x2_beyond_f16(w.y) | bf16x2_beyond_f16(w.z) | bf16x2_beyond_f16(w.w);
+                q[c] = make_uint4(pack_f16x2(bf16lo(w.x), bf16hi(w.x)), pack_f16x2(bf16lo(w.y), bf16hi(w.y)),
+                                  pack_f16x2(bf16lo(w.z), bf16hi(w.z)), pack_f16x2(bf16lo(w.w), bf16hi(w.w)));
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&bars[kQConv]);
+            for (int j = 0; ok && j < d.n_tiles; ++j) {
+                const uint32_t gs = gstep + j;
+                const int st = gs % kStages;
+                const uint32_t ph = (gs / kStages) & 1u;
+                const int k0 = (d.blk_lo + 8 * j) * kBlockSize;
+                const bool edge = k0 < d.kv_lo || k0 + kKv > d.kv_hi;
+                for (int h = 0; h < 4; ++h, ++code) {
+                    const int s = code % kCodeStages;
+                    if (!wait_or_fail(&bars[kCodeFull + s], (code / kCodeStages) & 1, fail, a.status) ||
+                        (!(h & 1) && gs >= kStages &&
+                         !wait_or_fail(&bars[(h < 2 ? kKEmpty : kVEmpty) + st], ph ^ 1u, fail, a.status))) {
+                        ok = false;
+                        break;
+                    }
+                    if (h == 0) {
+                        // softmax is at most two steps behind the K tile that is free now
+                        if (ct < 8) {
+                            const float sv = has ? value_scale(vs, a.status) : 1.f;
+                            s_scale[(gs % kScaleSlots) * 8 + ct] =
+                                make_float4(has ? ks * a.scale_log2 : 0.f, log2_scale(sv), 1.f / sv, 0.f);
+                        }
+                        if (ct < 32) {
+                            __syncwarp();
+                            if (ct == 0) mbar_arrive(&bars[kScaleFull + gs % kScaleSlots]);
+                        }
+                        if (j + 1 < d.n_tiles) fetch_scales(j + 1);
+                    }
+                    // 16 codes of a row become two 16-byte chunks of f16 in one of the
+                    // tile's 64-column halves; threads of the two halves write their
+                    // chunks in opposite order, so that eight threads of a row never
+                    // meet in a bank
+                    const uint4 *src = reinterpret_cast<const uint4 *>(sCode + s * kCodeBytes);
+                    uint8_t *dst = (h < 2 ? sK : sV) + st * kTile;
+                    const int c16 = ct & 7, half = c16 >> 2, swap = half;
+#pragma unroll 4
+                    for (int i = 0; i < kCodeRows * 8 / kWidenThreads; ++i) {
+                        const int rr = (ct >> 3) + i * (kWidenThreads / 8);
+                        const int r = (h & 1) * kCodeRows + rr;
+                        const uint4 w = src[rr * 8 + c16];
+                        uint4 x, y;
+                        e4m3x4_to_f16x2x2(w.x, x.x, x.y);
+                        e4m3x4_to_f16x2x2(w.y, x.z, x.w);
+                        e4m3x4_to_f16x2x2(w.z, y.x, y.y);
+                        e4m3x4_to_f16x2x2(w.w, y.z, y.w);
+                        if (edge && h >= 2 && (k0 + r < d.kv_lo || k0 + r >= d.kv_hi)) x = y = make_uint4(0, 0, 0, 0);
+                        uint8_t *row = dst + half * kHalf + r * 128;
+                        const int c = 2 * (c16 & 3);
+                        *reinterpret_cast<uint4 *>(row + (((c + swap) ^ (r & 7)) << 4)) = swap ? y : x;
+                        *reinterpret_cast<uint4 *>(row + (((c + 1 - swap) ^ (r & 7)) << 4)) = swap ? x : y;
+                    }
+                    mbar_arrive(&bars[kCodeEmpty + s]);
+                    if (h & 1) {
+                        fence_proxy_async_smem();
+                        mbar_arrive(&bars[(h < 2 ? kKConv : kVConv) + st]);
+                    } else {
+                        fence_proxy_async_smem();
+                    }
+                }
+            }
+            gstep += d.n_tiles;
+        }
+        if (beyond) report(a.status, PA_DEV_RANGE);
+    } else {
+        // ---------------- softmax groups ----------------
+        const int x = (warp - 2) / (kGroup / 32);
+        const int gw = (warp - 2) % (kGroup / 32);
+        const int quarter = warp & 3;
+        const int part = gw >> 2;                     // columns [64 part, + 64)
+        const int r = quarter * 32 + lane;            // tile row = TMEM lane
+        const int tr = r / a.group;
+        const uint32_t lane_off = ((uint32_t)(quarter * 32) << 16) + part * kCols;
+        const uint32_t s_base = tmem + col_s(x) + lane_off;
+        const uint32_t o_base = tmem + col_o(x) + lane_off;
+        float *red = reinterpret_cast<float *>(base + kOffRed) + x * 2 * 2 * kRows;
+        uint32_t sc = 0;      // S / P / P.V phases of this group (global)
+        uint32_t ex = 0;      // exchanges through `red` (their slot alternates)
+        uint32_t gstep = 0;
+        bool ok = true;
+        for (int it = 0;; ++it) {
+            const int slot = it & 1;
+            const bool got_item = warp_wait(&bars[kItemFull + slot], (it >> 1) & 1, fail, a.status);
+            const int item = got_item ? s_item[slot] : -1;
+            mbar_arrive(&bars[kItemEmpty + slot]);
+            // all threads of the group decide alike, so that they reach its named barriers equally often
+            if (!group_all(x, item >= 0 && ok && !*fail)) break;
+            Item d;
+            describe_item(a, item, by_length, false, perm, d);
+            if (x == 0 || d.has_b) {
+                const int tx0 = d.t0 + x * tok_per_tile;
+                const int ntok = min(tok_per_tile, d.T - tx0);
+                const bool real = tr < ntok;
+                // this row attends to positions [wlo, qpos]; a 32-column chunk needs no
+                // mask when it lies inside every row's range of the tile
+                const int qpos = d.C + tx0 + min(tr, ntok - 1);
+                const int qpos_lo = d.C + tx0, qpos_hi = d.C + tx0 + ntok - 1;
+                const int wlo = a.window > 0 ? qpos + 1 - a.window : INT_MIN;
+                // The row's reference (log2 units): an integer, or -inf before the row
+                // has seen a position; O and l are relative to it.
+                float m_used = -INFINITY, l = 0.f;
+                for (int j = 0; j < d.n_tiles; ++j) {
+                    const uint32_t gs = gstep + j;
+                    const bool got = ok && warp_wait(&bars[kSFull + x], sc & 1, fail, a.status) &&
+                                     warp_wait(&bars[kScaleFull + gs % kScaleSlots], (gs / kScaleSlots) & 1, fail, a.status);
+                    const int k0 = (d.blk_lo + 8 * j) * kBlockSize + part * kCols;
+                    const float4 *scales = s_scale + (gs % kScaleSlots) * 8 + part * (kCols / kBlockSize);
+                    // One pass over S: a chunk's weights 2^(s ck + lv - ref) replace it in
+                    // f16, unless they sum to more than 2^15: then ref rises to the next
+                    // integer at or above the chunk's largest exponent and the chunk is
+                    // computed again.  Each chunk keeps the reference it was written with.
+                    float mref = m_used;
+                    float cref0 = m_used, cref1 = m_used, csum0 = 0.f, csum1 = 0.f;
+                    if (got) {
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < kCols; c += 32) {
+                            const int kc = k0 + c;
+                            const bool masked = (kc + 31 > qpos_lo) || (a.window > 0 && kc < qpos_hi + 1 - a.window);
+                            const float4 *e = scales + (c >> 4);
+                            uint32_t pp[16];
+                            float sum[2];
+                            {
+                                uint32_t v[32];
+                                tmem_ld32(s_base + c, v);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int blk = 0; blk < 2; ++blk) {
+                                    const float4 sb = e[blk];
+                                    const uint64_t k2 = f2_pack(sb.x, sb.x), nm2 = f2_pack(sb.y - mref, sb.y - mref);
+                                    uint64_t ps2 = f2_pack(0.f, 0.f);
+#pragma unroll
+                                    for (int i = 16 * blk; i < 16 * blk + 16; i += 2) {
+                                        float x0, x1;
+                                        f2_unpack(f2_fma(f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), k2, nm2), x0, x1);
+                                        float p0 = ex2_fast(x0), p1 = ex2_fast(x1);
+                                        if (masked) {
+                                            if (!(kc + i <= qpos && kc + i >= wlo)) p0 = 0.f;
+                                            if (!(kc + i + 1 <= qpos && kc + i + 1 >= wlo)) p1 = 0.f;
+                                        }
+                                        ps2 = f2_add(ps2, f2_pack(p0, p1));
+                                        pp[i >> 1] = pack_f16x2(p0, p1);
+                                    }
+                                    float lo, hi;
+                                    f2_unpack(ps2, lo, hi);
+                                    sum[blk] = lo + hi;
+                                }
+                            }
+                            const bool over = !(sum[0] + sum[1] <= kChunkSumMax);
+                            float psum = fmaf(sum[0], e[0].z, sum[1] * e[1].z);
+                            if (__any_sync(0xffffffffu, over)) {
+                                // the whole warp; S is still in place
+                                const float2 r2 = chunk_weights_again(s_base + c, e, mref, over, masked, kc, qpos, wlo);
+                                psum = r2.x;
+                                mref = r2.y;
+                            } else {
+                                tmem_st16(s_base + c, pp);
+                            }
+                            if (c == 0) {
+                                cref0 = mref;
+                                csum0 = psum;
+                            } else {
+                                cref1 = mref;
+                                csum1 = psum;
+                            }
+                        }
+                        tmem_wait_st();
+                    }
+                    // the two threads of the row agree on the larger reference
+                    const int rp = ex & 1;
+                    ++ex;
+                    red[(rp * 2 + part) * kRows + r] = mref;
+                    pair_sync(x, quarter);
+                    const float rref = fmaxf(mref, red[(rp * 2 + (part ^ 1)) * kRows + r]);
+                    const uint32_t my_sc = sc++;
+                    if (!got) {
+                        ok = false;
+                        continue;
+                    }
+                    // chunks written against a smaller reference are scaled by the exact
+                    // power of two between them
+                    const float f0 = pow2_diff(cref0, rref), f1 = pow2_diff(cref1, rref);
+                    if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) scale_chunk_weights(s_base, f0, f1);
+                    const float psum = csum0 * f0 + csum1 * f1;
+                    // O and l follow when the reference moved, once every P.V of this
+                    // tile issued so far has landed
+                    const bool need = rref > m_used;
+                    const float alpha = need ? pow2_diff(m_used, rref) : 1.f;
+                    if (j >= 1 && __any_sync(0xffffffffu, need)) {
+                        if (!warp_wait(&bars[kPvDone + x], (my_sc - 1) & 1, fail, a.status)) {
+                            ok = false;
+                            continue;
+                        }
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < kCols; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(o_base + c, o);
+                            tmem_wait_ld();
+                            const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                float r0, r1;
+                                f2_unpack(f2_mul(f2_pack(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), a2), r0, r1);
+                                o[i] = __float_as_uint(r0);
+                                o[i + 1] = __float_as_uint(r1);
+                            }
+                            tmem_st32(o_base + c, o);
+                        }
+                        tmem_wait_st();
+                    }
+                    if (need) {
+                        l *= alpha;
+                        m_used = rref;
+                    }
+                    l += psum;
+                    tc_fence_before();
+                    mbar_arrive(&bars[kPFull + x]);
+                }
+                // the row sum is the two parts' sums
+                const int sx = ex & 1;
+                ++ex;
+                red[(sx * 2 + part) * kRows + r] = l;
+                pair_sync(x, quarter);
+                const float l_row = l + red[(sx * 2 + (part ^ 1)) * kRows + r];
+                const bool drained = warp_wait(&bars[kDrain], it & 1, fail, a.status);
+                if (__all_sync(0xffffffffu, ok) && drained) {
+                    tc_fence_after();
+                    const float inv = l_row == 0.f ? 0.f : 1.f / l_row;
+                    __nv_bfloat16 *orow =
+                        static_cast<__nv_bfloat16 *>(a.out) +
+                        ((int64_t)(d.q0 + tx0 + tr) * a.num_q_heads + d.kvh * a.group + (r % a.group)) * kD + part * kCols;
+#pragma unroll 1
+                    for (int c = 0; c < kCols; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o_base + c, o);
+                        tmem_wait_ld();
+                        if (real) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    w[k] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * k]) * inv,
+                                                       __uint_as_float(o[8 * q + 2 * k + 1]) * inv);
+                                *reinterpret_cast<uint4 *>(orow + c + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        }
+                    }
+                }
+                if (!drained) ok = false;
+            } else {
+                // tile B has no rows in this item: keep the drain phase in step
+                if (!warp_wait(&bars[kDrain], it & 1, fail, a.status)) ok = false;
+            }
+            tc_fence_before();
+            mbar_arrive(&bars[kOFree + x]);          // O has been read out
+            gstep += d.n_tiles;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// The query as [rows][KV head][head of the group][head_dim]: a box of 128 / group
+// rows x group heads x 64 elements is one half of a 128-row tile.
+bool encode_query_map(CUtensorMap *map, const void *query, int rows, int num_q_heads, int num_kv_heads) {
+    static PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    if (enc == nullptr) return false;
+    const int group = num_q_heads / num_kv_heads;
+    cuuint64_t dims[4] = {kD, (cuuint64_t)group, (cuuint64_t)num_kv_heads, (cuuint64_t)rows};
+    cuuint64_t strides[3] = {kD * 2, (cuuint64_t)group * kD * 2, (cuuint64_t)num_q_heads * kD * 2};
+    cuuint32_t box[4] = {64, (cuuint32_t)group, 1, (cuuint32_t)(kRows / group)};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(query), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sms() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+        (void)cudaGetLastError();
+        return 152;
+    }
+    return n;
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" size_t pa_prefill_block_fp8_workspace_bytes(void) { return kWorkspaceBytes; }
+
+extern "C" pa_status pa_prefill_block_fp8(void *out, const void *query, const void *key_cache, const void *value_cache,
+                                          const float *k_scales, const float *v_scales, const int32_t *block_tables,
+                                          const int32_t *context_lens, const int32_t *query_start, int num_seqs,
+                                          int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                          int max_blocks_per_seq, int num_blocks, int num_query_tokens,
+                                          int max_query_len, float scale, int window, void *workspace,
+                                          size_t workspace_bytes, int32_t *device_status, void *stream) {
+    if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
+        block_size != kBlockSize || max_blocks_per_seq < 0 || max_blocks_per_seq > 0x7fffffff / kBlockSize ||
+        num_blocks <= 0 || num_query_tokens < 0 || max_query_len < 0 || window < 0 || !(scale == scale))
+        return PA_ERR_INVALID_ARG;
+    const int group = num_q_heads / num_kv_heads;
+    if (head_dim != kD || (group != 1 && group != 2 && group != 4 && group != 8 && group != 16))
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || num_query_tokens == 0 || max_query_len == 0) return PA_OK;
+    if (!out || !query || !key_cache || !value_cache || !k_scales || !v_scales || !context_lens || !query_start ||
+        (!block_tables && max_blocks_per_seq > 0))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(query) || !aligned16(key_cache) || !aligned16(value_cache) ||
+        ((reinterpret_cast<uintptr_t>(k_scales) | reinterpret_cast<uintptr_t>(v_scales) |
+          reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens) |
+          reinterpret_cast<uintptr_t>(query_start)) & 3u))
+        return PA_ERR_INVALID_ARG;
+    if (workspace == nullptr || workspace_bytes < kWorkspaceBytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
+    const int64_t rows = (int64_t)num_blocks * num_kv_heads * kBlockSize;
+    const int64_t tiles = ((int64_t)max_query_len * group + kQT * kRows - 1) / (kQT * kRows);
+    const int64_t items = tiles * num_kv_heads * num_seqs;
+    if (rows >= ((int64_t)1 << 31) || items >= ((int64_t)1 << 31) - kThreads) return PA_ERR_UNSUPPORTED;
+    CUtensorMap qmap, kmap, vmap;
+    if (!encode_query_map(&qmap, query, num_query_tokens, num_q_heads, num_kv_heads) ||
+        !encode_block8_map(&kmap, key_cache, rows, false) || !encode_block8_map(&vmap, value_cache, rows, false))
+        return cuda_failure(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
+    PrefillArgs a = {};
+    a.out = out;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.query_start = query_start;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.status = device_status;
+    a.num_seqs = num_seqs;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.group = group;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.num_query_tokens = num_query_tokens;
+    a.max_query_len = max_query_len;
+    a.window = window;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.n_mt = (int)tiles;
+    a.num_items = (int)items;
+    a.work_counter = static_cast<unsigned int *>(workspace);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(unsigned int), st);
+    if (e != cudaSuccess) return cuda_failure(e, "cudaMemsetAsync(prefill ticket)");
+    e = cudaFuncSetAttribute(pa_prefill_block8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return cuda_failure(e, "cudaFuncSetAttribute(block-scaled prefill)");
+    const int64_t grid = std::min<int64_t>(items, sms());
+    e = launch_chained(pa_prefill_block8_kernel, dim3((unsigned)grid), dim3(kThreads), (size_t)kSmemBytes, st, qmap,
+                       kmap, vmap, a);
+    if (e != cudaSuccess) return cuda_failure(e, "pa_prefill_block8_kernel launch");
+    count_launches(1);
+    return PA_OK;
+}

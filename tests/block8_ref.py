@@ -116,14 +116,15 @@ def write_blocks(rows, slots, values, scales):
             scales[blk, h] = scale
 
 
-def attention(q, kv, ks, vv, vs, table, lo, hi, scale):
+def attention(q, kv, ks, vv, vs, table, lo, hi, scale, floor=1.0):
     """One query group [g][D] over positions [lo, hi) of one sequence and KV head: output, and the
     error a kernel may make beside the output's own rounding.  kv, vv: code values
     [blocks][16][D] of the head, ks, vs its scales [blocks].
 
     The weights w = 2^(s + log2 sv - m) are rounded to f16: 2^-11 of each, or 2^-25 where w is below
-    f16's normal range, in units in which the largest is at least 1.  f32 sums and 2^x add less than
-    2^-15 of the weighted magnitudes."""
+    f16's normal range, in units in which the largest is at least 1 (floor: the decode kernel's case;
+    prefill's largest is at least 1/2 and a weight may be rounded again when a later reference scales
+    it: floor 4).  f32 sums and 2^x add less than 2^-15 of the weighted magnitudes."""
     if hi <= lo:
         return np.zeros_like(q), np.zeros_like(q)
     pos = np.arange(lo, hi)
@@ -134,8 +135,8 @@ def attention(q, kv, ks, vv, vs, table, lo, hi, scale):
     l = p.sum(-1, keepdims=True)
     out, mass = p @ v / l, p @ np.abs(v) / l
     w = p * vs[blk]
-    floor = 2.0 ** -25 * w.max(-1, keepdims=True) / l * np.abs(vv[blk, off]).sum(0)
-    return out, (2.0 ** -11 + 2.0 ** -15) * mass + floor
+    tail = floor * 2.0 ** -25 * w.max(-1, keepdims=True) / l * np.abs(vv[blk, off]).sum(0)
+    return out, (2.0 ** -11 + 2.0 ** -15) * mass + tail
 
 
 def pools(g, blocks, heads, dim, spread=1.5):

@@ -45,7 +45,7 @@ class Pool:
         return [t.cuda() for t in (self.kc, self.vc, self.ks, self.vs)] + [
             torch.from_numpy(self.tables).cuda(), torch.from_numpy(self.lens).cuda()]
 
-    def reference(self, q, rows, scale, window=0):
+    def reference(self, q, rows, scale, window=0, floor=1.0):
         """q [rows][Hq][D] float64; rows: (sequence, last position) of each."""
         group = q.shape[1] // self.hkv
         kv, vv = R.decode_codes(self.kc), R.decode_codes(self.vc)
@@ -56,7 +56,7 @@ class Pool:
             for h in range(self.hkv):
                 j = slice(h * group, (h + 1) * group)
                 out[i, j], bound[i, j] = R.attention(q[i, j], kv[:, h], ks[:, h], vv[:, h], vs[:, h], self.tables[b],
-                                                     lo, last + 1, scale)
+                                                     lo, last + 1, scale, floor)
         return out, bound
 
 
@@ -187,3 +187,126 @@ def test_decode_graph_replay_and_streams(pkv):
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def _prefill(pkv, p, chunks, hq, window=0, scale=None, status=None, q=None, longest=None, **over):
+    start = np.concatenate([[0], np.cumsum(chunks)]).astype(np.int32)
+    q = _query(p, int(start[-1]), hq) if q is None else q
+    out = pkv.prefill_block_fp8(q.cuda(), *p.device(), torch.from_numpy(start).cuda(), longest, scale, window=window,
+                                status=status, **over)
+    rows = [(b, int(p.lens[b]) - n + i) for b, n in enumerate(chunks) for i in range(n)]
+    return q, out, rows
+
+
+PREFILL = [  # chunks, lengths
+    ([1], [1]), ([17], [17]), ([130], [200]), ([5, 1, 40], [5, 33, 300]), ([0, 64, 0, 3], [0, 64, 50, 131]),
+    ([300], [700]), ([16, 128, 129], [16, 1000, 129])]
+
+
+@pytest.mark.parametrize("chunks,lens", PREFILL)
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (4, 2), (8, 2), (8, 1), (16, 1)])
+def test_prefill_matches(pkv, chunks, lens, hq, hkv):
+    p = Pool(sum(chunks) + hq, lens, hkv)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q, out, rows = _prefill(pkv, p, chunks, hq, status=status)
+    ref, bound = p.reference(q.double().numpy(), rows, D ** -0.5, floor=4.0)
+    _check(out, ref, bound, f"{hq}/{hkv}")
+    assert int(status.item()) == 0
+
+
+@pytest.mark.parametrize("window", [1, 15, 16, 100, 129, 1000])
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (8, 1)])
+def test_prefill_window(pkv, window, hq, hkv):
+    chunks, lens = [40, 1, 200], [40, 333, 700]
+    p = Pool(window, lens, hkv)
+    q, out, rows = _prefill(pkv, p, chunks, hq, window=window)
+    ref, bound = p.reference(q.double().numpy(), rows, D ** -0.5, window, floor=4.0)
+    _check(out, ref, bound, f"W={window}")
+
+
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (8, 1)])
+def test_prefill_rising_scores_and_scales(pkv, hq, hkv):
+    """References that rise in later tiles, value scales over the whole range, key scales that are no
+    powers of two, a negative softmax scale."""
+    lens, chunks = [600, 400], [50, 400]
+    p = Pool(21, lens, hkv, poison=False)
+    p.vs[:] = torch.exp2(torch.randint(-32, 32, p.vs.shape, generator=p.g).float())
+    p.ks[p.tables[0, :38]] *= torch.linspace(0.2, 60.0, 38)[:, None]
+    p.vs[p.tables[1, :25]] = torch.rand(25, hkv, generator=p.g) + 0.1
+    p.vs[p.tables[1, 13]] = 3.0e4
+    for scale in (D ** -0.5, -0.02):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        q, out, rows = _prefill(pkv, p, chunks, hq, scale=scale, status=status)
+        pick = list(range(0, len(rows), 7))
+        ref, bound = p.reference(q.double().numpy()[pick], [rows[i] for i in pick], scale, floor=4.0)
+        _check(out[pick], ref, bound, f"scale {scale}")
+        assert int(status.item()) == 0
+
+
+def test_prefill_many_items(pkv):
+    """More items than SMs, long and short chunks together; rows sampled."""
+    rng = np.random.default_rng(0)
+    chunks = [int(x) for x in rng.integers(1, 400, 12)] + [1] * 70
+    lens = [c + int(x) for c, x in zip(chunks, rng.integers(0, 900, len(chunks)))]
+    p = Pool(2, lens, 2, spread=0.7)
+    q, out, rows = _prefill(pkv, p, chunks, 8, longest=max(chunks))
+    pick = sorted(rng.choice(len(rows), 300, replace=False).tolist())
+    ref, bound = p.reference(q.double().numpy()[pick], [rows[i] for i in pick], D ** -0.5, floor=4.0)
+    _check(out[pick], ref, bound)
+
+
+def test_prefill_flags(pkv):
+    from paged_kv_cache_100_gb300 import _lib
+    chunks, lens = [20, 30], [60, 40]
+    for what, bit in (("query", _lib.PA_DEV_RANGE), ("scale", _lib.PA_DEV_RANGE), ("table", _lib.PA_DEV_BAD_BLOCK_ID),
+                      ("length", _lib.PA_DEV_BAD_CONTEXT_LEN), ("longest", _lib.PA_DEV_BAD_QUERY_LEN)):
+        p = Pool(5, lens, 2, poison=False)
+        q = _query(p, 50, 4)
+        longest = 30
+        if what == "query":
+            q[45, 0, 0] = -1e6
+        if what == "scale":
+            p.vs[p.tables[1, 1]] = float("nan")
+        if what == "table":
+            p.tables[1, 0] = -7
+        if what == "length":
+            p.lens[1] = 29
+        if what == "longest":
+            longest = 20
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        _, out, rows = _prefill(pkv, p, chunks, 4, status=status, q=q, longest=longest)
+        assert int(status.item()) == bit, what
+        ref, bound = p.reference(q.double().numpy()[:20], rows[:20], D ** -0.5, floor=4.0)
+        _check(out[:20], ref, bound, what)
+
+
+def test_prefill_leaves_rows_behind_the_last_sequence(pkv):
+    p = Pool(8, [50], 1)
+    q = _query(p, 64, 4)
+    out = torch.full((64, 4, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    start = torch.tensor([0, 50], dtype=torch.int32, device="cuda")
+    pkv.prefill_block_fp8(q.cuda(), *p.device(), start, 50, out=out)
+    ref, bound = p.reference(q.double().numpy()[:50], [(0, i) for i in range(50)], D ** -0.5, floor=4.0)
+    _check(out[:50], ref, bound)
+    assert (out[50:] == 7.0).all()
+
+
+def test_prefill_graph_and_decode_agree(pkv):
+    """A chunk of one token is a decode; a captured prefill replays the same bytes."""
+    lens = [300, 17, 1000]
+    p = Pool(31, lens, 2, spread=0.7)
+    q = _query(p, 3, 8).cuda()
+    dev = p.device()
+    start = torch.arange(4, dtype=torch.int32, device="cuda")
+    one = pkv.prefill_block_fp8(q, *dev, start, 1)
+    ref, bound = p.reference(q.cpu().double().numpy(), [(b, n - 1) for b, n in enumerate(lens)], D ** -0.5, floor=4.0)
+    _check(one, ref, bound)
+    _check(pkv.decode_block_fp8(q, *dev), ref, bound)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = pkv.prefill_block_fp8(q, *dev, start, 1)
+    for _ in range(2):
+        out.zero_()
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, one)

@@ -94,6 +94,23 @@ def test_decode_block_fp8_workspace(lib):
         assert f(*args) == bad
 
 
+PREFILL = dict(out=A, query=2 * A, key_cache=3 * A, value_cache=4 * A, k_scales=5 * A, v_scales=6 * A, tables=7 * A,
+               lens=8 * A, start=9 * A, num_seqs=1, hq=8, hkv=2, dim=128, block_size=16, max_blocks=4, num_blocks=8,
+               tokens=5, longest=5, scale=0.1, window=0, workspace=10 * A, workspace_bytes=1 << 20, status=None, stream=None)
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(num_seqs=-1), BAD), (dict(hq=7), BAD), (dict(block_size=8), BAD), (dict(max_blocks=-1), BAD),
+    (dict(num_blocks=0), BAD), (dict(tokens=-1), BAD), (dict(longest=-1), BAD), (dict(window=-1), BAD),
+    (dict(scale=float("nan")), BAD), (dict(out=None), BAD), (dict(start=None), BAD), (dict(k_scales=None), BAD),
+    (dict(v_scales=6 * A + 1), BAD), (dict(query=2 * A + 8), BAD), (dict(tables=None), BAD), (dict(dim=64), UNSUPPORTED),
+    (dict(hq=6), UNSUPPORTED), (dict(hq=64), UNSUPPORTED), (dict(num_blocks=1 << 26), UNSUPPORTED),
+    (dict(workspace=None), WORKSPACE), (dict(workspace_bytes=16), WORKSPACE), (dict(workspace=10 * A + 8), WORKSPACE),
+    (dict(num_seqs=0, out=None), OK), (dict(tokens=0, out=None), OK), (dict(longest=0, out=None), OK)])
+def test_prefill_block_fp8_refuses(lib, over, expect):
+    assert _call(lib.pa_prefill_block_fp8, PREFILL, over) == expect
+
+
 def test_rotary_turns(lib):
     for kind, factor in (("none", 1.0), ("linear", 4.0), ("ntk", 8.0), ("by_parts", 8.0)):
         for rot in (2, 6, 64, 122, 128):
