@@ -36,7 +36,6 @@
 #include <math.h>
 
 #include <algorithm>
-#include <climits>
 #include <mutex>
 
 #include "pa_block8.cuh"
@@ -56,14 +55,14 @@ constexpr int kTile = 2 * kHalf;         // 128 rows x 256 bytes
 constexpr int kCols = 64;                // S / O columns per softmax thread (two per row)
 constexpr int kGroup = 2 * kRows;        // softmax threads per Q tile
 constexpr int kWidenWarp0 = 2 + kQT * kGroup / 32;
-constexpr int kWidenThreads = 64;
+constexpr int kWidenThreads = 128;
 constexpr int kThreads = kWidenWarp0 * 32 + kWidenThreads;
 constexpr int kStages = 2;               // f16 K tiles, f16 V tiles
 constexpr int kCodeStages = 3;           // half tiles of codes
 constexpr int kCodeRows = 64;            // positions of a half tile
 constexpr int kCodeBytes = kCodeRows * kD;
 constexpr int kScaleSlots = 4;
-constexpr float kChunkSumMax = 32768.f;  // largest weight sum of a 32-column chunk kept as computed
+constexpr float kChunkSumMax = 32768.f;  // largest weight sum of a 32-column chunk kept as computed: f16 holds its weights
 constexpr size_t kWorkspaceBytes = 256;  // the ticket counter (rounded up)
 
 // shared memory map (offsets from the 1024-byte aligned dynamic base)
@@ -158,36 +157,34 @@ __device__ __forceinline__ float pow2_diff(float a, float b) {
 // A block's scales as the softmax uses them: x = key scale * softmax scale *
 // log2(e), y = log2 of the value scale, z = 1 / value scale.
 //
-// Weights of the 32-column chunk of S at taddr (its first column is position kc,
-// its two blocks' scales e[0], e[1]) written over it as 16 f16 pairs.  A lane
-// whose first attempt summed past the limit (over) first raises its reference to
-// the next integer at or above the chunk's largest attended exponent.  Returns
-// (weights divided by the value scales, summed; reference).  Out of line, so
-// that the common path keeps its registers; called by all lanes of a warp.
-__device__ __noinline__ float2 chunk_weights_again(uint32_t taddr, const float4 *e, float ref, bool over, bool masked,
-                                                   int kc, int qpos, int wlo) {
+// The general form of a 32-column chunk's weights (S at taddr, first column at
+// position kc, its two blocks' scales e[0], e[1]), for chunks that some row sees
+// only in part and for those whose weights would grow past the reference's
+// range: a row whose largest attended exponent is more than 2^10 above its
+// reference (or has none) raises it to the next integer at or above.  The
+// weights replace S as 16 f16 pairs.  Returns (weights divided by the value
+// scales, summed; reference).  Out of line, so that the common path is short and
+// keeps its registers; called by all lanes of a warp.
+__device__ __noinline__ float2 chunk_weights_general(uint32_t taddr, const float4 *e, float ref, int kc, int qpos, int wlo) {
     uint32_t v[32];
     tmem_ld32(taddr, v);
     tmem_wait_ld();
-    if (over) {
-        float rmax = -INFINITY;
+    const int lo = wlo - kc, hi = qpos - kc;         // attended columns
+    float rmax = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (!masked || (kc + i <= qpos && kc + i >= wlo))
-                rmax = fmaxf(rmax, fmaf(__uint_as_float(v[i]), e[i >> 4].x, e[i >> 4].y));
-        const float nref = ceilf(rmax);
-        if (nref > ref) ref = nref;      // else scores that are not finite: as computed before
+    for (int i = 0; i < 32; ++i) {
+        const float x = i >= lo && i <= hi ? fmaf(__uint_as_float(v[i]), e[i >> 4].x, e[i >> 4].y) : -INFINITY;
+        v[i] = __float_as_uint(x);
+        rmax = fmaxf(rmax, x);
     }
+    if (rmax > ref + 10.f) ref = ceilf(rmax);
+    // before a row has seen anything its weights are 0: any finite reference does
+    const float r = ref == -INFINITY ? 0.f : ref;
     uint32_t pp[16];
     float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-        float p0 = ex2_fast(fmaf(__uint_as_float(v[i]), e[i >> 4].x, e[i >> 4].y - ref));
-        float p1 = ex2_fast(fmaf(__uint_as_float(v[i + 1]), e[i >> 4].x, e[i >> 4].y - ref));
-        if (masked) {
-            if (!(kc + i <= qpos && kc + i >= wlo)) p0 = 0.f;
-            if (!(kc + i + 1 <= qpos && kc + i + 1 >= wlo)) p1 = 0.f;
-        }
+        const float p0 = ex2_fast(__uint_as_float(v[i]) - r), p1 = ex2_fast(__uint_as_float(v[i + 1]) - r);
         sum[i >> 4] += p0 + p1;
         pp[i >> 1] = pack_f16x2(p0, p1);
     }
@@ -638,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // mask when it lies inside every row's range of the tile
                 const int qpos = d.C + tx0 + min(tr, ntok - 1);
                 const int qpos_lo = d.C + tx0, qpos_hi = d.C + tx0 + ntok - 1;
-                const int wlo = a.window > 0 ? qpos + 1 - a.window : INT_MIN;
+                const int wlo = a.window > 0 ? max(0, qpos + 1 - a.window) : 0;
                 // The row's reference (log2 units): an integer, or -inf before the row
                 // has seen a position; O and l are relative to it.
                 float m_used = -INFINITY, l = 0.f;
@@ -649,9 +646,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int k0 = (d.blk_lo + 8 * j) * kBlockSize + part * kCols;
                     const float4 *scales = s_scale + (gs % kScaleSlots) * 8 + part * (kCols / kBlockSize);
                     // One pass over S: a chunk's weights 2^(s ck + lv - ref) replace it in
-                    // f16, unless they sum to more than 2^15: then ref rises to the next
-                    // integer at or above the chunk's largest exponent and the chunk is
-                    // computed again.  Each chunk keeps the reference it was written with.
+                    // f16, unless they sum to more than 2^15 or some row sees only part
+                    // of the chunk: those take the general form, where the reference may
+                    // rise.  Each chunk keeps the reference it was written with.
                     float mref = m_used;
                     float cref0 = m_used, cref1 = m_used, csum0 = 0.f, csum1 = 0.f;
                     if (got) {
@@ -659,28 +656,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                         for (int c = 0; c < kCols; c += 32) {
                             const int kc = k0 + c;
-                            const bool masked = (kc + 31 > qpos_lo) || (a.window > 0 && kc < qpos_hi + 1 - a.window);
                             const float4 *e = scales + (c >> 4);
-                            uint32_t pp[16];
-                            float sum[2];
-                            {
-                                uint32_t v[32];
+                            bool general = kc + 31 > qpos_lo || (a.window > 0 && kc < qpos_hi + 1 - a.window);
+                            float psum;
+                            if (!general) {
+                                uint32_t v[32], pp[16];
                                 tmem_ld32(s_base + c, v);
+                                const float4 e0 = e[0], e1 = e[1];
                                 tmem_wait_ld();
+                                float sum[2];
 #pragma unroll
                                 for (int blk = 0; blk < 2; ++blk) {
-                                    const float4 sb = e[blk];
-                                    const uint64_t k2 = f2_pack(sb.x, sb.x), nm2 = f2_pack(sb.y - mref, sb.y - mref);
+                                    const float ck = blk ? e1.x : e0.x, off = (blk ? e1.y : e0.y) - mref;
+                                    const uint64_t k2 = f2_pack(ck, ck), nm2 = f2_pack(off, off);
                                     uint64_t ps2 = f2_pack(0.f, 0.f);
 #pragma unroll
                                     for (int i = 16 * blk; i < 16 * blk + 16; i += 2) {
                                         float x0, x1;
                                         f2_unpack(f2_fma(f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), k2, nm2), x0, x1);
-                                        float p0 = ex2_fast(x0), p1 = ex2_fast(x1);
-                                        if (masked) {
-                                            if (!(kc + i <= qpos && kc + i >= wlo)) p0 = 0.f;
-                                            if (!(kc + i + 1 <= qpos && kc + i + 1 >= wlo)) p1 = 0.f;
-                                        }
+                                        const float p0 = ex2_fast(x0), p1 = ex2_fast(x1);
                                         ps2 = f2_add(ps2, f2_pack(p0, p1));
                                         pp[i >> 1] = pack_f16x2(p0, p1);
                                     }
@@ -688,16 +682,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     f2_unpack(ps2, lo, hi);
                                     sum[blk] = lo + hi;
                                 }
+                                psum = fmaf(sum[0], e0.z, sum[1] * e1.z);
+                                general = __any_sync(0xffffffffu, !(sum[0] + sum[1] <= kChunkSumMax));
+                                if (!general) tmem_st16(s_base + c, pp);
                             }
-                            const bool over = !(sum[0] + sum[1] <= kChunkSumMax);
-                            float psum = fmaf(sum[0], e[0].z, sum[1] * e[1].z);
-                            if (__any_sync(0xffffffffu, over)) {
-                                // the whole warp; S is still in place
-                                const float2 r2 = chunk_weights_again(s_base + c, e, mref, over, masked, kc, qpos, wlo);
+                            if (general) {           // the whole warp; S is still in place
+                                const float2 r2 = chunk_weights_general(s_base + c, e, mref, kc, qpos, wlo);
                                 psum = r2.x;
                                 mref = r2.y;
-                            } else {
-                                tmem_st16(s_base + c, pp);
                             }
                             if (c == 0) {
                                 cref0 = mref;
