@@ -107,7 +107,10 @@ struct PrefillArgs {
     unsigned int *work_counter;
 };
 
+// A phase that is complete passes at once; the failure flag (another shared
+// memory round trip) is looked at only before a wait that may last.
 __device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, volatile int *fail, int32_t *status) {
+    if (mbar_try_wait(bar, parity)) return true;
     if (*fail) return false;
     if (mbar_wait_bounded(bar, parity)) return true;
     *fail = 1;
@@ -208,9 +211,40 @@ __device__ __noinline__ void scale_chunk_weights(uint32_t taddr, float f0, float
     tmem_wait_st();
 }
 
+// Scales this thread's 64 columns of O by alpha.
+__device__ __noinline__ void scale_output(uint32_t taddr, float alpha) {
+    const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll 1
+    for (int c = 0; c < kCols; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(taddr + c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            float r0, r1;
+            f2_unpack(f2_mul(f2_pack(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), a2), r0, r1);
+            o[i] = __float_as_uint(r0);
+            o[i + 1] = __float_as_uint(r1);
+        }
+        tmem_st32(taddr + c, o);
+    }
+    tmem_wait_st();
+}
+
 // The two warps of a softmax group that hold the same 32 rows meet here.
 __device__ __forceinline__ void pair_sync(int x, int quarter) {
     asm volatile("bar.sync %0, 64;" ::"r"(5 + 4 * x + quarter) : "memory");
+}
+// The same, with the OR of `v` over their threads.
+__device__ __forceinline__ bool pair_any(int x, int quarter, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(5 + 4 * x + quarter)
+        : "memory");
+    return r != 0;
 }
 
 // AND of `v` over the threads of softmax group x.
@@ -701,52 +735,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tmem_wait_st();
                     }
-                    // the two threads of the row agree on the larger reference
-                    const int rp = ex & 1;
-                    ++ex;
-                    red[(rp * 2 + part) * kRows + r] = mref;
-                    pair_sync(x, quarter);
-                    const float rref = fmaxf(mref, red[(rp * 2 + (part ^ 1)) * kRows + r]);
                     const uint32_t my_sc = sc++;
-                    if (!got) {
+                    float psum = csum0 + csum1;
+                    // A reference that rose anywhere in the 32 rows (rare after the first
+                    // steps): the two threads of each row agree on the larger one.
+                    if (pair_any(x, quarter, mref != m_used)) {
+                        const int rp = ex & 1;
+                        ++ex;
+                        red[(rp * 2 + part) * kRows + r] = mref;
+                        pair_sync(x, quarter);
+                        const float rref = fmaxf(mref, red[(rp * 2 + (part ^ 1)) * kRows + r]);
+                        if (got) {
+                            // chunks written against a smaller reference are scaled by
+                            // the exact power of two between them
+                            const float f0 = pow2_diff(cref0, rref), f1 = pow2_diff(cref1, rref);
+                            if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) scale_chunk_weights(s_base, f0, f1);
+                            psum = csum0 * f0 + csum1 * f1;
+                            // O and l follow, once every P.V of this tile issued so far
+                            // has landed
+                            const float alpha = rref > m_used ? pow2_diff(m_used, rref) : 1.f;
+                            if (j >= 1) {
+                                if (!warp_wait(&bars[kPvDone + x], (my_sc - 1) & 1, fail, a.status)) ok = false;
+                                tc_fence_after();
+                                if (ok) scale_output(o_base, alpha);
+                            }
+                            l *= alpha;
+                            m_used = rref > m_used ? rref : m_used;
+                        }
+                    }
+                    if (!got || !ok) {
                         ok = false;
                         continue;
-                    }
-                    // chunks written against a smaller reference are scaled by the exact
-                    // power of two between them
-                    const float f0 = pow2_diff(cref0, rref), f1 = pow2_diff(cref1, rref);
-                    if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) scale_chunk_weights(s_base, f0, f1);
-                    const float psum = csum0 * f0 + csum1 * f1;
-                    // O and l follow when the reference moved, once every P.V of this
-                    // tile issued so far has landed
-                    const bool need = rref > m_used;
-                    const float alpha = need ? pow2_diff(m_used, rref) : 1.f;
-                    if (j >= 1 && __any_sync(0xffffffffu, need)) {
-                        if (!warp_wait(&bars[kPvDone + x], (my_sc - 1) & 1, fail, a.status)) {
-                            ok = false;
-                            continue;
-                        }
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int c = 0; c < kCols; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(o_base + c, o);
-                            tmem_wait_ld();
-                            const uint64_t a2 = f2_pack(alpha, alpha);
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                float r0, r1;
-                                f2_unpack(f2_mul(f2_pack(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), a2), r0, r1);
-                                o[i] = __float_as_uint(r0);
-                                o[i + 1] = __float_as_uint(r1);
-                            }
-                            tmem_st32(o_base + c, o);
-                        }
-                        tmem_wait_st();
-                    }
-                    if (need) {
-                        l *= alpha;
-                        m_used = rref;
                     }
                     l += psum;
                     tc_fence_before();
