@@ -582,9 +582,11 @@ pa_status pa_decode_block_fp8(void *out, const void *query, const void *key_cach
  * A sequence whose query_start entries fall, leave [0, num_query_tokens] or
  * exceed its context length is not computed and flagged PA_DEV_BAD_CONTEXT_LEN.
  * Supported: head_dim 128, group 1, 2, 4, 8 or 16.
- * Arithmetic: both products on tcgen05 tensor cores, f16 operands and f32 sums.
- * Codes are widened exactly; queries are converted to f16 (exact for |q| in
- * [2^-14, 65504], others flag PA_DEV_RANGE); weights are rounded to f16 as in
+ * Arithmetic: both products on tcgen05 tensor cores with f32 sums.  Q K^T runs
+ * on the codes, a query row as the sum of two E4M3 rows times a power of two:
+ * exact but for elements below 2^-9 of the row's largest, which are off by at
+ * most 2^-17 of it (a row with an infinite or NaN element gives NaN).  P V runs
+ * on f16: codes widen exactly, weights are rounded as in
  * pa_decode_block_fp8.  A NaN value reaches every row of the 256-row tiles that
  * process its position, also rows before it.
  */

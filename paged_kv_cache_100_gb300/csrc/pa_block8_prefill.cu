@@ -8,23 +8,26 @@
 // divided by the value scale.
 //
 // One CTA computes two 128-row tiles (A, then B) of (token, query head of the
-// group) rows of one sequence and KV head over 128-position K/V tiles.  The
-// second operand of both products is the cache's codes widened to f16 (exact),
-// so queries and weights are f16 too (queries are exact for |q| in
-// [2^-14, 65504]; bf16 weights would be too coarse for the output).
-//   warp 0       TMA producer: both Q tiles, then the codes of each K/V step in
-//                half tiles of four blocks through a ring of kCodeStages;
+// group) rows of one sequence and KV head over 128-position K/V tiles.
+//   Q K^T runs on the codes as they are (kind::f8f6f4).  A bf16 query has 8
+//   significant bits and E4M3 has 4, so a query row is the sum of two rows of
+//   codes times a power of two, q = 2^e (q1 + q2) with q1 the nearest code and
+//   q2 the rest, exact but for elements below 2^-9 of the row's largest, which
+//   are off by at most 2^-17 of it; S = Q1 K^T + Q2 K^T at the 8-bit rate costs
+//   what one 16-bit product would, and K is not touched.
+//   P V runs on f16: the weights need 11 bits (bf16's 8 would be too coarse for
+//   the output), so V's codes are widened to f16 (exact) in shared memory.
+//   warp 0       TMA producer: both Q tiles, then the K and V codes of each step;
 //   warp 1       MMA issuer, ping-pong between the tiles:
 //                  S_A(0) S_B(0) | PV_A(j) S_A(j+1) PV_B(j) S_B(j+1) | ...
-//                S = Q K^T and O += P V accumulate in tensor memory, P is read
-//                from tensor memory, written there over its own S;
+//                S and O += P V accumulate in tensor memory, P is read from
+//                tensor memory, written there over its own S;
 //   warps 2..9   softmax of tile A, warps 10..17 of tile B: two threads per row,
 //                64 of the 128 columns of S and O each, one pass over S per step
 //                against an integer reference that rises only when a chunk's
-//                weights would leave f16's range;
-//   warps 18..   widen: Q tiles in place (bf16 to f16), each half tile of codes
-//                into the f16 K or V tile, positions outside the item's range
-//                zeroed in V; they also stage the blocks' scales.
+//                weights would leave f16's range; they also split their Q tile;
+//   warps 18, 19 widen each V tile, zeroing positions outside the item's range,
+//                and stage the blocks' scales.
 // Persistent CTAs take items from a ticket counter; barrier phases are counted
 // across items, so an item's loads start under the end of the one before.
 // Every wait is bounded (about a second); one that gives up sets PA_DEV_TIMEOUT,
@@ -55,12 +58,12 @@ constexpr int kTile = 2 * kHalf;         // 128 rows x 256 bytes
 constexpr int kCols = 64;                // S / O columns per softmax thread (two per row)
 constexpr int kGroup = 2 * kRows;        // softmax threads per Q tile
 constexpr int kWidenWarp0 = 2 + kQT * kGroup / 32;
-constexpr int kWidenThreads = 128;
+constexpr int kWidenThreads = 64;
 constexpr int kThreads = kWidenWarp0 * 32 + kWidenThreads;
-constexpr int kStages = 2;               // f16 K tiles, f16 V tiles
-constexpr int kCodeStages = 3;           // half tiles of codes
-constexpr int kCodeRows = 64;            // positions of a half tile
-constexpr int kCodeBytes = kCodeRows * kD;
+constexpr int kCodeTile = kKv * kD;      // codes of a K or V tile
+constexpr int kKStages = 3;              // K code tiles
+constexpr int kCodeStages = 2;           // V code tiles
+constexpr int kVStages = 2;              // f16 V tiles
 constexpr int kScaleSlots = 4;
 constexpr float kChunkSumMax = 32768.f;  // largest weight sum of a 32-column chunk kept as computed: f16 holds its weights
 constexpr size_t kWorkspaceBytes = 256;  // the ticket counter (rounded up)
@@ -68,17 +71,18 @@ constexpr size_t kWorkspaceBytes = 256;  // the ticket counter (rounded up)
 // shared memory map (offsets from the 1024-byte aligned dynamic base)
 constexpr int kOffQ = 0;
 constexpr int kOffK = kOffQ + kQT * kTile;
-constexpr int kOffV = kOffK + kStages * kTile;
-constexpr int kOffCode = kOffV + kStages * kTile;
-constexpr int kOffScale = kOffCode + kCodeStages * kCodeBytes;   // float4 [kScaleSlots][8]
-constexpr int kOffRed = kOffScale + kScaleSlots * 8 * 16;        // float [kQT][2 parities][2][128]
+constexpr int kOffV = kOffK + kKStages * kCodeTile;
+constexpr int kOffCode = kOffV + kVStages * kTile;
+constexpr int kOffScale = kOffCode + kCodeStages * kCodeTile;    // float4 [kScaleSlots][8]
+constexpr int kOffQScale = kOffScale + kScaleSlots * 8 * 16;     // float [kQT][128]
+constexpr int kOffRed = kOffQScale + kQT * kRows * 4;        // float [kQT][2 parities][2][128]
 constexpr int kPermMax = 64;
 constexpr int kOffPerm = kOffRed + kQT * 2 * 2 * kRows * 4;      // int [kPermMax]
 constexpr int kOffBar = kOffPerm + kPermMax * 4;
 
-constexpr int kQFull = 0, kQConv = 1, kQFree = 2, kDrain = 3, kCodeFull = 4, kCodeEmpty = kCodeFull + kCodeStages,
-              kKConv = kCodeEmpty + kCodeStages, kKEmpty = kKConv + kStages, kVConv = kKEmpty + kStages,
-              kVEmpty = kVConv + kStages, kSFull = kVEmpty + kStages, kPFull = kSFull + kQT, kPvDone = kPFull + kQT,
+constexpr int kQFull = 0, kQFree = 1, kDrain = 2, kQSplit = 3, kKFull = kQSplit + kQT, kKEmpty = kKFull + kKStages,
+              kCodeFull = kKEmpty + kKStages, kCodeEmpty = kCodeFull + kCodeStages, kVConv = kCodeEmpty + kCodeStages,
+              kVEmpty = kVConv + kVStages, kSFull = kVEmpty + kVStages, kPFull = kSFull + kQT, kPvDone = kPFull + kQT,
               kOFree = kPvDone + kQT, kItemFull = kOFree + kQT, kItemEmpty = kItemFull + 2,
               kScaleFull = kItemEmpty + 2, kNumBars = kScaleFull + kScaleSlots;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;                 // TMEM slot, failure flag, item order, item queue [2]
@@ -88,6 +92,30 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 constexpr uint32_t kTmemCols = 512;      // S_A, S_B, O_A, O_B
 __device__ __forceinline__ uint32_t col_s(int x) { return (uint32_t)(x * kKv); }
 __device__ __forceinline__ uint32_t col_o(int x) { return (uint32_t)(kQT * kKv + x * kD); }
+
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t x) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// D[tmem] (+)= A[smem] * B[smem], both E4M3; issued by one thread.
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor: E4M3 operands (format 0), K-major, f32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
 
 struct PrefillArgs {
     void *out;
@@ -161,14 +189,15 @@ __device__ __forceinline__ float pow2_diff(float a, float b) {
 // log2(e), y = log2 of the value scale, z = 1 / value scale.
 //
 // The general form of a 32-column chunk's weights (S at taddr, first column at
-// position kc, its two blocks' scales e[0], e[1]), for chunks that some row sees
+// position kc, its two blocks' scales e[0], e[1], the row's query scale qs), for chunks that some row sees
 // only in part and for those whose weights would grow past the reference's
 // range: a row whose largest attended exponent is more than 2^10 above its
 // reference (or has none) raises it to the next integer at or above.  The
 // weights replace S as 16 f16 pairs.  Returns (weights divided by the value
 // scales, summed; reference).  Out of line, so that the common path is short and
 // keeps its registers; called by all lanes of a warp.
-__device__ __noinline__ float2 chunk_weights_general(uint32_t taddr, const float4 *e, float ref, int kc, int qpos, int wlo) {
+__device__ __noinline__ float2 chunk_weights_general(uint32_t taddr, const float4 *e, float qs, float ref, int kc, int qpos,
+                                                     int wlo) {
     uint32_t v[32];
     tmem_ld32(taddr, v);
     tmem_wait_ld();
@@ -176,7 +205,7 @@ __device__ __noinline__ float2 chunk_weights_general(uint32_t taddr, const float
     float rmax = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-        const float x = i >= lo && i <= hi ? fmaf(__uint_as_float(v[i]), e[i >> 4].x, e[i >> 4].y) : -INFINITY;
+        const float x = i >= lo && i <= hi ? fmaf(__uint_as_float(v[i]), e[i >> 4].x * qs, e[i >> 4].y) : -INFINITY;
         v[i] = __float_as_uint(x);
         rmax = fmaxf(rmax, x);
     }
@@ -231,6 +260,53 @@ __device__ __noinline__ void scale_output(uint32_t taddr, float alpha) {
     tmem_wait_st();
 }
 
+// Splits rows [first, 128), every `step`-th, of a Q tile (bf16, two 128-byte pieces
+// per row) in place into q1 and q2 (E4M3, one piece each), and leaves the rows'
+// scales 2^e.  Eight neighbouring lanes share a row: lane c owns elements 16 c ..
+// 16 c + 15, two chunks of the bf16 row and one of each row of codes.
+__device__ __forceinline__ void split_query(uint8_t *tile, float *scales, int first, int step, int c) {
+#pragma unroll 1
+    for (int r = first; r < kRows; r += step) {
+        const int sw = r & 7;
+        uint8_t *row = tile + r * 128;
+        const uint8_t *src = row + (c >> 2) * kHalf;
+        const uint4 w0 = *reinterpret_cast<const uint4 *>(src + (((2 * (c & 3)) ^ sw) << 4));
+        const uint4 w1 = *reinterpret_cast<const uint4 *>(src + (((2 * (c & 3) + 1) ^ sw) << 4));
+        const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        uint32_t amax = 0;                           // as bits: magnitudes compare like integers
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = max(amax, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        // 2^e with amax < 2^(e + 8): every code is below 256; an infinite or NaN
+        // element makes the row NaN
+        const int e = max((int)(amax >> 23) - 127 - 7, -100);
+        const float up = __uint_as_float((uint32_t)(127 - e) << 23);      // 2^-e
+        const bool bad = amax >= 0x7f800000u;
+        uint32_t c1[4], c2[4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // the scaled pair is exact in f16 (down to 2^-24), its first codes'
+            // difference too
+            const uint32_t x = pack_f16x2(bf16lo(w[i]) * up, bf16hi(w[i]) * up);
+            const uint32_t p1 = f16x2_to_e4m3x2(x);
+            const uint32_t p2 = f16x2_to_e4m3x2(sub_f16x2(x, e4m3x2_to_f16x2(p1)));
+            if (i & 1) {
+                c1[i >> 1] |= p1 << 16;
+                c2[i >> 1] |= p2 << 16;
+            } else {
+                c1[i >> 1] = p1;
+                c2[i >> 1] = p2;
+            }
+        }
+        if (bad) c1[0] = c1[1] = c1[2] = c1[3] = 0x7f7f7f7fu;
+        __syncwarp();                                // the rows have been read
+        *reinterpret_cast<uint4 *>(row + ((c ^ sw) << 4)) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
+        *reinterpret_cast<uint4 *>(row + kHalf + ((c ^ sw) << 4)) = make_uint4(c2[0], c2[1], c2[2], c2[3]);
+        if (c == 0) scales[r] = 1.f / up;
+    }
+}
+
 // The two warps of a softmax group that hold the same 32 rows meet here.
 __device__ __forceinline__ void pair_sync(int x, int quarter) {
     asm volatile("bar.sync %0, 64;" ::"r"(5 + 4 * x + quarter) : "memory");
@@ -245,6 +321,10 @@ __device__ __forceinline__ bool pair_any(int x, int quarter, bool v) {
         : "r"((uint32_t)v), "r"(5 + 4 * x + quarter)
         : "memory");
     return r != 0;
+}
+
+__device__ __forceinline__ void group_sync(int x) {
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + x), "n"(kGroup) : "memory");
 }
 
 // AND of `v` over the threads of softmax group x.
@@ -326,10 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kNumBars; ++i) {
             int n = 1;
-            if (i == kQConv || (i >= kCodeEmpty && i < kCodeEmpty + kCodeStages) || (i >= kKConv && i < kKConv + kStages) ||
-                (i >= kVConv && i < kVConv + kStages))
+            if ((i >= kCodeEmpty && i < kCodeEmpty + kCodeStages) || (i >= kVConv && i < kVConv + kVStages) ||
+                i >= kScaleFull)
                 n = kWidenThreads;
-            if ((i >= kPFull && i < kPFull + kQT) || (i >= kOFree && i < kOFree + kQT)) n = kGroup;
+            if ((i >= kQSplit && i < kQSplit + kQT) || (i >= kPFull && i < kPFull + kQT) || (i >= kOFree && i < kOFree + kQT)) n = kGroup;
             if (i >= kItemEmpty && i < kItemEmpty + 2) n = 1 + kQT * kGroup + kWidenThreads;
             mbar_init(&bars[i], n);
         }
@@ -390,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- TMA producer (and item fetch) ----------------
         if (lane == 0) {
             int q_issued = -1;
-            uint32_t code = 0;                      // half tiles issued
+            uint32_t gstep = 0, k_issued = 0, v_issued = 0;
             bool ok = true;
             for (int it = 0;; ++it) {
                 int item = -1;
@@ -433,45 +513,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         rows[i] = (phys * a.num_kv_heads + d.kvh) * kBlockSize;
                     }
-                    // K's two halves, then V's
-                    for (int h = 0; h < 4; ++h, ++code) {
-                        const int s = code % kCodeStages;
-                        if (code >= kCodeStages &&
-                            !wait_or_fail(&bars[kCodeEmpty + s], ((code / kCodeStages) - 1) & 1, fail, a.status)) {
-                            ok = false;
-                            break;
-                        }
-                        const int first = (h & 1) * 4, n = max(0, min(4, nb - first));
-                        const CUtensorMap *map = h < 2 ? &kmap : &vmap;
-                        mbar_arrive_expect_tx(&bars[kCodeFull + s], n * kBlockSize * kD);
-                        for (int i = 0; i < n; ++i)
-                            tma_load_2d(sCode + s * kCodeBytes + i * kBlockSize * kD, map, 0, rows[first + i],
-                                        &bars[kCodeFull + s]);
+                    const uint32_t gs = gstep + j;
+                    if (gs >= kKStages &&
+                        !wait_or_fail(&bars[kKEmpty + gs % kKStages], (gs / kKStages - 1) & 1, fail, a.status)) {
+                        ok = false;
+                        break;
                     }
+                    mbar_arrive_expect_tx(&bars[kKFull + gs % kKStages], nb * kBlockSize * kD);
+                    for (int i = 0; i < nb; ++i)
+                        tma_load_2d(sK + (gs % kKStages) * kCodeTile + i * kBlockSize * kD, &kmap, 0, rows[i],
+                                    &bars[kKFull + gs % kKStages]);
+                    k_issued = gs + 1;
+                    if (gs >= kCodeStages &&
+                        !wait_or_fail(&bars[kCodeEmpty + gs % kCodeStages], (gs / kCodeStages - 1) & 1, fail, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&bars[kCodeFull + gs % kCodeStages], nb * kBlockSize * kD);
+                    for (int i = 0; i < nb; ++i)
+                        tma_load_2d(sCode + (gs % kCodeStages) * kCodeTile + i * kBlockSize * kD, &vmap, 0, rows[i],
+                                    &bars[kCodeFull + gs % kCodeStages]);
+                    v_issued = gs + 1;
                 }
+                gstep += d.n_tiles;
             }
             // no copy of ours may still be landing when the CTA leaves
             if (q_issued >= 0) (void)mbar_wait_bounded(&bars[kQFull], q_issued & 1);
-            for (uint32_t j = code > kCodeStages ? code - kCodeStages : 0; j < code; ++j)
+            for (uint32_t j = k_issued > kKStages ? k_issued - kKStages : 0; j < k_issued; ++j)
+                (void)mbar_wait_bounded(&bars[kKFull + j % kKStages], (j / kKStages) & 1);
+            for (uint32_t j = v_issued > kCodeStages ? v_issued - kCodeStages : 0; j < v_issued; ++j)
                 (void)mbar_wait_bounded(&bars[kCodeFull + j % kCodeStages], (j / kCodeStages) & 1);
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
         if (lane == 0) {
-            constexpr uint32_t idS = idesc_f16_f32(kRows, kKv, false);
+            constexpr uint32_t idS = idesc_e4m3_f32(kRows, kKv);
             constexpr uint32_t idPV = idesc_f16_f32(kRows, kD, true);
             const uint32_t q_u = smem_u32(sQ), k_u = smem_u32(sK), v_u = smem_u32(sV);
             uint32_t gstep = 0;
-            uint32_t pcount[kQT] = {0, 0};
+            uint32_t pcount[kQT] = {0, 0}, b_items = 0;
             bool ok = true;
             auto issue_s = [&](int x, uint32_t gs) {
-                const uint32_t qb = q_u + x * kTile, kb = k_u + (gs % kStages) * kTile;
+                const uint32_t kb = k_u + (gs % kKStages) * kCodeTile;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t o = (k >> 2) * kHalf + (k & 3) * 32;
-                    umma_bf16(tmem + col_s(x), sw128_desc(qb + o, 16, 1024), sw128_desc(kb + o, 16, 1024), idS,
-                              k > 0 ? 1u : 0u);
-                }
+                for (int k = 0; k < 8; ++k)          // q1, then q2, in steps of 32 codes
+                    umma_f8(tmem + col_s(x), sw128_desc(q_u + x * kTile + (k >> 2) * kHalf + (k & 3) * 32, 16, 1024),
+                            sw128_desc(kb + (k & 3) * 32, 16, 1024), idS, k > 0 ? 1u : 0u);
                 umma_commit(&bars[kSFull + x]);
             };
             // P of tokens [16 k, 16 k + 16): f16 pairs from column 32 (k / 2) + 8 (k % 2) of the S buffer
@@ -481,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the first P.V of an item overwrites O: the item before must have read it out
                 if (j == 0 && it >= 1 && !wait_or_fail(&bars[kOFree + x], (it - 1) & 1, fail, a.status)) return false;
                 tc_fence_after();
-                const uint32_t vb = v_u + (gs % kStages) * kTile;
+                const uint32_t vb = v_u + (gs % kVStages) * kTile;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     umma_bf16_tmem_a(tmem + col_o(x), tmem + col_s(x) + 32 * (k >> 1) + 8 * (k & 1),
@@ -495,24 +582,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Item d;
                 describe_item(a, item, by_length, false, perm, d);
                 const int n = d.n_tiles;
-                if (!wait_or_fail(&bars[kQConv], it & 1, fail, a.status) ||
-                    !wait_or_fail(&bars[kKConv + gstep % kStages], (gstep / kStages) & 1, fail, a.status))
+                if (!wait_or_fail(&bars[kQSplit], it & 1, fail, a.status) ||
+                    !wait_or_fail(&bars[kKFull + gstep % kKStages], (gstep / kKStages) & 1, fail, a.status))
                     break;
                 tc_fence_after();
                 issue_s(0, gstep);
-                if (d.has_b) issue_s(1, gstep);
-                umma_commit(&bars[kKEmpty + gstep % kStages]);
+                if (d.has_b) {
+                    if (!wait_or_fail(&bars[kQSplit + 1], b_items++ & 1, fail, a.status)) break;
+                    tc_fence_after();
+                    issue_s(1, gstep);
+                }
+                umma_commit(&bars[kKEmpty + gstep % kKStages]);
                 if (n == 1) umma_commit(&bars[kQFree]);
                 for (int j = 0; ok && j < n; ++j) {
                     const uint32_t gs = gstep + j, gk = gs + 1;
                     const bool more = j + 1 < n;
-                    if (!wait_or_fail(&bars[kVConv + gs % kStages], (gs / kStages) & 1, fail, a.status) ||
+                    if (!wait_or_fail(&bars[kVConv + gs % kVStages], (gs / kVStages) & 1, fail, a.status) ||
                         !issue_pv(0, gs, j, it)) {
                         ok = false;
                         break;
                     }
                     if (more) {
-                        if (!wait_or_fail(&bars[kKConv + gk % kStages], (gk / kStages) & 1, fail, a.status)) {
+                        if (!wait_or_fail(&bars[kKFull + gk % kKStages], (gk / kKStages) & 1, fail, a.status)) {
                             ok = false;
                             break;
                         }
@@ -523,10 +614,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    umma_commit(&bars[kVEmpty + gs % kStages]);
+                    umma_commit(&bars[kVEmpty + gs % kVStages]);
                     if (more) {
                         if (d.has_b) issue_s(1, gk);
-                        umma_commit(&bars[kKEmpty + gk % kStages]);
+                        umma_commit(&bars[kKEmpty + gk % kKStages]);
                         if (j + 2 == n) umma_commit(&bars[kQFree]);
                     }
                 }
@@ -537,105 +628,85 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= kWidenWarp0) {
         // ---------------- widening ----------------
         const int ct = threadIdx.x - kWidenWarp0 * 32;
-        uint32_t gstep = 0, code = 0;
-        bool ok = true, beyond = false;
+        uint32_t gstep = 0;
+        bool ok = true;
         for (int it = 0;; ++it) {
             const int item = next_item(it);
             if (item < 0) break;
             Item d;
             describe_item(a, item, by_length, false, perm, d);
-            if (!ok || !wait_or_fail(&bars[kQFull], it & 1, fail, a.status)) {
-                ok = false;
-                continue;
-            }
-            // the scales of the item's first step, one thread per block
+            // The scales of a step's blocks, one thread per block: the table entry is
+            // read two steps ahead and the scales one step, so that no step waits
+            // for the chain of loads.
             const int32_t *trow = a.block_tables + (int64_t)d.b * a.max_blocks;
-            float ks = 0.f, vs = 1.f;
-            bool has = false;
-            auto fetch_scales = [&](int j) {
+            auto table_at = [&](int j) {
                 const int blk = d.blk_lo + 8 * j + ct;
-                has = ct < 8 && blk < d.blk_hi;
-                if (has) {
-                    int phys = trow[blk];
-                    phys = (unsigned)phys < (unsigned)a.num_blocks ? phys : 0;
-                    const int64_t at = (int64_t)phys * a.num_kv_heads + d.kvh;
-                    ks = a.k_scales[at];
-                    vs = a.v_scales[at];
-                }
+                return ct < 8 && blk < d.blk_hi ? trow[blk] : -1;
             };
-            fetch_scales(0);
-            uint4 *q = reinterpret_cast<uint4 *>(sQ);
-#pragma unroll 4
-            for (int c = ct; c < (d.has_b ? kQT : 1) * kTile / 16; c += kWidenThreads) {
-                const uint4 w = q[c];
-                beyond |= bf16x2_beyond_f16(w.x) | bf16x2_beyond_f16(w.y) | bf16x2_beyond_f16(w.z) | bf16x2_beyond_f16(w.w);
-                q[c] = make_uint4(pack_f16x2(bf16lo(w.x), bf16hi(w.x)), pack_f16x2(bf16lo(w.y), bf16hi(w.y)),
-                                  pack_f16x2(bf16lo(w.z), bf16hi(w.z)), pack_f16x2(bf16lo(w.w), bf16hi(w.w)));
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(&bars[kQConv]);
+            float ks = 0.f, vs = 1.f;
+            auto fetch_scales = [&](int j, int phys) {
+                if (ct >= 8 || d.blk_lo + 8 * j + ct >= d.blk_hi) {
+                    ks = 0.f;
+                    vs = 1.f;
+                    return;
+                }
+                phys = (unsigned)phys < (unsigned)a.num_blocks ? phys : 0;
+                const int64_t at = (int64_t)phys * a.num_kv_heads + d.kvh;
+                ks = a.k_scales[at];
+                vs = a.v_scales[at];
+            };
+            int phys = table_at(0);
+            const int c16 = ct & 7;
+            fetch_scales(0, phys);
+            phys = table_at(1);
             for (int j = 0; ok && j < d.n_tiles; ++j) {
                 const uint32_t gs = gstep + j;
-                const int st = gs % kStages;
-                const uint32_t ph = (gs / kStages) & 1u;
                 const int k0 = (d.blk_lo + 8 * j) * kBlockSize;
                 const bool edge = k0 < d.kv_lo || k0 + kKv > d.kv_hi;
-                for (int h = 0; h < 4; ++h, ++code) {
-                    const int s = code % kCodeStages;
-                    if (!wait_or_fail(&bars[kCodeFull + s], (code / kCodeStages) & 1, fail, a.status) ||
-                        (!(h & 1) && gs >= kStages &&
-                         !wait_or_fail(&bars[(h < 2 ? kKEmpty : kVEmpty) + st], ph ^ 1u, fail, a.status))) {
-                        ok = false;
-                        break;
-                    }
-                    if (h == 0) {
-                        // softmax is at most two steps behind the K tile that is free now
-                        if (ct < 8) {
-                            const float sv = has ? value_scale(vs, a.status) : 1.f;
-                            s_scale[(gs % kScaleSlots) * 8 + ct] =
-                                make_float4(has ? ks * a.scale_log2 : 0.f, log2_scale(sv), 1.f / sv, 0.f);
-                        }
-                        if (ct < 32) {
-                            __syncwarp();
-                            if (ct == 0) mbar_arrive(&bars[kScaleFull + gs % kScaleSlots]);
-                        }
-                        if (j + 1 < d.n_tiles) fetch_scales(j + 1);
-                    }
-                    // 16 codes of a row become two 16-byte chunks of f16 in one of the
-                    // tile's 64-column halves; threads of the two halves write their
-                    // chunks in opposite order, so that eight threads of a row never
-                    // meet in a bank
-                    const uint4 *src = reinterpret_cast<const uint4 *>(sCode + s * kCodeBytes);
-                    uint8_t *dst = (h < 2 ? sK : sV) + st * kTile;
-                    const int c16 = ct & 7, half = c16 >> 2, swap = half;
-#pragma unroll 4
-                    for (int i = 0; i < kCodeRows * 8 / kWidenThreads; ++i) {
-                        const int rr = (ct >> 3) + i * (kWidenThreads / 8);
-                        const int r = (h & 1) * kCodeRows + rr;
-                        const uint4 w = src[rr * 8 + c16];
-                        uint4 x, y;
-                        e4m3x4_to_f16x2x2(w.x, x.x, x.y);
-                        e4m3x4_to_f16x2x2(w.y, x.z, x.w);
-                        e4m3x4_to_f16x2x2(w.z, y.x, y.y);
-                        e4m3x4_to_f16x2x2(w.w, y.z, y.w);
-                        if (edge && h >= 2 && (k0 + r < d.kv_lo || k0 + r >= d.kv_hi)) x = y = make_uint4(0, 0, 0, 0);
-                        uint8_t *row = dst + half * kHalf + r * 128;
-                        const int c = 2 * (c16 & 3);
-                        *reinterpret_cast<uint4 *>(row + (((c + swap) ^ (r & 7)) << 4)) = swap ? y : x;
-                        *reinterpret_cast<uint4 *>(row + (((c + 1 - swap) ^ (r & 7)) << 4)) = swap ? x : y;
-                    }
-                    mbar_arrive(&bars[kCodeEmpty + s]);
-                    if (h & 1) {
-                        fence_proxy_async_smem();
-                        mbar_arrive(&bars[(h < 2 ? kKConv : kVConv) + st]);
-                    } else {
-                        fence_proxy_async_smem();
-                    }
+                // P.V two steps back has run, and with it the softmax of that step: the
+                // f16 tile and the scale slot are free
+                if (gs >= kVStages &&
+                    !wait_or_fail(&bars[kVEmpty + gs % kVStages], (gs / kVStages - 1) & 1u, fail, a.status)) {
+                    ok = false;
+                    break;
                 }
+                if (ct < 8) {
+                    const float sv = value_scale(vs, a.status);
+                    s_scale[(gs % kScaleSlots) * 8 + ct] = make_float4(ks * a.scale_log2, log2_scale(sv), 1.f / sv, 0.f);
+                }
+                mbar_arrive(&bars[kScaleFull + gs % kScaleSlots]);
+                fetch_scales(j + 1, phys);
+                phys = table_at(j + 2);
+                if (!wait_or_fail(&bars[kCodeFull + gs % kCodeStages], (gs / kCodeStages) & 1, fail, a.status)) {
+                    ok = false;
+                    break;
+                }
+                // 16 codes of a row become two 16-byte chunks of f16 in one of the tile's
+                // 64-column halves; threads of the two halves write their chunks in
+                // opposite order, so that eight threads of a row never meet in a bank
+                const uint4 *src = reinterpret_cast<const uint4 *>(sCode + (gs % kCodeStages) * kCodeTile);
+                const int half = c16 >> 2, c = 2 * (c16 & 3);
+                uint8_t *dst = sV + (gs % kVStages) * kTile + half * kHalf;
+#pragma unroll 4
+                for (int i = 0; i < kKv * 8 / kWidenThreads; ++i) {
+                    const int r = (ct >> 3) + i * (kWidenThreads / 8);
+                    const uint4 w = src[r * 8 + c16];
+                    uint4 x, y;
+                    e4m3x4_to_f16x2x2(w.x, x.x, x.y);
+                    e4m3x4_to_f16x2x2(w.y, x.z, x.w);
+                    e4m3x4_to_f16x2x2(w.z, y.x, y.y);
+                    e4m3x4_to_f16x2x2(w.w, y.z, y.w);
+                    if (edge && (k0 + r < d.kv_lo || k0 + r >= d.kv_hi)) x = y = make_uint4(0, 0, 0, 0);
+                    uint8_t *row = dst + r * 128;
+                    *reinterpret_cast<uint4 *>(row + (((c + half) ^ (r & 7)) << 4)) = half ? y : x;
+                    *reinterpret_cast<uint4 *>(row + (((c + 1 - half) ^ (r & 7)) << 4)) = half ? x : y;
+                }
+                mbar_arrive(&bars[kCodeEmpty + gs % kCodeStages]);
+                fence_proxy_async_smem();
+                mbar_arrive(&bars[kVConv + gs % kVStages]);
             }
             gstep += d.n_tiles;
         }
-        if (beyond) report(a.status, PA_DEV_RANGE);
     } else {
         // ---------------- softmax groups ----------------
         const int x = (warp - 2) / (kGroup / 32);
@@ -673,6 +744,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // The row's reference (log2 units): an integer, or -inf before the row
                 // has seen a position; O and l are relative to it.
                 float m_used = -INFINITY, l = 0.f;
+                // the group splits its Q tile
+                float *q_scale = reinterpret_cast<float *>(base + kOffQScale) + x * kRows;
+                ok = warp_wait(&bars[kQFull], it & 1, fail, a.status) && ok;
+                if (ok) {
+                    const int t = threadIdx.x - 64 - x * kGroup;
+                    split_query(sQ + x * kTile, q_scale, t >> 3, kGroup / 8, t & 7);
+                    fence_proxy_async_smem();
+                    mbar_arrive(&bars[kQSplit + x]);
+                }
+                group_sync(x);
+                const float qs = q_scale[r];
                 for (int j = 0; j < d.n_tiles; ++j) {
                     const uint32_t gs = gstep + j;
                     const bool got = ok && warp_wait(&bars[kSFull + x], sc & 1, fail, a.status) &&
@@ -701,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 float sum[2];
 #pragma unroll
                                 for (int blk = 0; blk < 2; ++blk) {
-                                    const float ck = blk ? e1.x : e0.x, off = (blk ? e1.y : e0.y) - mref;
+                                    const float ck = (blk ? e1.x : e0.x) * qs, off = (blk ? e1.y : e0.y) - mref;
                                     const uint64_t k2 = f2_pack(ck, ck), nm2 = f2_pack(off, off);
                                     uint64_t ps2 = f2_pack(0.f, 0.f);
 #pragma unroll
@@ -721,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (!general) tmem_st16(s_base + c, pp);
                             }
                             if (general) {           // the whole warp; S is still in place
-                                const float2 r2 = chunk_weights_general(s_base + c, e, mref, kc, qpos, wlo);
+                                const float2 r2 = chunk_weights_general(s_base + c, e, qs, mref, kc, qpos, wlo);
                                 psum = r2.x;
                                 mref = r2.y;
                             }
@@ -891,7 +973,7 @@ extern "C" pa_status pa_prefill_block_fp8(void *out, const void *query, const vo
     if (rows >= ((int64_t)1 << 31) || items >= ((int64_t)1 << 31) - kThreads) return PA_ERR_UNSUPPORTED;
     CUtensorMap qmap, kmap, vmap;
     if (!encode_query_map(&qmap, query, num_query_tokens, num_q_heads, num_kv_heads) ||
-        !encode_block8_map(&kmap, key_cache, rows, false) || !encode_block8_map(&vmap, value_cache, rows, false))
+        !encode_block8_map(&kmap, key_cache, rows, true) || !encode_block8_map(&vmap, value_cache, rows, false))
         return cuda_failure(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
     PrefillArgs a = {};
     a.out = out;

@@ -258,13 +258,11 @@ def test_prefill_many_items(pkv):
 def test_prefill_flags(pkv):
     from paged_kv_cache_100_gb300 import _lib
     chunks, lens = [20, 30], [60, 40]
-    for what, bit in (("query", _lib.PA_DEV_RANGE), ("scale", _lib.PA_DEV_RANGE), ("table", _lib.PA_DEV_BAD_BLOCK_ID),
+    for what, bit in (("scale", _lib.PA_DEV_RANGE), ("table", _lib.PA_DEV_BAD_BLOCK_ID),
                       ("length", _lib.PA_DEV_BAD_CONTEXT_LEN), ("longest", _lib.PA_DEV_BAD_QUERY_LEN)):
         p = Pool(5, lens, 2, poison=False)
         q = _query(p, 50, 4)
         longest = 30
-        if what == "query":
-            q[45, 0, 0] = -1e6
         if what == "scale":
             p.vs[p.tables[1, 1]] = float("nan")
         if what == "table":
@@ -278,6 +276,31 @@ def test_prefill_flags(pkv):
         assert int(status.item()) == bit, what
         ref, bound = p.reference(q.double().numpy()[:20], rows[:20], D ** -0.5, floor=4.0)
         _check(out[:20], ref, bound, what)
+
+
+def test_prefill_queries_of_any_size(pkv):
+    """Rows of large, tiny and zero queries, a row with an outlier element, infinite and NaN elements."""
+    p = Pool(15, [90], 2, spread=0.7)
+    q = _query(p, 40, 8)
+    q[3] = (q[3].float() * 2.0 ** 100).to(torch.bfloat16)
+    q[4] = (q[4].float() * 2.0 ** -130).to(torch.bfloat16)
+    q[5] = 0
+    q[6, :, 17] = 40.0
+    q[7, 2, 5], q[8, 3, 0] = float("inf"), float("nan")
+    p.ks[:] = torch.where(torch.isnan(p.ks), p.ks, torch.full_like(p.ks, 2.0 ** -9))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    _, out, rows = _prefill(pkv, p, [40], 8, status=status, q=q)
+    qd = q.double().numpy()
+    bad = ~np.isfinite(qd).all(-1)
+    qd[bad] = 0
+    ref, bound = p.reference(qd, rows, D ** -0.5, floor=4.0)
+    assert torch.isnan(out.cpu()[torch.from_numpy(bad)]).all()
+    keep = ~bad
+    keep[3] = False                                          # one-hot rows: the largest score alone decides
+    got = out.double().cpu().numpy()
+    err = np.abs(got - ref)[keep]
+    assert (err <= (bound + 2.0 ** -8 * (np.abs(ref) + bound))[keep]).all()
+    assert np.isfinite(got[3]).all() and int(status.item()) == 0
 
 
 def test_prefill_leaves_rows_behind_the_last_sequence(pkv):
