@@ -27,7 +27,7 @@
 //                against an integer reference that rises only when a chunk's
 //                weights would leave f16's range; they also split their Q tile;
 //   warps 18, 19 widen each V tile, zeroing positions outside the item's range,
-//                and stage the blocks' scales.
+//                and stage the scales of the step after.
 // Persistent CTAs take items from a ticket counter; barrier phases are counted
 // across items, so an item's loads start under the end of the one before.
 // Every wait is bounded (about a second); one that gives up sets PA_DEV_TIMEOUT,
@@ -59,12 +59,13 @@ constexpr int kCols = 64;                // S / O columns per softmax thread (tw
 constexpr int kGroup = 2 * kRows;        // softmax threads per Q tile
 constexpr int kWidenWarp0 = 2 + kQT * kGroup / 32;
 constexpr int kWidenThreads = 64;
-constexpr int kThreads = kWidenWarp0 * 32 + kWidenThreads;
+constexpr int kThreads = kWidenWarp0 * 32 + kWidenThreads;   // 640: one warp more would cost 16 registers a thread
 constexpr int kCodeTile = kKv * kD;      // codes of a K or V tile
 constexpr int kKStages = 3;              // K code tiles
 constexpr int kCodeStages = 2;           // V code tiles
 constexpr int kVStages = 2;              // f16 V tiles
 constexpr int kScaleSlots = 4;
+
 constexpr float kChunkSumMax = 32768.f;  // largest weight sum of a 32-column chunk kept as computed: f16 holds its weights
 constexpr size_t kWorkspaceBytes = 256;  // the ticket counter (rounded up)
 
@@ -101,6 +102,15 @@ __device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t x) {
 __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
     const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
     return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
 
 // D[tmem] (+)= A[smem] * B[smem], both E4M3; issued by one thread.
@@ -406,8 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kNumBars; ++i) {
             int n = 1;
-            if ((i >= kCodeEmpty && i < kCodeEmpty + kCodeStages) || (i >= kVConv && i < kVConv + kVStages) ||
-                i >= kScaleFull)
+            if ((i >= kCodeEmpty && i < kCodeEmpty + kCodeStages) || (i >= kVConv && i < kVConv + kVStages))
                 n = kWidenThreads;
             if ((i >= kQSplit && i < kQSplit + kQT) || (i >= kPFull && i < kPFull + kQT) || (i >= kOFree && i < kOFree + kQT)) n = kGroup;
             if (i >= kItemEmpty && i < kItemEmpty + 2) n = 1 + kQT * kGroup + kWidenThreads;
@@ -546,88 +555,109 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
-        if (lane == 0) {
-            constexpr uint32_t idS = idesc_e4m3_f32(kRows, kKv);
-            constexpr uint32_t idPV = idesc_f16_f32(kRows, kD, true);
-            const uint32_t q_u = smem_u32(sQ), k_u = smem_u32(sK), v_u = smem_u32(sV);
-            uint32_t gstep = 0;
-            uint32_t pcount[kQT] = {0, 0}, b_items = 0;
-            bool ok = true;
-            auto issue_s = [&](int x, uint32_t gs) {
-                const uint32_t kb = k_u + (gs % kKStages) * kCodeTile;
+        // The whole warp runs the loop and one elected lane issues: descriptors then
+        // stay in uniform registers.  Issued from a one-lane branch, a batch of eight
+        // products took about 600 cycles and the issuing lane bounded the step.
+        constexpr uint32_t idS = idesc_e4m3_f32(kRows, kKv);
+        constexpr uint32_t idPV = idesc_f16_f32(kRows, kD, true);
+        const uint64_t q_desc = sw128_desc(smem_u32(sQ), 16, 1024), k_desc = sw128_desc(smem_u32(sK), 16, 1024),
+                       v_desc = sw128_desc(smem_u32(sV), kHalf, 1024);
+        uint32_t gstep = 0;
+        uint32_t pcount[kQT] = {0, 0}, b_items = 0;
+        bool ok = true;
+        // S_x = Q_x K^T: q1, then q2, in steps of 32 codes (descriptors count 16 bytes)
+        auto issue_s = [&](int x, uint32_t gs) {
+            tc_fence_after();
+            const uint64_t qd = q_desc + (uint64_t)(x * (kTile / 16)), kd = k_desc + (uint64_t)((gs % kKStages) * (kCodeTile / 16));
+            if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)          // q1, then q2, in steps of 32 codes
-                    umma_f8(tmem + col_s(x), sw128_desc(q_u + x * kTile + (k >> 2) * kHalf + (k & 3) * 32, 16, 1024),
-                            sw128_desc(kb + (k & 3) * 32, 16, 1024), idS, k > 0 ? 1u : 0u);
+                for (int k = 0; k < 8; ++k)
+                    umma_f8(tmem + col_s(x), qd + (uint64_t)((k >> 2) * (kHalf / 16) + (k & 3) * 2), kd + (uint64_t)((k & 3) * 2),
+                            idS, k > 0 ? 1u : 0u);
                 umma_commit(&bars[kSFull + x]);
-            };
-            // P of tokens [16 k, 16 k + 16): f16 pairs from column 32 (k / 2) + 8 (k % 2) of the S buffer
-            auto issue_pv = [&](int x, uint32_t gs, int j, int it) -> bool {
-                if (!wait_or_fail(&bars[kPFull + x], pcount[x] & 1, fail, a.status)) return false;
-                ++pcount[x];
-                // the first P.V of an item overwrites O: the item before must have read it out
-                if (j == 0 && it >= 1 && !wait_or_fail(&bars[kOFree + x], (it - 1) & 1, fail, a.status)) return false;
-                tc_fence_after();
-                const uint32_t vb = v_u + (gs % kVStages) * kTile;
+            }
+            __syncwarp();
+        };
+        // O_x += P_x V: P of tokens [16 k, 16 k + 16) is f16 pairs from column
+        // 32 (k / 2) + 8 (k % 2) of the S buffer
+        auto issue_pv = [&](int x, uint32_t gs, int j, int it) -> bool {
+            if (!warp_wait(&bars[kPFull + x], pcount[x] & 1, fail, a.status)) return false;
+            ++pcount[x];
+            // the first P.V of an item overwrites O: the item before must have read it out
+            if (j == 0 && it >= 1 && !warp_wait(&bars[kOFree + x], (it - 1) & 1, fail, a.status)) return false;
+            tc_fence_after();
+            const uint64_t vd = v_desc + (uint64_t)((gs % kVStages) * (kTile / 16));
+            if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     umma_bf16_tmem_a(tmem + col_o(x), tmem + col_s(x) + 32 * (k >> 1) + 8 * (k & 1),
-                                     sw128_desc(vb + k * 2048, kHalf, 1024), idPV, (j > 0 || k > 0) ? 1u : 0u);
+                                     vd + (uint64_t)(k * (2048 / 16)), idPV, (j > 0 || k > 0) ? 1u : 0u);
                 umma_commit(&bars[kPvDone + x]);
-                return true;
-            };
-            for (int it = 0; ok; ++it) {
-                const int item = next_item(it);
-                if (item < 0) break;
-                Item d;
-                describe_item(a, item, by_length, false, perm, d);
-                const int n = d.n_tiles;
-                if (!wait_or_fail(&bars[kQSplit], it & 1, fail, a.status) ||
-                    !wait_or_fail(&bars[kKFull + gstep % kKStages], (gstep / kKStages) & 1, fail, a.status))
-                    break;
-                tc_fence_after();
-                issue_s(0, gstep);
-                if (d.has_b) {
-                    if (!wait_or_fail(&bars[kQSplit + 1], b_items++ & 1, fail, a.status)) break;
-                    tc_fence_after();
-                    issue_s(1, gstep);
-                }
-                umma_commit(&bars[kKEmpty + gstep % kKStages]);
-                if (n == 1) umma_commit(&bars[kQFree]);
-                for (int j = 0; ok && j < n; ++j) {
-                    const uint32_t gs = gstep + j, gk = gs + 1;
-                    const bool more = j + 1 < n;
-                    if (!wait_or_fail(&bars[kVConv + gs % kVStages], (gs / kVStages) & 1, fail, a.status) ||
-                        !issue_pv(0, gs, j, it)) {
-                        ok = false;
-                        break;
-                    }
-                    if (more) {
-                        if (!wait_or_fail(&bars[kKFull + gk % kKStages], (gk / kKStages) & 1, fail, a.status)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        issue_s(0, gk);
-                    }
-                    if (d.has_b && !issue_pv(1, gs, j, it)) {
-                        ok = false;
-                        break;
-                    }
-                    umma_commit(&bars[kVEmpty + gs % kVStages]);
-                    if (more) {
-                        if (d.has_b) issue_s(1, gk);
-                        umma_commit(&bars[kKEmpty + gk % kKStages]);
-                        if (j + 2 == n) umma_commit(&bars[kQFree]);
-                    }
-                }
-                umma_commit(&bars[kDrain]);          // every MMA of the item has completed once it flips
-                gstep += n;
             }
+            __syncwarp();
+            return true;
+        };
+        auto commit = [&](int bar) {
+            if (elect_one()) umma_commit(&bars[bar]);
+            __syncwarp();
+        };
+        for (int it = 0; ok; ++it) {
+            const int slot = it & 1;
+            const int item = warp_wait(&bars[kItemFull + slot], (it >> 1) & 1, fail, a.status) ? s_item[slot] : -1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kItemEmpty + slot]);
+            if (item < 0) break;
+            Item d;
+            describe_item(a, item, by_length, false, perm, d);
+            const int n = d.n_tiles;
+            if (!warp_wait(&bars[kQSplit], it & 1, fail, a.status) ||
+                !warp_wait(&bars[kKFull + gstep % kKStages], (gstep / kKStages) & 1, fail, a.status))
+                break;
+            issue_s(0, gstep);
+            if (d.has_b) {
+                if (!warp_wait(&bars[kQSplit + 1], b_items++ & 1, fail, a.status)) break;
+                issue_s(1, gstep);
+            }
+            commit(kKEmpty + gstep % kKStages);
+            if (n == 1) commit(kQFree);
+            for (int j = 0; j < n; ++j) {
+                const uint32_t gs = gstep + j, gk = gs + 1;
+                const bool more = j + 1 < n;
+                if (!warp_wait(&bars[kVConv + gs % kVStages], (gs / kVStages) & 1, fail, a.status) || !issue_pv(0, gs, j, it)) {
+                    ok = false;
+                    break;
+                }
+                if (more) {
+                    if (!warp_wait(&bars[kKFull + gk % kKStages], (gk / kKStages) & 1, fail, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    issue_s(0, gk);
+                }
+                if (d.has_b && !issue_pv(1, gs, j, it)) {
+                    ok = false;
+                    break;
+                }
+                commit(kVEmpty + gs % kVStages);
+                if (more) {
+                    if (d.has_b) issue_s(1, gk);
+                    commit(kKEmpty + gk % kKStages);
+                    if (j + 2 == n) commit(kQFree);
+                }
+            }
+            commit(kDrain);                          // every MMA of the item has completed once it flips
+            gstep += n;
         }
     } else if (warp >= kWidenWarp0) {
         // ---------------- widening ----------------
+        // 16 codes of a row become two 16-byte chunks of f16 in one of the tile's
+        // 64-column halves; threads of the two halves write their chunks in opposite
+        // order, so that eight threads of a row never meet in a bank.  Eight rows are
+        // loaded before the first is written: the loop is bound by latency.
         const int ct = threadIdx.x - kWidenWarp0 * 32;
+        const int c16 = ct & 7, half = c16 >> 2, c = 2 * (c16 & 3);
+        constexpr int kRowStep = kWidenThreads / 8, kBatch = 8;
+        static_assert(kKv % (kRowStep * kBatch) == 0 && kRowStep % 8 == 0, "whole batches, one swizzle phase per thread");
         uint32_t gstep = 0;
         bool ok = true;
         for (int it = 0;; ++it) {
@@ -635,75 +665,87 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (item < 0) break;
             Item d;
             describe_item(a, item, by_length, false, perm, d);
-            // The scales of a step's blocks, one thread per block: the table entry is
-            // read two steps ahead and the scales one step, so that no step waits
-            // for the chain of loads.
+            // The scales of a step's blocks, one thread per block of the first warp.  The
+            // table entry is read two steps ahead and the scales one step, so that no
+            // step waits for the chain of loads; the slot written last held the scales of
+            // four steps back, whose softmax came before P.V of two steps back, which
+            // this loop has waited for.
             const int32_t *trow = a.block_tables + (int64_t)d.b * a.max_blocks;
+            float ks = 0.f, vs = 1.f;
+            int phys = -1;
             auto table_at = [&](int j) {
                 const int blk = d.blk_lo + 8 * j + ct;
-                return ct < 8 && blk < d.blk_hi ? trow[blk] : -1;
+                phys = ct < 8 && blk < d.blk_hi ? trow[blk] : -1;
             };
-            float ks = 0.f, vs = 1.f;
-            auto fetch_scales = [&](int j, int phys) {
-                if (ct >= 8 || d.blk_lo + 8 * j + ct >= d.blk_hi) {
-                    ks = 0.f;
-                    vs = 1.f;
-                    return;
+            auto fetch_scales = [&](int j) {
+                ks = 0.f;
+                vs = 1.f;
+                if (ct < 8 && d.blk_lo + 8 * j + ct < d.blk_hi) {
+                    const int64_t at = (int64_t)((unsigned)phys < (unsigned)a.num_blocks ? phys : 0) * a.num_kv_heads + d.kvh;
+                    ks = a.k_scales[at];
+                    vs = a.v_scales[at];
                 }
-                phys = (unsigned)phys < (unsigned)a.num_blocks ? phys : 0;
-                const int64_t at = (int64_t)phys * a.num_kv_heads + d.kvh;
-                ks = a.k_scales[at];
-                vs = a.v_scales[at];
             };
-            int phys = table_at(0);
-            const int c16 = ct & 7;
-            fetch_scales(0, phys);
-            phys = table_at(1);
-            for (int j = 0; ok && j < d.n_tiles; ++j) {
-                const uint32_t gs = gstep + j;
-                const int k0 = (d.blk_lo + 8 * j) * kBlockSize;
-                const bool edge = k0 < d.kv_lo || k0 + kKv > d.kv_hi;
-                // P.V two steps back has run, and with it the softmax of that step: the
-                // f16 tile and the scale slot are free
-                if (gs >= kVStages &&
-                    !wait_or_fail(&bars[kVEmpty + gs % kVStages], (gs / kVStages - 1) & 1u, fail, a.status)) {
-                    ok = false;
-                    break;
-                }
+            auto stage_scales = [&](uint32_t gs) {
+                if (ct >= 32) return;
                 if (ct < 8) {
                     const float sv = value_scale(vs, a.status);
                     s_scale[(gs % kScaleSlots) * 8 + ct] = make_float4(ks * a.scale_log2, log2_scale(sv), 1.f / sv, 0.f);
                 }
-                mbar_arrive(&bars[kScaleFull + gs % kScaleSlots]);
-                fetch_scales(j + 1, phys);
-                phys = table_at(j + 2);
-                if (!wait_or_fail(&bars[kCodeFull + gs % kCodeStages], (gs / kCodeStages) & 1, fail, a.status)) {
+                __syncwarp();
+                if (ct == 0) mbar_arrive(&bars[kScaleFull + gs % kScaleSlots]);
+            };
+            table_at(0);
+            fetch_scales(0);
+            table_at(1);
+            if (ok) stage_scales(gstep);
+            fetch_scales(1);
+            table_at(2);
+            for (int j = 0; ok && j < d.n_tiles; ++j) {
+                const uint32_t gs = gstep + j;
+                if (!wait_or_fail(&bars[kCodeFull + gs % kCodeStages], (gs / kCodeStages) & 1, fail, a.status) ||
+                    (gs >= kVStages &&
+                     !wait_or_fail(&bars[kVEmpty + gs % kVStages], (gs / kVStages - 1) & 1u, fail, a.status))) {
                     ok = false;
                     break;
                 }
-                // 16 codes of a row become two 16-byte chunks of f16 in one of the tile's
-                // 64-column halves; threads of the two halves write their chunks in
-                // opposite order, so that eight threads of a row never meet in a bank
-                const uint4 *src = reinterpret_cast<const uint4 *>(sCode + (gs % kCodeStages) * kCodeTile);
-                const int half = c16 >> 2, c = 2 * (c16 & 3);
-                uint8_t *dst = sV + (gs % kVStages) * kTile + half * kHalf;
-#pragma unroll 4
-                for (int i = 0; i < kKv * 8 / kWidenThreads; ++i) {
-                    const int r = (ct >> 3) + i * (kWidenThreads / 8);
-                    const uint4 w = src[r * 8 + c16];
-                    uint4 x, y;
-                    e4m3x4_to_f16x2x2(w.x, x.x, x.y);
-                    e4m3x4_to_f16x2x2(w.y, x.z, x.w);
-                    e4m3x4_to_f16x2x2(w.z, y.x, y.y);
-                    e4m3x4_to_f16x2x2(w.w, y.z, y.w);
-                    if (edge && (k0 + r < d.kv_lo || k0 + r >= d.kv_hi)) x = y = make_uint4(0, 0, 0, 0);
-                    uint8_t *row = dst + r * 128;
-                    *reinterpret_cast<uint4 *>(row + (((c + half) ^ (r & 7)) << 4)) = half ? y : x;
-                    *reinterpret_cast<uint4 *>(row + (((c + 1 - half) ^ (r & 7)) << 4)) = half ? x : y;
+                const uint4 *src = reinterpret_cast<const uint4 *>(sCode + (gs % kCodeStages) * kCodeTile) + ct;
+                uint8_t *dst = sV + (gs % kVStages) * kTile + half * kHalf + (ct >> 3) * 128;
+                const int sw = (ct >> 3) & 7, at0 = ((c + half) ^ sw) << 4, at1 = ((c + 1 - half) ^ sw) << 4;
+#pragma unroll
+                for (int b = 0; b < kKv / kRowStep; b += kBatch) {
+                    uint4 w[kBatch];
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) w[i] = src[(b + i) * kWidenThreads];
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        uint4 x, y;
+                        e4m3x4_to_f16x2x2(w[i].x, x.x, x.y);
+                        e4m3x4_to_f16x2x2(w[i].y, x.z, x.w);
+                        e4m3x4_to_f16x2x2(w[i].z, y.x, y.y);
+                        e4m3x4_to_f16x2x2(w[i].w, y.z, y.w);
+                        *reinterpret_cast<uint4 *>(dst + (b + i) * kRowStep * 128 + at0) = half ? y : x;
+                        *reinterpret_cast<uint4 *>(dst + (b + i) * kRowStep * 128 + at1) = half ? x : y;
+                    }
                 }
                 mbar_arrive(&bars[kCodeEmpty + gs % kCodeStages]);
+                // positions outside the item's range may hold anything, NaN among it
+                const int k0 = (d.blk_lo + 8 * j) * kBlockSize;
+                if (k0 < d.kv_lo || k0 + kKv > d.kv_hi) {
+                    for (int r = ct >> 3; r < kKv; r += kRowStep)
+                        if (k0 + r < d.kv_lo || k0 + r >= d.kv_hi) {
+                            uint8_t *row = dst + (r - (ct >> 3)) * 128;
+                            *reinterpret_cast<uint4 *>(row + at0) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4 *>(row + at1) = make_uint4(0, 0, 0, 0);
+                        }
+                }
                 fence_proxy_async_smem();
                 mbar_arrive(&bars[kVConv + gs % kVStages]);
+                if (j + 1 < d.n_tiles) {
+                    stage_scales(gs + 1);
+                    fetch_scales(j + 2);
+                    table_at(j + 3);
+                }
             }
             gstep += d.n_tiles;
         }
