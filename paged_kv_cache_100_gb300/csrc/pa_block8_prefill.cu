@@ -623,17 +623,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < n; ++j) {
                 const uint32_t gs = gstep + j, gk = gs + 1;
                 const bool more = j + 1 < n;
-                if (!warp_wait(&bars[kVConv + gs % kVStages], (gs / kVStages) & 1, fail, a.status) || !issue_pv(0, gs, j, it)) {
+                // what is usually there already first: these waits run beside the
+                // products in flight, the one for P does not
+                if (!warp_wait(&bars[kVConv + gs % kVStages], (gs / kVStages) & 1, fail, a.status) ||
+                    (more && !warp_wait(&bars[kKFull + gk % kKStages], (gk / kKStages) & 1, fail, a.status)) ||
+                    !issue_pv(0, gs, j, it)) {
                     ok = false;
                     break;
                 }
-                if (more) {
-                    if (!warp_wait(&bars[kKFull + gk % kKStages], (gk / kKStages) & 1, fail, a.status)) {
-                        ok = false;
-                        break;
-                    }
-                    issue_s(0, gk);
-                }
+                if (more) issue_s(0, gk);
                 if (d.has_b && !issue_pv(1, gs, j, it)) {
                     ok = false;
                     break;
