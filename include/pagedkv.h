@@ -474,7 +474,7 @@ pa_status pa_plan_step(int32_t *block_tables, const int32_t *context_lens, const
  *                       0.1 ln(factor) + 1 for a factor above 1
  *  turns             host uint64 [rotary_dim / 2]: theta_i / (2 pi), as a
  *                    64-bit fraction of a whole turn
- *  attention_factor  host float: multiplies cos and sin (1 otherwise)
+ *  attention_factor  host double: multiplies cos and sin (1 otherwise)
  * Host only; no CUDA call.
  */
 typedef enum pa_rotary_scaling {
@@ -483,7 +483,7 @@ typedef enum pa_rotary_scaling {
     PA_ROTARY_NTK = 2,
     PA_ROTARY_BY_PARTS = 3
 } pa_rotary_scaling;
-pa_status pa_rotary_turns(uint64_t *turns, float *attention_factor, int rotary_dim, double base,
+pa_status pa_rotary_turns(uint64_t *turns, double *attention_factor, int rotary_dim, double base,
                           pa_rotary_scaling scaling, double factor, double original_context,
                           double beta_fast, double beta_slow);
 
@@ -491,8 +491,8 @@ pa_status pa_rotary_turns(uint64_t *turns, float *attention_factor, int rotary_d
  * Rotary positions on the new tokens' queries and keys, and the cache write.
  * Every token i's first rotary_dim elements of each query and key head are
  * turned by its position's angles,
- *   y0 = A (x0 cos - x1 sin), y1 = A (x1 cos + x0 sin),  A = attention_factor,
- * where the pairs (x0, x1) are elements (j, j + rotary_dim / 2), or
+ *   y0 = A (x0 cos - x1 sin), y1 = A (x1 cos + x0 sin),  A = attention_factor
+ * in [2^-20, 2^20], where the pairs (x0, x1) are elements (j, j + rotary_dim / 2), or
  * (2 j, 2 j + 1) when interleaved != 0; the rest is copied.  Queries go to
  * query_out, keys and values to their slots.
  *  query, key, value  device, dtype (f32 or bf16): head h of token i begins at
@@ -528,11 +528,14 @@ pa_status pa_rotary_turns(uint64_t *turns, float *attention_factor, int rotary_d
  * entries spread over 33 to 62 is dropped and flagged PA_DEV_BAD_SLOT, farther
  * ones of one block race.  Of two tokens with one slot in a block-scaled pool
  * the later one is stored, in other pools they race.
- * Arithmetic: f32, rounded once.  One kernel launch.
+ * Arithmetic: f32, rounded once.  A code is the nearest one to the f32 quotient of
+ * the exact turned key: elements next to a border of two codes are computed
+ * again in 64 bits.
+ * One kernel launch.
  */
 pa_status pa_rope_cache_write(void *query_out, const void *query, const void *key, const void *value,
                               const int32_t *positions, const uint64_t *turns,
-                              float attention_factor, int rotary_dim, int interleaved,
+                              double attention_factor, int rotary_dim, int interleaved,
                               void *key_cache, void *value_cache, float *k_scales, float *v_scales,
                               const int64_t *slot_mapping, int num_tokens, int num_q_heads,
                               int num_kv_heads, int head_dim, int64_t query_out_stride,

@@ -560,7 +560,7 @@ def rotary_plan(rotary_dim, base=10000.0, *, interleaved=False, scaling="none", 
         raise ValueError(f"scaling must be one of {sorted(_lib.PA_ROTARY_SCALINGS)}")
     rotary_dim = int(rotary_dim)
     host = torch.empty(max(rotary_dim, 0) // 2, dtype=torch.int64)
-    a = ctypes.c_float()
+    a = ctypes.c_double()
     buf = host.data_ptr() if host.numel() else ctypes.addressof(ctypes.c_uint64())
     rc = lib().pa_rotary_turns(buf, ctypes.addressof(a), rotary_dim, float(base), _lib.PA_ROTARY_SCALINGS[scaling],
                                float(factor), float(original_context), float(beta_fast), float(beta_slow))

@@ -58,7 +58,7 @@ SIGNATURES = {
     "pa_plan_step": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp,
                            vp]),
     "pa_rotary_turns": (i32, [vp, vp, i32, f64, i32, f64, f64, f64, f64]),
-    "pa_rope_cache_write": (i32, [vp, vp, vp, vp, vp, vp, f32, i32, i32, vp, vp, vp, vp, vp, i32, i32,
+    "pa_rope_cache_write": (i32, [vp, vp, vp, vp, vp, vp, f64, i32, i32, vp, vp, vp, vp, vp, i32, i32,
                                   i32, i32, i64, i64, i64, i64, i32, i32, i32, i32, vp, vp]),
     "pa_decode_block_fp8_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32, i32, i32]),
     "pa_decode_block_fp8": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32,

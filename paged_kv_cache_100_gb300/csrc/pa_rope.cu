@@ -19,12 +19,18 @@
 // the division of an element by it is exact, and a block whose scale grows when
 // a row is appended has its earlier rows re-encoded without error (apart from
 // codes that become subnormal).
+// A key's code is that of its exact rotation rounded to f32: an element whose
+// 32-bit value lies so near a border of two codes that its error could cross it
+// (about one in 10^5) is computed again in 64 bits, and so is the largest
+// magnitude when it lies next to a scale's border.
+//
+// The kernel moves bytes: a launch has CTAs that turn rows (queries; keys and
+// values too for float pools) and CTAs that encode blocks, the latter first.
 #include <cuda_runtime.h>
 #include <math.h>
 
-#include <cmath>
-
 #include <algorithm>
+#include <cmath>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -32,10 +38,17 @@
 namespace pa {
 namespace {
 
+constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
 constexpr int kWindow = 32;          // entries of slot_mapping among which a block's tokens lie
+constexpr int kMaxTile = 16;         // entries of slot_mapping whose blocks a CTA encodes
 constexpr int kMinExp = -32, kMaxExp = 31;
+// Error of a turned element in 32 bits, per |x0| + |x1|: the angle is held to
+// 2^-24 of half a turn (pi 2^-24), sincospi to 2 units of 2^-23, and three
+// roundings of 2^-24: below 2^-20.8; a multiplication by the inverse of a scale
+// that is no power of two adds 2^-23.
+constexpr float kTurnError = 7.2e-7f;            // 2^-20.4
 
 struct RopeArgs {
     const void *query, *key, *value;
@@ -47,13 +60,14 @@ struct RopeArgs {
     const int64_t *slot_mapping;
     int32_t *status;
     int64_t q_stride, k_stride, v_stride, q_out_stride;   // elements between tokens
-    float factor;
+    double factor;
     int num_tokens, num_q_heads, num_kv_heads, head_dim, rotary_dim;
     int interleaved;
     int num_blocks;
-    int tokens_per_cta;              // of the row CTAs
-    int row_ctas;                    // CTAs that turn rows; the rest take blocks
-    int tile_tokens;                 // tokens of a block CTA
+    int whole;                       // every unit of a row is a whole vector
+    int quick_tiles;                 // encode_quick's shapes (bf16 rows of 128, whole pairs in a lane)
+    int tile_ctas, tile_tokens;      // CTAs that encode blocks, and the entries each looks at
+    int row_tokens, row_splits;      // tokens of a row CTA; CTAs that share a token's rows
 };
 
 // cos and sin of position p's angle for one pair, times the attention factor
@@ -65,77 +79,103 @@ __device__ __forceinline__ float2 turn_of(int32_t p, uint64_t turns, float facto
     return make_float2(c * factor, s * factor);
 }
 
+// The same rotation in 64 bits: y0, or y1 when `second`.
+__device__ __noinline__ double exact_turn(float x0, float x1, bool second, int32_t p, uint64_t turns, double factor) {
+    double s, c;
+    sincospi((double)(int64_t)((uint64_t)(int64_t)p * turns) * 0x1p-63, &s, &c);
+    return (second ? fma((double)x1, c, (double)x0 * s) : fma((double)x0, c, -(double)x1 * s)) * factor;
+}
+
+// Code of y / scale, y in 64 bits: of the f32 quotient, as everywhere.
+__device__ __forceinline__ uint32_t exact_code(double y, float scale) {
+    return f32x2_to_e4m3x2((float)(y / (double)scale), 0.f) & 0xffu;
+}
+
 // N consecutive elements as floats; a vector access when `whole`
 template <typename T>
 struct Vec;
 template <>
 struct Vec<float> {
     static constexpr int N = 4;
-    static __device__ __forceinline__ void load(const float *p, bool whole, int n, float (&x)[4]) {
-        if (whole) {
-            const float4 v = *reinterpret_cast<const float4 *>(p);
-            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = i < n ? p[i] : 0.f;
-        }
+    static __device__ __forceinline__ void widen(const uint4 &v, float (&x)[4]) {
+        x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
     }
-    static __device__ __forceinline__ void store(float *p, bool whole, int n, const float (&x)[4]) {
-        if (whole) {
-            *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < n) p[i] = x[i];
-        }
+    static __device__ __forceinline__ uint4 narrow(const float (&x)[4]) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
     }
 };
 template <>
 struct Vec<__nv_bfloat16> {
     static constexpr int N = 8;
-    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool whole, int n, float (&x)[8]) {
-        if (whole) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(p);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    static __device__ __forceinline__ void widen(const uint4 &v, float (&x)[8]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[2 * i] = bf16lo(w[i]), x[2 * i + 1] = bf16hi(w[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = i < n ? __bfloat162float(p[i]) : 0.f;
-        }
+        for (int i = 0; i < 4; ++i) x[2 * i] = bf16lo(w[i]), x[2 * i + 1] = bf16hi(w[i]);
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16 *p, bool whole, int n, const float (&x)[8]) {
-        if (whole) {
-            *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                       pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < n) p[i] = __float2bfloat16_rn(x[i]);
-        }
+    static __device__ __forceinline__ uint4 narrow(const float (&x)[8]) {
+        return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                          pack_bf16x2(x[6], x[7]));
     }
 };
+template <typename T>
+__device__ __forceinline__ float to_float(T x) {
+    if constexpr (sizeof(T) == 4) return x;
+    else return __bfloat162float(x);
+}
+template <typename T>
+__device__ __forceinline__ T from_float(float x) {
+    if constexpr (sizeof(T) == 4) return x;
+    else return __float2bfloat16_rn(x);
+}
+template <typename T>
+__device__ __forceinline__ void load_vec(const T *p, bool whole, int n, float (&x)[Vec<T>::N]) {
+    if (whole) {
+        Vec<T>::widen(*reinterpret_cast<const uint4 *>(p), x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < Vec<T>::N; ++i) x[i] = i < n ? to_float(p[i]) : 0.f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_vec(T *p, bool whole, int n, const float (&x)[Vec<T>::N]) {
+    if (whole) {
+        *reinterpret_cast<uint4 *>(p) = Vec<T>::narrow(x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < Vec<T>::N; ++i)
+            if (i < n) p[i] = from_float<T>(x[i]);
+    }
+}
 
 // A row is cut into units that touch nothing of one another, so that rows may
-// be turned in place: `pair` units (N pairs of halves, or N / 2 neighbouring
-// pairs) and units of up to N elements behind rotary_dim.  Accesses are vectors
-// where the pieces begin on 16 bytes, else single elements.
+// be turned in place: pair units (N pairs of halves, or N / 2 neighbouring
+// pairs) and units of up to N elements behind rotary_dim.
 template <typename T>
-__device__ __forceinline__ void turn_unit(const T *src, T *dst, int unit, int pair_units, int dim, int rot,
+__device__ __forceinline__ int pair_units(const RopeArgs &a) {
+    constexpr int N = Vec<T>::N;
+    return a.interleaved ? (a.rotary_dim + N - 1) / N : (a.rotary_dim / 2 + N - 1) / N;
+}
+template <typename T>
+__device__ __forceinline__ int row_units(const RopeArgs &a) {
+    return pair_units<T>(a) + (a.head_dim - a.rotary_dim + Vec<T>::N - 1) / Vec<T>::N;
+}
+
+// One unit of a row of any shape; accesses are vectors where the pieces begin on
+// 16 bytes, else single elements.
+template <typename T>
+__device__ __forceinline__ void turn_unit(const T *src, T *dst, int unit, int pairs, int dim, int rot,
                                           bool interleaved, const float2 *table) {
     constexpr int N = Vec<T>::N;
-    if (unit >= pair_units) {
-        const int at = rot + (unit - pair_units) * N;
+    float x[N], y[N];
+    if (unit >= pairs) {
+        const int at = rot + (unit - pairs) * N;
         const int n = min(N, dim - at);
         const bool whole = n == N && at % N == 0;
-        float x[N];
-        Vec<T>::load(src + at, whole, n, x);
-        Vec<T>::store(dst + at, whole, n, x);
+        load_vec<T>(src + at, whole, n, x);
+        store_vec<T>(dst + at, whole, n, x);
     } else if (interleaved) {
-        const int at = unit * N;
-        const int n = min(N, rot - at);
-        float x[N];
-        Vec<T>::load(src + at, n == N, n, x);
+        const int at = unit * N, n = min(N, rot - at);
+        load_vec<T>(src + at, n == N, n, x);
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
             const float2 cs = i < n ? table[(at + i) >> 1] : make_float2(1.f, 0.f);
@@ -143,14 +183,13 @@ __device__ __forceinline__ void turn_unit(const T *src, T *dst, int unit, int pa
             x[i] = x0 * cs.x - x1 * cs.y;
             x[i + 1] = x1 * cs.x + x0 * cs.y;
         }
-        Vec<T>::store(dst + at, n == N, n, x);
+        store_vec<T>(dst + at, n == N, n, x);
     } else {
         const int half = rot / 2, at = unit * N;
         const int n = min(N, half - at);
         const bool whole = half % N == 0;
-        float x[N], y[N];
-        Vec<T>::load(src + at, whole, n, x);
-        Vec<T>::load(src + half + at, whole, n, y);
+        load_vec<T>(src + at, whole, n, x);
+        load_vec<T>(src + half + at, whole, n, y);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const float2 cs = i < n ? table[at + i] : make_float2(1.f, 0.f);
@@ -158,61 +197,139 @@ __device__ __forceinline__ void turn_unit(const T *src, T *dst, int unit, int pa
             x[i] = x0 * cs.x - x1 * cs.y;
             y[i] = x1 * cs.x + x0 * cs.y;
         }
-        Vec<T>::store(dst + at, whole, n, x);
-        Vec<T>::store(dst + half + at, whole, n, y);
+        store_vec<T>(dst + at, whole, n, x);
+        store_vec<T>(dst + half + at, whole, n, y);
     }
 }
 
-// Rows: queries to query_out and, with float pools, keys and values to their slots.
+// Where row `row` of token `tok` is read and written: queries, then keys, then
+// values (float pools).  False when the token has no slot.
 template <typename T>
-__device__ __forceinline__ void turn_rows(const RopeArgs &a, float2 *table, bool pools) {
+__device__ __forceinline__ bool row_at(const RopeArgs &a, int64_t tok, int row, const T **src, T **dst) {
+    const int D = a.head_dim;
+    if (row < a.num_q_heads) {
+        *src = static_cast<const T *>(a.query) + tok * a.q_stride + (int64_t)row * D;
+        *dst = static_cast<T *>(a.query_out) + tok * a.q_out_stride + (int64_t)row * D;
+        return true;
+    }
+    row -= a.num_q_heads;
+    const bool v = row >= a.num_kv_heads;
+    if (v) row -= a.num_kv_heads;
+    const int64_t slot = a.slot_mapping[tok];
+    if (slot < 0) return false;
+    if (slot >= (int64_t)a.num_blocks * kBlockSize) {
+        if (row == 0) report(a.status, PA_DEV_BAD_SLOT);
+        return false;
+    }
+    const int64_t blk = slot / kBlockSize, off = slot - blk * kBlockSize;
+    *src = static_cast<const T *>(v ? a.value : a.key) + tok * (v ? a.v_stride : a.k_stride) + (int64_t)row * D;
+    *dst = static_cast<T *>(v ? a.value_cache : a.key_cache) + ((blk * a.num_kv_heads + row) * kBlockSize + off) * D;
+    return true;
+}
+
+// Rows whose units are whole vectors.  A thread keeps one unit of the row and
+// the cos and sin of its pairs in registers while it goes through a token's
+// rows, two at a time; the loads of both are issued before either is turned.
+template <typename T, bool kInterleaved>
+__device__ __forceinline__ void turn_whole_rows(const RopeArgs &a, int64_t t0, int nt, int split, int rows,
+                                                const float2 *table) {
+    constexpr int N = Vec<T>::N, P = kInterleaved ? N / 2 : N;
+    const int half = a.rotary_dim / 2, pairs = pair_units<T>(a), units = row_units<T>(a);
+    const int per_pass = kRopeThreads / units;
+    const int unit = threadIdx.x % units, first = threadIdx.x / units;
+    if (first >= per_pass) return;
+    const bool pair = unit < pairs;
+    const int at = pair ? unit * N : a.rotary_dim + (unit - pairs) * N;
+    const int step = per_pass * a.row_splits;
+    for (int t = 0; t < nt; ++t) {
+        float2 cs[P];
+        if (pair) {
+            const float4 *c = reinterpret_cast<const float4 *>(table + t * half + unit * P);
+#pragma unroll
+            for (int i = 0; i < P; i += 2) {
+                const float4 v = c[i / 2];
+                cs[i] = make_float2(v.x, v.y);
+                cs[i + 1] = make_float2(v.z, v.w);
+            }
+        }
+        for (int r = first + split * per_pass; r < rows; r += 2 * step) {
+            const T *src[2];
+            T *dst[2];
+            bool on[2];
+            uint4 x[2], y[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                on[u] = r + u * step < rows && row_at<T>(a, t0 + t, r + u * step, &src[u], &dst[u]);
+                if (on[u]) {
+                    x[u] = *reinterpret_cast<const uint4 *>(src[u] + at);
+                    if (!kInterleaved && pair) y[u] = *reinterpret_cast<const uint4 *>(src[u] + at + half);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (!on[u]) continue;
+                // values are not turned
+                if (pair && r + u * step < a.num_q_heads + a.num_kv_heads) {
+                    float p[N], q[N];
+                    Vec<T>::widen(x[u], p);
+                    if constexpr (kInterleaved) {
+#pragma unroll
+                        for (int i = 0; i < N; i += 2) {
+                            q[i] = p[i] * cs[i / 2].x - p[i + 1] * cs[i / 2].y;
+                            q[i + 1] = p[i + 1] * cs[i / 2].x + p[i] * cs[i / 2].y;
+                        }
+                        x[u] = Vec<T>::narrow(q);
+                    } else {
+                        float s[N], o[N];
+                        Vec<T>::widen(y[u], q);
+#pragma unroll
+                        for (int i = 0; i < N; ++i) {
+                            s[i] = p[i] * cs[i].x - q[i] * cs[i].y;
+                            o[i] = q[i] * cs[i].x + p[i] * cs[i].y;
+                        }
+                        x[u] = Vec<T>::narrow(s);
+                        y[u] = Vec<T>::narrow(o);
+                    }
+                }
+                *reinterpret_cast<uint4 *>(dst[u] + at) = x[u];
+                if (!kInterleaved && pair) *reinterpret_cast<uint4 *>(dst[u] + at + half) = y[u];
+            }
+        }
+    }
+}
+
+// The rows of a CTA's tokens: queries to query_out and, with float pools, keys
+// and values to their slots.
+template <typename T>
+__device__ __forceinline__ void turn_rows(const RopeArgs &a, int cta, float2 *table, bool pools) {
     constexpr int N = Vec<T>::N;
     const int D = a.head_dim, rot = a.rotary_dim, half = rot / 2;
-    const int64_t t0 = (int64_t)blockIdx.x * a.tokens_per_cta;
-    const int nt = (int)min((int64_t)a.tokens_per_cta, a.num_tokens - t0);
+    const int group = cta / a.row_splits, split = cta - group * a.row_splits;
+    const int64_t t0 = (int64_t)group * a.row_tokens;
+    const int nt = (int)min((int64_t)a.row_tokens, a.num_tokens - t0);
     for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
         const int t = i / half;
-        table[i] = turn_of(a.positions[t0 + t], a.turns[i - t * half], a.factor);
+        table[i] = turn_of(a.positions[t0 + t], a.turns[i - t * half], (float)a.factor);
     }
     __syncthreads();
-    const int pair_units = a.interleaved ? (rot + N - 1) / N : (half + N - 1) / N;
-    const int units = pair_units + (D - rot + N - 1) / N;
-    const int copy_units = D / N;
-    const int q_items = a.num_q_heads * units;
-    const int k_items = pools ? a.num_kv_heads * units : 0;
-    const int v_items = pools ? a.num_kv_heads * copy_units : 0;
-    const int per_token = q_items + k_items + v_items;
-    for (int i = threadIdx.x; i < nt * per_token; i += kRopeThreads) {
-        const int t = i / per_token;
-        int item = i - t * per_token;
-        const int64_t tok = t0 + t;
-        if (item < q_items) {
-            const int h = item / units;
-            turn_unit<T>(static_cast<const T *>(a.query) + tok * a.q_stride + (int64_t)h * D,
-                         static_cast<T *>(a.query_out) + tok * a.q_out_stride + (int64_t)h * D, item - h * units,
-                         pair_units, D, rot, a.interleaved, table + t * half);
-            continue;
-        }
-        item -= q_items;
-        const int64_t slot = a.slot_mapping[tok];
-        if (slot < 0) continue;
-        if (slot >= (int64_t)a.num_blocks * kBlockSize) {
-            if (item == 0) report(a.status, PA_DEV_BAD_SLOT);
-            continue;
-        }
-        const int64_t blk = slot / kBlockSize, off = slot - blk * kBlockSize;
-        if (item < k_items) {
-            const int h = item / units;
-            turn_unit<T>(static_cast<const T *>(a.key) + tok * a.k_stride + (int64_t)h * D,
-                         static_cast<T *>(a.key_cache) + ((blk * a.num_kv_heads + h) * kBlockSize + off) * D,
-                         item - h * units, pair_units, D, rot, a.interleaved, table + t * half);
+    const int rows = a.num_q_heads + (pools ? 2 * a.num_kv_heads : 0);
+    if (a.whole) {
+        if (a.interleaved) turn_whole_rows<T, true>(a, t0, nt, split, rows, table);
+        else turn_whole_rows<T, false>(a, t0, nt, split, rows, table);
+        return;
+    }
+    const int pairs = pair_units<T>(a), units = row_units<T>(a);
+    const int turned = a.num_q_heads + a.num_kv_heads;
+    for (int i = split * kRopeThreads + threadIdx.x; i < nt * rows * units; i += kRopeThreads * a.row_splits) {
+        const int t = i / (rows * units), row = (i - t * rows * units) / units, unit = i % units;
+        const T *src;
+        T *dst;
+        if (!row_at<T>(a, t0 + t, row, &src, &dst)) continue;
+        if (row < turned) {
+            turn_unit<T>(src, dst, unit, pairs, D, rot, a.interleaved, table + t * half);
         } else {
-            item -= k_items;
-            const int h = item / copy_units, at = (item - h * copy_units) * N;
-            const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.value) + tok * a.v_stride +
-                                                             (int64_t)h * D + at);
-            *reinterpret_cast<uint4 *>(static_cast<T *>(a.value_cache) +
-                                       ((blk * a.num_kv_heads + h) * kBlockSize + off) * D + at) = v;
+            for (int at = unit * N; at < D; at += units * N)         // rows are whole 16-byte pieces
+                *reinterpret_cast<uint4 *>(dst + at) = *reinterpret_cast<const uint4 *>(src + at);
         }
     }
 }
@@ -226,206 +343,440 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 }
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// Blocks: a CTA takes the blocks whose first token of this call lies among its
-// tile_tokens entries; a warp takes one (block, KV head) of K or of V at a time,
-// stages its turned rows in shared memory, finds the scale and encodes.
-// Shared memory: cos and sin of tile_tokens + 31 tokens, then per warp 16 rows
-// of head_dim floats.
+// The block of one KV head that a warp encodes, K or V.
+struct Tile {
+    int64_t tok;                     // first token
+    int h, value;                    // KV head; 1: values
+    int lead;                        // tok's place in the CTA's table of cos and sin
+    int low, n;                      // lowest offset written; rows written
+    const uint16_t *list;            // their (entry - tok) | offset << 8
+    uint8_t *codes;
+    float *scale;
+};
 template <typename T>
-__device__ __forceinline__ void encode_blocks(const RopeArgs &a, float2 *table) {
+__device__ __forceinline__ const T *tile_row(const RopeArgs &a, const Tile &w, int j) {
+    return static_cast<const T *>(w.value ? a.value : a.key) + (w.tok + j) * (w.value ? a.v_stride : a.k_stride) +
+           (int64_t)w.h * a.head_dim;
+}
+
+// The pair of element d of a row: false when d is not turned.
+__device__ __forceinline__ bool pair_of(const RopeArgs &a, int d, int *first, int *second, int *pair) {
+    const int half = a.rotary_dim / 2;
+    if (d >= a.rotary_dim) return false;
+    *pair = a.interleaved ? d >> 1 : (d < half ? d : d - half);
+    *first = a.interleaved ? d & ~1 : *pair;
+    *second = a.interleaved ? d | 1 : *pair + half;
+    return true;
+}
+
+// Element d of the row of entry `tok + j` in 64 bits.
+template <typename T>
+__device__ __forceinline__ double exact_element(const RopeArgs &a, const Tile &w, int j, int d) {
+    const T *row = tile_row<T>(a, w, j);
+    int first, second, pair;
+    if (!pair_of(a, d, &first, &second, &pair)) return (double)to_float(row[d]);
+    return exact_turn(to_float(row[first]), to_float(row[second]), d == second, a.positions[w.tok + j], a.turns[pair], a.factor);
+}
+
+// Scale exponent of a tile of turned keys whose 32-bit maximum lies next to a
+// border: the elements near the maximum again in 64 bits.  A whole warp.
+template <typename T>
+__device__ __noinline__ int exact_exponent(const RopeArgs &a, const Tile &w, float amax, const float2 *table) {
+    const int half = a.rotary_dim / 2;
+    double top = 0.0;
+    for (int k = 0; k < w.n; ++k) {
+        const int j = w.list[k] & 0xff;
+        const T *row = tile_row<T>(a, w, j);
+        for (int d = threadIdx.x & 31; d < a.head_dim; d += 32) {
+            int first, second, pair;
+            float x = to_float(row[d]);
+            if (pair_of(a, d, &first, &second, &pair)) {
+                const float2 cs = table[(w.lead + j) * half + pair];
+                const float x0 = to_float(row[first]), x1 = to_float(row[second]);
+                x = d == second ? x1 * cs.x + x0 * cs.y : x0 * cs.x - x1 * cs.y;
+            }
+            if (fabsf(x) >= amax * (1.f - 0x1p-17f)) top = fmax(top, fabs(exact_element<T>(a, w, j, d)));
+        }
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top = fmax(top, __shfl_xor_sync(kAll, top, o));
+    int e = scale_exponent(amax * (1.f - 0x1p-18f));
+    return top <= 448.0 * (double)pow2i(e) ? e : min(e + 1, kMaxExp);
+}
+
+// The tile's scale from the maximum of the rows written: at least the old one
+// where earlier rows stay, which are then re-encoded if it grew.
+template <typename T>
+__device__ __forceinline__ float tile_scale(const RopeArgs &a, const Tile &w, float amax, float old, const float2 *table) {
+    const int lane = threadIdx.x & 31, D = a.head_dim;
+    if (amax > 448.f * pow2i(kMaxExp) && lane == 0) report(a.status, PA_DEV_RANGE);
+    int e = scale_exponent(amax);
+    if (!w.value && a.rotary_dim > 0 &&
+        scale_exponent(amax * (1.f - 0x1p-18f)) != scale_exponent(amax * (1.f + 0x1p-18f)))
+        e = exact_exponent<T>(a, w, amax, table);
+    const float scale = fmaxf(pow2i(e), old);
+    if (w.low > 0 && scale != old) {
+        const float f = old / scale;
+        for (int i = lane * 4; i < w.low * D; i += 128) {
+            uint32_t *p = reinterpret_cast<uint32_t *>(w.codes + i);
+            uint32_t lo, hi;
+            e4m3x4_to_f16x2x2(*p, lo, hi);
+            *p = f32x2_to_e4m3x2(f16lo(lo) * f, f16hi(lo) * f) | (f32x2_to_e4m3x2(f16lo(hi) * f, f16hi(hi) * f) << 16);
+        }
+    }
+    if (lane == 0) *w.scale = scale;
+    return scale;
+}
+__device__ __forceinline__ bool is_pow2(float x) { return (__float_as_uint(x) & 0x7fffffu) == 0; }
+
+// Encodes a tile of bf16 rows of 128: half a warp holds a row, a lane 8 of its
+// elements (kMode 1: 4 l .. and their partners 64 + 4 l ..; else 8 l ..).  The
+// rows are turned once for the maximum and, read again from L1, once more for
+// the codes.  kMode 0: not turned; 1: halves; 2: neighbours.
+template <int kMode>
+__device__ __forceinline__ void encode_quick(const RopeArgs &a, const Tile &w, float old, const float2 *table) {
+    const int lane = threadIdx.x & 31, hl = lane & 15, side = lane >> 4;
+    const int half = a.rotary_dim / 2;
+    const bool turned = kMode == 1 || (kMode == 2 && 8 * hl < a.rotary_dim);
+    auto load = [&](int i) {
+        uint4 r = make_uint4(0u, 0u, 0u, 0u);
+        if (2 * i + side < w.n) {
+            const __nv_bfloat16 *row = tile_row<__nv_bfloat16>(a, w, w.list[2 * i + side] & 0xff);
+            if constexpr (kMode == 1) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(row + 4 * hl);
+                const uint2 y = *reinterpret_cast<const uint2 *>(row + 64 + 4 * hl);
+                r = make_uint4(x.x, x.y, y.x, y.y);
+            } else {
+                r = *reinterpret_cast<const uint4 *>(row + 8 * hl);
+            }
+        }
+        return r;
+    };
+    // the lane's pairs of row i: x0[k], x1[k] and their cos and sin
+    auto pairs = [&](int i, const uint4 &raw, float (&x0)[4], float (&x1)[4], float4 (&cs)[2]) {
+        const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (kMode == 1) {
+                x0[k] = k & 1 ? bf16hi(r[k >> 1]) : bf16lo(r[k >> 1]);
+                x1[k] = k & 1 ? bf16hi(r[2 + (k >> 1)]) : bf16lo(r[2 + (k >> 1)]);
+            } else {
+                x0[k] = bf16lo(r[k]);
+                x1[k] = bf16hi(r[k]);
+            }
+        }
+        if (turned) {
+            const int j = 2 * i + side < w.n ? w.list[2 * i + side] & 0xff : 0;
+            const float4 *c = reinterpret_cast<const float4 *>(table + (w.lead + j) * half + 4 * hl);
+            cs[0] = c[0];
+            cs[1] = c[1];
+        } else {
+            cs[0] = cs[1] = make_float4(1.f, 0.f, 1.f, 0.f);
+        }
+    };
+    float amax = 0.f;                                // fmaxf passes over NaN
+#pragma unroll 1
+    for (int b = 0; 2 * b < w.n; b += 4) {
+        uint4 raw[4];                                // eight rows on their way
+#pragma unroll
+        for (int i = 0; i < 4; ++i) raw[i] = load(b + i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (2 * (b + i) >= w.n) break;
+            float x0[4], x1[4];
+            float4 cs[2];
+            pairs(b + i, raw[i], x0, x1, cs);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float c = k & 1 ? cs[k >> 1].z : cs[k >> 1].x, s = k & 1 ? cs[k >> 1].w : cs[k >> 1].y;
+                if constexpr (kMode == 0) amax = fmaxf(amax, fmaxf(fabsf(x0[k]), fabsf(x1[k])));
+                else amax = fmaxf(amax, fmaxf(fabsf(x0[k] * c - x1[k] * s), fabsf(x1[k] * c + x0[k] * s)));
+            }
+        }
+    }
+    amax = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(amax)));
+    const float scale = tile_scale<__nv_bfloat16>(a, w, amax, old, table);
+    const float inv = 1.f / scale;
+    const bool exact = is_pow2(scale);
+    uint4 ahead = load(0);
+#pragma unroll 1
+    for (int i = 0; 2 * i < w.n; ++i) {
+        const uint4 raw = ahead;
+        ahead = load(i + 1);
+        float x0[4], x1[4];
+        float4 cs[2];
+        pairs(i, raw, x0, x1, cs);
+        uint32_t out[2];                             // codes of x0 and of x1 (mode 1), else in order
+        if constexpr (kMode == 0) {
+            if (!exact) {                            // a scale that someone else chose is divided by
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x0[k] = __fdiv_rn(x0[k], scale), x1[k] = __fdiv_rn(x1[k], scale);
+            }
+            const float m = exact ? inv : 1.f;
+            out[0] = f32x2_to_e4m3x2(x0[0] * m, x1[0] * m) | (f32x2_to_e4m3x2(x0[1] * m, x1[1] * m) << 16);
+            out[1] = f32x2_to_e4m3x2(x0[2] * m, x1[2] * m) | (f32x2_to_e4m3x2(x0[3] * m, x1[3] * m) << 16);
+        } else {
+            // the codes of the value less and more its error: where they differ the
+            // pair's codes come from 64 bits
+            float y0[4], y1[4], err[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float c = k & 1 ? cs[k >> 1].z : cs[k >> 1].x, s = k & 1 ? cs[k >> 1].w : cs[k >> 1].y;
+                y0[k] = (x0[k] * c - x1[k] * s) * inv;
+                y1[k] = (x1[k] * c + x0[k] * s) * inv;
+                err[k] = (fabsf(x0[k]) + fabsf(x1[k])) * (kTurnError * (float)a.factor * inv);
+                if (!turned) {
+                    err[k] = 0.f;
+                    if (!exact) y0[k] = __fdiv_rn(x0[k], scale), y1[k] = __fdiv_rn(x1[k], scale);
+                }
+            }
+            uint32_t lo[2], hi[2];
+            auto code4 = [&](float p, float q, float r, float t) {
+                return f32x2_to_e4m3x2(p, q) | (f32x2_to_e4m3x2(r, t) << 16);
+            };
+            if constexpr (kMode == 1) {
+                lo[0] = code4(y0[0] - err[0], y0[1] - err[1], y0[2] - err[2], y0[3] - err[3]);
+                hi[0] = code4(y0[0] + err[0], y0[1] + err[1], y0[2] + err[2], y0[3] + err[3]);
+                lo[1] = code4(y1[0] - err[0], y1[1] - err[1], y1[2] - err[2], y1[3] - err[3]);
+                hi[1] = code4(y1[0] + err[0], y1[1] + err[1], y1[2] + err[2], y1[3] + err[3]);
+            } else {
+                lo[0] = code4(y0[0] - err[0], y1[0] - err[0], y0[1] - err[1], y1[1] - err[1]);
+                hi[0] = code4(y0[0] + err[0], y1[0] + err[0], y0[1] + err[1], y1[1] + err[1]);
+                lo[1] = code4(y0[2] - err[2], y1[2] - err[2], y0[3] - err[3], y1[3] - err[3]);
+                hi[1] = code4(y0[2] + err[2], y1[2] + err[2], y0[3] + err[3], y1[3] + err[3]);
+            }
+            out[0] = lo[0];
+            out[1] = lo[1];
+            if (((lo[0] ^ hi[0]) | (lo[1] ^ hi[1])) != 0 && 2 * i + side < w.n) {
+                const int j = w.list[2 * i + side] & 0xff;
+#pragma unroll 1
+                for (int b = 0; b < 8; ++b) {
+                    if ((((lo[b >> 2] ^ hi[b >> 2]) >> (8 * (b & 3))) & 0xffu) == 0) continue;
+                    const int d = kMode == 1 ? (b >> 2) * 64 + 4 * hl + (b & 3) : 8 * hl + b;
+                    const uint32_t c = exact_code(exact_element<__nv_bfloat16>(a, w, j, d), scale);
+                    const uint32_t mask = 0xffu << (8 * (b & 3));
+                    if (b < 4) out[0] = (out[0] & ~mask) | (c << (8 * (b & 3)));
+                    else out[1] = (out[1] & ~mask) | (c << (8 * (b & 3)));
+                }
+            }
+        }
+        if (2 * i + side < w.n) {
+            uint8_t *row = w.codes + (w.list[2 * i + side] >> 8) * 128;
+            if constexpr (kMode == 1) {
+                *reinterpret_cast<uint32_t *>(row + 4 * hl) = out[0];
+                *reinterpret_cast<uint32_t *>(row + 64 + 4 * hl) = out[1];
+            } else {
+                *reinterpret_cast<uint2 *>(row + 8 * hl) = make_uint2(out[0], out[1]);
+            }
+        }
+    }
+}
+
+// Encodes a tile of any shape: the turned rows pass through shared memory.  The
+// error of an element is bounded by that of the largest one.
+template <typename T>
+__device__ __forceinline__ void encode_any(const RopeArgs &a, const Tile &w, float old, const float2 *table, float *rows) {
     constexpr int N = Vec<T>::N;
-    const int D = a.head_dim, rot = a.rotary_dim, half = rot / 2;
+    const int lane = threadIdx.x & 31, D = a.head_dim, rot = w.value ? 0 : a.rotary_dim, half = rot / 2;
+    for (int k = 0; k < w.n; ++k) {
+        const int j = w.list[k] & 0xff;
+        const T *src = tile_row<T>(a, w, j);
+        const float2 *cs = table + (w.lead + j) * half;
+        float *row = rows + k * D;
+        for (int at = lane * N; at < D; at += 32 * N) {
+            float x[N];
+            load_vec<T>(src + at, true, N, x);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int d = at + i;
+                int first, second, pair;
+                if (!w.value && pair_of(a, d, &first, &second, &pair)) {
+                    const float other = to_float(src[d == second ? first : second]);
+                    const float2 c = cs[pair];
+                    row[d] = d == second ? x[i] * c.x + other * c.y : x[i] * c.x - other * c.y;
+                } else {
+                    row[d] = x[i];
+                }
+            }
+        }
+    }
+    __syncwarp();
+    float amax = 0.f;
+    for (int i = lane * 4; i < w.n * D; i += 128) {
+        const float4 x = *reinterpret_cast<const float4 *>(rows + i);
+        amax = fmaxf(fmaxf(fmaxf(amax, fabsf(x.x)), fmaxf(fabsf(x.y), fabsf(x.z))), fabsf(x.w));
+    }
+    amax = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(amax)));
+    const float scale = tile_scale<T>(a, w, amax, old, table);
+    const float inv = 1.f / scale;
+    const bool exact = is_pow2(scale);
+    // |x0| + |x1| of a pair is at most twice the larger of its turned elements
+    const float err = rot > 0 ? 2.f * amax * (kTurnError * inv) : 0.f;
+    for (int k = 0; k < w.n; ++k) {
+        const int j = w.list[k] & 0xff;
+        for (int c = lane * 4; c < D; c += 128) {
+            const float4 x = *reinterpret_cast<const float4 *>(rows + k * D + c);
+            float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = exact || c + i < rot ? y[i] * inv : __fdiv_rn(y[i], scale);
+            uint32_t lo = 0, hi = 0;
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+                const float e0 = c + i < rot ? err : 0.f, e1 = c + i + 1 < rot ? err : 0.f;
+                lo |= f32x2_to_e4m3x2(y[i] - e0, y[i + 1] - e1) << (8 * i);
+                hi |= f32x2_to_e4m3x2(y[i] + e0, y[i + 1] + e1) << (8 * i);
+            }
+            if (lo != hi) {
+                const uint32_t was = lo ^ hi;
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i)
+                    if ((was >> (8 * i)) & 0xffu)
+                        lo = (lo & ~(0xffu << (8 * i))) | (exact_code(exact_element<T>(a, w, j, c + i), scale) << (8 * i));
+            }
+            *reinterpret_cast<uint32_t *>(w.codes + (w.list[k] >> 8) * D + c) = lo;
+        }
+    }
+    __syncwarp();                                    // the rows are read
+}
+
+// Blocks: a CTA takes the blocks whose first token of this call lies among its
+// tile_tokens entries; a warp takes one (block, KV head) of K or of V at a time.
+// Shared memory: cos and sin of tile_tokens + 31 tokens, then (encode_any) per
+// warp 16 rows of head_dim floats.
+template <typename T>
+__device__ __forceinline__ void encode_blocks(const RopeArgs &a, int cta, float2 *table) {
+    const int half = a.rotary_dim / 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t t0 = (int64_t)(blockIdx.x - a.row_ctas) * a.tile_tokens;
+    const int64_t t0 = (int64_t)cta * a.tile_tokens;
     const int nt = (int)min((int64_t)a.tile_tokens, a.num_tokens - t0);
-    const int reach = (int)min((int64_t)nt + kWindow - 1, a.num_tokens - t0);
-    float *rows = reinterpret_cast<float *>(table + (a.tile_tokens + kWindow - 1) * half) + warp * kBlockSize * D;
     const int64_t limit = (int64_t)a.num_blocks * kBlockSize;
-    const int pair_units = a.interleaved ? (rot + N - 1) / N : (half + N - 1) / N;
-    const int units = pair_units + (D - rot + N - 1) / N;
 
     // the leaders (a block's first token: none of the kWindow - 1 entries before
-    // has the same block) and how many tokens of the reach belong to them
-    __shared__ int s_lead[kWindow], s_count, s_last;
+    // has the same block), and their blocks' rows
+    __shared__ int s_lead[kMaxTile], s_low[kMaxTile], s_n[kMaxTile], s_count, s_last;
+    __shared__ int64_t s_blk[kMaxTile];
+    __shared__ uint16_t s_list[kMaxTile][kBlockSize];
     if (threadIdx.x == 0) s_count = s_last = 0;
     __syncthreads();
     for (int i = warp; i < nt; i += kRopeWarps) {
         const int64_t tok = t0 + i;
-        const int64_t slot = a.slot_mapping[tok];
-        if (slot >= limit && lane == 0) report(a.status, PA_DEV_BAD_SLOT);
-        if (slot < 0 || slot >= limit) continue;
-        const int64_t blk = slot / kBlockSize, prev = tok - 1 - lane, far = prev - (kWindow - 1), next = tok + lane;
+        const int64_t prev = tok - 1 - lane, far = prev - (kWindow - 1), next = tok + lane;
         const int64_t sp = lane < kWindow - 1 && prev >= 0 ? a.slot_mapping[prev] : -1;
         const int64_t sf = lane < kWindow - 1 && far >= 0 ? a.slot_mapping[far] : -1;
         const int64_t sn = next < a.num_tokens ? a.slot_mapping[next] : -1;
-        const unsigned mine = __ballot_sync(0xffffffffu, sn >= 0 && sn / kBlockSize == blk);
+        const int64_t slot = __shfl_sync(kAll, sn, 0);
+        if (slot >= limit && lane == 0) report(a.status, PA_DEV_BAD_SLOT);
+        if (slot < 0 || slot >= limit) continue;
+        const int64_t blk = slot / kBlockSize;
         // the block's tokens spread over more than kWindow entries: this one is
         // out of its leader's reach, or would lead a second time
-        if (__any_sync(0xffffffffu, sf >= 0 && sf / kBlockSize == blk)) {
+        if (__any_sync(kAll, sf >= 0 && sf / kBlockSize == blk)) {
             if (lane == 0) report(a.status, PA_DEV_BAD_SLOT);
             continue;
         }
-        if (__any_sync(0xffffffffu, sp >= 0 && sp / kBlockSize == blk)) continue;
+        if (__any_sync(kAll, sp >= 0 && sp / kBlockSize == blk)) continue;
+        // rows: of two tokens with one slot the later one
+        const bool mine = sn >= 0 && sn / kBlockSize == blk;
+        const int off = mine ? (int)(sn % kBlockSize) : kBlockSize + lane;
+        const unsigned same = __match_any_sync(kAll, off);
+        const bool kept = mine && lane == 31 - __clz((int)same);
+        const unsigned rows = __ballot_sync(kAll, kept);
+        const int low = __reduce_min_sync(kAll, off);
+        int place = 0;
         if (lane == 0) {
-            s_lead[atomicAdd(&s_count, 1)] = i;
-            atomicMax(&s_last, i + 31 - __clz((int)mine));
+            place = atomicAdd(&s_count, 1);
+            atomicMax(&s_last, i + 31 - __clz((int)rows));
+            s_lead[place] = i;
+            s_low[place] = low;
+            s_n[place] = __popc(rows);
+            s_blk[place] = blk;
         }
+        place = __shfl_sync(kAll, place, 0);
+        if (kept) s_list[place][__popc(rows & ((1u << lane) - 1u))] = (uint16_t)(lane | (off << 8));
     }
     __syncthreads();
     const int leads = s_count;
     if (leads == 0) return;
-    for (int i = threadIdx.x; i < (min(s_last, reach - 1) + 1) * half; i += kRopeThreads) {
+    for (int i = threadIdx.x; i < (s_last + 1) * half; i += kRopeThreads) {
         const int t = i / half;
-        table[i] = turn_of(a.positions[t0 + t], a.turns[i - t * half], a.factor);
+        table[i] = turn_of(a.positions[t0 + t], a.turns[i - t * half], (float)a.factor);
     }
     __syncthreads();
 
-    for (int item = warp; item < leads * a.num_kv_heads * 2; item += kRopeWarps) {
-        const int which = item & 1, h = (item >> 1) % a.num_kv_heads, lead = s_lead[(item >> 1) / a.num_kv_heads];
-        const int64_t tok = t0 + lead;
-        const int64_t blk = a.slot_mapping[tok] / kBlockSize;
-        const int64_t mine_slot = tok + lane < a.num_tokens ? a.slot_mapping[tok + lane] : -1;
-        const bool is_mine = mine_slot >= 0 && mine_slot / kBlockSize == blk;
-        const unsigned members = __ballot_sync(0xffffffffu, is_mine);
-        const int off = is_mine ? (int)(mine_slot % kBlockSize) : kBlockSize;
-        const int low = __reduce_min_sync(0xffffffffu, off);
-        const unsigned put = __reduce_or_sync(0xffffffffu, is_mine ? 1u << off : 0u);   // offsets written
-        uint8_t *tile = static_cast<uint8_t *>(which ? a.value_cache : a.key_cache) +
-                        (blk * a.num_kv_heads + h) * kBlockSize * (int64_t)D;
-        float *scale_at = (which ? a.v_scales : a.k_scales) + blk * a.num_kv_heads + h;
-        const float old = low > 0 ? *scale_at : 0.f;
-        // turned rows; a slot that is listed twice keeps the later token
-        for (unsigned m = members; m != 0; m &= m - 1) {
-            const int j = __ffs((int)m) - 1;
-            float *row = rows + __shfl_sync(0xffffffffu, off, j) * D;
-            const T *src = static_cast<const T *>(which ? a.value : a.key) +
-                           (tok + j) * (which ? a.v_stride : a.k_stride) + (int64_t)h * D;
-            if (which) {
-                for (int at = lane * N; at < D; at += 32 * N) {
-                    float x[N];
-                    Vec<T>::load(src + at, true, N, x);
-#pragma unroll
-                    for (int i = 0; i < N; ++i) row[at + i] = x[i];
-                }
-            } else {
-                const float2 *cs = table + (lead + j) * half;
-                for (int u = lane; u < units; u += 32) {
-                    float x[N], y[N];
-                    if (u >= pair_units) {
-                        const int at = rot + (u - pair_units) * N, n = min(N, D - at);
-                        Vec<T>::load(src + at, n == N && at % N == 0, n, x);
-#pragma unroll
-                        for (int i = 0; i < N; ++i)
-                            if (i < n) row[at + i] = x[i];
-                    } else if (a.interleaved) {
-                        const int at = u * N, n = min(N, rot - at);
-                        Vec<T>::load(src + at, n == N, n, x);
-#pragma unroll
-                        for (int i = 0; i < N; i += 2)
-                            if (i < n) {
-                                const float2 c = cs[(at + i) >> 1];
-                                row[at + i] = x[i] * c.x - x[i + 1] * c.y;
-                                row[at + i + 1] = x[i + 1] * c.x + x[i] * c.y;
-                            }
-                    } else {
-                        const int at = u * N, n = min(N, half - at);
-                        const bool whole = half % N == 0;
-                        Vec<T>::load(src + at, whole, n, x);
-                        Vec<T>::load(src + half + at, whole, n, y);
-#pragma unroll
-                        for (int i = 0; i < N; ++i)
-                            if (i < n) {
-                                const float2 c = cs[at + i];
-                                row[at + i] = x[i] * c.x - y[i] * c.y;
-                                row[half + at + i] = y[i] * c.x + x[i] * c.y;
-                            }
-                    }
-                }
-            }
-            __syncwarp();
-        }
-        float amax = 0.f;                            // fmaxf passes over NaN
-        for (unsigned m = put; m != 0; m &= m - 1) {
-            const float *row = rows + (__ffs((int)m) - 1) * D;
-            for (int c = lane * 4; c < D; c += 128) {
-                const float4 x = *reinterpret_cast<const float4 *>(row + c);
-                amax = fmaxf(fmaxf(fmaxf(amax, fabsf(x.x)), fmaxf(fabsf(x.y), fabsf(x.z))), fabsf(x.w));
+    float *rows = reinterpret_cast<float *>(table + (a.tile_tokens + kWindow - 1) * half) + warp * kBlockSize * a.head_dim;
+    const int per_lead = 2 * a.num_kv_heads;
+    for (int item = warp; item < leads * per_lead; item += kRopeWarps) {
+        const int at = item / per_lead, rest = item - at * per_lead;
+        Tile w;
+        w.value = rest >= a.num_kv_heads;
+        w.h = w.value ? rest - a.num_kv_heads : rest;
+        w.lead = s_lead[at];
+        w.tok = t0 + w.lead;
+        w.low = s_low[at];
+        w.n = s_n[at];
+        w.list = s_list[at];
+        const int64_t place = s_blk[at] * a.num_kv_heads + w.h;
+        w.codes = static_cast<uint8_t *>(w.value ? a.value_cache : a.key_cache) + place * kBlockSize * a.head_dim;
+        w.scale = (w.value ? a.v_scales : a.k_scales) + place;
+        const float old = w.low > 0 ? *w.scale : 0.f;
+        if constexpr (sizeof(T) == 2) {
+            if (a.quick_tiles) {
+                if (w.value || half == 0) encode_quick<0>(a, w, old, table);
+                else if (a.interleaved) encode_quick<2>(a, w, old, table);
+                else encode_quick<1>(a, w, old, table);
+                continue;
             }
         }
-        amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-        if (amax > 448.f * pow2i(kMaxExp) && lane == 0) report(a.status, PA_DEV_RANGE);
-        const float scale = fmaxf(pow2i(scale_exponent(amax)), old);
-        // dividing by a power of two is multiplying by its inverse; a scale that
-        // someone else chose is divided by
-        const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0;
-        const float inv = 1.f / scale;
-        if (low > 0 && scale != old) {
-            const float f = old / scale;
-            for (int r = 0; r < low; ++r)
-                for (int c = lane * 4; c < D; c += 128) {
-                    uint32_t *p = reinterpret_cast<uint32_t *>(tile + r * D + c);
-                    uint32_t lo, hi;
-                    e4m3x4_to_f16x2x2(*p, lo, hi);
-                    *p = f32x2_to_e4m3x2(f16lo(lo) * f, f16hi(lo) * f) |
-                         (f32x2_to_e4m3x2(f16lo(hi) * f, f16hi(hi) * f) << 16);
-                }
-        }
-        for (unsigned m = put; m != 0; m &= m - 1) {
-            const int r = __ffs((int)m) - 1;
-            for (int c = lane * 4; c < D; c += 128) {
-                float4 x = *reinterpret_cast<const float4 *>(rows + r * D + c);
-                if (pow2)
-                    x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-                else
-                    x = make_float4(__fdiv_rn(x.x, scale), __fdiv_rn(x.y, scale), __fdiv_rn(x.z, scale),
-                                    __fdiv_rn(x.w, scale));
-                *reinterpret_cast<uint32_t *>(tile + r * D + c) =
-                    f32x2_to_e4m3x2(x.x, x.y) | (f32x2_to_e4m3x2(x.z, x.w) << 16);
-            }
-        }
-        if (lane == 0) *scale_at = scale;
-        __syncwarp();                                // the rows are read
+        encode_any<T>(a, w, old, table, rows);
     }
 }
 
 template <typename T, bool kBlocks>
-__global__ void __launch_bounds__(kRopeThreads) pa_rope_write_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 4) pa_rope_write_kernel(const RopeArgs a) {
     extern __shared__ __align__(16) float2 s_table[];
     grid_dependency_wait();
     grid_dependents_launch();
     if constexpr (kBlocks) {
-        if ((int)blockIdx.x >= a.row_ctas) {
-            encode_blocks<T>(a, s_table);
+        if ((int)blockIdx.x < a.tile_ctas) {
+            encode_blocks<T>(a, blockIdx.x, s_table);
             return;
         }
     }
-    turn_rows<T>(a, s_table, !kBlocks);
+    turn_rows<T>(a, blockIdx.x - a.tile_ctas, s_table, !kBlocks);
 }
 
-// Frequencies for rotary positions; see the header.
 double ramp_index(double turns, double dim, double base, double context) {
     return dim * log(context / (turns * 2.0 * M_PI)) / (2.0 * log(base));
 }
 
 template <typename T>
 pa_status launch_rope(RopeArgs &a, bool blocks, cudaStream_t stream) {
-    const int half = a.rotary_dim / 2;
-    // enough CTAs to fill the GPU, and tokens together where there are many
-    // (their cos and sin are computed side by side)
-    int tpc = 1;
-    while (tpc < 16 && a.num_tokens / (2 * tpc) >= 4 * 152) tpc *= 2;
-    a.tokens_per_cta = tpc;
-    const int64_t rows = a.num_q_heads > 0 || !blocks ? ((int64_t)a.num_tokens + tpc - 1) / tpc : 0;
-    int64_t grid = rows;
-    size_t smem = (size_t)tpc * half * sizeof(float2);
+    constexpr int N = 16 / (int)sizeof(T);
+    const int D = a.head_dim, rot = a.rotary_dim, half = rot / 2;
+    a.whole = a.interleaved ? rot % N == 0 : half % N == 0;
+    a.quick_tiles = blocks && sizeof(T) == 2 && D == 128 &&
+                    (rot == 0 || (a.interleaved ? rot % 8 == 0 : rot == 128));
+    const int rows = a.num_q_heads + (blocks ? 0 : 2 * a.num_kv_heads);
+    // tokens share a CTA where there are enough for four CTAs per SM; where there
+    // are fewer than SMs, CTAs share a token's rows
+    const int64_t n = a.num_tokens;
+    a.row_tokens = 1;
+    while (a.row_tokens < 8 && n / (2 * a.row_tokens) >= 4 * 152) a.row_tokens *= 2;
+    const int units = (a.interleaved ? (rot + N - 1) / N : (half + N - 1) / N) + (D - rot + N - 1) / N;
+    const int passes = (rows + kRopeThreads / units - 1) / (kRopeThreads / units);
+    a.row_splits = (int)std::max<int64_t>(1, std::min<int64_t>(passes, 2 * 152 / n));
+    a.tile_tokens = 1;
+    while (a.tile_tokens < kMaxTile && n / (2 * a.tile_tokens) >= 2 * 152) a.tile_tokens *= 2;
+    int64_t grid = rows > 0 ? (n + a.row_tokens - 1) / a.row_tokens * a.row_splits : 0;
+    size_t smem = (size_t)a.row_tokens * half * sizeof(float2);
+    a.tile_ctas = 0;
     if (blocks) {
-        a.tile_tokens = tpc;
-        grid += ((int64_t)a.num_tokens + a.tile_tokens - 1) / a.tile_tokens;
+        a.tile_ctas = (int)((n + a.tile_tokens - 1) / a.tile_tokens);
+        grid += a.tile_ctas;
         smem = std::max(smem, (size_t)(a.tile_tokens + kWindow - 1) * half * sizeof(float2) +
-                                  (size_t)kRopeWarps * kBlockSize * a.head_dim * sizeof(float));
+                                  (a.quick_tiles ? 0 : (size_t)kRopeWarps * kBlockSize * D * sizeof(float)));
     }
     if (grid >= ((int64_t)1 << 31)) return PA_ERR_UNSUPPORTED;
-    a.row_ctas = (int)rows;
     auto kernel = blocks ? pa_rope_write_kernel<T, true> : pa_rope_write_kernel<T, false>;
     if (smem > 48 * 1024) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -442,7 +793,7 @@ pa_status launch_rope(RopeArgs &a, bool blocks, cudaStream_t stream) {
 
 using namespace pa;
 
-extern "C" pa_status pa_rotary_turns(uint64_t *turns, float *attention_factor, int rotary_dim, double base,
+extern "C" pa_status pa_rotary_turns(uint64_t *turns, double *attention_factor, int rotary_dim, double base,
                                      pa_rotary_scaling scaling, double factor, double original_context,
                                      double beta_fast, double beta_slow) {
     if (!turns || !attention_factor || rotary_dim < 0 || rotary_dim % 2 != 0 || !(base > 1.0) || !(factor > 0.0) ||
@@ -473,12 +824,12 @@ extern "C" pa_status pa_rotary_turns(uint64_t *turns, float *attention_factor, i
         const double frac = t - floor(t);
         turns[i] = frac >= 1.0 ? 0 : (uint64_t)ldexp(frac, 64);
     }
-    *attention_factor = scaling == PA_ROTARY_BY_PARTS && factor > 1.0 ? (float)(0.1 * log(factor) + 1.0) : 1.f;
+    *attention_factor = scaling == PA_ROTARY_BY_PARTS && factor > 1.0 ? 0.1 * log(factor) + 1.0 : 1.0;
     return PA_OK;
 }
 
 extern "C" pa_status pa_rope_cache_write(void *query_out, const void *query, const void *key, const void *value,
-                                         const int32_t *positions, const uint64_t *turns, float attention_factor,
+                                         const int32_t *positions, const uint64_t *turns, double attention_factor,
                                          int rotary_dim, int interleaved, void *key_cache, void *value_cache,
                                          float *k_scales, float *v_scales, const int64_t *slot_mapping,
                                          int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
@@ -487,7 +838,7 @@ extern "C" pa_status pa_rope_cache_write(void *query_out, const void *query, con
                                          pa_dtype cache_dtype, int32_t *device_status, void *stream) {
     if (num_tokens < 0 || num_q_heads < 0 || num_kv_heads <= 0 || head_dim <= 0 || rotary_dim < 0 ||
         rotary_dim > head_dim || rotary_dim % 2 != 0 || block_size != kBlockSize || num_blocks <= 0 ||
-        !std::isfinite(attention_factor))
+        !(attention_factor >= 0x1p-20 && attention_factor <= 0x1p20))
         return PA_ERR_INVALID_ARG;
     if (dtype != PA_DTYPE_F32 && dtype != PA_DTYPE_BF16) return PA_ERR_INVALID_ARG;
     if (cache_dtype != dtype && cache_dtype != PA_DTYPE_FP8_E4M3) return PA_ERR_INVALID_ARG;
