@@ -18,7 +18,6 @@ slot_mapping int64 [num_tokens]; copy pairs int32 [num_pairs][2].
 from __future__ import annotations
 
 import collections
-import contextlib
 import ctypes
 import math
 
@@ -453,41 +452,9 @@ def prefill(query, key_cache, value_cache, block_tables, context_lens, query_sta
     return out
 
 
-def _same_device(first, **others):
-    """The CUDA device index of ``first``; every other tensor must be on it."""
-    if not first.is_cuda:
-        raise ValueError("tensors must be CUDA tensors")
-    dev = first.get_device()
-    for name, t in others.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} must be a CUDA tensor on device {dev}")
-    return dev
-
-
-@contextlib.contextmanager
-def _elsewhere(dev, stream):
-    torch = _torch()
-    with torch.cuda.device(dev):
-        if stream is None:
-            yield
-        else:
-            with torch.cuda.stream(stream):
-                yield
-
-
-_HERE = contextlib.nullcontext()
-
-
-def _on(dev, stream):
-    """Makes ``dev`` the current device and ``stream`` (if given) the current stream, so that
-    the launch goes to the tensors' device and what the call allocates belongs to the stream
-    that uses it; nothing to do in the common case."""
-    if stream is None:
-        if _torch().cuda.current_device() == dev:
-            return _HERE
-    elif stream.device.index != dev:
-        raise ValueError("stream must be one of the tensors' device")
-    return _elsewhere(dev, stream)
+def _given(stream):
+    """Address of a given stream for the compiled binding (None: the tensors' current one)."""
+    return None if stream is None else stream.cuda_stream
 
 
 StepPlan = collections.namedtuple("StepPlan", "context_lens query_start slot_mapping positions num_free")
@@ -501,46 +468,12 @@ def plan_step(block_tables, context_lens, new_lens, free_blocks, num_free, token
     """Block tables, slots and positions of one step's new tokens on the GPU (``pa_plan_step``).
 
     ``block_tables`` is filled in place with blocks from the end of the free stack
-    ``free_blocks[:num_free]``; ``out`` (a ``StepPlan``) receives the rest, a new one by default."""
-    torch = _torch()
-    B, max_blocks = block_tables.shape
-    i32 = torch.int32
-    if context_lens.shape != (B,) or new_lens.shape != (B,):
-        raise ValueError("context_lens and new_lens must be [num_seqs]")
-    if num_free.numel() != 1 or free_blocks.dim() != 1:
-        raise ValueError("free_blocks must be [capacity], num_free [1]")
-    N = int(token_capacity)
-    if N < 0:
-        raise ValueError("token_capacity must not be negative")
-    dev = _same_device(block_tables, context_lens=context_lens, new_lens=new_lens, free_blocks=free_blocks,
-                       num_free=num_free, status=status)
-    with _on(dev, stream):
-        if out is None:
-            # one allocation for all five, the 8-byte slots first, each part on 16 bytes
-            at = [8 * N]
-            for n in (N, B + 1, B, 1):
-                at[-1] = (at[-1] + 15) & ~15
-                at.append(at[-1] + 4 * n)
-            buf = torch.empty(at[-1], dtype=torch.uint8, device=block_tables.device)
-            part = lambda i, n: buf[at[i]:at[i] + 4 * n].view(i32)  # noqa: E731
-            out = StepPlan(part(2, B), part(1, B + 1), buf[:8 * N].view(torch.int64), part(0, N), part(3, 1))
-        else:
-            out = StepPlan(*out)
-            if (out.context_lens.shape != (B,) or out.query_start.shape != (B + 1,) or
-                    out.slot_mapping.shape != (N,) or out.positions.shape != (N,) or out.num_free.numel() != 1):
-                raise ValueError("out does not fit num_seqs and token_capacity")
-            _same_device(block_tables, **out._asdict())
-        rc = lib().pa_plan_step(
-            _dev(block_tables, "block_tables", i32), _dev(context_lens, "context_lens", i32),
-            _dev(new_lens, "new_lens", i32), _dev(free_blocks, "free_blocks", i32),
-            _dev(num_free, "num_free", i32), _dev(out.context_lens, "out.context_lens", i32),
-            _dev(out.query_start, "out.query_start", i32),
-            _dev(out.slot_mapping, "out.slot_mapping", torch.int64),
-            _dev(out.positions, "out.positions", i32), _dev(out.num_free, "out.num_free", i32), B,
-            max_blocks, BLOCK_SIZE, int(num_blocks), free_blocks.shape[0], N, _status_ptr(status),
-            _stream(stream, block_tables))
-    check(rc, "pa_plan_step")
-    return out
+    ``free_blocks[:num_free]``; ``out`` (a ``StepPlan``) receives the rest, new tensors by default."""
+    r = _lib.binding().plan_step(block_tables, context_lens, new_lens, free_blocks, num_free,
+                                 token_capacity, num_blocks, out, status, _given(stream))
+    if type(r) is int:
+        check(r, "pa_plan_step")
+    return StepPlan._make(r) if out is None else out
 
 
 RotaryPlan = collections.namedtuple("RotaryPlan", "turns attention_factor rotary_dim interleaved")
@@ -561,23 +494,15 @@ def rotary_plan(rotary_dim, base=10000.0, *, interleaved=False, scaling="none", 
     rotary_dim = int(rotary_dim)
     host = torch.empty(max(rotary_dim, 0) // 2, dtype=torch.int64)
     a = ctypes.c_double()
-    buf = host.data_ptr() if host.numel() else ctypes.addressof(ctypes.c_uint64())
+    none = ctypes.c_uint64()
+    buf = host.data_ptr() if host.numel() else ctypes.addressof(none)
     rc = lib().pa_rotary_turns(buf, ctypes.addressof(a), rotary_dim, float(base), _lib.PA_ROTARY_SCALINGS[scaling],
                                float(factor), float(original_context), float(beta_fast), float(beta_slow))
     check(rc, "pa_rotary_turns")
     return RotaryPlan(host.to(device), a.value, rotary_dim, bool(interleaved))
 
 
-def _rows(t, name, shape, dtype):
-    """Address and token stride of [tokens][heads][head_dim] rows, whose tokens may lie apart."""
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    stride = t.stride()
-    if (shape[2] > 1 and stride[2] != 1) or (shape[1] > 1 and stride[1] != shape[2]):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), (stride[0] if shape[0] > 1 else shape[1] * shape[2])
+_NO_ROPE = RotaryPlan(None, 1.0, 0, False)
 
 
 def rope_cache_write(query, key, value, positions, rope, key_cache, value_cache, slot_mapping, *,
@@ -589,56 +514,13 @@ def rope_cache_write(query, key, value, positions, rope, key_cache, value_cache,
     the same type, or of E4M3 codes with ``k_scales`` / ``v_scales`` [num_blocks][Hkv].  Returns
     ``query_out`` (a new tensor by default; may be ``query``); ``query`` None writes keys and
     values only."""
-    torch = _torch()
-    NB, Hkv, BS, D = key_cache.shape
-    T = slot_mapping.shape[0]
-    if BS != BLOCK_SIZE or value_cache.shape != key_cache.shape:
-        raise ValueError("pools must be [num_blocks][num_kv_heads][16][head_dim]")
-    dev = _same_device(key_cache, value_cache=value_cache, query=query, key=key, value=value,
-                       positions=positions, slot_mapping=slot_mapping, k_scales=k_scales,
-                       v_scales=v_scales, query_out=query_out, status=status,
-                       turns=None if rope is None else rope.turns)
-    dtype = key.dtype
-    code = _dtype_code(key)
-    fp8 = _is_fp8(key_cache)
-    ks = vs = None
-    if fp8:
-        if k_scales is None or v_scales is None or k_scales.shape != (NB, Hkv) or v_scales.shape != (NB, Hkv):
-            raise ValueError("E4M3 pools need k_scales and v_scales [num_blocks][num_kv_heads]")
-        if not _is_fp8(value_cache):
-            raise TypeError("both pools must hold E4M3 codes")
-        ks, vs = _dev(k_scales, "k_scales", torch.float32), _dev(v_scales, "v_scales", torch.float32)
-    elif key_cache.dtype != dtype or value_cache.dtype != dtype:
-        raise TypeError("pools must have the rows' element type, or hold E4M3 codes")
-    k_ptr, k_stride = _rows(key, "key", (T, Hkv, D), dtype)
-    v_ptr, v_stride = _rows(value, "value", (T, Hkv, D), dtype)
-    pos = turns = None
-    rot, factor, inter = 0, 1.0, 0
-    if rope is not None and rope.rotary_dim > 0:
-        if positions is None or positions.shape != (T,):
-            raise ValueError("positions must be [num_tokens]")
-        pos, turns = _dev(positions, "positions", torch.int32), _dev(rope.turns, "turns", torch.int64)
-        rot, factor, inter = rope.rotary_dim, rope.attention_factor, int(rope.interleaved)
-        if rope.turns.numel() * 2 != rot:
-            raise ValueError("rope: turns must be [rotary_dim / 2]")
-    with _on(dev, stream):
-        Hq, q_ptr, q_stride, o_ptr, o_stride = 0, None, 0, None, 0
-        if query is not None:
-            if query.dim() != 3:
-                raise ValueError("query must be [num_tokens][num_q_heads][head_dim]")
-            Hq = query.shape[1]
-            shape = (T, Hq, D)
-            q_ptr, q_stride = _rows(query, "query", shape, dtype)
-            if query_out is None:
-                query_out = torch.empty(shape, dtype=dtype, device=query.device)
-            o_ptr, o_stride = _rows(query_out, "query_out", shape, dtype)
-        rc = lib().pa_rope_cache_write(
-            o_ptr, q_ptr, k_ptr, v_ptr, pos, turns, factor, rot, inter, _dev(key_cache, "key_cache"),
-            _dev(value_cache, "value_cache"), ks, vs, _dev(slot_mapping, "slot_mapping", torch.int64), T, Hq,
-            Hkv, D, o_stride, q_stride, k_stride, v_stride, BS, NB, code,
-            _lib.PA_DTYPE_FP8_E4M3 if fp8 else code, _status_ptr(status), _stream(stream, key_cache))
-    check(rc, "pa_rope_cache_write")
-    return query_out
+    turns, factor, rotary_dim, interleaved = _NO_ROPE if rope is None else rope
+    r = _lib.binding().rope_cache_write(query, key, value, positions, turns, factor, rotary_dim, interleaved,
+                                        key_cache, value_cache, slot_mapping, k_scales, v_scales, query_out,
+                                        status, _given(stream))
+    if type(r) is int:
+        check(r, "pa_rope_cache_write")
+    return query_out if query_out is not None and query is not None else r
 
 
 def decode_block_fp8_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
@@ -651,57 +533,18 @@ def decode_block_fp8_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_d
     return int(n)
 
 
-def _block_fp8_pools(query, key_cache, value_cache, k_scales, v_scales, block_tables, num_seqs):
-    torch = _torch()
-    NB, Hkv, BS, D = key_cache.shape
-    if BS != BLOCK_SIZE or D != query.shape[2] or value_cache.shape != key_cache.shape:
-        raise ValueError("pools must be [num_blocks][num_kv_heads][16][head_dim] like query")
-    if not (_is_fp8(key_cache) and _is_fp8(value_cache)) or query.dtype != torch.bfloat16:
-        raise TypeError("E4M3 pools and a bfloat16 query are expected")
-    if k_scales.shape != (NB, Hkv) or v_scales.shape != (NB, Hkv):
-        raise ValueError("k_scales / v_scales must be [num_blocks][num_kv_heads]")
-    if block_tables.dim() != 2 or block_tables.shape[0] != num_seqs:
-        raise ValueError("block_tables must be [num_seqs][max_blocks]")
-    return NB, Hkv, D
-
-
 def decode_block_fp8(query, key_cache, value_cache, k_scales, v_scales, block_tables, context_lens,
                      scale=None, *, window=0, out=None, partition_size=0, workspace=None, status=None,
                      stream=None):
     """Paged decode over E4M3 pools with one scale per block and KV head
     (``pa_decode_block_fp8``); ``window`` > 0 attends to the last positions only.  Returns
     ``out`` (bf16)."""
-    torch = _torch()
-    B, Hq, D = query.shape
-    NB, Hkv, D = _block_fp8_pools(query, key_cache, value_cache, k_scales, v_scales, block_tables, B)
-    if context_lens.shape != (B,):
-        raise ValueError("context_lens must be [num_seqs]")
-    max_blocks = block_tables.shape[1]
-    dev = _same_device(query, key_cache=key_cache, value_cache=value_cache, k_scales=k_scales,
-                       v_scales=v_scales, block_tables=block_tables, context_lens=context_lens, out=out,
-                       workspace=workspace, status=status)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty(query.shape, dtype=query.dtype, device=query.device)
-        elif out.shape != query.shape or out.dtype != query.dtype:
-            raise ValueError("out must match query")
-        if workspace is None:
-            need = lib().pa_decode_block_fp8_workspace_bytes(B, Hq, Hkv, D, max_blocks, BLOCK_SIZE, int(window),
-                                                             int(partition_size))
-            if 0 < need < 1 << 62:     # invalid sizes are the call's to refuse
-                workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
-        ws_ptr, ws_bytes = None, 0
-        if workspace is not None:
-            ws_ptr, ws_bytes = _dev(workspace, "workspace"), workspace.nbytes
-        rc = lib().pa_decode_block_fp8(
-            _dev(out, "out"), _dev(query, "query"), _dev(key_cache, "key_cache"),
-            _dev(value_cache, "value_cache"), _dev(k_scales, "k_scales", torch.float32),
-            _dev(v_scales, "v_scales", torch.float32), _dev(block_tables, "block_tables", torch.int32),
-            _dev(context_lens, "context_lens", torch.int32), B, Hq, Hkv, D, BLOCK_SIZE, max_blocks, NB,
-            D ** -0.5 if scale is None else float(scale), int(window), int(partition_size), ws_ptr, ws_bytes,
-            _status_ptr(status), _stream(stream, query))
-    check(rc, "pa_decode_block_fp8")
-    return out
+    r = _lib.binding().decode_block_fp8(query, key_cache, value_cache, k_scales, v_scales, block_tables,
+                                        context_lens, scale, window, out, partition_size, workspace, status,
+                                        _given(stream))
+    if type(r) is int:
+        check(r, "pa_decode_block_fp8")
+    return r if out is None else out
 
 
 def prefill_block_fp8(query, key_cache, value_cache, k_scales, v_scales, block_tables, context_lens, query_start,
@@ -709,34 +552,14 @@ def prefill_block_fp8(query, key_cache, value_cache, k_scales, v_scales, block_t
                       stream=None):
     """Chunked prefill over E4M3 pools with one scale per block and KV head
     (``pa_prefill_block_fp8``); arguments as ``prefill``.  Returns ``out`` (bf16)."""
-    torch = _torch()
-    N, Hq, D = query.shape
-    B = context_lens.shape[0]
-    NB, Hkv, D = _block_fp8_pools(query, key_cache, value_cache, k_scales, v_scales, block_tables, B)
-    if query_start.shape != (B + 1,):
-        raise ValueError("query_start must be [num_seqs + 1]")
-    dev = _same_device(query, key_cache=key_cache, value_cache=value_cache, k_scales=k_scales,
-                       v_scales=v_scales, block_tables=block_tables, context_lens=context_lens,
-                       query_start=query_start, out=out, workspace=workspace, status=status)
-    with _on(dev, stream):
-        if max_query_len is None:
-            max_query_len = int((query_start[1:] - query_start[:-1]).max().item()) if B else 0
-        if out is None:
-            out = torch.empty(query.shape, dtype=query.dtype, device=query.device)
-        elif out.shape != query.shape or out.dtype != query.dtype:
-            raise ValueError("out must match query")
-        if workspace is None:
-            workspace = torch.empty(lib().pa_prefill_block_fp8_workspace_bytes(), dtype=torch.uint8, device=query.device)
-        rc = lib().pa_prefill_block_fp8(
-            _dev(out, "out"), _dev(query, "query"), _dev(key_cache, "key_cache"),
-            _dev(value_cache, "value_cache"), _dev(k_scales, "k_scales", torch.float32),
-            _dev(v_scales, "v_scales", torch.float32), _dev(block_tables, "block_tables", torch.int32),
-            _dev(context_lens, "context_lens", torch.int32), _dev(query_start, "query_start", torch.int32), B, Hq,
-            Hkv, D, BLOCK_SIZE, block_tables.shape[1], NB, N, int(max_query_len),
-            D ** -0.5 if scale is None else float(scale), int(window), _dev(workspace, "workspace"),
-            workspace.nbytes, _status_ptr(status), _stream(stream, query))
-    check(rc, "pa_prefill_block_fp8")
-    return out
+    if max_query_len is None:
+        max_query_len = int((query_start[1:] - query_start[:-1]).max().item()) if query_start.numel() > 1 else 0
+    r = _lib.binding().prefill_block_fp8(query, key_cache, value_cache, k_scales, v_scales, block_tables,
+                                         context_lens, query_start, max_query_len, scale, window, out, workspace,
+                                         status, _given(stream))
+    if type(r) is int:
+        check(r, "pa_prefill_block_fp8")
+    return r if out is None else out
 
 
 def _staging_ptr(t, nbytes):

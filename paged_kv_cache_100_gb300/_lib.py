@@ -156,6 +156,31 @@ def lib():
     return _lib
 
 
+_binding = None
+
+
+def binding():
+    """The compiled tensor binding (``_build/_pagedkv_torch.so``) on the loaded library."""
+    global _binding
+    if _binding is None:
+        import importlib.util
+        import torch  # noqa: F401  its libraries come first
+        path = os.path.join(HERE, "_build", "_pagedkv_torch.so")
+        if not os.path.exists(path):
+            raise RuntimeError(
+                f"paged_kv_cache_100_gb300: tensor binding not built ({path} missing); "
+                "run paged_kv_cache_100_gb300.build.build() first")
+        handle = lib()
+        spec = importlib.util.spec_from_file_location("_pagedkv_torch", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.bind(*[ctypes.cast(getattr(handle, n), vp).value for n in (
+            "pa_plan_step", "pa_rope_cache_write", "pa_decode_block_fp8", "pa_decode_block_fp8_workspace_bytes",
+            "pa_prefill_block_fp8", "pa_prefill_block_fp8_workspace_bytes")])
+        _binding = mod
+    return _binding
+
+
 def check(status: int, what: str) -> None:
     if status != PA_OK:
         raise PagedKVError(status, what)

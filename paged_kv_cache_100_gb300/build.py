@@ -14,11 +14,13 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libpagedkv.so")
+BINDING_MODULE = "_pagedkv_torch.so"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CU_SOURCES = ["pa_decode.cu", "pa_cache.cu", "pa_decode_noalloc.cu", "pa_prefill.cu", "pa_plan.cu",
               "pa_rope.cu", "pa_block8_decode.cu", "pa_block8_prefill.cu"]
 CPP_SOURCES = ["block_manager.cpp"]
+BINDING = "torch_binding.cpp"     # its own module: it follows the installed torch, the library does not
 HEADERS = ["pa_device.cuh", "pa_internal.h", "pa_tc.cuh", "pa_block8.cuh"]
 
 
@@ -30,12 +32,28 @@ def _nvcc() -> str:
 
 
 def _stale(lib: str) -> bool:
-    if not os.path.exists(lib):
+    binding = os.path.join(os.path.dirname(lib), BINDING_MODULE)
+    if not os.path.exists(lib) or (lib == LIB and not os.path.exists(binding)):
         return True
     t = os.path.getmtime(lib)
-    deps = [os.path.join(CSRC, f) for f in CU_SOURCES + CPP_SOURCES + HEADERS]
+    deps = [os.path.join(CSRC, f) for f in CU_SOURCES + CPP_SOURCES + HEADERS + [BINDING]]
     deps += [os.path.join(INCLUDE, "pagedkv.h"), os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _binding_command(out: str) -> list:
+    """The compiled tensor binding: a CPython module linked against the installed torch."""
+    import sysconfig
+    import torch
+    tdir = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(tdir, "include"),
+           os.path.join(tdir, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    libs = os.path.join(tdir, "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[f"-I{d}" for d in inc], os.path.join(CSRC, BINDING), "-o", out, f"-L{libs}", f"-Wl,-rpath,{libs}",
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, defines=(), build_dir=None) -> str:
@@ -67,6 +85,9 @@ def build(force: bool = False, verbose_ptxas: bool = False, defines=(), build_di
                os.path.join(CSRC, src), "-o", obj]
         jobs.append((cmd, src))
         objs.append(obj)
+    binding = os.path.join(bdir, BINDING_MODULE)
+    if build_dir is None:
+        jobs.append((_binding_command(binding + f".tmp{os.getpid()}"), BINDING))
     procs = [(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT), src)
              for cmd, src in jobs]
     failed = []
@@ -79,6 +100,8 @@ def build(force: bool = False, verbose_ptxas: bool = False, defines=(), build_di
             failed.append(src)
     if failed:
         raise RuntimeError(f"compilation failed: {', '.join(failed)}")
+    if build_dir is None:
+        os.replace(binding + f".tmp{os.getpid()}", binding)
     tmp = lib + f".tmp{os.getpid()}"
     subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, lib)
