@@ -580,8 +580,10 @@ pa_status pa_decode_block_fp8(void *out, const void *query, const void *key_cach
  * context_lens, max_query_len, window, causal mask) with the pools and scales
  * of pa_decode_block_fp8.
  *  workspace         device scratch of at least
- *                    pa_prefill_block_fp8_workspace_bytes() bytes, 16-byte
- *                    aligned; calls that run at the same time need their own
+ *                    pa_prefill_block_fp8_workspace_bytes(...) bytes, 16-byte
+ *                    aligned; calls that run at the same time need their own.
+ *                    Small calls are cut along the context to fill the GPU and
+ *                    keep partial outputs there; a second kernel merges them
  * A sequence whose query_start entries fall, leave [0, num_query_tokens] or
  * exceed its context length is not computed and flagged PA_DEV_BAD_CONTEXT_LEN.
  * Supported: head_dim 128, group 1, 2, 4, 8 or 16.
@@ -593,7 +595,9 @@ pa_status pa_decode_block_fp8(void *out, const void *query, const void *key_cach
  * pa_decode_block_fp8.  A NaN value reaches every row of the 256-row tiles that
  * process its position, also rows before it.
  */
-size_t pa_prefill_block_fp8_workspace_bytes(void);
+size_t pa_prefill_block_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
+                                            int head_dim, int max_blocks_per_seq,
+                                            int num_query_tokens, int max_query_len, int window);
 pa_status pa_prefill_block_fp8(void *out, const void *query, const void *key_cache,
                                const void *value_cache, const float *k_scales,
                                const float *v_scales, const int32_t *block_tables,

@@ -63,7 +63,7 @@ SIGNATURES = {
     "pa_decode_block_fp8_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32, i32, i32]),
     "pa_decode_block_fp8": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32,
                                   f32, i32, i32, vp, sz, vp, vp]),
-    "pa_prefill_block_fp8_workspace_bytes": (sz, []),
+    "pa_prefill_block_fp8_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32, i32, i32]),
     "pa_prefill_block_fp8": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
                                    i32, i32, i32, f32, i32, vp, sz, vp, vp]),
     "pa_swap_bytes": (sz, [i32, i32, i32, i32]),

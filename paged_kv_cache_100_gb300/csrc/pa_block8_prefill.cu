@@ -28,6 +28,10 @@
 //                weights would leave f16's range; they also split their Q tile;
 //   warps 18, 19 widen each V tile, zeroing positions outside the item's range,
 //                and stage the scales of the step after.
+// With fewer items than SMs each is cut along its context into parts, whose
+// (reference, sum, output) a second kernel merges: a chunk of a few tokens over a
+// long context would otherwise keep one SM per KV head busy (16 tokens on 8192
+// with 8 KV heads: 123 us whole, 24 us in 16 parts).
 // Persistent CTAs take items from a ticket counter; barrier phases are counted
 // across items, so an item's loads start under the end of the one before.
 // Every wait is bounded (about a second); one that gives up sets PA_DEV_TIMEOUT,
@@ -142,7 +146,10 @@ struct PrefillArgs {
     float scale_log2;
     int n_mt;                            // pair tiles per (sequence, KV head)
     int num_items;
-    unsigned int *work_counter;
+    unsigned int *work_counter;          // nullptr: one item per CTA
+    int splits;                          // parts an item is cut into at most
+    float *part_o;                       // [(token * Hq + head) * splits + part][128]
+    float2 *part_ml;                     // (reference, sum)
 };
 
 // A phase that is complete passes at once; the failure flag (another shared
@@ -355,13 +362,29 @@ struct Item {
     int q0, T, C;       // first query row of the chunk, its tokens, context before it
     int t0;             // first token of tile A
     int kv_lo, kv_hi, blk_lo, blk_hi, n_tiles;
+    int part, parts;
     bool has_b;
 };
 
+// The positions, blocks and steps of the 256-row tile that begins at token t0 of
+// d's chunk (d.C, d.T), and the parts they are cut into.
+__device__ __forceinline__ void tile_range(const PrefillArgs &a, Item &d) {
+    const int tok_per_tile = kRows / a.group;
+    d.kv_hi = d.C + min(d.T, d.t0 + kQT * tok_per_tile);
+    d.kv_lo = a.window > 0 ? max(0, d.C + d.t0 + 1 - a.window) : 0;
+    d.blk_lo = d.kv_lo / kBlockSize;
+    d.blk_hi = (d.kv_hi + kBlockSize - 1) / kBlockSize;
+    d.n_tiles = (d.blk_hi - d.blk_lo + 7) / 8;
+    d.parts = min(a.splits, d.n_tiles);
+}
+
+template <bool kCut>
 __device__ __forceinline__ bool describe_item(const PrefillArgs &a, int item, bool by_length, bool say, const int *perm,
                                               Item &d) {
     const int tok_per_tile = kRows / a.group;
     const int lmax = a.max_blocks * kBlockSize;
+    d.part = kCut ? item % a.splits : 0;
+    if constexpr (kCut) item /= a.splits;
     // by_length: every group's longest tile, then every group's next one, ...;
     // else the tiles of a (sequence, KV head) together, longest first
     const int groups = a.num_seqs * a.num_kv_heads;
@@ -373,7 +396,7 @@ __device__ __forceinline__ bool describe_item(const PrefillArgs &a, int item, bo
     d.q0 = a.query_start[d.b];
     const int end = a.query_start[d.b + 1];
     const int L = a.context_lens[d.b];
-    const bool first = say && x == 0 && d.kvh == 0;
+    const bool first = say && x == 0 && d.kvh == 0 && d.part == 0;
     if (d.q0 < 0 || end < d.q0 || end > a.num_query_tokens || end - d.q0 > L || L > lmax) {
         if (first) report(a.status, PA_DEV_BAD_CONTEXT_LEN);
         return false;
@@ -383,15 +406,20 @@ __device__ __forceinline__ bool describe_item(const PrefillArgs &a, int item, bo
     d.t0 = (a.n_mt - 1 - x) * kQT * tok_per_tile;
     if (d.t0 >= d.T) return false;
     d.C = L - d.T;
-    d.kv_hi = d.C + min(d.T, d.t0 + kQT * tok_per_tile);
-    d.kv_lo = a.window > 0 ? max(0, d.C + d.t0 + 1 - a.window) : 0;
-    d.blk_lo = d.kv_lo / kBlockSize;
-    d.blk_hi = (d.kv_hi + kBlockSize - 1) / kBlockSize;
+    tile_range(a, d);
+    if constexpr (kCut) {
+        if (d.part >= d.parts) return false;
+        const int lo = d.part * d.n_tiles / d.parts, hi = (d.part + 1) * d.n_tiles / d.parts;
+        d.blk_hi = min(d.blk_hi, d.blk_lo + 8 * hi);
+        d.blk_lo += 8 * lo;
+        d.n_tiles = hi - lo;
+    }
     d.has_b = d.t0 + tok_per_tile < d.T;
-    d.n_tiles = (d.blk_hi - d.blk_lo + 7) / 8;
     return true;
 }
 
+// kCut: items are cut along the context and leave partial outputs.
+template <bool kCut>
 __global__ void __launch_bounds__(kThreads, 1)
     pa_prefill_block8_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                              const __grid_constant__ CUtensorMap vmap, const PrefillArgs a) {
@@ -480,14 +508,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             int q_issued = -1;
             uint32_t gstep = 0, k_issued = 0, v_issued = 0;
-            bool ok = true;
+            bool ok = true, taken = false;
             for (int it = 0;; ++it) {
                 int item = -1;
                 Item d;
                 while (ok) {
-                    const int t = (int)atomicAdd(a.work_counter, 1u);
+                    int t = a.num_items;
+                    if (a.work_counter != nullptr) t = (int)atomicAdd(a.work_counter, 1u);
+                    else if (it == 0 && !taken) t = blockIdx.x;
+                    taken = true;
                     if (t >= a.num_items) break;
-                    if (describe_item(a, t, by_length, true, perm, d)) {
+                    if (describe_item<kCut>(a, t, by_length, true, perm, d)) {
                         item = t;
                         break;
                     }
@@ -608,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&bars[kItemEmpty + slot]);
             if (item < 0) break;
             Item d;
-            describe_item(a, item, by_length, false, perm, d);
+            describe_item<kCut>(a, item, by_length, false, perm, d);
             const int n = d.n_tiles;
             if (!warp_wait(&bars[kQSplit], it & 1, fail, a.status) ||
                 !warp_wait(&bars[kKFull + gstep % kKStages], (gstep / kKStages) & 1, fail, a.status))
@@ -662,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int item = next_item(it);
             if (item < 0) break;
             Item d;
-            describe_item(a, item, by_length, false, perm, d);
+            describe_item<kCut>(a, item, by_length, false, perm, d);
             // The scales of a step's blocks, one thread per block of the first warp.  The
             // table entry is read two steps ahead and the scales one step, so that no
             // step waits for the chain of loads; the slot written last held the scales of
@@ -771,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // all threads of the group decide alike, so that they reach its named barriers equally often
             if (!group_all(x, item >= 0 && ok && !*fail)) break;
             Item d;
-            describe_item(a, item, by_length, false, perm, d);
+            describe_item<kCut>(a, item, by_length, false, perm, d);
             if (x == 0 || d.has_b) {
                 const int tx0 = d.t0 + x * tok_per_tile;
                 const int ntok = min(tok_per_tile, d.T - tx0);
@@ -900,7 +931,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pair_sync(x, quarter);
                 const float l_row = l + red[(sx * 2 + (part ^ 1)) * kRows + r];
                 const bool drained = warp_wait(&bars[kDrain], it & 1, fail, a.status);
-                if (__all_sync(0xffffffffu, ok) && drained) {
+                if (kCut && __all_sync(0xffffffffu, ok) && drained && d.parts > 1) {
+                    tc_fence_after();
+                    const int64_t prow = ((int64_t)(d.q0 + tx0 + tr) * a.num_q_heads + d.kvh * a.group + (r % a.group)) *
+                                             a.splits + d.part;
+                    float4 *po = reinterpret_cast<float4 *>(a.part_o + prow * kD + part * kCols);
+#pragma unroll 1
+                    for (int c = 0; c < kCols; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o_base + c, o);
+                        tmem_wait_ld();
+                        if (real) {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                po[c / 4 + q] = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
+                                                            __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
+                        }
+                    }
+                    if (real && part == 0) a.part_ml[prow] = make_float2(m_used, l_row);
+                } else if (__all_sync(0xffffffffu, ok) && drained) {
                     tc_fence_after();
                     const float inv = l_row == 0.f ? 0.f : 1.f / l_row;
                     __nv_bfloat16 *orow =
@@ -942,6 +991,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// Merges the parts of the rows whose tile was cut, one warp a row.
+__global__ void __launch_bounds__(128) pa_merge_prefill8_kernel(const PrefillArgs a) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (row >= (int64_t)a.num_query_tokens * a.num_q_heads) return;
+    const int token = (int)(row / a.num_q_heads);
+    // the last sequence that begins at or before the token
+    int lo = 0, hi = a.num_seqs;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (a.query_start[mid] <= token) lo = mid;
+        else hi = mid;
+    }
+    Item d;
+    d.q0 = a.query_start[lo];
+    const int end = a.query_start[lo + 1], L = a.context_lens[lo];
+    if (token < d.q0 || token >= end || end > a.num_query_tokens || end - d.q0 > L || L > a.max_blocks * kBlockSize ||
+        token - d.q0 >= a.n_mt * (kQT * kRows / a.group))
+        return;
+    d.T = end - d.q0;
+    d.C = L - d.T;
+    const int tokens = kQT * kRows / a.group;
+    d.t0 = (token - d.q0) / tokens * tokens;
+    tile_range(a, d);
+    if (d.parts <= 1) return;
+    const float2 *ml = a.part_ml + row * a.splits;
+    const float4 *po = reinterpret_cast<const float4 *>(a.part_o + row * a.splits * kD);
+    float M = -INFINITY;
+    for (int p = 0; p < d.parts; ++p) M = fmaxf(M, ml[p].x);
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = 0; p0 < d.parts; p0 += 8) {
+        float4 v[8];
+        float2 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const bool in = p0 + i < d.parts;
+            v[i] = in ? po[(int64_t)(p0 + i) * 32 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[i] = in ? ml[p0 + i] : make_float2(-INFINITY, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float f = pow2_diff(x[i].x, M);
+            sum = fmaf(f, x[i].y, sum);
+            acc.x = fmaf(f, v[i].x, acc.x);
+            acc.y = fmaf(f, v[i].y, acc.y);
+            acc.z = fmaf(f, v[i].z, acc.z);
+            acc.w = fmaf(f, v[i].w, acc.w);
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * kD + 4 * lane) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+}
+
 // The query as [rows][KV head][head of the group][head_dim]: a box of 128 / group
 // rows x group heads x 64 elements is one half of a 128-row tile.
 bool encode_query_map(CUtensorMap *map, const void *query, int rows, int num_q_heads, int num_kv_heads) {
@@ -981,7 +1087,44 @@ int sms() {
 
 using namespace pa;
 
-extern "C" size_t pa_prefill_block_fp8_workspace_bytes(void) { return kWorkspaceBytes; }
+namespace {
+
+bool group_ok(int group) { return group == 1 || group == 2 || group == 4 || group == 8 || group == 16; }
+
+// Items of a call, and the parts they are cut into: as many as fill the SMs,
+// none shorter than four steps of a full-length context (a part costs its CTA's
+// start and end, and the merge a kernel).
+struct Cut {
+    int64_t tiles, items;
+    int splits;
+};
+Cut cut_of(int num_seqs, int num_q_heads, int num_kv_heads, int max_blocks, int window, int max_query_len) {
+    Cut c;
+    const int group = num_q_heads / num_kv_heads;
+    c.tiles = ((int64_t)max_query_len * group + kQT * kRows - 1) / (kQT * kRows);
+    c.items = c.tiles * num_kv_heads * num_seqs;
+    int64_t blocks = max_blocks;
+    if (window > 0) blocks = std::min<int64_t>(blocks, ((int64_t)window + kQT * kRows / group) / kBlockSize + 2);
+    const int64_t steps = (blocks + 7) / 8;
+    c.splits = c.items > 0 ? (int)std::max<int64_t>(1, std::min<int64_t>(sms() / c.items, steps / 4)) : 1;
+    return c;
+}
+size_t part_rows_bytes(int64_t rows) { return (size_t)rows * kD * sizeof(float); }
+
+}  // namespace
+
+extern "C" size_t pa_prefill_block_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                                       int max_blocks_per_seq, int num_query_tokens,
+                                                       int max_query_len, int window) {
+    if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 || head_dim != kD ||
+        !group_ok(num_q_heads / num_kv_heads) || max_blocks_per_seq < 0 ||
+        max_blocks_per_seq > 0x7fffffff / kBlockSize || num_query_tokens < 0 || max_query_len < 0 || window < 0)
+        return (size_t)-1;
+    const Cut c = cut_of(num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq, window, max_query_len);
+    if (c.splits <= 1) return kWorkspaceBytes;
+    const int64_t rows = (int64_t)num_query_tokens * num_q_heads * c.splits;
+    return part_rows_bytes(rows) + (size_t)rows * sizeof(float2);
+}
 
 extern "C" pa_status pa_prefill_block_fp8(void *out, const void *query, const void *key_cache, const void *value_cache,
                                           const float *k_scales, const float *v_scales, const int32_t *block_tables,
@@ -995,8 +1138,7 @@ extern "C" pa_status pa_prefill_block_fp8(void *out, const void *query, const vo
         num_blocks <= 0 || num_query_tokens < 0 || max_query_len < 0 || window < 0 || !(scale == scale))
         return PA_ERR_INVALID_ARG;
     const int group = num_q_heads / num_kv_heads;
-    if (head_dim != kD || (group != 1 && group != 2 && group != 4 && group != 8 && group != 16))
-        return PA_ERR_UNSUPPORTED;
+    if (head_dim != kD || !group_ok(group)) return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0 || num_query_tokens == 0 || max_query_len == 0) return PA_OK;
     if (!out || !query || !key_cache || !value_cache || !k_scales || !v_scales || !context_lens || !query_start ||
         (!block_tables && max_blocks_per_seq > 0))
@@ -1006,10 +1148,12 @@ extern "C" pa_status pa_prefill_block_fp8(void *out, const void *query, const vo
           reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens) |
           reinterpret_cast<uintptr_t>(query_start)) & 3u))
         return PA_ERR_INVALID_ARG;
-    if (workspace == nullptr || workspace_bytes < kWorkspaceBytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
+    const size_t need = pa_prefill_block_fp8_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                                             max_blocks_per_seq, num_query_tokens, max_query_len, window);
+    if (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)) return PA_ERR_WORKSPACE;
     const int64_t rows = (int64_t)num_blocks * num_kv_heads * kBlockSize;
-    const int64_t tiles = ((int64_t)max_query_len * group + kQT * kRows - 1) / (kQT * kRows);
-    const int64_t items = tiles * num_kv_heads * num_seqs;
+    const Cut cut = cut_of(num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq, window, max_query_len);
+    const int64_t items = cut.items * cut.splits;
     if (rows >= ((int64_t)1 << 31) || items >= ((int64_t)1 << 31) - kThreads) return PA_ERR_UNSUPPORTED;
     CUtensorMap qmap, kmap, vmap;
     if (!encode_query_map(&qmap, query, num_query_tokens, num_q_heads, num_kv_heads) ||
@@ -1033,18 +1177,32 @@ extern "C" pa_status pa_prefill_block_fp8(void *out, const void *query, const vo
     a.max_query_len = max_query_len;
     a.window = window;
     a.scale_log2 = scale * 1.4426950408889634f;
-    a.n_mt = (int)tiles;
+    a.n_mt = (int)cut.tiles;
     a.num_items = (int)items;
-    a.work_counter = static_cast<unsigned int *>(workspace);
+    a.splits = cut.splits;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(unsigned int), st);
-    if (e != cudaSuccess) return cuda_failure(e, "cudaMemsetAsync(prefill ticket)");
-    e = cudaFuncSetAttribute(pa_prefill_block8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess) return cuda_failure(e, "cudaFuncSetAttribute(block-scaled prefill)");
     const int64_t grid = std::min<int64_t>(items, sms());
-    e = launch_chained(pa_prefill_block8_kernel, dim3((unsigned)grid), dim3(kThreads), (size_t)kSmemBytes, st, qmap,
+    cudaError_t e;
+    if (cut.splits > 1) {
+        a.part_o = static_cast<float *>(workspace);
+        a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) +
+                                               part_rows_bytes((int64_t)num_query_tokens * num_q_heads * cut.splits));
+    } else if (items > grid) {
+        a.work_counter = static_cast<unsigned int *>(workspace);
+        e = cudaMemsetAsync(workspace, 0, sizeof(unsigned int), st);
+        if (e != cudaSuccess) return cuda_failure(e, "cudaMemsetAsync(prefill ticket)");
+    }
+    auto kernel = cut.splits > 1 ? pa_prefill_block8_kernel<true> : pa_prefill_block8_kernel<false>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return cuda_failure(e, "cudaFuncSetAttribute(block-scaled prefill)");
+    e = launch_chained(kernel, dim3((unsigned)grid), dim3(kThreads), (size_t)kSmemBytes, st, qmap,
                        kmap, vmap, a);
     if (e != cudaSuccess) return cuda_failure(e, "pa_prefill_block8_kernel launch");
+    count_launches(1);
+    if (cut.splits == 1) return PA_OK;
+    const int64_t merge = ((int64_t)num_query_tokens * num_q_heads + 3) / 4;
+    e = launch_chained(pa_merge_prefill8_kernel, dim3((unsigned)merge), dim3(128), 0, st, a);
+    if (e != cudaSuccess) return cuda_failure(e, "pa_merge_prefill8_kernel launch");
     count_launches(1);
     return PA_OK;
 }

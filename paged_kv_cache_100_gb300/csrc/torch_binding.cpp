@@ -152,6 +152,16 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// `count` elements of `type` that begin at byte `at` of a byte tensor, sharing its
+// storage (one allocation for several outputs).
+at::Tensor part_of(const at::Tensor &whole, int64_t at, int64_t count, at::ScalarType type) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(),
+                                                            c10::scalarTypeToTypeMeta(type));
+    t.unsafeGetTensorImpl()->set_storage_offset(at / (int64_t)c10::elementSize(type));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous({count});
+    return t;
+}
+
 // plan_step(block_tables, context_lens, new_lens, free_blocks, num_free, token_capacity, num_blocks,
 //           out (five tensors or None), status, stream) -> tuple of five tensors
 PyObject *plan_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
@@ -187,11 +197,20 @@ PyObject *plan_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
             if (PySequence_Fast_GET_SIZE(seq) != 5) bad_value("out must be a StepPlan");
             for (int i = 0; i < 5; ++i) out[i] = tensor(PySequence_Fast_GET_ITEM(seq, i), names[i]);
         }
-        for (int i = 0; i < 5; ++i) {
+        at::Tensor whole;
+        int64_t at = 0;                  // in bytes, every part on 16
+        if (a[7] == Py_None) whole = at::empty({8 * capacity + 4 * (capacity + 2 * B + 2) + 64}, tables.options().dtype(at::kByte));
+        static const int order[5] = {2, 3, 1, 0, 4};
+        for (int i : order) {
             const at::ScalarType type = i == 2 ? at::kLong : at::kInt;
-            if (a[7] == Py_None) out[i] = at::empty({sizes[i]}, tables.options().dtype(type));
-            else if (i == 4 ? out[i].numel() != 1 : out[i].sizes() != at::IntArrayRef{sizes[i]})
+            const int64_t size = i == 2 ? 8 : 4;
+            if (a[7] == Py_None) {
+                out[i] = part_of(whole, at, sizes[i], type);
+                at = (at + sizes[i] * size + 15) & ~int64_t(15);
+            } else if (i == 4 ? out[i].numel() != 1 : out[i].sizes() != at::IntArrayRef{sizes[i]})
+                {
                 bad_value("out does not fit num_seqs and token_capacity");
+            }
             p[i] = address<void>(out[i], names[i], dev, type);
         }
         const pa_status rc =
@@ -392,10 +411,14 @@ PyObject *prefill_block_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const float scale = a[9] == Py_None ? (float)(1.0 / std::sqrt((double)p.head_dim)) : (float)number(a[9]);
         Place place(p.dev, a[14]);
         at::Tensor out = output_of(a[11], q, p.dev);
-        at::Tensor w = workspace_of(a[12], a[12] == Py_None ? f_prefill_bytes() : 0, q, p);
+        const int tokens = int_of(q.size(0), "query");
+        const size_t need = a[12] != Py_None ? 0
+                                             : f_prefill_bytes(p.num_seqs, p.hq, p.hkv, p.head_dim, p.max_blocks, tokens,
+                                                               longest, window);
+        at::Tensor w = workspace_of(a[12], need, q, p);
         const pa_status rc = call(f_prefill, out.data_ptr(), (const void *)p.query, (const void *)p.kc, (const void *)p.vc,
                                   p.ks, p.vs, p.tables, p.lens, p_start, p.num_seqs, p.hq, p.hkv, p.head_dim, (int)kBlock,
-                                  p.max_blocks, p.num_blocks, int_of(q.size(0), "query"), longest, scale, window, p.workspace,
+                                  p.max_blocks, p.num_blocks, tokens, longest, scale, window, p.workspace,
                                   p.workspace_bytes, p.status, (void *)place.at);
         if (rc != PA_OK) return PyLong_FromLong(rc);
         return THPVariable_Wrap(out);

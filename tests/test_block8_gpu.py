@@ -255,6 +255,22 @@ def test_prefill_many_items(pkv):
     _check(out[pick], ref, bound)
 
 
+@pytest.mark.parametrize("hq,hkv", [(8, 1), (4, 2)])
+@pytest.mark.parametrize("window", [0, 900])
+def test_prefill_cut_along_the_context(pkv, hq, hkv, window):
+    """Few rows over long contexts: items are cut into parts and merged, short sequences beside them not."""
+    chunks, lens = [5, 70, 3, 0, 20], [3000, 2100, 3, 17, 900]
+    p = Pool(hq + window, lens, hkv, spread=0.7)
+    need = pkv.lib().pa_prefill_block_fp8_workspace_bytes(len(lens), hq, hkv, D, p.tables.shape[1], sum(chunks), 70, window)
+    assert need > sum(chunks) * hq * D * 4 or window
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.full((need + 64,), 0xAB, dtype=torch.uint8, device="cuda")
+    q, out, rows = _prefill(pkv, p, chunks, hq, window=window, status=status, longest=70, workspace=ws[:need])
+    ref, bound = p.reference(q.double().numpy(), rows, D ** -0.5, window, floor=4.0)
+    _check(out, ref, bound, f"{hq}/{hkv}")
+    assert (ws[need:] == 0xAB).all() and int(status.item()) == 0
+
+
 def test_prefill_flags(pkv):
     from paged_kv_cache_100_gb300 import _lib
     chunks, lens = [20, 30], [60, 40]

@@ -106,9 +106,20 @@ PREFILL = dict(out=A, query=2 * A, key_cache=3 * A, value_cache=4 * A, k_scales=
     (dict(v_scales=6 * A + 1), BAD), (dict(query=2 * A + 8), BAD), (dict(tables=None), BAD), (dict(dim=64), UNSUPPORTED),
     (dict(hq=6), UNSUPPORTED), (dict(hq=64), UNSUPPORTED), (dict(num_blocks=1 << 26), UNSUPPORTED),
     (dict(workspace=None), WORKSPACE), (dict(workspace_bytes=16), WORKSPACE), (dict(workspace=10 * A + 8), WORKSPACE),
+    (dict(max_blocks=512, workspace_bytes=4096), WORKSPACE),          # cut along the context: partial outputs
     (dict(num_seqs=0, out=None), OK), (dict(tokens=0, out=None), OK), (dict(longest=0, out=None), OK)])
 def test_prefill_block_fp8_refuses(lib, over, expect):
     assert _call(lib.pa_prefill_block_fp8, PREFILL, over) == expect
+
+
+def test_prefill_block_fp8_workspace(lib):
+    f, bad = lib.pa_prefill_block_fp8_workspace_bytes, ctypes.c_size_t(-1).value
+    assert f(16, 64, 8, 128, 544, 8192, 512, 0) < 4096        # enough items: the ticket alone
+    assert f(1, 64, 8, 128, 513, 16, 16, 0) >= 16 * 64 * 2 * (128 * 4 + 8)
+    assert f(1, 64, 8, 128, 513, 16, 16, 100) < 4096          # a short window is not cut
+    for args in ((-1, 8, 2, 128, 4, 5, 5, 0), (1, 7, 2, 128, 4, 5, 5, 0), (1, 8, 2, 64, 4, 5, 5, 0),
+                 (1, 6, 2, 128, 4, 5, 5, 0), (1, 8, 2, 128, -4, 5, 5, 0), (1, 8, 2, 128, 4, 5, 5, -1)):
+        assert f(*args) == bad
 
 
 def test_rotary_turns(lib):
