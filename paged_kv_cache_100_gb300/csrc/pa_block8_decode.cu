@@ -274,8 +274,20 @@ __global__ void __launch_bounds__(NW * 32)
     idx -= b * axis;
     const int kvh = idx / a.splits;
     const int first_head = kvh * a.heads * a.splits + (idx - kvh * a.splits) * a.heads;
+    // What depends on the CTA's place alone is loaded together, so that a CTA
+    // waits one memory round trip before its first tile is requested: the length,
+    // the table entries of the warp's first blocks (a window moves the partition
+    // with the length; then the table follows it) and the query.  The scales,
+    // which follow the table, arrive while the first tiles do.  All of it is the
+    // warp's own business: no barrier before the merge.
+    const int len = a.context_lens[b];
+    const int32_t *row_table = a.block_tables + (int64_t)b * a.max_blocks;
+    const int ahead = part * a.part_blocks + warp + NW * lane;
+    int first_phys = a.window == 0 && warp + NW * lane < a.part_blocks && ahead < a.max_blocks ? row_table[ahead] : -1;
+    Warp8 state;
+    state.init(a, b, first_head, lane);
     Span w;
-    if (!span_of(a, a.context_lens[b], part, threadIdx.x == 0 && part == 0 && idx == 0, w)) return;
+    if (!span_of(a, len, part, threadIdx.x == 0 && part == 0 && idx == 0, w)) return;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -283,46 +295,50 @@ __global__ void __launch_bounds__(NW * 32)
     uint64_t *bars = reinterpret_cast<uint64_t *>(entries + a.part_blocks);
     float *s_m = reinterpret_cast<float *>(bars + NW * STAGES);
     float *s_l = s_m + NW * kHeads;
-    __shared__ int s_fail;
-    if (threadIdx.x == 0) {
-        s_fail = 0;
-        tma_prefetch_desc(&kmap);
-        tma_prefetch_desc(&vmap);
-    }
-    const int32_t *table = a.block_tables + (int64_t)b * a.max_blocks + w.blk0;
-    for (int i = threadIdx.x; i < w.nblk; i += NW * 32) {
-        int phys = table[i];
-        if ((unsigned)phys >= (unsigned)a.num_blocks) {
-            report(a.status, PA_DEV_BAD_BLOCK_ID);
-            phys = 0;
-        }
-        const int64_t at = (int64_t)phys * a.num_kv_heads + kvh;
-        const float sv = value_scale(a.v_scales[at], a.status);
-        entries[i] = Entry{(int)(at * kBlockSize), a.k_scales[at] * a.scale_log2, log2_scale(sv), 1.f / sv};
-    }
+    __shared__ int s_fail[NW];
+    const int count = w.nblk > warp ? (w.nblk - warp + NW - 1) / NW : 0;
     uint64_t *my_bars = bars + warp * STAGES;
     uint8_t *my_ring = ring + warp * STAGES * kStageBytes;
     if (lane == 0) {
+        s_fail[warp] = 0;
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
 #pragma unroll
         for (int s = 0; s < STAGES; ++s) mbar_init(&my_bars[s], 1);
         fence_mbar_init();
     }
-    __syncthreads();
-    Warp8 state;
-    state.init(a, b, first_head, lane);
+    auto entry_of = [&](int phys) {
+        if ((unsigned)phys >= (unsigned)a.num_blocks) {
+            report(a.status, PA_DEV_BAD_BLOCK_ID);
+            phys = 0;
+        }
+        return (int64_t)phys * a.num_kv_heads + kvh;
+    };
+    const int32_t *table = row_table + w.blk0 + warp;
+    if (a.window > 0) first_phys = lane < count ? table[NW * lane] : -1;
+    const int64_t first_at = lane < count ? entry_of(first_phys) : 0;
+    const int first_row = (int)(first_at * kBlockSize);
 
-    const int count = w.nblk > warp ? (w.nblk - warp + NW - 1) / NW : 0;
     const uint64_t policy = l2_policy_evict_first();     // tiles are read once: they leave L2 first
-    auto issue = [&](int it) {
+    auto issue_row = [&](int it, int row) {
         const int s = it % STAGES;
-        const int row = entries[warp + it * NW].row;
         uint8_t *kt = my_ring + s * kStageBytes;
         mbar_arrive_expect_tx(&my_bars[s], kStageBytes);
         tma_load_2d_hint(kt, &kmap, 0, row, &my_bars[s], policy);
         tma_load_2d_hint(kt + kTileBytes, &vmap, 0, row, &my_bars[s], policy);
     };
-    if (lane == 0)
-        for (int it = 0; it < STAGES && it < count; ++it) issue(it);
+    auto issue = [&](int it) { issue_row(it, entries[warp + it * NW].row); };
+#pragma unroll
+    for (int it = 0; it < STAGES; ++it) {
+        const int row = __shfl_sync(kFull, first_row, it);
+        if (lane == 0 && it < count) issue_row(it, row);
+    }
+    for (int k = lane; k < count; k += 32) {
+        const int64_t at = k == lane ? first_at : entry_of(table[NW * k]);
+        const float sv = value_scale(a.v_scales[at], a.status);
+        entries[warp + k * NW] = Entry{(int)(at * kBlockSize), a.k_scales[at] * a.scale_log2, log2_scale(sv), 1.f / sv};
+    }
+    __syncwarp();
     bool ok = true;
     int it = 0;
     for (; it < count; ++it) {
@@ -346,14 +362,17 @@ __global__ void __launch_bounds__(NW * 32)
             (void)mbar_wait_bounded(&my_bars[k % STAGES], (k / STAGES) & 1);
         if (lane == 0) {
             report(a.status, PA_DEV_TIMEOUT);
-            s_fail = 1;
+            s_fail[warp] = 1;
         }
     }
     // the ring is idle: the warps' states are merged over it
     float *acc = reinterpret_cast<float *>(my_ring);
     state.finish(a.heads, acc, s_m + warp * kHeads, s_l + warp * kHeads);
     __syncthreads();
-    if (s_fail) return;
+    bool failed = false;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) failed |= s_fail[k] != 0;
+    if (failed) return;
     const bool whole = w.nparts == 1;
     for (int i = threadIdx.x; i < a.heads * kD; i += NW * 32) {
         const int h = i / kD, d = i % kD;
@@ -379,37 +398,43 @@ __global__ void __launch_bounds__(NW * 32)
     }
 }
 
-// Merges the partitions of a (sequence, query head) row, one warp a row: a lane
-// owns four of the 128 columns, partials are read eight at a time so that their
-// latencies overlap.
-__global__ void __launch_bounds__(128) pa_merge_block8_kernel(const Block8Args a) {
+// Merges the partitions of a (sequence, query head) row, one CTA a row: warp w
+// takes partials w, w + kMergeWarps, ..., a lane four of the 128 columns, four
+// partials on their way at a time; the warps' sums meet in shared memory.  (One
+// warp a row took 16 us for the 128 partials of one 32768-token context.)
+constexpr int kMergeWarps = 4;
+__global__ void __launch_bounds__(32 * kMergeWarps) pa_merge_block8_kernel(const Block8Args a) {
+    __shared__ float4 s_acc[kMergeWarps][32];
+    __shared__ float s_sum[kMergeWarps], s_max[kMergeWarps];
     grid_dependency_wait();
     grid_dependents_launch();
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= (int64_t)a.num_seqs * a.num_q_heads) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = blockIdx.x;
     Span w;
     span_of(a, a.context_lens[row / a.num_q_heads], 0, false, w);
     if (w.nparts <= 1) return;
     const float2 *ml = a.part_ml + row * a.max_parts;
     const float4 *po = reinterpret_cast<const float4 *>(a.part_o + row * a.max_parts * kD);
-    float M = -INFINITY;
-    for (int p = lane; p < w.nparts; p += 32) M = fmaxf(M, ml[p].x);
-#pragma unroll
-    for (int k = 16; k >= 1; k >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, k));
-    float sum = 0.f;
+    float M = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p0 = 0; p0 < w.nparts; p0 += 8) {
-        float4 v[8];
-        float2 x[8];
+    for (int p0 = warp; p0 < w.nparts; p0 += 4 * kMergeWarps) {
+        float4 v[4];
+        float2 x[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const bool in = p0 + i < w.nparts;
-            v[i] = in ? po[(int64_t)(p0 + i) * 32 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
-            x[i] = in ? ml[p0 + i] : make_float2(-INFINITY, 0.f);
+        for (int i = 0; i < 4; ++i) {
+            const int p = p0 + i * kMergeWarps;
+            v[i] = p < w.nparts ? po[(int64_t)p * 32 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[i] = p < w.nparts ? ml[p] : make_float2(-INFINITY, 0.f);
         }
+        float top = M;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, x[i].x);
+        const float g = M == -INFINITY ? 0.f : exp2f(M - top);
+        M = top;
+        sum *= g;
+        acc = make_float4(acc.x * g, acc.y * g, acc.z * g, acc.w * g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
             const float f = x[i].x == -INFINITY ? 0.f : exp2f(x[i].x - M);
             sum = fmaf(f, x[i].y, sum);
             acc.x = fmaf(f, v[i].x, acc.x);
@@ -417,6 +442,28 @@ __global__ void __launch_bounds__(128) pa_merge_block8_kernel(const Block8Args a
             acc.z = fmaf(f, v[i].z, acc.z);
             acc.w = fmaf(f, v[i].w, acc.w);
         }
+    }
+    s_acc[warp][lane] = acc;
+    if (lane == 0) {
+        s_sum[warp] = sum;
+        s_max[warp] = M;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kMergeWarps; ++k) top = fmaxf(top, s_max[k]);
+    sum = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kMergeWarps; ++k) {
+        const float f = s_max[k] == -INFINITY ? 0.f : exp2f(s_max[k] - top);
+        const float4 v = s_acc[k][lane];
+        sum = fmaf(f, s_sum[k], sum);
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * kD + 4 * lane) =
@@ -587,10 +634,10 @@ extern "C" pa_status pa_decode_block_fp8(void *out, const void *query, const voi
     a.window = window;
     a.scale_log2 = scale * 1.4426950408889634f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    pa_status s = launch_decode<4, 3>(a, key_cache, value_cache, rows, st);
+    pa_status s = launch_decode<4, 2>(a, key_cache, value_cache, rows, st);
     if (s != PA_OK || p.max_parts <= 1) return s;
-    const int64_t merge = ((int64_t)num_seqs * num_q_heads + 3) / 4;
-    cudaError_t e = launch_chained(pa_merge_block8_kernel, dim3((unsigned)merge), dim3(128), 0, st, a);
+    cudaError_t e = launch_chained(pa_merge_block8_kernel, dim3((unsigned)(num_seqs * num_q_heads)),
+                                   dim3(32 * kMergeWarps), 0, st, a);
     if (e != cudaSuccess) return cuda_failure(e, "pa_merge_block8_kernel launch");
     count_launches(1);
     return PA_OK;
