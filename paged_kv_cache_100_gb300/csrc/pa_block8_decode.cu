@@ -11,6 +11,12 @@
 // and O^T[128 x 8 heads] += V^T P^T, so one pass over K/V serves the group; a
 // group of more than 8 heads is split over CTAs that follow one another and
 // find the tiles in L2.  Codes widen to f16 exactly.
+//
+// Few sequences: a context is cut into parts so that the GPU is full.  Up to
+// eight parts form a thread-block cluster, cut each context evenly and merge
+// through distributed shared memory, so that the call is one launch without
+// scratch memory; more parts (or a partition size of the caller's) leave partials
+// in the workspace for a second kernel.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -67,16 +73,35 @@ struct Span {
     int L, start, blk0, nblk, nparts;
 };
 
-// Partition `part` of a context of `len` tokens; false when it lies past the end.
-__device__ __forceinline__ bool span_of(const Block8Args &a, int len, int part, bool say, Span &w) {
+// Blocks of a context of `len` tokens: [*first, *blocks), the first position
+// attended in *start; *L the length, clamped.
+__device__ __forceinline__ void range_of(const Block8Args &a, int len, bool say, int *L, int *start, int *first,
+                                         int *blocks) {
     const int lmax = a.max_blocks * kBlockSize;
     if (len < 0 || len > lmax) {
         if (say) report(a.status, PA_DEV_BAD_CONTEXT_LEN);
         len = len < 0 ? 0 : lmax;
     }
-    w.L = len;
-    w.start = a.window > 0 && len > a.window ? len - a.window : 0;
-    const int first = w.start / kBlockSize, blocks = (len + kBlockSize - 1) / kBlockSize;
+    *L = len;
+    *start = a.window > 0 && len > a.window ? len - a.window : 0;
+    *first = *start / kBlockSize;
+    *blocks = (len + kBlockSize - 1) / kBlockSize;
+}
+
+// Part `part` of `parts` of a context, cut evenly.
+__device__ __forceinline__ void even_span(const Block8Args &a, int len, int part, int parts, bool say, Span &w) {
+    int first, blocks;
+    range_of(a, len, say, &w.L, &w.start, &first, &blocks);
+    const int n = max(blocks - first, 0);
+    w.blk0 = first + (int)((int64_t)part * n / parts);
+    w.nblk = first + (int)((int64_t)(part + 1) * n / parts) - w.blk0;
+    w.nparts = 1;
+}
+
+// Partition `part` of a context of `len` tokens; false when it lies past the end.
+__device__ __forceinline__ bool span_of(const Block8Args &a, int len, int part, bool say, Span &w) {
+    int first, blocks;
+    range_of(a, len, say, &w.L, &w.start, &first, &blocks);
     w.nparts = blocks <= first ? 1 : (blocks - first + a.part_blocks - 1) / a.part_blocks;
     if (part >= w.nparts) return false;
     w.blk0 = first + part * a.part_blocks;
@@ -257,7 +282,25 @@ struct Shape {
     }
 };
 
-template <int NW, int STAGES>
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A float of another CTA of the cluster, at the same shared-memory offset as ours.
+__device__ __forceinline__ float remote_f32(const float *mine, uint32_t rank) {
+    uint32_t addr;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(mine)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// kParts > 1: the grid's clusters of kParts CTAs each work on one (sequence, KV head).
+template <int NW, int STAGES, int kParts>
 __global__ void __launch_bounds__(NW * 32)
     pa_decode_block8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                             const Block8Args a) {
@@ -267,9 +310,14 @@ __global__ void __launch_bounds__(NW * 32)
     // CTAs go partition by partition, so that the shorter last partitions (and
     // the empty ones of short sequences) end the grid
     const int axis = a.num_kv_heads * a.splits;
-    int idx = blockIdx.x;
-    const int part = idx / (a.num_seqs * axis);
-    idx -= part * a.num_seqs * axis;
+    int idx = blockIdx.x, part;
+    if constexpr (kParts > 1) {
+        part = (int)cluster_rank();
+        idx /= kParts;
+    } else {
+        part = idx / (a.num_seqs * axis);
+        idx -= part * a.num_seqs * axis;
+    }
     const int b = idx / axis;
     idx -= b * axis;
     const int kvh = idx / a.splits;
@@ -282,12 +330,15 @@ __global__ void __launch_bounds__(NW * 32)
     // warp's own business: no barrier before the merge.
     const int len = a.context_lens[b];
     const int32_t *row_table = a.block_tables + (int64_t)b * a.max_blocks;
+    const bool early = kParts == 1 && a.window == 0;     // the partition does not move with the length
     const int ahead = part * a.part_blocks + warp + NW * lane;
-    int first_phys = a.window == 0 && warp + NW * lane < a.part_blocks && ahead < a.max_blocks ? row_table[ahead] : -1;
+    int first_phys = early && warp + NW * lane < a.part_blocks && ahead < a.max_blocks ? row_table[ahead] : -1;
     Warp8 state;
     state.init(a, b, first_head, lane);
     Span w;
-    if (!span_of(a, len, part, threadIdx.x == 0 && part == 0 && idx == 0, w)) return;
+    const bool say = threadIdx.x == 0 && part == 0 && idx == 0;
+    if constexpr (kParts > 1) even_span(a, len, part, kParts, say, w);
+    else if (!span_of(a, len, part, say, w)) return;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -315,7 +366,7 @@ __global__ void __launch_bounds__(NW * 32)
         return (int64_t)phys * a.num_kv_heads + kvh;
     };
     const int32_t *table = row_table + w.blk0 + warp;
-    if (a.window > 0) first_phys = lane < count ? table[NW * lane] : -1;
+    if (!early) first_phys = lane < count ? table[NW * lane] : -1;
     const int64_t first_at = lane < count ? entry_of(first_phys) : 0;
     const int first_row = (int)(first_at * kBlockSize);
 
@@ -372,11 +423,11 @@ __global__ void __launch_bounds__(NW * 32)
     bool failed = false;
 #pragma unroll
     for (int k = 0; k < NW; ++k) failed |= s_fail[k] != 0;
-    if (failed) return;
-    const bool whole = w.nparts == 1;
-    for (int i = threadIdx.x; i < a.heads * kD; i += NW * 32) {
-        const int h = i / kD, d = i % kD;
-        float M = -INFINITY, O = 0.f, sum = 0.f;
+    auto merged = [&](int i, float &M, float &sum) {     // element i of the CTA's state
+        const int h = i / kD;
+        float O = 0.f;
+        M = -INFINITY;
+        sum = 0.f;
 #pragma unroll
         for (int k = 0; k < NW; ++k) M = fmaxf(M, s_m[k * kHeads + h]);
 #pragma unroll
@@ -386,14 +437,69 @@ __global__ void __launch_bounds__(NW * 32)
             sum = fmaf(f, s_l[k * kHeads + h], sum);
             O = fmaf(f, reinterpret_cast<const float *>(ring + k * STAGES * kStageBytes)[i], O);
         }
-        const int64_t head = (int64_t)b * a.num_q_heads + first_head + h;
-        if (whole) {
-            // a NaN sum stays NaN; an empty context gives zeros
-            static_cast<__nv_bfloat16 *>(a.out)[head * kD + d] = __float2bfloat16_rn(sum == 0.f ? 0.f : O / sum);
-        } else {
-            const int64_t row = head * a.max_parts + part;
-            a.part_o[row * kD + d] = O;
-            if (d == 0) a.part_ml[row] = make_float2(M, sum);
+        return O;
+    };
+    const int64_t head0 = (int64_t)b * a.num_q_heads + first_head;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + head0 * kD;
+    if constexpr (kParts > 1) {
+        // The parts' states side by side in the cluster's shared memory: each CTA
+        // merges its share of the elements.  A part that gave up keeps its place at
+        // the barriers and leaves the output alone.
+        constexpr int kEach = kHeads * kD / (NW * 32);
+        float O[kEach], M[kEach], sum[kEach];
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int i = threadIdx.x + e * NW * 32;
+            if (i < a.heads * kD) O[e] = merged(i, M[e], sum[e]);
+        }
+        __syncthreads();                                 // the warps' states are read
+        float *state_o = reinterpret_cast<float *>(ring), *state_m = s_m, *state_l = s_l;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int i = threadIdx.x + e * NW * 32;
+            if (i >= a.heads * kD) continue;
+            state_o[i] = O[e];
+            if (i % kD == 0) {
+                state_m[i / kD] = M[e];
+                state_l[i / kD] = failed ? __int_as_float(0x7fffffff) : sum[e];
+            }
+        }
+        cluster_sync();
+        for (int i = (int)threadIdx.x + part * NW * 32; i < a.heads * kD; i += kParts * NW * 32) {
+            const int h = i / kD;
+            float pm[kParts], pl[kParts], po[kParts], top = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < kParts; ++r) {
+                pm[r] = remote_f32(state_m + h, r);
+                pl[r] = remote_f32(state_l + h, r);
+                po[r] = remote_f32(state_o + i, r);
+            }
+#pragma unroll
+            for (int r = 0; r < kParts; ++r) top = fmaxf(top, pm[r]);
+            float o = 0.f, l = 0.f;
+#pragma unroll
+            for (int r = 0; r < kParts; ++r) {
+                const float f = pm[r] == -INFINITY ? 0.f : exp2f(pm[r] - top);
+                l = fmaf(f, pl[r], l);
+                o = fmaf(f, po[r], o);
+            }
+            out[i] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
+        }
+        cluster_sync();                                  // no CTA leaves while its state is read
+    } else {
+        if (failed) return;
+        const bool whole = w.nparts == 1;
+        for (int i = threadIdx.x; i < a.heads * kD; i += NW * 32) {
+            float M, sum;
+            const float O = merged(i, M, sum);
+            if (whole) {
+                // a NaN sum stays NaN; an empty context gives zeros
+                out[i] = __float2bfloat16_rn(sum == 0.f ? 0.f : O / sum);
+            } else {
+                const int64_t row = (head0 + i / kD) * a.max_parts + part;
+                a.part_o[row * kD + i % kD] = O;
+                if (i % kD == 0) a.part_ml[row] = make_float2(M, sum);
+            }
         }
     }
 }
@@ -492,27 +598,41 @@ int heads_per_cta(int group) {
 
 struct Plan {
     int part_blocks, max_parts;
+    int cluster;                 // CTAs of a cluster; > 1: max_parts is 1
 };
 
-// Blocks a context can span and their partitions.  partition_size 0: the
-// longest of 4096 .. 128 tokens that gives four CTAs per SM.
+// How contexts are cut.  partition_size 0: parts enough for four CTAs per SM
+// (sequences are ragged, and a CTA's start and end overlap others' streaming),
+// none of fewer than 8 blocks, nor of more than 128, or 256 where there are CTAs
+// enough (70B-shaped batch 196 us whole, 207 in halves; eight 32768-token
+// contexts 303 us in 2048-token parts, 324 in 4096, 462 in 16384).  Up to 8 parts
+// of a small call are clusters: the GPU time is the same, the host issues one
+// launch instead of two (5 us, 8 otherwise); in larger calls clusters lose (32
+// ragged sequences 28.6 us, 26.5 with a merge kernel).
 bool plan_of(int num_seqs, int axis, int max_blocks, int window, int partition_size, Plan *p) {
     if (partition_size != 0 && (partition_size < kBlockSize || partition_size > kMaxPartition || partition_size % kBlockSize))
         return false;
     int span = max_blocks;
     if (window > 0) span = std::min(span, (window - 1) / kBlockSize + 2);
-    int size = partition_size;
-    if (size == 0) {
-        const int64_t target = 4LL * sms();
-        for (size = 4096; size > 128; size /= 2) {
-            const int64_t parts = std::max(1, (span + size / kBlockSize - 1) / (size / kBlockSize));
-            if ((int64_t)num_seqs * axis * parts >= target) break;
-        }
+    p->cluster = 1;
+    if (partition_size != 0) {
+        p->part_blocks = partition_size / kBlockSize;
+        p->max_parts = std::max(1, (span + p->part_blocks - 1) / p->part_blocks);
+        return true;
     }
-    p->part_blocks = size / kBlockSize;
-    p->max_parts = std::max(1, (span + p->part_blocks - 1) / p->part_blocks);
-    // blocks are spread evenly over the partitions of a full-length context
-    if (partition_size == 0) p->part_blocks = std::max(1, (span + p->max_parts - 1) / p->max_parts);
+    const int64_t ctas = std::max<int64_t>(1, (int64_t)num_seqs * axis), target = 4LL * sms();
+    const int most = ctas >= target ? 256 : 128;
+    int64_t parts = std::max<int64_t>((target + ctas - 1) / ctas, (span + most - 1) / most);
+    parts = std::max<int64_t>(1, std::min<int64_t>(parts, (span + 7) / 8));
+    const int cluster = parts <= 2 ? 2 : parts <= 4 ? 4 : 8;
+    if (parts > 1 && parts <= 8 && ctas * cluster <= target) {
+        p->cluster = cluster;
+        p->max_parts = 1;
+        p->part_blocks = (span + p->cluster - 1) / p->cluster + 1;
+    } else {
+        p->part_blocks = std::max(1, (int)((span + parts - 1) / parts));
+        p->max_parts = std::max(1, (span + p->part_blocks - 1) / p->part_blocks);
+    }
     return true;
 }
 
@@ -524,17 +644,29 @@ size_t workspace_of(int num_seqs, int num_q_heads, int max_parts) {
     return rows_bytes(rows) + (size_t)rows * sizeof(float2);
 }
 
-template <int NW, int STAGES>
+template <int NW, int STAGES, int kParts>
 pa_status launch_decode(const Block8Args &a, const void *kc, const void *vc, int64_t rows, cudaStream_t st) {
     CUtensorMap kmap, vmap;
     if (!encode_block8_map(&kmap, kc, rows, true) || !encode_block8_map(&vmap, vc, rows, true))
         return cuda_failure(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
     const size_t smem = Shape<NW, STAGES>::smem(a.part_blocks);
-    auto kernel = pa_decode_block8_kernel<NW, STAGES>;
+    auto kernel = pa_decode_block8_kernel<NW, STAGES, kParts>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return cuda_failure(e, "cudaFuncSetAttribute(block-scaled decode)");
-    const int64_t grid = (int64_t)a.num_seqs * a.num_kv_heads * a.splits * a.max_parts;
-    e = launch_chained(kernel, dim3((unsigned)grid), dim3(NW * 32), smem, st, kmap, vmap, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((int64_t)a.num_seqs * a.num_kv_heads * a.splits * a.max_parts * kParts));
+    cfg.blockDim = dim3(NW * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kParts;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kParts > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, kmap, vmap, a);
     if (e != cudaSuccess) return cuda_failure(e, "pa_decode_block8_kernel launch");
     count_launches(1);
     return PA_OK;
@@ -605,7 +737,7 @@ extern "C" pa_status pa_decode_block_fp8(void *out, const void *query, const voi
         return PA_ERR_INVALID_ARG;
     const int64_t rows = (int64_t)num_blocks * num_kv_heads * kBlockSize;
     if (rows >= ((int64_t)1 << 31) ||
-        (int64_t)num_seqs * num_q_heads * p.max_parts >= ((int64_t)1 << 31))
+        (int64_t)num_seqs * num_q_heads * p.max_parts * p.cluster >= ((int64_t)1 << 31))
         return PA_ERR_UNSUPPORTED;
     const size_t need = workspace_of(num_seqs, num_q_heads, p.max_parts);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace))) return PA_ERR_WORKSPACE;
@@ -634,7 +766,11 @@ extern "C" pa_status pa_decode_block_fp8(void *out, const void *query, const voi
     a.window = window;
     a.scale_log2 = scale * 1.4426950408889634f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    pa_status s = launch_decode<4, 2>(a, key_cache, value_cache, rows, st);
+    const auto launch = p.cluster == 1   ? launch_decode<4, 2, 1>
+                        : p.cluster == 2 ? launch_decode<4, 2, 2>
+                        : p.cluster == 4 ? launch_decode<4, 2, 4>
+                                         : launch_decode<4, 2, 8>;
+    pa_status s = launch(a, key_cache, value_cache, rows, st);
     if (s != PA_OK || p.max_parts <= 1) return s;
     cudaError_t e = launch_chained(pa_merge_block8_kernel, dim3((unsigned)(num_seqs * num_q_heads)),
                                    dim3(32 * kMergeWarps), 0, st, a);

@@ -67,6 +67,7 @@ struct RopeArgs {
     int whole;                       // every unit of a row is a whole vector
     int quick_tiles;                 // encode_quick's shapes (bf16 rows of 128, whole pairs in a lane)
     int tile_ctas, tile_tokens;      // CTAs that encode blocks, and the entries each looks at
+    int tile_splits;                 // CTAs that share the KV heads of the same entries
     int row_tokens, row_splits;      // tokens of a row CTA; CTAs that share a token's rows
 };
 
@@ -647,7 +648,8 @@ template <typename T>
 __device__ __forceinline__ void encode_blocks(const RopeArgs &a, int cta, float2 *table) {
     const int half = a.rotary_dim / 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t t0 = (int64_t)cta * a.tile_tokens;
+    const int split = cta % a.tile_splits;
+    const int64_t t0 = (int64_t)(cta / a.tile_splits) * a.tile_tokens;
     const int nt = (int)min((int64_t)a.tile_tokens, a.num_tokens - t0);
     const int64_t limit = (int64_t)a.num_blocks * kBlockSize;
 
@@ -657,6 +659,12 @@ __device__ __forceinline__ void encode_blocks(const RopeArgs &a, int cta, float2
     __shared__ int64_t s_blk[kMaxTile];
     __shared__ uint16_t s_list[kMaxTile][kBlockSize];
     if (threadIdx.x == 0) s_count = s_last = 0;
+    // this thread's first position and frequency, on their way while the leaders
+    // are found
+    const int t_first = half > 0 ? threadIdx.x / half : 0;
+    const bool first_in = half > 0 && t0 + t_first < a.num_tokens && t_first < nt + kWindow - 1;
+    const int32_t pos_first = first_in ? a.positions[t0 + t_first] : 0;
+    const uint64_t turns_first = first_in ? a.turns[threadIdx.x - t_first * half] : 0;
     __syncthreads();
     for (int i = warp; i < nt; i += kRopeWarps) {
         const int64_t tok = t0 + i;
@@ -697,7 +705,9 @@ __device__ __forceinline__ void encode_blocks(const RopeArgs &a, int cta, float2
     __syncthreads();
     const int leads = s_count;
     if (leads == 0) return;
-    for (int i = threadIdx.x; i < (s_last + 1) * half; i += kRopeThreads) {
+    const int pairs = (s_last + 1) * half;
+    if ((int)threadIdx.x < pairs) table[threadIdx.x] = turn_of(pos_first, turns_first, (float)a.factor);
+    for (int i = threadIdx.x + kRopeThreads; i < pairs; i += kRopeThreads) {
         const int t = i / half;
         table[i] = turn_of(a.positions[t0 + t], a.turns[i - t * half], (float)a.factor);
     }
@@ -705,7 +715,7 @@ __device__ __forceinline__ void encode_blocks(const RopeArgs &a, int cta, float2
 
     float *rows = reinterpret_cast<float *>(table + (a.tile_tokens + kWindow - 1) * half) + warp * kBlockSize * a.head_dim;
     const int per_lead = 2 * a.num_kv_heads;
-    for (int item = warp; item < leads * per_lead; item += kRopeWarps) {
+    for (int item = warp + split * kRopeWarps; item < leads * per_lead; item += kRopeWarps * a.tile_splits) {
         const int at = item / per_lead, rest = item - at * per_lead;
         Tile w;
         w.value = rest >= a.num_kv_heads;
@@ -771,7 +781,9 @@ pa_status launch_rope(RopeArgs &a, bool blocks, cudaStream_t stream) {
     size_t smem = (size_t)a.row_tokens * half * sizeof(float2);
     a.tile_ctas = 0;
     if (blocks) {
-        a.tile_ctas = (int)((n + a.tile_tokens - 1) / a.tile_tokens);
+        const int items = 2 * a.num_kv_heads;
+        a.tile_splits = (int)std::max<int64_t>(1, std::min<int64_t>((items + kRopeWarps - 1) / kRopeWarps, 4 * 152 / n));
+        a.tile_ctas = (int)((n + a.tile_tokens - 1) / a.tile_tokens * a.tile_splits);
         grid += a.tile_ctas;
         smem = std::max(smem, (size_t)(a.tile_tokens + kWindow - 1) * half * sizeof(float2) +
                                   (a.quick_tiles ? 0 : (size_t)kRopeWarps * kBlockSize * D * sizeof(float)));

@@ -169,6 +169,22 @@ def test_decode_long_context_and_given_workspace(pkv):
         assert (ws[need:] == 0xAB).all()
 
 
+@pytest.mark.parametrize("longest", [20, 250, 500, 900])
+@pytest.mark.parametrize("hq,hkv,window", [(2, 2, 0), (14, 2, 0), (6, 2, 120)])
+def test_decode_cut_into_clusters(pkv, longest, hq, hkv, window):
+    """Contexts that are cut into two, four and eight parts, and not at all."""
+    lens = [min(n + 3 * i, longest) for i in range(2) for n in LENS] + [longest]
+    p = Pool(longest + hq, lens, hkv, spread=0.7)
+    q = _query(p, len(lens), hq)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.full((16,), 0xAB, dtype=torch.uint8, device="cuda")
+    assert pkv.decode_block_fp8_workspace_bytes(len(lens), hq, hkv, D, p.tables.shape[1], 0, window) == 0
+    out = pkv.decode_block_fp8(q.cuda(), *p.device(), window=window, status=status, workspace=ws)
+    ref, bound = p.reference(q.double().numpy(), [(b, n - 1) for b, n in enumerate(lens)], D ** -0.5, window)
+    _check(out, ref, bound, f"{longest}")
+    assert int(status.item()) == 0 and (ws == 0xAB).all()
+
+
 def test_decode_graph_replay_and_streams(pkv):
     p = Pool(11, [900, 1, 2000, 64], 4)
     q = _query(p, 4, 16).cuda()
