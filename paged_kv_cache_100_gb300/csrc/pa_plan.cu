@@ -29,10 +29,7 @@
 namespace pa {
 namespace {
 
-constexpr int kPlanThreads = 256;
 constexpr int kPlanItems = 4;                       // sequences per thread and round
-constexpr int kSeqs = kPlanThreads * kPlanItems;    // sequences per round
-constexpr int kPlanWarps = kPlanThreads / 32;
 
 struct PlanArgs {
     int32_t *block_tables;
@@ -58,18 +55,23 @@ __device__ __forceinline__ int blocks_of(int tokens) {
     return (int)(((unsigned)tokens + (kBlockSize - 1)) / kBlockSize);
 }
 
+// kPlanThreads: 256 where one round of 1024 sequences holds the batch (64
+// sequences 3.1 us, 4.1 with 512), else 512 (4096 sequences 7.5 us, 8.8 with 256).
+template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) pa_plan_step_kernel(const PlanArgs a) {
-    // ends, first blocks and held tokens of the round's sequences; a sequence
-    // that is not served ends where the served ones end
-    __shared__ int s_end[kSeqs], s_new[kSeqs], s_off[kSeqs], s_len[kSeqs];
+    constexpr int kSeqs = kPlanThreads * kPlanItems, kPlanWarps = kPlanThreads / 32;
+    // ends, first blocks and held tokens of the round's sequences; one that is not
+    // served ends nowhere
+    __shared__ int s_end[kSeqs], s_off[kSeqs], s_len[kSeqs];
     __shared__ int64_t s_warp[2][kPlanWarps];
     __shared__ int s_total[2], s_used[2];           // alternate between rounds
     grid_dependency_wait();
     grid_dependents_launch();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool last = blockIdx.x + 1 == gridDim.x;  // goes through every round, and reports
     int free = *a.num_free;
     if (free < 0 || free > a.free_capacity) {
-        if (blockIdx.x == 0 && tid == 0) report(a.status, PA_DEV_BAD_BLOCK_ID);
+        if (last && tid == 0) report(a.status, PA_DEV_BAD_BLOCK_ID);
         free = free < 0 ? 0 : a.free_capacity;
     }
     const int t_lo = (int)min((int64_t)a.token_capacity, (int64_t)blockIdx.x * a.tokens_per_cta);
@@ -80,20 +82,43 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_step_kernel(const PlanAr
     if (blockIdx.x == 0 && tid == 0) a.query_start[0] = 0;
     __syncthreads();
     int round = 0;
+    // a round's lengths are loaded while the round before is worked on
+    int next_len[kPlanItems], next_add[kPlanItems];
+    static_assert(kPlanItems == 4, "one 16-byte load");
+    const bool vec = ((reinterpret_cast<uintptr_t>(a.context_lens) | reinterpret_cast<uintptr_t>(a.new_lens)) & 15u) == 0;
+    auto fetch = [&](int64_t base) {
+        const int64_t b0 = base + tid * kPlanItems;
+        if (vec && b0 + kPlanItems <= a.num_seqs) {
+            const int4 x = *reinterpret_cast<const int4 *>(a.context_lens + b0);
+            const int4 y = *reinterpret_cast<const int4 *>(a.new_lens + b0);
+            next_len[0] = x.x, next_len[1] = x.y, next_len[2] = x.z, next_len[3] = x.w;
+            next_add[0] = y.x, next_add[1] = y.y, next_add[2] = y.z, next_add[3] = y.w;
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < kPlanItems; ++j) {
+            next_len[j] = b0 + j < a.num_seqs ? a.context_lens[b0 + j] : 0;
+            next_add[j] = b0 + j < a.num_seqs ? a.new_lens[b0 + j] : 0;
+        }
+    };
+    fetch(0);
     for (int64_t base = 0; base < a.num_seqs; base += kSeqs, ++round) {
+        // a CTA whose tokens are written and that has no later round's sequences to
+        // write is done (the last one counts the free blocks that are left)
+        if (t_hi <= total && !last && (unsigned)round > blockIdx.x) return;
         int len[kPlanItems], add[kPlanItems], need[kPlanItems];
         int64_t sum_need = 0, sum_new = 0;
 #pragma unroll
         for (int j = 0; j < kPlanItems; ++j) {
-            const int64_t b = base + tid * kPlanItems + j;
-            len[j] = b < a.num_seqs ? a.context_lens[b] : 0;
-            add[j] = b < a.num_seqs ? a.new_lens[b] : 0;
+            len[j] = next_len[j];
+            add[j] = next_add[j];
         }
+        fetch(base + kSeqs);
 #pragma unroll
         for (int j = 0; j < kPlanItems; ++j) {
             if (len[j] < 0 || add[j] < 0 ||
                 (int64_t)len[j] + add[j] > (int64_t)a.max_blocks * kBlockSize) {
-                if (blockIdx.x == 0) report(a.status, PA_DEV_BAD_CONTEXT_LEN);
+                if (last) report(a.status, PA_DEV_BAD_CONTEXT_LEN);
                 add[j] = 0;
             }
             need[j] = add[j] > 0 ? blocks_of(len[j] + add[j]) - blocks_of(len[j]) : 0;
@@ -117,6 +142,7 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_step_kernel(const PlanAr
         }
         __syncthreads();
         int64_t before_need = carry_need, before_new = carry_new;
+#pragma unroll
         for (int w = 0; w < kPlanWarps; ++w) {
             const int64_t x = s_warp[0][w], y = s_warp[1][w];
             if (w < warp) {
@@ -138,7 +164,6 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_step_kernel(const PlanAr
             const int k = tid * kPlanItems + j;
             s_off[k] = served[j] ? (int)at_need : 0;
             s_len[k] = len[j];
-            s_new[k] = served[j] ? add[j] : 0;
             at_need += need[j];
             at_new += add[j];
             s_end[k] = served[j] ? (int)at_new : 0x7fffffff;
@@ -147,7 +172,7 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_step_kernel(const PlanAr
                 last_need = (int)at_need;
             }
         }
-        if (cut && blockIdx.x == 0) report(a.status, PA_DEV_NO_BLOCKS);
+        if (cut && last) report(a.status, PA_DEV_NO_BLOCKS);
         // the sums never fall, so the served prefix's totals are their maxima
         const int slot = round & 1;
         last_new = __reduce_max_sync(0xffffffffu, last_new);
@@ -161,7 +186,8 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_step_kernel(const PlanAr
         total = max(total, s_total[slot]);
         used = max(used, s_used[slot]);
         if (tid == 0) s_total[slot ^ 1] = s_used[slot ^ 1] = 0;
-        if (round % gridDim.x == blockIdx.x) {
+        // round r's sequences are written by CTA r, those past the grid by the last
+        if (blockIdx.x == min((unsigned)round, gridDim.x - 1)) {
 #pragma unroll
             for (int j = 0; j < kPlanItems; ++j) {
                 const int64_t b = base + tid * kPlanItems + j;
@@ -171,26 +197,39 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_step_kernel(const PlanAr
                 }
             }
         }
-        for (int i = max(t_lo, total_before) + tid; i < min(t_hi, total); i += kPlanThreads) {
-            int k = 0;                               // the first sequence that ends behind token i
+        // two tokens of a thread at a time: their searches and loads overlap
+        const int i_end = min(t_hi, total);
+        for (int i0 = max(t_lo, total_before) + tid; i0 < i_end; i0 += 2 * kPlanThreads) {
+            int k[2] = {0, 0}, pos[2];
+            int32_t *entry[2];
+            int32_t phys[2];
+            bool fresh[2];
 #pragma unroll
-            for (int step = kSeqs / 2; step >= 1; step >>= 1)
-                if (s_end[k + step - 1] <= i) k += step;
-            const int pos = s_len[k] + i - (s_end[k] - s_new[k]);
-            const int blk = pos / kBlockSize;
-            int32_t *entry = a.block_tables + (base + k) * a.max_blocks + blk;
-            const int have = blocks_of(s_len[k]);
-            int32_t phys;
-            if (blk >= have) {
-                phys = a.free_blocks[free - 1 - (s_off[k] + blk - have)];
-                if (pos % kBlockSize == 0) *entry = phys;
-            } else {
-                phys = *entry;
+            for (int step = kSeqs / 2; step >= 1; step >>= 1)        // the first sequence that ends behind the token
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    if (s_end[k[u] + step - 1] <= i0 + u * kPlanThreads) k[u] += step;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int i = i0 + u * kPlanThreads;
+                if (i >= i_end) continue;
+                const int len = s_len[k[u]];
+                pos[u] = len + i - (k[u] > 0 ? s_end[k[u] - 1] : total_before);
+                const int blk = pos[u] / kBlockSize, have = blocks_of(len);
+                entry[u] = a.block_tables + (base + k[u]) * a.max_blocks + blk;
+                fresh[u] = blk >= have;
+                phys[u] = fresh[u] ? a.free_blocks[free - 1 - (s_off[k[u]] + blk - have)] : *entry[u];
             }
-            const bool good = (unsigned)phys < (unsigned)a.num_blocks;
-            if (!good) report(a.status, PA_DEV_BAD_BLOCK_ID);
-            a.slot_mapping[i] = good ? (int64_t)phys * kBlockSize + pos % kBlockSize : -1;
-            a.positions[i] = pos;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int i = i0 + u * kPlanThreads;
+                if (i >= i_end) continue;
+                if (fresh[u] && pos[u] % kBlockSize == 0) *entry[u] = phys[u];
+                const bool good = (unsigned)phys[u] < (unsigned)a.num_blocks;
+                if (!good) report(a.status, PA_DEV_BAD_BLOCK_ID);
+                a.slot_mapping[i] = good ? (int64_t)phys[u] * kBlockSize + pos[u] % kBlockSize : -1;
+                a.positions[i] = pos[u];
+            }
         }
         __syncthreads();                             // the round's arrays are read
     }
@@ -198,7 +237,7 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_step_kernel(const PlanAr
         a.slot_mapping[i] = -1;
         a.positions[i] = 0;
     }
-    if (blockIdx.x == 0 && tid == 0) *a.num_free_out = free - used;
+    if (last && tid == 0) *a.num_free_out = free - used;
 }
 
 bool overlap(const void *p, size_t n, const void *q, size_t m) {
@@ -258,11 +297,15 @@ extern "C" pa_status pa_plan_step(int32_t *block_tables, const int32_t *context_
     a.num_blocks = num_blocks;
     a.free_capacity = free_capacity;
     a.token_capacity = token_capacity;
-    // one token per thread up to 128 CTAs, then longer ranges
-    const int per_thread = std::max(1, (int)(((int64_t)token_capacity + 128 * kPlanThreads - 1) / (128 * kPlanThreads)));
-    a.tokens_per_cta = per_thread * kPlanThreads;
+    const int threads = num_seqs <= 256 * kPlanItems ? 256 : 512;
+    // one token per thread up to 128 CTAs, then longer ranges: every CTA goes
+    // through the lengths, and more of them get in one another's way (216 CTAs
+    // took 10.6 us where 108 take 7.5)
+    const int per_thread = std::max(1, (int)(((int64_t)token_capacity + 128 * threads - 1) / (128 * threads)));
+    a.tokens_per_cta = per_thread * threads;
     const int grid = std::max(1, (int)(((int64_t)token_capacity + a.tokens_per_cta - 1) / a.tokens_per_cta));
-    cudaError_t e = launch_chained(pa_plan_step_kernel, dim3((unsigned)grid), dim3(kPlanThreads), 0,
+    cudaError_t e = launch_chained(threads == 256 ? pa_plan_step_kernel<256> : pa_plan_step_kernel<512>,
+                                   dim3((unsigned)grid), dim3((unsigned)threads), 0,
                                    static_cast<cudaStream_t>(stream), a);
     if (e != cudaSuccess) return cuda_failure(e, "pa_plan_step_kernel launch");
     count_launches(1);
