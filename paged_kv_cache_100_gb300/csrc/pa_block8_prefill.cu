@@ -43,6 +43,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <climits>
 #include <mutex>
 
 #include "pa_block8.cuh"
@@ -215,10 +216,18 @@ __device__ __forceinline__ float pow2_diff(float a, float b) {
 // keeps its registers; called by all lanes of a warp.
 __device__ __noinline__ float2 chunk_weights_general(uint32_t taddr, const float4 *e, float qs, float ref, int kc, int qpos,
                                                      int wlo) {
+    const int lo = wlo - kc, hi = qpos - kc;         // attended columns
+    if (__all_sync(0xffffffffu, hi < 0 || lo > 31)) {
+        // past the diagonal (or before the window) for all of the warp's rows
+        uint32_t zero[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) zero[i] = 0u;
+        tmem_st16(taddr, zero);
+        return make_float2(0.f, ref);
+    }
     uint32_t v[32];
     tmem_ld32(taddr, v);
     tmem_wait_ld();
-    const int lo = wlo - kc, hi = qpos - kc;         // attended columns
     float rmax = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
@@ -456,10 +465,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&kmap);
         tma_prefetch_desc(&vmap);
     }
-    if (warp == 2) {
-        // item order: longest first across all groups when the chunks bring more
-        // tokens than the contexts held before (causal tiles from short to long);
-        // else a group's tiles together, their K/V shared in L2
+    // Item order, where CTAs take items in turn: longest first across all groups
+    // when the chunks bring more tokens than the contexts held before (causal tiles
+    // from short to long); else a group's tiles together, their K/V shared in L2.
+    if (warp == 2 && a.work_counter != nullptr) {
         long long cached = 0, fresh = 0;
         for (int i = lane; i < a.num_seqs; i += 32) {
             const int T = a.query_start[i + 1] - a.query_start[i];
@@ -474,17 +483,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) *s_order = cached < fresh ? 1 : 0;
         if (a.num_seqs <= kPermMax) {
-            // sequences longest context first, so that the call ends on short ones
+            // sequences longest context first (ties by index), so that the call ends
+            // on short ones
+            static_assert(kPermMax == 64, "two sequences per lane");
             int *perm = reinterpret_cast<int *>(base + kOffPerm);
-            for (int i = lane; i < a.num_seqs; i += 32) {
-                const int li = a.context_lens[i];
-                int r = 0;
-                for (int j = 0; j < a.num_seqs; ++j) {
-                    const int lj = a.context_lens[j];
-                    r += (lj > li) | ((lj == li) & (j < i));
-                }
-                perm[r] = i;
+            const int l0 = lane < a.num_seqs ? a.context_lens[lane] : INT_MIN;
+            const int l1 = lane + 32 < a.num_seqs ? a.context_lens[lane + 32] : INT_MIN;
+            int r0 = 0, r1 = 0;
+            for (int j = 0; j < a.num_seqs; ++j) {
+                const int lj = __shfl_sync(0xffffffffu, j < 32 ? l0 : l1, j & 31);
+                r0 += (lj > l0) | ((lj == l0) & (j < lane));
+                r1 += (lj > l1) | ((lj == l1) & (j < lane + 32));
             }
+            if (lane < a.num_seqs) perm[r0] = lane;
+            if (lane + 32 < a.num_seqs) perm[r1] = lane + 32;
         }
     }
     if (warp == 1) tmem_alloc(tslot, kTmemCols);
@@ -492,8 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    const bool by_length = *s_order != 0;
-    const int *perm = a.num_seqs <= kPermMax ? reinterpret_cast<const int *>(base + kOffPerm) : nullptr;
+    const bool by_length = a.work_counter != nullptr && *s_order != 0;
+    const int *perm = a.work_counter != nullptr && a.num_seqs <= kPermMax ? reinterpret_cast<const int *>(base + kOffPerm) : nullptr;
 
     // the next item of a consumer role, -1 at the end (or after a wait gave up)
     auto next_item = [&](int it) -> int {
