@@ -333,6 +333,26 @@ __device__ __forceinline__ void split_query(uint8_t *tile, float *scales, int fi
     }
 }
 
+// Four lanes with four rows' chunks q of 16 bytes each, a[4 q ..]: afterwards lane
+// p holds chunk p of the four rows, a[4 i ..] that of row i.
+__device__ __forceinline__ void quad_transpose(uint32_t (&a)[16], int lane) {
+#pragma unroll
+    for (int s = 1; s <= 2; s <<= 1) {
+        const bool up = (lane & s) != 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (q & s) continue;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t send = up ? a[4 * q + k] : a[4 * (q + s) + k];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, send, s);
+                if (up) a[4 * q + k] = got;
+                else a[4 * (q + s) + k] = got;
+            }
+        }
+    }
+}
+
 // The two warps of a softmax group that hold the same 32 rows meet here.
 __device__ __forceinline__ void pair_sync(int x, int quarter) {
     asm volatile("bar.sync %0, 64;" ::"r"(5 + 4 * x + quarter) : "memory");
@@ -964,25 +984,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else if (__all_sync(0xffffffffu, ok) && drained) {
                     tc_fence_after();
                     const float inv = l_row == 0.f ? 0.f : 1.f / l_row;
-                    __nv_bfloat16 *orow =
-                        static_cast<__nv_bfloat16 *>(a.out) +
-                        ((int64_t)(d.q0 + tx0 + tr) * a.num_q_heads + d.kvh * a.group + (r % a.group)) * kD + part * kCols;
+                    // four lanes exchange their rows' chunks, so that they write 64
+                    // bytes of one row together: a lane's own row would be written in
+                    // half sectors, 32 rows at a time
+                    const int64_t out_row =
+                        real ? (int64_t)(d.q0 + tx0 + tr) * a.num_q_heads + d.kvh * a.group + (r % a.group) : -1;
+                    int64_t row[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) row[i] = __shfl_sync(0xffffffffu, out_row, (lane & ~3) + i);
+                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + part * kCols + 8 * (lane & 3);
 #pragma unroll 1
                     for (int c = 0; c < kCols; c += 32) {
-                        uint32_t o[32];
+                        uint32_t o[32], w[16];
                         tmem_ld32(o_base + c, o);
                         tmem_wait_ld();
-                        if (real) {
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                uint32_t w[4];
+                        for (int k = 0; k < 16; ++k)
+                            w[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+                        quad_transpose(w, lane);
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    w[k] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * k]) * inv,
-                                                       __uint_as_float(o[8 * q + 2 * k + 1]) * inv);
-                                *reinterpret_cast<uint4 *>(orow + c + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                        }
+                        for (int i = 0; i < 4; ++i)
+                            if (row[i] >= 0)
+                                *reinterpret_cast<uint4 *>(out + row[i] * kD + c) =
+                                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                     }
                 }
                 if (!drained) ok = false;
