@@ -452,7 +452,7 @@ pa_status pa_prefill(void *out, const void *query, const void *key_cache, const 
  * Outputs may overlap neither inputs nor one another (PA_ERR_INVALID_ARG), so a
  * captured step uses two sets of lengths and counts in turn.  Shared blocks are
  * the host manager's business: a block about to be written is private.
- * One kernel launch; all arrays are device memory.
+ * One kernel launch; all arrays are device memory.  token_capacity at most 2^30.
  */
 pa_status pa_plan_step(int32_t *block_tables, const int32_t *context_lens, const int32_t *new_lens,
                        const int32_t *free_blocks, const int32_t *num_free,
@@ -553,7 +553,8 @@ pa_status pa_rope_cache_write(void *query_out, const void *query, const void *ke
  *                    (others are clamped and flagged PA_DEV_RANGE)
  *  window            0 = the whole context; W > 0: the last W positions, as in
  *                    pa_decode_sliding_window
- *  workspace         at least pa_decode_block_fp8_workspace_bytes(...) bytes
+ *  workspace         at least pa_decode_block_fp8_workspace_bytes(...) bytes;
+ *                    calls that run at the same time need their own
  * Everything else is as in pa_decode_fp8.  Supported: head_dim 128, any group
  * (one of more than 8 query heads is split into parts of its largest divisor up
  * to 8, which read the same tiles).

@@ -452,9 +452,13 @@ def prefill(query, key_cache, value_cache, block_tables, context_lens, query_sta
     return out
 
 
-def _given(stream):
-    """Address of a given stream for the compiled binding (None: the tensors' current one)."""
-    return None if stream is None else stream.cuda_stream
+def _given(stream, t):
+    """Address of a given stream for the compiled binding (None: the current one of ``t``'s device)."""
+    if stream is None:
+        return None
+    if t.is_cuda and stream.device != t.device:
+        raise ValueError("stream must be one of the tensors' device")
+    return stream.cuda_stream
 
 
 StepPlan = collections.namedtuple("StepPlan", "context_lens query_start slot_mapping positions num_free")
@@ -470,7 +474,7 @@ def plan_step(block_tables, context_lens, new_lens, free_blocks, num_free, token
     ``block_tables`` is filled in place with blocks from the end of the free stack
     ``free_blocks[:num_free]``; ``out`` (a ``StepPlan``) receives the rest, new tensors by default."""
     r = _lib.binding().plan_step(block_tables, context_lens, new_lens, free_blocks, num_free,
-                                 token_capacity, num_blocks, out, status, _given(stream))
+                                 token_capacity, num_blocks, out, status, _given(stream, block_tables))
     if type(r) is int:
         check(r, "pa_plan_step")
     return StepPlan._make(r) if out is None else out
@@ -517,7 +521,7 @@ def rope_cache_write(query, key, value, positions, rope, key_cache, value_cache,
     turns, factor, rotary_dim, interleaved = _NO_ROPE if rope is None else rope
     r = _lib.binding().rope_cache_write(query, key, value, positions, turns, factor, rotary_dim, interleaved,
                                         key_cache, value_cache, slot_mapping, k_scales, v_scales, query_out,
-                                        status, _given(stream))
+                                        status, _given(stream, key_cache))
     if type(r) is int:
         check(r, "pa_rope_cache_write")
     return query_out if query_out is not None and query is not None else r
@@ -541,7 +545,7 @@ def decode_block_fp8(query, key_cache, value_cache, k_scales, v_scales, block_ta
     ``out`` (bf16)."""
     r = _lib.binding().decode_block_fp8(query, key_cache, value_cache, k_scales, v_scales, block_tables,
                                         context_lens, scale, window, out, partition_size, workspace, status,
-                                        _given(stream))
+                                        _given(stream, query))
     if type(r) is int:
         check(r, "pa_decode_block_fp8")
     return r if out is None else out
@@ -556,7 +560,7 @@ def prefill_block_fp8(query, key_cache, value_cache, k_scales, v_scales, block_t
         max_query_len = int((query_start[1:] - query_start[:-1]).max().item()) if query_start.numel() > 1 else 0
     r = _lib.binding().prefill_block_fp8(query, key_cache, value_cache, k_scales, v_scales, block_tables,
                                          context_lens, query_start, max_query_len, scale, window, out, workspace,
-                                         status, _given(stream))
+                                         status, _given(stream, query))
     if type(r) is int:
         check(r, "pa_prefill_block_fp8")
     return r if out is None else out

@@ -260,6 +260,7 @@ extern "C" pa_status pa_plan_step(int32_t *block_tables, const int32_t *context_
     if (num_seqs < 0 || max_blocks_per_seq < 0 || block_size != kBlockSize || num_blocks <= 0 ||
         free_capacity < 0 || token_capacity < 0 || max_blocks_per_seq > 0x7fffffff / kBlockSize)
         return PA_ERR_INVALID_ARG;
+    if (token_capacity > 1 << 30) return PA_ERR_UNSUPPORTED;   // token indexes stay within 32 bits
     if (!query_start || !num_free || !num_free_out || (num_seqs > 0 && (!context_lens || !new_lens || !context_lens_out)) ||
         (num_seqs > 0 && max_blocks_per_seq > 0 && !block_tables) || (free_capacity > 0 && !free_blocks) ||
         (token_capacity > 0 && (!slot_mapping || !positions)))

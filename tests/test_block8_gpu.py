@@ -365,3 +365,36 @@ def test_prefill_graph_and_decode_agree(pkv):
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, one)
+
+
+def test_pools_past_32_bits(pkv):
+    """A pool of more than 2^32 bytes: writes, decode and prefill at its far end."""
+    blocks, hkv, hq, n = 2_200_000, 1, 4, 70
+    kc = torch.zeros(blocks, hkv, 16, D, dtype=torch.uint8, device="cuda")
+    vc = torch.zeros_like(kc)
+    ks, vs = (torch.ones(blocks, hkv, device="cuda") for _ in range(2))
+    assert kc.numel() > 1 << 32
+    g = torch.Generator().manual_seed(1)
+    table = torch.tensor([[blocks - 1, 3, blocks - 700, blocks - 2, 5]], dtype=torch.int32)
+    x = torch.randn(n, 2 * hkv, D, generator=g).to(torch.bfloat16)
+    pos = torch.arange(n)
+    slots = table[0][pos // 16].long() * 16 + pos % 16
+    xd = x.cuda()
+    pkv.rope_cache_write(None, xd[:, :1], xd[:, 1:], None, None, kc, vc, slots.cuda(), k_scales=ks, v_scales=vs)
+    small = torch.tensor([blocks - 1, 3, blocks - 700, blocks - 2, 5])
+    kv, vv = R.decode_codes(kc[small.cuda()]), R.decode_codes(vc[small.cuda()])
+    kss, vss = ks[small.cuda()].double().cpu().numpy(), vs[small.cuda()].double().cpu().numpy()
+    for got, ref in ((kv * kss[:, :, None, None], x[:, 0]), (vv * vss[:, :, None, None], x[:, 1])):
+        rows = got[:, 0].reshape(80, D)[:n]
+        assert (np.abs(rows - ref.double().numpy()) <= 2.0 ** -4 * np.abs(ref.double().numpy()) + 2.0 ** -10 * kss.max()).all()
+    assert int(kc.view(torch.int64).count_nonzero()) <= n * D // 8        # nothing else was written
+    q = torch.randn(3, hq, D, generator=g).to(torch.bfloat16)
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    args = (kc, vc, ks, vs, table.cuda(), lens)
+    start = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    order = np.arange(5)
+    for rows, out in (([n - 1], pkv.decode_block_fp8(q[2:].cuda(), *args)), ([n - 3, n - 2, n - 1], pkv.prefill_block_fp8(q.cuda(), *args, start, 3))):
+        for i, last in enumerate(rows):
+            qq = q[2 if len(rows) == 1 else i].double().numpy()
+            ref, bound = R.attention(qq, kv[:, 0], kss[:, 0], vv[:, 0], vss[:, 0], order, 0, last + 1, D ** -0.5, floor=4.0)
+            _check(out[i], ref, bound)

@@ -44,6 +44,10 @@ def test_plan_refuses(lib, over):
     assert _call(lib.pa_plan_step, PLAN, over) == BAD
 
 
+def test_plan_refuses_a_capacity_past_its_indexes(lib):
+    assert _call(lib.pa_plan_step, PLAN, dict(token_capacity=(1 << 30) + 1, positions=1 << 40, free_out=1 << 44)) == UNSUPPORTED
+
+
 ROPE = dict(query_out=A, query=2 * A, key=3 * A, value=4 * A, positions=5 * A, turns=6 * A, factor=1.0, rotary_dim=128,
             interleaved=0, key_cache=7 * A, value_cache=8 * A, k_scales=9 * A, v_scales=10 * A, slots=11 * A, tokens=2,
             hq=8, hkv=2, dim=128, qo_stride=1024, q_stride=1024, k_stride=256, v_stride=256, block_size=16,
