@@ -599,40 +599,55 @@ int heads_per_cta(int group) {
 struct Plan {
     int part_blocks, max_parts;
     int cluster;                 // CTAs of a cluster; > 1: max_parts is 1
+    bool narrow;                 // CTAs of one warp
 };
 
 // How contexts are cut.  partition_size 0: parts enough for four CTAs per SM
 // (sequences are ragged, and a CTA's start and end overlap others' streaming),
 // none of fewer than 8 blocks, nor of more than 128, or 256 where there are CTAs
 // enough (70B-shaped batch 196 us whole, 207 in halves; eight 32768-token
-// contexts 303 us in 2048-token parts, 324 in 4096, 462 in 16384).  Up to 8 parts
-// of a small call are clusters: the GPU time is the same, the host issues one
-// launch instead of two (5 us, 8 otherwise); in larger calls clusters lose (32
-// ragged sequences 28.6 us, 26.5 with a merge kernel).
+// contexts 303 us in 2048-token parts, 324 in 4096, 462 in 16384).  With more than
+// one CTA per SM from the sequences alone, parts have 40 blocks at least, and a
+// number of CTAs that is short of four by an eighth is left (256 CTAs on 512 tokens
+// 9.6 us whole, 15.0 in 4 parts, on 2048 25.8 / 22.5 in 3; 320 CTAs on 512 10.9 /
+// 13.3 in 2, on 2048 27.5 / 26.8; 592 CTAs on 512 15.3 / 20.7, on 2048 39.9 / 43.5).
+// Up to 8 parts of a small call are clusters: the GPU time is the same, the host
+// issues one launch instead of two (5 us, 8 otherwise); in larger calls clusters
+// lose (32 ragged sequences 28.6 us, 26.5 with a merge kernel).
+//
+// Where the CTAs are more than the five of four warps that an SM holds and their
+// parts short, CTAs have one warp, 16 of which an SM holds: a short part's time is
+// its start (length, table, scales, first tiles one after another) and its end.
+// 960 CTAs on contexts of up to 64 tokens 7.5 us against 9.9, 256 tokens 15.3 /
+// 16.4, 384 tokens 19.7 / 19.1; 2048 CTAs on 256 tokens 21.7 / 25.8, 384 29.6 /
+// 31.1, 512 35.7 / 35.4, 768 50 / 46; 8192 CTAs on 64 tokens 41 / 77, 256 71 / 106,
+// 384 91 / 121; but 720 CTAs on 256 tokens 14.9 / 11.6.
 bool plan_of(int num_seqs, int axis, int max_blocks, int window, int partition_size, Plan *p) {
     if (partition_size != 0 && (partition_size < kBlockSize || partition_size > kMaxPartition || partition_size % kBlockSize))
         return false;
     int span = max_blocks;
     if (window > 0) span = std::min(span, (window - 1) / kBlockSize + 2);
     p->cluster = 1;
+    p->narrow = false;
+    const int64_t ctas = std::max<int64_t>(1, (int64_t)num_seqs * axis), target = 4LL * sms();
     if (partition_size != 0) {
         p->part_blocks = partition_size / kBlockSize;
-        p->max_parts = std::max(1, (span + p->part_blocks - 1) / p->part_blocks);
-        return true;
-    }
-    const int64_t ctas = std::max<int64_t>(1, (int64_t)num_seqs * axis), target = 4LL * sms();
-    const int most = ctas >= target ? 256 : 128;
-    int64_t parts = std::max<int64_t>((target + ctas - 1) / ctas, (span + most - 1) / most);
-    parts = std::max<int64_t>(1, std::min<int64_t>(parts, (span + 7) / 8));
-    const int cluster = parts <= 2 ? 2 : parts <= 4 ? 4 : 8;
-    if (parts > 1 && parts <= 8 && ctas * cluster <= target) {
-        p->cluster = cluster;
-        p->max_parts = 1;
-        p->part_blocks = (span + p->cluster - 1) / p->cluster + 1;
     } else {
+        const int most = ctas >= target ? 256 : 128;
+        int64_t parts = std::max<int64_t>((target - ctas / 8 + ctas - 1) / ctas, (span + most - 1) / most);
+        parts = std::max<int64_t>(1, std::min<int64_t>(parts, 4 * ctas > target ? span / 40 : (span + 7) / 8));
+        const int cluster = parts <= 2 ? 2 : parts <= 4 ? 4 : 8;
+        if (parts > 1 && parts <= 8 && ctas * cluster <= target) {
+            p->cluster = cluster;
+            p->max_parts = 1;
+            p->part_blocks = (span + p->cluster - 1) / p->cluster + 1;
+            return true;
+        }
         p->part_blocks = std::max(1, (int)((span + parts - 1) / parts));
-        p->max_parts = std::max(1, (span + p->part_blocks - 1) / p->part_blocks);
     }
+    p->max_parts = std::max(1, (span + p->part_blocks - 1) / p->part_blocks);
+    const int64_t all = ctas * p->max_parts;
+    p->narrow = p->part_blocks <= (all > 10LL * sms() ? 24 : all > 5LL * sms() ? 16 : 0);
     return true;
 }
 
@@ -766,7 +781,7 @@ extern "C" pa_status pa_decode_block_fp8(void *out, const void *query, const voi
     a.window = window;
     a.scale_log2 = scale * 1.4426950408889634f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const auto launch = p.cluster == 1   ? launch_decode<4, 2, 1>
+    const auto launch = p.cluster == 1   ? p.narrow ? launch_decode<1, 3, 1> : launch_decode<4, 2, 1>
                         : p.cluster == 2 ? launch_decode<4, 2, 2>
                         : p.cluster == 4 ? launch_decode<4, 2, 4>
                                          : launch_decode<4, 2, 8>;

@@ -185,6 +185,20 @@ def test_decode_cut_into_clusters(pkv, longest, hq, hkv, window):
     assert int(status.item()) == 0 and (ws == 0xAB).all()
 
 
+@pytest.mark.parametrize("hq,hkv,window,partition", [(16, 16, 0, 0), (48, 16, 0, 0), (16, 16, 100, 0), (32, 16, 0, 64),
+                                                     (11, 1, 30, 16)])
+def test_decode_many_short_contexts(pkv, hq, hkv, window, partition):
+    """More CTAs than the GPU holds, each with a short part: one warp per CTA."""
+    lens = [(37 * i) % 256 for i in range(110)] + [256]
+    p = Pool(hq + window + partition, lens, hkv, spread=0.7)
+    q = _query(p, len(lens), hq)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = pkv.decode_block_fp8(q.cuda(), *p.device(), window=window, status=status, partition_size=partition)
+    ref, bound = p.reference(q.double().numpy(), [(b, n - 1) for b, n in enumerate(lens)], D ** -0.5, window)
+    _check(out, ref, bound, f"{hq}/{hkv} W={window} P={partition}")
+    assert (out[0] == 0).all() and int(status.item()) == 0
+
+
 def test_decode_graph_replay_and_streams(pkv):
     p = Pool(11, [900, 1, 2000, 64], 4)
     q = _query(p, 4, 16).cuda()
