@@ -593,8 +593,8 @@ pa_status pa_decode_block_fp8(void *out, const void *query, const void *key_cach
  * exact but for elements below 2^-9 of the row's largest, which are off by at
  * most 2^-17 of it (a row with an infinite or NaN element gives NaN).  P V runs
  * on f16: codes widen exactly, weights are rounded as in
- * pa_decode_block_fp8.  A NaN value reaches every row of the 256-row tiles that
- * process its position, also rows before it.
+ * pa_decode_block_fp8.  A NaN code of V makes its element NaN in the rows that
+ * attend to its position, and in no other.
  */
 size_t pa_prefill_block_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
                                             int head_dim, int max_blocks_per_seq,

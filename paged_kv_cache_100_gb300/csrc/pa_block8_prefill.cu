@@ -31,7 +31,7 @@
 // With fewer items than SMs each is cut along its context into parts, whose
 // (reference, sum, output) a second kernel merges: a chunk of a few tokens over a
 // long context would otherwise keep one SM per KV head busy (16 tokens on 8192
-// with 8 KV heads: 123 us whole, 24 us in 16 parts).
+// with 8 KV heads: 123 us whole, 28 us in 16 parts).
 // Persistent CTAs take items from a ticket counter; barrier phases are counted
 // across items, so an item's loads start under the end of the one before.
 // Every wait is bounded (about a second); one that gives up sets PA_DEV_TIMEOUT,
@@ -91,8 +91,8 @@ constexpr int kQFull = 0, kQFree = 1, kDrain = 2, kQSplit = 3, kKFull = kQSplit 
               kVEmpty = kVConv + kVStages, kSFull = kVEmpty + kVStages, kPFull = kSFull + kQT, kPvDone = kPFull + kQT,
               kOFree = kPvDone + kQT, kItemFull = kOFree + kQT, kItemEmpty = kItemFull + 2,
               kScaleFull = kItemEmpty + 2, kNumBars = kScaleFull + kScaleSlots;
-constexpr int kOffMisc = kOffBar + kNumBars * 8;                 // TMEM slot, failure flag, item order, item queue [2]
-constexpr int kSmemBytes = kOffMisc + 32;
+constexpr int kOffMisc = kOffBar + kNumBars * 8;                 // TMEM slot, failure flag, item order, item queue [2], NaN marks [4]
+constexpr int kSmemBytes = kOffMisc + 48;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
 constexpr uint32_t kTmemCols = 512;      // S_A, S_B, O_A, O_B
@@ -139,6 +139,7 @@ struct PrefillArgs {
     const int32_t *query_start;
     const float *k_scales;
     const float *v_scales;
+    const uint8_t *value_cache;
     int32_t *status;
     int num_seqs, num_q_heads, num_kv_heads, group;
     int max_blocks, num_blocks;
@@ -262,6 +263,71 @@ __device__ __noinline__ void scale_chunk_weights(uint32_t taddr, float f0, float
 #pragma unroll
         for (int i = 0; i < 16; ++i) q[i] = pack_f16x2(f16lo(w[i]) * f, f16hi(w[i]) * f);
         tmem_st16(taddr + c, q);
+    }
+    tmem_wait_st();
+}
+
+// x + 0 * w per half: NaN once w was (w finite otherwise).
+__device__ __forceinline__ void note_nan(uint32_t &x, uint32_t w) {
+    asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(x) : "r"(w), "r"(0u));
+}
+
+// Zeroes the NaNs among a widening thread's f16 values of a V tile; true if there
+// were any (rows outside the item's range are zero already).
+template <int kRowStep>
+__device__ __noinline__ bool clear_nan(uint8_t *dst, int at0, int at1) {
+    uint32_t seen[2] = {0u, 0u};
+#pragma unroll 4
+    for (int i = 0; i < kKv / kRowStep; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(dst + i * kRowStep * 128 + at0);
+        const uint4 y = *reinterpret_cast<const uint4 *>(dst + i * kRowStep * 128 + at1);
+        note_nan(seen[0], x.x), note_nan(seen[1], x.y), note_nan(seen[0], x.z), note_nan(seen[1], x.w);
+        note_nan(seen[0], y.x), note_nan(seen[1], y.y), note_nan(seen[0], y.z), note_nan(seen[1], y.w);
+    }
+    if (((seen[0] | seen[1]) & 0x7fff7fffu) == 0u) return false;
+#pragma unroll 1
+    for (int i = 0; i < 2 * kKv / kRowStep; ++i) {
+        uint32_t *p = reinterpret_cast<uint32_t *>(dst + (i >> 1) * kRowStep * 128 + (i & 1 ? at1 : at0));
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+            uint32_t w = p[k];
+            if ((w & 0x7fffu) > 0x7c00u) w &= 0xffff0000u;
+            if ((w & 0x7fff0000u) > 0x7c000000u) w &= 0xffffu;
+            p[k] = w;
+        }
+    }
+    return true;
+}
+
+// NaN codes among the 64 columns that a thread holds of O (V's columns from
+// `column` on), at those positions of `steps` steps from block blk_lo on that its
+// row, at position qpos, attends to: these elements of O become NaN.  A whole warp.
+__device__ __noinline__ void poison_output(const PrefillArgs &a, uint32_t o_base, int b, int kvh, int column, int blk_lo,
+                                           int steps, int qpos) {
+    const int32_t *table = a.block_tables + (int64_t)b * a.max_blocks;
+    const int first = max(blk_lo * kBlockSize, a.window > 0 ? qpos + 1 - a.window : 0);
+    const int end = min(blk_lo * kBlockSize + steps * kKv, qpos + 1);
+    uint64_t mask = 0;
+#pragma unroll 1
+    for (int p = first; p < end; ++p) {
+        const int phys = table[p / kBlockSize];
+        const int64_t tile = (int64_t)((unsigned)phys < (unsigned)a.num_blocks ? phys : 0) * a.num_kv_heads + kvh;
+        const uint32_t *codes =
+            reinterpret_cast<const uint32_t *>(a.value_cache + (tile * kBlockSize + p % kBlockSize) * kD + column);
+#pragma unroll 1
+        for (int k = 0; k < kCols; ++k)
+            if (((codes[k >> 2] >> (8 * (k & 3))) & 0x7fu) == 0x7fu) mask |= 1ull << k;
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int c = 0; c < kCols; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_base + c, o);
+        tmem_wait_ld();
+        const uint32_t m = (uint32_t)(mask >> c);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = (m >> i) & 1u ? 0x7fc00000u : o[i];
+        tmem_st32(o_base + c, o);
     }
     tmem_wait_st();
 }
@@ -468,6 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *fail = reinterpret_cast<volatile int *>(base + kOffMisc + 4);
     volatile int *s_order = reinterpret_cast<volatile int *>(base + kOffMisc + 8);
     volatile int *s_item = reinterpret_cast<volatile int *>(base + kOffMisc + 16);   // [2]
+    volatile int *s_nan = reinterpret_cast<volatile int *>(base + kOffMisc + 32);    // [4]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -480,6 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars[i], n);
         }
         *fail = 0;
+        for (int i = 0; i < 4; ++i) s_nan[i] = 0;
         fence_mbar_init();
         tma_prefetch_desc(&qmap);
         tma_prefetch_desc(&kmap);
@@ -719,6 +787,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c16 = ct & 7, half = c16 >> 2, c = 2 * (c16 & 3);
         constexpr int kRowStep = kWidenThreads / 8, kBatch = 8;
         static_assert(kKv % (kRowStep * kBatch) == 0 && kRowStep % 8 == 0, "whole batches, one swizzle phase per thread");
+        // A NaN code reaches every row of the tile, as 0 * NaN those that do not attend
+        // to it.  In tiles that some row attends to in part it becomes 0 here, and the
+        // item is marked (four marks: this loop runs at most two items ahead of the
+        // softmax), so that its rows get their NaNs at the end.  (Looking for NaNs in
+        // the loop above, in every tile or in a second copy of it, cost 9 and 7 %.)
         uint32_t gstep = 0;
         bool ok = true;
         for (int it = 0;; ++it) {
@@ -800,6 +873,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<uint4 *>(row + at1) = make_uint4(0, 0, 0, 0);
                         }
                 }
+                const bool partial = k0 + kKv > d.C + d.t0 + 1 || (a.window > 0 && k0 < d.kv_hi - a.window);
+                if (partial && clear_nan<kRowStep>(dst, at0, at1)) s_nan[it & 3] = it + 1;
                 fence_proxy_async_smem();
                 mbar_arrive(&bars[kVConv + gs % kVStages]);
                 if (j + 1 < d.n_tiles) {
@@ -963,6 +1038,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pair_sync(x, quarter);
                 const float l_row = l + red[(sx * 2 + (part ^ 1)) * kRows + r];
                 const bool drained = warp_wait(&bars[kDrain], it & 1, fail, a.status);
+                if (drained && s_nan[it & 3] == it + 1) {
+                    tc_fence_after();
+                    poison_output(a, o_base, d.b, d.kvh, part * kCols, d.blk_lo, d.n_tiles, qpos);
+                }
                 if (kCut && __all_sync(0xffffffffu, ok) && drained && d.parts > 1) {
                     tc_fence_after();
                     const int64_t prow = ((int64_t)(d.q0 + tx0 + tr) * a.num_q_heads + d.kvh * a.group + (r % a.group)) *
@@ -1202,6 +1281,7 @@ extern "C" pa_status pa_prefill_block_fp8(void *out, const void *query, const vo
     a.query_start = query_start;
     a.k_scales = k_scales;
     a.v_scales = v_scales;
+    a.value_cache = static_cast<const uint8_t *>(value_cache);
     a.status = device_status;
     a.num_seqs = num_seqs;
     a.num_q_heads = num_q_heads;

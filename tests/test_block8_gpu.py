@@ -349,6 +349,33 @@ def test_prefill_queries_of_any_size(pkv):
     assert np.isfinite(got[3]).all() and int(status.item()) == 0
 
 
+@pytest.mark.parametrize("hq,hkv,window,chunks,lens", [(4, 2, 0, [300, 40], [310, 700]), (8, 1, 70, [300, 40], [310, 700]),
+                                                       (2, 2, 0, [12], [2100]), (32, 2, 900, [9], [2100]),
+                                                       (8, 8, 0, [200] * 24, [200] * 24)])
+def test_prefill_nan_values_reach_the_rows_that_attend_to_them(pkv, hq, hkv, window, chunks, lens):
+    """A NaN code of V gives NaN in its column to the rows that attend to its position, and to no other:
+    not to rows before it in its chunk, nor to rows whose window has passed it."""
+    p = Pool(hq + window, lens, hkv, spread=0.7)
+    nan = [(b, pos, h, d) for b, n in enumerate(lens)
+           for pos, h, d in ((n - 2, 0, 3), (n - chunks[b] // 2, hkv - 1, 127), (n - chunks[b], 0, 64), (n // 3, 0, 5))][:24]
+    for k, (b, pos, h, d) in enumerate(nan):
+        p.vc[p.tables[b, pos // 16], h, pos % 16, d] = 0x7F if k % 2 else 0xFF
+    q, out, rows = _prefill(pkv, p, chunks, hq, window=window)
+    want = np.zeros((len(rows), hq, D), bool)
+    group = hq // hkv
+    for i, (b, last) in enumerate(rows):
+        for bb, pos, h, d in nan:
+            if bb == b and pos <= last and (window == 0 or pos > last - window):
+                want[i, h * group:(h + 1) * group, d] = True
+    got = out.double().cpu().numpy()
+    assert want.any() and (np.isnan(got) == want).all()
+    for b, pos, h, d in nan:
+        p.vc[p.tables[b, pos // 16], h, pos % 16, d] = 0
+    ref, bound = p.reference(q.double().numpy(), rows, D ** -0.5, window, floor=4.0)
+    err = np.abs(got - ref)
+    assert (err <= bound + 2.0 ** -8 * (np.abs(ref) + bound))[~want].all()
+
+
 def test_prefill_leaves_rows_behind_the_last_sequence(pkv):
     p = Pool(8, [50], 1)
     q = _query(p, 64, 4)
