@@ -499,7 +499,8 @@ pa_status pa_rotary_turns(uint64_t *turns, double *attention_factor, int rotary_
  *                    i * stride + h * head_dim elements, so that slices of one
  *                    projection output can be passed; 16-byte aligned, strides
  *                    multiples of 16 bytes
- *  query_out         as query; may be query itself (same stride).
+ *  query_out         as query; may be query itself (same stride), else its rows
+ *                    touch no row of query, key or value (PA_ERR_INVALID_ARG).
  *                    num_q_heads 0: keys and values only
  *  positions         device int32 [num_tokens], any value
  *  turns             device uint64 [rotary_dim / 2] (pa_rotary_turns).  The

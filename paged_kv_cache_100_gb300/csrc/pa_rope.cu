@@ -755,6 +755,17 @@ __global__ void __launch_bounds__(kRopeThreads, 4) pa_rope_write_kernel(const Ro
     turn_rows<T>(a, blockIdx.x - a.tile_ctas, s_table, !kBlocks);
 }
 
+// Whether rows of w bytes, n of them s bytes apart from p, touch rows of v bytes
+// t apart from q (a slice of one buffer's rows does not touch the slice beside it;
+// with unlike strides the whole ranges count).
+bool rows_touch(const void *p, int64_t s, int64_t w, const void *q, int64_t t, int64_t v, int64_t n) {
+    const intptr_t x = reinterpret_cast<intptr_t>(p), y = reinterpret_cast<intptr_t>(q);
+    if (w == 0 || v == 0 || x >= y + (n - 1) * t + v || y >= x + (n - 1) * s + w) return false;
+    if (n == 1 || s != t) return true;
+    const int64_t r = ((y - x) % s + s) % s;         // the other row begins r behind one of ours
+    return r < w || r + v > s;
+}
+
 double ramp_index(double turns, double dim, double base, double context) {
     return dim * log(context / (turns * 2.0 * M_PI)) / (2.0 * log(base));
 }
@@ -874,7 +885,15 @@ extern "C" pa_status pa_rope_cache_write(void *query_out, const void *query, con
     if (blocks && (!k_scales || !v_scales || (reinterpret_cast<uintptr_t>(k_scales) & 3u) ||
                    (reinterpret_cast<uintptr_t>(v_scales) & 3u)))
         return PA_ERR_INVALID_ARG;
-    if (num_q_heads > 0 && query == query_out && query_stride != query_out_stride) return PA_ERR_INVALID_ARG;
+    if (num_q_heads > 0) {
+        // rows are read and written by many CTAs: query_out is query itself or apart from the inputs
+        const int64_t n = num_tokens, qs = query_stride * esize, os = query_out_stride * esize, w = q_row * esize;
+        const bool same = query == query_out && (query_stride == query_out_stride || n == 1);
+        if ((!same && rows_touch(query_out, os, w, query, qs, w, n)) ||
+            rows_touch(query_out, os, w, key, key_stride * esize, kv_row * esize, n) ||
+            rows_touch(query_out, os, w, value, value_stride * esize, kv_row * esize, n))
+            return PA_ERR_INVALID_ARG;
+    }
     // items of one CTA are counted in 32 bits
     if ((q_row + 2 * kv_row) * 16 >= ((int64_t)1 << 31)) return PA_ERR_UNSUPPORTED;
     RopeArgs a = {};

@@ -71,6 +71,14 @@ def test_rope_write_refuses(lib, over, expect):
     assert _call(lib.pa_rope_cache_write, ROPE, over) == expect
 
 
+@pytest.mark.parametrize("over", [
+    dict(query_out=2 * A + 2048), dict(query_out=2 * A - 2048), dict(query_out=2 * A + 16, q_stride=2048, qo_stride=2048),
+    dict(query_out=2 * A, qo_stride=2048), dict(query_out=3 * A), dict(query_out=4 * A + 512, v_stride=1024),
+    dict(query=2 * A, query_out=2 * A, key=2 * A + 2032, q_stride=1536, qo_stride=1536, k_stride=1536)])
+def test_rope_write_refuses_outputs_over_inputs(lib, over):
+    assert _call(lib.pa_rope_cache_write, ROPE, over) == BAD
+
+
 DECODE = dict(out=A, query=2 * A, key_cache=3 * A, value_cache=4 * A, k_scales=5 * A, v_scales=6 * A, tables=7 * A,
               lens=8 * A, num_seqs=1, hq=8, hkv=2, dim=128, block_size=16, max_blocks=4, num_blocks=8, scale=0.1, window=0,
               partition=0, workspace=None, workspace_bytes=0, status=None, stream=None)
