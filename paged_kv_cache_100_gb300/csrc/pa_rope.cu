@@ -640,6 +640,12 @@ __device__ __forceinline__ void encode_any(const RopeArgs &a, const Tile &w, flo
     __syncwarp();                                    // the rows are read
 }
 
+// cos and sin of a CTA's tokens and of those that may follow in its blocks; an even
+// number of entries, so that what lies behind them is on 16 bytes
+__host__ __device__ __forceinline__ int tile_table_entries(int tile_tokens, int half) {
+    return ((tile_tokens + kWindow - 1) * half + 1) & ~1;
+}
+
 // Blocks: a CTA takes the blocks whose first token of this call lies among its
 // tile_tokens entries; a warp takes one (block, KV head) of K or of V at a time.
 // Shared memory: cos and sin of tile_tokens + 31 tokens, then (encode_any) per
@@ -713,7 +719,7 @@ __device__ __forceinline__ void encode_blocks(const RopeArgs &a, int cta, float2
     }
     __syncthreads();
 
-    float *rows = reinterpret_cast<float *>(table + (a.tile_tokens + kWindow - 1) * half) + warp * kBlockSize * a.head_dim;
+    float *rows = reinterpret_cast<float *>(table + tile_table_entries(a.tile_tokens, half)) + warp * kBlockSize * a.head_dim;
     const int per_lead = 2 * a.num_kv_heads;
     for (int item = warp + split * kRopeWarps; item < leads * per_lead; item += kRopeWarps * a.tile_splits) {
         const int at = item / per_lead, rest = item - at * per_lead;
@@ -796,7 +802,7 @@ pa_status launch_rope(RopeArgs &a, bool blocks, cudaStream_t stream) {
         a.tile_splits = (int)std::max<int64_t>(1, std::min<int64_t>((items + kRopeWarps - 1) / kRopeWarps, 4 * 152 / n));
         a.tile_ctas = (int)((n + a.tile_tokens - 1) / a.tile_tokens * a.tile_splits);
         grid += a.tile_ctas;
-        smem = std::max(smem, (size_t)(a.tile_tokens + kWindow - 1) * half * sizeof(float2) +
+        smem = std::max(smem, (size_t)tile_table_entries(a.tile_tokens, half) * sizeof(float2) +
                                   (a.quick_tiles ? 0 : (size_t)kRopeWarps * kBlockSize * D * sizeof(float)));
     }
     if (grid >= ((int64_t)1 << 31)) return PA_ERR_UNSUPPORTED;

@@ -240,3 +240,43 @@ def test_large_batch_uses_many_tokens_per_block(pkv):
     assert torch.equal(whole, torch.cat(parts))
     for u, v in zip(a, b):
         assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("codes", [True, False])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,rot,interleaved,Hq,Hkv", [(256, 74, False, 1, 1), (128, 18, True, 3, 1), (64, 50, False, 2, 2),
+                                                      (64, 64, True, 1, 1), (128, 128, False, 3, 1), (16, 2, False, 5, 3),
+                                                      (128, 96, True, 0, 4)])
+@pytest.mark.parametrize("seqs,longest", [(2, 700), (6, 520), (130, 40), (40, 300)])
+def test_large_batches_of_any_shape(pkv, seqs, longest, D, rot, interleaved, Hq, Hkv, dtype, codes):
+    """Calls large enough that thread blocks take 2, 4, 8 and 16 tokens' blocks (and several tokens' rows),
+    in every kind of row, against calls of one sequence or part of one."""
+    rng = np.random.default_rng(seqs + D + rot)
+    slots, pos, blocks = _chunks(rng, seqs, longest)
+    T = slots.size
+    g, qkv, fk, fv = _inputs(seqs + rot, T, Hq, Hkv, D, dtype, blocks + T)
+    x = qkv.cuda()
+    rope = pkv.rotary_plan(rot, interleaved=interleaved)
+    if codes:
+        kc, ks = R.pools(g, blocks, Hkv, D)
+        pool = (kc, ks, kc, ks)
+    else:
+        kc = torch.zeros(blocks, Hkv, 16, D, dtype=dtype)
+        pool = (kc, None, kc, None)
+    a, b = [[None if t is None else t.cuda() for t in pool] for _ in range(2)]
+    p, s = torch.from_numpy(pos).cuda(), torch.from_numpy(slots).cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    run = lambda c, lo, hi: pkv.rope_cache_write(  # noqa: E731
+        x[lo:hi, :Hq] if Hq else None, x[lo:hi, Hq:Hq + Hkv], x[lo:hi, Hq + Hkv:], p[lo:hi], rope, c[0], c[2], s[lo:hi],
+        k_scales=c[1], v_scales=c[3], status=status)
+    whole = run(a, 0, T)
+    ends = [0]
+    for i in range(1, T):
+        if slots[i] // 16 != slots[i - 1] // 16 and i - ends[-1] > 150:
+            ends.append(i)
+    parts = [run(b, lo, hi) for lo, hi in zip(ends, ends[1:] + [T])]
+    if Hq:
+        assert torch.equal(whole, torch.cat(parts))
+    for u, v in zip(a, b):
+        assert u is None or torch.equal(u, v)
+    assert int(status.item()) == 0
