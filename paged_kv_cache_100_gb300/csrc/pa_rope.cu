@@ -42,7 +42,7 @@ constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
 constexpr int kWindow = 32;          // entries of slot_mapping among which a block's tokens lie
-constexpr int kMaxTile = 16;         // entries of slot_mapping whose blocks a CTA encodes
+constexpr int kMaxTile = 64;         // entries of slot_mapping whose blocks a CTA encodes
 constexpr int kMinExp = -32, kMaxExp = 31;
 // Error of a turned element in 32 bits, per |x0| + |x1|: the angle is held to
 // 2^-24 of half a turn (pi 2^-24), sincospi to 2 units of 2^-23, and three
@@ -92,7 +92,7 @@ __device__ __forceinline__ uint32_t exact_code(double y, float scale) {
     return f32x2_to_e4m3x2((float)(y / (double)scale), 0.f) & 0xffu;
 }
 
-// N consecutive elements as floats; a vector access when `whole`
+// 16 bytes of a row as floats
 template <typename T>
 struct Vec;
 template <>
@@ -128,29 +128,10 @@ __device__ __forceinline__ T from_float(float x) {
     if constexpr (sizeof(T) == 4) return x;
     else return __float2bfloat16_rn(x);
 }
-template <typename T>
-__device__ __forceinline__ void load_vec(const T *p, bool whole, int n, float (&x)[Vec<T>::N]) {
-    if (whole) {
-        Vec<T>::widen(*reinterpret_cast<const uint4 *>(p), x);
-    } else {
-#pragma unroll
-        for (int i = 0; i < Vec<T>::N; ++i) x[i] = i < n ? to_float(p[i]) : 0.f;
-    }
-}
-template <typename T>
-__device__ __forceinline__ void store_vec(T *p, bool whole, int n, const float (&x)[Vec<T>::N]) {
-    if (whole) {
-        *reinterpret_cast<uint4 *>(p) = Vec<T>::narrow(x);
-    } else {
-#pragma unroll
-        for (int i = 0; i < Vec<T>::N; ++i)
-            if (i < n) p[i] = from_float<T>(x[i]);
-    }
-}
 
-// A row is cut into units that touch nothing of one another, so that rows may
-// be turned in place: pair units (N pairs of halves, or N / 2 neighbouring
-// pairs) and units of up to N elements behind rotary_dim.
+// A row whose pieces are whole vectors is cut into units that touch nothing of one
+// another, so that rows may be turned in place: pair units (N pairs of halves, or
+// N / 2 neighbouring pairs) and units of N elements behind rotary_dim.
 template <typename T>
 __device__ __forceinline__ int pair_units(const RopeArgs &a) {
     constexpr int N = Vec<T>::N;
@@ -161,46 +142,32 @@ __device__ __forceinline__ int row_units(const RopeArgs &a) {
     return pair_units<T>(a) + (a.head_dim - a.rotary_dim + Vec<T>::N - 1) / Vec<T>::N;
 }
 
-// One unit of a row of any shape; accesses are vectors where the pieces begin on
-// 16 bytes, else single elements.
+// N elements of a row from element `at` on, a multiple of N, and in `o` the other
+// element of each one's pair (where there is one).
 template <typename T>
-__device__ __forceinline__ void turn_unit(const T *src, T *dst, int unit, int pairs, int dim, int rot,
-                                          bool interleaved, const float2 *table) {
+__device__ __forceinline__ void load_pairs(const T *row, int at, int rot, bool interleaved, float (&x)[Vec<T>::N],
+                                           float (&o)[Vec<T>::N]) {
     constexpr int N = Vec<T>::N;
-    float x[N], y[N];
-    if (unit >= pairs) {
-        const int at = rot + (unit - pairs) * N;
-        const int n = min(N, dim - at);
-        const bool whole = n == N && at % N == 0;
-        load_vec<T>(src + at, whole, n, x);
-        store_vec<T>(dst + at, whole, n, x);
-    } else if (interleaved) {
-        const int at = unit * N, n = min(N, rot - at);
-        load_vec<T>(src + at, n == N, n, x);
+    const int half = rot / 2;
+    Vec<T>::widen(*reinterpret_cast<const uint4 *>(row + at), x);
+    if (interleaved || at >= rot) {
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            const float2 cs = i < n ? table[(at + i) >> 1] : make_float2(1.f, 0.f);
-            const float x0 = x[i], x1 = x[i + 1];
-            x[i] = x0 * cs.x - x1 * cs.y;
-            x[i + 1] = x1 * cs.x + x0 * cs.y;
-        }
-        store_vec<T>(dst + at, n == N, n, x);
+        for (int i = 0; i < N; ++i) o[i] = x[i ^ 1];
+    } else if (half % N == 0) {
+        Vec<T>::widen(*reinterpret_cast<const uint4 *>(row + (at < half ? at + half : at - half)), o);
     } else {
-        const int half = rot / 2, at = unit * N;
-        const int n = min(N, half - at);
-        const bool whole = half % N == 0;
-        load_vec<T>(src + at, whole, n, x);
-        load_vec<T>(src + half + at, whole, n, y);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float2 cs = i < n ? table[at + i] : make_float2(1.f, 0.f);
-            const float x0 = x[i], x1 = y[i];
-            x[i] = x0 * cs.x - x1 * cs.y;
-            y[i] = x1 * cs.x + x0 * cs.y;
+            const int d = at + i;
+            o[i] = d < rot ? to_float(row[d < half ? d + half : d - half]) : 0.f;
         }
-        store_vec<T>(dst + at, whole, n, x);
-        store_vec<T>(dst + half + at, whole, n, y);
     }
+}
+// Element d < rot turned: x itself, o the other one of its pair.
+__device__ __forceinline__ float turned(float x, float o, int d, int half, bool interleaved, const float2 *table) {
+    const bool second = interleaved ? d & 1 : d >= half;
+    const float2 cs = table[interleaved ? d >> 1 : (second ? d - half : d)];
+    return second ? x * cs.x + o * cs.y : x * cs.x - o * cs.y;
 }
 
 // Where row `row` of token `tok` is read and written: queries, then keys, then
@@ -231,18 +198,21 @@ __device__ __forceinline__ bool row_at(const RopeArgs &a, int64_t tok, int row, 
 // Rows whose units are whole vectors.  A thread keeps one unit of the row and
 // the cos and sin of its pairs in registers while it goes through a token's
 // rows, two at a time; the loads of both are issued before either is turned.
+// Tokens of few rows are turned side by side.
 template <typename T, bool kInterleaved>
 __device__ __forceinline__ void turn_whole_rows(const RopeArgs &a, int64_t t0, int nt, int split, int rows,
                                                 const float2 *table) {
     constexpr int N = Vec<T>::N, P = kInterleaved ? N / 2 : N;
     const int half = a.rotary_dim / 2, pairs = pair_units<T>(a), units = row_units<T>(a);
     const int per_pass = kRopeThreads / units;
-    const int unit = threadIdx.x % units, first = threadIdx.x / units;
-    if (first >= per_pass) return;
+    const int unit = threadIdx.x % units, place = threadIdx.x / units;
+    const int abreast = max(1, per_pass / rows);         // tokens of a pass
+    const int t_first = abreast > 1 ? place / rows : 0, first = place - t_first * rows;
+    if (place >= per_pass || t_first >= abreast) return;
     const bool pair = unit < pairs;
     const int at = pair ? unit * N : a.rotary_dim + (unit - pairs) * N;
     const int step = per_pass * a.row_splits;
-    for (int t = 0; t < nt; ++t) {
+    for (int t = t_first; t < nt; t += abreast) {
         float2 cs[P];
         if (pair) {
             const float4 *c = reinterpret_cast<const float4 *>(table + t * half + unit * P);
@@ -299,12 +269,51 @@ __device__ __forceinline__ void turn_whole_rows(const RopeArgs &a, int64_t t0, i
     }
 }
 
+// Rows of any shape: a thread has one vector of a row, and reads the other elements
+// of its pairs where they are.  All of a row is read in one pass, so that a barrier
+// before the stores is enough to turn rows in place.
+template <typename T>
+__device__ __forceinline__ void turn_any_rows(const RopeArgs &a, int64_t t0, int nt, int split, int rows,
+                                              const float2 *table) {
+    constexpr int N = Vec<T>::N;
+    const int rot = a.rotary_dim, half = rot / 2, chunks = a.head_dim / N;
+    const int per_pass = kRopeThreads / chunks;
+    const int at = threadIdx.x % chunks * N, place = threadIdx.x / chunks;
+    const int abreast = max(1, per_pass / rows);
+    const int t_first = abreast > 1 ? place / rows : 0, first = place - t_first * rows;
+    const bool mine = place < per_pass && t_first < abreast;
+    const int turned_rows = a.num_q_heads + a.num_kv_heads;
+    const bool meet = a.query == a.query_out && !a.interleaved;
+    for (int tb = 0; tb < nt; tb += abreast) {
+        for (int rb = split * per_pass; rb < rows; rb += per_pass * a.row_splits) {
+            const int t = tb + t_first, r = rb + first;
+            const T *src;
+            T *dst;
+            float x[N], o[N];
+            const bool on = mine && t < nt && r < rows && row_at<T>(a, t0 + t, r, &src, &dst);
+            if (on) {
+                load_pairs<T>(src, at, r < turned_rows ? rot : 0, a.interleaved, x, o);
+                if (r < turned_rows && at < rot) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+                        if (at + i < rot) o[i] = turned(x[i], o[i], at + i, half, a.interleaved, table + t * half);
+                        else o[i] = x[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) o[i] = x[i];
+                }
+            }
+            if (meet) __syncthreads();
+            if (on) *reinterpret_cast<uint4 *>(dst + at) = Vec<T>::narrow(o);
+        }
+    }
+}
+
 // The rows of a CTA's tokens: queries to query_out and, with float pools, keys
 // and values to their slots.
 template <typename T>
 __device__ __forceinline__ void turn_rows(const RopeArgs &a, int cta, float2 *table, bool pools) {
-    constexpr int N = Vec<T>::N;
-    const int D = a.head_dim, rot = a.rotary_dim, half = rot / 2;
+    const int half = a.rotary_dim / 2;
     const int group = cta / a.row_splits, split = cta - group * a.row_splits;
     const int64_t t0 = (int64_t)group * a.row_tokens;
     const int nt = (int)min((int64_t)a.row_tokens, a.num_tokens - t0);
@@ -319,20 +328,7 @@ __device__ __forceinline__ void turn_rows(const RopeArgs &a, int cta, float2 *ta
         else turn_whole_rows<T, false>(a, t0, nt, split, rows, table);
         return;
     }
-    const int pairs = pair_units<T>(a), units = row_units<T>(a);
-    const int turned = a.num_q_heads + a.num_kv_heads;
-    for (int i = split * kRopeThreads + threadIdx.x; i < nt * rows * units; i += kRopeThreads * a.row_splits) {
-        const int t = i / (rows * units), row = (i - t * rows * units) / units, unit = i % units;
-        const T *src;
-        T *dst;
-        if (!row_at<T>(a, t0 + t, row, &src, &dst)) continue;
-        if (row < turned) {
-            turn_unit<T>(src, dst, unit, pairs, D, rot, a.interleaved, table + t * half);
-        } else {
-            for (int at = unit * N; at < D; at += units * N)         // rows are whole 16-byte pieces
-                *reinterpret_cast<uint4 *>(dst + at) = *reinterpret_cast<const uint4 *>(src + at);
-        }
-    }
+    turn_any_rows<T>(a, t0, nt, split, rows, table);
 }
 
 // The smallest e in [kMinExp, kMaxExp] with amax <= 448 * 2^e (448 = 1.75 * 2^8).
@@ -405,15 +401,20 @@ __device__ __noinline__ int exact_exponent(const RopeArgs &a, const Tile &w, flo
     return top <= 448.0 * (double)pow2i(e) ? e : min(e + 1, kMaxExp);
 }
 
-// The tile's scale from the maximum of the rows written: at least the old one
-// where earlier rows stay, which are then re-encoded if it grew.
+// The tile's scale from the largest magnitudes of the rows written, of turned
+// elements (to 2^-18 of it) and of others (exact): at least the old one where
+// earlier rows stay, which are then re-encoded if it grew.
 template <typename T>
-__device__ __forceinline__ float tile_scale(const RopeArgs &a, const Tile &w, float amax, float old, const float2 *table) {
+__device__ __forceinline__ float tile_scale(const RopeArgs &a, const Tile &w, float turned_max, float other_max, float old,
+                                            const float2 *table) {
     const int lane = threadIdx.x & 31, D = a.head_dim;
+    turned_max = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(turned_max)));
+    other_max = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(other_max)));
+    const float amax = fmaxf(turned_max, other_max);
     if (amax > 448.f * pow2i(kMaxExp) && lane == 0) report(a.status, PA_DEV_RANGE);
     int e = scale_exponent(amax);
-    if (!w.value && a.rotary_dim > 0 &&
-        scale_exponent(amax * (1.f - 0x1p-18f)) != scale_exponent(amax * (1.f + 0x1p-18f)))
+    if (scale_exponent(fmaxf(turned_max * (1.f - 0x1p-18f), other_max)) !=
+        scale_exponent(fmaxf(turned_max * (1.f + 0x1p-18f), other_max)))
         e = exact_exponent<T>(a, w, amax, table);
     const float scale = fmaxf(pow2i(e), old);
     if (w.low > 0 && scale != old) {
@@ -495,8 +496,7 @@ __device__ __forceinline__ void encode_quick(const RopeArgs &a, const Tile &w, f
             }
         }
     }
-    amax = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(amax)));
-    const float scale = tile_scale<__nv_bfloat16>(a, w, amax, old, table);
+    const float scale = tile_scale<__nv_bfloat16>(a, w, turned ? amax : 0.f, turned ? 0.f : amax, old, table);
     const float inv = 1.f / scale;
     const bool exact = is_pow2(scale);
     uint4 ahead = load(0);
@@ -573,83 +573,81 @@ __device__ __forceinline__ void encode_quick(const RopeArgs &a, const Tile &w, f
     }
 }
 
-// Encodes a tile of any shape: the turned rows pass through shared memory.  The
-// error of an element is bounded by that of the largest one.
+// Encodes a tile of any shape: a lane keeps its place in the rows and goes through
+// them, once for the maximum and once for the codes.
 template <typename T>
-__device__ __forceinline__ void encode_any(const RopeArgs &a, const Tile &w, float old, const float2 *table, float *rows) {
+__device__ __noinline__ void encode_any(const RopeArgs &a, const Tile &w, float old, const float2 *table) {
     constexpr int N = Vec<T>::N;
     const int lane = threadIdx.x & 31, D = a.head_dim, rot = w.value ? 0 : a.rotary_dim, half = rot / 2;
-    for (int k = 0; k < w.n; ++k) {
-        const int j = w.list[k] & 0xff;
-        const T *src = tile_row<T>(a, w, j);
-        const float2 *cs = table + (w.lead + j) * half;
-        float *row = rows + k * D;
-        for (int at = lane * N; at < D; at += 32 * N) {
-            float x[N];
-            load_vec<T>(src + at, true, N, x);
+    const int chunks = D / N, abreast = max(1, 32 / chunks), sub = chunks < 32 ? lane / chunks : 0;
+    const int first = sub < abreast ? sub : w.n;     // row
+    const int at0 = (lane - sub * chunks) * N;
+    float turned_max = 0.f, other_max = 0.f;         // fmaxf passes over NaN
+    for (int at = at0; at < D; at += 32 * N) {
+#pragma unroll 1
+        for (int k = first; k < w.n; k += abreast) {
+            const int j = w.list[k] & 0xff;
+            const float2 *cs = table + (w.lead + j) * half;
+            float x[N], o[N];
+            load_pairs<T>(tile_row<T>(a, w, j), at, rot, a.interleaved, x, o);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (at + i < rot) turned_max = fmaxf(turned_max, fabsf(turned(x[i], o[i], at + i, half, a.interleaved, cs)));
+                else other_max = fmaxf(other_max, fabsf(x[i]));
+            }
+        }
+    }
+    const float scale = tile_scale<T>(a, w, turned_max, other_max, old, table);
+    const float inv = 1.f / scale;
+    const bool exact = is_pow2(scale);
+    const float unit = kTurnError * (float)a.factor * inv;
+    for (int at = at0; at < D; at += 32 * N) {
+#pragma unroll 1
+        for (int k = first; k < w.n; k += abreast) {
+            const int j = w.list[k] & 0xff;
+            const float2 *cs = table + (w.lead + j) * half;
+            float x[N], o[N];
+            load_pairs<T>(tile_row<T>(a, w, j), at, rot, a.interleaved, x, o);
+            uint32_t lo[N / 4], hi[N / 4];
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int d = at + i;
-                int first, second, pair;
-                if (!w.value && pair_of(a, d, &first, &second, &pair)) {
-                    const float other = to_float(src[d == second ? first : second]);
-                    const float2 c = cs[pair];
-                    row[d] = d == second ? x[i] * c.x + other * c.y : x[i] * c.x - other * c.y;
+                // the codes of the value less and more its error; where they differ the code
+                // comes from 64 bits
+                if (d < rot) {
+                    const float err = (fabsf(x[i]) + fabsf(o[i])) * unit;
+                    const float y = turned(x[i], o[i], d, half, a.interleaved, cs) * inv;
+                    x[i] = y - err;
+                    o[i] = y + err;
                 } else {
-                    row[d] = x[i];
+                    x[i] = o[i] = exact ? x[i] * inv : __fdiv_rn(x[i], scale);
                 }
             }
-        }
-    }
-    __syncwarp();
-    float amax = 0.f;
-    for (int i = lane * 4; i < w.n * D; i += 128) {
-        const float4 x = *reinterpret_cast<const float4 *>(rows + i);
-        amax = fmaxf(fmaxf(fmaxf(amax, fabsf(x.x)), fmaxf(fabsf(x.y), fabsf(x.z))), fabsf(x.w));
-    }
-    amax = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(amax)));
-    const float scale = tile_scale<T>(a, w, amax, old, table);
-    const float inv = 1.f / scale;
-    const bool exact = is_pow2(scale);
-    // |x0| + |x1| of a pair is at most twice the larger of its turned elements
-    const float err = rot > 0 ? 2.f * amax * (kTurnError * inv) : 0.f;
-    for (int k = 0; k < w.n; ++k) {
-        const int j = w.list[k] & 0xff;
-        for (int c = lane * 4; c < D; c += 128) {
-            const float4 x = *reinterpret_cast<const float4 *>(rows + k * D + c);
-            float y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = exact || c + i < rot ? y[i] * inv : __fdiv_rn(y[i], scale);
-            uint32_t lo = 0, hi = 0;
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-                const float e0 = c + i < rot ? err : 0.f, e1 = c + i + 1 < rot ? err : 0.f;
-                lo |= f32x2_to_e4m3x2(y[i] - e0, y[i + 1] - e1) << (8 * i);
-                hi |= f32x2_to_e4m3x2(y[i] + e0, y[i + 1] + e1) << (8 * i);
+            for (int b = 0; b < N / 4; ++b) {
+                lo[b] = f32x2_to_e4m3x2(x[4 * b], x[4 * b + 1]) | (f32x2_to_e4m3x2(x[4 * b + 2], x[4 * b + 3]) << 16);
+                hi[b] = f32x2_to_e4m3x2(o[4 * b], o[4 * b + 1]) | (f32x2_to_e4m3x2(o[4 * b + 2], o[4 * b + 3]) << 16);
             }
-            if (lo != hi) {
-                const uint32_t was = lo ^ hi;
+#pragma unroll
+            for (int b = 0; b < N / 4; ++b) {
+                if (lo[b] == hi[b]) continue;
+                const uint32_t differ = lo[b] ^ hi[b];
 #pragma unroll 1
                 for (int i = 0; i < 4; ++i)
-                    if ((was >> (8 * i)) & 0xffu)
-                        lo = (lo & ~(0xffu << (8 * i))) | (exact_code(exact_element<T>(a, w, j, c + i), scale) << (8 * i));
+                    if ((differ >> (8 * i)) & 0xffu)
+                        lo[b] = (lo[b] & ~(0xffu << (8 * i))) |
+                                (exact_code(exact_element<T>(a, w, j, at + 4 * b + i), scale) << (8 * i));
             }
-            *reinterpret_cast<uint32_t *>(w.codes + (w.list[k] >> 8) * D + c) = lo;
+            uint8_t *out = w.codes + (w.list[k] >> 8) * D + at;
+            if constexpr (N == 8) *reinterpret_cast<uint2 *>(out) = make_uint2(lo[0], lo[1]);
+            else *reinterpret_cast<uint32_t *>(out) = lo[0];
         }
     }
-    __syncwarp();                                    // the rows are read
-}
-
-// cos and sin of a CTA's tokens and of those that may follow in its blocks; an even
-// number of entries, so that what lies behind them is on 16 bytes
-__host__ __device__ __forceinline__ int tile_table_entries(int tile_tokens, int half) {
-    return ((tile_tokens + kWindow - 1) * half + 1) & ~1;
 }
 
 // Blocks: a CTA takes the blocks whose first token of this call lies among its
 // tile_tokens entries; a warp takes one (block, KV head) of K or of V at a time.
-// Shared memory: cos and sin of tile_tokens + 31 tokens, then (encode_any) per
-// warp 16 rows of head_dim floats.
+// Shared memory: cos and sin of tile_tokens + 31 tokens.
 template <typename T>
 __device__ __forceinline__ void encode_blocks(const RopeArgs &a, int cta, float2 *table) {
     const int half = a.rotary_dim / 2;
@@ -719,7 +717,6 @@ __device__ __forceinline__ void encode_blocks(const RopeArgs &a, int cta, float2
     }
     __syncthreads();
 
-    float *rows = reinterpret_cast<float *>(table + tile_table_entries(a.tile_tokens, half)) + warp * kBlockSize * a.head_dim;
     const int per_lead = 2 * a.num_kv_heads;
     for (int item = warp + split * kRopeWarps; item < leads * per_lead; item += kRopeWarps * a.tile_splits) {
         const int at = item / per_lead, rest = item - at * per_lead;
@@ -743,7 +740,7 @@ __device__ __forceinline__ void encode_blocks(const RopeArgs &a, int cta, float2
                 continue;
             }
         }
-        encode_any<T>(a, w, old, table, rows);
+        encode_any<T>(a, w, old, table);
     }
 }
 
@@ -784,16 +781,23 @@ pa_status launch_rope(RopeArgs &a, bool blocks, cudaStream_t stream) {
     a.quick_tiles = blocks && sizeof(T) == 2 && D == 128 &&
                     (rot == 0 || (a.interleaved ? rot % 8 == 0 : rot == 128));
     const int rows = a.num_q_heads + (blocks ? 0 : 2 * a.num_kv_heads);
-    // tokens share a CTA where there are enough for four CTAs per SM; where there
-    // are fewer than SMs, CTAs share a token's rows
+    // tokens share a CTA where there are enough for four CTAs per SM, more than
+    // eight where a token has few rows; where there are fewer than SMs, CTAs share a
+    // token's rows
     const int64_t n = a.num_tokens;
+    const int units = a.whole && !a.interleaved ? (half + D - rot) / N : D / N;
+    const int most = std::max(8, std::min(32, 4096 / std::max(1, rows * units)));
     a.row_tokens = 1;
-    while (a.row_tokens < 8 && n / (2 * a.row_tokens) >= 4 * 152) a.row_tokens *= 2;
-    const int units = (a.interleaved ? (rot + N - 1) / N : (half + N - 1) / N) + (D - rot + N - 1) / N;
+    while (2 * a.row_tokens <= most && n / (2 * a.row_tokens) >= 4 * 152) a.row_tokens *= 2;
     const int passes = (rows + kRopeThreads / units - 1) / (kRopeThreads / units);
     a.row_splits = (int)std::max<int64_t>(1, std::min<int64_t>(passes, 2 * 152 / n));
+    // blocks: 16 tokens a CTA where there are enough, more where the KV heads are too
+    // few to give each warp two tiles (and the table stays within 48 KiB)
+    const int tile_most = std::min(kMaxTile, std::max(16, 16 * kRopeWarps / a.num_kv_heads));
     a.tile_tokens = 1;
-    while (a.tile_tokens < kMaxTile && n / (2 * a.tile_tokens) >= 2 * 152) a.tile_tokens *= 2;
+    while (a.tile_tokens < tile_most && n / (2 * a.tile_tokens) >= 2 * 152 &&
+           (a.tile_tokens < 8 || (2 * a.tile_tokens + kWindow - 1) * half * (int)sizeof(float2) <= 48 * 1024))
+        a.tile_tokens *= 2;
     int64_t grid = rows > 0 ? (n + a.row_tokens - 1) / a.row_tokens * a.row_splits : 0;
     size_t smem = (size_t)a.row_tokens * half * sizeof(float2);
     a.tile_ctas = 0;
@@ -802,12 +806,11 @@ pa_status launch_rope(RopeArgs &a, bool blocks, cudaStream_t stream) {
         a.tile_splits = (int)std::max<int64_t>(1, std::min<int64_t>((items + kRopeWarps - 1) / kRopeWarps, 4 * 152 / n));
         a.tile_ctas = (int)((n + a.tile_tokens - 1) / a.tile_tokens * a.tile_splits);
         grid += a.tile_ctas;
-        smem = std::max(smem, (size_t)tile_table_entries(a.tile_tokens, half) * sizeof(float2) +
-                                  (a.quick_tiles ? 0 : (size_t)kRopeWarps * kBlockSize * D * sizeof(float)));
+        smem = std::max(smem, (size_t)(a.tile_tokens + kWindow - 1) * half * sizeof(float2));
     }
     if (grid >= ((int64_t)1 << 31)) return PA_ERR_UNSUPPORTED;
     auto kernel = blocks ? pa_rope_write_kernel<T, true> : pa_rope_write_kernel<T, false>;
-    if (smem > 48 * 1024) {
+    if (smem > 44 * 1024) {                          // with the static arrays above the default limit of 48 KiB
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return cuda_failure(e, "cudaFuncSetAttribute(rope)");
     }
