@@ -65,7 +65,7 @@ struct RopeArgs {
     int interleaved;
     int num_blocks;
     int whole;                       // every unit of a row is a whole vector
-    int quick_tiles;                 // encode_quick's shapes (bf16 rows of 128, whole pairs in a lane)
+    int unit_tiles;                  // encode_units' rows: bf16, rotary_dim a multiple of 8
     int tile_ctas, tile_tokens;      // CTAs that encode blocks, and the entries each looks at
     int tile_splits;                 // CTAs that share the KV heads of the same entries
     int row_tokens, row_splits;      // tokens of a row CTA; CTAs that share a token's rows
@@ -431,25 +431,32 @@ __device__ __forceinline__ float tile_scale(const RopeArgs &a, const Tile &w, fl
 }
 __device__ __forceinline__ bool is_pow2(float x) { return (__float_as_uint(x) & 0x7fffffu) == 0; }
 
-// Encodes a tile of bf16 rows of 128: half a warp holds a row, a lane 8 of its
-// elements (kMode 1: 4 l .. and their partners 64 + 4 l ..; else 8 l ..).  The
-// rows are turned once for the maximum and, read again from L1, once more for
-// the codes.  kMode 0: not turned; 1: halves; 2: neighbours.
-template <int kMode>
-__device__ __forceinline__ void encode_quick(const RopeArgs &a, const Tile &w, float old, const float2 *table) {
-    const int lane = threadIdx.x & 31, hl = lane & 15, side = lane >> 4;
-    const int half = a.rotary_dim / 2;
-    const bool turned = kMode == 1 || (kMode == 2 && 8 * hl < a.rotary_dim);
+// Encodes a tile of bf16 rows that are cut into whole units of 8 elements (rotary_dim
+// a multiple of 8): a lane keeps its unit u and goes through the rows, 32 / units of
+// them abreast.  A unit of the turned part is 4 u .. and their partners half + 4 u ..
+// (kMode 1, halves) or 8 u .. (kMode 2, neighbours); others are 8 u .. (kMode 0: all).
+// The rows are turned once for the maximum and, read again from L1, once more for
+// the codes.  kDim: head_dim, all of which is turned (or none, kMode 0), or 0 where
+// that is not known beforehand.
+template <int kMode, int kDim>
+__device__ __forceinline__ void encode_units(const RopeArgs &a, const Tile &w, float old, const float2 *table) {
+    const int D = kDim > 0 ? kDim : a.head_dim, units = D / 8, abreast = 32 / units;
+    const int lane = threadIdx.x & 31, side = lane / units, u = lane - side * units;
+    const int half = kDim > 0 ? kDim / 2 : a.rotary_dim / 2;
+    const bool turned = kMode != 0 && (kDim > 0 || 8 * u < a.rotary_dim);
+    const int d0 = kMode == 1 && turned ? 4 * u : 8 * u, d1 = kMode == 1 && turned ? half + 4 * u : 8 * u + 4;
+    const int n = side < abreast ? w.n : 0;
+    auto row_of = [&](int i) { return abreast * i + side; };
     auto load = [&](int i) {
         uint4 r = make_uint4(0u, 0u, 0u, 0u);
-        if (2 * i + side < w.n) {
-            const __nv_bfloat16 *row = tile_row<__nv_bfloat16>(a, w, w.list[2 * i + side] & 0xff);
+        if (row_of(i) < n) {
+            const __nv_bfloat16 *row = tile_row<__nv_bfloat16>(a, w, w.list[row_of(i)] & 0xff);
             if constexpr (kMode == 1) {
-                const uint2 x = *reinterpret_cast<const uint2 *>(row + 4 * hl);
-                const uint2 y = *reinterpret_cast<const uint2 *>(row + 64 + 4 * hl);
+                const uint2 x = *reinterpret_cast<const uint2 *>(row + d0);
+                const uint2 y = *reinterpret_cast<const uint2 *>(row + d1);
                 r = make_uint4(x.x, x.y, y.x, y.y);
             } else {
-                r = *reinterpret_cast<const uint4 *>(row + 8 * hl);
+                r = *reinterpret_cast<const uint4 *>(row + d0);
             }
         }
         return r;
@@ -468,31 +475,35 @@ __device__ __forceinline__ void encode_quick(const RopeArgs &a, const Tile &w, f
             }
         }
         if (turned) {
-            const int j = 2 * i + side < w.n ? w.list[2 * i + side] & 0xff : 0;
-            const float4 *c = reinterpret_cast<const float4 *>(table + (w.lead + j) * half + 4 * hl);
+            const int j = row_of(i) < n ? w.list[row_of(i)] & 0xff : 0;
+            const float4 *c = reinterpret_cast<const float4 *>(table + (w.lead + j) * half + 4 * u);
             cs[0] = c[0];
             cs[1] = c[1];
-        } else {
-            cs[0] = cs[1] = make_float4(1.f, 0.f, 1.f, 0.f);
         }
+    };
+    // (what is not turned passes unchanged: 1 x0 - 0 x1 would not where x1 is infinite)
+    auto turn = [&](float &x0, float &x1, const float4 (&cs)[2], int k) {
+        const float c = k & 1 ? cs[k >> 1].z : cs[k >> 1].x, s = k & 1 ? cs[k >> 1].w : cs[k >> 1].y;
+        const float y = x0 * c - x1 * s;
+        x1 = turned ? x1 * c + x0 * s : x1;
+        x0 = turned ? y : x0;
     };
     float amax = 0.f;                                // fmaxf passes over NaN
 #pragma unroll 1
-    for (int b = 0; 2 * b < w.n; b += 4) {
-        uint4 raw[4];                                // eight rows on their way
+    for (int b = 0; abreast * b < w.n; b += 4) {
+        uint4 raw[4];                                // four rows of the lane on their way
 #pragma unroll
         for (int i = 0; i < 4; ++i) raw[i] = load(b + i);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (2 * (b + i) >= w.n) break;
+            if (abreast * (b + i) >= w.n) break;
             float x0[4], x1[4];
             float4 cs[2];
             pairs(b + i, raw[i], x0, x1, cs);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float c = k & 1 ? cs[k >> 1].z : cs[k >> 1].x, s = k & 1 ? cs[k >> 1].w : cs[k >> 1].y;
-                if constexpr (kMode == 0) amax = fmaxf(amax, fmaxf(fabsf(x0[k]), fabsf(x1[k])));
-                else amax = fmaxf(amax, fmaxf(fabsf(x0[k] * c - x1[k] * s), fabsf(x1[k] * c + x0[k] * s)));
+                if constexpr (kMode != 0) turn(x0[k], x1[k], cs, k);
+                amax = fmaxf(amax, fmaxf(fabsf(x0[k]), fabsf(x1[k])));
             }
         }
     }
@@ -501,19 +512,19 @@ __device__ __forceinline__ void encode_quick(const RopeArgs &a, const Tile &w, f
     const bool exact = is_pow2(scale);
     uint4 ahead = load(0);
 #pragma unroll 1
-    for (int i = 0; 2 * i < w.n; ++i) {
+    for (int i = 0; abreast * i < w.n; ++i) {
         const uint4 raw = ahead;
         ahead = load(i + 1);
         float x0[4], x1[4];
         float4 cs[2];
         pairs(i, raw, x0, x1, cs);
         uint32_t out[2];                             // codes of x0 and of x1 (mode 1), else in order
-        if constexpr (kMode == 0) {
-            if (!exact) {                            // a scale that someone else chose is divided by
+        if (!exact && !turned) {                     // a scale that someone else chose is divided by
 #pragma unroll
-                for (int k = 0; k < 4; ++k) x0[k] = __fdiv_rn(x0[k], scale), x1[k] = __fdiv_rn(x1[k], scale);
-            }
-            const float m = exact ? inv : 1.f;
+            for (int k = 0; k < 4; ++k) x0[k] = __fdiv_rn(x0[k], scale), x1[k] = __fdiv_rn(x1[k], scale);
+        }
+        const float m = exact || turned ? inv : 1.f;
+        if constexpr (kMode == 0) {
             out[0] = f32x2_to_e4m3x2(x0[0] * m, x1[0] * m) | (f32x2_to_e4m3x2(x0[1] * m, x1[1] * m) << 16);
             out[1] = f32x2_to_e4m3x2(x0[2] * m, x1[2] * m) | (f32x2_to_e4m3x2(x0[3] * m, x1[3] * m) << 16);
         } else {
@@ -522,14 +533,12 @@ __device__ __forceinline__ void encode_quick(const RopeArgs &a, const Tile &w, f
             float y0[4], y1[4], err[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float c = k & 1 ? cs[k >> 1].z : cs[k >> 1].x, s = k & 1 ? cs[k >> 1].w : cs[k >> 1].y;
-                y0[k] = (x0[k] * c - x1[k] * s) * inv;
-                y1[k] = (x1[k] * c + x0[k] * s) * inv;
-                err[k] = (fabsf(x0[k]) + fabsf(x1[k])) * (kTurnError * (float)a.factor * inv);
-                if (!turned) {
-                    err[k] = 0.f;
-                    if (!exact) y0[k] = __fdiv_rn(x0[k], scale), y1[k] = __fdiv_rn(x1[k], scale);
-                }
+                err[k] = turned ? (fabsf(x0[k]) + fabsf(x1[k])) * (kTurnError * (float)a.factor * inv) : 0.f;
+                y0[k] = x0[k];
+                y1[k] = x1[k];
+                turn(y0[k], y1[k], cs, k);
+                y0[k] *= m;
+                y1[k] *= m;
             }
             uint32_t lo[2], hi[2];
             auto code4 = [&](float p, float q, float r, float t) {
@@ -548,12 +557,12 @@ __device__ __forceinline__ void encode_quick(const RopeArgs &a, const Tile &w, f
             }
             out[0] = lo[0];
             out[1] = lo[1];
-            if (((lo[0] ^ hi[0]) | (lo[1] ^ hi[1])) != 0 && 2 * i + side < w.n) {
-                const int j = w.list[2 * i + side] & 0xff;
+            if (((lo[0] ^ hi[0]) | (lo[1] ^ hi[1])) != 0 && row_of(i) < n) {
+                const int j = w.list[row_of(i)] & 0xff;
 #pragma unroll 1
                 for (int b = 0; b < 8; ++b) {
                     if ((((lo[b >> 2] ^ hi[b >> 2]) >> (8 * (b & 3))) & 0xffu) == 0) continue;
-                    const int d = kMode == 1 ? (b >> 2) * 64 + 4 * hl + (b & 3) : 8 * hl + b;
+                    const int d = (b < 4 ? d0 : d1) + (b & 3);
                     const uint32_t c = exact_code(exact_element<__nv_bfloat16>(a, w, j, d), scale);
                     const uint32_t mask = 0xffu << (8 * (b & 3));
                     if (b < 4) out[0] = (out[0] & ~mask) | (c << (8 * (b & 3)));
@@ -561,16 +570,20 @@ __device__ __forceinline__ void encode_quick(const RopeArgs &a, const Tile &w, f
                 }
             }
         }
-        if (2 * i + side < w.n) {
-            uint8_t *row = w.codes + (w.list[2 * i + side] >> 8) * 128;
+        if (row_of(i) < n) {
+            uint8_t *row = w.codes + (w.list[row_of(i)] >> 8) * D;
             if constexpr (kMode == 1) {
-                *reinterpret_cast<uint32_t *>(row + 4 * hl) = out[0];
-                *reinterpret_cast<uint32_t *>(row + 64 + 4 * hl) = out[1];
+                *reinterpret_cast<uint32_t *>(row + d0) = out[0];
+                *reinterpret_cast<uint32_t *>(row + d1) = out[1];
             } else {
-                *reinterpret_cast<uint2 *>(row + 8 * hl) = make_uint2(out[0], out[1]);
+                *reinterpret_cast<uint2 *>(row + d0) = make_uint2(out[0], out[1]);
             }
         }
     }
+}
+template <int kMode>
+__device__ __noinline__ void encode_units_any(const RopeArgs &a, const Tile &w, float old, const float2 *table) {
+    encode_units<kMode, 0>(a, w, old, table);
 }
 
 // Encodes a tile of any shape: a lane keeps its place in the rows and goes through
@@ -733,10 +746,17 @@ __device__ __forceinline__ void encode_blocks(const RopeArgs &a, int cta, float2
         w.scale = (w.value ? a.v_scales : a.k_scales) + place;
         const float old = w.low > 0 ? *w.scale : 0.f;
         if constexpr (sizeof(T) == 2) {
-            if (a.quick_tiles) {
-                if (w.value || half == 0) encode_quick<0>(a, w, old, table);
-                else if (a.interleaved) encode_quick<2>(a, w, old, table);
-                else encode_quick<1>(a, w, old, table);
+            const int mode = w.value || half == 0 ? 0 : a.interleaved ? 2 : 1;
+            if (a.head_dim == 128 && (mode == 0 || a.rotary_dim == 128)) {
+                if (mode == 0) encode_units<0, 128>(a, w, old, table);
+                else if (mode == 1) encode_units<1, 128>(a, w, old, table);
+                else encode_units<2, 128>(a, w, old, table);
+                continue;
+            }
+            if (a.unit_tiles || w.value) {
+                if (mode == 0) encode_units_any<0>(a, w, old, table);
+                else if (mode == 1) encode_units_any<1>(a, w, old, table);
+                else encode_units_any<2>(a, w, old, table);
                 continue;
             }
         }
@@ -778,8 +798,7 @@ pa_status launch_rope(RopeArgs &a, bool blocks, cudaStream_t stream) {
     constexpr int N = 16 / (int)sizeof(T);
     const int D = a.head_dim, rot = a.rotary_dim, half = rot / 2;
     a.whole = a.interleaved ? rot % N == 0 : half % N == 0;
-    a.quick_tiles = blocks && sizeof(T) == 2 && D == 128 &&
-                    (rot == 0 || (a.interleaved ? rot % 8 == 0 : rot == 128));
+    a.unit_tiles = blocks && sizeof(T) == 2 && rot % 8 == 0;
     const int rows = a.num_q_heads + (blocks ? 0 : 2 * a.num_kv_heads);
     // tokens share a CTA where there are enough for four CTAs per SM, more than
     // eight where a token has few rows; where there are fewer than SMs, CTAs share a
