@@ -32,6 +32,13 @@
 // (reference, sum, output) a second kernel merges: a chunk of a few tokens over a
 // long context would otherwise keep one SM per KV head busy (16 tokens on 8192
 // with 8 KV heads: 123 us whole, 28 us in 16 parts).
+// 16 chunks of 512 tokens on contexts of up to 8192 with 64 query heads on 8: 940 us,
+// 1133 TFLOP/s (0.66 of the sustained 16-bit rate).  A step of 128 positions takes
+// about 3400 cycles, of which the tensor pipe is busy for 2048 (Q K^T 8-bit, both
+// halves of the query, 1024; P V 1024); the rest is the exchange between softmax and
+// MMA that two tiles in turn do not hide, and some 20000 cycles at an item's ends
+// (split of the query, first step, output).  K and V widened to f16 for a 16-bit
+// Q K^T took 1308 us.
 // Persistent CTAs take items from a ticket counter; barrier phases are counted
 // across items, so an item's loads start under the end of the one before.
 // Every wait is bounded (about a second); one that gives up sets PA_DEV_TIMEOUT,

