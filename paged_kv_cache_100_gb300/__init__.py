@@ -10,6 +10,10 @@ library's CUDA kernels.  There is no CPU fallback.
     pkv.block_copy(key_cache, value_cache, cow_pairs)
     out = pkv.decode(query, key_cache, value_cache, block_tables, context_lens)
 
+A whole step on the GPU, over E4M3 pools with one scale per block and KV head:
+``plan_step``, ``rope_cache_write`` (with a ``rotary_plan``), ``decode_block_fp8`` and
+``prefill_block_fp8``; these go through a compiled binding.
+
 Layouts: pools [num_blocks][num_kv_heads][16][head_dim]; query/out
 [num_seqs][num_q_heads][head_dim]; block_tables int32 [num_seqs][max_blocks];
 context_lens int32 [num_seqs]; new rows [num_tokens][num_kv_heads][head_dim];
