@@ -77,6 +77,7 @@ constexpr int kKStages = 3;              // K code tiles
 constexpr int kCodeStages = 2;           // V code tiles
 constexpr int kVStages = 2;              // f16 V tiles
 constexpr int kScaleSlots = 4;
+constexpr int kPartSteps = 3;            // steps of a part at least
 
 constexpr float kChunkSumMax = 32768.f;  // largest weight sum of a 32-column chunk kept as computed: f16 holds its weights
 constexpr size_t kWorkspaceBytes = 256;  // the ticket counter (rounded up)
@@ -477,7 +478,7 @@ __device__ __forceinline__ void tile_range(const PrefillArgs &a, Item &d) {
     d.blk_lo = d.kv_lo / kBlockSize;
     d.blk_hi = (d.kv_hi + kBlockSize - 1) / kBlockSize;
     d.n_tiles = (d.blk_hi - d.blk_lo + 7) / 8;
-    d.parts = min(a.splits, d.n_tiles);
+    d.parts = max(1, min(a.splits, d.n_tiles / kPartSteps));
 }
 
 template <bool kCut>
@@ -1213,22 +1214,35 @@ namespace {
 
 bool group_ok(int group) { return group == 1 || group == 2 || group == 4 || group == 8 || group == 16; }
 
-// Items of a call, and the parts they are cut into: as many as fill the SMs,
-// none shorter than four steps of a full-length context (a part costs its CTA's
-// start and end, and the merge a kernel).
+// Items of a call, and the parts they are cut into at most.  With no more items than
+// SMs it is the number with the least estimated time on full-length contexts, in
+// steps: an item costs some five beside its own (its CTA's start and end), the merge
+// kernel three and the partial outputs their traffic (a step is about 1.7 us).  10
+// chunks of up to 9 tokens on up to 5712 with 8 heads, 80 items: 64 us in 3 parts, 83
+// whole.  More items than SMs are left whole: they differ in length, and tickets even
+// that out (272 items of 2 chunks of up to 526 tokens: 157 us, 183 in 2 parts; 228 of
+// two of up to 1817: 91 / 118).
 struct Cut {
     int64_t tiles, items;
     int splits;
 };
-Cut cut_of(int num_seqs, int num_q_heads, int num_kv_heads, int max_blocks, int window, int max_query_len) {
+Cut cut_of(int num_seqs, int num_q_heads, int num_kv_heads, int max_blocks, int window, int num_query_tokens,
+           int max_query_len) {
     Cut c;
     const int group = num_q_heads / num_kv_heads;
     c.tiles = ((int64_t)max_query_len * group + kQT * kRows - 1) / (kQT * kRows);
     c.items = c.tiles * num_kv_heads * num_seqs;
+    c.splits = 1;
     int64_t blocks = max_blocks;
     if (window > 0) blocks = std::min<int64_t>(blocks, ((int64_t)window + kQT * kRows / group) / kBlockSize + 2);
-    const int64_t steps = (blocks + 7) / 8;
-    c.splits = c.items > 0 ? (int)std::max<int64_t>(1, std::min<int64_t>(sms() / c.items, steps / 4)) : 1;
+    const int64_t steps = (blocks + 7) / 8, n = sms();
+    if (c.items == 0 || c.items > n) return c;
+    const double row_steps = 2. * (kD * sizeof(float) + sizeof(float2)) * num_query_tokens * num_q_heads / 6.0e6 / 1.7;
+    double best = 1e300;
+    for (int64_t k = 1; k == 1 || (k <= 64 && k <= steps / kPartSteps); ++k) {
+        const double cost = (double)((c.items * k + n - 1) / n * (5 + (steps + k - 1) / k)) + (k > 1 ? 3. + k * row_steps : 0.);
+        if (cost < best) best = cost, c.splits = (int)k;
+    }
     return c;
 }
 size_t part_rows_bytes(int64_t rows) { return (size_t)rows * kD * sizeof(float); }
@@ -1242,10 +1256,10 @@ extern "C" size_t pa_prefill_block_fp8_workspace_bytes(int num_seqs, int num_q_h
         !group_ok(num_q_heads / num_kv_heads) || max_blocks_per_seq < 0 ||
         max_blocks_per_seq > 0x7fffffff / kBlockSize || num_query_tokens < 0 || max_query_len < 0 || window < 0)
         return (size_t)-1;
-    const Cut c = cut_of(num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq, window, max_query_len);
+    const Cut c = cut_of(num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq, window, num_query_tokens, max_query_len);
     if (c.splits <= 1) return kWorkspaceBytes;
     const int64_t rows = (int64_t)num_query_tokens * num_q_heads * c.splits;
-    return part_rows_bytes(rows) + (size_t)rows * sizeof(float2);
+    return kWorkspaceBytes + part_rows_bytes(rows) + (size_t)rows * sizeof(float2);
 }
 
 extern "C" pa_status pa_prefill_block_fp8(void *out, const void *query, const void *key_cache, const void *value_cache,
@@ -1274,7 +1288,7 @@ extern "C" pa_status pa_prefill_block_fp8(void *out, const void *query, const vo
                                                              max_blocks_per_seq, num_query_tokens, max_query_len, window);
     if (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)) return PA_ERR_WORKSPACE;
     const int64_t rows = (int64_t)num_blocks * num_kv_heads * kBlockSize;
-    const Cut cut = cut_of(num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq, window, max_query_len);
+    const Cut cut = cut_of(num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq, window, num_query_tokens, max_query_len);
     const int64_t items = cut.items * cut.splits;
     if (rows >= ((int64_t)1 << 31) || items >= ((int64_t)1 << 31) - kThreads) return PA_ERR_UNSUPPORTED;
     CUtensorMap qmap, kmap, vmap;
@@ -1307,10 +1321,11 @@ extern "C" pa_status pa_prefill_block_fp8(void *out, const void *query, const vo
     const int64_t grid = std::min<int64_t>(items, sms());
     cudaError_t e;
     if (cut.splits > 1) {
-        a.part_o = static_cast<float *>(workspace);
-        a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) +
+        a.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kWorkspaceBytes);
+        a.part_ml = reinterpret_cast<float2 *>(reinterpret_cast<uint8_t *>(a.part_o) +
                                                part_rows_bytes((int64_t)num_query_tokens * num_q_heads * cut.splits));
-    } else if (items > grid) {
+    }
+    if (items > grid) {
         a.work_counter = static_cast<unsigned int *>(workspace);
         e = cudaMemsetAsync(workspace, 0, sizeof(unsigned int), st);
         if (e != cudaSuccess) return cuda_failure(e, "cudaMemsetAsync(prefill ticket)");

@@ -301,6 +301,22 @@ def test_prefill_cut_along_the_context(pkv, hq, hkv, window):
     assert (ws[need:] == 0xAB).all() and int(status.item()) == 0
 
 
+def test_prefill_cut_into_more_parts_than_sms(pkv):
+    """80 items of which the long ones are cut in three: CTAs take several parts each, by ticket."""
+    lens = [6000, 3000, 1500] + [20 + 37 * i for i in range(37)]
+    chunks = [1 + i % 7 for i in range(40)]
+    p = Pool(21, lens, 2, spread=0.7)
+    need = pkv.lib().pa_prefill_block_fp8_workspace_bytes(len(lens), 4, 2, D, p.tables.shape[1], sum(chunks), 7, 0)
+    assert need > 2 * sum(chunks) * 4 * D * 4
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.full((need + 64,), 0xAB, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        q, out, rows = _prefill(pkv, p, chunks, 4, status=status, longest=7, workspace=ws[:need])
+        ref, bound = p.reference(q.double().numpy(), rows, D ** -0.5, floor=4.0)
+        _check(out, ref, bound)
+    assert (ws[need:] == 0xAB).all() and int(status.item()) == 0
+
+
 def test_prefill_flags(pkv):
     from paged_kv_cache_100_gb300 import _lib
     chunks, lens = [20, 30], [60, 40]
