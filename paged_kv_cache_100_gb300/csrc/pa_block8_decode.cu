@@ -617,6 +617,12 @@ struct Plan {
 // number of CTAs that is short of four by an eighth is left (256 CTAs on 512 tokens
 // 9.6 us whole, 15.0 in 4 parts, on 2048 25.8 / 22.5 in 3; 320 CTAs on 512 10.9 /
 // 13.3 in 2, on 2048 27.5 / 26.8; 592 CTAs on 512 15.3 / 20.7, on 2048 39.9 / 43.5).
+// The parts follow the table's width, as only the GPU knows the lengths, and a wide
+// table's last parts are often empty: a grid beyond 32 CTAs per SM is made of the
+// largest parts only (tables of 8192 entries: 64 7B-shaped contexts 106 us, 178 in
+// 4096-token parts; 1024 contexts of up to 64 tokens with 8 KV heads 267 / 621, 41
+// with tables of their size).  Parts cut by each context's own length, or taken in
+// stretches by a loop in the kernel, cost 5 to 12 % where the table fits.
 // Up to 8 parts of a small call are clusters: the GPU time is the same, the host
 // issues one launch instead of two (5 us, 8 otherwise); in larger calls clusters
 // lose (32 ragged sequences 28.6 us, 26.5 with a merge kernel).
@@ -649,6 +655,9 @@ bool plan_of(int num_seqs, int axis, int max_blocks, int window, int partition_s
             p->part_blocks = (span + p->cluster - 1) / p->cluster + 1;
             return true;
         }
+        const int largest = kMaxPartition / kBlockSize;
+        parts = std::min(parts, std::max<int64_t>(std::max<int64_t>((target + ctas - 1) / ctas, 8 * target / ctas),
+                                                  (span + largest - 1) / largest));
         p->part_blocks = std::max(1, (int)((span + parts - 1) / parts));
     }
     p->max_parts = std::max(1, (span + p->part_blocks - 1) / p->part_blocks);
