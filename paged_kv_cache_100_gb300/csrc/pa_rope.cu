@@ -21,7 +21,7 @@
 // codes that become subnormal).
 // A key's code is that of its exact rotation rounded to f32: an element whose
 // 32-bit value lies so near a border of two codes that its error could cross it
-// (about one in 10^5) is computed again in 64 bits, and so is the largest
+// (about one in 7000) is computed again in 64 bits, and so is the largest
 // magnitude when it lies next to a scale's border.
 //
 // The kernel moves bytes: a launch has CTAs that turn rows (queries; keys and
