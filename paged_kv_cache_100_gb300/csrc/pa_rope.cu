@@ -275,6 +275,99 @@ __device__ __forceinline__ void turn_whole_rows(const RopeArgs &a, int64_t t0, i
     }
 }
 
+__device__ __forceinline__ void copy_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// The same for CTAs that turn several tokens into float pools: a thread's loads go
+// kAhead - 1 rows ahead into places of its own in shared memory (nothing is shared,
+// so nothing waits but the thread for its own copies), as registers do not hold
+// that many.  27832 tokens of 8 f32 heads of 128 44.5 us against 57.7, 8192 tokens
+// of 80 bf16 heads 56.6 / 60.3, of 80 f32 heads 106.2 / 104.8; one token a CTA 0.3
+// us slower; beside CTAs that encode blocks, which wait longer then, 67.2 / 65.7; 4
+// or 6 rows ahead 44.3 and 47.4 us.
+constexpr int kAhead = 3;
+template <typename T, bool kInterleaved>
+__device__ __forceinline__ void turn_many_rows(const RopeArgs &a, int64_t t0, int nt, int split, int rows,
+                                               const float2 *table, uint4 *places) {
+    constexpr int N = Vec<T>::N, P = kInterleaved ? N / 2 : N;
+    const int half = a.rotary_dim / 2, pairs = pair_units<T>(a), units = row_units<T>(a);
+    const int per_pass = kRopeThreads / units;
+    const int unit = threadIdx.x % units, place = threadIdx.x / units;
+    const int abreast = max(1, per_pass / rows);         // tokens of a pass
+    const int t_first = abreast > 1 ? place / rows : 0, first = place - t_first * rows;
+    if (place >= per_pass || t_first >= abreast) return;
+    const bool pair = unit < pairs;
+    const int at = pair ? unit * N : a.rotary_dim + (unit - pairs) * N;
+    const int step = per_pass * a.row_splits, r0 = first + split * per_pass;
+    if (r0 >= rows) return;
+    uint4 *mine = places + threadIdx.x;                  // [kAhead][2][kRopeThreads]
+    int pt = t_first, pr = r0, pslot = 0;
+    auto prefetch = [&]() {
+        const T *src;
+        T *dst;
+        if (pt < nt && row_at<T>(a, t0 + pt, pr, &src, &dst)) {
+            copy_async16(mine + pslot * 2 * kRopeThreads, src + at);
+            if (!kInterleaved && pair) copy_async16(mine + (pslot * 2 + 1) * kRopeThreads, src + at + half);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        pslot = pslot + 1 == kAhead ? 0 : pslot + 1;
+        pr += step;
+        if (pr >= rows) pr = r0, pt += abreast;
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead - 1; ++i) prefetch();
+    int slot = 0;
+    for (int t = t_first; t < nt; t += abreast) {
+        float2 cs[P];
+        if (pair) {
+            const float4 *c = reinterpret_cast<const float4 *>(table + t * half + unit * P);
+#pragma unroll
+            for (int i = 0; i < P; i += 2) {
+                const float4 v = c[i / 2];
+                cs[i] = make_float2(v.x, v.y);
+                cs[i + 1] = make_float2(v.z, v.w);
+            }
+        }
+        for (int r = r0; r < rows; r += step) {
+            prefetch();
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+            const uint4 *from = mine + slot * 2 * kRopeThreads;
+            slot = slot + 1 == kAhead ? 0 : slot + 1;
+            const T *src;
+            T *dst;
+            if (!row_at<T>(a, t0 + t, r, &src, &dst)) continue;
+            uint4 x = from[0];
+            if (pair && r < a.num_q_heads + a.num_kv_heads) {
+                float p[N], q[N];
+                Vec<T>::widen(x, p);
+                if constexpr (kInterleaved) {
+#pragma unroll
+                    for (int i = 0; i < N; i += 2) {
+                        q[i] = p[i] * cs[i / 2].x - p[i + 1] * cs[i / 2].y;
+                        q[i + 1] = p[i + 1] * cs[i / 2].x + p[i] * cs[i / 2].y;
+                    }
+                    x = Vec<T>::narrow(q);
+                } else {
+                    float s[N], o[N];
+                    Vec<T>::widen(from[kRopeThreads], q);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        s[i] = p[i] * cs[i].x - q[i] * cs[i].y;
+                        o[i] = q[i] * cs[i].x + p[i] * cs[i].y;
+                    }
+                    x = Vec<T>::narrow(s);
+                    *reinterpret_cast<uint4 *>(dst + at + half) = Vec<T>::narrow(o);
+                }
+            } else if (!kInterleaved && pair) {
+                *reinterpret_cast<uint4 *>(dst + at + half) = from[kRopeThreads];
+            }
+            *reinterpret_cast<uint4 *>(dst + at) = x;
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // Rows of any shape: a thread has one vector of a row, and reads the other elements
 // of its pairs where they are.  All of a row is read in one pass, so that a barrier
 // before the stores is enough to turn rows in place.
@@ -329,6 +422,12 @@ __device__ __forceinline__ void turn_rows(const RopeArgs &a, int cta, float2 *ta
     }
     __syncthreads();
     const int rows = a.num_q_heads + (pools ? 2 * a.num_kv_heads : 0);
+    if (pools && a.whole && a.row_tokens >= 2) {
+        uint4 *places = reinterpret_cast<uint4 *>(table + ((a.row_tokens * half + 1) & ~1));
+        if (a.interleaved) turn_many_rows<T, true>(a, t0, nt, split, rows, table, places);
+        else turn_many_rows<T, false>(a, t0, nt, split, rows, table, places);
+        return;
+    }
     if (a.whole) {
         if (a.interleaved) turn_whole_rows<T, true>(a, t0, nt, split, rows, table);
         else turn_whole_rows<T, false>(a, t0, nt, split, rows, table);
@@ -826,7 +925,8 @@ pa_status launch_rope(RopeArgs &a, bool blocks, cudaStream_t stream) {
            (a.tile_tokens < 8 || (2 * a.tile_tokens + kWindow - 1) * half * (int)sizeof(float2) <= 100 * 1024))
         a.tile_tokens *= 2;
     int64_t grid = rows > 0 ? (n + a.row_tokens - 1) / a.row_tokens * a.row_splits : 0;
-    size_t smem = (size_t)a.row_tokens * half * sizeof(float2);
+    size_t smem = (size_t)((a.row_tokens * half + 1) & ~1) * sizeof(float2);
+    if (!blocks && a.whole && a.row_tokens >= 2) smem += (size_t)kAhead * 2 * kRopeThreads * sizeof(uint4);
     a.tile_ctas = 0;
     if (blocks) {
         const int items = 2 * a.num_kv_heads;
