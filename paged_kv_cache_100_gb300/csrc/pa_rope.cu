@@ -930,7 +930,11 @@ pa_status launch_rope(RopeArgs &a, bool blocks, cudaStream_t stream) {
     a.tile_ctas = 0;
     if (blocks) {
         const int items = 2 * a.num_kv_heads;
-        a.tile_splits = (int)std::max<int64_t>(1, std::min<int64_t>((items + kRopeWarps - 1) / kRopeWarps, 4 * 152 / n));
+        // CTAs share a block's tiles where there are fewer than SMs, and where one would
+        // have more than two a warp: it would end the grid alone (3696 tokens of 32 KV
+        // heads of 128 50 us, 79 by one CTA, 58 with one tile a warp; of 64 52 / 85 / 53)
+        a.tile_splits = (int)std::max<int64_t>(1, std::min<int64_t>((items + kRopeWarps - 1) / kRopeWarps,
+                                                                    std::max<int64_t>(4 * 152 / n, items / 16)));
         a.tile_ctas = (int)((n + a.tile_tokens - 1) / a.tile_tokens * a.tile_splits);
         grid += a.tile_ctas;
         smem = std::max(smem, (size_t)(a.tile_tokens + kWindow - 1) * half * sizeof(float2));
