@@ -777,10 +777,12 @@ __device__ __forceinline__ void encode_blocks(const RopeArgs &a, int cta, float2
 
     // the leaders (a block's first token: none of the kWindow - 1 entries before
     // has the same block), and their blocks' rows
-    __shared__ int s_lead[kMaxTile], s_low[kMaxTile], s_n[kMaxTile], s_count, s_last;
+    __shared__ int s_low[kMaxTile], s_n[kMaxTile], s_count, s_last;
+    __shared__ uint8_t s_lead[kMaxTile];                 // in order: CTAs that share a tile agree on it
     __shared__ int64_t s_blk[kMaxTile];
     __shared__ uint16_t s_list[kMaxTile][kBlockSize];
-    if (threadIdx.x == 0) s_count = s_last = 0;
+    if (threadIdx.x == 0) s_last = 0;
+    if (threadIdx.x < kMaxTile) s_n[threadIdx.x] = 0;
     // this thread's first position and frequency, on their way while the leaders
     // are found
     const int t_first = half > 0 ? threadIdx.x / half : 0;
@@ -812,17 +814,22 @@ __device__ __forceinline__ void encode_blocks(const RopeArgs &a, int cta, float2
         const bool kept = mine && lane == 31 - __clz((int)same);
         const unsigned rows = __ballot_sync(kAll, kept);
         const int low = __reduce_min_sync(kAll, off);
-        int place = 0;
         if (lane == 0) {
-            place = atomicAdd(&s_count, 1);
             atomicMax(&s_last, i + 31 - __clz((int)rows));
-            s_lead[place] = i;
-            s_low[place] = low;
-            s_n[place] = __popc(rows);
-            s_blk[place] = blk;
+            s_low[i] = low;
+            s_n[i] = __popc(rows);
+            s_blk[i] = blk;
         }
-        place = __shfl_sync(kAll, place, 0);
-        if (kept) s_list[place][__popc(rows & ((1u << lane) - 1u))] = (uint16_t)(lane | (off << 8));
+        if (kept) s_list[i][__popc(rows & ((1u << lane) - 1u))] = (uint16_t)(lane | (off << 8));
+    }
+    __syncthreads();
+    if (warp == 0) {
+        static_assert(kMaxTile == 64, "two entries per lane");
+        const unsigned lo = __ballot_sync(kAll, s_n[lane] > 0), hi = __ballot_sync(kAll, s_n[lane + 32] > 0);
+        const unsigned below = (1u << lane) - 1u;
+        if ((lo >> lane) & 1u) s_lead[__popc(lo & below)] = (uint8_t)lane;
+        if ((hi >> lane) & 1u) s_lead[__popc(lo) + __popc(hi & below)] = (uint8_t)(lane + 32);
+        if (lane == 0) s_count = __popc(lo) + __popc(hi);
     }
     __syncthreads();
     const int leads = s_count;
@@ -837,11 +844,11 @@ __device__ __forceinline__ void encode_blocks(const RopeArgs &a, int cta, float2
 
     const int per_lead = 2 * a.num_kv_heads;
     for (int item = warp + split * kRopeWarps; item < leads * per_lead; item += kRopeWarps * a.tile_splits) {
-        const int at = item / per_lead, rest = item - at * per_lead;
+        const int rank = item / per_lead, rest = item - rank * per_lead, at = s_lead[rank];
         Tile w;
         w.value = rest >= a.num_kv_heads;
         w.h = w.value ? rest - a.num_kv_heads : rest;
-        w.lead = s_lead[at];
+        w.lead = at;
         w.tok = t0 + w.lead;
         w.low = s_low[at];
         w.n = s_n[at];

@@ -280,3 +280,29 @@ def test_large_batches_of_any_shape(pkv, seqs, longest, D, rot, interleaved, Hq,
     for u, v in zip(a, b):
         assert u is None or torch.equal(u, v)
     assert int(status.item()) == 0
+
+
+def test_tiles_shared_by_thread_blocks(pkv):
+    """Many KV heads and several blocks begun per thread block: the thread blocks that share a tile's
+    (block, head) pairs take each pair once, in every run."""
+    rng = np.random.default_rng(3)
+    slots, pos, blocks = _chunks(rng, 110, 11)
+    T, Hkv, D = slots.size, 17, 64
+    assert T >= 616                                          # two tokens a thread block
+    g, qkv, _, _ = _inputs(5, T, 0, Hkv, D, torch.float32, blocks + T)
+    x = qkv.cuda()
+    rope = pkv.rotary_plan(D, interleaved=True)
+    kc, ks = R.pools(g, blocks, Hkv, D)
+    p, s = torch.from_numpy(pos).cuda(), torch.from_numpy(slots).cuda()
+    run = lambda c, lo, hi: pkv.rope_cache_write(  # noqa: E731
+        None, x[lo:hi, :Hkv], x[lo:hi, Hkv:], p[lo:hi], rope, c[0], c[2], s[lo:hi], k_scales=c[1], v_scales=c[3])
+    fresh = lambda: [t.cuda() for t in (kc, ks, kc, ks)]  # noqa: E731
+    want = fresh()
+    ends = [0] + [i for i in range(1, T) if slots[i] // 16 != slots[i - 1] // 16] + [T]
+    for lo, hi in zip(ends, ends[1:]):
+        run(want, lo, hi)
+    for _ in range(30):
+        got = fresh()
+        run(got, 0, T)
+        for u, v in zip(got, want):
+            assert torch.equal(u, v)
