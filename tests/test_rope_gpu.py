@@ -246,7 +246,7 @@ def test_large_batch_uses_many_tokens_per_block(pkv):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("D,rot,interleaved,Hq,Hkv", [(256, 74, False, 1, 1), (128, 18, True, 3, 1), (64, 50, False, 2, 2),
                                                       (64, 64, True, 1, 1), (128, 128, False, 3, 1), (16, 2, False, 5, 3),
-                                                      (128, 96, True, 0, 4), (64, 48, False, 0, 20)])
+                                                      (128, 96, True, 0, 4), (64, 48, False, 0, 20), (256, 256, False, 1, 1)])
 @pytest.mark.parametrize("seqs,longest", [(2, 700), (6, 520), (130, 40), (40, 300), (60, 900)])
 def test_large_batches_of_any_shape(pkv, seqs, longest, D, rot, interleaved, Hq, Hkv, dtype, codes):
     """Calls large enough that thread blocks take 2, 4, 8, 16 and 64 tokens' blocks (and several tokens' rows),
