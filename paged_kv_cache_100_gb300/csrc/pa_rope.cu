@@ -70,8 +70,9 @@ struct RopeArgs {
     int num_tokens, num_q_heads, num_kv_heads, head_dim, rotary_dim;
     int interleaved;
     int num_blocks;
+    int table_row;                   // entries of a token in a table of cos and sin: rotary_dim / 2, rounded up to 4
     int whole;                       // every unit of a row is a whole vector
-    int unit_tiles;                  // encode_units' rows: bf16, rotary_dim a multiple of 8
+    int unit_tiles;                  // encode_units' rows: bf16, neighbouring pairs or rotary_dim a multiple of 8
     int tile_ctas, tile_tokens;      // CTAs that encode blocks, and the entries each looks at
     int tile_splits;                 // CTAs that share the KV heads of the same entries
     int row_tokens, row_splits;      // tokens of a row CTA; CTAs that share a token's rows
@@ -136,16 +137,17 @@ __device__ __forceinline__ T from_float(float x) {
 }
 
 // A row whose pieces are whole vectors is cut into units that touch nothing of one
-// another, so that rows may be turned in place: pair units (N pairs of halves, or
-// N / 2 neighbouring pairs) and units of N elements behind rotary_dim.
+// another, so that rows may be turned in place: with neighbouring pairs N elements
+// each, the last of the turned ones perhaps in part; with halves N pairs each, then
+// N elements each behind rotary_dim.
 template <typename T>
 __device__ __forceinline__ int pair_units(const RopeArgs &a) {
     constexpr int N = Vec<T>::N;
-    return a.interleaved ? (a.rotary_dim + N - 1) / N : (a.rotary_dim / 2 + N - 1) / N;
+    return a.interleaved ? (a.rotary_dim + N - 1) / N : a.rotary_dim / 2 / N;
 }
 template <typename T>
 __device__ __forceinline__ int row_units(const RopeArgs &a) {
-    return pair_units<T>(a) + (a.head_dim - a.rotary_dim + Vec<T>::N - 1) / Vec<T>::N;
+    return a.interleaved ? a.head_dim / Vec<T>::N : pair_units<T>(a) + (a.head_dim - a.rotary_dim) / Vec<T>::N;
 }
 
 // N elements of a row from element `at` on, a multiple of N, and in `o` the other
@@ -216,12 +218,13 @@ __device__ __forceinline__ void turn_whole_rows(const RopeArgs &a, int64_t t0, i
     const int t_first = abreast > 1 ? place / rows : 0, first = place - t_first * rows;
     if (place >= per_pass || t_first >= abreast) return;
     const bool pair = unit < pairs;
-    const int at = pair ? unit * N : a.rotary_dim + (unit - pairs) * N;
+    const int at = kInterleaved || pair ? unit * N : a.rotary_dim + (unit - pairs) * N;
+    const int some = kInterleaved ? half - unit * P : P;     // pairs of the unit that are turned, if below P
     const int step = per_pass * a.row_splits;
     for (int t = t_first; t < nt; t += abreast) {
         float2 cs[P];
         if (pair) {
-            const float4 *c = reinterpret_cast<const float4 *>(table + t * half + unit * P);
+            const float4 *c = reinterpret_cast<const float4 *>(table + t * a.table_row + unit * P);
 #pragma unroll
             for (int i = 0; i < P; i += 2) {
                 const float4 v = c[i / 2];
@@ -252,8 +255,8 @@ __device__ __forceinline__ void turn_whole_rows(const RopeArgs &a, int64_t t0, i
                     if constexpr (kInterleaved) {
 #pragma unroll
                         for (int i = 0; i < N; i += 2) {
-                            q[i] = p[i] * cs[i / 2].x - p[i + 1] * cs[i / 2].y;
-                            q[i + 1] = p[i + 1] * cs[i / 2].x + p[i] * cs[i / 2].y;
+                            q[i] = i / 2 < some ? p[i] * cs[i / 2].x - p[i + 1] * cs[i / 2].y : p[i];
+                            q[i + 1] = i / 2 < some ? p[i + 1] * cs[i / 2].x + p[i] * cs[i / 2].y : p[i + 1];
                         }
                         x[u] = Vec<T>::narrow(q);
                     } else {
@@ -298,7 +301,8 @@ __device__ __forceinline__ void turn_many_rows(const RopeArgs &a, int64_t t0, in
     const int t_first = abreast > 1 ? place / rows : 0, first = place - t_first * rows;
     if (place >= per_pass || t_first >= abreast) return;
     const bool pair = unit < pairs;
-    const int at = pair ? unit * N : a.rotary_dim + (unit - pairs) * N;
+    const int at = kInterleaved || pair ? unit * N : a.rotary_dim + (unit - pairs) * N;
+    const int some = kInterleaved ? half - unit * P : P;     // pairs of the unit that are turned, if below P
     const int step = per_pass * a.row_splits, r0 = first + split * per_pass;
     if (r0 >= rows) return;
     uint4 *mine = places + threadIdx.x;                  // [kAhead][2][kRopeThreads]
@@ -321,7 +325,7 @@ __device__ __forceinline__ void turn_many_rows(const RopeArgs &a, int64_t t0, in
     for (int t = t_first; t < nt; t += abreast) {
         float2 cs[P];
         if (pair) {
-            const float4 *c = reinterpret_cast<const float4 *>(table + t * half + unit * P);
+            const float4 *c = reinterpret_cast<const float4 *>(table + t * a.table_row + unit * P);
 #pragma unroll
             for (int i = 0; i < P; i += 2) {
                 const float4 v = c[i / 2];
@@ -344,8 +348,8 @@ __device__ __forceinline__ void turn_many_rows(const RopeArgs &a, int64_t t0, in
                 if constexpr (kInterleaved) {
 #pragma unroll
                     for (int i = 0; i < N; i += 2) {
-                        q[i] = p[i] * cs[i / 2].x - p[i + 1] * cs[i / 2].y;
-                        q[i + 1] = p[i + 1] * cs[i / 2].x + p[i] * cs[i / 2].y;
+                        q[i] = i / 2 < some ? p[i] * cs[i / 2].x - p[i + 1] * cs[i / 2].y : p[i];
+                        q[i + 1] = i / 2 < some ? p[i + 1] * cs[i / 2].x + p[i] * cs[i / 2].y : p[i + 1];
                     }
                     x = Vec<T>::narrow(q);
                 } else {
@@ -368,8 +372,8 @@ __device__ __forceinline__ void turn_many_rows(const RopeArgs &a, int64_t t0, in
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Rows of any shape: a thread has one vector of a row, and reads the other elements
-// of its pairs where they are.  All of a row is read in one pass, so that a barrier
+// Rows of halves that are no whole vectors: a thread has one vector of a row, and
+// reads the other elements of its pairs where they are.  All of a row is read in one pass, so that a barrier
 // before the stores is enough to turn rows in place.
 template <typename T>
 __device__ __forceinline__ void turn_any_rows(const RopeArgs &a, int64_t t0, int nt, int split, int rows,
@@ -382,7 +386,7 @@ __device__ __forceinline__ void turn_any_rows(const RopeArgs &a, int64_t t0, int
     const int t_first = abreast > 1 ? place / rows : 0, first = place - t_first * rows;
     const bool mine = place < per_pass && t_first < abreast;
     const int turned_rows = a.num_q_heads + a.num_kv_heads;
-    const bool meet = a.query == a.query_out && !a.interleaved;
+    const bool meet = a.query == a.query_out;
     for (int tb = 0; tb < nt; tb += abreast) {
         for (int rb = split * per_pass; rb < rows; rb += per_pass * a.row_splits) {
             const int t = tb + t_first, r = rb + first;
@@ -391,11 +395,11 @@ __device__ __forceinline__ void turn_any_rows(const RopeArgs &a, int64_t t0, int
             float x[N], o[N];
             const bool on = mine && t < nt && r < rows && row_at<T>(a, t0 + t, r, &src, &dst);
             if (on) {
-                load_pairs<T>(src, at, r < turned_rows ? rot : 0, a.interleaved, x, o);
+                load_pairs<T>(src, at, r < turned_rows ? rot : 0, false, x, o);
                 if (r < turned_rows && at < rot) {
 #pragma unroll
                     for (int i = 0; i < N; ++i)
-                        if (at + i < rot) o[i] = turned(x[i], o[i], at + i, half, a.interleaved, table + t * half);
+                        if (at + i < rot) o[i] = turned(x[i], o[i], at + i, half, false, table + t * a.table_row);
                         else o[i] = x[i];
                 } else {
 #pragma unroll
@@ -418,12 +422,12 @@ __device__ __forceinline__ void turn_rows(const RopeArgs &a, int cta, float2 *ta
     const int nt = (int)min((int64_t)a.row_tokens, a.num_tokens - t0);
     for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
         const int t = i / half;
-        table[i] = turn_of(a.positions[t0 + t], a.turns[i - t * half], (float)a.factor);
+        table[t * a.table_row + i - t * half] = turn_of(a.positions[t0 + t], a.turns[i - t * half], (float)a.factor);
     }
     __syncthreads();
     const int rows = a.num_q_heads + (pools ? 2 * a.num_kv_heads : 0);
     if (pools && a.whole && a.row_tokens >= 2) {
-        uint4 *places = reinterpret_cast<uint4 *>(table + ((a.row_tokens * half + 1) & ~1));
+        uint4 *places = reinterpret_cast<uint4 *>(table + a.row_tokens * a.table_row);
         if (a.interleaved) turn_many_rows<T, true>(a, t0, nt, split, rows, table, places);
         else turn_many_rows<T, false>(a, t0, nt, split, rows, table, places);
         return;
@@ -493,7 +497,7 @@ __device__ __noinline__ int exact_exponent(const RopeArgs &a, const Tile &w, flo
             int first, second, pair;
             float x = to_float(row[d]);
             if (pair_of(a, d, &first, &second, &pair)) {
-                const float2 cs = table[(w.lead + j) * half + pair];
+                const float2 cs = table[(w.lead + j) * a.table_row + pair];
                 const float x0 = to_float(row[first]), x1 = to_float(row[second]);
                 x = d == second ? x1 * cs.x + x0 * cs.y : x0 * cs.x - x1 * cs.y;
             }
@@ -536,8 +540,8 @@ __device__ __forceinline__ float tile_scale(const RopeArgs &a, const Tile &w, fl
 }
 __device__ __forceinline__ bool is_pow2(float x) { return (__float_as_uint(x) & 0x7fffffu) == 0; }
 
-// Encodes a tile of bf16 rows that are cut into whole units of 8 elements (rotary_dim
-// a multiple of 8): a lane keeps its unit u and goes through the rows, 32 / units of
+// Encodes a tile of bf16 rows that are cut into whole units of 8 elements (neighbouring
+// pairs, or rotary_dim a multiple of 8): a lane keeps its unit u and goes through the rows, 32 / units of
 // them abreast.  A unit of the turned part is 4 u .. and their partners half + 4 u ..
 // (kMode 1, halves) or 8 u .. (kMode 2, neighbours); others are 8 u .. (kMode 0: all).
 // The rows are turned once for the maximum and, read again from L1, once more for
@@ -549,6 +553,8 @@ __device__ __forceinline__ void encode_units(const RopeArgs &a, const Tile &w, f
     const int lane = threadIdx.x & 31, side = lane / units, u = lane - side * units;
     const int half = kDim > 0 ? kDim / 2 : a.rotary_dim / 2;
     const bool turned = kMode != 0 && (kDim > 0 || 8 * u < a.rotary_dim);
+    // pairs of the unit that are turned: all or none but at the end of neighbouring ones
+    const int some = !turned ? 0 : kMode == 2 && kDim == 0 ? min(half - 4 * u, 4) : 4;
     const int d0 = kMode == 1 && turned ? 4 * u : 8 * u, d1 = kMode == 1 && turned ? half + 4 * u : 8 * u + 4;
     const int n = side < abreast ? w.n : 0;
     auto row_of = [&](int i) { return abreast * i + side; };
@@ -581,7 +587,7 @@ __device__ __forceinline__ void encode_units(const RopeArgs &a, const Tile &w, f
         }
         if (turned) {
             const int j = row_of(i) < n ? w.list[row_of(i)] & 0xff : 0;
-            const float4 *c = reinterpret_cast<const float4 *>(table + (w.lead + j) * half + 4 * u);
+            const float4 *c = reinterpret_cast<const float4 *>(table + (w.lead + j) * a.table_row + 4 * u);
             cs[0] = c[0];
             cs[1] = c[1];
         }
@@ -590,10 +596,10 @@ __device__ __forceinline__ void encode_units(const RopeArgs &a, const Tile &w, f
     auto turn = [&](float &x0, float &x1, const float4 (&cs)[2], int k) {
         const float c = k & 1 ? cs[k >> 1].z : cs[k >> 1].x, s = k & 1 ? cs[k >> 1].w : cs[k >> 1].y;
         const float y = x0 * c - x1 * s;
-        x1 = turned ? x1 * c + x0 * s : x1;
-        x0 = turned ? y : x0;
+        x1 = k < some ? x1 * c + x0 * s : x1;
+        x0 = k < some ? y : x0;
     };
-    float amax = 0.f;                                // fmaxf passes over NaN
+    float amax = 0.f, other = 0.f;                   // of turned pairs and others; fmaxf passes over NaN
 #pragma unroll 1
     for (int b = 0; abreast * b < w.n; b += 4) {
         uint4 raw[4];                                // four rows of the lane on their way
@@ -608,11 +614,13 @@ __device__ __forceinline__ void encode_units(const RopeArgs &a, const Tile &w, f
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 if constexpr (kMode != 0) turn(x0[k], x1[k], cs, k);
-                amax = fmaxf(amax, fmaxf(fabsf(x0[k]), fabsf(x1[k])));
+                const float top = fmaxf(fabsf(x0[k]), fabsf(x1[k]));
+                if (k < some) amax = fmaxf(amax, top);
+                else other = fmaxf(other, top);
             }
         }
     }
-    const float scale = tile_scale<__nv_bfloat16>(a, w, turned ? amax : 0.f, turned ? 0.f : amax, old, table);
+    const float scale = tile_scale<__nv_bfloat16>(a, w, amax, other, old, table);
     const float inv = 1.f / scale;
     const bool exact = is_pow2(scale);
     uint4 ahead = load(0);
@@ -624,12 +632,13 @@ __device__ __forceinline__ void encode_units(const RopeArgs &a, const Tile &w, f
         float4 cs[2];
         pairs(i, raw, x0, x1, cs);
         uint32_t out[2];                             // codes of x0 and of x1 (mode 1), else in order
-        if (!exact && !turned) {                     // a scale that someone else chose is divided by
+        if (!exact) {                                // a scale that someone else chose is divided by
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x0[k] = __fdiv_rn(x0[k], scale), x1[k] = __fdiv_rn(x1[k], scale);
+            for (int k = 0; k < 4; ++k)
+                if (k >= some) x0[k] = __fdiv_rn(x0[k], scale), x1[k] = __fdiv_rn(x1[k], scale);
         }
-        const float m = exact || turned ? inv : 1.f;
         if constexpr (kMode == 0) {
+            const float m = exact ? inv : 1.f;
             out[0] = f32x2_to_e4m3x2(x0[0] * m, x1[0] * m) | (f32x2_to_e4m3x2(x0[1] * m, x1[1] * m) << 16);
             out[1] = f32x2_to_e4m3x2(x0[2] * m, x1[2] * m) | (f32x2_to_e4m3x2(x0[3] * m, x1[3] * m) << 16);
         } else {
@@ -638,7 +647,8 @@ __device__ __forceinline__ void encode_units(const RopeArgs &a, const Tile &w, f
             float y0[4], y1[4], err[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                err[k] = turned ? (fabsf(x0[k]) + fabsf(x1[k])) * (kTurnError * (float)a.factor * inv) : 0.f;
+                const float m = exact || k < some ? inv : 1.f;
+                err[k] = k < some ? (fabsf(x0[k]) + fabsf(x1[k])) * (kTurnError * (float)a.factor * inv) : 0.f;
                 y0[k] = x0[k];
                 y1[k] = x1[k];
                 turn(y0[k], y1[k], cs, k);
@@ -705,7 +715,7 @@ __device__ __noinline__ void encode_any(const RopeArgs &a, const Tile &w, float 
 #pragma unroll 1
         for (int k = first; k < w.n; k += abreast) {
             const int j = w.list[k] & 0xff;
-            const float2 *cs = table + (w.lead + j) * half;
+            const float2 *cs = table + (w.lead + j) * a.table_row;
             float x[N], o[N];
             load_pairs<T>(tile_row<T>(a, w, j), at, rot, a.interleaved, x, o);
 #pragma unroll
@@ -723,7 +733,7 @@ __device__ __noinline__ void encode_any(const RopeArgs &a, const Tile &w, float 
 #pragma unroll 1
         for (int k = first; k < w.n; k += abreast) {
             const int j = w.list[k] & 0xff;
-            const float2 *cs = table + (w.lead + j) * half;
+            const float2 *cs = table + (w.lead + j) * a.table_row;
             float x[N], o[N];
             load_pairs<T>(tile_row<T>(a, w, j), at, rot, a.interleaved, x, o);
             uint32_t lo[N / 4], hi[N / 4];
@@ -835,10 +845,11 @@ __device__ __forceinline__ void encode_blocks(const RopeArgs &a, int cta, float2
     const int leads = s_count;
     if (leads == 0) return;
     const int pairs = (s_last + 1) * half;
-    if ((int)threadIdx.x < pairs) table[threadIdx.x] = turn_of(pos_first, turns_first, (float)a.factor);
+    if ((int)threadIdx.x < pairs)
+        table[t_first * a.table_row + threadIdx.x - t_first * half] = turn_of(pos_first, turns_first, (float)a.factor);
     for (int i = threadIdx.x + kRopeThreads; i < pairs; i += kRopeThreads) {
         const int t = i / half;
-        table[i] = turn_of(a.positions[t0 + t], a.turns[i - t * half], (float)a.factor);
+        table[t * a.table_row + i - t * half] = turn_of(a.positions[t0 + t], a.turns[i - t * half], (float)a.factor);
     }
     __syncthreads();
 
@@ -909,8 +920,9 @@ template <typename T>
 pa_status launch_rope(RopeArgs &a, bool blocks, cudaStream_t stream) {
     constexpr int N = 16 / (int)sizeof(T);
     const int D = a.head_dim, rot = a.rotary_dim, half = rot / 2;
-    a.whole = a.interleaved ? rot % N == 0 : half % N == 0;
-    a.unit_tiles = blocks && sizeof(T) == 2 && rot % 8 == 0;
+    a.table_row = (half + 3) & ~3;
+    a.whole = a.interleaved || half % N == 0;
+    a.unit_tiles = blocks && sizeof(T) == 2 && (a.interleaved || rot % 8 == 0);
     const int rows = a.num_q_heads + (blocks ? 0 : 2 * a.num_kv_heads);
     // tokens share a CTA where there are enough for four CTAs per SM, more than
     // eight where a token has few rows (64 query heads of 128: 61 us with 4 or 8
@@ -929,10 +941,10 @@ pa_status launch_rope(RopeArgs &a, bool blocks, cudaStream_t stream) {
     const int tile_most = std::min(kMaxTile, std::max(16, 16 * kRopeWarps / a.num_kv_heads));
     a.tile_tokens = 1;
     while (a.tile_tokens < tile_most && n / (2 * a.tile_tokens) >= 2 * 152 &&
-           (a.tile_tokens < 8 || (2 * a.tile_tokens + kWindow - 1) * half * (int)sizeof(float2) <= 100 * 1024))
+           (a.tile_tokens < 8 || (2 * a.tile_tokens + kWindow - 1) * a.table_row * (int)sizeof(float2) <= 100 * 1024))
         a.tile_tokens *= 2;
     int64_t grid = rows > 0 ? (n + a.row_tokens - 1) / a.row_tokens * a.row_splits : 0;
-    size_t smem = (size_t)((a.row_tokens * half + 1) & ~1) * sizeof(float2);
+    size_t smem = (size_t)a.row_tokens * a.table_row * sizeof(float2);
     if (!blocks && a.whole && a.row_tokens >= 2) smem += (size_t)kAhead * 2 * kRopeThreads * sizeof(uint4);
     a.tile_ctas = 0;
     if (blocks) {
@@ -944,7 +956,7 @@ pa_status launch_rope(RopeArgs &a, bool blocks, cudaStream_t stream) {
                                                                     std::max<int64_t>(4 * 152 / n, items / 16)));
         a.tile_ctas = (int)((n + a.tile_tokens - 1) / a.tile_tokens * a.tile_splits);
         grid += a.tile_ctas;
-        smem = std::max(smem, (size_t)(a.tile_tokens + kWindow - 1) * half * sizeof(float2));
+        smem = std::max(smem, (size_t)(a.tile_tokens + kWindow - 1) * a.table_row * sizeof(float2));
     }
     if (grid >= ((int64_t)1 << 31)) return PA_ERR_UNSUPPORTED;
     auto kernel = blocks ? pa_rope_write_kernel<T, true> : pa_rope_write_kernel<T, false>;
