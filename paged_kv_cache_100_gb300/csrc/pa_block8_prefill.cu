@@ -782,6 +782,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (j + 2 == n) commit(kQFree);
                 }
             }
+            // Group 1 keeps no other phase of an item without a tile B in step, and waits for
+            // this one by parity: it completes for item `it` only when the group has left
+            // item it - 1, or two short items could pass while the group is still at the end
+            // of a longer one, and its wait would then match a phase that is still running.
+            // (Group 0 is waited for before the item's first P V.)
+            if (it >= 1 && !warp_wait(&bars[kOFree + 1], (it - 1) & 1, fail, a.status)) ok = false;
             commit(kDrain);                          // every MMA of the item has completed once it flips
             gstep += n;
         }

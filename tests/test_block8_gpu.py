@@ -455,3 +455,34 @@ def test_pools_past_32_bits(pkv):
             qq = q[2 if len(rows) == 1 else i].double().numpy()
             ref, bound = R.attention(qq, kv[:, 0], kss[:, 0], vv[:, 0], vss[:, 0], order, 0, last + 1, D ** -0.5, floor=4.0)
             _check(out[i], ref, bound)
+
+
+@pytest.mark.parametrize("window", [0, 300])
+def test_prefill_nan_values_beside_many_short_chunks(pkv, window):
+    """More items than SMs, of which those with two tiles of rows hold NaN codes and most others have one
+    tile: the NaNs stay with the rows that attend to them, and no wait gives up."""
+    hq, hkv = 16, 2                                          # 16 tokens a tile
+    rng = np.random.default_rng(window)
+    chunks = [40 if i % 20 == 0 else 1 + i % 3 for i in range(240)]
+    lens = [n + int(x) for n, x in zip(chunks, rng.integers(0, 120, len(chunks)))]
+    lens[0] = lens[100] = 2500
+    p = Pool(77 + window, lens, hkv, spread=0.7)
+    nan = [(b, pos, b // 20 % hkv, 5 * (b % 25)) for b in range(0, 240, 20) for pos in (lens[b] - 2, lens[b] - 30, lens[b] // 2)]
+    for k, (b, pos, h, d) in enumerate(nan):
+        p.vc[p.tables[b, pos // 16], h, pos % 16, d] = 0x7F if k % 2 else 0xFF
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q, out, rows = _prefill(pkv, p, chunks, hq, window=window, status=status, longest=40)
+    want = np.zeros((len(rows), hq, D), bool)
+    for i, (b, last) in enumerate(rows):
+        for bb, pos, h, d in nan:
+            if bb == b and pos <= last and (window == 0 or pos > last - window):
+                want[i, h * hq // hkv:(h + 1) * hq // hkv, d] = True
+    got = out.double().cpu().numpy()
+    assert want.any() and (np.isnan(got) == want).all()
+    assert int(status.item()) == 0
+    for b, pos, h, d in nan:
+        p.vc[p.tables[b, pos // 16], h, pos % 16, d] = 0
+    pick = sorted(rng.choice(len(rows), 250, replace=False).tolist())
+    ref, bound = p.reference(q.double().numpy()[pick], [rows[i] for i in pick], D ** -0.5, window, floor=4.0)
+    err = np.abs(got[pick] - ref)
+    assert (err <= bound + 2.0 ** -8 * (np.abs(ref) + bound))[~want[pick]].all()
