@@ -307,24 +307,57 @@ __device__ __noinline__ bool clear_nan(uint8_t *dst, int at0, int at1) {
     return true;
 }
 
+// Steps that every row of an item attends to whole begin in [lo, hi].  In the other
+// ones NaN codes of V are 0 in the widened tile.
+struct Whole {
+    int lo, hi;
+    __device__ __forceinline__ bool has(int k0) const { return k0 >= lo && k0 <= hi; }
+};
+
 // NaN codes among the 64 columns that a thread holds of O (V's columns from
-// `column` on), at those positions of `steps` steps from block blk_lo on that its
-// row, at position qpos, attends to: these elements of O become NaN.  A whole warp.
+// `column` on), at those positions of `steps` steps from block blk_lo on, in steps
+// that some row attends to only in part, that its row, at position qpos, attends
+// to: these elements of O become NaN.  (The NaNs of the other steps went through
+// the product.)  A whole warp, whose lanes read 8 positions' codes at a time; the
+// steps with a part of the diagonal or of the window's start are few whatever the
+// context's length.  16 chunks of 512 tokens on contexts of up to 8192, NaN codes in
+// every chunk: 1.08 ms, 0.95 without.  (Each thread reading all positions of its row for
+// itself took 239 ms, and other warps wait a second at most.)
 __device__ __noinline__ void poison_output(const PrefillArgs &a, uint32_t o_base, int b, int kvh, int column, int blk_lo,
-                                           int steps, int qpos) {
+                                           int steps, int kv_hi, Whole whole, int qpos) {
     const int32_t *table = a.block_tables + (int64_t)b * a.max_blocks;
-    const int first = max(blk_lo * kBlockSize, a.window > 0 ? qpos + 1 - a.window : 0);
-    const int end = min(blk_lo * kBlockSize + steps * kKv, qpos + 1);
+    const int lane = threadIdx.x & 31;
+    const int first = a.window > 0 ? qpos + 1 - a.window : 0;
     uint64_t mask = 0;
 #pragma unroll 1
-    for (int p = first; p < end; ++p) {
-        const int phys = table[p / kBlockSize];
-        const int64_t tile = (int64_t)((unsigned)phys < (unsigned)a.num_blocks ? phys : 0) * a.num_kv_heads + kvh;
-        const uint32_t *codes =
-            reinterpret_cast<const uint32_t *>(a.value_cache + (tile * kBlockSize + p % kBlockSize) * kD + column);
+    for (int j = 0; j < steps; ++j) {
+        const int k0 = blk_lo * kBlockSize + j * kKv;
+        if (whole.has(k0)) continue;
 #pragma unroll 1
-        for (int k = 0; k < kCols; ++k)
-            if (((codes[k >> 2] >> (8 * (k & 3))) & 0x7fu) == 0x7fu) mask |= 1ull << k;
+        for (int p0 = k0; p0 < min(k0 + kKv, kv_hi); p0 += 8) {
+            const int p = p0 + (lane >> 2);
+            uint32_t nans = 0;                       // one bit for each of 16 codes
+            if (p < kv_hi) {
+                const int phys = table[p / kBlockSize];
+                const int64_t tile = (int64_t)((unsigned)phys < (unsigned)a.num_blocks ? phys : 0) * a.num_kv_heads + kvh;
+                const uint4 w = *reinterpret_cast<const uint4 *>(
+                    a.value_cache + (tile * kBlockSize + p % kBlockSize) * kD + column + (lane & 3) * 16);
+                const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    // the top bit of each byte that is 0x7f without its sign; then side by side
+                    const uint32_t top = ((words[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                    nans |= (((top >> 7) * 0x01020408u) >> 24) << (4 * k);
+                }
+            }
+            uint32_t hits = __ballot_sync(0xffffffffu, nans != 0);
+            while (hits != 0) {
+                const int src = __ffs(hits) - 1, at = p0 + (src >> 2);
+                hits &= hits - 1;
+                const uint32_t bits = __shfl_sync(0xffffffffu, nans, src);
+                if (at >= first && at <= qpos) mask |= (uint64_t)bits << (16 * (src & 3));
+            }
+        }
     }
     __syncwarp();
 #pragma unroll 1
@@ -479,6 +512,11 @@ __device__ __forceinline__ void tile_range(const PrefillArgs &a, Item &d) {
     d.blk_hi = (d.kv_hi + kBlockSize - 1) / kBlockSize;
     d.n_tiles = (d.blk_hi - d.blk_lo + 7) / 8;
     d.parts = max(1, min(a.splits, d.n_tiles / kPartSteps));
+}
+
+// The steps that all of the item's rows, from position C + t0 to kv_hi - 1, attend to whole.
+__device__ __forceinline__ Whole whole_steps(const PrefillArgs &a, const Item &d) {
+    return Whole{a.window > 0 ? d.kv_hi - a.window : 0, d.C + d.t0 + 1 - kKv};
 }
 
 template <bool kCut>
@@ -887,8 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<uint4 *>(row + at1) = make_uint4(0, 0, 0, 0);
                         }
                 }
-                const bool partial = k0 + kKv > d.C + d.t0 + 1 || (a.window > 0 && k0 < d.kv_hi - a.window);
-                if (partial && clear_nan<kRowStep>(dst, at0, at1)) s_nan[it & 3] = it + 1;
+                if (!whole_steps(a, d).has(k0) && clear_nan<kRowStep>(dst, at0, at1)) s_nan[it & 3] = it + 1;
                 fence_proxy_async_smem();
                 mbar_arrive(&bars[kVConv + gs % kVStages]);
                 if (j + 1 < d.n_tiles) {
@@ -1054,7 +1091,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool drained = warp_wait(&bars[kDrain], it & 1, fail, a.status);
                 if (drained && s_nan[it & 3] == it + 1) {
                     tc_fence_after();
-                    poison_output(a, o_base, d.b, d.kvh, part * kCols, d.blk_lo, d.n_tiles, qpos);
+                    poison_output(a, o_base, d.b, d.kvh, part * kCols, d.blk_lo, d.n_tiles, d.kv_hi, whole_steps(a, d), qpos);
                 }
                 if (kCut && __all_sync(0xffffffffu, ok) && drained && d.parts > 1) {
                     tc_fence_after();

@@ -486,3 +486,23 @@ def test_prefill_nan_values_beside_many_short_chunks(pkv, window):
     ref, bound = p.reference(q.double().numpy()[pick], [rows[i] for i in pick], D ** -0.5, window, floor=4.0)
     err = np.abs(got[pick] - ref)
     assert (err <= bound + 2.0 ** -8 * (np.abs(ref) + bound))[~want[pick]].all()
+
+
+@pytest.mark.parametrize("window", [0, 50000])
+def test_prefill_nan_values_in_long_contexts(pkv, window):
+    """NaN codes at a long context's beginning and end, in steps that all rows attend to and in the steps of
+    the diagonal and of the window's start: each reaches the rows that attend to it, and no wait gives up."""
+    hq, hkv, chunk, length = 8, 1, 40, 60000
+    p = Pool(5 + window, [length, 100], hkv, spread=0.7)
+    nan = [(pos, d) for d, pos in enumerate((3, 130, length // 2, length - 45, length - 30, length - 2, length - 50000 - 1,
+                                             length - 50000 - 20, length - 50000 + 7))] + [(length - 9, 127), (length - 9, 64)]
+    for pos, d in nan:
+        p.vc[p.tables[0, pos // 16], 0, pos % 16, d] = 0x7F
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q, out, rows = _prefill(pkv, p, [chunk, 7], hq, window=window, status=status, longest=chunk)
+    want = np.zeros((len(rows), hq, D), bool)
+    for i, (b, last) in enumerate(rows):
+        for pos, d in nan:
+            if b == 0 and pos <= last and (window == 0 or pos > last - window):
+                want[i, :, d] = True
+    assert (np.isnan(out.double().cpu().numpy()) == want).all() and int(status.item()) == 0
