@@ -98,7 +98,7 @@ constexpr int kQFull = 0, kQFree = 1, kDrain = 2, kQSplit = 3, kKFull = kQSplit 
               kCodeFull = kKEmpty + kKStages, kCodeEmpty = kCodeFull + kCodeStages, kVConv = kCodeEmpty + kCodeStages,
               kVEmpty = kVConv + kVStages, kSFull = kVEmpty + kVStages, kPFull = kSFull + kQT, kPvDone = kPFull + kQT,
               kOFree = kPvDone + kQT, kItemFull = kOFree + kQT, kItemEmpty = kItemFull + 2,
-              kScaleFull = kItemEmpty + 2, kNumBars = kScaleFull + kScaleSlots;
+              kScaleFull = kItemEmpty + 2, kEnd = kScaleFull + kScaleSlots, kNumBars = kEnd + 1;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;                 // TMEM slot, failure flag, item order, item queue [2], NaN marks [4]
 constexpr int kSmemBytes = kOffMisc + 48;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -829,6 +829,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             commit(kDrain);                          // every MMA of the item has completed once it flips
             gstep += n;
         }
+        // after a wait that gave up products may still be running: the CTA's memory is
+        // theirs until they are done
+        commit(kEnd);
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bars[kEnd], 0)) && lane == 0) report(a.status, PA_DEV_TIMEOUT);
     } else if (warp >= kWidenWarp0) {
         // ---------------- widening ----------------
         // 16 codes of a row become two 16-byte chunks of f16 in one of the tile's
