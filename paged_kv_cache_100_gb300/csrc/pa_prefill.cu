@@ -731,6 +731,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (j + 2 == n) umma_commit(&bars[kQFree]);   // the item's last QK^T is issued
                     }
                 }
+                // Group 1 keeps no other phase of an item without a tile B in step, and waits
+                // for this one by parity: it must have left the item before when it completes
+                if (it >= 1 && !wait_or_fail(&bars[kOFree + 1], (it - 1) & 1, fail, a.status)) ok = false;
                 // every MMA of this item has completed once kDrain flips
                 umma_commit(&bars[kDrain]);
                 gstep += n;
