@@ -86,7 +86,7 @@ constexpr int kOffQ = 0;                          // kQT tiles
 constexpr int kOffK = kOffQ + kQT * kTile;        // kStages tiles
 constexpr int kOffV = kOffK + kStages * kTile;    // kStages tiles
 constexpr int kOffBar = kOffV + kStages * kTile;
-constexpr int kNumBars = 5 * kStages + 15;
+constexpr int kNumBars = 5 * kStages + 16;
 constexpr int kOffRed = kOffBar + 256;            // [kQT][2 parities][kSplit][128] floats
 constexpr int kPermMax = 64;                      // prefill: sequences ordered by length (at most)
 constexpr int kOffPerm = kOffRed + kQT * 2 * kSplit * kRows * 4;   // int [kPermMax]
@@ -100,8 +100,8 @@ constexpr int kQFull = 0, kKFull = 1, kKEmpty = kKFull + kStages, kVFull = kKEmp
               kVEmpty = kVFull + kStages, kVConv = kVEmpty + kStages, kSFull = kVConv + kStages,
               kPFull = kSFull + kQT,
               kPvDone = kPFull + kQT, kOFree = kPvDone + kQT, kItemFull = kOFree + kQT,
-              kItemEmpty = kItemFull + 2, kQFree = kItemEmpty + 2, kDrain = kQFree + 1;
-static_assert(kDrain + 1 == kNumBars, "barrier count");
+              kItemEmpty = kItemFull + 2, kQFree = kItemEmpty + 2, kDrain = kQFree + 1, kEnd = kDrain + 1;
+static_assert(kEnd + 1 == kNumBars, "barrier count");
 // barriers, then the TMEM slot, the failure flag, the prefix-mode context bound
 // and the two-entry item queue
 static_assert(kNumBars * 8 + 20 <= 256, "barrier block");
@@ -465,6 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars[kItemEmpty + q], 1 + kQT * kGroup + kConvThreads);
         }
         mbar_init(&bars[kDrain], 1);
+        mbar_init(&bars[kEnd], 1);
         *fail = 0;
         *s_maxl = 0;
         fence_mbar_init();
@@ -738,6 +739,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 umma_commit(&bars[kDrain]);
                 gstep += n;
             }
+            // after a wait that gave up products may still be running: the CTA's memory is
+            // theirs until they are done
+            umma_commit(&bars[kEnd]);
+            if (!mbar_wait_bounded(&bars[kEnd], 0)) report(a.status, PA_DEV_TIMEOUT);
         }
     } else if (warp >= kConvWarp0) {
         // ---------------- V conversion ----------------
