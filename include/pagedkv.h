@@ -559,10 +559,13 @@ pa_status pa_rope_cache_write(void *query_out, const void *query, const void *ke
  * Everything else is as in pa_decode_fp8.  Supported: head_dim 128, any group
  * (one of more than 8 query heads is split into parts of its largest divisor up
  * to 8, which read the same tiles).
- * Arithmetic: codes are widened exactly; the query is rounded to f16 once (as
- * in pa_decode_fp8, with PA_DEV_RANGE); a value scale enters the exponent of
- * its tokens' weights, which are rounded to f16 relative to the largest of
- * them; sums are fp32.
+ * Arithmetic: codes are widened exactly; a query row is brought up by a power
+ * of two until its largest magnitude is at least 2^14 and then rounded to f16,
+ * exact but for elements below 2^-29 of the largest, which are off by at most
+ * 2^-39 of it (an element of magnitude 65536 or more, or infinite, becomes
+ * infinite and the call flags PA_DEV_RANGE, as in pa_decode_fp8); a value scale
+ * enters the exponent of its tokens' weights, which are rounded to f16 relative
+ * to the largest of them; sums are fp32.
  */
 size_t pa_decode_block_fp8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
                                            int head_dim, int max_blocks_per_seq, int block_size,

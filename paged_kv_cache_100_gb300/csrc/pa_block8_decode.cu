@@ -144,32 +144,58 @@ struct Warp8 {
     uint32_t qb[8][2];
     float o[8][4];
     float m0, m1, l0, l1;
+    float qs0, qs1;              // powers of two of heads 2t and 2t + 1: what their scores are multiplied by
     int lane, g, t;
     uint32_t koff[4], voff_a[4], voff_b[4];
 
-    __device__ __forceinline__ void init(const Block8Args &a, int b, int first_head, int lane_) {
+    // This lane's part of the query: elements 32 c + 8 t .. + 7 of row g.
+    __device__ __forceinline__ void load(const Block8Args &a, int b, int first_head, int lane_, uint4 (&w)[4]) {
         lane = lane_;
         g = lane >> 2;
         t = lane & 3;
+        const uint4 *q = reinterpret_cast<const uint4 *>(
+            static_cast<const __nv_bfloat16 *>(a.query) + ((int64_t)b * a.num_q_heads + first_head + g) * kD);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) w[c] = g < a.heads ? q[4 * c + t] : make_uint4(0u, 0u, 0u, 0u);
+    }
+
+    __device__ __forceinline__ void init(const Block8Args &a, const uint4 (&w)[4]) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             koff[c] = code_at(g, 32 * c + 8 * t);
             voff_a[c] = code_at(2 * t, 32 * c + 4 * g);
             voff_b[c] = code_at(2 * t + 1, 32 * c + 4 * g);
         }
-        const uint32_t *q = reinterpret_cast<const uint32_t *>(
-            static_cast<const __nv_bfloat16 *>(a.query) + ((int64_t)b * a.num_q_heads + first_head + g) * kD);
-        const bool real = g < a.heads;
-        bool beyond = false;
+        uint32_t amax = 0;                               // as bits: magnitudes compare like integers
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int d = 32 * (k >> 1) + 8 * t + 4 * (k & 1);
-            const uint32_t w0 = real ? q[d / 2] : 0u, w1 = real ? q[d / 2 + 1] : 0u;
-            qb[k][0] = pack_f16x2(bf16lo(w0), bf16hi(w0));
-            qb[k][1] = pack_f16x2(bf16lo(w1), bf16hi(w1));
-            beyond |= bf16x2_beyond_f16(w0) | bf16x2_beyond_f16(w1);
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (uint32_t x : {w[c].x, w[c].y, w[c].z, w[c].w})
+                amax = max(amax, max((x << 16) & 0x7fffffffu, x & 0x7fff0000u));
+        if (amax >= 0x47800000u) {                       // 65536 or more: looked at again, as NaN is none of them
+            bool beyond = false;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                beyond |= bf16x2_beyond_f16(w[c].x) | bf16x2_beyond_f16(w[c].y) | bf16x2_beyond_f16(w[c].z) | bf16x2_beyond_f16(w[c].w);
+            if (beyond) report(a.status, PA_DEV_RANGE);  // the f16 query is not the query
         }
-        if (beyond) report(a.status, PA_DEV_RANGE);      // the f16 query is not the query
+        amax = max(amax, __shfl_xor_sync(kFull, amax, 1));
+        amax = max(amax, __shfl_xor_sync(kFull, amax, 2));
+        // A row is brought up by a power of two so that its largest magnitude lies in
+        // [2^14, 2^15): f16 then holds every element exactly but those below 2^-29 of it,
+        // which are off by at most 2^-39 of it.
+        const int up = min(max(14 + 127 - (int)(amax >> 23), 0), 126);
+        const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+        const int down = (127 - up) << 23;               // 2^-up, of row g
+        qs0 = __int_as_float(__shfl_sync(kFull, down, 8 * t));
+        qs1 = __int_as_float(__shfl_sync(kFull, down, 8 * t + 4));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            qb[2 * c][0] = pack_f16x2(bf16lo(w[c].x) * f, bf16hi(w[c].x) * f);
+            qb[2 * c][1] = pack_f16x2(bf16lo(w[c].y) * f, bf16hi(w[c].y) * f);
+            qb[2 * c + 1][0] = pack_f16x2(bf16lo(w[c].z) * f, bf16hi(w[c].z) * f);
+            qb[2 * c + 1][1] = pack_f16x2(bf16lo(w[c].w) * f, bf16hi(w[c].w) * f);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         m0 = m1 = -INFINITY;
@@ -192,10 +218,11 @@ struct Warp8 {
             mma_f16_16816(s, x, qb[2 * c + 1][0], qb[2 * c + 1][1]);
         }
         const bool v0 = g >= nlo && g < nvalid, v1 = g + 8 >= nlo && g + 8 < nvalid;
-        s[0] = v0 ? fmaf(s[0], e.ck, e.lv) : -INFINITY;
-        s[1] = v0 ? fmaf(s[1], e.ck, e.lv) : -INFINITY;
-        s[2] = v1 ? fmaf(s[2], e.ck, e.lv) : -INFINITY;
-        s[3] = v1 ? fmaf(s[3], e.ck, e.lv) : -INFINITY;
+        const float ck0 = e.ck * qs0, ck1 = e.ck * qs1;
+        s[0] = v0 ? fmaf(s[0], ck0, e.lv) : -INFINITY;
+        s[1] = v0 ? fmaf(s[1], ck1, e.lv) : -INFINITY;
+        s[2] = v1 ? fmaf(s[2], ck0, e.lv) : -INFINITY;
+        s[3] = v1 ? fmaf(s[3], ck1, e.lv) : -INFINITY;
         float mx0 = fmaxf(s[0], s[2]), mx1 = fmaxf(s[1], s[3]);
 #pragma unroll
         for (int k = 4; k < 32; k <<= 1) {
@@ -306,6 +333,8 @@ __device__ __forceinline__ float remote_f32(const float *mine, uint32_t rank) {
 }
 
 // kParts > 1: the grid's clusters of kParts CTAs each work on one (sequence, KV head).
+// (117 registers in the widest form, four CTAs of four warps per SM; held to 96 for a fifth,
+// by a launch bound or otherwise, the 70B-shaped batch took 200 to 204 us instead of 193.)
 template <int NW, int STAGES, int kParts>
 __global__ void __launch_bounds__(NW * 32)
     pa_decode_block8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -340,7 +369,8 @@ __global__ void __launch_bounds__(NW * 32)
     const int ahead = part * a.part_blocks + warp + NW * lane;
     int first_phys = early && warp + NW * lane < a.part_blocks && ahead < a.max_blocks ? row_table[ahead] : -1;
     Warp8 state;
-    state.init(a, b, first_head, lane);
+    uint4 query[4];
+    state.load(a, b, first_head, lane, query);
     Span w;
     const bool say = threadIdx.x == 0 && part == 0 && idx == 0;
     if constexpr (kParts > 1) even_span(a, len, part, kParts, say, w);
@@ -390,6 +420,7 @@ __global__ void __launch_bounds__(NW * 32)
         const int row = __shfl_sync(kFull, first_row, it);
         if (lane == 0 && it < count) issue_row(it, row);
     }
+    state.init(a, query);                                // under the tiles' latency
     for (int k = lane; k < count; k += 32) {
         const int64_t at = k == lane ? first_at : entry_of(table[NW * k]);
         const float sv = value_scale(a.v_scales[at], a.status);
@@ -627,7 +658,7 @@ struct Plan {
 // issues one launch instead of two (5 us, 8 otherwise); in larger calls clusters
 // lose (32 ragged sequences 28.6 us, 26.5 with a merge kernel).
 //
-// Where the CTAs are more than the five of four warps that an SM holds and their
+// Where there are more than five CTAs per SM (which holds four of four warps) and their
 // parts short, CTAs have one warp, 16 of which an SM holds: a short part's time is
 // its start (length, table, scales, first tiles one after another) and its end.
 // 960 CTAs on contexts of up to 64 tokens 7.5 us against 9.9, 256 tokens 15.3 /

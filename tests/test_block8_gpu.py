@@ -120,6 +120,27 @@ def test_decode_scales_of_any_size(pkv, hq, hkv):
     assert int(status.item()) == 0
 
 
+@pytest.mark.parametrize("hq,hkv,longest", [(16, 2, 100), (5, 1, 700), (48, 16, 200)])
+def test_decode_queries_of_any_size(pkv, hq, hkv, longest):
+    """Rows of tiny, mixed and zero queries, with key scales that bring their scores back into the usual range:
+    small elements count like any others."""
+    lens = [longest, 33, longest // 2, 17, 64, 50, 1] + ([40] * 103 if hq == 48 else [])
+    p = Pool(hq + longest, lens, hkv, spread=0.7)
+    q = _query(p, len(lens), hq)
+    for b, e in enumerate((-17, -26, -60, -96)):             # two of the rows with the first heads as they were
+        q[b, b % 2:] = (q[b, b % 2:].float() * 2.0 ** e).to(torch.bfloat16)
+        p.ks[p.tables[b, :-(-lens[b] // 16)]] *= 2.0 ** -e
+    for b in (1, 3):
+        q[b, 0] = 0
+    q[4, :, 3] *= 2.0 ** 10                                  # one large element beside the others
+    q[5, :, ::2] = (q[5, :, ::2].float() * 2.0 ** -12).to(torch.bfloat16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = pkv.decode_block_fp8(q.cuda(), *p.device(), status=status)
+    ref, bound = p.reference(q.double().numpy(), [(b, n - 1) for b, n in enumerate(lens)], D ** -0.5)
+    _check(out, ref, bound)
+    assert int(status.item()) == 0
+
+
 def test_decode_flags_bad_scales_tables_lengths_and_queries(pkv):
     from paged_kv_cache_100_gb300 import _lib
     lens = [40, 40]
