@@ -474,6 +474,9 @@ __global__ void __launch_bounds__(NW * 32)
             sum = fmaf(f, s_l[k * kHeads + h], sum);
             O = fmaf(f, reinterpret_cast<const float *>(ring + k * STAGES * kStageBytes)[i], O);
         }
+        // after a wait that gave up the row is NaN, through its partial sums too: what an earlier
+        // call left in the workspace must not pass for an output
+        if (failed) sum = __int_as_float(0x7fffffff);
         return O;
     };
     const int64_t head0 = (int64_t)b * a.num_q_heads + first_head;
@@ -481,7 +484,7 @@ __global__ void __launch_bounds__(NW * 32)
     if constexpr (kParts > 1) {
         // The parts' states side by side in the cluster's shared memory: each CTA
         // merges its share of the elements.  A part that gave up keeps its place at
-        // the barriers and leaves the output alone.
+        // the barriers; its sum makes the row NaN.
         constexpr int kEach = kHeads * kD / (NW * 32);
         float O[kEach], M[kEach], sum[kEach];
 #pragma unroll
@@ -498,7 +501,7 @@ __global__ void __launch_bounds__(NW * 32)
             state_o[i] = O[e];
             if (i % kD == 0) {
                 state_m[i / kD] = M[e];
-                state_l[i / kD] = failed ? __int_as_float(0x7fffffff) : sum[e];
+                state_l[i / kD] = sum[e];
             }
         }
         cluster_sync();
@@ -524,7 +527,6 @@ __global__ void __launch_bounds__(NW * 32)
         }
         cluster_sync();                                  // no CTA leaves while its state is read
     } else {
-        if (failed) return;
         const bool whole = w.nparts == 1;
         for (int i = threadIdx.x; i < a.heads * kD; i += NW * 32) {
             float M, sum;

@@ -99,8 +99,8 @@ constexpr int kQFull = 0, kQFree = 1, kDrain = 2, kQSplit = 3, kKFull = kQSplit 
               kVEmpty = kVConv + kVStages, kSFull = kVEmpty + kVStages, kPFull = kSFull + kQT, kPvDone = kPFull + kQT,
               kOFree = kPvDone + kQT, kItemFull = kOFree + kQT, kItemEmpty = kItemFull + 2,
               kScaleFull = kItemEmpty + 2, kEnd = kScaleFull + kScaleSlots, kNumBars = kEnd + 1;
-constexpr int kOffMisc = kOffBar + kNumBars * 8;                 // TMEM slot, failure flag, item order, item queue [2], NaN marks [4]
-constexpr int kSmemBytes = kOffMisc + 48;
+constexpr int kOffMisc = kOffBar + kNumBars * 8;                 // TMEM slot, failure flag, item order, item queue [2], NaN marks [4], items taken [4]
+constexpr int kSmemBytes = kOffMisc + 64;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
 constexpr uint32_t kTmemCols = 512;      // S_A, S_B, O_A, O_B
@@ -581,6 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *s_order = reinterpret_cast<volatile int *>(base + kOffMisc + 8);
     volatile int *s_item = reinterpret_cast<volatile int *>(base + kOffMisc + 16);   // [2]
     volatile int *s_nan = reinterpret_cast<volatile int *>(base + kOffMisc + 32);    // [4]
+    volatile int *s_taken = reinterpret_cast<volatile int *>(base + kOffMisc + 48);  // [4]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -593,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars[i], n);
         }
         *fail = 0;
-        for (int i = 0; i < 4; ++i) s_nan[i] = 0;
+        for (int i = 0; i < 4; ++i) s_nan[i] = 0, s_taken[i] = -1;
         fence_mbar_init();
         tma_prefetch_desc(&qmap);
         tma_prefetch_desc(&kmap);
@@ -670,6 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const int slot = it & 1;
+                if (item >= 0) s_taken[it & 3] = item;
                 if (it >= 2 && !wait_or_fail(&bars[kItemEmpty + slot], ((it >> 1) - 1) & 1, fail, a.status)) item = -1;
                 s_item[slot] = item;
                 mbar_arrive(&bars[kItemFull + slot]);
@@ -1158,6 +1160,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
+    }
+    // After a wait that gave up, the parts that this CTA was at (it has four items at most in
+    // hand) become NaN: what an earlier call left in the workspace must not pass for an output.
+    if (kCut && *fail) {
+        for (int k = 0; k < 4; ++k) {
+            Item d;
+            if (s_taken[k] < 0 || !describe_item<kCut>(a, s_taken[k], by_length, false, perm, d)) continue;
+            const int rows = min(kQT * tok_per_tile, d.T - d.t0) * a.group;
+            for (int i = threadIdx.x; i < rows; i += kThreads) {
+                const int64_t row = (int64_t)(d.q0 + d.t0 + i / a.group) * a.num_q_heads + d.kvh * a.group + i % a.group;
+                a.part_ml[row * a.splits + d.part] = make_float2(-INFINITY, __int_as_float(0x7fffffff));
+            }
+        }
     }
 }
 
