@@ -1184,19 +1184,28 @@ __global__ void __launch_bounds__(128) pa_merge_prefill8_kernel(const PrefillArg
     const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     if (row >= (int64_t)a.num_query_tokens * a.num_q_heads) return;
     const int token = (int)(row / a.num_q_heads);
-    // the last sequence that begins at or before the token
-    int lo = 0, hi = a.num_seqs;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (a.query_start[mid] <= token) lo = mid;
-        else hi = mid;
-    }
+    // The sequence that the token belongs to, among those that were computed: entries of
+    // query_start that fall or leave the rows say nothing about the others, so all are
+    // looked at (a cut call has no more sequences than the GPU has SMs).
     Item d;
-    d.q0 = a.query_start[lo];
-    const int end = a.query_start[lo + 1], L = a.context_lens[lo];
-    if (token < d.q0 || token >= end || end > a.num_query_tokens || end - d.q0 > L || L > a.max_blocks * kBlockSize ||
-        token - d.q0 >= a.n_mt * (kQT * kRows / a.group))
-        return;
+    int end = 0, L = 0, found = -1;
+    for (int b = lane; b - lane < a.num_seqs && found < 0; b += 32) {
+        bool mine = false;
+        if (b < a.num_seqs) {
+            d.q0 = a.query_start[b];
+            end = a.query_start[b + 1];
+            L = a.context_lens[b];
+            mine = d.q0 >= 0 && token >= d.q0 && token < end && end <= a.num_query_tokens && end - d.q0 <= L &&
+                   L <= a.max_blocks * kBlockSize;
+        }
+        const unsigned who = __ballot_sync(0xffffffffu, mine);
+        if (who != 0) found = __ffs(who) - 1;
+    }
+    if (found < 0) return;
+    d.q0 = __shfl_sync(0xffffffffu, d.q0, found);
+    end = __shfl_sync(0xffffffffu, end, found);
+    L = __shfl_sync(0xffffffffu, L, found);
+    if (token - d.q0 >= a.n_mt * (kQT * kRows / a.group)) return;
     d.T = end - d.q0;
     d.C = L - d.T;
     const int tokens = kQT * kRows / a.group;

@@ -361,6 +361,28 @@ def test_prefill_flags(pkv):
         _check(out[:20], ref, bound, what)
 
 
+@pytest.mark.parametrize("bad", [200, -5, 1 << 30])
+@pytest.mark.parametrize("longest,blocks", [(30, None), (30, 400)])
+def test_prefill_bad_start_entries_leave_other_sequences_alone(pkv, bad, longest, blocks):
+    """An entry of query_start that falls or leaves the rows: its two sequences are flagged and not computed,
+    those beside them are, with their contexts cut into parts or not."""
+    from paged_kv_cache_100_gb300 import _lib
+    chunks, lens = [20, 7, 11, 30, 5], [60, 5000 if blocks else 40, 3000 if blocks else 33, 2000 if blocks else 50, 1500 if blocks else 9]
+    p = Pool(40, lens, 2, width=blocks, spread=0.7)
+    start = np.concatenate([[0], np.cumsum(chunks)]).astype(np.int32)
+    q = _query(p, int(start[-1]), 4)
+    given = start.copy()
+    given[2] = bad                                           # sequences 1 and 2
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pkv.prefill_block_fp8(q.cuda(), *p.device(), torch.from_numpy(given).cuda(), longest, out=out, status=status)
+    rows = [(b, lens[b] - n + i) for b, n in enumerate(chunks) for i in range(n)]
+    pick = [i for i, (b, _) in enumerate(rows) if b in (0, 3, 4)]
+    ref, bound = p.reference(q.double().numpy()[pick], [rows[i] for i in pick], D ** -0.5, floor=4.0)
+    _check(out[pick], ref, bound, f"{bad}")
+    assert (out[20:38] == 7.0).all() and int(status.item()) == _lib.PA_DEV_BAD_CONTEXT_LEN
+
+
 def test_prefill_queries_of_any_size(pkv):
     """Rows of large, tiny and zero queries, a row with an outlier element, infinite and NaN elements."""
     p = Pool(15, [90], 2, spread=0.7)
