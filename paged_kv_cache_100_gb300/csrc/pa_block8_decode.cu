@@ -749,6 +749,7 @@ bool encode_block8_map(CUtensorMap *map, const void *pool, int64_t rows, bool sw
             enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
     });
     if (enc == nullptr) return false;
+    bind_context();
     cuuint64_t dims[2] = {kD, (cuuint64_t)rows};
     cuuint64_t strides[1] = {kD};
     cuuint32_t box[2] = {kD, kBlockSize};

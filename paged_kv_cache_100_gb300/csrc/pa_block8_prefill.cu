@@ -1256,6 +1256,7 @@ bool encode_query_map(CUtensorMap *map, const void *query, int rows, int num_q_h
             enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
     });
     if (enc == nullptr) return false;
+    bind_context();
     const int group = num_q_heads / num_kv_heads;
     cuuint64_t dims[4] = {kD, (cuuint64_t)group, (cuuint64_t)num_kv_heads, (cuuint64_t)rows};
     cuuint64_t strides[3] = {kD * 2, (cuuint64_t)group * kD * 2, (cuuint64_t)num_q_heads * kD * 2};

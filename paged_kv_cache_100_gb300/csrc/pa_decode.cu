@@ -1613,6 +1613,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 bool encode_pool_map(CUtensorMap *map, const void *pool, int64_t rows, int D, int elem_bytes) {
     auto enc = tensor_map_encoder();
     if (enc == nullptr) return false;
+    bind_context();
     cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)D * elem_bytes};
     cuuint32_t box[2] = {(cuuint32_t)(128 / elem_bytes), 16};

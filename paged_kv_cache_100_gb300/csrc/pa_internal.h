@@ -21,6 +21,15 @@ pa_status cuda_failure(cudaError_t err, const char *where);
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Gives this host thread a current context.  The driver's cuTensorMapEncodeTiled needs
+// one, and a thread whose first call into CUDA is one of ours has none yet: the runtime
+// binds its device's primary context with the first call that asks the device.
+inline void bind_context() {
+    static thread_local bool bound = false;
+    size_t unused;
+    if (!bound) bound = cudaDeviceGetLimit(&unused, cudaLimitStackSize) == cudaSuccess;
+}
+
 // Launches a kernel with programmatic stream serialisation: it may be scheduled
 // while the previous kernel in the stream is still running.  Every kernel of
 // this library starts with griddepcontrol.wait (nothing before it reads global

@@ -1117,6 +1117,7 @@ pa_status encode_maps(const void *query, int query_rows, int num_q_heads, int nu
                       CUtensorMap *qmap, CUtensorMap *kmap, CUtensorMap *vmap) {
     auto enc = encoder();
     if (enc == nullptr) return cuda_failure(cudaErrorInvalidValue, "cuTensorMapEncodeTiled lookup");
+    bind_context();
     const int group = num_q_heads / num_kv_heads;
     {
         cuuint64_t dims[4] = {(cuuint64_t)kD, (cuuint64_t)group, (cuuint64_t)num_kv_heads,
