@@ -714,7 +714,7 @@ pa_status launch_decode(const Block8Args &a, const void *kc, const void *vc, int
         return cuda_failure(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
     const size_t smem = Shape<NW, STAGES>::smem(a.part_blocks);
     auto kernel = pa_decode_block8_kernel<NW, STAGES, kParts>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(kernel, Shape<NW, STAGES>::smem(kMaxPartition / kBlockSize));
     if (e != cudaSuccess) return cuda_failure(e, "cudaFuncSetAttribute(block-scaled decode)");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((int64_t)a.num_seqs * a.num_kv_heads * a.splits * a.max_parts * kParts));

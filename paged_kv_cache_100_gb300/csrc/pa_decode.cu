@@ -1626,11 +1626,6 @@ bool encode_pool_map(CUtensorMap *map, const void *pool, int64_t rows, int D, in
     return r == CUDA_SUCCESS;
 }
 
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 // Warps per CTA and TMA stages per warp of the bf16 kernels (compile-time
 // tunables, one pair per consumer).  What sets the speed on GB300 is the
 // number of consumer warps resident per SM, not the depth of each ring:
@@ -1704,9 +1699,10 @@ pa_status launch_bf16(const DecodeArgs &a, const void *kc, const void *vc, int64
     if (!encode_pool_map(&kmap, kc, rows, D, Consumer::kElemBytes) ||
         !encode_pool_map(&vmap, vc, rows, D, Consumer::kElemBytes))
         return cuda_failure(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
-    const size_t smem = TmaLayout<D, Consumer::kElemBytes, NW, STAGES>::smem_bytes(a.part_blocks);
+    using Layout = TmaLayout<D, Consumer::kElemBytes, NW, STAGES>;
+    const size_t smem = Layout::smem_bytes(a.part_blocks);
     auto kernel = pa_decode_bf16_kernel<D, Consumer, NW, STAGES>;
-    cudaError_t e = allow_smem(kernel, smem);
+    cudaError_t e = allow_smem(kernel, Layout::smem_bytes(kMaxPartition / kBlockSize));
     if (e != cudaSuccess) return cuda_failure(e, "cudaFuncSetAttribute(decode)");
     // partitions this kernel owns (the workspace rows before part_base belong to
     // the shared-prefix kernel)
@@ -2348,13 +2344,13 @@ pa_status shared_prefix_common(void *out, const void *query, const void *key_cac
         cudaError_t e;
         if (head_dim == 128) {
             auto kernel = pa_prefix_kernel<128, kPrefixStages>;
-            e = allow_smem(kernel, smem);
+            e = allow_smem(kernel, 227 * 1024);     // a table entry per block of a chunk
             if (e == cudaSuccess)
                 e = launch_chained(kernel, dim3(grid), dim3((kPrefixWarps + 1) * 32), smem, st,
                                    kmap, vmap, a);
         } else {
             auto kernel = pa_prefix_kernel<64, kPrefixStages>;
-            e = allow_smem(kernel, smem);
+            e = allow_smem(kernel, 227 * 1024);     // a table entry per block of a chunk
             if (e == cudaSuccess)
                 e = launch_chained(kernel, dim3(grid), dim3((kPrefixWarps + 1) * 32), smem, st,
                                    kmap, vmap, a);

@@ -30,6 +30,15 @@ inline void bind_context() {
     if (!bound) bound = cudaDeviceGetLimit(&unused, cudaLimitStackSize) == cudaSuccess;
 }
 
+// Lets a kernel's launches ask for up to `most` bytes of dynamic shared memory.  The
+// limit belongs to the kernel, not to a launch: `most` is the same in every call, what
+// the largest launch asks for, so that no host thread lowers it between another's
+// call of this and its launch.
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t most) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+}
+
 // Launches a kernel with programmatic stream serialisation: it may be scheduled
 // while the previous kernel in the stream is still running.  Every kernel of
 // this library starts with griddepcontrol.wait (nothing before it reads global

@@ -49,6 +49,7 @@ constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
 constexpr int kWindow = 32;          // entries of slot_mapping among which a block's tokens lie
 constexpr int kMaxTile = 64;         // entries of slot_mapping whose blocks a CTA encodes
+constexpr int kMostTables = 100 * 1024;   // dynamic shared memory of a CTA at most
 constexpr int kMinExp = -32, kMaxExp = 31;
 // Error of a turned element in 32 bits, per |x0| + |x1|: the angle is held to
 // 2^-24 of half a turn (pi 2^-24), sincospi to 2 units of 2^-23, and three
@@ -941,7 +942,7 @@ pa_status launch_rope(RopeArgs &a, bool blocks, cudaStream_t stream) {
     const int tile_most = std::min(kMaxTile, std::max(16, 16 * kRopeWarps / a.num_kv_heads));
     a.tile_tokens = 1;
     while (a.tile_tokens < tile_most && n / (2 * a.tile_tokens) >= 2 * 152 &&
-           (a.tile_tokens < 8 || (2 * a.tile_tokens + kWindow - 1) * a.table_row * (int)sizeof(float2) <= 100 * 1024))
+           (a.tile_tokens < 8 || (2 * a.tile_tokens + kWindow - 1) * a.table_row * (int)sizeof(float2) <= kMostTables))
         a.tile_tokens *= 2;
     int64_t grid = rows > 0 ? (n + a.row_tokens - 1) / a.row_tokens * a.row_splits : 0;
     size_t smem = (size_t)a.row_tokens * a.table_row * sizeof(float2);
@@ -961,7 +962,7 @@ pa_status launch_rope(RopeArgs &a, bool blocks, cudaStream_t stream) {
     if (grid >= ((int64_t)1 << 31)) return PA_ERR_UNSUPPORTED;
     auto kernel = blocks ? pa_rope_write_kernel<T, true> : pa_rope_write_kernel<T, false>;
     if (smem > 44 * 1024) {                          // with the static arrays above the default limit of 48 KiB
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaError_t e = allow_smem(kernel, kMostTables);
         if (e != cudaSuccess) return cuda_failure(e, "cudaFuncSetAttribute(rope)");
     }
     cudaError_t e = launch_chained(kernel, dim3((unsigned)grid), dim3(kRopeThreads), smem, stream, a);

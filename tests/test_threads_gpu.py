@@ -65,3 +65,47 @@ def test_a_threads_first_call(pkv):
         call(None, want)
         errors, _ = _together([lambda st: call(st, got)], 1)
         assert not errors and torch.equal(got, want)
+
+
+def test_decodes_of_different_partitions(pkv):
+    g = torch.Generator().manual_seed(1)
+    lens = [700, 33, 1]
+    tables, blocks = R.tables_for(g, lens, width=1024)
+    kc, ks = R.pools(g, blocks, 2, D)
+    dev = [t.cuda() for t in (kc, kc, ks, ks, torch.from_numpy(tables), torch.tensor(lens, dtype=torch.int32))]
+    q = torch.randn(3, 4, D, generator=g).to(torch.bfloat16).cuda()
+    sizes = [512, 16384, 4096, 8192]
+    want = [pkv.decode_block_fp8(q, *dev, partition_size=p) for p in sizes]
+    head = torch.ones(2, device="cuda")
+    flat = [pkv.decode_fp8(q, dev[0], dev[1], head, head, dev[4], dev[5], partition_size=p) for p in sizes]
+    torch.cuda.synchronize()
+    errors, got = _together([lambda s, p=p: pkv.decode_block_fp8(q, *dev, partition_size=p, stream=s) for p in sizes], 3000)
+    assert not errors and all(torch.equal(a, b) for a, b in zip(got, want))
+    errors, got = _together([lambda s, p=p: pkv.decode_fp8(q, dev[0], dev[1], head, head, dev[4], dev[5], partition_size=p, stream=s)
+                             for p in sizes], 3000)
+    assert not errors and all(torch.equal(a, b) for a, b in zip(got, flat))
+
+
+def test_rotary_writes_of_different_sizes(pkv):
+    """Thread blocks of 16 and of 64 tokens, whose tables of angles differ in size."""
+    dim, calls, checks = 256, [], []
+    for n, hkv in ((12000, 1), (40000, 1), (12000, 4)):
+        x = torch.randn(n, 2 * hkv, dim, device="cuda", generator=torch.Generator("cuda").manual_seed(n)).to(torch.bfloat16)
+        pos = torch.arange(n, dtype=torch.int32, device="cuda")
+        slots = torch.arange(n, device="cuda")
+        pools = [torch.zeros(-(-n // 16), hkv, 16, dim, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        scales = [torch.zeros(-(-n // 16), hkv, device="cuda") for _ in range(2)]
+        rope = pkv.rotary_plan(dim)
+
+        def call(stream, x=x, pos=pos, slots=slots, pools=pools, scales=scales, rope=rope, hkv=hkv):
+            pkv.rope_cache_write(None, x[:, :hkv], x[:, hkv:], pos, rope, pools[0], pools[1], slots,
+                                 k_scales=scales[0], v_scales=scales[1], stream=stream)
+
+        call(None)
+        checks.append((pools, [p.clone() for p in pools]))
+        calls.append(call)
+    torch.cuda.synchronize()
+    errors, _ = _together(calls, 3000)
+    assert not errors
+    for pools, want in checks:
+        assert all(torch.equal(a, b) for a, b in zip(pools, want))
