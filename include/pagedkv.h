@@ -525,9 +525,9 @@ pa_status pa_rotary_turns(uint64_t *turns, double *attention_factor, int rotary_
  * Codes round to nearest even; NaN stays NaN; a magnitude above 448 * 2^31
  * saturates and the call flags PA_DEV_RANGE.
  * The tokens of one block must lie within 32 consecutive entries of
- * slot_mapping (chunks and decode steps in order do); a token of a block whose
- * entries spread over 33 to 62 is dropped and flagged PA_DEV_BAD_SLOT, farther
- * ones of one block race.  Of two tokens with one slot in a block-scaled pool
+ * slot_mapping (chunks and decode steps in order do); a token 32 to 62 entries
+ * behind another of its block is dropped, farther ones race and leave the block
+ * (no other) undefined; both are flagged PA_DEV_BAD_SLOT.  Of two tokens with one slot in a block-scaled pool
  * the later one is stored, in other pools they race.
  * Arithmetic: f32, rounded once.  A code is the nearest one to the f32 quotient of
  * the exact turned key: elements next to a border of two codes are computed

@@ -48,6 +48,10 @@ constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
 constexpr int kWindow = 32;          // entries of slot_mapping among which a block's tokens lie
+constexpr int kFarOwn = 1024;        // entries whose blocks a CTA of find_far looks for,
+constexpr int kFarPart = 16384;      // and entries among which it does
+constexpr int kFarSlots = 2048;      // places of its table: a power of two, never more than half full
+static_assert(kFarPart % kFarOwn == 0, "a CTA's own entries are looked at by one CTA");
 constexpr int kMaxTile = 64;         // entries of slot_mapping whose blocks a CTA encodes
 constexpr int kMostTables = 100 * 1024;   // dynamic shared memory of a CTA at most
 constexpr int kMinExp = -32, kMaxExp = 31;
@@ -76,6 +80,7 @@ struct RopeArgs {
     int unit_tiles;                  // encode_units' rows: bf16, neighbouring pairs or rotary_dim a multiple of 8
     int tile_ctas, tile_tokens;      // CTAs that encode blocks, and the entries each looks at
     int tile_splits;                 // CTAs that share the KV heads of the same entries
+    int far_ctas, far_parts;         // CTAs that look for far tokens of a block, and those of the same own entries
     int row_tokens, row_splits;      // tokens of a row CTA; CTAs that share a token's rows
 };
 
@@ -888,18 +893,71 @@ __device__ __forceinline__ void encode_blocks(const RopeArgs &a, int cta, float2
     }
 }
 
+// Tokens of one block must lie within kWindow entries.  Those a little farther apart are
+// seen (and dropped) where blocks are led; two groups farther apart are encoded by
+// CTAs that know nothing of one another, so these CTAs look for them and flag the call.
+// A CTA puts its own entries' blocks into a table in shared memory and looks up the
+// entries of its part of the list behind them.  Quadratic, but of 8 bytes an entry and
+// 1024 at a time: 40192 tokens of one head of 64 34.5 us, 33.2 without; 8192 tokens of 80
+// heads of 128 62.3 / 62.2.  (Looking in the CTAs that encode, so that one group could be
+// chosen and the others dropped, took 61 and 63.3 us.)
+__device__ __forceinline__ void find_far(const RopeArgs &a, int cta, uint32_t *keys) {
+    uint32_t *first = keys + kFarSlots;                  // an entry of the block at the same place
+    const int owner = cta / a.far_parts, part = cta - owner * a.far_parts;
+    const int64_t own = (int64_t)owner * kFarOwn, limit = (int64_t)a.num_blocks * kBlockSize;
+    const int64_t lo = max(own, (int64_t)part * kFarPart), hi = min((int64_t)a.num_tokens, (int64_t)(part + 1) * kFarPart);
+    if (lo >= hi) return;
+    for (int i = threadIdx.x; i < kFarSlots; i += kRopeThreads) keys[i] = 0;
+    __syncthreads();
+    auto place_of = [](uint32_t blk) { return (blk * 2654435761u) >> 21; };
+    static_assert(kFarSlots == 1 << 11, "place_of");
+    for (int i = threadIdx.x; i < kFarOwn && own + i < a.num_tokens; i += kRopeThreads) {
+        const int64_t slot = a.slot_mapping[own + i];
+        if (slot < 0 || slot >= limit) continue;
+        const uint32_t blk = (uint32_t)(slot / kBlockSize);
+        for (uint32_t h = place_of(blk);; h = (h + 1) % kFarSlots) {
+            const uint32_t old = atomicCAS(&keys[h], 0u, blk + 1);
+            if (old == 0) first[h] = (uint32_t)(own + i);
+            if (old == 0 || old == blk + 1) break;
+        }
+    }
+    __syncthreads();
+    bool far = false;
+    for (int64_t e = lo + threadIdx.x; e < hi; e += 8 * kRopeThreads) {
+        int64_t slot[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) slot[u] = e + u * kRopeThreads < hi ? a.slot_mapping[e + u * kRopeThreads] : -1;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (slot[u] < 0 || slot[u] >= limit) continue;
+            const uint32_t blk = (uint32_t)(slot[u] / kBlockSize);
+            for (uint32_t h = place_of(blk); keys[h] != 0; h = (h + 1) % kFarSlots)
+                if (keys[h] == blk + 1) {
+                    const int64_t d = e + u * kRopeThreads - first[h];
+                    far |= d >= kWindow || d <= -kWindow;
+                    break;
+                }
+        }
+    }
+    if (far) report(a.status, PA_DEV_BAD_SLOT);
+}
+
 template <typename T, bool kBlocks>
 __global__ void __launch_bounds__(kRopeThreads, 4) pa_rope_write_kernel(const RopeArgs a) {
     extern __shared__ __align__(16) float2 s_table[];
     grid_dependency_wait();
     grid_dependents_launch();
     if constexpr (kBlocks) {
-        if ((int)blockIdx.x < a.tile_ctas) {
-            encode_blocks<T>(a, blockIdx.x, s_table);
+        if ((int)blockIdx.x < a.far_ctas) {
+            find_far(a, blockIdx.x, reinterpret_cast<uint32_t *>(s_table));
+            return;
+        }
+        if ((int)blockIdx.x < a.far_ctas + a.tile_ctas) {
+            encode_blocks<T>(a, blockIdx.x - a.far_ctas, s_table);
             return;
         }
     }
-    turn_rows<T>(a, blockIdx.x - a.tile_ctas, s_table, !kBlocks);
+    turn_rows<T>(a, blockIdx.x - a.far_ctas - a.tile_ctas, s_table, !kBlocks);
 }
 
 // Whether rows of w bytes, n of them s bytes apart from p, touch rows of v bytes
@@ -947,8 +1005,16 @@ pa_status launch_rope(RopeArgs &a, bool blocks, cudaStream_t stream) {
     int64_t grid = rows > 0 ? (n + a.row_tokens - 1) / a.row_tokens * a.row_splits : 0;
     size_t smem = (size_t)a.row_tokens * a.table_row * sizeof(float2);
     if (!blocks && a.whole && a.row_tokens >= 2) smem += (size_t)kAhead * 2 * kRopeThreads * sizeof(uint4);
-    a.tile_ctas = 0;
+    a.tile_ctas = a.far_ctas = 0;
     if (blocks) {
+        if (n > kWindow) {
+            a.far_parts = (int)((n + kFarPart - 1) / kFarPart);
+            const int64_t far = (n + kFarOwn - 1) / kFarOwn * a.far_parts;
+            if (far >= ((int64_t)1 << 30)) return PA_ERR_UNSUPPORTED;
+            a.far_ctas = (int)far;
+            grid += far;
+            smem = std::max(smem, (size_t)2 * kFarSlots * sizeof(uint32_t));
+        }
         const int items = 2 * a.num_kv_heads;
         // CTAs share a block's tiles where there are fewer than SMs, and where one would
         // have more than two a warp: it would end the grid alone (3696 tokens of 32 KV

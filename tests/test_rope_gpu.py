@@ -306,3 +306,81 @@ def test_tiles_shared_by_thread_blocks(pkv):
         run(got, 0, T)
         for u, v in zip(got, want):
             assert torch.equal(u, v)
+
+
+def _groups(slots, limit):
+    """The slots of a call whose tokens a block-scaled write stores, and the blocks that it does not answer for.
+    Tokens of a block led by one entry are those among the 32 from it on; an entry 32 to 62 behind another of its
+    block is dropped; groups farther apart race."""
+    slots, by_block = np.asarray(slots), {}
+    keep = np.full(slots.shape, -1, np.int64)
+    for i, s in enumerate(slots):
+        if 0 <= s < limit:
+            by_block.setdefault(int(s) // 16, []).append(i)
+    racing = []
+    for blk, entries in by_block.items():
+        keep[[i for i in entries if i - entries[0] < 32]] = slots[[i for i in entries if i - entries[0] < 32]]
+        if max(np.diff(entries), default=0) > 62:
+            racing.append(blk)
+    return keep, racing
+
+
+def _spread(rng, kind, n, blocks):
+    if kind == "steps":                                      # token by token over 64 sequences
+        return np.concatenate([np.arange(64) * 160 + 5 + t for t in range(n // 64)])
+    if kind == "twice":                                      # a chunk, other tokens, the same chunk
+        return np.concatenate([np.arange(7, n // 3), np.full(n // 3, -1), np.arange(7, n // 3)])
+    parts = []
+    while sum(map(len, parts)) < n:                          # whole blocks, pieces and gaps
+        blk = int(rng.integers(0, blocks)) * 16
+        x = rng.random()
+        if x < 0.4:
+            parts.append(blk + np.arange(16))
+        elif x < 0.8:
+            parts.append(blk + rng.integers(0, 16, int(rng.integers(1, 12))))
+        else:
+            parts.append(np.full(int(rng.integers(1, 90)), -1))
+    return np.concatenate(parts)[:n]
+
+
+@pytest.mark.parametrize("hkv", [1, 9])
+@pytest.mark.parametrize("kind,n,blocks", [("steps", 640, 700), ("steps", 2560, 700), ("twice", 300, 40), ("twice", 6000, 400),
+                                           ("mixed", 150, 8), ("mixed", 900, 100), ("mixed", 5000, 700), ("mixed", 21000, 4000)])
+def test_tokens_of_a_block_far_apart(pkv, kind, n, blocks, hkv):
+    """Tokens of one block anywhere in the list: the call is flagged, and all other blocks are written as ever."""
+    from paged_kv_cache_100_gb300 import _lib
+    D = 32
+    rng = np.random.default_rng(n + blocks)
+    slots = _spread(rng, kind, n, blocks).astype(np.int64)
+    T = slots.size
+    g = torch.Generator().manual_seed(n)
+    rows = (torch.randn(T, hkv, D, generator=g) * torch.exp2(2 * torch.randn(T, hkv, 1, generator=g))).to(torch.bfloat16)
+    kc, ks = R.pools(g, blocks, hkv, D)
+    kv, kss = R.decode_codes(kc), ks.double().numpy().copy()
+    keep, racing = _groups(slots, blocks * 16)
+    R.write_blocks(rows.double().numpy(), keep, kv, kss)
+    fine = np.setdiff1d(np.arange(blocks), racing)
+    assert len(fine) > 0
+    kd, ksd, vd, vsd = kc.cuda(), ks.cuda(), kc.cuda(), ks.cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pkv.rope_cache_write(None, rows.cuda(), rows.cuda(), None, None, kd, vd, torch.from_numpy(slots).cuda(),
+                         k_scales=ksd, v_scales=vsd, status=status)
+    assert int(status.item()) == (_lib.PA_DEV_BAD_SLOT if racing or (keep != slots).any() else 0)
+    for codes, scales in ((kd, ksd), (vd, vsd)):
+        assert np.array_equal(scales.cpu().double().numpy()[fine], kss[fine])
+        assert np.array_equal(R.decode_codes(codes)[fine], kv[fine])
+
+
+@pytest.mark.parametrize("n,at,back", [(33, 32, 32), (64, 63, 63), (64, 63, 31), (1025, 1024, 1024), (1100, 1050, 30),
+                                       (20000, 19999, 19999), (20000, 17000, 600), (20000, 16400, 20), (20000, 1023, 1000)])
+def test_one_token_far_from_the_others_of_its_block(pkv, n, at, back):
+    """A single entry whose block another one has, at every distance: flagged beyond the 32 entries."""
+    from paged_kv_cache_100_gb300 import _lib
+    slots = torch.arange(n, dtype=torch.int64) * 16          # a block for every token
+    slots[at] = slots[at - back] + 3
+    rows = torch.ones(n, 1, 16, dtype=torch.bfloat16, device="cuda")
+    codes = [torch.zeros(n, 1, 16, 16, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.ones(n, 1, device="cuda") for _ in range(2)]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pkv.rope_cache_write(None, rows, rows, None, None, *codes, slots.cuda(), k_scales=scales[0], v_scales=scales[1], status=status)
+    assert int(status.item()) == (_lib.PA_DEV_BAD_SLOT if back >= 32 else 0)
