@@ -580,6 +580,27 @@ pa_status pa_decode_block_fp8(void *out, const void *query, const void *key_cach
                               int32_t *device_status, void *stream);
 
 /*
+ * The same over the flat rows of a step plan: sequence b's query and output row
+ * is query_start[b] (pa_plan_step, pa_prefill), of num_query_tokens rows.  Where
+ * a sequence brings nothing the rows behind it move up, and row b is another's.
+ *  query_start       device int32 [num_seqs + 1], or NULL: row b (num_query_tokens
+ *                    = num_seqs), as pa_decode_block_fp8 does
+ * A sequence without a row is passed over; one with more than one is too and is
+ * flagged PA_DEV_BAD_QUERY_LEN, one whose entries fall or leave the rows
+ * PA_DEV_BAD_CONTEXT_LEN.  Rows of no sequence are left as they were.  Workspace
+ * as for pa_decode_block_fp8.
+ */
+pa_status pa_decode_block_fp8_rows(void *out, const void *query, const void *key_cache,
+                                   const void *value_cache, const float *k_scales,
+                                   const float *v_scales, const int32_t *block_tables,
+                                   const int32_t *context_lens, const int32_t *query_start,
+                                   int num_seqs, int num_query_tokens, int num_q_heads,
+                                   int num_kv_heads, int head_dim, int block_size,
+                                   int max_blocks_per_seq, int num_blocks, float scale, int window,
+                                   int partition_size, void *workspace, size_t workspace_bytes,
+                                   int32_t *device_status, void *stream);
+
+/*
  * Chunked prefill attention over E4M3 pools with one scale per block and KV
  * head, filled by pa_rope_cache_write: pa_prefill's semantics (query_start,
  * context_lens, max_query_len, window, causal mask) with the pools and scales

@@ -542,14 +542,15 @@ def decode_block_fp8_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_d
 
 
 def decode_block_fp8(query, key_cache, value_cache, k_scales, v_scales, block_tables, context_lens,
-                     scale=None, *, window=0, out=None, partition_size=0, workspace=None, status=None,
-                     stream=None):
+                     scale=None, *, query_start=None, window=0, out=None, partition_size=0, workspace=None,
+                     status=None, stream=None):
     """Paged decode over E4M3 pools with one scale per block and KV head
-    (``pa_decode_block_fp8``); ``window`` > 0 attends to the last positions only.  Returns
-    ``out`` (bf16)."""
+    (``pa_decode_block_fp8``); ``window`` > 0 attends to the last positions only.  Row b of
+    ``query`` is sequence b's, or row ``query_start[b]`` of a step plan's flat rows (sequences
+    that bring nothing have none; ``pa_decode_block_fp8_rows``).  Returns ``out`` (bf16)."""
     r = _lib.binding().decode_block_fp8(query, key_cache, value_cache, k_scales, v_scales, block_tables,
                                         context_lens, scale, window, out, partition_size, workspace, status,
-                                        _given(stream, query))
+                                        _given(stream, query), query_start)
     if type(r) is int:
         check(r, "pa_decode_block_fp8")
     return r if out is None else out

@@ -63,6 +63,8 @@ SIGNATURES = {
     "pa_decode_block_fp8_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32, i32, i32]),
     "pa_decode_block_fp8": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32,
                                   f32, i32, i32, vp, sz, vp, vp]),
+    "pa_decode_block_fp8_rows": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32,
+                                       f32, i32, i32, vp, sz, vp, vp]),
     "pa_prefill_block_fp8_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32, i32, i32]),
     "pa_prefill_block_fp8": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
                                    i32, i32, i32, f32, i32, vp, sz, vp, vp]),
@@ -175,7 +177,7 @@ def binding():
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)
         mod.bind(*[ctypes.cast(getattr(handle, n), vp).value for n in (
-            "pa_plan_step", "pa_rope_cache_write", "pa_decode_block_fp8", "pa_decode_block_fp8_workspace_bytes",
+            "pa_plan_step", "pa_rope_cache_write", "pa_decode_block_fp8_rows", "pa_decode_block_fp8_workspace_bytes",
             "pa_prefill_block_fp8", "pa_prefill_block_fp8_workspace_bytes")])
         _binding = mod
     return _binding

@@ -53,12 +53,13 @@ struct Block8Args {
     const void *query;
     const int32_t *block_tables;
     const int32_t *context_lens;
+    const int32_t *query_start;  // sequence b's row is query_start[b]; nullptr: row b
     const float *k_scales;       // [num_blocks][num_kv_heads]
     const float *v_scales;
     float *part_o;               // [(b * Hq + h) * max_parts + part][128]
     float2 *part_ml;             // (reference, sum)
     int32_t *status;
-    int num_seqs, num_q_heads, num_kv_heads;
+    int num_seqs, num_rows, num_q_heads, num_kv_heads;
     int heads;                   // query heads of a CTA
     int splits;                  // CTAs of a (sequence, KV head, partition)
     int max_blocks, num_blocks;
@@ -115,6 +116,18 @@ __device__ __forceinline__ bool span_of(const Block8Args &a, int len, int part, 
     return true;
 }
 
+// The row of query and output that is sequence b's, or -1: it brings none, or more
+// than the one that a decode step has.
+__device__ __forceinline__ int row_of(const Block8Args &a, int b, bool say) {
+    if (a.query_start == nullptr) return b;
+    const int at = a.query_start[b], end = a.query_start[b + 1];
+    if (end == at) return -1;
+    const bool outside = at < 0 || end < at || end > a.num_rows;
+    if (!outside && end == at + 1) return at;
+    if (say) report(a.status, outside ? PA_DEV_BAD_CONTEXT_LEN : PA_DEV_BAD_QUERY_LEN);
+    return -1;
+}
+
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
@@ -149,12 +162,12 @@ struct Warp8 {
     uint32_t koff[4], voff_a[4], voff_b[4];
 
     // This lane's part of the query: elements 32 c + 8 t .. + 7 of row g.
-    __device__ __forceinline__ void load(const Block8Args &a, int b, int first_head, int lane_, uint4 (&w)[4]) {
+    __device__ __forceinline__ void load(const Block8Args &a, int row, int first_head, int lane_, uint4 (&w)[4]) {
         lane = lane_;
         g = lane >> 2;
         t = lane & 3;
         const uint4 *q = reinterpret_cast<const uint4 *>(
-            static_cast<const __nv_bfloat16 *>(a.query) + ((int64_t)b * a.num_q_heads + first_head + g) * kD);
+            static_cast<const __nv_bfloat16 *>(a.query) + ((int64_t)row * a.num_q_heads + first_head + g) * kD);
 #pragma unroll
         for (int c = 0; c < 4; ++c) w[c] = g < a.heads ? q[4 * c + t] : make_uint4(0u, 0u, 0u, 0u);
     }
@@ -368,11 +381,13 @@ __global__ void __launch_bounds__(NW * 32)
     const bool early = kParts == 1 && a.window == 0;     // the partition does not move with the length
     const int ahead = part * a.part_blocks + warp + NW * lane;
     int first_phys = early && warp + NW * lane < a.part_blocks && ahead < a.max_blocks ? row_table[ahead] : -1;
+    const bool say = threadIdx.x == 0 && part == 0 && idx == 0;
+    const int row = row_of(a, b, say);
+    if (row < 0) return;                                 // (a cluster's CTAs all leave)
     Warp8 state;
     uint4 query[4];
-    state.load(a, b, first_head, lane, query);
+    state.load(a, row, first_head, lane, query);
     Span w;
-    const bool say = threadIdx.x == 0 && part == 0 && idx == 0;
     if constexpr (kParts > 1) even_span(a, len, part, kParts, say, w);
     else if (!span_of(a, len, part, say, w)) return;
 
@@ -407,18 +422,18 @@ __global__ void __launch_bounds__(NW * 32)
     const int first_row = (int)(first_at * kBlockSize);
 
     const uint64_t policy = l2_policy_evict_first();     // tiles are read once: they leave L2 first
-    auto issue_row = [&](int it, int row) {
+    auto issue_row = [&](int it, int pool_row) {
         const int s = it % STAGES;
         uint8_t *kt = my_ring + s * kStageBytes;
         mbar_arrive_expect_tx(&my_bars[s], kStageBytes);
-        tma_load_2d_hint(kt, &kmap, 0, row, &my_bars[s], policy);
-        tma_load_2d_hint(kt + kTileBytes, &vmap, 0, row, &my_bars[s], policy);
+        tma_load_2d_hint(kt, &kmap, 0, pool_row, &my_bars[s], policy);
+        tma_load_2d_hint(kt + kTileBytes, &vmap, 0, pool_row, &my_bars[s], policy);
     };
     auto issue = [&](int it) { issue_row(it, entries[warp + it * NW].row); };
 #pragma unroll
     for (int it = 0; it < STAGES; ++it) {
-        const int row = __shfl_sync(kFull, first_row, it);
-        if (lane == 0 && it < count) issue_row(it, row);
+        const int at = __shfl_sync(kFull, first_row, it);
+        if (lane == 0 && it < count) issue_row(it, at);
     }
     state.init(a, query);                                // under the tiles' latency
     for (int k = lane; k < count; k += 32) {
@@ -480,7 +495,7 @@ __global__ void __launch_bounds__(NW * 32)
         return O;
     };
     const int64_t head0 = (int64_t)b * a.num_q_heads + first_head;
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + head0 * kD;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + ((int64_t)row * a.num_q_heads + first_head) * kD;
     if constexpr (kParts > 1) {
         // The parts' states side by side in the cluster's shared memory: each CTA
         // merges its share of the elements.  A part that gave up keeps its place at
@@ -535,9 +550,9 @@ __global__ void __launch_bounds__(NW * 32)
                 // a NaN sum stays NaN; an empty context gives zeros
                 out[i] = __float2bfloat16_rn(sum == 0.f ? 0.f : O / sum);
             } else {
-                const int64_t row = (head0 + i / kD) * a.max_parts + part;
-                a.part_o[row * kD + i % kD] = O;
-                if (i % kD == 0) a.part_ml[row] = make_float2(M, sum);
+                const int64_t at = (head0 + i / kD) * a.max_parts + part;
+                a.part_o[at * kD + i % kD] = O;
+                if (i % kD == 0) a.part_ml[at] = make_float2(M, sum);
             }
         }
     }
@@ -556,8 +571,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) pa_merge_block8_kernel(const
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t row = blockIdx.x;
     Span w;
-    span_of(a, a.context_lens[row / a.num_q_heads], 0, false, w);
-    if (w.nparts <= 1) return;
+    const int b = (int)(row / a.num_q_heads), out_row = row_of(a, b, false);
+    span_of(a, a.context_lens[b], 0, false, w);
+    if (w.nparts <= 1 || out_row < 0) return;
     const float2 *ml = a.part_ml + row * a.max_parts;
     const float4 *po = reinterpret_cast<const float4 *>(a.part_o + row * a.max_parts * kD);
     float M = -INFINITY, sum = 0.f;
@@ -611,7 +627,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) pa_merge_block8_kernel(const
         acc.w = fmaf(f, v.w, acc.w);
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * kD + 4 * lane) =
+    const int64_t out_head = (int64_t)out_row * a.num_q_heads + (row - (int64_t)b * a.num_q_heads);
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + out_head * kD + 4 * lane) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
@@ -776,28 +793,30 @@ extern "C" size_t pa_decode_block_fp8_workspace_bytes(int num_seqs, int num_q_he
     return workspace_of(num_seqs, num_q_heads, p.max_parts);
 }
 
-extern "C" pa_status pa_decode_block_fp8(void *out, const void *query, const void *key_cache, const void *value_cache,
-                                         const float *k_scales, const float *v_scales, const int32_t *block_tables,
-                                         const int32_t *context_lens, int num_seqs, int num_q_heads, int num_kv_heads,
-                                         int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
-                                         float scale, int window, int partition_size, void *workspace,
-                                         size_t workspace_bytes, int32_t *device_status, void *stream) {
-    if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
+extern "C" pa_status pa_decode_block_fp8_rows(void *out, const void *query, const void *key_cache, const void *value_cache,
+                                              const float *k_scales, const float *v_scales, const int32_t *block_tables,
+                                              const int32_t *context_lens, const int32_t *query_start, int num_seqs,
+                                              int num_query_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                              int block_size, int max_blocks_per_seq, int num_blocks, float scale,
+                                              int window, int partition_size, void *workspace, size_t workspace_bytes,
+                                              int32_t *device_status, void *stream) {
+    if (num_seqs < 0 || num_query_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
         block_size != kBlockSize || max_blocks_per_seq < 0 || max_blocks_per_seq > 0x7fffffff / kBlockSize ||
-        num_blocks <= 0 || window < 0 || !(scale == scale))
+        num_blocks <= 0 || window < 0 || !(scale == scale) || (query_start == nullptr && num_query_tokens != num_seqs))
         return PA_ERR_INVALID_ARG;
     const int group = num_q_heads / num_kv_heads, heads = heads_per_cta(group), splits = group / heads;
     Plan p;
     if (!plan_of(num_seqs, num_kv_heads * splits, max_blocks_per_seq, window, partition_size, &p))
         return PA_ERR_INVALID_ARG;
     if (head_dim != kD) return PA_ERR_UNSUPPORTED;
-    if (num_seqs == 0) return PA_OK;
+    if (num_seqs == 0 || num_query_tokens == 0) return PA_OK;
     if (!out || !query || !key_cache || !value_cache || !k_scales || !v_scales || !context_lens ||
         (!block_tables && max_blocks_per_seq > 0))
         return PA_ERR_INVALID_ARG;
     if (!aligned16(out) || !aligned16(query) || !aligned16(key_cache) || !aligned16(value_cache) ||
         ((reinterpret_cast<uintptr_t>(k_scales) | reinterpret_cast<uintptr_t>(v_scales) |
-          reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens)) & 3u))
+          reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens) |
+          reinterpret_cast<uintptr_t>(query_start)) & 3u))
         return PA_ERR_INVALID_ARG;
     const int64_t rows = (int64_t)num_blocks * num_kv_heads * kBlockSize;
     if (rows >= ((int64_t)1 << 31) ||
@@ -810,6 +829,8 @@ extern "C" pa_status pa_decode_block_fp8(void *out, const void *query, const voi
     a.query = query;
     a.block_tables = block_tables;
     a.context_lens = context_lens;
+    a.query_start = query_start;
+    a.num_rows = num_query_tokens;
     a.k_scales = k_scales;
     a.v_scales = v_scales;
     if (need > 0) {
@@ -841,4 +862,16 @@ extern "C" pa_status pa_decode_block_fp8(void *out, const void *query, const voi
     if (e != cudaSuccess) return cuda_failure(e, "pa_merge_block8_kernel launch");
     count_launches(1);
     return PA_OK;
+}
+
+extern "C" pa_status pa_decode_block_fp8(void *out, const void *query, const void *key_cache, const void *value_cache,
+                                         const float *k_scales, const float *v_scales, const int32_t *block_tables,
+                                         const int32_t *context_lens, int num_seqs, int num_q_heads, int num_kv_heads,
+                                         int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
+                                         float scale, int window, int partition_size, void *workspace,
+                                         size_t workspace_bytes, int32_t *device_status, void *stream) {
+    return pa_decode_block_fp8_rows(out, query, key_cache, value_cache, k_scales, v_scales, block_tables, context_lens,
+                                    nullptr, num_seqs, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                    max_blocks_per_seq, num_blocks, scale, window, partition_size, workspace,
+                                    workspace_bytes, device_status, stream);
 }

@@ -25,7 +25,7 @@ namespace {
 
 decltype(&pa_plan_step) f_plan;
 decltype(&pa_rope_cache_write) f_rope;
-decltype(&pa_decode_block_fp8) f_decode;
+decltype(&pa_decode_block_fp8_rows) f_decode;
 decltype(&pa_decode_block_fp8_workspace_bytes) f_decode_bytes;
 decltype(&pa_prefill_block_fp8) f_prefill;
 decltype(&pa_prefill_block_fp8_workspace_bytes) f_prefill_bytes;
@@ -376,13 +376,17 @@ at::Tensor workspace_of(PyObject *given, size_t need, const at::Tensor &q, Pools
 }
 
 // decode_block_fp8(query, key_cache, value_cache, k_scales, v_scales, block_tables, context_lens, scale or
-//                  None, window, out, partition_size, workspace, status, stream) -> out
+//                  None, window, out, partition_size, workspace, status, stream, query_start or None) -> out
 PyObject *decode_block_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 14, [&]() -> PyObject * {
+    return guarded(n, 15, [&]() -> PyObject * {
         const int window = int_of(integer(a[8]), "window"), partition = int_of(integer(a[10]), "partition_size");
         const at::Tensor &q = tensor(a[0], "query"), &lens = tensor(a[6], "context_lens");
-        if (q.dim() == 3 && lens.sizes() != at::IntArrayRef{q.size(0)}) bad_value("context_lens must be [num_seqs]");
+        const at::Tensor *start = optional_tensor(a[14], "query_start");
+        if (!start && q.dim() == 3 && lens.sizes() != at::IntArrayRef{q.size(0)}) bad_value("context_lens must be [num_seqs]");
+        if (start && (lens.dim() != 1 || start->sizes() != at::IntArrayRef{lens.size(0) + 1}))
+            bad_value("query_start must be [num_seqs + 1]");
         Pools p = pools_of(a, a[12]);
+        const int32_t *p_start = start ? address<int32_t>(*start, "query_start", p.dev, at::kInt) : nullptr;
         const float scale = a[7] == Py_None ? (float)(1.0 / std::sqrt((double)p.head_dim)) : (float)number(a[7]);
         Place place(p.dev, a[13]);
         at::Tensor out = output_of(a[9], q, p.dev);
@@ -391,9 +395,9 @@ PyObject *decode_block_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                                               (int)kBlock, window, partition);
         at::Tensor w = workspace_of(a[11], need, q, p);
         const pa_status rc = call(f_decode, out.data_ptr(), (const void *)p.query, (const void *)p.kc, (const void *)p.vc, p.ks,
-                                  p.vs, p.tables, p.lens, p.num_seqs, p.hq, p.hkv, p.head_dim, (int)kBlock, p.max_blocks,
-                                  p.num_blocks, scale, window, partition, p.workspace, p.workspace_bytes, p.status,
-                                  (void *)place.at);
+                                  p.vs, p.tables, p.lens, p_start, p.num_seqs, int_of(q.size(0), "query"), p.hq, p.hkv,
+                                  p.head_dim, (int)kBlock, p.max_blocks, p.num_blocks, scale, window, partition, p.workspace,
+                                  p.workspace_bytes, p.status, (void *)place.at);
         if (rc != PA_OK) return PyLong_FromLong(rc);
         return THPVariable_Wrap(out);
     });

@@ -141,6 +141,36 @@ def test_decode_queries_of_any_size(pkv, hq, hkv, longest):
     assert int(status.item()) == 0
 
 
+@pytest.mark.parametrize("hq,hkv,partition,longest,seqs", [(8, 2, 0, 400, 7), (14, 2, 64, 400, 7), (16, 1, 0, 3000, 5),
+                                                           (32, 16, 0, 200, 60)])
+def test_decode_rows_of_a_plan(pkv, hq, hkv, partition, longest, seqs):
+    """Rows where query_start puts them: sequences that bring nothing, more than one token, or entries outside the
+    rows are passed over, and the rows of no sequence are left alone."""
+    from paged_kv_cache_100_gb300 import _lib
+    rng = np.random.default_rng(seqs)
+    lens = [int(x) for x in rng.integers(1, longest, seqs - 1)] + [longest]
+    p = Pool(hq, lens, hkv, spread=0.7)
+    for new, bit in ((rng.integers(0, 2, seqs), 0), ([1] * seqs, 0), ([0] * seqs, 0),
+                     ([2] + [1] * (seqs - 2) + [0], _lib.PA_DEV_BAD_QUERY_LEN), ([1, 1, "bad"] + [1] * (seqs - 3), _lib.PA_DEV_BAD_CONTEXT_LEN)):
+        counts = [0 if n == "bad" else int(n) for n in new]
+        start = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        total = int(start[-1])
+        if "bad" in list(new):
+            start[2] = -4                                    # sequences 1 and 2
+        rows = [(b, lens[b] - 1) for b in range(seqs) if counts[b] == 1 and not ("bad" in list(new) and b in (1, 2))]
+        at = [int(start[b]) for b, _ in rows]
+        q = _query(p, total + 3, hq)
+        out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = pkv.decode_block_fp8(q.cuda(), *p.device(), query_start=torch.from_numpy(start).cuda(), partition_size=partition,
+                                   out=out, status=status)
+        assert got is out and int(status.item()) == bit
+        ref, bound = p.reference(q.double().numpy()[at], rows, D ** -0.5)
+        _check(out[at], ref, bound, f"{bit}")
+        rest = np.setdiff1d(np.arange(total + 3), at)
+        assert (out[torch.from_numpy(rest).cuda()] == 7.0).all()
+
+
 def test_decode_flags_bad_scales_tables_lengths_and_queries(pkv):
     from paged_kv_cache_100_gb300 import _lib
     lens = [40, 40]

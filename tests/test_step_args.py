@@ -180,3 +180,27 @@ def test_bindings_refuse_shapes_and_types():
         pkv.decode_block_fp8(q, kc, kc, sc, sc, z(1, 1), z(2))
     with pytest.raises(ValueError):
         pkv.decode_block_fp8(q, z(2, 1, 8, 128, dt=torch.uint8), kc, sc, sc, z(1, 1), z(1))
+
+
+DECODE_ROWS = dict(out=A, query=2 * A, key_cache=3 * A, value_cache=4 * A, k_scales=5 * A, v_scales=6 * A, tables=7 * A,
+                   lens=8 * A, start=9 * A, num_seqs=3, tokens=2, hq=8, hkv=2, dim=128, block_size=16, max_blocks=4, num_blocks=8,
+                   scale=0.1, window=0, partition=0, workspace=None, workspace_bytes=0, status=None, stream=None)
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(tokens=-1), BAD), (dict(start=None), BAD), (dict(start=9 * A + 2), BAD), (dict(num_seqs=-1), BAD), (dict(hq=7), BAD),
+    (dict(query=None), BAD), (dict(dim=64), UNSUPPORTED), (dict(max_blocks=4000), WORKSPACE),
+    (dict(tokens=0, query=None), OK), (dict(num_seqs=0, tokens=0, start=None), OK), (dict(num_seqs=0), OK)])
+def test_decode_block_fp8_rows_refuses(lib, over, expect):
+    assert _call(lib.pa_decode_block_fp8_rows, DECODE_ROWS, over) == expect
+
+
+def test_decode_binding_checks_query_start():
+    z = lambda *s, dt=torch.int32: torch.zeros(*s, dtype=dt)  # noqa: E731
+    kc, sc = z(2, 1, 16, 128, dt=torch.uint8), z(2, 1, dt=torch.float32)
+    q = z(1, 1, 128, dt=torch.bfloat16)
+    for start in (z(2), z(4), z(3, 1)):
+        with pytest.raises(ValueError, match="query_start"):
+            pkv.decode_block_fp8(q, kc, kc, sc, sc, z(2, 1), z(2), query_start=start)
+    with pytest.raises(TypeError, match="query_start"):
+        pkv.decode_block_fp8(q, kc, kc, sc, sc, z(2, 1), z(2), query_start=3)

@@ -143,3 +143,30 @@ def test_captured_decode_step_replays(pkv):
         assert torch.equal(out, direct[i]), i
     assert torch.equal(a.tables, b.tables) and torch.equal(a.kc, b.kc) and torch.equal(a.vc, b.vc)
     assert int(a.status.item()) == 0 and int(b.status.item()) == 0
+
+
+def test_steps_in_which_some_sequences_bring_nothing(pkv):
+    """Decode steps of a padded batch: idle sequences, and one whose table is full (it is passed over and flagged),
+    move the others' rows in the flat list; query_start says where they are."""
+    from paged_kv_cache_100_gb300 import _lib
+    seqs, blocks, width = 7, 64, 3
+    s = Serving(pkv, seqs, blocks, width)
+    g = torch.Generator().manual_seed(9)
+    prompts = [20, 0, 48, 17, 3, 30, 9]                      # the third one's table is full
+    x = torch.randn(sum(prompts), HQ + 2 * HKV, D, generator=g).to(torch.bfloat16)
+    out, q, p = s.step(x.cuda(), torch.tensor(prompts, dtype=torch.int32, device="cuda"), max(prompts))
+    s.lens, s.num_free = p.context_lens, p.num_free
+    for step in range(4):
+        new = [int(b % 3 != step % 3) for b in range(seqs)]
+        taken = [n if not (b == 2 and n) else 0 for b, n in enumerate(new)]
+        x = torch.randn(seqs, HQ + 2 * HKV, D, generator=g).to(torch.bfloat16).cuda()
+        s.status.zero_()
+        p = pkv.plan_step(s.tables, s.lens, torch.tensor(new, dtype=torch.int32, device="cuda"), s.free, s.num_free, seqs, blocks,
+                          status=s.status)
+        q = pkv.rope_cache_write(x[:, :HQ], x[:, HQ:HQ + HKV], x[:, HQ + HKV:], p.positions, s.rope, s.kc, s.vc, p.slot_mapping,
+                                 k_scales=s.ks, v_scales=s.vs, status=s.status)
+        out = pkv.decode_block_fp8(q, s.kc, s.vc, s.ks, s.vs, s.tables, p.context_lens, query_start=p.query_start, status=s.status)
+        assert int(s.status.item()) == (_lib.PA_DEV_BAD_CONTEXT_LEN if new[2] else 0)
+        assert p.query_start.tolist() == [0] + np.cumsum(taken).tolist()
+        _check(s, out, q, p, taken)
+        s.lens, s.num_free = p.context_lens, p.num_free
