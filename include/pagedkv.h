@@ -374,6 +374,15 @@ pa_status pa_block_copy(void *key_cache, void *value_cache, const int32_t *src_d
                         pa_dtype dtype, int32_t *device_status, void *stream);
 
 /*
+ * The same over E4M3 pools with one scale per block and KV head: the blocks'
+ * scales (device float [num_blocks][num_kv_heads]) are copied with their codes.
+ * pa_block_copy alone would leave block dst under its own old scales.
+ */
+pa_status pa_block_copy_scaled(void *key_cache, void *value_cache, float *k_scales, float *v_scales,
+                               const int32_t *src_dst, int num_pairs, int num_kv_heads, int head_dim,
+                               int block_size, int num_blocks, int32_t *device_status, void *stream);
+
+/*
  * Chunked (paged) prefill attention ("PagedAttention por dentro", section
  * "Chunked prefill integrado con paged KV": prefill is cut into chunks that run
  * over the same paged KV cache as decode).  Sequence b brings a chunk of
@@ -664,6 +673,22 @@ pa_status pa_swap_out(const void *key_cache, const void *value_cache, const int3
 pa_status pa_swap_in(void *key_cache, void *value_cache, const int32_t *block_ids, int num_ids,
                      const void *staging, int num_kv_heads, int head_dim, int block_size,
                      int num_blocks, pa_dtype dtype, int32_t *device_status, void *stream);
+
+/*
+ * The same over E4M3 pools with one scale per block and KV head: the scales
+ * (device float [num_blocks][num_kv_heads]) leave and come back with their
+ * blocks, through
+ *  scale_staging  float [num_ids][2][num_kv_heads], K's then V's: memory of the
+ *                 same kinds as staging, 4-byte aligned
+ */
+pa_status pa_swap_out_scaled(const void *key_cache, const void *value_cache, const float *k_scales,
+                             const float *v_scales, const int32_t *block_ids, int num_ids, void *staging,
+                             float *scale_staging, int num_kv_heads, int head_dim, int block_size,
+                             int num_blocks, int32_t *device_status, void *stream);
+pa_status pa_swap_in_scaled(void *key_cache, void *value_cache, float *k_scales, float *v_scales,
+                            const int32_t *block_ids, int num_ids, const void *staging,
+                            const float *scale_staging, int num_kv_heads, int head_dim, int block_size,
+                            int num_blocks, int32_t *device_status, void *stream);
 
 /*
  * Host block manager: one pool of num_blocks blocks of block_size tokens,

@@ -399,17 +399,36 @@ def cache_write(key_cache, value_cache, key, value, slot_mapping, *, status=None
     check(rc, "pa_cache_write")
 
 
-def block_copy(key_cache, value_cache, src_dst, *, status=None, stream=None):
-    """Copy whole physical blocks (copy-on-write pairs) in both pools (``pa_block_copy``)."""
+def _block_scales(key_cache, value_cache, k_scales, v_scales):
+    """Addresses of block-scaled pools' scales, which go with their blocks (None, None without)."""
+    torch = _torch()
+    if k_scales is None and v_scales is None:
+        return None, None
+    if not (_is_fp8(key_cache) and _is_fp8(value_cache)):
+        raise TypeError("k_scales / v_scales belong to pools of E4M3 codes")
+    if k_scales is None or v_scales is None or k_scales.shape != key_cache.shape[:2] or v_scales.shape != key_cache.shape[:2]:
+        raise ValueError("k_scales / v_scales must be [num_blocks][num_kv_heads]")
+    return _dev(k_scales, "k_scales", torch.float32), _dev(v_scales, "v_scales", torch.float32)
+
+
+def block_copy(key_cache, value_cache, src_dst, *, k_scales=None, v_scales=None, status=None, stream=None):
+    """Copy whole physical blocks (copy-on-write pairs) in both pools (``pa_block_copy``).  Pools with a
+    scale per block need them here: ``k_scales`` / ``v_scales`` are copied with the blocks."""
     torch = _torch()
     NB, Hkv, BS, D = key_cache.shape
     P = src_dst.shape[0]
     if src_dst.dim() != 2 or src_dst.shape[1] != 2:
         raise ValueError("src_dst must be [num_pairs][2]")
-    rc = lib().pa_block_copy(
-        _dev(key_cache, "key_cache"), _dev(value_cache, "value_cache"),
-        _dev(src_dst, "src_dst", torch.int32), P, Hkv, D, BS, NB, _dtype_code(key_cache),
-        _status_ptr(status), _stream(stream, key_cache))
+    ks, vs = _block_scales(key_cache, value_cache, k_scales, v_scales)
+    pools = _dev(key_cache, "key_cache"), _dev(value_cache, "value_cache")
+    pairs = _dev(src_dst, "src_dst", torch.int32)
+    if ks is not None:
+        rc = lib().pa_block_copy_scaled(*pools, ks, vs, pairs, P, Hkv, D, BS, NB, _status_ptr(status),
+                                        _stream(stream, key_cache))
+        check(rc, "pa_block_copy_scaled")
+        return
+    rc = lib().pa_block_copy(*pools, pairs, P, Hkv, D, BS, NB, _dtype_code(key_cache), _status_ptr(status),
+                             _stream(stream, key_cache))
     check(rc, "pa_block_copy")
 
 
@@ -582,6 +601,12 @@ def _staging_ptr(t, nbytes):
     return t.data_ptr()
 
 
+def _scale_staging_ptr(t, count):
+    if t.dtype != _torch().float32:
+        raise TypeError("scale_staging must be float32")
+    return _staging_ptr(t, 4 * count)
+
+
 def _swap_geometry(key_cache, block_ids):
     torch = _torch()
     NB, Hkv, BS, D = key_cache.shape
@@ -593,27 +618,50 @@ def _swap_geometry(key_cache, block_ids):
     return NB, Hkv, BS, D, code, n, nbytes, _dev(block_ids, "block_ids", torch.int32)
 
 
-def swap_out(key_cache, value_cache, block_ids, staging=None, *, status=None, stream=None):
+def swap_out(key_cache, value_cache, block_ids, staging=None, *, k_scales=None, v_scales=None, scale_staging=None,
+             status=None, stream=None):
     """Copy the listed blocks (both pools) into ``staging`` ``[n][2][Hkv][16][D]``
     (``pa_swap_out``).  By default the staging is new page-locked host memory,
     written by the kernel over the CPU-GPU link; returns it (complete once the
-    stream reaches this point)."""
+    stream reaches this point).  Pools with a scale per block need ``k_scales`` /
+    ``v_scales`` here and in ``swap_in``: they go into ``scale_staging`` float32
+    ``[n][2][Hkv]``, and the pair of stagings is returned."""
     torch = _torch()
     NB, Hkv, BS, D, code, n, nbytes, ids = _swap_geometry(key_cache, block_ids)
+    ks, vs = _block_scales(key_cache, value_cache, k_scales, v_scales)
     if staging is None:
         staging = torch.empty((n, 2, Hkv, BS, D), dtype=key_cache.dtype, pin_memory=True)
-    rc = lib().pa_swap_out(_dev(key_cache, "key_cache"), _dev(value_cache, "value_cache"), ids,
-                           n, _staging_ptr(staging, nbytes), Hkv, D, BS, NB, code,
+    pools = _dev(key_cache, "key_cache"), _dev(value_cache, "value_cache")
+    if ks is not None:
+        if scale_staging is None:
+            scale_staging = torch.empty((n, 2, Hkv), dtype=torch.float32, pin_memory=True)
+        rc = lib().pa_swap_out_scaled(*pools, ks, vs, ids, n, _staging_ptr(staging, nbytes),
+                                      _scale_staging_ptr(scale_staging, n * 2 * Hkv), Hkv, D, BS, NB,
+                                      _status_ptr(status), _stream(stream, key_cache))
+        check(rc, "pa_swap_out_scaled")
+        return staging, scale_staging
+    rc = lib().pa_swap_out(*pools, ids, n, _staging_ptr(staging, nbytes), Hkv, D, BS, NB, code,
                            _status_ptr(status), _stream(stream, key_cache))
     check(rc, "pa_swap_out")
     return staging
 
 
-def swap_in(key_cache, value_cache, block_ids, staging, *, status=None, stream=None):
-    """Copy ``staging`` back into the listed blocks (``pa_swap_in``); ids distinct."""
+def swap_in(key_cache, value_cache, block_ids, staging, *, k_scales=None, v_scales=None, scale_staging=None,
+            status=None, stream=None):
+    """Copy ``staging`` (and ``scale_staging`` into ``k_scales`` / ``v_scales``) back into the listed
+    blocks (``pa_swap_in``); ids distinct."""
     NB, Hkv, BS, D, code, n, nbytes, ids = _swap_geometry(key_cache, block_ids)
-    rc = lib().pa_swap_in(_dev(key_cache, "key_cache"), _dev(value_cache, "value_cache"), ids,
-                          n, _staging_ptr(staging, nbytes), Hkv, D, BS, NB, code,
+    ks, vs = _block_scales(key_cache, value_cache, k_scales, v_scales)
+    if (ks is None) != (scale_staging is None):
+        raise ValueError("k_scales, v_scales and scale_staging go together")
+    pools = _dev(key_cache, "key_cache"), _dev(value_cache, "value_cache")
+    if ks is not None:
+        rc = lib().pa_swap_in_scaled(*pools, ks, vs, ids, n, _staging_ptr(staging, nbytes),
+                                     _scale_staging_ptr(scale_staging, n * 2 * Hkv), Hkv, D, BS, NB,
+                                     _status_ptr(status), _stream(stream, key_cache))
+        check(rc, "pa_swap_in_scaled")
+        return
+    rc = lib().pa_swap_in(*pools, ids, n, _staging_ptr(staging, nbytes), Hkv, D, BS, NB, code,
                           _status_ptr(status), _stream(stream, key_cache))
     check(rc, "pa_swap_in")
 

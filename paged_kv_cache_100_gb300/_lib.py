@@ -68,6 +68,9 @@ SIGNATURES = {
     "pa_prefill_block_fp8_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32, i32, i32]),
     "pa_prefill_block_fp8": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
                                    i32, i32, i32, f32, i32, vp, sz, vp, vp]),
+    "pa_block_copy_scaled": (i32, [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp]),
+    "pa_swap_out_scaled": (i32, [vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp]),
+    "pa_swap_in_scaled": (i32, [vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp]),
     "pa_swap_bytes": (sz, [i32, i32, i32, i32]),
     "pa_swap_out": (i32, [vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, vp, vp]),
     "pa_swap_in": (i32, [vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, vp, vp]),

@@ -124,8 +124,15 @@ pa_cache_write_fp8_kernel(uint4 *__restrict__ kc, uint4 *__restrict__ vc,
 constexpr int kCopyThreads = 256;
 constexpr int kChunksPerThread = 4;
 
+// Scales of block-scaled pools, which go with their blocks: [num_blocks][heads], or k
+// nullptr; staged [id][K, V][heads] by the swaps.
+struct Scales {
+    float *k, *v, *stage;
+    int heads;
+};
+
 __global__ void __launch_bounds__(kCopyThreads)
-pa_block_copy_kernel(uint4 *__restrict__ kc, uint4 *__restrict__ vc,
+pa_block_copy_kernel(uint4 *__restrict__ kc, uint4 *__restrict__ vc, Scales scales,
                      const int32_t *__restrict__ src_dst, int num_pairs, int64_t chunks_per_block,
                      int num_blocks, int32_t *status) {
     grid_dependency_wait();
@@ -148,6 +155,12 @@ pa_block_copy_kernel(uint4 *__restrict__ kc, uint4 *__restrict__ vc,
     if (__syncthreads_or(clash)) {
         if (blockIdx.y == 0 && threadIdx.x == 0) report(status, PA_DEV_BAD_COPY_PAIR);
         return;
+    }
+    if (scales.k != nullptr && blockIdx.y == 0) {
+        for (int h = threadIdx.x; h < scales.heads; h += kCopyThreads) {
+            scales.k[(int64_t)dst * scales.heads + h] = scales.k[(int64_t)src * scales.heads + h];
+            scales.v[(int64_t)dst * scales.heads + h] = scales.v[(int64_t)src * scales.heads + h];
+        }
     }
     const int64_t first = (int64_t)blockIdx.y * kCopyThreads * kChunksPerThread + threadIdx.x;
     const uint4 *ks = kc + (int64_t)src * chunks_per_block;
@@ -180,7 +193,7 @@ pa_block_copy_kernel(uint4 *__restrict__ kc, uint4 *__restrict__ vc,
 // flight before it stores.
 template <bool kOut>
 __global__ void __launch_bounds__(kCopyThreads)
-pa_swap_kernel(uint4 *__restrict__ kc, uint4 *__restrict__ vc, uint4 *__restrict__ stage,
+pa_swap_kernel(uint4 *__restrict__ kc, uint4 *__restrict__ vc, uint4 *__restrict__ stage, Scales scales,
                const int32_t *__restrict__ block_ids, int64_t chunks_per_block, int num_blocks,
                int32_t *status) {
     grid_dependency_wait();
@@ -190,6 +203,11 @@ pa_swap_kernel(uint4 *__restrict__ kc, uint4 *__restrict__ vc, uint4 *__restrict
         if (blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0)
             report(status, PA_DEV_BAD_BLOCK_ID);
         return;
+    }
+    if (scales.k != nullptr && blockIdx.y == 0) {
+        float *of = (blockIdx.z == 0 ? scales.k : scales.v) + (int64_t)id * scales.heads;
+        float *staged = scales.stage + ((int64_t)blockIdx.x * 2 + blockIdx.z) * scales.heads;
+        for (int h = threadIdx.x; h < scales.heads; h += kCopyThreads) (kOut ? staged : of)[h] = (kOut ? of : staged)[h];
     }
     uint4 *pool = (blockIdx.z == 0 ? kc : vc) + (int64_t)id * chunks_per_block;
     uint4 *st = stage + ((int64_t)blockIdx.x * 2 + blockIdx.z) * chunks_per_block;
@@ -275,10 +293,11 @@ extern "C" pa_status pa_cache_write(void *key_cache, void *value_cache, const vo
     return PA_OK;
 }
 
-extern "C" pa_status pa_block_copy(void *key_cache, void *value_cache, const int32_t *src_dst,
-                                   int num_pairs, int num_kv_heads, int head_dim, int block_size,
-                                   int num_blocks, pa_dtype dtype, int32_t *device_status,
-                                   void *stream) {
+namespace {
+
+pa_status block_copy(void *key_cache, void *value_cache, const Scales &scales, const int32_t *src_dst, int num_pairs,
+                     int num_kv_heads, int head_dim, int block_size, int num_blocks, pa_dtype dtype,
+                     int32_t *device_status, void *stream) {
     if (num_pairs < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size != kBlockSize ||
         num_blocks <= 0)
         return PA_ERR_INVALID_ARG;
@@ -298,11 +317,34 @@ extern "C" pa_status pa_block_copy(void *key_cache, void *value_cache, const int
     dim3 grid((unsigned)num_pairs, (unsigned)slices);
     cudaError_t e = launch_chained(
         pa_block_copy_kernel, grid, dim3(kCopyThreads), 0, static_cast<cudaStream_t>(stream),
-        static_cast<uint4 *>(key_cache), static_cast<uint4 *>(value_cache), src_dst, num_pairs,
+        static_cast<uint4 *>(key_cache), static_cast<uint4 *>(value_cache), scales, src_dst, num_pairs,
         chunks, num_blocks, device_status);
     if (e != cudaSuccess) return cuda_failure(e, "pa_block_copy_kernel launch");
     count_launches(1);
     return PA_OK;
+}
+
+bool scales_ok(const float *k_scales, const float *v_scales) {
+    return k_scales && v_scales &&
+           ((reinterpret_cast<uintptr_t>(k_scales) | reinterpret_cast<uintptr_t>(v_scales)) & 3u) == 0;
+}
+
+}  // namespace
+
+extern "C" pa_status pa_block_copy(void *key_cache, void *value_cache, const int32_t *src_dst,
+                                   int num_pairs, int num_kv_heads, int head_dim, int block_size,
+                                   int num_blocks, pa_dtype dtype, int32_t *device_status,
+                                   void *stream) {
+    return block_copy(key_cache, value_cache, Scales{}, src_dst, num_pairs, num_kv_heads, head_dim, block_size,
+                      num_blocks, dtype, device_status, stream);
+}
+
+extern "C" pa_status pa_block_copy_scaled(void *key_cache, void *value_cache, float *k_scales, float *v_scales,
+                                          const int32_t *src_dst, int num_pairs, int num_kv_heads, int head_dim,
+                                          int block_size, int num_blocks, int32_t *device_status, void *stream) {
+    if (num_pairs > 0 && !scales_ok(k_scales, v_scales)) return PA_ERR_INVALID_ARG;
+    return block_copy(key_cache, value_cache, Scales{k_scales, v_scales, nullptr, num_kv_heads}, src_dst, num_pairs,
+                      num_kv_heads, head_dim, block_size, num_blocks, PA_DTYPE_FP8_E4M3, device_status, stream);
 }
 
 extern "C" pa_status pa_cache_write_fp8(void *key_cache, void *value_cache, const void *key,
@@ -370,7 +412,7 @@ pa_status device_address(const void *p, void **dev) {
     }
 }
 
-pa_status swap_common(bool out, void *key_cache, void *value_cache, const int32_t *block_ids,
+pa_status swap_common(bool out, void *key_cache, void *value_cache, Scales scales, const int32_t *block_ids,
                       int num_ids, void *staging, int num_kv_heads, int head_dim, int block_size,
                       int num_blocks, pa_dtype dtype, int32_t *device_status, void *stream) {
     if (num_ids < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size != kBlockSize ||
@@ -389,6 +431,12 @@ pa_status swap_common(bool out, void *key_cache, void *value_cache, const int32_
     pa_status st = device_address(staging, &stage);
     if (st != PA_OK) return st;
     if (!aligned16(stage)) return PA_ERR_INVALID_ARG;
+    if (scales.k != nullptr) {
+        void *staged = nullptr;
+        st = device_address(scales.stage, &staged);
+        if (st != PA_OK) return st;
+        scales.stage = static_cast<float *>(staged);
+    }
     const int64_t chunks = block_bytes / 16;
     const int64_t per_cta = (int64_t)kCopyThreads * kChunksPerThread;
     const int64_t slices = (chunks + per_cta - 1) / per_cta;
@@ -398,7 +446,7 @@ pa_status swap_common(bool out, void *key_cache, void *value_cache, const int32_
     cudaError_t e = launch_chained(kernel, grid, dim3(kCopyThreads), 0,
                                    static_cast<cudaStream_t>(stream),
                                    static_cast<uint4 *>(key_cache), static_cast<uint4 *>(value_cache),
-                                   static_cast<uint4 *>(stage), block_ids, chunks, num_blocks,
+                                   static_cast<uint4 *>(stage), scales, block_ids, chunks, num_blocks,
                                    device_status);
     if (e != cudaSuccess) return cuda_failure(e, "pa_swap_kernel launch");
     count_launches(1);
@@ -418,7 +466,7 @@ extern "C" pa_status pa_swap_out(const void *key_cache, const void *value_cache,
                                  const int32_t *block_ids, int num_ids, void *staging,
                                  int num_kv_heads, int head_dim, int block_size, int num_blocks,
                                  pa_dtype dtype, int32_t *device_status, void *stream) {
-    return swap_common(true, const_cast<void *>(key_cache), const_cast<void *>(value_cache),
+    return swap_common(true, const_cast<void *>(key_cache), const_cast<void *>(value_cache), Scales{},
                        block_ids, num_ids, staging, num_kv_heads, head_dim, block_size,
                        num_blocks, dtype, device_status, stream);
 }
@@ -427,7 +475,31 @@ extern "C" pa_status pa_swap_in(void *key_cache, void *value_cache, const int32_
                                 int num_ids, const void *staging, int num_kv_heads, int head_dim,
                                 int block_size, int num_blocks, pa_dtype dtype,
                                 int32_t *device_status, void *stream) {
-    return swap_common(false, key_cache, value_cache, block_ids, num_ids,
+    return swap_common(false, key_cache, value_cache, Scales{}, block_ids, num_ids,
                        const_cast<void *>(staging), num_kv_heads, head_dim, block_size,
                        num_blocks, dtype, device_status, stream);
+}
+
+extern "C" pa_status pa_swap_out_scaled(const void *key_cache, const void *value_cache, const float *k_scales,
+                                        const float *v_scales, const int32_t *block_ids, int num_ids, void *staging,
+                                        float *scale_staging, int num_kv_heads, int head_dim, int block_size,
+                                        int num_blocks, int32_t *device_status, void *stream) {
+    if (num_ids > 0 && (!scales_ok(k_scales, v_scales) || !scales_ok(scale_staging, scale_staging)))
+        return PA_ERR_INVALID_ARG;
+    return swap_common(true, const_cast<void *>(key_cache), const_cast<void *>(value_cache),
+                       Scales{const_cast<float *>(k_scales), const_cast<float *>(v_scales), scale_staging, num_kv_heads},
+                       block_ids, num_ids, staging, num_kv_heads, head_dim, block_size, num_blocks, PA_DTYPE_FP8_E4M3,
+                       device_status, stream);
+}
+
+extern "C" pa_status pa_swap_in_scaled(void *key_cache, void *value_cache, float *k_scales, float *v_scales,
+                                       const int32_t *block_ids, int num_ids, const void *staging,
+                                       const float *scale_staging, int num_kv_heads, int head_dim, int block_size,
+                                       int num_blocks, int32_t *device_status, void *stream) {
+    if (num_ids > 0 && (!scales_ok(k_scales, v_scales) || !scales_ok(scale_staging, scale_staging)))
+        return PA_ERR_INVALID_ARG;
+    return swap_common(false, key_cache, value_cache,
+                       Scales{k_scales, v_scales, const_cast<float *>(scale_staging), num_kv_heads}, block_ids, num_ids,
+                       const_cast<void *>(staging), num_kv_heads, head_dim, block_size, num_blocks, PA_DTYPE_FP8_E4M3,
+                       device_status, stream);
 }

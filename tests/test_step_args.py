@@ -204,3 +204,24 @@ def test_decode_binding_checks_query_start():
             pkv.decode_block_fp8(q, kc, kc, sc, sc, z(2, 1), z(2), query_start=start)
     with pytest.raises(TypeError, match="query_start"):
         pkv.decode_block_fp8(q, kc, kc, sc, sc, z(2, 1), z(2), query_start=3)
+
+
+def test_block_scales_refusals(lib):
+    copy = dict(kc=A, vc=2 * A, ks=3 * A, vs=4 * A, pairs=5 * A, n=1, hkv=2, dim=128, block=16, blocks=4, status=None, stream=None)
+    for over, expect in ((dict(ks=None), BAD), (dict(vs=None), BAD), (dict(ks=3 * A + 2), BAD), (dict(kc=None), BAD), (dict(pairs=None), BAD),
+                         (dict(blocks=0), BAD), (dict(block=8), BAD), (dict(n=-1), BAD), (dict(n=0, ks=None), OK)):
+        assert _call(lib.pa_block_copy_scaled, copy, over) == expect
+    swap = dict(kc=A, vc=2 * A, ks=3 * A, vs=4 * A, ids=5 * A, n=1, staging=6 * A, scales=7 * A, hkv=2, dim=128, block=16, blocks=4,
+                status=None, stream=None)
+    for fn in (lib.pa_swap_out_scaled, lib.pa_swap_in_scaled):
+        for over, expect in ((dict(ks=None), BAD), (dict(vs=None), BAD), (dict(scales=None), BAD), (dict(scales=7 * A + 1), BAD),
+                             (dict(staging=None), BAD), (dict(ids=None), BAD), (dict(n=-1), BAD), (dict(n=0, ks=None, scales=None), OK)):
+            assert _call(fn, swap, over) == expect
+    z = lambda *s, dt=torch.int32: torch.zeros(*s, dtype=dt)  # noqa: E731
+    codes, rows, sc = z(2, 1, 16, 128, dt=torch.uint8), z(2, 1, 16, 128, dt=torch.bfloat16), z(2, 1, dt=torch.float32)
+    with pytest.raises(ValueError, match="k_scales"):
+        pkv.block_copy(codes, codes, z(1, 2), k_scales=sc)
+    with pytest.raises(ValueError, match="k_scales"):
+        pkv.block_copy(codes, codes, z(1, 2), k_scales=sc[:1], v_scales=sc)
+    with pytest.raises(TypeError, match="E4M3"):
+        pkv.block_copy(rows, rows, z(1, 2), k_scales=sc, v_scales=sc)
