@@ -481,8 +481,9 @@ pa_status pa_plan_step(int32_t *block_tables, const int32_t *context_lens, const
  *                       those that turn less than beta_slow times, a linear
  *                       ramp between (YaRN, Peng et al. 2023); attention factor
  *                       0.1 ln(factor) + 1 for a factor above 1
- *  turns             host uint64 [rotary_dim / 2]: theta_i / (2 pi), as a
- *                    64-bit fraction of a whole turn
+ *  turns             host uint64 [rotary_dim / 2]: theta_i / (2 pi), as the
+ *                    nearest 64-bit fraction of a whole turn (a pair that turns
+ *                    2^20 times or more a position is refused)
  *  attention_factor  host double: multiplies cos and sin (1 otherwise)
  * Host only; no CUDA call.
  */
@@ -514,7 +515,8 @@ pa_status pa_rotary_turns(uint64_t *turns, double *attention_factor, int rotary_
  *  positions         device int32 [num_tokens], any value
  *  turns             device uint64 [rotary_dim / 2] (pa_rotary_turns).  The
  *                    angle is the product modulo a whole turn in 64-bit
- *                    integers: exact to 2^-32 of a turn at any position
+ *                    integers, right to 2^-32 of a turn at any position; 32-bit
+ *                    rotations round it to 24 bits
  *  rotary_dim        even, 0 .. head_dim (0: no rotation)
  *  slot_mapping      device int64 [num_tokens]; negative = no cache write (the
  *                    query is turned all the same); a slot past the pool is

@@ -10,8 +10,8 @@
 //   y0 = x0 cos - x1 sin,  y1 = x1 cos + x0 sin   (times the attention factor).
 // Angles.  At far positions p * theta_i in 32 bits has lost the angle (p = 10^6:
 // an error of 0.06 rad), so theta_i comes as a 64-bit fixed-point fraction of a
-// full turn: the 64-bit product p * turns_i wraps at whole turns by itself and
-// its upper half is the angle to 2^-32 of a turn at any position.
+// full turn, the nearest one: the 64-bit product p * turns_i wraps at whole turns by
+// itself and its upper half is the angle to 2^-32 of a turn at any position.
 //
 // Block scales.  A block's scale is the smallest power of two 2^e, e in
 // [-32, 31], that holds its largest magnitude: amax <= 448 * 2^e.  E4M3 is a
@@ -971,6 +971,54 @@ bool rows_touch(const void *p, int64_t s, int64_t w, const void *q, int64_t t, i
     return r < w || r + v > s;
 }
 
+// Numbers of about 106 bits, hi + lo with lo at most half a unit of hi's last place (T. J.
+// Dekker, "A floating-point technique for extending the available precision", 1971).  A
+// frequency has to hold 64 bits of a turn, as positions up to 2^31 multiply its
+// error: in 53 bits the angle of position 2^31 would be off by 2^-25 of a turn.  Products are
+// written with fma, so that a compiler has none to contract and every machine agrees.
+struct Wide {
+    double hi, lo;
+};
+Wide sum_of(double a, double b) {
+    const double s = a + b, t = s - a;
+    return {s, (a - (s - t)) + (b - t)};
+}
+Wide plus(Wide a, Wide b) {
+    const Wide s = sum_of(a.hi, b.hi);
+    return sum_of(s.hi, s.lo + (a.lo + b.lo));
+}
+Wide times(Wide a, Wide b) {
+    const double p = a.hi * b.hi;
+    return sum_of(p, std::fma(a.lo, b.hi, std::fma(a.hi, b.lo, std::fma(a.hi, b.hi, -p))));
+}
+Wide times(Wide a, double b) { return times(a, Wide{b, 0.0}); }
+Wide over(Wide a, double b) {
+    const double q = a.hi / b;
+    return sum_of(q, (std::fma(-q, b, a.hi) + a.lo) / b);
+}
+// e^x, |x| below 700: 2^k e^r, e^r by its series at r / 512.
+Wide exp_of(Wide x) {
+    const double k = std::nearbyint(x.hi * 1.4426950408889634);
+    Wide r = plus(x, times(Wide{0x1.62e42fefa39efp-1, 0x1.abc9e3b39803fp-56}, -k));      // ln 2
+    r = {r.hi / 512.0, r.lo / 512.0};
+    Wide e = {1.0, 0.0};
+    for (int n = 9; n >= 1; --n) e = plus(Wide{1.0, 0.0}, over(times(r, e), n));         // |r|^10 / 10! is below 2^-126
+    for (int n = 0; n < 9; ++n) e = times(e, e);
+    return {std::ldexp(e.hi, (int)k), std::ldexp(e.lo, (int)k)};
+}
+// ln x: a step of Newton's method on e^y from y in 53 bits leaves about a third of the square of its error.
+Wide log_of(double x) {
+    const double y = std::log(x);
+    const Wide f = plus(times(exp_of(Wide{-y, 0.0}), x), Wide{-1.0, 0.0});               // x e^-y - 1
+    return plus(Wide{y, 0.0}, plus(f, times(times(f, f), -0.5)));
+}
+// The fraction of t, at least 0 and below 2^20, in units of 2^-64, to the nearest one modulo 1.
+uint64_t fraction_of(Wide t) {
+    const double f = t.hi - std::floor(t.hi), top = std::floor(f * 0x1p32);
+    const double rest = (f * 0x1p32 - top) * 0x1p32;                                     // exact
+    return ((uint64_t)top << 32) + (uint64_t)std::llround(rest + t.lo * 0x1p64);
+}
+
 double ramp_index(double turns, double dim, double base, double context) {
     return dim * log(context / (turns * 2.0 * M_PI)) / (2.0 * log(base));
 }
@@ -1056,22 +1104,27 @@ extern "C" pa_status pa_rotary_turns(uint64_t *turns, double *attention_factor, 
                                           !std::isfinite(beta_slow)))
         return PA_ERR_INVALID_ARG;
     const double d = rotary_dim;
-    if (scaling == PA_ROTARY_NTK && rotary_dim > 2) base *= pow(factor, d / (d - 2.0));
+    Wide log_base = log_of(base);
+    if (scaling == PA_ROTARY_NTK && rotary_dim > 2) log_base = plus(log_base, over(times(log_of(factor), d), d - 2.0));
     double lo = 0, hi = 1;
     if (scaling == PA_ROTARY_BY_PARTS) {
         lo = std::max(floor(ramp_index(beta_fast, d, base, original_context)), 0.0);
         hi = std::min(ceil(ramp_index(beta_slow, d, base, original_context)), d - 1.0);
     }
     for (int i = 0; i < rotary_dim / 2; ++i) {
-        double theta = pow(base, -2.0 * i / d);
-        if (scaling == PA_ROTARY_LINEAR) theta /= factor;
+        const Wide power = over(times(log_base, -2.0 * i), d);
+        if (!(fabs(power.hi) < 700.0)) return PA_ERR_INVALID_ARG;
+        Wide theta = exp_of(power);
+        if (scaling == PA_ROTARY_LINEAR) theta = over(theta, factor);
         if (scaling == PA_ROTARY_BY_PARTS) {
-            const double r = std::min(std::max((i - lo) / std::max(hi - lo, 0.001), 0.0), 1.0);
-            theta = theta * (1.0 - r) + theta / factor * r;
+            Wide r = hi - lo < 0.001 ? Wide{i > lo ? 1.0 : 0.0, 0.0} : over(Wide{i - lo, 0.0}, hi - lo);
+            if (!(r.hi > 0.0)) r = Wide{0.0, 0.0};
+            if (!(r.hi < 1.0)) r = Wide{1.0, 0.0};
+            theta = plus(times(theta, plus(Wide{1.0, 0.0}, Wide{-r.hi, -r.lo})), times(over(theta, factor), r));
         }
-        const double t = theta / (2.0 * M_PI);       // turns per position
-        const double frac = t - floor(t);
-        turns[i] = frac >= 1.0 ? 0 : (uint64_t)ldexp(frac, 64);
+        const Wide t = times(theta, Wide{0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57});     // turns per position
+        if (!(t.hi < 0x1p20)) return PA_ERR_INVALID_ARG;
+        turns[i] = fraction_of(t);
     }
     *attention_factor = scaling == PA_ROTARY_BY_PARTS && factor > 1.0 ? 0.1 * log(factor) + 1.0 : 1.0;
     return PA_OK;
