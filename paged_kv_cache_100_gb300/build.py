@@ -31,9 +31,24 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def _no_binding() -> str:
+    """Why the tensor binding cannot be built here ("" when it can): the C ABI needs neither torch nor
+    its headers, so a machine without them gets the library alone."""
+    import importlib.util
+    import sysconfig
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return "torch is not installed"
+    for header in (os.path.join(os.path.dirname(spec.origin), "include", "ATen", "core", "Tensor.h"),
+                   os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        if not os.path.exists(header):
+            return f"{header} is missing"
+    return ""
+
+
 def _stale(lib: str) -> bool:
     binding = os.path.join(os.path.dirname(lib), BINDING_MODULE)
-    if not os.path.exists(lib) or (lib == LIB and not os.path.exists(binding)):
+    if not os.path.exists(lib) or (lib == LIB and not os.path.exists(binding) and not _no_binding()):
         return True
     t = os.path.getmtime(lib)
     deps = [os.path.join(CSRC, f) for f in CU_SOURCES + CPP_SOURCES + HEADERS + [BINDING]]
@@ -60,7 +75,8 @@ def build(force: bool = False, verbose_ptxas: bool = False, defines=(), build_di
     """Compile and link the library; returns its path.
 
     ``defines`` (e.g. ``["PA_DECODE_STAGES=2"]``) and ``build_dir`` produce a
-    variant build elsewhere; the default build is ``_build/libpagedkv.so``.
+    variant build elsewhere; the default build is ``_build/libpagedkv.so``, and
+    beside it the tensor binding where torch and its headers are there.
     """
     bdir = build_dir or BUILD
     lib = os.path.join(bdir, "libpagedkv.so")
@@ -85,9 +101,14 @@ def build(force: bool = False, verbose_ptxas: bool = False, defines=(), build_di
                os.path.join(CSRC, src), "-o", obj]
         jobs.append((cmd, src))
         objs.append(obj)
-    binding = os.path.join(bdir, BINDING_MODULE)
+    binding, bound = os.path.join(bdir, BINDING_MODULE), False
     if build_dir is None:
-        jobs.append((_binding_command(binding + f".tmp{os.getpid()}"), BINDING))
+        reason = _no_binding()
+        if reason:
+            sys.stderr.write(f"--- {BINDING}: not built, {reason}\n")
+        else:
+            bound = True
+            jobs.append((_binding_command(binding + f".tmp{os.getpid()}"), BINDING))
     procs = [(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT), src)
              for cmd, src in jobs]
     failed = []
@@ -98,13 +119,17 @@ def build(force: bool = False, verbose_ptxas: bool = False, defines=(), build_di
             sys.stderr.write(f"--- {src}\n{text}")
         if p.returncode != 0:
             failed.append(src)
-    if failed:
+    if [f for f in failed if f != BINDING]:
         raise RuntimeError(f"compilation failed: {', '.join(failed)}")
-    if build_dir is None:
+    if bound and not failed:
         os.replace(binding + f".tmp{os.getpid()}", binding)
+    elif build_dir is None and os.path.exists(binding):
+        os.remove(binding)                # one made for another build of the library
     tmp = lib + f".tmp{os.getpid()}"
     subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, lib)
+    if failed:                            # the library itself is there
+        raise RuntimeError(f"compilation failed: {', '.join(failed)}")
     return lib
 
 
