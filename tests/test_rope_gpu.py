@@ -384,3 +384,122 @@ def test_one_token_far_from_the_others_of_its_block(pkv, n, at, back):
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     pkv.rope_cache_write(None, rows, rows, None, None, *codes, slots.cuda(), k_scales=scales[0], v_scales=scales[1], status=status)
     assert int(status.item()) == (_lib.PA_DEV_BAD_SLOT if back >= 32 else 0)
+
+
+def _exact_keys(rope, pos, x, interleaved):
+    """Keys [tokens][heads][D] turned in float64 from the plan's own 64-bit frequencies, and |x0| + |x1| of each
+    element's pair (times the attention factor)."""
+    turns = [int(t) % (1 << 64) for t in rope.turns.cpu().tolist()]
+    whole = [[(int(p) * t) % (1 << 64) for t in turns] for p in pos]
+    ang = 2 * np.pi * np.array([[(f - (1 << 64) if f >> 63 else f) / 2.0 ** 64 for f in row] for row in whole]).reshape(len(pos), -1)
+    a = rope.attention_factor
+    y, mass = R.rotate(x, a * np.cos(ang), a * np.sin(ang), interleaved)
+    return y, a * mass
+
+
+def _check_codes(pkv, rope, pos, keys, interleaved, close, expect_scales=None):
+    """Writes keys, a block for every 16 tokens, and requires the code of the f32 quotient of the exact key
+    everywhere.  The reference itself is off by a few units of 2^-53 of the pair's magnitudes: where 2^-46
+    of them moves the code, either is right (and those are next to none).  `close`: so many elements at least
+    lie where 2^-22 of the magnitudes, less than the error of 32-bit arithmetic, moves the code."""
+    T, H, D = keys.shape
+    blocks = -(-T // 16)
+    codes = [torch.zeros(blocks, H, 16, D, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.zeros(blocks, H, device="cuda") for _ in range(2)]
+    d = keys.cuda()
+    pkv.rope_cache_write(None, d, d, torch.tensor(pos, dtype=torch.int32, device="cuda"), rope, *codes, torch.arange(T, device="cuda"),
+                         k_scales=scales[0], v_scales=scales[1])
+    y, mass = _exact_keys(rope, pos, keys.double().numpy(), interleaved)
+    pad = np.zeros((blocks * 16 - T, H, D))
+    by_block = lambda t: np.concatenate([t, pad]).reshape(blocks, 16, H, D).transpose(0, 2, 1, 3)  # noqa: E731
+    y, mass = by_block(y), by_block(mass)
+    s = scales[0].double().cpu().numpy()
+    want = np.array([[R.block_scale(v) for v in row] for row in np.abs(y).max((2, 3))])
+    assert np.array_equal(s, want)
+    if expect_scales is not None:
+        assert np.array_equal(s[:, 0], expect_scales)
+    code = lambda v: torch.from_numpy((v / s[:, :, None, None]).astype(np.float32)).to(torch.float8_e4m3fn).view(torch.uint8).numpy()  # noqa: E731
+    got, low, high = codes[0].cpu().numpy(), code(y - 2.0 ** -46 * mass), code(y + 2.0 ** -46 * mass)
+    assert (got == code(y)).mean() > 1 - 1e-5
+    wrong = (got != low) & (got != high)
+    assert not wrong.any(), (int(wrong.sum()), np.argwhere(wrong)[:3].tolist())
+    assert (low != high).mean() < 1e-3
+    assert (code(y - 2.0 ** -22 * mass) != code(y + 2.0 ** -22 * mass)).sum() >= close
+
+
+SHAPES = [(128, 128, False), (128, 128, True), (128, 64, False), (128, 18, True), (64, 50, False), (256, 256, False), (16, 2, True),
+          (80, 48, False)]
+
+
+@pytest.mark.parametrize("scaling,factor", [("none", 1.0), ("by_parts", 8.0)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,rot,interleaved", SHAPES)
+def test_codes_are_those_of_the_exact_keys(pkv, D, rot, interleaved, dtype, scaling, factor):
+    """Half a million elements of each kind of row, some 70 of which lie where 32 bits do not tell their code."""
+    g = torch.Generator().manual_seed(D + rot)
+    T, H = (1 << 19) // (2 * D) + 5, 2
+    keys = (torch.randn(T, H, D, generator=g) * torch.exp2(torch.randn(T, H, 1, generator=g))).to(dtype)
+    pos = torch.randint(0, 1 << 20, (T,), generator=g).tolist()
+    _check_codes(pkv, pkv.rotary_plan(rot, 500000.0, interleaved=interleaved, scaling=scaling, factor=factor), pos, keys, interleaved, 1)
+
+
+@pytest.mark.parametrize("scaling,factor", [("none", 1.0), ("by_parts", 8.0)])
+@pytest.mark.parametrize("D,rot,interleaved", SHAPES)
+def test_codes_beside_the_borders_of_codes(pkv, D, rot, interleaved, scaling, factor):
+    """f32 rows whose first elements of pairs are solved for the border of two codes, one unit of the element
+    below to one above it."""
+    g = torch.Generator().manual_seed(7 * D + rot)
+    T, half = 320, rot // 2
+    rope = pkv.rotary_plan(rot, 500000.0, interleaved=interleaved, scaling=scaling, factor=factor)
+    pos = torch.randint(0, 1 << 20, (T,), generator=g).tolist()
+    keys = torch.randn(T, 1, D, generator=g).numpy()
+    first = np.arange(half) * 2 if interleaved else np.arange(half)
+    second = first + 1 if interleaved else first + half
+    one = np.zeros((T, 1, D))
+    one[..., first] = 1.0
+    c = _exact_keys(rope, pos, one, interleaved)[0][..., first]
+    one[..., first], one[..., second] = 0.0, 1.0
+    s = -_exact_keys(rope, pos, one, interleaved)[0][..., first]
+    # borders of codes: odd multiples of half a step, 16 to 31 quarters of it in each octave
+    border = (torch.randint(8, 16, c.shape, generator=g).double().numpy() + 0.5) * 2.0 ** torch.randint(-8, -2, c.shape, generator=g).double().numpy()
+    x0 = (border + keys[..., second] * s) / np.where(np.abs(c) < 0.05, 1.0, c)
+    nudged = x0.astype(np.float32)
+    nudge = torch.randint(-1, 2, c.shape, generator=g).numpy()
+    for k in (-1, 1):
+        nudged = np.where(nudge == k, np.nextafter(nudged, np.float32(k * np.inf)), nudged)
+    keys[..., first] = nudged
+    _check_codes(pkv, rope, pos, torch.from_numpy(keys), interleaved, T * half // 3)
+
+
+@pytest.mark.parametrize("scaling,factor", [("none", 1.0), ("by_parts", 8.0)])
+@pytest.mark.parametrize("D,rot,interleaved", SHAPES)
+def test_scales_beside_their_borders(pkv, D, rot, interleaved, scaling, factor):
+    """Blocks whose largest magnitude, a turned element, lies within a few units of 448 * 2^e, below and above."""
+    g = torch.Generator().manual_seed(11 * D + rot)
+    blocks, half = 96, rot // 2
+    T = blocks * 16
+    rope = pkv.rotary_plan(rot, 500000.0, interleaved=interleaved, scaling=scaling, factor=factor)
+    pos = torch.randint(0, 1 << 20, (T,), generator=g).tolist()
+    keys = torch.randn(T, 1, D, generator=g).numpy()
+    turns = [int(t) % (1 << 64) for t in rope.turns.cpu().tolist()]
+    expect = np.zeros(blocks)
+    for b in range(blocks):
+        e = b % 7 - 4
+        for _ in range(200):                                 # a token and a pair whose cosine is large
+            t, i = 16 * b + int(torch.randint(0, 16, (1,), generator=g)), int(torch.randint(0, half, (1,), generator=g))
+            ang = 2 * np.pi * ((pos[t] * turns[i]) % (1 << 64)) / 2.0 ** 64
+            if abs(np.cos(ang)) > 0.8:
+                break
+        else:
+            t, i = 16 * b, 0
+            pos[t], ang = 0, 0.0
+        d0, d1 = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+        x1 = np.float32(keys[t, 0, d1])
+        a = rope.attention_factor
+        x0 = np.float32((448.0 * 2.0 ** e + a * float(x1) * np.sin(ang)) / (a * np.cos(ang)))
+        for _ in range(b % 5):
+            x0 = np.nextafter(x0, np.float32((-1) ** (b // 5) * np.inf))
+        keys[t, 0, d0], keys[t, 0, d1] = x0, x1
+        y = a * (float(x0) * np.cos(ang) - float(x1) * np.sin(ang))
+        expect[b] = 2.0 ** e if abs(y) <= 448.0 * 2.0 ** e else 2.0 ** (e + 1)
+    _check_codes(pkv, rope, pos, torch.from_numpy(keys), interleaved, 0, expect)
