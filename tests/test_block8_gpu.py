@@ -250,6 +250,32 @@ def test_decode_many_short_contexts(pkv, hq, hkv, window, partition):
     assert (out[0] == 0).all() and int(status.item()) == 0
 
 
+@pytest.mark.parametrize("lens,hq,hkv,window", [([777], 32, 8, 0), (LENS, 8, 2, 0), ([40, 2100, 0, 2048], 8, 8, 0),
+                                                ([(37 * i) % 100 for i in range(80)], 8, 8, 0), ([(37 * i) % 100 for i in range(80)], 16, 8, 30),
+                                                ([5, 300] * 70, 12, 4, 0)])
+@pytest.mark.parametrize("width", [1000, 8192])
+def test_decode_with_tables_wider_than_the_contexts(pkv, lens, hq, hkv, window, width):
+    """Tables as wide as a model's limit, of which the contexts fill little: most parts of the grid are empty."""
+    p = Pool(width + len(lens), lens, hkv, spread=0.7, width=width)
+    q = _query(p, len(lens), hq)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = pkv.decode_block_fp8(q.cuda(), *p.device(), window=window, status=status)
+    ref, bound = p.reference(q.double().numpy(), [(b, n - 1) for b, n in enumerate(lens)], D ** -0.5, window)
+    _check(out, ref, bound, f"{width}")
+    assert int(status.item()) == 0
+
+
+@pytest.mark.parametrize("width", [700, 8192])
+def test_prefill_with_tables_wider_than_the_contexts(pkv, width):
+    for chunks, lens in (([5], [100]), ([16, 1, 40], [16, 333, 700])):
+        p = Pool(width + len(lens), lens, 2, spread=0.7, width=width)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        q, out, rows = _prefill(pkv, p, chunks, 8, status=status)
+        ref, bound = p.reference(q.double().numpy(), rows, D ** -0.5, floor=4.0)
+        _check(out, ref, bound, f"{width}")
+        assert int(status.item()) == 0
+
+
 def test_decode_graph_replay_and_streams(pkv):
     p = Pool(11, [900, 1, 2000, 64], 4)
     q = _query(p, 4, 16).cuda()
