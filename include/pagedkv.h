@@ -543,7 +543,7 @@ pa_status pa_rotary_turns(uint64_t *turns, double *attention_factor, int rotary_
  * Arithmetic: f32, rounded once.  A code is the nearest one to the f32 quotient of
  * the exact turned key: elements next to a border of two codes are computed
  * again in 64 bits.
- * One kernel launch.
+ * One kernel launch; at most 2^26 tokens into block-scaled pools.
  */
 pa_status pa_rope_cache_write(void *query_out, const void *query, const void *key, const void *value,
                               const int32_t *positions, const uint64_t *turns,

@@ -635,16 +635,6 @@ __global__ void __launch_bounds__(32 * kMergeWarps) pa_merge_block8_kernel(const
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-int sms() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
-        (void)cudaGetLastError();
-        return 152;
-    }
-    return n;
-}
-
 // Query heads of one CTA: the group, or its largest divisor up to 8.
 int heads_per_cta(int group) {
     int h = std::min(group, kHeads);
@@ -691,7 +681,7 @@ bool plan_of(int num_seqs, int axis, int max_blocks, int window, int partition_s
     if (window > 0) span = std::min(span, (window - 1) / kBlockSize + 2);
     p->cluster = 1;
     p->narrow = false;
-    const int64_t ctas = std::max<int64_t>(1, (int64_t)num_seqs * axis), target = 4LL * sms();
+    const int64_t ctas = std::max<int64_t>(1, (int64_t)num_seqs * axis), target = 4LL * device_sms();
     if (partition_size != 0) {
         p->part_blocks = partition_size / kBlockSize;
     } else {
@@ -712,7 +702,7 @@ bool plan_of(int num_seqs, int axis, int max_blocks, int window, int partition_s
     }
     p->max_parts = std::max(1, (span + p->part_blocks - 1) / p->part_blocks);
     const int64_t all = ctas * p->max_parts;
-    p->narrow = p->part_blocks <= (all > 10LL * sms() ? 24 : all > 5LL * sms() ? 16 : 0);
+    p->narrow = p->part_blocks <= (all > 10LL * device_sms() ? 24 : all > 5LL * device_sms() ? 16 : 0);
     return true;
 }
 

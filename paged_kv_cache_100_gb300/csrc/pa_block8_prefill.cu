@@ -1267,16 +1267,6 @@ bool encode_query_map(CUtensorMap *map, const void *query, int rows, int num_q_h
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int sms() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
-        (void)cudaGetLastError();
-        return 152;
-    }
-    return n;
-}
-
 }  // namespace
 }  // namespace pa
 
@@ -1307,7 +1297,7 @@ Cut cut_of(int num_seqs, int num_q_heads, int num_kv_heads, int max_blocks, int 
     c.splits = 1;
     int64_t blocks = max_blocks;
     if (window > 0) blocks = std::min<int64_t>(blocks, ((int64_t)window + kQT * kRows / group) / kBlockSize + 2);
-    const int64_t steps = (blocks + 7) / 8, n = sms();
+    const int64_t steps = (blocks + 7) / 8, n = device_sms();
     if (c.items == 0 || c.items > n) return c;
     const double row_steps = 2. * (kD * sizeof(float) + sizeof(float2)) * num_query_tokens * num_q_heads / 6.0e6 / 1.7;
     double best = 1e300;
@@ -1390,7 +1380,7 @@ extern "C" pa_status pa_prefill_block_fp8(void *out, const void *query, const vo
     a.num_items = (int)items;
     a.splits = cut.splits;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int64_t grid = std::min<int64_t>(items, sms());
+    const int64_t grid = std::min<int64_t>(items, device_sms());
     cudaError_t e;
     if (cut.splits > 1) {
         a.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kWorkspaceBytes);

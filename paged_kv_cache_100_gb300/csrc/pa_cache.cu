@@ -241,6 +241,16 @@ pa_status cuda_failure(cudaError_t err, const char *where) {
     return PA_ERR_CUDA;
 }
 
+int device_sms() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+        (void)cudaGetLastError();
+        return 152;
+    }
+    return n;
+}
+
 }  // namespace pa
 
 using namespace pa;

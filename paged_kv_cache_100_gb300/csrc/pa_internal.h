@@ -19,6 +19,9 @@ void count_launches(uint64_t n);
 // Records the message of a failed CUDA call for pa_last_error() and returns PA_ERR_CUDA.
 pa_status cuda_failure(cudaError_t err, const char *where);
 
+// SMs of the current device.
+int device_sms();
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Gives this host thread a current context.  The driver's cuTensorMapEncodeTiled needs

@@ -48,6 +48,7 @@ constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
 constexpr int kWindow = 32;          // entries of slot_mapping among which a block's tokens lie
+constexpr int kMostTokens = 1 << 26; // of a call into block-scaled pools (find_far's CTAs are counted in 32 bits)
 constexpr int kFarOwn = 1024;        // entries whose blocks a CTA of find_far looks for,
 constexpr int kFarPart = 16384;      // and entries among which it does
 constexpr int kFarSlots = 2048;      // places of its table: a power of two, never more than half full
@@ -494,7 +495,6 @@ __device__ __forceinline__ double exact_element(const RopeArgs &a, const Tile &w
 // border: the elements near the maximum again in 64 bits.  A whole warp.
 template <typename T>
 __device__ __noinline__ int exact_exponent(const RopeArgs &a, const Tile &w, float amax, const float2 *table) {
-    const int half = a.rotary_dim / 2;
     double top = 0.0;
     for (int k = 0; k < w.n; ++k) {
         const int j = w.list[k] & 0xff;
@@ -1035,19 +1035,19 @@ pa_status launch_rope(RopeArgs &a, bool blocks, cudaStream_t stream) {
     // eight where a token has few rows (64 query heads of 128: 61 us with 4 or 8
     // tokens a CTA, 64.5 with 16); where there are fewer than SMs, CTAs share a
     // token's rows
-    const int64_t n = a.num_tokens;
+    const int64_t n = a.num_tokens, sms = device_sms();
     const int units = a.whole && !a.interleaved ? (half + D - rot) / N : D / N;
     const int most = std::max(8, std::min(32, 4096 / std::max(1, rows * units)));
     a.row_tokens = 1;
-    while (2 * a.row_tokens <= most && n / (2 * a.row_tokens) >= 4 * 152) a.row_tokens *= 2;
+    while (2 * a.row_tokens <= most && n / (2 * a.row_tokens) >= 4 * sms) a.row_tokens *= 2;
     const int passes = (rows + kRopeThreads / units - 1) / (kRopeThreads / units);
-    a.row_splits = (int)std::max<int64_t>(1, std::min<int64_t>(passes, 2 * 152 / n));
+    a.row_splits = (int)std::max<int64_t>(1, std::min<int64_t>(passes, 2 * sms / n));
     // blocks: 16 tokens a CTA where there are enough, more where the KV heads are too
     // few to give each warp two tiles (and the table leaves room for two CTAs: 14554
     // tokens of one head of 256 47 us, 57 with 16 tokens a CTA)
     const int tile_most = std::min(kMaxTile, std::max(16, 16 * kRopeWarps / a.num_kv_heads));
     a.tile_tokens = 1;
-    while (a.tile_tokens < tile_most && n / (2 * a.tile_tokens) >= 2 * 152 &&
+    while (a.tile_tokens < tile_most && n / (2 * a.tile_tokens) >= 2 * sms &&
            (a.tile_tokens < 8 || (2 * a.tile_tokens + kWindow - 1) * a.table_row * (int)sizeof(float2) <= kMostTables))
         a.tile_tokens *= 2;
     int64_t grid = rows > 0 ? (n + a.row_tokens - 1) / a.row_tokens * a.row_splits : 0;
@@ -1057,10 +1057,8 @@ pa_status launch_rope(RopeArgs &a, bool blocks, cudaStream_t stream) {
     if (blocks) {
         if (n > kWindow) {
             a.far_parts = (int)((n + kFarPart - 1) / kFarPart);
-            const int64_t far = (n + kFarOwn - 1) / kFarOwn * a.far_parts;
-            if (far >= ((int64_t)1 << 30)) return PA_ERR_UNSUPPORTED;
-            a.far_ctas = (int)far;
-            grid += far;
+            a.far_ctas = (int)((n + kFarOwn - 1) / kFarOwn * a.far_parts);
+            grid += a.far_ctas;
             smem = std::max(smem, (size_t)2 * kFarSlots * sizeof(uint32_t));
         }
         const int items = 2 * a.num_kv_heads;
@@ -1068,7 +1066,7 @@ pa_status launch_rope(RopeArgs &a, bool blocks, cudaStream_t stream) {
         // have more than two a warp: it would end the grid alone (3696 tokens of 32 KV
         // heads of 128 50 us, 79 by one CTA, 58 with one tile a warp; of 64 52 / 85 / 53)
         a.tile_splits = (int)std::max<int64_t>(1, std::min<int64_t>((items + kRopeWarps - 1) / kRopeWarps,
-                                                                    std::max<int64_t>(4 * 152 / n, items / 16)));
+                                                                    std::max<int64_t>(4 * sms / n, items / 16)));
         a.tile_ctas = (int)((n + a.tile_tokens - 1) / a.tile_tokens * a.tile_splits);
         grid += a.tile_ctas;
         smem = std::max(smem, (size_t)(a.tile_tokens + kWindow - 1) * a.table_row * sizeof(float2));
@@ -1147,6 +1145,7 @@ extern "C" pa_status pa_rope_cache_write(void *query_out, const void *query, con
     const bool blocks = cache_dtype == PA_DTYPE_FP8_E4M3;
     const int esize = dtype == PA_DTYPE_F32 ? 4 : 2;
     if (head_dim > 256 || (head_dim * esize) % 16 != 0 || (blocks && head_dim % 16 != 0)) return PA_ERR_UNSUPPORTED;
+    if (blocks && num_tokens > kMostTokens) return PA_ERR_UNSUPPORTED;
     const int64_t q_row = (int64_t)num_q_heads * head_dim, kv_row = (int64_t)num_kv_heads * head_dim;
     if (num_tokens == 0) return PA_OK;
     if (num_q_heads > 0 && (!query || !query_out || query_stride < q_row || query_out_stride < q_row ||

@@ -225,3 +225,8 @@ def test_block_scales_refusals(lib):
         pkv.block_copy(codes, codes, z(1, 2), k_scales=sc[:1], v_scales=sc)
     with pytest.raises(TypeError, match="E4M3"):
         pkv.block_copy(rows, rows, z(1, 2), k_scales=sc, v_scales=sc)
+
+
+def test_rope_write_refuses_more_tokens_than_it_counts(lib):
+    wide = dict(tokens=(1 << 26) + 1, query_out=1 << 50, query=1 << 51, key=1 << 52, value=1 << 53)
+    assert _call(lib.pa_rope_cache_write, ROPE, wide) == UNSUPPORTED
