@@ -20,7 +20,7 @@
 //
 // Bound by memory: 64 ragged contexts of up to 2048 tokens with 32 KV heads, 560 MB,
 // 89 us (6.3 TB/s, 0.93 of a copy); 256 of up to 4096 with 64 query heads on 8, 1.24
-// GB, 196 us (0.93); eight of 32768, 2.15 GB, 302 us (7.1 TB/s).  Four warps with
+// GB, 195 us (0.94); eight of 32768, 2.15 GB, 305 us (7.1 TB/s).  Four warps with
 // rings of two blocks each were the best shape there: 4x3 6x2 6x3 8x1 8x2 3x2 2x2 2x3
 // were up to 18 % slower on one of the three.  One short request is latency: 6 us.
 #include <cuda.h>
@@ -346,8 +346,8 @@ __device__ __forceinline__ float remote_f32(const float *mine, uint32_t rank) {
 }
 
 // kParts > 1: the grid's clusters of kParts CTAs each work on one (sequence, KV head).
-// (117 registers in the widest form, four CTAs of four warps per SM; held to 96 for a fifth,
-// by a launch bound or otherwise, the 70B-shaped batch took 200 to 204 us instead of 193.)
+// (121 registers without clusters, four CTAs of four warps per SM; held to 96 for a fifth, by
+// a launch bound or otherwise, the 70B-shaped batch took 200 to 204 us instead of 193.)
 template <int NW, int STAGES, int kParts>
 __global__ void __launch_bounds__(NW * 32)
     pa_decode_block8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -659,9 +659,10 @@ struct Plan {
 // 13.3 in 2, on 2048 27.5 / 26.8; 592 CTAs on 512 15.3 / 20.7, on 2048 39.9 / 43.5).
 // The parts follow the table's width, as only the GPU knows the lengths, and a wide
 // table's last parts are often empty: a grid beyond 32 CTAs per SM is made of the
-// largest parts only (tables of 8192 entries: 64 7B-shaped contexts 106 us, 178 in
-// 4096-token parts; 1024 contexts of up to 64 tokens with 8 KV heads 267 / 621, 41
-// with tables of their size).  Parts cut by each context's own length, or taken in
+// largest parts only (tables of 8192 entries: 64 7B-shaped contexts 97 us, 89 with tables
+// of their size; 1024 contexts of up to 64 tokens with 8 KV heads 126 / 24; 8 of 2048 with 8
+// KV heads 23.5 / 15.7; in 4096-token parts the first two took 178 and 621 when this
+// form took 106 and 267).  Parts cut by each context's own length, or taken in
 // stretches by a loop in the kernel, cost 5 to 12 % where the table fits.
 // Up to 8 parts of a small call are clusters: the GPU time is the same, the host
 // issues one launch instead of two (5 us, 8 otherwise); in larger calls clusters
@@ -670,10 +671,9 @@ struct Plan {
 // Where there are more than five CTAs per SM (which holds four of four warps) and their
 // parts short, CTAs have one warp, 16 of which an SM holds: a short part's time is
 // its start (length, table, scales, first tiles one after another) and its end.
-// 960 CTAs on contexts of up to 64 tokens 7.5 us against 9.9, 256 tokens 15.3 /
-// 16.4, 384 tokens 19.7 / 19.1; 2048 CTAs on 256 tokens 21.7 / 25.8, 384 29.6 /
-// 31.1, 512 35.7 / 35.4, 768 50 / 46; 8192 CTAs on 64 tokens 41 / 77, 256 71 / 106,
-// 384 91 / 121; but 720 CTAs on 256 tokens 14.9 / 11.6.
+// Contexts between half of and all of 64 tokens: 960 CTAs 5.7 us against 7.5, 8192 24 / 48; of
+// 256: 720 CTAs 13.5 / 12.9, 960 14.1 / 14.7, 2048 22.5 / 25.7, 8192 69 / 83; of 384: 960
+// 18.8 / 18.2, 2048 31.0 / 31.8, 8192 99 / 104; 2048 CTAs on 512 tokens 39.6 / 38.6, on 768 57 / 53.
 bool plan_of(int num_seqs, int axis, int max_blocks, int window, int partition_size, Plan *p) {
     if (partition_size != 0 && (partition_size < kBlockSize || partition_size > kMaxPartition || partition_size % kBlockSize))
         return false;
