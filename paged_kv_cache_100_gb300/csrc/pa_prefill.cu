@@ -732,17 +732,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (j + 2 == n) umma_commit(&bars[kQFree]);   // the item's last QK^T is issued
                     }
                 }
-                // Group 1 keeps no other phase of an item without a tile B in step, and waits
-                // for this one by parity: it must have left the item before when it completes
-                if (it >= 1 && !wait_or_fail(&bars[kOFree + 1], (it - 1) & 1, fail, a.status)) ok = false;
                 // every MMA of this item has completed once kDrain flips
                 umma_commit(&bars[kDrain]);
                 gstep += n;
             }
-            // after a wait that gave up products may still be running: the CTA's memory is
-            // theirs until they are done
-            umma_commit(&bars[kEnd]);
-            if (!mbar_wait_bounded(&bars[kEnd], 0)) report(a.status, PA_DEV_TIMEOUT);
         }
     } else if (warp >= kConvWarp0) {
         // ---------------- V conversion ----------------
@@ -791,6 +784,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     vt[c] = h;
                     vmax = __hmax2(__hmax2(vmax, abs_f16x2(h.x)),
                                    __hmax2(__hmax2(abs_f16x2(h.y), abs_f16x2(h.z)), abs_f16x2(h.w)));
+                }
+                // Group 1 keeps no phase of an item without a tile B in step but the drain, which
+                // it waits for by parity: no item drains before the group has left the one
+                // before.  Seen to here, where nothing waits for this warp's next instruction (in
+                // the MMA warp it cost 1 %).
+                if (j + 1 == d.n_tiles && it >= 1 && !wait_or_fail(&bars[kOFree + 1], (it - 1) & 1, fail, a.status)) {
+                    ok = false;
+                    break;
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&bars[kVConv + st]);
@@ -1089,6 +1090,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
+        // after a wait that gave up products may still be running: the CTA's memory is
+        // theirs until they are done
+        if (lane == 0) {
+            umma_commit(&bars[kEnd]);
+            if (!mbar_wait_bounded(&bars[kEnd], 0)) report(a.status, PA_DEV_TIMEOUT);
+        }
+        __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
