@@ -25,12 +25,13 @@
 // magnitude when it lies next to a scale's border.
 //
 // The kernel moves bytes: a launch has CTAs that turn rows (queries; keys and
-// values too for float pools) and CTAs that encode blocks, the latter first.
-// 8192 tokens of 64 query and 8 KV heads of 128 into E4M3 pools: 61 us for 319 MB,
-// 5.2 TB/s or 0.77 of a copy.  The query rows alone take 48 us and the blocks alone
+// values too for float pools) and, first, a few that look for far tokens of a block and
+// CTAs that encode blocks.
+// 8192 tokens of 64 query and 8 KV heads of 128 into E4M3 pools: 63 us for 319 MB,
+// 5.1 TB/s or 0.75 of a copy.  The query rows alone take 48 us and the blocks alone
 // 36, mostly the arithmetic of two passes (the maximum, then the codes), of which
 // the rows' traffic hides half; the two kinds of CTA mixed from the start instead
-// of blocks first took 65 to 74 us.  A step of 256 tokens of that shape takes 7.8
+// of blocks first took 65 to 74 us.  A step of 256 tokens of that shape takes 8.4
 // us, of 64 tokens into bf16 pools 2.9: latency.
 #include <cuda_runtime.h>
 #include <math.h>
