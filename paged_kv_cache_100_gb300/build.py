@@ -21,7 +21,7 @@ CU_SOURCES = ["pa_decode.cu", "pa_cache.cu", "pa_decode_noalloc.cu", "pa_prefill
               "pa_rope.cu", "pa_block8_decode.cu", "pa_block8_prefill.cu"]
 CPP_SOURCES = ["block_manager.cpp"]
 BINDING = "torch_binding.cpp"     # its own module: it follows the installed torch, the library does not
-HEADERS = ["pa_device.cuh", "pa_internal.h", "pa_tc.cuh", "pa_block8.cuh"]
+HEADERS = ["pa_device.cuh", "pa_internal.h", "pa_tc.cuh", "pa_block8.cuh", "pa_rope.cuh"]
 
 
 def _nvcc() -> str:
