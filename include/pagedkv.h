@@ -646,6 +646,118 @@ pa_status pa_prefill_block_fp8(void *out, const void *query, const void *key_cac
                                void *stream);
 
 /*
+ * Pools held in 4 bits ("KV cache: la memoria de trabajo que sostiene la
+ * inferencia LLM", section "Trucos para que el cuaderno sea más fino").  A
+ * pool is bytes [num_blocks][num_kv_heads][16][9 * head_dim / 16]; head_dim is
+ * a multiple of 16, at most 256.  The 9 * head_dim bytes of a block's tile of
+ * one KV head are, in this order,
+ *   16 rows of head_dim / 2 bytes of codes: element 2i of a token in the low
+ *      half of byte i, element 2i + 1 in the high half.  E2M1 codes (the OCP
+ *      microscaling formats' 4-bit floating point numbers): a sign bit, then
+ *      0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *   16 rows of head_dim / 16 scale bytes, one for every 16 elements: a positive
+ *      number of 5 exponent bits (bias 15) and 3 mantissa bits, the bits 14 to 7
+ *      of an f16.  0xff (an f16's NaN) stands for 16 elements that hold a NaN
+ * An element is its code's value times its scale: exact in f16, bf16 and f32.
+ * Sixteen elements of largest magnitude amax have the scale amax / 6 rounded to
+ * nearest (ties to even), at least 2^-17 and at most 10240, 0 where amax is 0;
+ * a code is the nearest one to element / scale (ties to even), 6 at most.
+ * Magnitudes beyond 61440 saturate and the call flags PA_DEV_RANGE; 16
+ * elements with a NaN among them read back as NaN.  Bytes above 0xe2 other than
+ * 0xff are never written; what they stand for leaves f16's range.
+ * pa_block_copy, pa_swap_out and pa_swap_in take these pools as
+ * PA_DTYPE_FP8_E4M3 ones of head_dim 9 * head_dim / 16: scales lie with codes.
+ *
+ * pa_rope_cache_write_fp4: pa_rope_cache_write into such pools.  All arguments
+ * are as there, but no scales: a row's depend on nothing but the row, so tokens
+ * may come in any order and a block's other rows stay as they are.  Two tokens
+ * with the same slot race and leave that slot (no other) undefined.  A key's
+ * codes and scales are those of its exact rotation: what lies next to a border
+ * is computed again in 64 bits.  One kernel launch.
+ */
+pa_status pa_rope_cache_write_fp4(void *query_out, const void *query, const void *key,
+                                  const void *value, const int32_t *positions,
+                                  const uint64_t *turns, double attention_factor, int rotary_dim,
+                                  int interleaved, void *key_cache, void *value_cache,
+                                  const int64_t *slot_mapping, int num_tokens, int num_q_heads,
+                                  int num_kv_heads, int head_dim, int64_t query_out_stride,
+                                  int64_t query_stride, int64_t key_stride, int64_t value_stride,
+                                  int block_size, int num_blocks, pa_dtype dtype,
+                                  int32_t *device_status, void *stream);
+
+/*
+ * Reads contexts in 4-bit pools back, block by block:
+ *  key_out, value_out  dtype (f32 or bf16) [num_seqs * W][num_kv_heads][16]
+ *                    [head_dim], 16-byte aligned: the block of sequence b's table
+ *                    entry j becomes block b * W + j, exact, its rows past the
+ *                    context zero.  Blocks past the context, and with window > 0
+ *                    those wholly before the last `window` positions, are left as
+ *                    they were and their table entries are not read
+ *  max_context_len   no context is longer: W = ceil(max_context_len / 16), at
+ *                    most max_blocks_per_seq; 0: W = max_blocks_per_seq.  A context
+ *                    length outside [0, 16 W] is clamped and flagged
+ *                    PA_DEV_BAD_CONTEXT_LEN, a table entry out of range is read as
+ *                    block 0 and flagged PA_DEV_BAD_BLOCK_ID
+ * The outputs are pools of pa_prefill and pa_decode, with tables of entries
+ * b * W + j.  Outputs that overlap an input or one another are refused
+ * (PA_ERR_INVALID_ARG).  One kernel launch.
+ */
+pa_status pa_cache_read_fp4(void *key_out, void *value_out, const void *key_cache,
+                            const void *value_cache, const int32_t *block_tables,
+                            const int32_t *context_lens, int num_seqs, int num_kv_heads,
+                            int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
+                            int max_context_len, int window, pa_dtype dtype,
+                            int32_t *device_status, void *stream);
+
+/*
+ * Paged decode attention over 4-bit pools; query rows as in
+ * pa_decode_block_fp8_rows (query_start NULL: row b is sequence b's, and
+ * num_query_tokens = num_seqs), window, partition_size, workspace, device_status
+ * and stream as in pa_decode_block_fp8.  bfloat16 query and out; head_dim 64, 128
+ * or 256; any group (one of more than 8 query heads is split into parts of its
+ * largest divisor up to 8, which read the same tiles).
+ * Arithmetic: codes times scales are exact; query rows and weights are rounded
+ * to f16 as in pa_decode_block_fp8; sums are fp32.  A row that attends to a NaN
+ * becomes NaN: in the elements that a NaN value stands for, or whole where a key
+ * holds one.  Rows that are not attended may hold anything.
+ */
+size_t pa_decode_fp4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int max_blocks_per_seq, int block_size, int window,
+                                     int partition_size);
+pa_status pa_decode_fp4(void *out, const void *query, const void *key_cache,
+                        const void *value_cache, const int32_t *block_tables,
+                        const int32_t *context_lens, const int32_t *query_start, int num_seqs,
+                        int num_query_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                        int block_size, int max_blocks_per_seq, int num_blocks, float scale,
+                        int window, int partition_size, void *workspace, size_t workspace_bytes,
+                        int32_t *device_status, void *stream);
+
+/*
+ * Chunked prefill over 4-bit pools: pa_prefill's semantics, shapes and
+ * arithmetic.  The blocks that the chunks attend to are read back once as bf16
+ * (exact) into the workspace, where the tensor-core kernel finds them; every tile
+ * of 256 query rows and every query head of a group would widen them again.
+ *  max_context_len   as in pa_cache_read_fp4: it sizes the workspace
+ *  workspace         at least pa_prefill_fp4_workspace_bytes(...) bytes, 16-byte
+ *                    aligned (num_seqs * W blocks of bf16 keys and values; calls
+ *                    that run at the same time need their own)
+ * A sequence whose query_start entries fall, leave [0, num_query_tokens] or
+ * exceed its context length, or whose context is longer than max_context_len or its
+ * table, is not computed and flagged PA_DEV_BAD_CONTEXT_LEN.
+ * A memset and two kernel launches.
+ */
+size_t pa_prefill_fp4_workspace_bytes(int num_seqs, int num_kv_heads, int head_dim,
+                                      int max_blocks_per_seq, int max_context_len);
+pa_status pa_prefill_fp4(void *out, const void *query, const void *key_cache,
+                         const void *value_cache, const int32_t *block_tables,
+                         const int32_t *context_lens, const int32_t *query_start, int num_seqs,
+                         int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                         int max_blocks_per_seq, int num_blocks, int num_query_tokens,
+                         int max_query_len, int max_context_len, float scale, int window,
+                         void *workspace, size_t workspace_bytes, int32_t *device_status,
+                         void *stream);
+
+/*
  * Swap of blocks between the pools and a staging buffer ("PagedAttention por
  * dentro", section "Evicción y preemption", strategy 2 "swap": the blocks of
  * a preempted sequence move to CPU memory, freeing device memory, and come

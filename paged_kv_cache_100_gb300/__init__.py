@@ -32,7 +32,8 @@ BLOCK_SIZE = 16
 
 __all__ = ["prefill", "swap_out", "swap_in", "decode", "decode_fp8", "decode_sliding_window", "decode_shared_prefix", "decode_shared_prefix_fp8", "shared_prefix_blocks", "decode_workspace_bytes", "decode_partition_size",
            "plan_step", "StepPlan", "rotary_plan", "RotaryPlan", "rope_cache_write", "decode_block_fp8",
-           "decode_block_fp8_workspace_bytes", "prefill_block_fp8", "cache_write", "cache_write_fp8", "block_copy", "launch_count", "BlockManager",
+           "decode_block_fp8_workspace_bytes", "prefill_block_fp8", "fp4_pool", "rope_cache_write_fp4", "cache_read_fp4",
+           "decode_fp4", "decode_fp4_workspace_bytes", "prefill_fp4", "prefill_fp4_workspace_bytes", "cache_write", "cache_write_fp8", "block_copy", "launch_count", "BlockManager",
            "PagedKVError", "BLOCK_SIZE", "library_path"]
 
 
@@ -587,6 +588,98 @@ def prefill_block_fp8(query, key_cache, value_cache, k_scales, v_scales, block_t
                                          status, _given(stream, query))
     if type(r) is int:
         check(r, "pa_prefill_block_fp8")
+    return r if out is None else out
+
+
+def fp4_pool(num_blocks, num_kv_heads, head_dim, device="cuda"):
+    """A pool held in 4 bits, zero: uint8 ``[num_blocks][num_kv_heads][16][9 * head_dim / 16]``.
+
+    The ``9 * head_dim`` bytes of a block's tile of one KV head are its 16 rows' E2M1 codes (two a
+    byte, the even element in the low half), then their scales, one byte per 16 elements (bits 14
+    to 7 of a float16); ``block_copy``, ``swap_out`` and ``swap_in`` take such pools as they are."""
+    if head_dim <= 0 or head_dim > 256 or head_dim % 16:
+        raise ValueError("head_dim must be a multiple of 16, at most 256")
+    torch = _torch()
+    return torch.zeros((num_blocks, num_kv_heads, BLOCK_SIZE, 9 * head_dim // 16), dtype=torch.uint8, device=device)
+
+
+def rope_cache_write_fp4(query, key, value, positions, rope, key_cache, value_cache, slot_mapping, *, query_out=None,
+                         status=None, stream=None):
+    """Rotary positions on new queries and keys, and the write into pools held in 4 bits
+    (``pa_rope_cache_write_fp4``); rows, ``rope`` and ``query_out`` as in ``rope_cache_write``.
+
+    A row's codes and scales depend on that row alone: tokens may come in any order, and the
+    other rows of their blocks stay as they are."""
+    turns, factor, rotary_dim, interleaved = _NO_ROPE if rope is None else rope
+    r = _lib.binding().rope_cache_write_fp4(query, key, value, positions, turns, factor, rotary_dim, interleaved,
+                                            key_cache, value_cache, slot_mapping, query_out, status,
+                                            _given(stream, key_cache))
+    if type(r) is int:
+        check(r, "pa_rope_cache_write_fp4")
+    return query_out if query_out is not None and query is not None else r
+
+
+def cache_read_fp4(key_cache, value_cache, block_tables, context_lens, *, dtype=None, max_context_len=None, window=0,
+                   key_out=None, value_out=None, status=None, stream=None):
+    """Reads contexts in 4-bit pools back (``pa_cache_read_fp4``): the block of sequence b's table
+    entry j becomes block ``b * W + j`` of ``key_out`` / ``value_out`` [B * W][Hkv][16][D], exact.
+
+    ``dtype`` bfloat16 (the default) or float32, or that of ``key_out``; W is the tables' width, or
+    that of contexts of ``max_context_len`` tokens.  A block's rows past its context are zero; blocks past
+    the context, or before its last ``window`` positions, are left as they were."""
+    torch = _torch()
+    if dtype is None:
+        dtype = torch.bfloat16 if key_out is None and value_out is None else (key_out if key_out is not None else value_out).dtype
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("blocks are read back as bfloat16 or float32")
+    r = _lib.binding().cache_read_fp4(key_cache, value_cache, block_tables, context_lens, dtype == torch.float32,
+                                      max_context_len, window, key_out, value_out, status, _given(stream, key_cache))
+    if type(r) is int:
+        check(r, "pa_cache_read_fp4")
+    return r
+
+
+def decode_fp4_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, partition_size=0,
+                               window=0) -> int:
+    """Scratch ``decode_fp4`` needs for these sizes (0: none)."""
+    n = lib().pa_decode_fp4_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                                            BLOCK_SIZE, window, partition_size)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("invalid arguments for pa_decode_fp4_workspace_bytes")
+    return int(n)
+
+
+def decode_fp4(query, key_cache, value_cache, block_tables, context_lens, scale=None, *, query_start=None, window=0,
+               out=None, partition_size=0, workspace=None, status=None, stream=None):
+    """Paged decode over pools held in 4 bits (``pa_decode_fp4``); arguments as ``decode_block_fp8``
+    without scales.  Returns ``out`` (bf16)."""
+    r = _lib.binding().decode_fp4(query, key_cache, value_cache, block_tables, context_lens, scale, query_start, window,
+                                  out, partition_size, workspace, status, _given(stream, query))
+    if type(r) is int:
+        check(r, "pa_decode_fp4")
+    return r if out is None else out
+
+
+def prefill_fp4_workspace_bytes(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, max_context_len=None) -> int:
+    """Scratch ``prefill_fp4`` needs for these sizes."""
+    n = lib().pa_prefill_fp4_workspace_bytes(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, max_context_len or 0)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("invalid arguments for pa_prefill_fp4_workspace_bytes")
+    return int(n)
+
+
+def prefill_fp4(query, key_cache, value_cache, block_tables, context_lens, query_start, max_query_len=None, scale=None, *,
+                max_context_len=None, window=0, out=None, workspace=None, status=None, stream=None):
+    """Chunked prefill over pools held in 4 bits (``pa_prefill_fp4``); arguments as ``prefill``.
+
+    The contexts' blocks are read back once into the workspace, of the tables' width or, smaller, that of
+    contexts of ``max_context_len`` tokens.  Returns ``out`` (bf16)."""
+    if max_query_len is None:
+        max_query_len = int((query_start[1:] - query_start[:-1]).max().item()) if query_start.numel() > 1 else 0
+    r = _lib.binding().prefill_fp4(query, key_cache, value_cache, block_tables, context_lens, query_start, max_query_len,
+                                   scale, max_context_len, window, out, workspace, status, _given(stream, query))
+    if type(r) is int:
+        check(r, "pa_prefill_fp4")
     return r if out is None else out
 
 

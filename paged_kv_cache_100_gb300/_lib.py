@@ -68,6 +68,15 @@ SIGNATURES = {
     "pa_prefill_block_fp8_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32, i32, i32]),
     "pa_prefill_block_fp8": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
                                    i32, i32, i32, f32, i32, vp, sz, vp, vp]),
+    "pa_rope_cache_write_fp4": (i32, [vp, vp, vp, vp, vp, vp, f64, i32, i32, vp, vp, vp, i32, i32, i32, i32, i64, i64, i64,
+                                      i64, i32, i32, i32, vp, vp]),
+    "pa_cache_read_fp4": (i32, [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32, vp, vp]),
+    "pa_decode_fp4_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32, i32, i32]),
+    "pa_decode_fp4": (i32, [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, f32, i32, i32, vp, sz, vp,
+                            vp]),
+    "pa_prefill_fp4_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
+    "pa_prefill_fp4": (i32, [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32, i32, f32, i32, vp, sz,
+                             vp, vp]),
     "pa_block_copy_scaled": (i32, [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp]),
     "pa_swap_out_scaled": (i32, [vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp]),
     "pa_swap_in_scaled": (i32, [vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp]),
@@ -181,7 +190,8 @@ def binding():
         spec.loader.exec_module(mod)
         mod.bind(*[ctypes.cast(getattr(handle, n), vp).value for n in (
             "pa_plan_step", "pa_rope_cache_write", "pa_decode_block_fp8_rows", "pa_decode_block_fp8_workspace_bytes",
-            "pa_prefill_block_fp8", "pa_prefill_block_fp8_workspace_bytes")])
+            "pa_prefill_block_fp8", "pa_prefill_block_fp8_workspace_bytes", "pa_rope_cache_write_fp4", "pa_cache_read_fp4",
+            "pa_decode_fp4", "pa_decode_fp4_workspace_bytes", "pa_prefill_fp4", "pa_prefill_fp4_workspace_bytes")])
         _binding = mod
     return _binding
 

@@ -18,10 +18,10 @@ BINDING_MODULE = "_pagedkv_torch.so"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CU_SOURCES = ["pa_decode.cu", "pa_cache.cu", "pa_decode_noalloc.cu", "pa_prefill.cu", "pa_plan.cu",
-              "pa_rope.cu", "pa_block8_decode.cu", "pa_block8_prefill.cu"]
+              "pa_rope.cu", "pa_block8_decode.cu", "pa_block8_prefill.cu", "pa_fp4_cache.cu", "pa_fp4_decode.cu"]
 CPP_SOURCES = ["block_manager.cpp"]
 BINDING = "torch_binding.cpp"     # its own module: it follows the installed torch, the library does not
-HEADERS = ["pa_device.cuh", "pa_internal.h", "pa_tc.cuh", "pa_block8.cuh", "pa_rope.cuh"]
+HEADERS = ["pa_device.cuh", "pa_internal.h", "pa_tc.cuh", "pa_block8.cuh", "pa_rope.cuh", "pa_fp4.cuh"]
 
 
 def _nvcc() -> str:

@@ -1,0 +1,580 @@
+// Quantising a paged cache to 4 bits as it is written, with rotary positions on the
+// new tokens' queries and keys, and reading it back ("PagedAttention por dentro",
+// section "La tabla de páginas (block table)"; "KV cache: la memoria de trabajo que
+// sostiene la inferencia LLM", section "Trucos para que el cuaderno sea más fino").
+// The format is in pa_fp4.cuh, the mathematics of the angles in pa_rope.cu.
+//
+// Write.  Sixteen elements of a row are the unit: their scale depends on nothing
+// else, so a token's row is written without a look at the rest of its block, and a
+// thread takes one unit: it turns the elements, finds the scale and the codes, and
+// stores 8 bytes of codes and one of scale.  Other CTAs of the launch turn the
+// queries' rows.
+//   A key's codes and scale are those of its exact rotation: where a 32-bit value
+// lies so near a border of two codes that its error could cross it (or the largest
+// magnitude so near one of two scales) it is computed again in 64 bits.
+//
+// Read.  Blocks of the contexts become blocks of bf16 or f32 rows: eight elements a
+// thread, 4 bytes of codes in, 16 or 32 bytes out.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "pa_fp4.cuh"
+#include "pa_rope.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kMostTables = 100 * 1024;          // dynamic shared memory of a CTA at most
+constexpr int kMostEncodeTokens = 16;            // tokens of a CTA that encodes
+
+// Entry of pair `p` in a token's row of the table of cos and sin: 16 bytes of room
+// behind every 16 pairs, so that lanes that read the pairs of neighbouring units meet
+// in no bank.
+__host__ __device__ constexpr int skewed(int p) { return p + (p >> 4) * 2; }
+
+// The code of d / scale in 64 bits (0 where the scale is 0).
+__device__ __noinline__ uint32_t exact_e2m1(double d, float scale) {
+    const double q = scale > 0.f ? fabs(d) / (double)scale : 0.0;
+    const uint32_t m = (q > 0.25) + (q >= 0.75) + (q > 1.25) + (q >= 1.75) + (q > 2.5) + (q >= 3.5) + (q > 5.0);
+    return m | (d < 0.0 ? 8u : 0u);
+}
+
+// Element d of a row of token `tok` in 64 bits.
+template <typename T>
+__device__ __forceinline__ double exact_of(const RopeArgs &a, const T *row, int64_t tok, int d) {
+    int first, second, pair;
+    if (!pair_of(a, d, &first, &second, &pair)) return (double)to_float(row[d]);
+    return exact_turn(to_float(row[first]), to_float(row[second]), d == second, a.positions[tok], a.turns[pair], a.factor);
+}
+
+// Scale of the unit from element d0 on in 64 bits.
+template <typename T>
+__device__ __noinline__ uint32_t exact_scale(const RopeArgs &a, const T *row, int64_t tok, int d0, float near) {
+    double top = 0.0;
+    for (int i = 0; i < 16; ++i) top = fmax(top, fabs(exact_of<T>(a, row, tok, d0 + i)));
+    return fp4_scale_of<double>(near, top);
+}
+
+// How a unit's elements are turned: not at all, as halves whose pairs lie in whole units,
+// as neighbours, or as any halves.
+enum { kPlain = 0, kHalves = 1, kNeighbours = 2, kAny = 3 };
+
+// Encodes the unit from element d0 on of `row`, a row of token tok.  cs: the token's
+// row of the table.
+template <typename T, int kMode>
+__device__ __forceinline__ void encode_unit(const RopeArgs &a, const T *row, int64_t tok, int d0, const float2 *cs,
+                                            uint8_t *codes, uint8_t *scale_at) {
+    constexpr int N = Vec<T>::N;
+    constexpr bool kBf16 = sizeof(T) == 2;
+    const int rot = a.rotary_dim, half = rot / 2;
+    float y[16], err[16];
+    if constexpr (kMode == kHalves) {
+        const bool on = d0 < rot, second = d0 >= half;
+        const int other = on ? (second ? d0 - half : d0 + half) : d0;
+        const float4 *c = reinterpret_cast<const float4 *>(cs + skewed(on ? (second ? d0 - half : d0) : 0));
+#pragma unroll
+        for (int v = 0; v < 16 / N; ++v) {
+            float x[N], o[N];
+            Vec<T>::widen(reinterpret_cast<const uint4 *>(row + d0)[v], x);
+            Vec<T>::widen(reinterpret_cast<const uint4 *>(row + other)[v], o);
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const float4 w = c[(v * N + i) / 2];
+                const int k = v * N + i;
+                const float s0 = second ? w.y : -w.y, s1 = second ? w.w : -w.w;
+                y[k] = on ? x[i] * w.x + o[i] * s0 : x[i];
+                y[k + 1] = on ? x[i + 1] * w.z + o[i + 1] * s1 : x[i + 1];
+                err[k] = on ? fabsf(x[i]) + fabsf(o[i]) : 0.f;
+                err[k + 1] = on ? fabsf(x[i + 1]) + fabsf(o[i + 1]) : 0.f;
+            }
+        }
+    } else if constexpr (kMode == kNeighbours) {
+        const int some = (rot - d0) / 2;                 // pairs of the unit that are turned, if below 8
+        const float2 *c = cs + skewed(d0 / 2 < half ? d0 / 2 : 0);
+#pragma unroll
+        for (int v = 0; v < 16 / N; ++v) {
+            float x[N];
+            Vec<T>::widen(reinterpret_cast<const uint4 *>(row + d0)[v], x);
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const int k = v * N + i;
+                const bool on = k / 2 < some;
+                const float2 w = on ? c[k / 2] : make_float2(1.f, 0.f);
+                y[k] = on ? x[i] * w.x - x[i + 1] * w.y : x[i];
+                y[k + 1] = on ? x[i + 1] * w.x + x[i] * w.y : x[i + 1];
+                err[k] = err[k + 1] = on ? fabsf(x[i]) + fabsf(x[i + 1]) : 0.f;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < 16 / N; ++v) {
+            float x[N], o[N];
+            if constexpr (kMode == kAny) {
+                load_pairs<T>(row, d0 + v * N, rot, false, x, o);
+            } else {
+                Vec<T>::widen(reinterpret_cast<const uint4 *>(row + d0)[v], x);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int k = v * N + i, d = d0 + k;
+                y[k] = x[i];
+                err[k] = 0.f;
+                if constexpr (kMode == kAny) {
+                    if (d < rot) {
+                        const bool second = d >= half;
+                        const float2 w = cs[skewed(second ? d - half : d)];
+                        y[k] = second ? x[i] * w.x + o[i] * w.y : x[i] * w.x - o[i] * w.y;
+                        err[k] = fabsf(x[i]) + fabsf(o[i]);
+                    }
+                }
+            }
+        }
+    }
+    uint32_t top = 0;                                    // as bits: magnitudes compare like integers, NaN above all
+    float most = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        top = max(top, __float_as_uint(y[k]) & 0x7fffffffu);
+        if constexpr (kMode != kPlain) most = fmaxf(most, err[k]);
+    }
+    if (top > 0x7f800000u) {
+        *reinterpret_cast<uint2 *>(codes) = make_uint2(0u, 0u);
+        *scale_at = (uint8_t)kFp4NanScale;
+        return;
+    }
+    const float amax = __uint_as_float(top);
+    if (amax > kFp4Top) report(a.status, PA_DEV_RANGE);
+    uint32_t byte = fp4_scale_of(amax, amax);
+    const float turn_err = kTurnError * (float)a.factor;
+    if constexpr (kMode != kPlain) {
+        const float e = most * turn_err, lo = fmaxf(amax - e, 0.f), hi = amax + e;
+        if (fp4_scale_of(lo, lo) != fp4_scale_of(hi, hi)) byte = exact_scale<T>(a, row, tok, d0, amax);
+    }
+    const float scale = fp4_scale_value(byte), inv = byte != 0 ? 1.f / scale : 0.f;
+    uint32_t out[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        float lo[8], hi[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float q = y[8 * p + i] * inv;
+            if constexpr (kMode == kPlain && kBf16) {
+                // A bf16 element divided by a scale of 4 bits is a border of two codes or at least
+                // 2^-9 of it away; the product with the inverse is off by 2^-23, which rounding to
+                // 16 bits takes back.
+                lo[i] = __uint_as_float((__float_as_uint(q) + 0x80u) & 0xffffff00u);
+            } else {
+                const float e = kMode == kPlain ? fabsf(q) * 0x1p-22f
+                                                : fmaxf(err[8 * p + i] * turn_err * inv, fabsf(q) * 0x1p-22f);
+                lo[i] = q - e;
+                hi[i] = q + e;
+            }
+        }
+        out[p] = f32x8_to_e2m1x8(lo);
+        if constexpr (!(kMode == kPlain && kBf16)) {
+            // the codes of the value less and more its error: where they differ the code comes from 64 bits
+            const uint32_t differ = out[p] ^ f32x8_to_e2m1x8(hi);
+            if (differ != 0) {
+#pragma unroll 1
+                for (int i = 0; i < 8; ++i) {
+                    if (((differ >> (4 * i)) & 15u) == 0) continue;
+                    const int d = d0 + 8 * p + i;
+                    const double x = kMode == kPlain ? (double)to_float(row[d]) : exact_of<T>(a, row, tok, d);
+                    out[p] = (out[p] & ~(15u << (4 * i))) | (exact_e2m1(x, scale) << (4 * i));
+                }
+            }
+        }
+    }
+    *reinterpret_cast<uint2 *>(codes) = make_uint2(out[0], out[1]);
+    *scale_at = (uint8_t)byte;
+}
+
+// The keys' and values' units of a CTA's tokens.
+template <typename T, int kMode>
+__device__ __forceinline__ void encode_tokens(const RopeArgs &a, int cta, float2 *table) {
+    const int half = a.rotary_dim / 2, D = a.head_dim, units = D / 16, per_token = 2 * a.num_kv_heads * units;
+    const int group = cta / a.tile_splits, split = cta - group * a.tile_splits;
+    const int64_t t0 = (int64_t)group * a.tile_tokens, limit = (int64_t)a.num_blocks * kBlockSize;
+    const int nt = (int)min((int64_t)a.tile_tokens, a.num_tokens - t0);
+    const int table_row = skewed(a.table_row);
+    if constexpr (kMode != kPlain) {
+        for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
+            const int t = i / half, p = i - t * half;
+            table[t * table_row + skewed(p)] = turn_of(a.positions[t0 + t], a.turns[p], (float)a.factor);
+        }
+        __syncthreads();
+    }
+    for (int i = threadIdx.x + split * kRopeThreads; i < nt * per_token; i += a.tile_splits * kRopeThreads) {
+        const int t = i / per_token, rest = i - t * per_token, row = rest / units, unit = rest - row * units;
+        const bool value = row >= a.num_kv_heads;
+        const int h = value ? row - a.num_kv_heads : row;
+        const int64_t tok = t0 + t, slot = a.slot_mapping[tok];
+        if (slot < 0) continue;
+        if (slot >= limit) {
+            if (rest == 0) report(a.status, PA_DEV_BAD_SLOT);
+            continue;
+        }
+        const int64_t blk = slot / kBlockSize;
+        const int off = (int)(slot - blk * kBlockSize);
+        uint8_t *tile = static_cast<uint8_t *>(value ? a.value_cache : a.key_cache) +
+                        (blk * a.num_kv_heads + h) * fp4_tile_bytes(D);
+        uint8_t *codes = tile + off * (D / 2) + unit * 8, *scale = tile + fp4_scales_at(D) + off * units + unit;
+        const T *src = static_cast<const T *>(value ? a.value : a.key) + tok * (value ? a.v_stride : a.k_stride) +
+                       (int64_t)h * D;
+        if (value) encode_unit<T, kPlain>(a, src, tok, unit * 16, nullptr, codes, scale);
+        else encode_unit<T, kMode>(a, src, tok, unit * 16, table + t * table_row, codes, scale);
+    }
+}
+
+template <typename T, int kMode>
+__global__ void __launch_bounds__(kRopeThreads) pa_rope_write_fp4_kernel(const RopeArgs a) {
+    extern __shared__ __align__(16) float2 s_table[];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    if ((int)blockIdx.x < a.tile_ctas) encode_tokens<T, kMode>(a, blockIdx.x, s_table);
+    else turn_rows<T>(a, blockIdx.x - a.tile_ctas, s_table, false);
+}
+
+template <typename T>
+pa_status launch_write(RopeArgs &a, cudaStream_t stream) {
+    const int64_t n = a.num_tokens, sms = device_sms();
+    const int64_t row_ctas = plan_rows<T>(a, a.num_q_heads);
+    const int half = a.rotary_dim / 2;
+    a.tile_tokens = 1;
+    while (a.tile_tokens < kMostEncodeTokens && n / (2 * a.tile_tokens) >= 4 * sms) a.tile_tokens *= 2;
+    const int64_t items = (int64_t)a.tile_tokens * 2 * a.num_kv_heads * (a.head_dim / 16);
+    const int64_t passes = (items + kRopeThreads - 1) / kRopeThreads;
+    a.tile_splits = (int)std::max<int64_t>(1, std::min<int64_t>(passes, 4 * sms * a.tile_tokens / n));
+    const int64_t tiles = (n + a.tile_tokens - 1) / a.tile_tokens * a.tile_splits, grid = tiles + row_ctas;
+    if (grid >= ((int64_t)1 << 31)) return PA_ERR_UNSUPPORTED;
+    a.tile_ctas = (int)tiles;
+    const size_t smem = std::max((size_t)a.tile_tokens * skewed(a.table_row), (size_t)a.row_tokens * a.table_row) * sizeof(float2);
+    const auto kernel = half == 0        ? pa_rope_write_fp4_kernel<T, kPlain>
+                        : a.interleaved  ? pa_rope_write_fp4_kernel<T, kNeighbours>
+                        : half % 16 == 0 ? pa_rope_write_fp4_kernel<T, kHalves>
+                                         : pa_rope_write_fp4_kernel<T, kAny>;
+    if (smem > 44 * 1024) {
+        cudaError_t e = allow_smem(kernel, kMostTables);
+        if (e != cudaSuccess) return cuda_failure(e, "cudaFuncSetAttribute(4-bit write)");
+    }
+    cudaError_t e = launch_chained(kernel, dim3((unsigned)grid), dim3(kRopeThreads), smem, stream, a);
+    if (e != cudaSuccess) return cuda_failure(e, "pa_rope_write_fp4_kernel launch");
+    count_launches(1);
+    return PA_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Reading back
+// ---------------------------------------------------------------------------
+constexpr int kReadThreads = 256;
+
+struct ReadArgs {
+    void *key_out, *value_out;       // [num_seqs * width][num_kv_heads][16][head_dim]
+    const uint8_t *key_cache, *value_cache;
+    const int32_t *block_tables;
+    const int32_t *context_lens;
+    const int32_t *query_start;      // nullptr, or chunks whose rows each have their window
+    int32_t *tables_out;             // nullptr, or [num_seqs][width]: where each block went
+    int32_t *lens_out;               // with query_start: the lengths, -1 where a sequence's rows leave the query's
+    int32_t *status;
+    int num_seqs, num_kv_heads, head_dim;
+    int max_blocks, num_blocks, width, window;
+    int num_rows;                    // of the query
+    int splits;                      // CTAs of a block
+};
+
+// f16 pair times f16 pair, exact, as two floats
+__device__ __forceinline__ float2 product_of(uint32_t codes, uint32_t scale) {
+    const uint32_t v = mul_f16x2(codes, scale);
+    return make_float2(f16lo(v), f16hi(v));
+}
+
+// One CTA (or `splits`) a block of a context.  kDim: head_dim, or 0 where it is none of the
+// usual ones.
+template <typename T, int kDim>
+__global__ void __launch_bounds__(kReadThreads) pa_read_fp4_kernel(const ReadArgs a) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int D = kDim > 0 ? kDim : a.head_dim;
+    const int at = blockIdx.x / a.splits, split = blockIdx.x - at * a.splits;
+    const int b = at / a.width, j = at - b * a.width;
+    int len = a.context_lens[b];
+    const int phys_ahead = a.block_tables[(int64_t)b * a.max_blocks + j];
+    const bool first_thread = threadIdx.x == 0 && split == 0;
+    if (len < 0 || len > a.width * kBlockSize) {
+        if (first_thread && j == 0) report(a.status, PA_DEV_BAD_CONTEXT_LEN);
+        len = len < 0 ? 0 : a.width * kBlockSize;
+    }
+    if (first_thread && a.tables_out != nullptr) a.tables_out[at] = at;
+    int64_t chunk = 1;
+    if (a.query_start != nullptr) {
+        const int64_t from = a.query_start[b], end = a.query_start[b + 1];
+        const bool outside = from < 0 || end < from || end > a.num_rows;
+        chunk = end - from;
+        if (first_thread && j == 0) a.lens_out[b] = outside ? -1 : a.context_lens[b];
+        if (outside || chunk == 0) return;               // no row attends to the context
+    }
+    // a chunk's first row is the one that looks farthest back
+    const int64_t start = a.window > 0 ? len - chunk + 1 - a.window : 0;
+    const int rows = min(len - j * kBlockSize, kBlockSize);      // of the block
+    if (rows <= 0 || (int64_t)(j + 1) * kBlockSize <= start) return;
+    int phys = phys_ahead;
+    if ((unsigned)phys >= (unsigned)a.num_blocks) {
+        if (first_thread) report(a.status, PA_DEV_BAD_BLOCK_ID);
+        phys = 0;
+    }
+    const int chunks = D / 8, per_tile = kBlockSize * chunks, all = 2 * a.num_kv_heads * per_tile;
+    const int64_t in = (int64_t)phys * a.num_kv_heads, out = (int64_t)at * a.num_kv_heads;
+#pragma unroll 4
+    for (int u = threadIdx.x + split * kReadThreads; u < all; u += a.splits * kReadThreads) {
+        int tile = u / per_tile;
+        const int rest = u - tile * per_tile, row = rest / chunks, c = rest - row * chunks;
+        const bool value = tile >= a.num_kv_heads;
+        if (value) tile -= a.num_kv_heads;
+        const uint8_t *src = (value ? a.value_cache : a.key_cache) + (in + tile) * fp4_tile_bytes(D);
+        T *dst = static_cast<T *>(value ? a.value_out : a.key_out) + (out + tile) * kBlockSize * D + rest * 8;
+        float2 v[4];
+        if (row < rows) {
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(src + rest * 4);
+            const uint32_t s = fp4_scale_pair<0>(src[fp4_scales_at(D) + row * (D / 16) + c / 2]);
+            uint32_t x[4];
+            e2m1x8_to_f16x2x4(w, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = product_of(x[i], s);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = make_float2(0.f, 0.f);
+        }
+        if constexpr (sizeof(T) == 4) {
+            reinterpret_cast<float4 *>(dst)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+            reinterpret_cast<float4 *>(dst)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+        } else {
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                                                         pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+        }
+    }
+}
+
+template <typename T>
+pa_status launch_read(ReadArgs &a, cudaStream_t stream) {
+    const int64_t blocks = (int64_t)a.num_seqs * a.width;
+    const int64_t passes = ((int64_t)2 * a.num_kv_heads * kBlockSize * (a.head_dim / 8) + kReadThreads - 1) / kReadThreads;
+    a.splits = (int)std::max<int64_t>(1, std::min<int64_t>(passes, 8LL * device_sms() / blocks));
+    if (blocks * a.splits >= ((int64_t)1 << 31)) return PA_ERR_UNSUPPORTED;
+    const auto kernel = a.head_dim == 64    ? pa_read_fp4_kernel<T, 64>
+                        : a.head_dim == 128 ? pa_read_fp4_kernel<T, 128>
+                        : a.head_dim == 256 ? pa_read_fp4_kernel<T, 256>
+                                            : pa_read_fp4_kernel<T, 0>;
+    cudaError_t e = launch_chained(kernel, dim3((unsigned)(blocks * a.splits)), dim3(kReadThreads), 0, stream, a);
+    if (e != cudaSuccess) return cuda_failure(e, "pa_read_fp4_kernel launch");
+    count_launches(1);
+    return PA_OK;
+}
+
+// Whether n bytes from p on meet m bytes from q on.
+bool ranges_meet(const void *p, size_t n, const void *q, size_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
+    return n > 0 && m > 0 && x < y + m && y < x + n;
+}
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Sizes of head_dim that a pool's rows may have.
+bool pool_head_dim(int head_dim) { return head_dim > 0 && head_dim <= 256 && head_dim % 16 == 0; }
+
+// What prefill stages: the prefill's own workspace, tables, then the blocks.
+struct Stage {
+    size_t tables, lens, keys, values, bytes;
+};
+Stage stage_of(int num_seqs, int num_kv_heads, int head_dim, int width) {
+    auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    const size_t pool = up((size_t)num_seqs * width * num_kv_heads * kBlockSize * head_dim * 2);
+    Stage s;
+    s.tables = up(pa_prefill_workspace_bytes());
+    s.lens = s.tables + up((size_t)num_seqs * width * sizeof(int32_t));
+    s.keys = s.lens + up((size_t)num_seqs * sizeof(int32_t));
+    s.values = s.keys + pool;
+    s.bytes = s.values + pool;
+    return s;
+}
+// Blocks of a sequence that are read: max_context_len's, or the table's where it is 0.
+int width_of(int max_blocks_per_seq, int max_context_len) {
+    if (max_context_len == 0) return max_blocks_per_seq;
+    return std::min(max_blocks_per_seq, (int)(((int64_t)max_context_len + kBlockSize - 1) / kBlockSize));
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" pa_status pa_rope_cache_write_fp4(void *query_out, const void *query, const void *key, const void *value,
+                                             const int32_t *positions, const uint64_t *turns, double attention_factor,
+                                             int rotary_dim, int interleaved, void *key_cache, void *value_cache,
+                                             const int64_t *slot_mapping, int num_tokens, int num_q_heads,
+                                             int num_kv_heads, int head_dim, int64_t query_out_stride,
+                                             int64_t query_stride, int64_t key_stride, int64_t value_stride,
+                                             int block_size, int num_blocks, pa_dtype dtype, int32_t *device_status,
+                                             void *stream) {
+    if (num_tokens < 0 || num_q_heads < 0 || num_kv_heads <= 0 || head_dim <= 0 || rotary_dim < 0 ||
+        rotary_dim > head_dim || rotary_dim % 2 != 0 || block_size != kBlockSize || num_blocks <= 0 ||
+        !(attention_factor >= 0x1p-20 && attention_factor <= 0x1p20) || (dtype != PA_DTYPE_F32 && dtype != PA_DTYPE_BF16))
+        return PA_ERR_INVALID_ARG;
+    if (!pool_head_dim(head_dim)) return PA_ERR_UNSUPPORTED;
+    const int esize = dtype == PA_DTYPE_F32 ? 4 : 2;
+    const int64_t q_row = (int64_t)num_q_heads * head_dim, kv_row = (int64_t)num_kv_heads * head_dim;
+    if (num_tokens == 0) return PA_OK;
+    if (num_q_heads > 0 && (!query || !query_out || query_stride < q_row || query_out_stride < q_row ||
+                            !aligned16(query) || !aligned16(query_out) || (query_stride * esize) % 16 != 0 ||
+                            (query_out_stride * esize) % 16 != 0))
+        return PA_ERR_INVALID_ARG;
+    if (!key || !value || !key_cache || !value_cache || !slot_mapping || key_stride < kv_row || value_stride < kv_row ||
+        !aligned16(key) || !aligned16(value) || !aligned16(key_cache) || !aligned16(value_cache) ||
+        (key_stride * esize) % 16 != 0 || (value_stride * esize) % 16 != 0 ||
+        (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+        return PA_ERR_INVALID_ARG;
+    if (rotary_dim > 0 && (!positions || !turns || !aligned4(positions) || (reinterpret_cast<uintptr_t>(turns) & 7u)))
+        return PA_ERR_INVALID_ARG;
+    if (num_q_heads > 0) {
+        // rows are read and written by many CTAs: query_out is query itself or apart from the inputs
+        const int64_t n = num_tokens, qs = query_stride * esize, os = query_out_stride * esize, w = q_row * esize;
+        const bool same = query == query_out && (query_stride == query_out_stride || n == 1);
+        if ((!same && rows_touch(query_out, os, w, query, qs, w, n)) ||
+            rows_touch(query_out, os, w, key, key_stride * esize, kv_row * esize, n) ||
+            rows_touch(query_out, os, w, value, value_stride * esize, kv_row * esize, n))
+            return PA_ERR_INVALID_ARG;
+    }
+    // items of one CTA are counted in 32 bits
+    if ((q_row + 2 * kv_row) * kMostEncodeTokens >= ((int64_t)1 << 31)) return PA_ERR_UNSUPPORTED;
+    RopeArgs a = {};
+    a.query = query;
+    a.key = key;
+    a.value = value;
+    a.query_out = query_out;
+    a.key_cache = key_cache;
+    a.value_cache = value_cache;
+    a.positions = positions;
+    a.turns = turns;
+    a.slot_mapping = slot_mapping;
+    a.status = device_status;
+    a.q_stride = query_stride;
+    a.k_stride = key_stride;
+    a.v_stride = value_stride;
+    a.q_out_stride = query_out_stride;
+    a.factor = attention_factor;
+    a.num_tokens = num_tokens;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.rotary_dim = rotary_dim;
+    a.interleaved = interleaved != 0;
+    a.num_blocks = num_blocks;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return dtype == PA_DTYPE_F32 ? launch_write<float>(a, st) : launch_write<__nv_bfloat16>(a, st);
+}
+
+extern "C" pa_status pa_cache_read_fp4(void *key_out, void *value_out, const void *key_cache, const void *value_cache,
+                                       const int32_t *block_tables, const int32_t *context_lens, int num_seqs,
+                                       int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                                       int num_blocks, int max_context_len, int window, pa_dtype dtype,
+                                       int32_t *device_status, void *stream) {
+    if (num_seqs < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size != kBlockSize || max_blocks_per_seq < 0 ||
+        max_blocks_per_seq > 0x7fffffff / kBlockSize || num_blocks <= 0 || max_context_len < 0 || window < 0 ||
+        (dtype != PA_DTYPE_F32 && dtype != PA_DTYPE_BF16))
+        return PA_ERR_INVALID_ARG;
+    if (!pool_head_dim(head_dim)) return PA_ERR_UNSUPPORTED;
+    const int width = width_of(max_blocks_per_seq, max_context_len);
+    if (num_seqs == 0 || width == 0) return PA_OK;
+    if (!key_out || !value_out || !key_cache || !value_cache || !block_tables || !context_lens || !aligned16(key_out) ||
+        !aligned16(value_out) || !aligned16(key_cache) || !aligned16(value_cache) || !aligned4(block_tables) ||
+        !aligned4(context_lens))
+        return PA_ERR_INVALID_ARG;
+    // units of a block and blocks of a call are counted in 32 bits
+    if ((int64_t)num_kv_heads * 4 * head_dim >= ((int64_t)1 << 30) || (int64_t)num_seqs * width >= ((int64_t)1 << 31))
+        return PA_ERR_UNSUPPORTED;
+    const size_t in = (size_t)num_blocks * num_kv_heads * fp4_tile_bytes(head_dim);
+    const size_t out = (size_t)num_seqs * width * num_kv_heads * kBlockSize * head_dim * (dtype == PA_DTYPE_F32 ? 4 : 2);
+    for (const void *o : {key_out, value_out})
+        if (ranges_meet(o, out, key_cache, in) || ranges_meet(o, out, value_cache, in) ||
+            ranges_meet(o, out, block_tables, (size_t)num_seqs * max_blocks_per_seq * sizeof(int32_t)) ||
+            ranges_meet(o, out, context_lens, (size_t)num_seqs * sizeof(int32_t)))
+            return PA_ERR_INVALID_ARG;
+    if (ranges_meet(key_out, out, value_out, out)) return PA_ERR_INVALID_ARG;
+    ReadArgs a = {};
+    a.key_out = key_out;
+    a.value_out = value_out;
+    a.key_cache = static_cast<const uint8_t *>(key_cache);
+    a.value_cache = static_cast<const uint8_t *>(value_cache);
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.status = device_status;
+    a.num_seqs = num_seqs;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.width = width;
+    a.window = window;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return dtype == PA_DTYPE_F32 ? launch_read<float>(a, st) : launch_read<__nv_bfloat16>(a, st);
+}
+
+extern "C" size_t pa_prefill_fp4_workspace_bytes(int num_seqs, int num_kv_heads, int head_dim, int max_blocks_per_seq,
+                                                 int max_context_len) {
+    if (num_seqs < 0 || num_kv_heads <= 0 || head_dim <= 0 || max_blocks_per_seq < 0 ||
+        max_blocks_per_seq > 0x7fffffff / kBlockSize || max_context_len < 0)
+        return (size_t)-1;
+    return stage_of(num_seqs, num_kv_heads, head_dim, width_of(max_blocks_per_seq, max_context_len)).bytes;
+}
+
+extern "C" pa_status pa_prefill_fp4(void *out, const void *query, const void *key_cache, const void *value_cache,
+                                    const int32_t *block_tables, const int32_t *context_lens,
+                                    const int32_t *query_start, int num_seqs, int num_q_heads, int num_kv_heads,
+                                    int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
+                                    int num_query_tokens, int max_query_len, int max_context_len, float scale, int window,
+                                    void *workspace, size_t workspace_bytes, int32_t *device_status, void *stream) {
+    if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 || head_dim <= 0 ||
+        block_size != kBlockSize || max_blocks_per_seq < 0 || max_blocks_per_seq > 0x7fffffff / kBlockSize ||
+        num_blocks <= 0 || num_query_tokens < 0 || max_query_len < 0 || max_context_len < 0 || window < 0 ||
+        !(scale == scale))
+        return PA_ERR_INVALID_ARG;
+    const int group = num_q_heads / num_kv_heads;
+    if (head_dim != 128 || (group != 1 && group != 2 && group != 4 && group != 8 && group != 16)) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || num_query_tokens == 0 || max_query_len == 0) return PA_OK;
+    const int width = width_of(max_blocks_per_seq, max_context_len);
+    if (!out || !query || !key_cache || !value_cache || !context_lens || !query_start || !block_tables || width == 0 ||
+        !aligned16(out) || !aligned16(query) || !aligned16(key_cache) || !aligned16(value_cache) ||
+        !aligned4(block_tables) || !aligned4(context_lens) || !aligned4(query_start))
+        return PA_ERR_INVALID_ARG;
+    const int64_t staged = (int64_t)num_seqs * width;
+    if ((int64_t)num_kv_heads * 4 * head_dim >= ((int64_t)1 << 30) || staged * num_kv_heads * kBlockSize >= ((int64_t)1 << 31))
+        return PA_ERR_UNSUPPORTED;
+    const Stage s = stage_of(num_seqs, num_kv_heads, head_dim, width);
+    if (workspace == nullptr || workspace_bytes < s.bytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
+    uint8_t *w = static_cast<uint8_t *>(workspace);
+    ReadArgs a = {};
+    a.key_out = w + s.keys;
+    a.value_out = w + s.values;
+    a.key_cache = static_cast<const uint8_t *>(key_cache);
+    a.value_cache = static_cast<const uint8_t *>(value_cache);
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.query_start = query_start;
+    a.tables_out = reinterpret_cast<int32_t *>(w + s.tables);
+    a.lens_out = reinterpret_cast<int32_t *>(w + s.lens);
+    a.num_rows = num_query_tokens;
+    a.status = device_status;
+    a.num_seqs = num_seqs;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.width = width;
+    a.window = window;
+    const pa_status rc = launch_read<__nv_bfloat16>(a, static_cast<cudaStream_t>(stream));
+    if (rc != PA_OK) return rc;
+    return pa_prefill(out, query, a.key_out, a.value_out, a.tables_out, a.lens_out, query_start, num_seqs, num_q_heads,
+                      num_kv_heads, head_dim, block_size, width, (int)staged, num_query_tokens, max_query_len, scale,
+                      PA_DTYPE_BF16, window, w, s.tables, device_status, stream);
+}

@@ -1,0 +1,842 @@
+// Paged decode attention over pools held in 4 bits ("KV cache: la memoria de trabajo
+// que sostiene la inferencia LLM", section "Trucos para que el cuaderno sea más fino":
+// quantising the cache), one query token per sequence.  The format is in pa_fp4.cuh.
+//
+// One CTA handles one (sequence, KV head, partition).  Each warp owns every NW-th
+// block of the partition and streams it through its own ring of slots: a block's K
+// and V tiles are 9 head_dim bytes each, whole in the pool, so a bulk copy brings one.
+// The group's query heads are the N columns of mma.sync m16n8k16 tiles in transposed
+// form, S^T[16 tokens x 8 heads] = K Q^T and O^T[head_dim x 8 heads] += V^T P^T, so
+// one pass over K/V serves the group; a group of more than 8 heads is split over
+// CTAs that follow one another and find the tiles in L2.  Codes times scales are
+// exact in f16.
+//
+// Few sequences: a context is cut into parts so that the GPU is full.  Up to eight
+// parts form a thread-block cluster that merges through distributed shared memory;
+// more parts leave partials in the workspace for a second kernel.
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "pa_device.cuh"
+#include "pa_fp4.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+namespace {
+
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kHeads = 8;                        // query heads of a CTA at most
+// a head's reference maximum moves only when a score exceeds it by more than
+// 2^8: the weights stay in [0, 256], which f16 holds
+constexpr float kLazyLog2 = 8.f;
+
+struct Fp4Args {
+    void *out;
+    const void *query;
+    const uint8_t *key_cache, *value_cache;
+    const int32_t *block_tables;
+    const int32_t *context_lens;
+    const int32_t *query_start;  // sequence b's row is query_start[b]; nullptr: row b
+    float *part_o;               // [(b * Hq + h) * max_parts + part][head_dim]
+    float2 *part_ml;             // (reference, sum)
+    int32_t *status;
+    int num_seqs, num_rows, num_q_heads, num_kv_heads;
+    int heads;                   // query heads of a CTA
+    int splits;                  // CTAs of a (sequence, KV head, partition)
+    int max_blocks, num_blocks;
+    int part_blocks, max_parts;
+    int window;
+    float scale_log2;
+};
+
+struct Span {
+    int L, start, blk0, nblk, nparts;
+};
+
+// Blocks of a context of `len` tokens: [*first, *blocks), the first position
+// attended in *start; *L the length, clamped.
+__device__ __forceinline__ void range_of(const Fp4Args &a, int len, bool say, int *L, int *start, int *first,
+                                         int *blocks) {
+    const int lmax = a.max_blocks * kBlockSize;
+    if (len < 0 || len > lmax) {
+        if (say) report(a.status, PA_DEV_BAD_CONTEXT_LEN);
+        len = len < 0 ? 0 : lmax;
+    }
+    *L = len;
+    *start = a.window > 0 && len > a.window ? len - a.window : 0;
+    *first = *start / kBlockSize;
+    *blocks = (len + kBlockSize - 1) / kBlockSize;
+}
+
+// Part `part` of `parts` of a context, cut evenly.
+__device__ __forceinline__ void even_span(const Fp4Args &a, int len, int part, int parts, bool say, Span &w) {
+    int first, blocks;
+    range_of(a, len, say, &w.L, &w.start, &first, &blocks);
+    const int n = max(blocks - first, 0);
+    w.blk0 = first + (int)((int64_t)part * n / parts);
+    w.nblk = first + (int)((int64_t)(part + 1) * n / parts) - w.blk0;
+    w.nparts = 1;
+}
+
+// Partition `part` of a context of `len` tokens; false when it lies past the end.
+__device__ __forceinline__ bool span_of(const Fp4Args &a, int len, int part, bool say, Span &w) {
+    int first, blocks;
+    range_of(a, len, say, &w.L, &w.start, &first, &blocks);
+    w.nparts = blocks <= first ? 1 : (blocks - first + a.part_blocks - 1) / a.part_blocks;
+    if (part >= w.nparts) return false;
+    w.blk0 = first + part * a.part_blocks;
+    w.nblk = max(min(w.blk0 + a.part_blocks, blocks) - w.blk0, 0);
+    return true;
+}
+
+// The row of query and output that is sequence b's, or -1: it brings none, or more
+// than the one that a decode step has.
+__device__ __forceinline__ int row_of(const Fp4Args &a, int b, bool say) {
+    if (a.query_start == nullptr) return b;
+    const int at = a.query_start[b], end = a.query_start[b + 1];
+    if (end == at) return -1;
+    const bool outside = at < 0 || end < at || end > a.num_rows;
+    if (!outside && end == at + 1) return at;
+    if (say) report(a.status, outside ? PA_DEV_BAD_CONTEXT_LEN : PA_DEV_BAD_QUERY_LEN);
+    return -1;
+}
+
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+    uint32_t v;
+    asm volatile("{\n\t.reg .u16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(addr));
+    return v;
+}
+// kWords (1, 2 or 4) words from a place aligned to them
+template <int kWords>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t *w) {
+    if constexpr (kWords == 1) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+    else if constexpr (kWords == 2) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+    else
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(addr));
+}
+
+// A tile, whole and contiguous in its pool, into shared memory.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
+// One warp's attention state over its blocks: 8 query heads (columns; those past
+// the group have a zero query and are not stored).  Lane (g, t) = (lane / 4, lane %
+// 4) holds scores of tile rows g and g + 8 for heads 2t and 2t + 1.
+//  * S^T: the contraction may visit the head dimension in any order as long as K and
+//    Q agree, so lane t of a row reads a quarter of it (of each 128 elements) in
+//    consecutive pieces of 16 bytes, 32 codes under two scales.
+//  * O^T: the A operand needs two tokens of one element in a register.  Lane g reads
+//    the 16 codes under scale g of four tokens; codes of two tokens are paired
+//    within bytes (the even elements, then the odd ones), so that widening gives the pair.
+//  * Tile row r stands for token r, but rows 4, 5 and 6, 7 (and 12 to 15) are
+//    swapped: the four tokens that lanes t = 0 to 3 read together are then two even
+//    and two odd ones, which meet in each bank twice instead of four times.
+template <int D>
+struct Warp4 {
+    static constexpr int kRow = D / 2;           // bytes of a row's codes
+    static constexpr int kScales = D / 16;       // of a row
+    static constexpr int kKWords = D / 32;       // words of a row's codes that a lane reads for K
+    static constexpr int kLoad = D == 64 ? 2 : 4;        // words of one load for K
+
+    uint32_t qb[D / 16][2];
+    float o[D / 16][4];
+    float m0, m1, l0, l1;
+    float qs0, qs1;              // powers of two of heads 2t and 2t + 1: what their scores are multiplied by
+    int lane, g, t;
+    uint32_t kcode, kscale, vcode[2], vscale[2];
+
+    // First element of this lane's K word w, and of its V word v.
+    __device__ __forceinline__ int k_at(int w) const { return D == 64 ? 16 * t + 8 * w : 128 * (w / 4) + 32 * t + 8 * (w % 4); }
+    __device__ __forceinline__ int v_at(int v) const { return D == 64 ? 8 * g : 128 * (v / 2) + 16 * g + 8 * (v % 2); }
+
+    __device__ __forceinline__ void load(const Fp4Args &a, int row, int first_head, int lane_, uint4 (&w)[kKWords]) {
+        lane = lane_;
+        g = lane >> 2;
+        t = lane & 3;
+        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.query) + ((int64_t)row * a.num_q_heads + first_head + g) * D;
+#pragma unroll
+        for (int c = 0; c < kKWords; ++c)
+            w[c] = g < a.heads ? *reinterpret_cast<const uint4 *>(q + k_at(c)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+
+    __device__ __forceinline__ void init(const Fp4Args &a, const uint4 (&w)[kKWords]) {
+        const int token = g < 4 ? g : g ^ 1, pair = t < 2 ? 2 * t : 2 * t + 1;
+        kcode = (uint32_t)(token * kRow + k_at(0) / 2);
+        kscale = (uint32_t)(fp4_scales_at(D) + token * kScales + k_at(0) / 16);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            vcode[i] = (uint32_t)((pair ^ i) * kRow + v_at(0) / 2);
+            vscale[i] = (uint32_t)(fp4_scales_at(D) + (pair ^ i) * kScales + v_at(0) / 16);
+        }
+        uint32_t amax = 0;                               // as bits: magnitudes compare like integers
+#pragma unroll
+        for (int c = 0; c < kKWords; ++c)
+#pragma unroll
+            for (uint32_t x : {w[c].x, w[c].y, w[c].z, w[c].w})
+                amax = max(amax, max((x << 16) & 0x7fffffffu, x & 0x7fff0000u));
+        if (amax >= 0x47800000u) {                       // 65536 or more: looked at again, as NaN is none of them
+            bool beyond = false;
+#pragma unroll
+            for (int c = 0; c < kKWords; ++c)
+                beyond |= bf16x2_beyond_f16(w[c].x) | bf16x2_beyond_f16(w[c].y) | bf16x2_beyond_f16(w[c].z) | bf16x2_beyond_f16(w[c].w);
+            if (beyond) report(a.status, PA_DEV_RANGE);  // the f16 query is not the query
+        }
+        amax = max(amax, __shfl_xor_sync(kFull, amax, 1));
+        amax = max(amax, __shfl_xor_sync(kFull, amax, 2));
+        // A row is brought up by a power of two so that its largest magnitude lies in
+        // [2^14, 2^15): f16 then holds every element exactly but those below 2^-29 of it,
+        // which are off by at most 2^-39 of it.
+        const int up = min(max(14 + 127 - (int)(amax >> 23), 0), 126);
+        const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+        const int down = (127 - up) << 23;               // 2^-up, of row g
+        qs0 = __int_as_float(__shfl_sync(kFull, down, 8 * t)) * a.scale_log2;
+        qs1 = __int_as_float(__shfl_sync(kFull, down, 8 * t + 4)) * a.scale_log2;
+#pragma unroll
+        for (int c = 0; c < kKWords; ++c) {
+            qb[2 * c][0] = pack_f16x2(bf16lo(w[c].x) * f, bf16hi(w[c].x) * f);
+            qb[2 * c][1] = pack_f16x2(bf16lo(w[c].y) * f, bf16hi(w[c].y) * f);
+            qb[2 * c + 1][0] = pack_f16x2(bf16lo(w[c].z) * f, bf16hi(w[c].z) * f);
+            qb[2 * c + 1][1] = pack_f16x2(bf16lo(w[c].w) * f, bf16hi(w[c].w) * f);
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        m0 = m1 = -INFINITY;
+        l0 = l1 = 0.f;
+    }
+
+    // One block, of which the rows [nlo, nvalid) are attended (at least one).
+    __device__ __forceinline__ void block(uint32_t ktile, uint32_t vtile, int nlo, int nvalid) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kKWords / kLoad; ++c) {
+            uint32_t r0[kLoad], r1[kLoad];
+            lds_words<kLoad>(ktile + kcode + 64 * c, r0);
+            lds_words<kLoad>(ktile + kcode + 64 * c + 8 * kRow, r1);
+            uint32_t c0, c1;
+            if constexpr (D == 64) {
+                c0 = lds8(ktile + kscale);
+                c1 = lds8(ktile + kscale + 8 * kScales);
+            } else {
+                c0 = lds16(ktile + kscale + 8 * c);
+                c1 = lds16(ktile + kscale + 8 * c + 8 * kScales);
+            }
+            const uint32_t s0[2] = {fp4_scale_pair<0>(c0), fp4_scale_pair<1>(c0)};
+            const uint32_t s1[2] = {fp4_scale_pair<0>(c1), fp4_scale_pair<1>(c1)};
+#pragma unroll
+            for (int w = 0; w < kLoad; ++w) {
+                uint32_t x[4], y[4];
+                e2m1x8_to_f16x2x4(r0[w], x);
+                e2m1x8_to_f16x2x4(r1[w], y);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = mul_f16x2(x[i], s0[w / 2]);
+                    y[i] = mul_f16x2(y[i], s1[w / 2]);
+                }
+                const int k = 2 * (c * kLoad + w);
+                const uint32_t first[4] = {x[0], y[0], x[1], y[1]}, second[4] = {x[2], y[2], x[3], y[3]};
+                mma_f16_16816(s, first, qb[k][0], qb[k][1]);
+                mma_f16_16816(s, second, qb[k + 1][0], qb[k + 1][1]);
+            }
+        }
+        const bool part = nlo > 0 || nvalid < kBlockSize;
+        s[0] *= qs0;
+        s[1] *= qs1;
+        s[2] *= qs0;
+        s[3] *= qs1;
+        if (part) {
+            const int token = g < 4 ? g : g ^ 1;
+            const bool v0 = token >= nlo && token < nvalid, v1 = token + 8 >= nlo && token + 8 < nvalid;
+            s[0] = v0 ? s[0] : -INFINITY;
+            s[1] = v0 ? s[1] : -INFINITY;
+            s[2] = v1 ? s[2] : -INFINITY;
+            s[3] = v1 ? s[3] : -INFINITY;
+        }
+        // every lane looks at its own scores; the column's maximum is only found where one rises
+        float mx0 = fmaxf(s[0], s[2]), mx1 = fmaxf(s[1], s[3]);
+        if (__any_sync(kFull, mx0 > m0 + kLazyLog2 || mx1 > m1 + kLazyLog2)) {
+#pragma unroll
+            for (int k = 4; k < 32; k <<= 1) {
+                mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, k));
+                mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, k));
+            }
+            const bool need0 = mx0 > m0 + kLazyLog2, need1 = mx1 > m1 + kLazyLog2;
+            const float a0 = need0 ? exp2f(m0 - mx0) : 1.f;      // 0 while m0 is -inf
+            const float a1 = need1 ? exp2f(m1 - mx1) : 1.f;
+            m0 = need0 ? mx0 : m0;
+            m1 = need1 ? mx1 : m1;
+            l0 *= a0;
+            l1 *= a1;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                o[i][0] *= a0;
+                o[i][1] *= a1;
+                o[i][2] *= a0;
+                o[i][3] *= a1;
+            }
+        }
+        const float w0 = ex2_fast(s[0] - m0), w1 = ex2_fast(s[1] - m1);
+        const float w2 = ex2_fast(s[2] - m0), w3 = ex2_fast(s[3] - m1);
+        l0 += w0 + w2;
+        l1 += w1 + w3;
+        // the weights enter the second product as f16, rounded once: 11 bits
+        // move an output by at most 2^-11 of the largest value it weighs, where
+        // bf16's 8 bits would be as coarse as the output's own rounding
+        const uint32_t b0 = movmatrix_trans(pack_f16x2(w0, w1));
+        const uint32_t b1 = movmatrix_trans(pack_f16x2(w2, w3));
+#pragma unroll
+        for (int c = 0; c < (D + 127) / 128; ++c) {
+            constexpr int kWords = D == 64 ? 1 : 2;
+            uint32_t w[4][kWords];                       // of tokens 2t, 2t + 1, 2t + 8, 2t + 9 (in swapped order)
+            uint32_t sc[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                lds_words<kWords>(vtile + vcode[i & 1] + 64 * c + (i & 2) * 4 * kRow, w[i]);
+                sc[i] = lds8(vtile + vscale[i & 1] + 8 * c + (i & 2) * 4 * kScales);
+            }
+            if (part) {
+                // rows that are not attended may hold any scale, NaN among them, and would reach the sum as 0 * NaN
+                const int p = t < 2 ? 2 * t : 2 * t + 1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int token = (p ^ (i & 1)) + (i & 2) * 4;
+                    sc[i] = token >= nlo && token < nvalid ? sc[i] : 0u;
+                }
+            }
+            const uint32_t sa = (sc[0] << 7) | (sc[1] << 23), sb = (sc[2] << 7) | (sc[3] << 23);
+#pragma unroll
+            for (int v = 0; v < kWords; ++v) {
+                constexpr uint32_t kLow = 0x0f0f0f0fu;
+                uint32_t ea[4], oa[4], eb[4], ob[4];
+                e2m1x8_to_f16x2x4((w[0][v] & kLow) | ((w[1][v] << 4) & ~kLow), ea);
+                e2m1x8_to_f16x2x4(((w[0][v] >> 4) & kLow) | (w[1][v] & ~kLow), oa);
+                e2m1x8_to_f16x2x4((w[2][v] & kLow) | ((w[3][v] << 4) & ~kLow), eb);
+                e2m1x8_to_f16x2x4(((w[2][v] >> 4) & kLow) | (w[3][v] & ~kLow), ob);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t x[4] = {mul_f16x2(ea[k], sa), mul_f16x2(oa[k], sa), mul_f16x2(eb[k], sb), mul_f16x2(ob[k], sb)};
+                    mma_f16_16816(o[4 * (c * kWords + v) + k], x, b0, b1);
+                }
+            }
+        }
+    }
+
+    // The state as acc[heads][D], m[heads], l[heads].
+    __device__ __forceinline__ void finish(int heads, float *acc, float *m, float *l) {
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) {
+            l0 += __shfl_xor_sync(kFull, l0, k);
+            l1 += __shfl_xor_sync(kFull, l1, k);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int h = 2 * t + e;
+            if (h >= heads) continue;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                *reinterpret_cast<float2 *>(acc + h * D + v_at(i / 4) + 2 * (i & 3)) = make_float2(o[i][e], o[i][2 + e]);
+            if (g == 0) {
+                m[h] = e ? m1 : m0;
+                l[h] = e ? l1 : l0;
+            }
+        }
+    }
+};
+
+template <int D, int NW, int STAGES>
+struct Shape {
+    static constexpr int kStage = 2 * fp4_tile_bytes(D);         // K and V
+    static constexpr int kRing = NW * STAGES * kStage;
+    static_assert(STAGES * kStage >= kHeads * D * 4, "a warp's state is merged over its ring");
+    static_assert(kRing % 16 == 0 && kStage % 16 == 0, "bulk copies");
+    static size_t smem(int part_blocks) {
+        return kRing + (size_t)((part_blocks + 1) & ~1) * sizeof(int) + NW * STAGES * 8 + 2 * NW * kHeads * sizeof(float);
+    }
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A float of another CTA of the cluster, at the same shared-memory offset as ours.
+__device__ __forceinline__ float remote_f32(const float *mine, uint32_t rank) {
+    uint32_t addr;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(mine)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// kParts > 1: the grid's clusters of kParts CTAs each work on one (sequence, KV head).
+template <int D, int NW, int STAGES, int kParts>
+__global__ void __launch_bounds__(NW * 32) pa_decode_fp4_kernel(const Fp4Args a) {
+    using S = Shape<D, NW, STAGES>;
+    constexpr uint32_t kTile = fp4_tile_bytes(D);
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // CTAs go partition by partition, so that the shorter last partitions (and
+    // the empty ones of short sequences) end the grid
+    const int axis = a.num_kv_heads * a.splits;
+    int idx = blockIdx.x, part;
+    if constexpr (kParts > 1) {
+        part = (int)cluster_rank();
+        idx /= kParts;
+    } else {
+        part = idx / (a.num_seqs * axis);
+        idx -= part * a.num_seqs * axis;
+    }
+    const int b = idx / axis;
+    idx -= b * axis;
+    const int kvh = idx / a.splits;
+    const int first_head = kvh * a.heads * a.splits + (idx - kvh * a.splits) * a.heads;
+    // What depends on the CTA's place alone is loaded together, so that a CTA waits one
+    // memory round trip before its first tile is requested: the length, the table
+    // entries of the warp's first blocks (a window moves the partition with the length;
+    // then the table follows it) and the query.  All of it is the warp's own business:
+    // no barrier before the merge.
+    const int len = a.context_lens[b];
+    const int32_t *row_table = a.block_tables + (int64_t)b * a.max_blocks;
+    const bool early = kParts == 1 && a.window == 0;     // the partition does not move with the length
+    const int ahead = part * a.part_blocks + warp + NW * lane;
+    int first_phys = early && warp + NW * lane < a.part_blocks && ahead < a.max_blocks ? row_table[ahead] : -1;
+    const bool say = threadIdx.x == 0 && part == 0 && idx == 0;
+    const int row = row_of(a, b, say);
+    if (row < 0) return;                                 // (a cluster's CTAs all leave)
+    Warp4<D> state;
+    uint4 query[Warp4<D>::kKWords];
+    state.load(a, row, first_head, lane, query);
+    Span w;
+    if constexpr (kParts > 1) even_span(a, len, part, kParts, say, w);
+    else if (!span_of(a, len, part, say, w)) return;
+
+    extern __shared__ __align__(128) uint8_t ring[];
+    int *entries = reinterpret_cast<int *>(ring + S::kRing);     // physical blocks of the partition
+    uint64_t *bars = reinterpret_cast<uint64_t *>(entries + ((a.part_blocks + 1) & ~1));
+    float *s_m = reinterpret_cast<float *>(bars + NW * STAGES);
+    float *s_l = s_m + NW * kHeads;
+    __shared__ int s_fail[NW];
+    const int count = w.nblk > warp ? (w.nblk - warp + NW - 1) / NW : 0;
+    uint64_t *my_bars = bars + warp * STAGES;
+    uint8_t *my_ring = ring + warp * STAGES * S::kStage;
+    if (lane == 0) {
+        s_fail[warp] = 0;
+#pragma unroll
+        for (int s = 0; s < STAGES; ++s) mbar_init(&my_bars[s], 1);
+        fence_mbar_init();
+    }
+    auto entry_of = [&](int phys) {
+        if ((unsigned)phys >= (unsigned)a.num_blocks) {
+            report(a.status, PA_DEV_BAD_BLOCK_ID);
+            phys = 0;
+        }
+        return phys;
+    };
+    const int32_t *table = row_table + w.blk0 + warp;
+    if (!early) first_phys = lane < count ? table[NW * lane] : -1;
+    const int first_at = lane < count ? entry_of(first_phys) : 0;
+
+    const uint64_t policy = l2_policy_evict_first();     // tiles are read once: they leave L2 first
+    auto issue_at = [&](int it, int phys) {
+        const int s = it % STAGES;
+        uint8_t *kt = my_ring + s * S::kStage;
+        const int64_t at = ((int64_t)phys * a.num_kv_heads + kvh) * kTile;
+        mbar_arrive_expect_tx(&my_bars[s], 2 * kTile);
+        bulk_load(kt, a.key_cache + at, kTile, &my_bars[s], policy);
+        bulk_load(kt + kTile, a.value_cache + at, kTile, &my_bars[s], policy);
+    };
+#pragma unroll
+    for (int it = 0; it < STAGES; ++it) {
+        const int at = __shfl_sync(kFull, first_at, it);
+        if (lane == 0 && it < count) issue_at(it, at);
+    }
+    state.init(a, query);                                // under the tiles' latency
+    for (int k = lane; k < count; k += 32) entries[warp + k * NW] = k == lane ? first_at : entry_of(table[NW * k]);
+    __syncwarp();
+    bool ok = true;
+    int it = 0;
+    for (; it < count; ++it) {
+        const int s = it % STAGES;
+        if (!__all_sync(kFull, mbar_wait_bounded(&my_bars[s], (it / STAGES) & 1))) {
+            ok = false;
+            break;
+        }
+        const int tok = (w.blk0 + warp + it * NW) * kBlockSize;
+        const uint32_t kt = smem_u32(my_ring + s * S::kStage);
+        state.block(kt, kt + kTile, max(0, w.start - tok), min(kBlockSize, w.L - tok));
+        __syncwarp();
+        if (lane == 0 && it + STAGES < count) {
+            fence_proxy_async_smem();
+            issue_at(it + STAGES, entries[warp + (it + STAGES) * NW]);
+        }
+    }
+    if (!ok) {
+        // copies in flight get a bounded chance to land before the memory is given up
+        for (int k = it; k < count && k < it + STAGES; ++k)
+            (void)mbar_wait_bounded(&my_bars[k % STAGES], (k / STAGES) & 1);
+        if (lane == 0) {
+            report(a.status, PA_DEV_TIMEOUT);
+            s_fail[warp] = 1;
+        }
+    }
+    // the ring is idle: the warps' states are merged over it
+    float *acc = reinterpret_cast<float *>(my_ring);
+    state.finish(a.heads, acc, s_m + warp * kHeads, s_l + warp * kHeads);
+    __syncthreads();
+    bool failed = false;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) failed |= s_fail[k] != 0;
+    auto merged = [&](int i, float &M, float &sum) {     // element i of the CTA's state
+        const int h = i / D;
+        float O = 0.f;
+        M = -INFINITY;
+        sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) M = fmaxf(M, s_m[k * kHeads + h]);
+#pragma unroll
+        for (int k = 0; k < NW; ++k) {
+            const float mk = s_m[k * kHeads + h];
+            const float f = mk == -INFINITY ? 0.f : exp2f(mk - M);
+            sum = fmaf(f, s_l[k * kHeads + h], sum);
+            O = fmaf(f, reinterpret_cast<const float *>(ring + k * STAGES * S::kStage)[i], O);
+        }
+        // after a wait that gave up the row is NaN, through its partial sums too: what an earlier
+        // call left in the workspace must not pass for an output
+        if (failed) sum = __int_as_float(0x7fffffff);
+        return O;
+    };
+    const int64_t head0 = (int64_t)b * a.num_q_heads + first_head;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + ((int64_t)row * a.num_q_heads + first_head) * D;
+    if constexpr (kParts > 1) {
+        // The parts' states side by side in the cluster's shared memory: each CTA
+        // merges its share of the elements.  A part that gave up keeps its place at
+        // the barriers; its sum makes the row NaN.
+        constexpr int kEach = kHeads * D / (NW * 32);
+        float O[kEach], M[kEach], sum[kEach];
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int i = threadIdx.x + e * NW * 32;
+            if (i < a.heads * D) O[e] = merged(i, M[e], sum[e]);
+        }
+        __syncthreads();                                 // the warps' states are read
+        float *state_o = reinterpret_cast<float *>(ring), *state_m = s_m, *state_l = s_l;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int i = threadIdx.x + e * NW * 32;
+            if (i >= a.heads * D) continue;
+            state_o[i] = O[e];
+            if (i % D == 0) {
+                state_m[i / D] = M[e];
+                state_l[i / D] = sum[e];
+            }
+        }
+        cluster_sync();
+        for (int i = (int)threadIdx.x + part * NW * 32; i < a.heads * D; i += kParts * NW * 32) {
+            const int h = i / D;
+            float pm[kParts], pl[kParts], po[kParts], top = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < kParts; ++r) {
+                pm[r] = remote_f32(state_m + h, r);
+                pl[r] = remote_f32(state_l + h, r);
+                po[r] = remote_f32(state_o + i, r);
+            }
+#pragma unroll
+            for (int r = 0; r < kParts; ++r) top = fmaxf(top, pm[r]);
+            float o = 0.f, l = 0.f;
+#pragma unroll
+            for (int r = 0; r < kParts; ++r) {
+                const float f = pm[r] == -INFINITY ? 0.f : exp2f(pm[r] - top);
+                l = fmaf(f, pl[r], l);
+                o = fmaf(f, po[r], o);
+            }
+            out[i] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
+        }
+        cluster_sync();                                  // no CTA leaves while its state is read
+    } else {
+        const bool whole = w.nparts == 1;
+        for (int i = threadIdx.x; i < a.heads * D; i += NW * 32) {
+            float M, sum;
+            const float O = merged(i, M, sum);
+            if (whole) {
+                // a NaN sum stays NaN; an empty context gives zeros
+                out[i] = __float2bfloat16_rn(sum == 0.f ? 0.f : O / sum);
+            } else {
+                const int64_t at = (head0 + i / D) * a.max_parts + part;
+                a.part_o[at * D + i % D] = O;
+                if (i % D == 0) a.part_ml[at] = make_float2(M, sum);
+            }
+        }
+    }
+}
+
+// Merges the partitions of a (sequence, query head) row, one CTA a row: warp w
+// takes partials w, w + kMergeWarps, ..., a lane four of 128 columns, four partials on
+// their way at a time; the warps' sums meet in shared memory.
+constexpr int kMergeWarps = 4;
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) pa_merge_fp4_kernel(const Fp4Args a) {
+    constexpr int kVec = D / 4, kPer = (kVec + 31) / 32;         // 16-byte pieces of a row, and of a lane
+    __shared__ float4 s_acc[kMergeWarps][kVec];
+    __shared__ float s_sum[kMergeWarps], s_max[kMergeWarps];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = blockIdx.x;
+    Span w;
+    const int b = (int)(row / a.num_q_heads), out_row = row_of(a, b, false);
+    span_of(a, a.context_lens[b], 0, false, w);
+    if (w.nparts <= 1 || out_row < 0) return;
+    const float2 *ml = a.part_ml + row * a.max_parts;
+    const float4 *po = reinterpret_cast<const float4 *>(a.part_o + row * a.max_parts * D);
+    float M = -INFINITY, sum = 0.f;
+    float4 acc[kPer];
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = warp; p0 < w.nparts; p0 += 4 * kMergeWarps) {
+        float4 v[4][kPer];
+        float2 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = p0 + i * kMergeWarps;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c)
+                v[i][c] = p < w.nparts && lane + 32 * c < kVec ? po[(int64_t)p * kVec + lane + 32 * c] : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[i] = p < w.nparts ? ml[p] : make_float2(-INFINITY, 0.f);
+        }
+        float top = M;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, x[i].x);
+        const float g = M == -INFINITY ? 0.f : exp2f(M - top);
+        M = top;
+        sum *= g;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) acc[c] = make_float4(acc[c].x * g, acc[c].y * g, acc[c].z * g, acc[c].w * g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float f = x[i].x == -INFINITY ? 0.f : exp2f(x[i].x - M);
+            sum = fmaf(f, x[i].y, sum);
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) {
+                acc[c].x = fmaf(f, v[i][c].x, acc[c].x);
+                acc[c].y = fmaf(f, v[i][c].y, acc[c].y);
+                acc[c].z = fmaf(f, v[i][c].z, acc[c].z);
+                acc[c].w = fmaf(f, v[i][c].w, acc[c].w);
+            }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < kPer; ++c)
+        if (lane + 32 * c < kVec) s_acc[warp][lane + 32 * c] = acc[c];
+    if (lane == 0) {
+        s_sum[warp] = sum;
+        s_max[warp] = M;
+    }
+    __syncthreads();
+    if ((int)threadIdx.x >= kVec) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kMergeWarps; ++k) top = fmaxf(top, s_max[k]);
+    sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kMergeWarps; ++k) {
+        const float f = s_max[k] == -INFINITY ? 0.f : exp2f(s_max[k] - top);
+        const float4 v = s_acc[k][threadIdx.x];
+        sum = fmaf(f, s_sum[k], sum);
+        o.x = fmaf(f, v.x, o.x);
+        o.y = fmaf(f, v.y, o.y);
+        o.z = fmaf(f, v.z, o.z);
+        o.w = fmaf(f, v.w, o.w);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t out_head = (int64_t)out_row * a.num_q_heads + (row - (int64_t)b * a.num_q_heads);
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + out_head * D + 4 * threadIdx.x) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+// Query heads of one CTA: the group, or its largest divisor up to 8.
+int heads_per_cta(int group) {
+    int h = std::min(group, kHeads);
+    while (group % h != 0) --h;
+    return h;
+}
+
+struct Plan {
+    int part_blocks, max_parts;
+    int cluster;                 // CTAs of a cluster; > 1: max_parts is 1
+    bool narrow;                 // CTAs of one warp
+};
+
+bool plan_of(int num_seqs, int axis, int max_blocks, int window, int partition_size, Plan *p) {
+    if (partition_size != 0 && (partition_size < kBlockSize || partition_size > kMaxPartition || partition_size % kBlockSize))
+        return false;
+    int span = max_blocks;
+    if (window > 0) span = std::min(span, (window - 1) / kBlockSize + 2);
+    p->cluster = 1;
+    p->narrow = false;
+    const int64_t ctas = std::max<int64_t>(1, (int64_t)num_seqs * axis), target = 4LL * device_sms();
+    if (partition_size != 0) {
+        p->part_blocks = partition_size / kBlockSize;
+    } else {
+        const int most = ctas >= target ? 256 : 128;
+        int64_t parts = std::max<int64_t>((target - ctas / 8 + ctas - 1) / ctas, (span + most - 1) / most);
+        parts = std::max<int64_t>(1, std::min<int64_t>(parts, 4 * ctas > target ? span / 40 : (span + 7) / 8));
+        const int cluster = parts <= 2 ? 2 : parts <= 4 ? 4 : 8;
+        if (parts > 1 && parts <= 8 && ctas * cluster <= target) {
+            p->cluster = cluster;
+            p->max_parts = 1;
+            p->part_blocks = (span + p->cluster - 1) / p->cluster + 1;
+            return true;
+        }
+        const int largest = kMaxPartition / kBlockSize;
+        parts = std::min(parts, std::max<int64_t>(std::max<int64_t>((target + ctas - 1) / ctas, 8 * target / ctas),
+                                                  (span + largest - 1) / largest));
+        p->part_blocks = std::max(1, (int)((span + parts - 1) / parts));
+    }
+    p->max_parts = std::max(1, (span + p->part_blocks - 1) / p->part_blocks);
+    const int64_t all = ctas * p->max_parts;
+    p->narrow = p->part_blocks <= (all > 10LL * device_sms() ? 24 : all > 5LL * device_sms() ? 16 : 0);
+    return true;
+}
+
+bool head_dim_ok(int head_dim) { return head_dim == 64 || head_dim == 128 || head_dim == 256; }
+
+size_t rows_bytes(int64_t rows, int head_dim) { return ((size_t)rows * head_dim * sizeof(float) + 255) & ~size_t(255); }
+
+size_t workspace_of(int num_seqs, int num_q_heads, int head_dim, int max_parts) {
+    if (max_parts <= 1) return 0;
+    const int64_t rows = (int64_t)num_seqs * num_q_heads * max_parts;
+    return rows_bytes(rows, head_dim) + (size_t)rows * sizeof(float2);
+}
+
+template <int D, int NW, int STAGES, int kParts>
+pa_status launch_decode(const Fp4Args &a, cudaStream_t st) {
+    using S = Shape<D, NW, STAGES>;
+    auto kernel = pa_decode_fp4_kernel<D, NW, STAGES, kParts>;
+    cudaError_t e = allow_smem(kernel, S::smem(kMaxPartition / kBlockSize));
+    if (e != cudaSuccess) return cuda_failure(e, "cudaFuncSetAttribute(4-bit decode)");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((int64_t)a.num_seqs * a.num_kv_heads * a.splits * a.max_parts * kParts));
+    cfg.blockDim = dim3(NW * 32);
+    cfg.dynamicSmemBytes = S::smem(a.part_blocks);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kParts;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kParts > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, a);
+    if (e != cudaSuccess) return cuda_failure(e, "pa_decode_fp4_kernel launch");
+    count_launches(1);
+    return PA_OK;
+}
+
+template <int D>
+pa_status launch_all(const Fp4Args &a, const Plan &p, cudaStream_t st) {
+    const auto launch = p.cluster == 1   ? p.narrow ? launch_decode<D, 1, 4, 1> : launch_decode<D, 4, 4, 1>
+                        : p.cluster == 2 ? launch_decode<D, 4, 4, 2>
+                        : p.cluster == 4 ? launch_decode<D, 4, 4, 4>
+                                         : launch_decode<D, 4, 4, 8>;
+    const pa_status s = launch(a, st);
+    if (s != PA_OK || p.max_parts <= 1) return s;
+    const cudaError_t e = launch_chained(pa_merge_fp4_kernel<D>, dim3((unsigned)(a.num_seqs * a.num_q_heads)),
+                                         dim3(32 * kMergeWarps), 0, st, a);
+    if (e != cudaSuccess) return cuda_failure(e, "pa_merge_fp4_kernel launch");
+    count_launches(1);
+    return PA_OK;
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" size_t pa_decode_fp4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                                int max_blocks_per_seq, int block_size, int window, int partition_size) {
+    if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 || !head_dim_ok(head_dim) ||
+        max_blocks_per_seq < 0 || max_blocks_per_seq > 0x7fffffff / kBlockSize || block_size != kBlockSize || window < 0)
+        return (size_t)-1;
+    const int group = num_q_heads / num_kv_heads;
+    Plan p;
+    if (!plan_of(num_seqs, num_kv_heads * (group / heads_per_cta(group)), max_blocks_per_seq, window, partition_size, &p))
+        return (size_t)-1;
+    return workspace_of(num_seqs, num_q_heads, head_dim, p.max_parts);
+}
+
+extern "C" pa_status pa_decode_fp4(void *out, const void *query, const void *key_cache, const void *value_cache,
+                                   const int32_t *block_tables, const int32_t *context_lens, const int32_t *query_start,
+                                   int num_seqs, int num_query_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                   int block_size, int max_blocks_per_seq, int num_blocks, float scale, int window,
+                                   int partition_size, void *workspace, size_t workspace_bytes, int32_t *device_status,
+                                   void *stream) {
+    if (num_seqs < 0 || num_query_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
+        block_size != kBlockSize || max_blocks_per_seq < 0 || max_blocks_per_seq > 0x7fffffff / kBlockSize ||
+        num_blocks <= 0 || window < 0 || !(scale == scale) || (query_start == nullptr && num_query_tokens != num_seqs))
+        return PA_ERR_INVALID_ARG;
+    const int group = num_q_heads / num_kv_heads, heads = heads_per_cta(group), splits = group / heads;
+    Plan p;
+    if (!plan_of(num_seqs, num_kv_heads * splits, max_blocks_per_seq, window, partition_size, &p))
+        return PA_ERR_INVALID_ARG;
+    if (!head_dim_ok(head_dim)) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || num_query_tokens == 0) return PA_OK;
+    if (!out || !query || !key_cache || !value_cache || !context_lens || (!block_tables && max_blocks_per_seq > 0))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(query) || !aligned16(key_cache) || !aligned16(value_cache) ||
+        ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens) |
+          reinterpret_cast<uintptr_t>(query_start)) & 3u))
+        return PA_ERR_INVALID_ARG;
+    if ((int64_t)num_seqs * num_q_heads * p.max_parts * p.cluster >= ((int64_t)1 << 31)) return PA_ERR_UNSUPPORTED;
+    const size_t need = workspace_of(num_seqs, num_q_heads, head_dim, p.max_parts);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace))) return PA_ERR_WORKSPACE;
+    Fp4Args a = {};
+    a.out = out;
+    a.query = query;
+    a.key_cache = static_cast<const uint8_t *>(key_cache);
+    a.value_cache = static_cast<const uint8_t *>(value_cache);
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.query_start = query_start;
+    if (need > 0) {
+        a.part_o = static_cast<float *>(workspace);
+        a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) +
+                                               rows_bytes((int64_t)num_seqs * num_q_heads * p.max_parts, head_dim));
+    }
+    a.status = device_status;
+    a.num_seqs = num_seqs;
+    a.num_rows = num_query_tokens;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.heads = heads;
+    a.splits = splits;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.part_blocks = p.part_blocks;
+    a.max_parts = p.max_parts;
+    a.window = window;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return head_dim == 64 ? launch_all<64>(a, p, st) : head_dim == 128 ? launch_all<128>(a, p, st) : launch_all<256>(a, p, st);
+}

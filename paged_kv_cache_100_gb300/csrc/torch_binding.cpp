@@ -15,6 +15,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <memory>
 #include <optional>
@@ -30,6 +31,12 @@ decltype(&pa_decode_block_fp8_rows) f_decode;
 decltype(&pa_decode_block_fp8_workspace_bytes) f_decode_bytes;
 decltype(&pa_prefill_block_fp8) f_prefill;
 decltype(&pa_prefill_block_fp8_workspace_bytes) f_prefill_bytes;
+decltype(&pa_rope_cache_write_fp4) f_rope4;
+decltype(&pa_cache_read_fp4) f_read4;
+decltype(&pa_decode_fp4) f_decode4;
+decltype(&pa_decode_fp4_workspace_bytes) f_decode4_bytes;
+decltype(&pa_prefill_fp4) f_prefill4;
+decltype(&pa_prefill_fp4_workspace_bytes) f_prefill4_bytes;
 
 constexpr int64_t kBlock = 16;
 
@@ -137,9 +144,9 @@ pa_status call(F f, A... args) {
 }
 
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 6, [&]() -> PyObject * {
-        void *p[6];
-        for (int i = 0; i < 6; ++i) {
+    return guarded(n, 12, [&]() -> PyObject * {
+        void *p[12];
+        for (int i = 0; i < 12; ++i) {
             p[i] = PyLong_AsVoidPtr(a[i]);
             if (p[i] == nullptr) bad_value("missing function");
         }
@@ -149,6 +156,12 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
         f_decode_bytes = reinterpret_cast<decltype(f_decode_bytes)>(p[3]);
         f_prefill = reinterpret_cast<decltype(f_prefill)>(p[4]);
         f_prefill_bytes = reinterpret_cast<decltype(f_prefill_bytes)>(p[5]);
+        f_rope4 = reinterpret_cast<decltype(f_rope4)>(p[6]);
+        f_read4 = reinterpret_cast<decltype(f_read4)>(p[7]);
+        f_decode4 = reinterpret_cast<decltype(f_decode4)>(p[8]);
+        f_decode4_bytes = reinterpret_cast<decltype(f_decode4_bytes)>(p[9]);
+        f_prefill4 = reinterpret_cast<decltype(f_prefill4)>(p[10]);
+        f_prefill4_bytes = reinterpret_cast<decltype(f_prefill4_bytes)>(p[11]);
         Py_RETURN_NONE;
     });
 }
@@ -314,6 +327,133 @@ PyObject *rope_cache_write(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// Sizes of pools held in 4 bits, uint8 [num_blocks][num_kv_heads][16][9 head_dim / 16].
+struct Pools4 {
+    int64_t num_blocks, hkv, head_dim;
+};
+Pools4 pools4_of(const at::Tensor &kc, const at::Tensor &vc) {
+    if (kc.scalar_type() != at::kByte || vc.scalar_type() != at::kByte) bad_type("4-bit pools must be uint8");
+    if (kc.dim() != 4 || kc.size(2) != kBlock || kc.size(3) % 9 != 0 || kc.size(3) == 0 || vc.sizes() != kc.sizes())
+        bad_value("4-bit pools must be [num_blocks][num_kv_heads][16][9 * head_dim / 16]");
+    return {kc.size(0), kc.size(1), kc.size(3) / 9 * 16};
+}
+
+// rope_cache_write_fp4(query or None, key, value, positions or None, turns or None, factor, rotary_dim,
+//                      interleaved, key_cache, value_cache, slot_mapping, query_out or None, status, stream)
+//                      -> query_out
+PyObject *rope_cache_write_fp4(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 14, [&]() -> PyObject * {
+        const at::Tensor *query = optional_tensor(a[0], "query"), *positions = optional_tensor(a[3], "positions"),
+                         *turns = optional_tensor(a[4], "turns"), *given = optional_tensor(a[11], "query_out"),
+                         *status = optional_tensor(a[12], "status");
+        const at::Tensor &key = tensor(a[1], "key"), &value = tensor(a[2], "value"), &kc = tensor(a[8], "key_cache"),
+                         &vc = tensor(a[9], "value_cache"), &slots = tensor(a[10], "slot_mapping");
+        const double factor = number(a[5]);
+        const int64_t rot = integer(a[6]);
+        const int interleaved = (int)integer(a[7]);
+        const Pools4 pools = pools4_of(kc, vc);
+        if (slots.dim() != 1) bad_value("slot_mapping must be [num_tokens]");
+        const int64_t Hkv = pools.hkv, D = pools.head_dim, T = slots.size(0);
+        const at::ScalarType type = key.scalar_type();
+        if (type != at::kFloat && type != at::kBFloat16) bad_type("rows must be float32 or bfloat16");
+        const Rows k = rows_of(key, "key", {T, Hkv, D}, type), v = rows_of(value, "value", {T, Hkv, D}, type);
+        if (rot > 0) {
+            if (!positions || positions->sizes() != at::IntArrayRef{T}) bad_value("positions must be [num_tokens]");
+            if (!turns || turns->numel() * 2 != rot) bad_value("rope: turns must be [rotary_dim / 2]");
+        }
+        int64_t Hq = 0;
+        if (query) {
+            if (query->dim() != 3) bad_value("query must be [num_tokens][num_q_heads][head_dim]");
+            Hq = query->size(1);
+        }
+        const int dev = device_of(kc, "key_cache");
+        on_device(key, "key", dev);
+        on_device(value, "value", dev);
+        void *p_kc = address(kc, "key_cache", dev), *p_vc = address(vc, "value_cache", dev);
+        const int64_t *p_slots = address<int64_t>(slots, "slot_mapping", dev, at::kLong);
+        const int32_t *p_pos = rot > 0 ? address<int32_t>(*positions, "positions", dev, at::kInt) : nullptr;
+        const uint64_t *p_turns =
+            rot > 0 ? reinterpret_cast<const uint64_t *>(address<int64_t>(*turns, "turns", dev, at::kLong)) : nullptr;
+        int32_t *p_status = status_of(status, dev);
+        Place place(dev, a[13]);
+        Rows q{nullptr, 0}, o{nullptr, 0};
+        at::Tensor out;
+        if (query) {
+            on_device(*query, "query", dev);
+            q = rows_of(*query, "query", {T, Hq, D}, type);
+            out = given ? *given : at::empty({T, Hq, D}, query->options());
+            on_device(out, "query_out", dev);
+            o = rows_of(out, "query_out", {T, Hq, D}, type);
+        }
+        const pa_status rc =
+            call(f_rope4, o.at, (const void *)q.at, (const void *)k.at, (const void *)v.at, p_pos, p_turns, factor,
+                 int_of(rot, "rotary_dim"), interleaved, p_kc, p_vc, p_slots, int_of(T, "num_tokens"),
+                 int_of(Hq, "num_q_heads"), int_of(Hkv, "num_kv_heads"), int_of(D, "head_dim"), o.stride, q.stride, k.stride,
+                 v.stride, (int)kBlock, int_of(pools.num_blocks, "num_blocks"),
+                 type == at::kFloat ? PA_DTYPE_F32 : PA_DTYPE_BF16, p_status, (void *)place.at);
+        if (rc != PA_OK) return PyLong_FromLong(rc);
+        if (!query) Py_RETURN_NONE;
+        return THPVariable_Wrap(out);
+    });
+}
+
+// Blocks of a sequence that cache_read_fp4 and prefill_fp4 read, and max_context_len (0: None).
+int64_t width_of(int64_t max_blocks, int longest) {
+    return longest == 0 ? max_blocks : std::min(max_blocks, ((int64_t)longest + kBlock - 1) / kBlock);
+}
+int longest_of(PyObject *given) {
+    if (given == Py_None) return 0;
+    const int v = int_of(integer(given), "max_context_len");
+    if (v < 1) bad_value("max_context_len must be positive");
+    return v;
+}
+
+// cache_read_fp4(key_cache, value_cache, block_tables, context_lens, f32, max_context_len or None, window,
+//                key_out, value_out, status, stream) -> (key_out, value_out)
+PyObject *cache_read_fp4(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 11, [&]() -> PyObject * {
+        const at::Tensor &kc = tensor(a[0], "key_cache"), &vc = tensor(a[1], "value_cache"),
+                         &tables = tensor(a[2], "block_tables"), &lens = tensor(a[3], "context_lens");
+        const at::Tensor *status = optional_tensor(a[9], "status");
+        const Pools4 pools = pools4_of(kc, vc);
+        if (lens.dim() != 1) bad_value("context_lens must be [num_seqs]");
+        if (tables.dim() != 2 || tables.size(0) != lens.size(0)) bad_value("block_tables must be [num_seqs][max_blocks]");
+        const int longest = longest_of(a[5]), window = int_of(integer(a[6]), "window");
+        const at::ScalarType type = integer(a[4]) ? at::kFloat : at::kBFloat16;
+        const int64_t B = lens.size(0), W = width_of(tables.size(1), longest);
+        const int dev = device_of(kc, "key_cache");
+        void *p_kc = address(kc, "key_cache", dev), *p_vc = address(vc, "value_cache", dev);
+        const int32_t *p_tables = address<int32_t>(tables, "block_tables", dev, at::kInt),
+                      *p_lens = address<int32_t>(lens, "context_lens", dev, at::kInt);
+        int32_t *p_status = status_of(status, dev);
+        Place place(dev, a[10]);
+        at::Tensor out[2];
+        static const char *names[2] = {"key_out", "value_out"};
+        for (int i = 0; i < 2; ++i) {
+            PyObject *given = a[7 + i];
+            if (given == Py_None) {
+                out[i] = at::empty({B * W, pools.hkv, kBlock, pools.head_dim}, kc.options().dtype(type));
+                continue;
+            }
+            out[i] = tensor(given, names[i]);
+            const at::IntArrayRef s = out[i].sizes();
+            if (s.size() != 4 || s[0] != B * W || s[1] != pools.hkv || s[2] != kBlock || s[3] != pools.head_dim)
+                bad_value(std::string(names[i]) + " must be [num_seqs * blocks][num_kv_heads][16][head_dim]");
+            address<void>(out[i], names[i], dev, type);
+        }
+        const pa_status rc =
+            call(f_read4, out[0].data_ptr(), out[1].data_ptr(), (const void *)p_kc, (const void *)p_vc, p_tables, p_lens,
+                 int_of(B, "num_seqs"), int_of(pools.hkv, "num_kv_heads"), int_of(pools.head_dim, "head_dim"), (int)kBlock,
+                 int_of(tables.size(1), "max_blocks"), int_of(pools.num_blocks, "num_blocks"), longest, window,
+                 type == at::kFloat ? PA_DTYPE_F32 : PA_DTYPE_BF16, p_status, (void *)place.at);
+        if (rc != PA_OK) return PyLong_FromLong(rc);
+        PyObject *t = PyTuple_New(2);
+        if (t == nullptr) throw PyFailed{};
+        for (int i = 0; i < 2; ++i) PyTuple_SET_ITEM(t, i, THPVariable_Wrap(out[i]));
+        return t;
+    });
+}
+
 // What decode and prefill check of their pools.
 struct Pools {
     int dev, num_blocks, hq, hkv, head_dim, num_seqs, max_blocks;
@@ -430,12 +570,94 @@ PyObject *prefill_block_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// What decode and prefill check of pools held in 4 bits.
+Pools pools4_of(const at::Tensor &q, const at::Tensor &kc, const at::Tensor &vc, const at::Tensor &tables, const at::Tensor &lens,
+                PyObject *status) {
+    const Pools4 s = pools4_of(kc, vc);
+    if (q.dim() != 3 || q.size(2) != s.head_dim) bad_value("query must be [rows][num_q_heads][head_dim] with the pools' head_dim");
+    if (q.scalar_type() != at::kBFloat16) bad_type("a bfloat16 query is expected");
+    if (lens.dim() != 1) bad_value("context_lens must be [num_seqs]");
+    if (tables.dim() != 2 || tables.size(0) != lens.size(0)) bad_value("block_tables must be [num_seqs][max_blocks]");
+    Pools p{};
+    p.dev = device_of(q, "query");
+    p.num_blocks = int_of(s.num_blocks, "num_blocks");
+    p.hq = int_of(q.size(1), "num_q_heads");
+    p.hkv = int_of(s.hkv, "num_kv_heads");
+    p.head_dim = int_of(s.head_dim, "head_dim");
+    p.num_seqs = int_of(lens.size(0), "num_seqs");
+    p.max_blocks = int_of(tables.size(1), "max_blocks");
+    p.query = address(q, "query", p.dev);
+    p.kc = address(kc, "key_cache", p.dev);
+    p.vc = address(vc, "value_cache", p.dev);
+    p.tables = address<int32_t>(tables, "block_tables", p.dev, at::kInt);
+    p.lens = address<int32_t>(lens, "context_lens", p.dev, at::kInt);
+    p.status = status_of(optional_tensor(status, "status"), p.dev);
+    return p;
+}
+
+// decode_fp4(query, key_cache, value_cache, block_tables, context_lens, scale or None, query_start or None, window,
+//            out, partition_size, workspace, status, stream) -> out
+PyObject *decode_fp4(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 13, [&]() -> PyObject * {
+        const int window = int_of(integer(a[7]), "window"), partition = int_of(integer(a[9]), "partition_size");
+        const at::Tensor &q = tensor(a[0], "query"), &lens = tensor(a[4], "context_lens");
+        const at::Tensor *start = optional_tensor(a[6], "query_start");
+        if (!start && q.dim() == 3 && lens.sizes() != at::IntArrayRef{q.size(0)}) bad_value("context_lens must be [num_seqs]");
+        if (start && (lens.dim() != 1 || start->sizes() != at::IntArrayRef{lens.size(0) + 1}))
+            bad_value("query_start must be [num_seqs + 1]");
+        Pools p = pools4_of(q, tensor(a[1], "key_cache"), tensor(a[2], "value_cache"), tensor(a[3], "block_tables"), lens, a[11]);
+        const int32_t *p_start = start ? address<int32_t>(*start, "query_start", p.dev, at::kInt) : nullptr;
+        const float scale = a[5] == Py_None ? (float)(1.0 / std::sqrt((double)p.head_dim)) : (float)number(a[5]);
+        Place place(p.dev, a[12]);
+        at::Tensor out = output_of(a[8], q, p.dev);
+        const size_t need = a[10] != Py_None ? 0
+                                             : f_decode4_bytes(p.num_seqs, p.hq, p.hkv, p.head_dim, p.max_blocks,
+                                                               (int)kBlock, window, partition);
+        at::Tensor w = workspace_of(a[10], need, q, p);
+        const pa_status rc = call(f_decode4, out.data_ptr(), (const void *)p.query, (const void *)p.kc, (const void *)p.vc,
+                                  p.tables, p.lens, p_start, p.num_seqs, int_of(q.size(0), "query"), p.hq, p.hkv, p.head_dim,
+                                  (int)kBlock, p.max_blocks, p.num_blocks, scale, window, partition, p.workspace,
+                                  p.workspace_bytes, p.status, (void *)place.at);
+        if (rc != PA_OK) return PyLong_FromLong(rc);
+        return THPVariable_Wrap(out);
+    });
+}
+
+// prefill_fp4(query, key_cache, value_cache, block_tables, context_lens, query_start, max_query_len, scale or None,
+//             max_context_len or None, window, out, workspace, status, stream) -> out
+PyObject *prefill_fp4(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 14, [&]() -> PyObject * {
+        const int longest_chunk = int_of(integer(a[6]), "max_query_len"), longest = longest_of(a[8]),
+                  window = int_of(integer(a[9]), "window");
+        const at::Tensor &q = tensor(a[0], "query"), &lens = tensor(a[4], "context_lens"), &start = tensor(a[5], "query_start");
+        if (lens.dim() != 1 || start.sizes() != at::IntArrayRef{lens.size(0) + 1}) bad_value("query_start must be [num_seqs + 1]");
+        Pools p = pools4_of(q, tensor(a[1], "key_cache"), tensor(a[2], "value_cache"), tensor(a[3], "block_tables"), lens, a[12]);
+        const int32_t *p_start = address<int32_t>(start, "query_start", p.dev, at::kInt);
+        const float scale = a[7] == Py_None ? (float)(1.0 / std::sqrt((double)p.head_dim)) : (float)number(a[7]);
+        Place place(p.dev, a[13]);
+        at::Tensor out = output_of(a[10], q, p.dev);
+        const size_t need =
+            a[11] != Py_None ? 0 : f_prefill4_bytes(p.num_seqs, p.hkv, p.head_dim, p.max_blocks, longest);
+        at::Tensor w = workspace_of(a[11], need, q, p);
+        const pa_status rc = call(f_prefill4, out.data_ptr(), (const void *)p.query, (const void *)p.kc, (const void *)p.vc,
+                                  p.tables, p.lens, p_start, p.num_seqs, p.hq, p.hkv, p.head_dim, (int)kBlock, p.max_blocks,
+                                  p.num_blocks, int_of(q.size(0), "query"), longest_chunk, longest, scale, window, p.workspace,
+                                  p.workspace_bytes, p.status, (void *)place.at);
+        if (rc != PA_OK) return PyLong_FromLong(rc);
+        return THPVariable_Wrap(out);
+    });
+}
+
 PyMethodDef methods[] = {
     {"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, nullptr},
     {"plan_step", (PyCFunction)(void (*)(void))plan_step, METH_FASTCALL, nullptr},
     {"rope_cache_write", (PyCFunction)(void (*)(void))rope_cache_write, METH_FASTCALL, nullptr},
     {"decode_block_fp8", (PyCFunction)(void (*)(void))decode_block_fp8, METH_FASTCALL, nullptr},
     {"prefill_block_fp8", (PyCFunction)(void (*)(void))prefill_block_fp8, METH_FASTCALL, nullptr},
+    {"rope_cache_write_fp4", (PyCFunction)(void (*)(void))rope_cache_write_fp4, METH_FASTCALL, nullptr},
+    {"cache_read_fp4", (PyCFunction)(void (*)(void))cache_read_fp4, METH_FASTCALL, nullptr},
+    {"decode_fp4", (PyCFunction)(void (*)(void))decode_fp4, METH_FASTCALL, nullptr},
+    {"prefill_fp4", (PyCFunction)(void (*)(void))prefill_fp4, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pagedkv_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

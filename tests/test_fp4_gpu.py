@@ -1,0 +1,473 @@
+"""Pools held in 4 bits: pa_rope_cache_write_fp4, pa_cache_read_fp4, pa_decode_fp4 and
+pa_prefill_fp4 against 64-bit implementations; codes, scales and values read back bit for bit."""
+import numpy as np
+import pytest
+import torch
+
+from tests import block8_ref as R
+from tests import fp4_ref as F
+
+pytestmark = pytest.mark.gpu
+
+# cos and sin: the angle is held to 2^-24 of at most half a turn (pi 2^-24 < 2^-22 radians), sincospi
+# to 2 units of 2^-23; two products and a sum of f32 round 3 times 2^-24.  Per |x0| + |x1|:
+TURN = 2.0 ** -22 + 2.0 ** -22 + 3 * 2.0 ** -24
+HALF_STEP = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+
+
+@pytest.fixture(scope="module")
+def pkv():
+    from paged_kv_cache_100_gb300.build import build
+    build()
+    import paged_kv_cache_100_gb300 as m
+    return m
+
+
+def _status():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def _angles(rope, pos):
+    """cos and sin (64 bits) of the plan's own fractions of a turn, exact at any position."""
+    turns = [int(t) % (1 << 64) for t in rope.turns.cpu().tolist()]
+    frac = np.array([[((int(p) * t) % (1 << 64)) / 2.0 ** 64 for t in turns] for p in pos]).reshape(len(pos), len(turns))
+    return rope.attention_factor * np.cos(2 * np.pi * frac), rope.attention_factor * np.sin(2 * np.pi * frac)
+
+
+def _written(pool, rows, slots):
+    """The pool after the write of rows [tokens][heads][D] (64 bits): codes and scale bytes."""
+    code, byte, _ = F.unpack(pool)
+    c, b = F.encode(rows)
+    for i, s in enumerate(slots):
+        if 0 <= s < pool.shape[0] * 16:
+            code[s // 16, :, s % 16], byte[s // 16, :, s % 16] = c[i], b[i]
+    return code, byte
+
+
+def _same(pool, want, what):
+    code, byte, _ = F.unpack(pool)
+    assert np.array_equal(byte, want[1]), (what, "scales", np.argwhere(byte != want[1])[:4].tolist())
+    assert np.array_equal(code, want[0]), (what, "codes", np.argwhere(code != want[0])[:4].tolist())
+
+
+# ---------------------------------------------------------------------------------------------
+# write
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,rot", [(128, 128), (64, 64), (128, 64), (128, 20), (64, 2), (256, 250), (96, 96), (80, 0), (16, 16),
+                                   (48, 46), (256, 256)])
+@pytest.mark.parametrize("T,Hq,Hkv", [(1, 4, 2), (37, 3, 3)])
+def test_write_matches(pkv, D, rot, dtype, interleaved, T, Hq, Hkv):
+    g = torch.Generator().manual_seed(D + rot + T)
+    blocks = 5
+    qkv = torch.randn(T, Hq + 2 * Hkv, D, generator=g) * torch.exp2(2 * torch.randn(T, Hq + 2 * Hkv, 1, generator=g))
+    qkv = qkv.to(dtype)
+    pos = torch.randint(0, 100000, (T,), generator=g, dtype=torch.int32)
+    slots = torch.randperm(blocks * 16, generator=g)[:T]
+    if T > 3:
+        slots[3] = -1
+    kc, vc = F.pool(g, blocks, Hkv, D), F.pool(g, blocks, Hkv, D)
+    rope = pkv.rotary_plan(rot, interleaved=interleaved)
+    x, kd, vd, status = qkv.cuda(), kc.cuda(), vc.cuda(), _status()
+    args = (x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], pos.cuda(), rope, kd, vd, slots.cuda())
+    out = pkv.rope_cache_write_fp4(x[:, :Hq], *args, status=status)
+    cos, sin = _angles(rope, pos.tolist())
+    ref, mass = R.rotate(qkv.double().numpy(), cos, sin, interleaved)
+    err = np.abs(out.double().cpu().numpy() - ref[:, :Hq])
+    m = mass[:, :Hq]
+    assert (err <= TURN * m + HALF_STEP[dtype] * (np.abs(ref[:, :Hq]) + TURN * m)).all()
+    _same(kd, _written(kc, ref[:, Hq:Hq + Hkv], slots.tolist()), "keys")
+    _same(vd, _written(vc, qkv[:, Hq + Hkv:].double().numpy(), slots.tolist()), "values")
+    assert int(status.item()) == 0
+    # in place on contiguous queries, and without queries
+    q = x[:, :Hq].contiguous()
+    again = pkv.rope_cache_write_fp4(q, *args, query_out=q)
+    assert again is q and torch.equal(q, out)
+    k2, v2 = kc.cuda(), vc.cuda()
+    assert pkv.rope_cache_write_fp4(None, *args[:4], k2, v2, args[6]) is None
+    assert torch.equal(k2, kd) and torch.equal(v2, vd)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_write_of_borders_and_extremes(pkv, dtype):
+    """Elements on and beside the borders of two codes and of two scales, and magnitudes of every size."""
+    D, rows = 64, []
+    rng = np.random.default_rng(5)
+    tie = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    for byte in list(range(1, 30)) + list(range(100, 140)) + [0xE0, 0xE1, 0xE2]:
+        s = F.SCALES[byte]
+        rows.append(np.concatenate([[6 * s], rng.choice(tie, 15) * s * rng.choice([-1, 1], 15)]))
+    mid = (F.SCALES[1:] + F.SCALES[:-1]) / 2 * 6                     # amax between two scales: ties to even
+    for m in mid:
+        rows.append(np.concatenate([[m], rng.uniform(-1, 1, 15) * m]))
+    for e in range(-40, 17):
+        rows.append(rng.standard_normal(16) * 2.0 ** e)
+    rows += [np.zeros(16), np.full(16, -0.0), np.full(16, 2.0 ** -133), np.full(16, 61440.0)]
+    x = np.stack(rows)
+    x = np.concatenate([x, np.zeros((-len(x) % 4, 16))]).reshape(-1, 1, D)
+    t = torch.from_numpy(x).to(dtype)
+    if dtype == torch.float32:                                       # and one step of f32 beside the borders
+        t = torch.cat([t, torch.nextafter(t, t * 2), torch.nextafter(t, t * 0)])
+    T = t.shape[0]
+    blocks = -(-T // 16)
+    kc, vc, status = pkv.fp4_pool(blocks, 1, D), pkv.fp4_pool(blocks, 1, D), _status()
+    slots = torch.arange(T).cuda()
+    pkv.rope_cache_write_fp4(None, t.cuda(), t.cuda(), None, None, kc, vc, slots, status=status)
+    want = _written(torch.zeros_like(vc).cpu(), t.double().numpy(), range(T))
+    _same(vc, want, "values")
+    _same(kc, want, "keys")                                          # not turned
+    assert int(status.item()) == (256 if (t.abs() > 61440).any() else 0)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_write_of_many_turned_keys(pkv, dtype, interleaved):
+    """Half a million turned keys, some pairs of very unlike halves: codes and scales of the exact rotation."""
+    g = torch.Generator().manual_seed(11)
+    T, H, D = 1000, 4, 128
+    k = torch.randn(T, H, D, generator=g)
+    k[:, 1, :64] *= 2.0 ** 14                                        # partners far larger than their own unit
+    k[:, 2] *= torch.exp2(4 * torch.randn(T, D, generator=g))
+    k = k.to(dtype)
+    pos = torch.randint(0, 1 << 30, (T,), generator=g, dtype=torch.int32)
+    rope = pkv.rotary_plan(D, 500000.0, interleaved=interleaved, scaling="by_parts", factor=8.0)
+    blocks = -(-T // 16)
+    kc, vc = pkv.fp4_pool(blocks, H, D), pkv.fp4_pool(blocks, H, D)
+    slots = torch.randperm(blocks * 16, generator=g)[:T]
+    pkv.rope_cache_write_fp4(None, k.cuda(), k.cuda(), pos.cuda(), rope, kc, vc, slots.cuda())
+    cos, sin = _angles(rope, pos.tolist())
+    ref, _ = R.rotate(k.double().numpy(), cos, sin, interleaved)
+    zero = torch.zeros(kc.shape, dtype=torch.uint8)
+    _same(vc, _written(zero, k.double().numpy(), slots.tolist()), "values")
+    _same(kc, _written(zero, ref, slots.tolist()), "keys")
+
+
+def test_write_of_nan_and_infinity(pkv):
+    D = 128
+    x = torch.randn(4, 2, D, generator=torch.Generator().manual_seed(3))
+    x[1, 0, 5], x[2, 1, 100], x[2, 1, 70] = float("nan"), float("inf"), -float("inf")
+    for dtype in (torch.float32, torch.bfloat16):
+        t = x.to(dtype)
+        kc, vc, status = pkv.fp4_pool(1, 2, D), pkv.fp4_pool(1, 2, D), _status()
+        pkv.rope_cache_write_fp4(None, t.cuda(), t.cuda(), None, None, kc, vc, torch.arange(4).cuda(), status=status)
+        _same(vc, _written(torch.zeros(vc.shape, dtype=torch.uint8), t.double().numpy(), range(4)), "values")
+        assert torch.equal(kc, vc) and int(status.item()) == 256
+        v = F.unpack(vc)[2][0]                                       # [heads][16][D]
+        assert np.isnan(v[0, 1, :16]).all() and not np.isnan(v[0, 1, 16:]).any()
+        assert v[1, 2, 100] == 61440 and v[1, 2, 70] == -61440
+    # turned: what a NaN reaches is NaN, the rest of the row is not
+    rope = pkv.rotary_plan(D)
+    kc, vc = pkv.fp4_pool(1, 2, D), pkv.fp4_pool(1, 2, D)
+    pkv.rope_cache_write_fp4(None, x.cuda(), x.cuda(), torch.ones(4, dtype=torch.int32).cuda(), rope, kc, vc, torch.arange(4).cuda())
+    v = F.unpack(kc)[2][0]
+    assert np.isnan(v[0, 1, :16]).all() and np.isnan(v[0, 1, 64:80]).all()
+    assert not np.isnan(v[0, 1, 16:64]).any() and not np.isnan(v[0, 0]).any() and not np.isnan(v[0, 3]).any()
+
+
+def test_write_slots(pkv):
+    """Slots past the pool are skipped and flagged, negative ones skipped; the query is turned all the same."""
+    g = torch.Generator().manual_seed(8)
+    x = torch.randn(5, 3, 64, generator=g).cuda()
+    kc, vc = F.pool(g, 2, 1, 64), F.pool(g, 2, 1, 64)
+    kd, vd, status = kc.cuda(), vc.cuda(), _status()
+    rope = pkv.rotary_plan(64)
+    pos = torch.arange(5, dtype=torch.int32).cuda()
+    out = pkv.rope_cache_write_fp4(x[:, :1], x[:, 1:2], x[:, 2:], pos, rope, kd, vd,
+                                   torch.tensor([-1, 32, 1 << 40, -(1 << 50), 1 << 62]).cuda(), status=status)
+    assert torch.equal(kd.cpu(), kc) and torch.equal(vd.cpu(), vc) and int(status.item()) == 4
+    ref, _ = R.rotate(x[:, :1].double().cpu().numpy(), *_angles(rope, range(5)), False)
+    assert np.allclose(out.double().cpu().numpy(), ref, atol=1e-5)
+    # no token at all
+    e = x[:0]
+    assert pkv.rope_cache_write_fp4(e[:, :1], e[:, 1:2], e[:, 2:], pos[:0], rope, kd, vd, torch.empty(0, dtype=torch.int64).cuda()).shape == (0, 1, 64)
+
+
+# ---------------------------------------------------------------------------------------------
+# read
+# ---------------------------------------------------------------------------------------------
+LENS = [1, 15, 16, 17, 0, 100, 513, 31]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,hkv", [(128, 3), (64, 8), (256, 1), (16, 2), (80, 5), (240, 1)])
+@pytest.mark.parametrize("window", [0, 1, 18, 16, 40])
+def test_read_matches(pkv, D, hkv, dtype, window):
+    p = F.Batch(D + hkv, LENS, hkv, D)
+    dev = p.device()
+    width = p.tables.shape[1]
+    first = [max(0, n - window) // 16 if window else 0 for n in LENS]
+    for b, f in enumerate(first):                                    # released blocks before the window
+        dev[2][b, :f] = -1
+    ko = torch.full((len(LENS) * width, hkv, 16, D), 7.0, dtype=dtype, device="cuda")
+    vo, status = ko.clone(), _status()
+    k, v = pkv.cache_read_fp4(*dev, window=window, key_out=ko, value_out=vo, status=status)
+    assert k is ko and v is vo and int(status.item()) == 0
+    for pool, out in ((p.kc, ko), (p.vc, vo)):
+        want = np.full((len(LENS), width, hkv, 16, D), 7.0)
+        val = F.unpack(pool)[2]
+        for b, n in enumerate(LENS):
+            for j in range(first[b], -(-n // 16)):
+                want[b, j] = val[p.tables[b, j]]
+                want[b, j, :, max(0, n - 16 * j):] = 0
+        assert np.array_equal(out.double().cpu().numpy().reshape(want.shape), want)
+
+
+def test_read_shapes_and_bounds(pkv):
+    p = F.Batch(4, [40, 3, 70], 2, 64)
+    dev = p.device()
+    k, v = pkv.cache_read_fp4(*dev)
+    assert k.shape == (15, 2, 16, 64) and k.dtype == v.dtype == torch.bfloat16
+    k, v = pkv.cache_read_fp4(*dev, dtype=torch.float32, max_context_len=33)
+    assert k.shape == (9, 2, 16, 64) and k.dtype == torch.float32
+    # contexts of 40 and 70 are cut to three blocks
+    status = _status()
+    ko = torch.zeros(9, 2, 16, 64, device="cuda")
+    vo = torch.zeros_like(ko)
+    pkv.cache_read_fp4(*dev, max_context_len=33, key_out=ko, value_out=vo, status=status)
+    assert int(status.item()) == 2
+    val = F.unpack(p.kc)[2]
+    assert np.array_equal(ko[6:].double().cpu().numpy(), val[p.tables[2, :3]])
+    assert pkv.cache_read_fp4(*dev, max_context_len=1000)[0].shape[0] == 15
+    # an entry out of range is read as block 0; lengths out of range are clamped
+    bad = dev[2].clone()
+    bad[0, 0], bad[2, 1] = p.blocks, -5
+    lens = torch.tensor([16, -3, 32], dtype=torch.int32, device="cuda")
+    status.zero_()
+    ko.zero_()
+    pkv.cache_read_fp4(dev[0], dev[1], bad, lens, max_context_len=48, key_out=ko, value_out=vo, status=status)
+    assert int(status.item()) == 3
+    first = F.unpack(p.kc)[2][0]
+    assert np.array_equal(ko[0].double().cpu().numpy(), first, equal_nan=True)
+    assert np.array_equal(ko[7].double().cpu().numpy(), first, equal_nan=True) and (ko[3:6] == 0).all()
+    # nothing to read
+    assert pkv.cache_read_fp4(dev[0], dev[1], dev[2][:0], dev[3][:0])[0].shape[0] == 0
+    assert pkv.cache_read_fp4(dev[0], dev[1], dev[2][:, :0].contiguous(), dev[3] * 0)[0].shape[0] == 0
+
+
+# ---------------------------------------------------------------------------------------------
+# decode
+# ---------------------------------------------------------------------------------------------
+DLENS = [1, 15, 16, 17, 0, 100, 513, 1100, 31]
+
+
+@pytest.mark.parametrize("D,hq,hkv", [(128, 8, 8), (128, 8, 4), (128, 6, 2), (128, 8, 2), (128, 5, 1), (128, 12, 2), (128, 7, 1),
+                                      (128, 16, 2), (128, 11, 1), (128, 24, 2), (128, 16, 1), (64, 8, 2), (64, 5, 1), (64, 3, 3),
+                                      (256, 4, 2), (256, 8, 1), (256, 2, 2)])
+@pytest.mark.parametrize("partition", [0, 64, 16384])
+def test_decode_matches(pkv, D, hq, hkv, partition):
+    p = F.Batch(hq * 10 + hkv + D, DLENS, hkv, D)
+    q, status = p.query(len(DLENS), hq), _status()
+    out = pkv.decode_fp4(q.cuda(), *p.device(), partition_size=partition, status=status)
+    ref, bound = p.reference(q.double().numpy(), [(b, n - 1) for b, n in enumerate(DLENS)])
+    F.check(out, ref, bound, f"{D} {hq}/{hkv} P={partition}")
+    assert (out[4] == 0).all() and int(status.item()) == 0
+
+
+@pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 100, 513, 5000])
+@pytest.mark.parametrize("D,hq,hkv,partition", [(128, 8, 8, 0), (128, 16, 2, 0), (64, 8, 2, 32), (256, 4, 1, 0)])
+def test_decode_window(pkv, window, D, hq, hkv, partition):
+    p = F.Batch(window, DLENS, hkv, D)
+    q, dev = p.query(len(DLENS), hq), p.device()
+    for b, n in enumerate(DLENS):                                    # released blocks before the window
+        dev[2][b, :max(0, n - window) // 16] = -1
+    status = _status()
+    out = pkv.decode_fp4(q.cuda(), *dev, window=window, partition_size=partition, status=status)
+    ref, bound = p.reference(q.double().numpy(), [(b, n - 1) for b, n in enumerate(DLENS)], window=window)
+    F.check(out, ref, bound, f"W={window}")
+    assert int(status.item()) == 0
+
+
+@pytest.mark.parametrize("seqs,hq,hkv,longest,width", [(1, 8, 2, 20000, None), (2, 4, 4, 3000, 2000), (40, 8, 8, 300, None),
+                                                       (200, 8, 8, 60, None), (64, 16, 2, 700, 900), (3, 32, 32, 900, None)])
+def test_decode_cuts(pkv, seqs, hq, hkv, longest, width):
+    """Clusters, parts with a merge, one-warp CTAs, tables wider than the contexts."""
+    rng = np.random.default_rng(seqs)
+    lens = rng.integers(0, longest + 1, seqs)
+    lens[0] = longest
+    p = F.Batch(seqs, lens, hkv, 128, width=width)
+    q = p.query(seqs, hq)
+    out = pkv.decode_fp4(q.cuda(), *p.device())
+    ref, bound = p.reference(q.double().numpy(), [(b, int(n) - 1) for b, n in enumerate(lens)])
+    F.check(out, ref, bound, f"{seqs}")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_decode_values_of_any_size(pkv, D):
+    """Keys and values from the smallest scales to the largest, large scores, rows of zeros."""
+    lens = [500, 500, 500, 40]
+    p = F.Batch(3, lens, 2, D, poison=False)
+    x = torch.randn(p.blocks, 2, 16, D, generator=p.g, dtype=torch.float64)
+    x *= torch.exp2(torch.randint(-18, 14, x.shape[:3], generator=p.g).double())[..., None]
+    x = x.clamp(-61440, 61440)
+    x[p.tables[3, 0]] = 0
+    p.vc = F.pack(*F.encode(x.numpy()))
+    q = p.query(4, 6)
+    q[1] *= 2.0 ** -20
+    q[2, 0] = 0
+    out = pkv.decode_fp4(q.cuda(), *p.device())
+    ref, bound = p.reference(q.double().numpy(), [(b, n - 1) for b, n in enumerate(lens)])
+    F.check(out, ref, bound)
+    # large scores: one position takes nearly all of the weight, references rise often
+    out = pkv.decode_fp4(q.cuda(), *p.device(), scale=4.0)
+    ref, bound = p.reference(q.double().numpy(), [(b, n - 1) for b, n in enumerate(lens)], scale=4.0)
+    # scores of up to 4 |q| |k| of f32 sums: 2^-22 of the sum of magnitudes moves a weight by as much
+    kv = F.unpack(p.kc)[2]
+    size = 4.0 * np.abs(q.double().numpy()).sum(-1).max() * np.abs(kv).max() * 2.0 ** -22
+    F.check(out, ref, bound + 2 * size * np.abs(F.unpack(p.vc)[2]).max())
+
+
+def test_decode_nan(pkv):
+    """A NaN that is attended reaches its row and no other; NaN and infinite scales elsewhere reach none."""
+    p = F.Batch(9, [50, 50, 50], 1, 128)
+    q = p.query(3, 4)
+    t = p.tables
+    p.scales(p.vc)[t[0, 1], 0, 3, 2] = 0xFF                          # elements 32 .. 47 of position 19
+    p.scales(p.kc)[t[1, 0], 0, 7, 0] = 0xFF
+    p.scales(p.kc)[t[2, 3], 0, 2:] = 0xF8                            # behind 50 positions: infinite
+    p.scales(p.vc)[t[2, 3], 0, 2:] = 0xF8
+    out = pkv.decode_fp4(q.cuda(), *p.device()).float().cpu()
+    assert out[0, :, 32:48].isnan().all() and not out[0, :, :32].isnan().any() and not out[0, :, 48:].isnan().any()
+    assert out[1].isnan().all() and not out[2].isnan().any()
+    # the window leaves both behind
+    out = pkv.decode_fp4(q.cuda(), *p.device(), window=30).float().cpu()
+    assert not out.isnan().any()
+
+
+def test_decode_status_and_bounds(pkv):
+    p = F.Batch(2, [40, 40, 40], 2, 128)
+    q, dev = p.query(3, 4), p.device()
+    bad = dev[2].clone()
+    bad[1, 1] = 1 << 30
+    status = _status()
+    good = pkv.decode_fp4(q.cuda(), *dev)
+    out = pkv.decode_fp4(q.cuda(), dev[0], dev[1], bad, dev[3], status=status)
+    assert int(status.item()) == 1 and torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
+    status.zero_()
+    lens = torch.tensor([40, -1, 49], dtype=torch.int32, device="cuda")
+    out = pkv.decode_fp4(q.cuda(), dev[0], dev[1], dev[2], lens, status=status)
+    assert int(status.item()) == 2 and torch.equal(out[0], good[0]) and (out[1] == 0).all()
+    status.zero_()
+    big = q.clone()
+    big[1, 2, 5] = 65536.0
+    pkv.decode_fp4(big.cuda(), *dev, status=status)
+    assert int(status.item()) == 256
+
+
+@pytest.mark.parametrize("partition", [0, 16])
+def test_decode_rows_of_a_plan(pkv, partition):
+    lens = [30, 0, 77, 200, 16]
+    p = F.Batch(6, lens, 2, 128)
+    q, dev, status = p.query(4, 6), p.device(), _status()
+    start = torch.tensor([0, 1, 1, 2, 2, 3], dtype=torch.int32, device="cuda")
+    out = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+    pkv.decode_fp4(q.cuda(), *dev, query_start=start, out=out, partition_size=partition, status=status)
+    ref, bound = p.reference(q[:3].double().numpy(), [(0, 29), (2, 76), (4, 15)])
+    F.check(out[:3], ref, bound)
+    assert (out[3] == 5).all() and int(status.item()) == 0           # a row of no sequence
+    for entries, flag in (([0, 1, 3, 3, 3, 4], 64), ([0, 1, 0, 1, 2, 9], 2), ([-1, 0, 0, 1, 1, 2], 2)):
+        status.zero_()
+        pkv.decode_fp4(q.cuda(), *dev, query_start=torch.tensor(entries, dtype=torch.int32, device="cuda"), out=out,
+                       partition_size=partition, status=status)
+        assert int(status.item()) & flag
+
+
+def test_pools_past_four_gigabytes(pkv):
+    """Blocks whose bytes begin past 2^32: written, read back and attended."""
+    hkv, D = 16, 128
+    blocks = (1 << 32) // (hkv * 9 * D) + 40
+    kc = torch.zeros(blocks, hkv, 16, 9 * D // 16, dtype=torch.uint8, device="cuda")
+    vc = torch.zeros_like(kc)
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(32, 2 * hkv, D, generator=g).to(torch.bfloat16)
+    table = torch.tensor([[blocks - 1, blocks - 30]], dtype=torch.int32)
+    slots = (table[0].long()[:, None] * 16 + torch.arange(16)).flatten()
+    pkv.rope_cache_write_fp4(None, x[:, :hkv].cuda(), x[:, hkv:].cuda(), None, None, kc, vc, slots.cuda())
+    k, v = pkv.cache_read_fp4(kc, vc, table.cuda(), torch.tensor([32], dtype=torch.int32).cuda(), dtype=torch.float32)
+    want = F.values_of(*F.encode(x.double().numpy()))
+    want = want.reshape(2, 16, 2 * hkv, D).transpose(0, 2, 1, 3)
+    assert np.array_equal(k.double().cpu().numpy(), want[:, :hkv]) and np.array_equal(v.double().cpu().numpy(), want[:, hkv:])
+    q = torch.randn(1, hkv, D, generator=g).to(torch.bfloat16)
+    out = pkv.decode_fp4(q.cuda(), kc, vc, table.cuda(), torch.tensor([32], dtype=torch.int32).cuda())
+    p = torch.softmax(torch.einsum("hd,hpd->hp", q[0].double(), torch.from_numpy(want[:, :hkv].transpose(1, 0, 2, 3).reshape(hkv, 32, D))) * D ** -0.5, -1)
+    vv = torch.from_numpy(want[:, hkv:].transpose(1, 0, 2, 3).reshape(hkv, 32, D))
+    ref = torch.einsum("hp,hpd->hd", p, vv)
+    mass = torch.einsum("hp,hpd->hd", p, vv.abs())
+    err = (out[0].double().cpu() - ref).abs()
+    assert (err <= (2.0 ** -11 + 2.0 ** -15) * 2 * mass + 2.0 ** -8 * ref.abs()).all()
+
+
+# ---------------------------------------------------------------------------------------------
+# prefill
+# ---------------------------------------------------------------------------------------------
+def _rows(lens, new):
+    return [(b, n - t + i) for b, (n, t) in enumerate(zip(lens, new)) for i in range(t)]
+
+
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (4, 2), (8, 2), (16, 2), (16, 1)])
+@pytest.mark.parametrize("window", [0, 1, 37, 300])
+def test_prefill_matches(pkv, hq, hkv, window):
+    lens, new = [1, 17, 130, 300, 64, 0, 33], [1, 17, 100, 3, 0, 0, 16]
+    p = F.Batch(hq + window, lens, hkv, 128)
+    dev = p.device()
+    q, status = p.query(sum(new) + 2, hq), _status()
+    start = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    if window:
+        for b, (n, t) in enumerate(zip(lens, new)):
+            dev[2][b, :max(0, n - t + 1 - window) // 16] = -1
+    out = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+    got = pkv.prefill_fp4(q.cuda(), *dev, start, window=window, out=out, status=status)
+    assert got is out and int(status.item()) == 0
+    n = sum(new)
+    ref, bound = p.reference(q[:n].double().numpy(), _rows(lens, new), window=window, floor=4.0)
+    F.check(out[:n], ref, bound, f"{hq}/{hkv} W={window}")
+    assert (out[n:] == 5).all()
+    # blocks of the longest context only
+    again = pkv.prefill_fp4(q.cuda(), *dev, start, 100, window=window, max_context_len=300,
+                            workspace=torch.full((pkv.prefill_fp4_workspace_bytes(7, hkv, 128, 19, 300),), 0xFF,
+                                                 dtype=torch.uint8, device="cuda"))
+    assert torch.equal(again[:n], out[:n])
+
+
+def test_prefill_refuses_rows_on_the_device(pkv):
+    """Sequences whose rows leave the query, or whose context is too long, are left out and flagged."""
+    lens, new = [40, 40, 40], [10, 10, 10]
+    p = F.Batch(1, lens, 1, 128)
+    q, dev, status = p.query(30, 4), p.device(), _status()
+    ref, bound = p.reference(q.double().numpy(), _rows(lens, new), floor=4.0)
+    # (in the last one rows 5 .. 9 are both the first's and the third's)
+    for start, ok, rows in (([0, 10, 20, 31], [0, 1], 10), ([-1, 10, 20, 30], [1, 2], 10), ([0, 10, 5, 15], [0], 5)):
+        status.zero_()
+        out = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+        pkv.prefill_fp4(q.cuda(), *dev, torch.tensor(start, dtype=torch.int32, device="cuda"), 10, out=out, status=status)
+        assert int(status.item()) & 2
+        for b in ok:
+            at = slice(10 * b, 10 * b + rows)
+            F.check(out[at], ref[at], bound[at], f"{start} {b}")
+    status.zero_()
+    out = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+    pkv.prefill_fp4(q.cuda(), *dev, torch.tensor([0, 10, 20, 30], dtype=torch.int32, device="cuda"), 10, max_context_len=30,
+                    out=out, status=status)
+    assert int(status.item()) == 2 and (out == 5).all()
+
+
+# ---------------------------------------------------------------------------------------------
+# blocks that move
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("D,hkv", [(128, 2), (64, 1), (16, 1), (80, 3)])
+def test_copy_and_swap(pkv, D, hkv):
+    g = torch.Generator().manual_seed(D)
+    kc, vc = F.pool(g, 9, hkv, D), F.pool(g, 9, hkv, D)
+    kd, vd = kc.cuda(), vc.cuda()
+    pkv.block_copy(kd, vd, torch.tensor([[2, 7], [0, 8]], dtype=torch.int32).cuda())
+    for src, pool in ((kc, kd), (vc, vd)):
+        want = src.clone()
+        want[7], want[8] = src[2], src[0]
+        assert torch.equal(pool.cpu(), want)
+    ids = torch.tensor([3, 1], dtype=torch.int32).cuda()
+    staging = pkv.swap_out(kd, vd, ids)
+    torch.cuda.synchronize()
+    assert torch.equal(staging[:, 0], kc[[3, 1]]) and torch.equal(staging[:, 1], vc[[3, 1]])
+    back = torch.tensor([5, 6], dtype=torch.int32).cuda()
+    pkv.swap_in(kd, vd, back, staging)
+    assert torch.equal(kd[5:7].cpu(), kc[[3, 1]]) and torch.equal(vd[5:7].cpu(), vc[[3, 1]])
