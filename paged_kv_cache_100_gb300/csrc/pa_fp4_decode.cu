@@ -3,8 +3,9 @@
 // quantising the cache), one query token per sequence.  The format is in pa_fp4.cuh.
 //
 // One CTA handles one (sequence, KV head, partition).  Each warp owns every NW-th
-// block of the partition and streams it through its own ring of slots: a block's K
-// and V tiles are 9 head_dim bytes each, whole in the pool, so a bulk copy brings one.
+// pair of blocks of the partition and streams it through its own ring of slots: a
+// block's K and V tiles are 9 head_dim bytes each, whole in the pool, so a bulk copy
+// brings one.
 // The group's query heads are the N columns of mma.sync m16n8k16 tiles in transposed
 // form, S^T[16 tokens x 8 heads] = K Q^T and O^T[head_dim x 8 heads] += V^T P^T, so
 // one pass over K/V serves the group; a group of more than 8 heads is split over
@@ -218,9 +219,9 @@ struct Warp4 {
         l0 = l1 = 0.f;
     }
 
-    // One block, of which the rows [nlo, nvalid) are attended (at least one).
-    __device__ __forceinline__ void block(uint32_t ktile, uint32_t vtile, int nlo, int nvalid) {
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
+    // S^T of a tile in this lane's fragment, times the scales of the query's heads and the softmax.
+    __device__ __forceinline__ void scores(uint32_t ktile, float (&s)[4]) const {
+        s[0] = s[1] = s[2] = s[3] = 0.f;
 #pragma unroll
         for (int c = 0; c < kKWords / kLoad; ++c) {
             uint32_t r0[kLoad], r1[kLoad];
@@ -252,51 +253,14 @@ struct Warp4 {
                 mma_f16_16816(s, second, qb[k + 1][0], qb[k + 1][1]);
             }
         }
-        const bool part = nlo > 0 || nvalid < kBlockSize;
         s[0] *= qs0;
         s[1] *= qs1;
         s[2] *= qs0;
         s[3] *= qs1;
-        if (part) {
-            const int token = g < 4 ? g : g ^ 1;
-            const bool v0 = token >= nlo && token < nvalid, v1 = token + 8 >= nlo && token + 8 < nvalid;
-            s[0] = v0 ? s[0] : -INFINITY;
-            s[1] = v0 ? s[1] : -INFINITY;
-            s[2] = v1 ? s[2] : -INFINITY;
-            s[3] = v1 ? s[3] : -INFINITY;
-        }
-        // every lane looks at its own scores; the column's maximum is only found where one rises
-        float mx0 = fmaxf(s[0], s[2]), mx1 = fmaxf(s[1], s[3]);
-        if (__any_sync(kFull, mx0 > m0 + kLazyLog2 || mx1 > m1 + kLazyLog2)) {
-#pragma unroll
-            for (int k = 4; k < 32; k <<= 1) {
-                mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, k));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, k));
-            }
-            const bool need0 = mx0 > m0 + kLazyLog2, need1 = mx1 > m1 + kLazyLog2;
-            const float a0 = need0 ? exp2f(m0 - mx0) : 1.f;      // 0 while m0 is -inf
-            const float a1 = need1 ? exp2f(m1 - mx1) : 1.f;
-            m0 = need0 ? mx0 : m0;
-            m1 = need1 ? mx1 : m1;
-            l0 *= a0;
-            l1 *= a1;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                o[i][0] *= a0;
-                o[i][1] *= a1;
-                o[i][2] *= a0;
-                o[i][3] *= a1;
-            }
-        }
-        const float w0 = ex2_fast(s[0] - m0), w1 = ex2_fast(s[1] - m1);
-        const float w2 = ex2_fast(s[2] - m0), w3 = ex2_fast(s[3] - m1);
-        l0 += w0 + w2;
-        l1 += w1 + w3;
-        // the weights enter the second product as f16, rounded once: 11 bits
-        // move an output by at most 2^-11 of the largest value it weighs, where
-        // bf16's 8 bits would be as coarse as the output's own rounding
-        const uint32_t b0 = movmatrix_trans(pack_f16x2(w0, w1));
-        const uint32_t b1 = movmatrix_trans(pack_f16x2(w2, w3));
+    }
+
+    // O^T += V^T P^T of a tile, of whose rows [nlo, nvalid) are attended.
+    __device__ __forceinline__ void values(uint32_t vtile, uint32_t b0, uint32_t b1, bool part, int nlo, int nvalid) {
 #pragma unroll
         for (int c = 0; c < (D + 127) / 128; ++c) {
             constexpr int kWords = D == 64 ? 1 : 2;
@@ -334,6 +298,66 @@ struct Warp4 {
         }
     }
 
+    // Two blocks side by side in shared memory (K, V, K, V), of whose 32 rows [nlo, nvalid) are
+    // attended (at least one; nvalid at most 16: the second block is not there, and what its
+    // place holds does not matter).
+    __device__ __forceinline__ void blocks(uint32_t tiles, int nlo, int nvalid) {
+        constexpr uint32_t kTile = fp4_tile_bytes(D);
+        float s[2][4];
+        scores(tiles, s[0]);
+        scores(tiles + 2 * kTile, s[1]);
+        const bool part = nlo > 0 || nvalid < 2 * kBlockSize;
+        if (part) {
+            const int token = g < 4 ? g : g ^ 1;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int r0 = token + u * kBlockSize, r1 = r0 + 8;
+                const bool v0 = r0 >= nlo && r0 < nvalid, v1 = r1 >= nlo && r1 < nvalid;
+                s[u][0] = v0 ? s[u][0] : -INFINITY;
+                s[u][1] = v0 ? s[u][1] : -INFINITY;
+                s[u][2] = v1 ? s[u][2] : -INFINITY;
+                s[u][3] = v1 ? s[u][3] : -INFINITY;
+            }
+        }
+        // every lane looks at its own scores; the column's maximum is only found where one rises
+        float mx0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
+        float mx1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
+        if (__any_sync(kFull, mx0 > m0 + kLazyLog2 || mx1 > m1 + kLazyLog2)) {
+#pragma unroll
+            for (int k = 4; k < 32; k <<= 1) {
+                mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, k));
+                mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, k));
+            }
+            const bool need0 = mx0 > m0 + kLazyLog2, need1 = mx1 > m1 + kLazyLog2;
+            const float a0 = need0 ? exp2f(m0 - mx0) : 1.f;      // 0 while m0 is -inf
+            const float a1 = need1 ? exp2f(m1 - mx1) : 1.f;
+            m0 = need0 ? mx0 : m0;
+            m1 = need1 ? mx1 : m1;
+            l0 *= a0;
+            l1 *= a1;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                o[i][0] *= a0;
+                o[i][1] *= a1;
+                o[i][2] *= a0;
+                o[i][3] *= a1;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float w0 = ex2_fast(s[u][0] - m0), w1 = ex2_fast(s[u][1] - m1);
+            const float w2 = ex2_fast(s[u][2] - m0), w3 = ex2_fast(s[u][3] - m1);
+            l0 += w0 + w2;
+            l1 += w1 + w3;
+            // the weights enter the second product as f16, rounded once: 11 bits
+            // move an output by at most 2^-11 of the largest value it weighs, where
+            // bf16's 8 bits would be as coarse as the output's own rounding
+            const uint32_t b0 = movmatrix_trans(pack_f16x2(w0, w1));
+            const uint32_t b1 = movmatrix_trans(pack_f16x2(w2, w3));
+            values(tiles + (2 * u + 1) * kTile, b0, b1, part, nlo - u * kBlockSize, nvalid - u * kBlockSize);
+        }
+    }
+
     // The state as acc[heads][D], m[heads], l[heads].
     __device__ __forceinline__ void finish(int heads, float *acc, float *m, float *l) {
 #pragma unroll
@@ -358,7 +382,7 @@ struct Warp4 {
 
 template <int D, int NW, int STAGES>
 struct Shape {
-    static constexpr int kStage = 2 * fp4_tile_bytes(D);         // K and V
+    static constexpr int kStage = 4 * fp4_tile_bytes(D);         // K, V, K, V of two blocks
     static constexpr int kRing = NW * STAGES * kStage;
     static_assert(STAGES * kStage >= kHeads * D * 4, "a warp's state is merged over its ring");
     static_assert(kRing % 16 == 0 && kStage % 16 == 0, "bulk copies");
@@ -386,7 +410,7 @@ __device__ __forceinline__ float remote_f32(const float *mine, uint32_t rank) {
 
 // kParts > 1: the grid's clusters of kParts CTAs each work on one (sequence, KV head).
 template <int D, int NW, int STAGES, int kParts>
-__global__ void __launch_bounds__(NW * 32) pa_decode_fp4_kernel(const Fp4Args a) {
+__global__ void __launch_bounds__(NW * 32, D == 256 ? 1 : 16 / NW) pa_decode_fp4_kernel(const Fp4Args a) {
     using S = Shape<D, NW, STAGES>;
     constexpr uint32_t kTile = fp4_tile_bytes(D);
     grid_dependency_wait();
@@ -415,8 +439,8 @@ __global__ void __launch_bounds__(NW * 32) pa_decode_fp4_kernel(const Fp4Args a)
     const int len = a.context_lens[b];
     const int32_t *row_table = a.block_tables + (int64_t)b * a.max_blocks;
     const bool early = kParts == 1 && a.window == 0;     // the partition does not move with the length
-    const int ahead = part * a.part_blocks + warp + NW * lane;
-    int first_phys = early && warp + NW * lane < a.part_blocks && ahead < a.max_blocks ? row_table[ahead] : -1;
+    const int in_part = 2 * (warp + NW * (lane >> 1)) + (lane & 1), ahead = part * a.part_blocks + in_part;
+    int first_phys = early && in_part < a.part_blocks && ahead < a.max_blocks ? row_table[ahead] : -1;
     const bool say = threadIdx.x == 0 && part == 0 && idx == 0;
     const int row = row_of(a, b, say);
     if (row < 0) return;                                 // (a cluster's CTAs all leave)
@@ -433,7 +457,7 @@ __global__ void __launch_bounds__(NW * 32) pa_decode_fp4_kernel(const Fp4Args a)
     float *s_m = reinterpret_cast<float *>(bars + NW * STAGES);
     float *s_l = s_m + NW * kHeads;
     __shared__ int s_fail[NW];
-    const int count = w.nblk > warp ? (w.nblk - warp + NW - 1) / NW : 0;
+    const int pairs = (w.nblk + 1) / 2, count = pairs > warp ? (pairs - warp + NW - 1) / NW : 0;
     uint64_t *my_bars = bars + warp * STAGES;
     uint8_t *my_ring = ring + warp * STAGES * S::kStage;
     if (lane == 0) {
@@ -449,26 +473,30 @@ __global__ void __launch_bounds__(NW * 32) pa_decode_fp4_kernel(const Fp4Args a)
         }
         return phys;
     };
-    const int32_t *table = row_table + w.blk0 + warp;
-    if (!early) first_phys = lane < count ? table[NW * lane] : -1;
-    const int first_at = lane < count ? entry_of(first_phys) : 0;
+    // the warp's blocks in its own order: block k is half of its pair k / 2
+    auto place_of = [&](int k) { return 2 * (warp + NW * (k >> 1)) + (k & 1); };
+    const int32_t *table = row_table + w.blk0;
+    if (!early) first_phys = place_of(lane) < w.nblk ? table[place_of(lane)] : -1;
+    const int first_at = place_of(lane) < w.nblk ? entry_of(first_phys) : 0;
 
     const uint64_t policy = l2_policy_evict_first();     // tiles are read once: they leave L2 first
-    auto issue_at = [&](int it, int phys) {
-        const int s = it % STAGES;
-        uint8_t *kt = my_ring + s * S::kStage;
-        const int64_t at = ((int64_t)phys * a.num_kv_heads + kvh) * kTile;
-        mbar_arrive_expect_tx(&my_bars[s], 2 * kTile);
-        bulk_load(kt, a.key_cache + at, kTile, &my_bars[s], policy);
-        bulk_load(kt + kTile, a.value_cache + at, kTile, &my_bars[s], policy);
+    // lanes 0 to 3 each bring a tile of pair `it`, whose blocks are phys (of the lane's)
+    const uint8_t *pool = lane & 1 ? a.value_cache : a.key_cache;
+    auto issue = [&](int it, int phys) {
+        const int s = it % STAGES, here = min(2, w.nblk - place_of(2 * it));
+        if (lane == 0) mbar_arrive_expect_tx(&my_bars[s], 2 * kTile * here);
+        __syncwarp();
+        if (lane < 2 * here)
+            bulk_load(my_ring + s * S::kStage + lane * kTile, pool + ((int64_t)phys * a.num_kv_heads + kvh) * kTile, kTile,
+                      &my_bars[s], policy);
     };
 #pragma unroll
     for (int it = 0; it < STAGES; ++it) {
-        const int at = __shfl_sync(kFull, first_at, it);
-        if (lane == 0 && it < count) issue_at(it, at);
+        const int at = __shfl_sync(kFull, first_at, 2 * it + (lane >> 1 & 1));
+        if (it < count) issue(it, at);
     }
     state.init(a, query);                                // under the tiles' latency
-    for (int k = lane; k < count; k += 32) entries[warp + k * NW] = k == lane ? first_at : entry_of(table[NW * k]);
+    for (int k = lane; place_of(k) < w.nblk; k += 32) entries[place_of(k)] = k == lane ? first_at : entry_of(table[place_of(k)]);
     __syncwarp();
     bool ok = true;
     int it = 0;
@@ -478,13 +506,12 @@ __global__ void __launch_bounds__(NW * 32) pa_decode_fp4_kernel(const Fp4Args a)
             ok = false;
             break;
         }
-        const int tok = (w.blk0 + warp + it * NW) * kBlockSize;
-        const uint32_t kt = smem_u32(my_ring + s * S::kStage);
-        state.block(kt, kt + kTile, max(0, w.start - tok), min(kBlockSize, w.L - tok));
+        const int place = place_of(2 * it), tok = (w.blk0 + place) * kBlockSize;
+        state.blocks(smem_u32(my_ring + s * S::kStage), max(0, w.start - tok), min(kBlockSize * min(2, w.nblk - place), w.L - tok));
         __syncwarp();
-        if (lane == 0 && it + STAGES < count) {
-            fence_proxy_async_smem();
-            issue_at(it + STAGES, entries[warp + (it + STAGES) * NW]);
+        if (it + STAGES < count) {
+            if (lane < 4) fence_proxy_async_smem();
+            issue(it + STAGES, entries[min(place_of(2 * (it + STAGES) + (lane >> 1 & 1)), w.nblk - 1)]);
         }
     }
     if (!ok) {
@@ -756,10 +783,10 @@ pa_status launch_decode(const Fp4Args &a, cudaStream_t st) {
 
 template <int D>
 pa_status launch_all(const Fp4Args &a, const Plan &p, cudaStream_t st) {
-    const auto launch = p.cluster == 1   ? p.narrow ? launch_decode<D, 1, 4, 1> : launch_decode<D, 4, 4, 1>
-                        : p.cluster == 2 ? launch_decode<D, 4, 4, 2>
-                        : p.cluster == 4 ? launch_decode<D, 4, 4, 4>
-                                         : launch_decode<D, 4, 4, 8>;
+    const auto launch = p.cluster == 1   ? p.narrow ? launch_decode<D, 1, 2, 1> : launch_decode<D, 4, 2, 1>
+                        : p.cluster == 2 ? launch_decode<D, 4, 2, 2>
+                        : p.cluster == 4 ? launch_decode<D, 4, 2, 4>
+                                         : launch_decode<D, 4, 2, 8>;
     const pa_status s = launch(a, st);
     if (s != PA_OK || p.max_parts <= 1) return s;
     const cudaError_t e = launch_chained(pa_merge_fp4_kernel<D>, dim3((unsigned)(a.num_seqs * a.num_q_heads)),
