@@ -28,6 +28,15 @@ namespace pa {
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
+#ifndef PNW
+#define PNW 4
+#endif
+#ifndef PST
+#define PST 2
+#endif
+#ifndef PLB
+#define PLB (16/NW)
+#endif
 constexpr int kHeads = 8;                        // query heads of a CTA at most
 // a head's reference maximum moves only when a score exceeds it by more than
 // 2^8: the weights stay in [0, 256], which f16 holds
@@ -111,7 +120,7 @@ __device__ __forceinline__ uint32_t lds8(uint32_t addr) {
 }
 __device__ __forceinline__ uint32_t lds16(uint32_t addr) {
     uint32_t v;
-    asm volatile("{\n\t.reg .u16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(addr));
+    asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(addr));
     return v;
 }
 // kWords (1, 2 or 4) words from a place aligned to them
@@ -123,6 +132,13 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t *w) {
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                      : "r"(addr));
+}
+
+// The low half of every byte of a, the high half of every byte of b.
+__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xe4;" : "=r"(d) : "r"(a), "r"(b), "r"(0x0f0f0f0fu));      // a & c | b & ~c
+    return d;
 }
 
 // A tile, whole and contiguous in its pool, into shared memory.
@@ -259,8 +275,8 @@ struct Warp4 {
         s[3] *= qs1;
     }
 
-    // O^T += V^T P^T of a tile, of whose rows [nlo, nvalid) are attended.
-    __device__ __forceinline__ void values(uint32_t vtile, uint32_t b0, uint32_t b1, bool part, int nlo, int nvalid) {
+    // O^T += V^T P^T of a tile.
+    __device__ __forceinline__ void values(uint32_t vtile, uint32_t b0, uint32_t b1) {
 #pragma unroll
         for (int c = 0; c < (D + 127) / 128; ++c) {
             constexpr int kWords = D == 64 ? 1 : 2;
@@ -271,24 +287,14 @@ struct Warp4 {
                 lds_words<kWords>(vtile + vcode[i & 1] + 64 * c + (i & 2) * 4 * kRow, w[i]);
                 sc[i] = lds8(vtile + vscale[i & 1] + 8 * c + (i & 2) * 4 * kScales);
             }
-            if (part) {
-                // rows that are not attended may hold any scale, NaN among them, and would reach the sum as 0 * NaN
-                const int p = t < 2 ? 2 * t : 2 * t + 1;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int token = (p ^ (i & 1)) + (i & 2) * 4;
-                    sc[i] = token >= nlo && token < nvalid ? sc[i] : 0u;
-                }
-            }
-            const uint32_t sa = (sc[0] << 7) | (sc[1] << 23), sb = (sc[2] << 7) | (sc[3] << 23);
+            const uint32_t sa = __byte_perm(sc[0], sc[1], 0x4101) >> 1, sb = __byte_perm(sc[2], sc[3], 0x4101) >> 1;
 #pragma unroll
             for (int v = 0; v < kWords; ++v) {
-                constexpr uint32_t kLow = 0x0f0f0f0fu;
                 uint32_t ea[4], oa[4], eb[4], ob[4];
-                e2m1x8_to_f16x2x4((w[0][v] & kLow) | ((w[1][v] << 4) & ~kLow), ea);
-                e2m1x8_to_f16x2x4(((w[0][v] >> 4) & kLow) | (w[1][v] & ~kLow), oa);
-                e2m1x8_to_f16x2x4((w[2][v] & kLow) | ((w[3][v] << 4) & ~kLow), eb);
-                e2m1x8_to_f16x2x4(((w[2][v] >> 4) & kLow) | (w[3][v] & ~kLow), ob);
+                e2m1x8_to_f16x2x4(low_halves(w[0][v], w[1][v] << 4), ea);
+                e2m1x8_to_f16x2x4(low_halves(w[0][v] >> 4, w[1][v]), oa);
+                e2m1x8_to_f16x2x4(low_halves(w[2][v], w[3][v] << 4), eb);
+                e2m1x8_to_f16x2x4(low_halves(w[2][v] >> 4, w[3][v]), ob);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t x[4] = {mul_f16x2(ea[k], sa), mul_f16x2(oa[k], sa), mul_f16x2(eb[k], sb), mul_f16x2(ob[k], sb)};
@@ -306,8 +312,15 @@ struct Warp4 {
         float s[2][4];
         scores(tiles, s[0]);
         scores(tiles + 2 * kTile, s[1]);
-        const bool part = nlo > 0 || nvalid < 2 * kBlockSize;
-        if (part) {
+        if (nlo > 0 || nvalid < 2 * kBlockSize) {
+            // rows that are not attended may hold any scale, NaN among them, and would reach the sum as 0 * NaN
+            if (lane < nlo || lane >= nvalid) {
+                const uint32_t at = tiles + (2 * (lane / kBlockSize) + 1) * kTile + fp4_scales_at(D) + lane % kBlockSize * kScales;
+#pragma unroll
+                for (int i = 0; i < kScales; i += 4) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + i), "r"(0u) : "memory");
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
             const int token = g < 4 ? g : g ^ 1;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -354,7 +367,7 @@ struct Warp4 {
             // bf16's 8 bits would be as coarse as the output's own rounding
             const uint32_t b0 = movmatrix_trans(pack_f16x2(w0, w1));
             const uint32_t b1 = movmatrix_trans(pack_f16x2(w2, w3));
-            values(tiles + (2 * u + 1) * kTile, b0, b1, part, nlo - u * kBlockSize, nvalid - u * kBlockSize);
+            values(tiles + (2 * u + 1) * kTile, b0, b1);
         }
     }
 
@@ -410,7 +423,7 @@ __device__ __forceinline__ float remote_f32(const float *mine, uint32_t rank) {
 
 // kParts > 1: the grid's clusters of kParts CTAs each work on one (sequence, KV head).
 template <int D, int NW, int STAGES, int kParts>
-__global__ void __launch_bounds__(NW * 32, D == 256 ? 1 : 16 / NW) pa_decode_fp4_kernel(const Fp4Args a) {
+__global__ void __launch_bounds__(NW * 32, D == 256 ? 1 : PLB) pa_decode_fp4_kernel(const Fp4Args a) {
     using S = Shape<D, NW, STAGES>;
     constexpr uint32_t kTile = fp4_tile_bytes(D);
     grid_dependency_wait();
@@ -783,7 +796,7 @@ pa_status launch_decode(const Fp4Args &a, cudaStream_t st) {
 
 template <int D>
 pa_status launch_all(const Fp4Args &a, const Plan &p, cudaStream_t st) {
-    const auto launch = p.cluster == 1   ? p.narrow ? launch_decode<D, 1, 2, 1> : launch_decode<D, 4, 2, 1>
+    const auto launch = p.cluster == 1   ? p.narrow ? launch_decode<D, 1, 2, 1> : launch_decode<D, PNW, PST, 1>
                         : p.cluster == 2 ? launch_decode<D, 4, 2, 2>
                         : p.cluster == 4 ? launch_decode<D, 4, 2, 4>
                                          : launch_decode<D, 4, 2, 8>;
