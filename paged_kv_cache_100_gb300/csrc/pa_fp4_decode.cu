@@ -28,15 +28,6 @@ namespace pa {
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
-#ifndef PNW
-#define PNW 4
-#endif
-#ifndef PST
-#define PST 2
-#endif
-#ifndef PLB
-#define PLB (16/NW)
-#endif
 constexpr int kHeads = 8;                        // query heads of a CTA at most
 // a head's reference maximum moves only when a score exceeds it by more than
 // 2^8: the weights stay in [0, 256], which f16 holds
@@ -58,6 +49,7 @@ struct Fp4Args {
     int max_blocks, num_blocks;
     int part_blocks, max_parts;
     int window;
+    int ordered;                 // CTAs take sequences longest first
     float scale_log2;
 };
 
@@ -111,6 +103,40 @@ __device__ __forceinline__ int row_of(const Fp4Args &a, int b, bool say) {
     if (!outside && end == at + 1) return at;
     if (say) report(a.status, outside ? PA_DEV_BAD_CONTEXT_LEN : PA_DEV_BAD_QUERY_LEN);
     return -1;
+}
+
+// The sequence of rank `rank` by length, longest first, in kClasses classes of length (within one,
+// in order).  A warp's work; every warp of the grid that asks agrees.
+constexpr int kOrdered = 256;                    // sequences at most
+constexpr int kClasses = 8;
+__device__ __forceinline__ int ranked(const Fp4Args &a, int rank) {
+    const int lane = threadIdx.x & 31, chunks = (a.num_seqs + 31) / 32;
+    int len[kOrdered / 32], most = 0;
+#pragma unroll
+    for (int c = 0; c < kOrdered / 32; ++c) {
+        const int i = 32 * c + lane;
+        len[c] = i < a.num_seqs ? max(a.context_lens[i], 0) : -1;
+        if (a.window > 0) len[c] = min(len[c], a.window);
+        most = max(most, len[c]);
+    }
+    most = __reduce_max_sync(kFull, most);
+    const float unit = (float)kClasses / ((float)most + 1.f);
+#pragma unroll
+    for (int c = 0; c < kOrdered / 32; ++c) len[c] = len[c] < 0 ? -1 : min((int)((float)len[c] * unit), kClasses - 1);
+    for (int k = kClasses - 1; k >= 0; --k) {
+#pragma unroll
+        for (int c = 0; c < kOrdered / 32; ++c) {
+            if (c >= chunks) break;
+            const unsigned here = __ballot_sync(kFull, len[c] == k);
+            const int n = __popc(here);
+            if (rank < n) {
+                const bool mine = ((here >> lane) & 1u) != 0 && __popc(here & ((1u << lane) - 1u)) == rank;
+                return 32 * c + __ffs((int)__ballot_sync(kFull, mine)) - 1;
+            }
+            rank -= n;
+        }
+    }
+    return 0;                                    // (every rank below num_seqs is found)
 }
 
 __device__ __forceinline__ uint32_t lds8(uint32_t addr) {
@@ -423,7 +449,7 @@ __device__ __forceinline__ float remote_f32(const float *mine, uint32_t rank) {
 
 // kParts > 1: the grid's clusters of kParts CTAs each work on one (sequence, KV head).
 template <int D, int NW, int STAGES, int kParts>
-__global__ void __launch_bounds__(NW * 32, D == 256 ? 1 : PLB) pa_decode_fp4_kernel(const Fp4Args a) {
+__global__ void __launch_bounds__(NW * 32, D == 256 ? 1 : 16 / NW) pa_decode_fp4_kernel(const Fp4Args a) {
     using S = Shape<D, NW, STAGES>;
     constexpr uint32_t kTile = fp4_tile_bytes(D);
     grid_dependency_wait();
@@ -440,8 +466,9 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 1 : PLB) pa_decode_fp4_ker
         part = idx / (a.num_seqs * axis);
         idx -= part * a.num_seqs * axis;
     }
-    const int b = idx / axis;
+    int b = idx / axis;
     idx -= b * axis;
+    if (kParts == 1 && a.ordered) b = ranked(a, b);
     const int kvh = idx / a.splits;
     const int first_head = kvh * a.heads * a.splits + (idx - kvh * a.splits) * a.heads;
     // What depends on the CTA's place alone is loaded together, so that a CTA waits one
@@ -725,6 +752,7 @@ struct Plan {
     int part_blocks, max_parts;
     int cluster;                 // CTAs of a cluster; > 1: max_parts is 1
     bool narrow;                 // CTAs of one warp
+    bool ordered;                // longest sequences first
 };
 
 bool plan_of(int num_seqs, int axis, int max_blocks, int window, int partition_size, Plan *p) {
@@ -733,7 +761,7 @@ bool plan_of(int num_seqs, int axis, int max_blocks, int window, int partition_s
     int span = max_blocks;
     if (window > 0) span = std::min(span, (window - 1) / kBlockSize + 2);
     p->cluster = 1;
-    p->narrow = false;
+    p->narrow = p->ordered = false;
     const int64_t ctas = std::max<int64_t>(1, (int64_t)num_seqs * axis), target = 4LL * device_sms();
     if (partition_size != 0) {
         p->part_blocks = partition_size / kBlockSize;
@@ -755,6 +783,7 @@ bool plan_of(int num_seqs, int axis, int max_blocks, int window, int partition_s
     }
     p->max_parts = std::max(1, (span + p->part_blocks - 1) / p->part_blocks);
     const int64_t all = ctas * p->max_parts;
+    p->ordered = p->max_parts == 1 && num_seqs > 1 && num_seqs <= kOrdered && ctas > target;
     p->narrow = p->part_blocks <= (all > 10LL * device_sms() ? 24 : all > 5LL * device_sms() ? 16 : 0);
     return true;
 }
@@ -796,7 +825,7 @@ pa_status launch_decode(const Fp4Args &a, cudaStream_t st) {
 
 template <int D>
 pa_status launch_all(const Fp4Args &a, const Plan &p, cudaStream_t st) {
-    const auto launch = p.cluster == 1   ? p.narrow ? launch_decode<D, 1, 2, 1> : launch_decode<D, PNW, PST, 1>
+    const auto launch = p.cluster == 1   ? p.narrow ? launch_decode<D, 1, 2, 1> : launch_decode<D, 4, 2, 1>
                         : p.cluster == 2 ? launch_decode<D, 4, 2, 2>
                         : p.cluster == 4 ? launch_decode<D, 4, 2, 4>
                                          : launch_decode<D, 4, 2, 8>;
@@ -876,6 +905,7 @@ extern "C" pa_status pa_decode_fp4(void *out, const void *query, const void *key
     a.part_blocks = p.part_blocks;
     a.max_parts = p.max_parts;
     a.window = window;
+    a.ordered = p.ordered;
     a.scale_log2 = scale * 1.4426950408889634f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return head_dim == 64 ? launch_all<64>(a, p, st) : head_dim == 128 ? launch_all<128>(a, p, st) : launch_all<256>(a, p, st);
