@@ -68,14 +68,14 @@ __device__ __forceinline__ float fp4_scale_value(uint32_t byte) {
 
 // The scale of 16 elements of which the largest magnitude is amax: amax / 6 to
 // nearest, ties to even, at least the smallest scale and at most kFp4TopScale; 0 for
-// 0.  `near` is amax to 2^-20; the decision compares amax itself with six times the
-// number midway between two scales, which is exact.
+// 0.  `near` is amax to 2^-20; the decision compares amax itself with *border, six times
+// the number midway between the two scales in question, which is exact.
 template <typename F>
-__device__ __forceinline__ uint32_t fp4_scale_of(float near, F amax) {
+__device__ __forceinline__ uint32_t fp4_scale_of(float near, F amax, float *border) {
     const float low = fminf(near, 2.f * kFp4Top) * ((1.f - 0x1p-18f) / 6.f);
     const uint32_t at = (uint32_t)__half_as_ushort(__float2half_rz(low)) >> 7;   // amax / 6 lies above it, below the second one above
-    const float mid = 6.f * __half2float(__ushort_as_half((unsigned short)((at << 7) + 64)));
-    const bool up = amax > (F)mid || (amax == (F)mid && (at & 1u) != 0);
+    *border = 6.f * __half2float(__ushort_as_half((unsigned short)((at << 7) + 64)));
+    const bool up = amax > (F)*border || (amax == (F)*border && (at & 1u) != 0);
     const uint32_t s = min(at + (up ? 1u : 0u), kFp4TopScale);
     return amax > (F)0 ? max(s, 1u) : 0u;
 }

@@ -5,10 +5,10 @@
 // The format is in pa_fp4.cuh, the mathematics of the angles in pa_rope.cu.
 //
 // Write.  Sixteen elements of a row are the unit: their scale depends on nothing
-// else, so a token's row is written without a look at the rest of its block, and a
-// thread takes one unit: it turns the elements, finds the scale and the codes, and
-// stores 8 bytes of codes and one of scale.  Other CTAs of the launch turn the
-// queries' rows.
+// else, so a token's row is written without a look at the rest of its block.  Two lanes
+// take two units of a row (a thread one, where rows are not made of pairs of them):
+// they turn the elements, find the scales and the codes, and store 8 bytes of codes and
+// one of scale a unit.  Other CTAs of the launch turn the queries' rows.
 //   A key's codes and scale are those of its exact rotation: where a 32-bit value
 // lies so near a border of two codes that its error could cross it (or the largest
 // magnitude so near one of two scales) it is computed again in 64 bits.
@@ -48,96 +48,40 @@ __device__ __forceinline__ double exact_of(const RopeArgs &a, const T *row, int6
     return exact_turn(to_float(row[first]), to_float(row[second]), d == second, a.positions[tok], a.turns[pair], a.factor);
 }
 
-// Scale of the unit from element d0 on in 64 bits.
+// The largest magnitude in 64 bits of those elements from d0 on that `which` has, which the
+// unit's others do not reach.  (An element takes more than a microsecond: 64-bit units are few.  With all
+// 16 of a unit 8192 tokens of 8 KV heads took 43 us, as one CTA had such a unit; with these 24.)
 template <typename T>
-__device__ __noinline__ uint32_t exact_scale(const RopeArgs &a, const T *row, int64_t tok, int d0, float near) {
+__device__ __noinline__ double exact_top(const RopeArgs &a, const T *row, int64_t tok, int d0, uint32_t which) {
     double top = 0.0;
-    for (int i = 0; i < 16; ++i) top = fmax(top, fabs(exact_of<T>(a, row, tok, d0 + i)));
-    return fp4_scale_of<double>(near, top);
+    for (; which != 0; which &= which - 1) top = fmax(top, fabs(exact_of<T>(a, row, tok, d0 + __ffs((int)which) - 1)));
+    return top;
 }
 
-// How a unit's elements are turned: not at all, as halves whose pairs lie in whole units,
-// as neighbours, or as any halves.
-enum { kPlain = 0, kHalves = 1, kNeighbours = 2, kAny = 3 };
+// Eight codes, of which `below` and `above` differ in some, from element d on of a row: those in 64 bits.
+template <typename T, bool kTurned>
+__device__ __noinline__ uint32_t exact_codes(const RopeArgs &a, const T *row, int64_t tok, int d, uint32_t below, uint32_t above,
+                                             float scale) {
+    for (int i = 0; i < 8; ++i) {
+        if ((((below ^ above) >> (4 * i)) & 15u) == 0) continue;
+        uint32_t c = 0;                                  // a zero of either sign
+        if ((((below | above) >> (4 * i)) & 7u) != 0)
+            c = exact_e2m1(kTurned ? exact_of<T>(a, row, tok, d + i) : (double)to_float(row[d + i]), scale);
+        below = (below & ~(15u << (4 * i))) | (c << (4 * i));
+        above = (above & ~(15u << (4 * i))) | (c << (4 * i));
+    }
+    return below;
+}
 
-// Encodes the unit from element d0 on of `row`, a row of token tok.  cs: the token's
-// row of the table.
-template <typename T, int kMode>
-__device__ __forceinline__ void encode_unit(const RopeArgs &a, const T *row, int64_t tok, int d0, const float2 *cs,
-                                            uint8_t *codes, uint8_t *scale_at) {
-    constexpr int N = Vec<T>::N;
-    constexpr bool kBf16 = sizeof(T) == 2;
-    const int rot = a.rotary_dim, half = rot / 2;
-    float y[16], err[16];
-    if constexpr (kMode == kHalves) {
-        const bool on = d0 < rot, second = d0 >= half;
-        const int other = on ? (second ? d0 - half : d0 + half) : d0;
-        const float4 *c = reinterpret_cast<const float4 *>(cs + skewed(on ? (second ? d0 - half : d0) : 0));
-#pragma unroll
-        for (int v = 0; v < 16 / N; ++v) {
-            float x[N], o[N];
-            Vec<T>::widen(reinterpret_cast<const uint4 *>(row + d0)[v], x);
-            Vec<T>::widen(reinterpret_cast<const uint4 *>(row + other)[v], o);
-#pragma unroll
-            for (int i = 0; i < N; i += 2) {
-                const float4 w = c[(v * N + i) / 2];
-                const int k = v * N + i;
-                const float s0 = second ? w.y : -w.y, s1 = second ? w.w : -w.w;
-                y[k] = on ? x[i] * w.x + o[i] * s0 : x[i];
-                y[k + 1] = on ? x[i + 1] * w.z + o[i + 1] * s1 : x[i + 1];
-                err[k] = on ? fabsf(x[i]) + fabsf(o[i]) : 0.f;
-                err[k + 1] = on ? fabsf(x[i + 1]) + fabsf(o[i + 1]) : 0.f;
-            }
-        }
-    } else if constexpr (kMode == kNeighbours) {
-        const int some = (rot - d0) / 2;                 // pairs of the unit that are turned, if below 8
-        const float2 *c = cs + skewed(d0 / 2 < half ? d0 / 2 : 0);
-#pragma unroll
-        for (int v = 0; v < 16 / N; ++v) {
-            float x[N];
-            Vec<T>::widen(reinterpret_cast<const uint4 *>(row + d0)[v], x);
-#pragma unroll
-            for (int i = 0; i < N; i += 2) {
-                const int k = v * N + i;
-                const bool on = k / 2 < some;
-                const float2 w = on ? c[k / 2] : make_float2(1.f, 0.f);
-                y[k] = on ? x[i] * w.x - x[i + 1] * w.y : x[i];
-                y[k + 1] = on ? x[i + 1] * w.x + x[i] * w.y : x[i + 1];
-                err[k] = err[k + 1] = on ? fabsf(x[i]) + fabsf(x[i + 1]) : 0.f;
-            }
-        }
-    } else {
-#pragma unroll
-        for (int v = 0; v < 16 / N; ++v) {
-            float x[N], o[N];
-            if constexpr (kMode == kAny) {
-                load_pairs<T>(row, d0 + v * N, rot, false, x, o);
-            } else {
-                Vec<T>::widen(reinterpret_cast<const uint4 *>(row + d0)[v], x);
-            }
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int k = v * N + i, d = d0 + k;
-                y[k] = x[i];
-                err[k] = 0.f;
-                if constexpr (kMode == kAny) {
-                    if (d < rot) {
-                        const bool second = d >= half;
-                        const float2 w = cs[skewed(second ? d - half : d)];
-                        y[k] = second ? x[i] * w.x + o[i] * w.y : x[i] * w.x - o[i] * w.y;
-                        err[k] = fabsf(x[i]) + fabsf(o[i]);
-                    }
-                }
-            }
-        }
-    }
+// Encodes a unit, elements y of token tok's row from element d0 on.  most: the largest
+// |x0| + |x1| of the pairs that were turned into them (0: none were).
+template <typename T, bool kTurned>
+__device__ __forceinline__ void encode16(const RopeArgs &a, const T *row, int64_t tok, int d0, const float (&y)[16], float most,
+                                         uint8_t *codes, uint8_t *scale_at) {
+    constexpr bool kSnapped = !kTurned && sizeof(T) == 2;
     uint32_t top = 0;                                    // as bits: magnitudes compare like integers, NaN above all
-    float most = 0.f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-        top = max(top, __float_as_uint(y[k]) & 0x7fffffffu);
-        if constexpr (kMode != kPlain) most = fmaxf(most, err[k]);
-    }
+    for (int k = 0; k < 16; ++k) top = max(top, __float_as_uint(y[k]) & 0x7fffffffu);
     if (top > 0x7f800000u) {
         *reinterpret_cast<uint2 *>(codes) = make_uint2(0u, 0u);
         *scale_at = (uint8_t)kFp4NanScale;
@@ -145,90 +89,327 @@ __device__ __forceinline__ void encode_unit(const RopeArgs &a, const T *row, int
     }
     const float amax = __uint_as_float(top);
     if (amax > kFp4Top) report(a.status, PA_DEV_RANGE);
-    uint32_t byte = fp4_scale_of(amax, amax);
-    const float turn_err = kTurnError * (float)a.factor;
-    if constexpr (kMode != kPlain) {
-        const float e = most * turn_err, lo = fmaxf(amax - e, 0.f), hi = amax + e;
-        if (fp4_scale_of(lo, lo) != fp4_scale_of(hi, hi)) byte = exact_scale<T>(a, row, tok, d0, amax);
+    float border;
+    uint32_t byte = fp4_scale_of(amax, amax, &border);
+    const float e = kTurned ? most * (kTurnError * (float)a.factor) : 0.f;       // error of an element
+    if (kTurned && most > 0.f && (fabsf(amax - border) <= e || amax <= e)) {
+        uint32_t which = 0;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) which |= fabsf(y[k]) >= amax - 2.f * e ? 1u << k : 0u;
+        byte = fp4_scale_of<double>(amax, exact_top<T>(a, row, tok, d0, which), &border);
     }
     const float scale = fp4_scale_value(byte), inv = byte != 0 ? 1.f / scale : 0.f;
+    // of a quotient, which is at most 6.4 near a border (larger ones saturate)
+    const float eq = e * inv + 0x1p-20f;
     uint32_t out[2];
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
         float lo[8], hi[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float q = y[8 * p + i] * inv;
-            if constexpr (kMode == kPlain && kBf16) {
+            if constexpr (kSnapped) {
                 // A bf16 element divided by a scale of 4 bits is a border of two codes or at least
                 // 2^-9 of it away; the product with the inverse is off by 2^-23, which rounding to
                 // 16 bits takes back.
-                lo[i] = __uint_as_float((__float_as_uint(q) + 0x80u) & 0xffffff00u);
+                lo[i] = __uint_as_float((__float_as_uint(y[8 * p + i] * inv) + 0x80u) & 0xffffff00u);
             } else {
-                const float e = kMode == kPlain ? fabsf(q) * 0x1p-22f
-                                                : fmaxf(err[8 * p + i] * turn_err * inv, fabsf(q) * 0x1p-22f);
-                lo[i] = q - e;
-                hi[i] = q + e;
+                lo[i] = fmaf(y[8 * p + i], inv, -eq);
+                hi[i] = fmaf(y[8 * p + i], inv, eq);
             }
         }
         out[p] = f32x8_to_e2m1x8(lo);
-        if constexpr (!(kMode == kPlain && kBf16)) {
-            // the codes of the value less and more its error: where they differ the code comes from 64 bits
-            const uint32_t differ = out[p] ^ f32x8_to_e2m1x8(hi);
-            if (differ != 0) {
-#pragma unroll 1
-                for (int i = 0; i < 8; ++i) {
-                    if (((differ >> (4 * i)) & 15u) == 0) continue;
-                    const int d = d0 + 8 * p + i;
-                    const double x = kMode == kPlain ? (double)to_float(row[d]) : exact_of<T>(a, row, tok, d);
-                    out[p] = (out[p] & ~(15u << (4 * i))) | (exact_e2m1(x, scale) << (4 * i));
-                }
-            }
+        if constexpr (!kSnapped) {
+            // The codes of the value less and more its error: where they differ (in more than the
+            // sign of a zero) the code comes from 64 bits.
+            const uint32_t above = f32x8_to_e2m1x8(hi);
+            if (out[p] != above) out[p] = exact_codes<T, kTurned>(a, row, tok, d0 + 8 * p, out[p], above, scale);
         }
     }
     *reinterpret_cast<uint2 *>(codes) = make_uint2(out[0], out[1]);
     *scale_at = (uint8_t)byte;
 }
 
-// The keys' and values' units of a CTA's tokens.
+// How a key's elements are turned: not at all, as halves or as neighbours, where two
+// lanes take two units of a row at a time, or in any way, where a thread takes one.
+enum { kPlain = 0, kHalves = 1, kNeighbours = 2, kAny = 3 };
+
+// Where a row of new keys or values lies.
+template <typename T>
+__device__ __forceinline__ const T *new_row(const RopeArgs &a, bool value, int64_t tok, int h) {
+    return static_cast<const T *>(value ? a.value : a.key) + tok * (value ? a.v_stride : a.k_stride) + (int64_t)h * a.head_dim;
+}
+
+// Two lanes' part of two units, A and B, of a row that is read in whole vectors: the
+// even lane has the first eight elements of each and finds A's scale, the odd one the
+// others and B's.  With halves the units lie head_dim / 2 apart, all of it turned, else
+// they follow one another.  (Half the registers of a thread with both units: 64 leave
+// the query rows' CTAs of the same kernel 32 warps on an SM.)
+template <typename T, int kMode>
+struct Pair {
+    static constexpr int N = Vec<T>::N, V = 8 / N;
+    static constexpr bool kTurned = kMode != kPlain, kSnapped = !kTurned && sizeof(T) == 2;
+    uint4 raw[2][V];
+    // d: this lane's first element of A and of B
+    __device__ __forceinline__ void load(const T *row, int d0, int d1) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int v = 0; v < V; ++v) raw[u][v] = reinterpret_cast<const uint4 *>(row + (u ? d1 : d0))[v];
+    }
+    // tile: where the row's block goes; nullptr: nothing is written.  cs: the token's row of the table.  Whole warps.
+    __device__ __forceinline__ void encode(const RopeArgs &a, int64_t tok, int h, const int (&d)[2], const float2 *cs, uint8_t *tile,
+                                           int off) const {
+        const bool odd = (threadIdx.x & 1) != 0, on = tile != nullptr;
+        float y[2][8];
+        uint32_t most[2] = {0, 0}, top[2] = {0, 0};      // the largest |x0| + |x1| of a pair, |y|: as bits, which compare like integers
+        bool turns[2] = {kTurned, kTurned};
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float w[N];
+                Vec<T>::widen(raw[u][v], w);
+#pragma unroll
+                for (int i = 0; i < N; ++i) y[u][v * N + i] = w[i];
+            }
+        if constexpr (kMode == kHalves) {
+            // (a value's lane that goes along has elements past the table)
+            const float4 *c = reinterpret_cast<const float4 *>(cs + skewed(on ? d[0] : 0));
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const float4 w = c[i / 2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float p = y[0][i + k], q = y[1][i + k], cosine = k ? w.z : w.x, sine = k ? w.w : w.y;
+                    most[0] = max(most[0], __float_as_uint(fabsf(p) + fabsf(q)));
+                    y[0][i + k] = p * cosine - q * sine;
+                    y[1][i + k] = q * cosine + p * sine;
+                }
+            }
+            most[1] = most[0];
+        } else if constexpr (kMode == kNeighbours) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int at = d[u] / 2, some = a.rotary_dim / 2 - at;       // of the four pairs, those that are turned
+                const float4 *c = reinterpret_cast<const float4 *>(cs + skewed(some > 0 ? at : 0));
+                turns[u] = some > 0;
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    const float4 w = c[i / 2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float p = y[u][2 * (i + k)], q = y[u][2 * (i + k) + 1], cosine = k ? w.z : w.x, sine = k ? w.w : w.y;
+                        most[u] = max(most[u], __float_as_uint(fabsf(p) + fabsf(q)));
+                        y[u][2 * (i + k)] = i + k < some ? p * cosine - q * sine : p;
+                        y[u][2 * (i + k) + 1] = i + k < some ? q * cosine + p * sine : q;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if constexpr (kSnapped) {
+                // on the bf16 pairs as they came
+                uint32_t m = 0;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (uint32_t w : {raw[u][v].x, raw[u][v].y, raw[u][v].z, raw[u][v].w}) m = __vmaxu2(m, w & 0x7fff7fffu);
+                top[u] = max(m << 16, m & 0xffff0000u);
+            } else {
+                if constexpr (kTurned) {
+                    float m = 0.f;                       // passes over NaN: most then is one, or infinite
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(y[u][i]));
+                    top[u] = __float_as_uint(m);
+                }
+                if (!kTurned || most[u] >= 0x7f800000u) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) top[u] = max(top[u], __float_as_uint(y[u][i]) & 0x7fffffffu);
+                }
+            }
+        }
+        // each lane gets the whole of its own unit
+        const uint32_t mine = max(odd ? top[1] : top[0], __shfl_xor_sync(kAll, odd ? top[0] : top[1], 1));
+        float e = 0.f;                                   // error of an element of the lane's own unit
+        if constexpr (kTurned) {
+            const uint32_t m0 = turns[0] ? most[0] : 0u, m1 = turns[1] ? most[1] : 0u;
+            e = __uint_as_float(max(odd ? m1 : m0, __shfl_xor_sync(kAll, odd ? m0 : m1, 1))) * (kTurnError * (float)a.factor);
+        }
+        const float amax = __uint_as_float(mine);
+        const bool nan = mine > 0x7f800000u;
+        float border;
+        uint32_t byte = nan ? kFp4NanScale : fp4_scale_of(amax, amax, &border);
+        if (!nan && amax > kFp4Top && on) report(a.status, PA_DEV_RANGE);
+        if constexpr (kTurned) {
+            const bool unsure = !nan && e > 0.f && on && (fabsf(amax - border) <= e || amax <= e);
+            if (__any_sync(kAll, unsure)) {
+                // both lanes' elements that may be the largest, in 64 bits
+                const float floor = unsure ? amax - 2.f * e : INFINITY, other_floor = __shfl_xor_sync(kAll, floor, 1);
+                uint32_t which[2] = {0, 0};
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) which[u] |= fabsf(y[u][i]) >= (odd == (u == 1) ? floor : other_floor) ? 1u << i : 0u;
+                const T *row = new_row<T>(a, false, tok, h);
+                const double a0 = exact_top<T>(a, row, tok, d[0], which[0]), a1 = exact_top<T>(a, row, tok, d[1], which[1]);
+                __syncwarp();
+                const double exact = fmax(odd ? a1 : a0, __shfl_xor_sync(kAll, odd ? a0 : a1, 1));
+                if (unsure) byte = fp4_scale_of<double>(amax, exact, &border);
+            }
+        }
+        const float scale = fp4_scale_value(byte), inv = byte != 0 ? 1.f / scale : 0.f;
+        const float other_inv = __shfl_xor_sync(kAll, inv, 1);
+        float other_e = 0.f, other_scale = 0.f;
+        if constexpr (kTurned) other_e = __shfl_xor_sync(kAll, e, 1);
+        if constexpr (!kSnapped) other_scale = __shfl_xor_sync(kAll, scale, 1);
+        if (!on) return;                                 // (no lane waits for this one from here on)
+        const int D = a.head_dim;
+        uint8_t *codes = tile + off * (D / 2);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const bool own = odd == (u == 1);
+            const float f = own ? inv : other_inv;
+            float lo[8];
+            uint32_t out;
+            if constexpr (kSnapped) {
+                // A bf16 element divided by a scale of 4 bits is a border of two codes or at least 2^-9 of it
+                // away; the product with the inverse is off by 2^-23, which rounding to 16 bits takes back.
+#pragma unroll
+                for (int i = 0; i < 8; ++i) lo[i] = __uint_as_float((__float_as_uint(y[u][i] * f) + 0x80u) & 0xffffff00u);
+                out = f32x8_to_e2m1x8(lo);
+            } else {
+                // The codes of the value less and more its error: where they differ (in more than the sign of a
+                // zero) the code comes from 64 bits.  A quotient is at most 6.4 near a border (larger ones saturate).
+                const float eq = (own ? e : other_e) * f + 0x1p-20f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) lo[i] = fmaf(y[u][i], f, -eq);
+                out = f32x8_to_e2m1x8(lo);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) lo[i] = fmaf(y[u][i], f, eq);
+                const uint32_t above = f32x8_to_e2m1x8(lo);
+                if (out != above)
+                    out = exact_codes<T, kTurned>(a, new_row<T>(a, !kTurned, tok, h), tok, d[u], out, above, own ? scale : other_scale);
+            }
+            *reinterpret_cast<uint32_t *>(codes + d[u] / 2) = isnan(f) ? 0u : out;
+            if (own) tile[fp4_scales_at(D) + off * (D / 16) + d[u] / 16] = (uint8_t)byte;
+        }
+    }
+};
+
+// The unit from element d0 on of a row, turned in any way.
+template <typename T, bool kTurned>
+__device__ __noinline__ void encode_any(const RopeArgs &a, const T *row, int64_t tok, int d0, const float2 *cs, uint8_t *codes,
+                                        uint8_t *scale) {
+    constexpr int N = Vec<T>::N;
+    const int rot = a.rotary_dim, half = rot / 2;
+    float y[16], most = 0.f;
+#pragma unroll
+    for (int v = 0; v < 16 / N; ++v) {
+        float x[N], o[N];
+        if constexpr (kTurned) load_pairs<T>(row, d0 + v * N, rot, a.interleaved, x, o);
+        else Vec<T>::widen(reinterpret_cast<const uint4 *>(row + d0)[v], x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int d = d0 + v * N + i;
+            y[v * N + i] = x[i];
+            if constexpr (kTurned) {
+                if (d < rot) {
+                    const bool second = a.interleaved ? d & 1 : d >= half;
+                    const float2 w = cs[skewed(a.interleaved ? d >> 1 : (second ? d - half : d))];
+                    y[v * N + i] = second ? x[i] * w.x + o[i] * w.y : x[i] * w.x - o[i] * w.y;
+                    most = fmaxf(most, fabsf(x[i]) + fabsf(o[i]));
+                }
+            }
+        }
+    }
+    encode16<T, kTurned>(a, row, tok, d0, y, most, codes + d0 / 2, scale + d0 / 16);
+}
+
+// The keys' and values' units of a CTA's tokens.  A thread keeps its 16 elements' place in
+// the rows, a unit (kAny) or a lane's part of two, and goes through the rows.
 template <typename T, int kMode>
 __device__ __forceinline__ void encode_tokens(const RopeArgs &a, int cta, float2 *table) {
-    const int half = a.rotary_dim / 2, D = a.head_dim, units = D / 16, per_token = 2 * a.num_kv_heads * units;
+    const int half = a.rotary_dim / 2, D = a.head_dim, per_row = D / 16, rows = 2 * a.num_kv_heads;
+    const int per_pass = kRopeThreads / per_row;
     const int group = cta / a.tile_splits, split = cta - group * a.tile_splits;
     const int64_t t0 = (int64_t)group * a.tile_tokens, limit = (int64_t)a.num_blocks * kBlockSize;
     const int nt = (int)min((int64_t)a.tile_tokens, a.num_tokens - t0);
     const int table_row = skewed(a.table_row);
-    if constexpr (kMode != kPlain) {
+    const int item = threadIdx.x % per_row, place = threadIdx.x / per_row, first = place + split * per_pass;
+    // row of the token, and the token: `rows` rows a token, per_pass * tile_splits rows on with every step
+    int t = first / rows, row = first - t * rows;
+    const int step = per_pass * a.tile_splits, step_t = step / rows, step_row = step - step_t * rows;
+    auto next = [&]() {
+        t += step_t;
+        row += step_row;
+        if (row >= rows) row -= rows, ++t;
+    };
+    // the tile and the row in it where the token goes (nullptr: it is not written)
+    auto tile_of = [&](int *off) -> uint8_t * {
+        if (place >= per_pass || t >= nt) return nullptr;
+        const int64_t slot = a.slot_mapping[t0 + t];
+        if (slot >= limit && row == 0 && item == 0) report(a.status, PA_DEV_BAD_SLOT);
+        if (slot < 0 || slot >= limit) return nullptr;
+        const bool value = row >= a.num_kv_heads;
+        *off = (int)slot & (kBlockSize - 1);
+        return static_cast<uint8_t *>(value ? a.value_cache : a.key_cache) +
+               ((slot / kBlockSize) * a.num_kv_heads + (value ? row - a.num_kv_heads : row)) * fp4_tile_bytes(D);
+    };
+    auto make_table = [&]() {
         for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
-            const int t = i / half, p = i - t * half;
-            table[t * table_row + skewed(p)] = turn_of(a.positions[t0 + t], a.turns[p], (float)a.factor);
+            const int at = i / half, k = i - at * half;
+            table[at * table_row + skewed(k)] = turn_of(a.positions[t0 + at], a.turns[k], (float)a.factor);
         }
         __syncthreads();
-    }
-    for (int i = threadIdx.x + split * kRopeThreads; i < nt * per_token; i += a.tile_splits * kRopeThreads) {
-        const int t = i / per_token, rest = i - t * per_token, row = rest / units, unit = rest - row * units;
-        const bool value = row >= a.num_kv_heads;
-        const int h = value ? row - a.num_kv_heads : row;
-        const int64_t tok = t0 + t, slot = a.slot_mapping[tok];
-        if (slot < 0) continue;
-        if (slot >= limit) {
-            if (rest == 0) report(a.status, PA_DEV_BAD_SLOT);
-            continue;
+    };
+    if constexpr (kMode == kAny) {
+        make_table();
+        for (; place < per_pass && t < nt; next()) {
+            int off;
+            uint8_t *tile = tile_of(&off);
+            if (tile == nullptr) continue;
+            const bool value = row >= a.num_kv_heads;
+            const T *src = new_row<T>(a, value, t0 + t, value ? row - a.num_kv_heads : row);
+            uint8_t *codes = tile + off * (D / 2), *scales = tile + fp4_scales_at(D) + off * per_row;
+            if (value || half == 0) encode_any<T, false>(a, src, t0 + t, 16 * item, nullptr, codes, scales);
+            else encode_any<T, true>(a, src, t0 + t, 16 * item, table + t * table_row, codes, scales);
         }
-        const int64_t blk = slot / kBlockSize;
-        const int off = (int)(slot - blk * kBlockSize);
-        uint8_t *tile = static_cast<uint8_t *>(value ? a.value_cache : a.key_cache) +
-                        (blk * a.num_kv_heads + h) * fp4_tile_bytes(D);
-        uint8_t *codes = tile + off * (D / 2) + unit * 8, *scale = tile + fp4_scales_at(D) + off * units + unit;
-        const T *src = static_cast<const T *>(value ? a.value : a.key) + tok * (value ? a.v_stride : a.k_stride) +
-                       (int64_t)h * D;
-        if (value) encode_unit<T, kPlain>(a, src, tok, unit * 16, nullptr, codes, scale);
-        else encode_unit<T, kMode>(a, src, tok, unit * 16, table + t * table_row, codes, scale);
+    } else {
+        // The first row's elements are on their way while the table is made.  Warps stay whole: lanes
+        // without a row, or whose token has no slot, go along.
+        Pair<T, kMode> x;
+        uint8_t *tile;
+        int off = 0, d[2], h, at;
+        bool value;
+        auto take = [&]() {
+            at = min(t, nt - 1);
+            value = row >= a.num_kv_heads;
+            h = value ? row - a.num_kv_heads : row;
+            const bool apart = kMode == kHalves && !value;
+            d[0] = (apart ? 16 : 32) * (item >> 1) + 8 * (item & 1);
+            d[1] = d[0] + (apart ? half : 16);
+            tile = tile_of(&off);
+            x.load(new_row<T>(a, value, t0 + at, h), d[0], d[1]);
+        };
+        take();
+        if constexpr (kMode != kPlain) make_table();
+        for (;;) {
+            const bool any_key = __any_sync(kAll, tile != nullptr && !value), any_value = __any_sync(kAll, tile != nullptr && value);
+            if (any_value)
+                reinterpret_cast<const Pair<T, kPlain> &>(x).encode(a, t0 + at, h, d, nullptr, value ? tile : nullptr, off);
+            __syncwarp();
+            if (any_key) x.encode(a, t0 + at, h, d, table + at * table_row, value ? nullptr : tile, off);
+            __syncwarp();
+            next();
+            if (!__any_sync(kAll, place < per_pass && t < nt)) break;
+            take();
+        }
     }
 }
 
 template <typename T, int kMode>
-__global__ void __launch_bounds__(kRopeThreads) pa_rope_write_fp4_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, kMode == kAny ? 3 : 4) pa_rope_write_fp4_kernel(const __grid_constant__ RopeArgs a) {
     extern __shared__ __align__(16) float2 s_table[];
     grid_dependency_wait();
     grid_dependents_launch();
@@ -243,17 +424,19 @@ pa_status launch_write(RopeArgs &a, cudaStream_t stream) {
     const int half = a.rotary_dim / 2;
     a.tile_tokens = 1;
     while (a.tile_tokens < kMostEncodeTokens && n / (2 * a.tile_tokens) >= 4 * sms) a.tile_tokens *= 2;
-    const int64_t items = (int64_t)a.tile_tokens * 2 * a.num_kv_heads * (a.head_dim / 16);
-    const int64_t passes = (items + kRopeThreads - 1) / kRopeThreads;
+    // units in pairs where rows are whole pairs of them and halves are whole units
+    const bool pairs = a.head_dim % 32 == 0 && (half == 0 || a.interleaved || a.rotary_dim == a.head_dim);
+    const int per_pass = kRopeThreads / (a.head_dim / 16);
+    const int64_t passes = ((int64_t)a.tile_tokens * 2 * a.num_kv_heads + per_pass - 1) / per_pass;
     a.tile_splits = (int)std::max<int64_t>(1, std::min<int64_t>(passes, 4 * sms * a.tile_tokens / n));
     const int64_t tiles = (n + a.tile_tokens - 1) / a.tile_tokens * a.tile_splits, grid = tiles + row_ctas;
     if (grid >= ((int64_t)1 << 31)) return PA_ERR_UNSUPPORTED;
     a.tile_ctas = (int)tiles;
     const size_t smem = std::max((size_t)a.tile_tokens * skewed(a.table_row), (size_t)a.row_tokens * a.table_row) * sizeof(float2);
-    const auto kernel = half == 0        ? pa_rope_write_fp4_kernel<T, kPlain>
-                        : a.interleaved  ? pa_rope_write_fp4_kernel<T, kNeighbours>
-                        : half % 16 == 0 ? pa_rope_write_fp4_kernel<T, kHalves>
-                                         : pa_rope_write_fp4_kernel<T, kAny>;
+    const auto kernel = !pairs          ? pa_rope_write_fp4_kernel<T, kAny>
+                        : half == 0     ? pa_rope_write_fp4_kernel<T, kPlain>
+                        : a.interleaved ? pa_rope_write_fp4_kernel<T, kNeighbours>
+                                        : pa_rope_write_fp4_kernel<T, kHalves>;
     if (smem > 44 * 1024) {
         cudaError_t e = allow_smem(kernel, kMostTables);
         if (e != cudaSuccess) return cuda_failure(e, "cudaFuncSetAttribute(4-bit write)");
