@@ -33,6 +33,13 @@ constexpr int kMostEncodeTokens = 16;            // tokens of a CTA that encodes
 // in no bank.
 __host__ __device__ constexpr int skewed(int p) { return p + (p >> 4) * 2; }
 
+// 1 / x to 2^-22 of it (x a normal number).
+__device__ __forceinline__ float inverse(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // The code of d / scale in 64 bits (0 where the scale is 0).
 __device__ __noinline__ uint32_t exact_e2m1(double d, float scale) {
     const double q = scale > 0.f ? fabs(d) / (double)scale : 0.0;
@@ -258,7 +265,7 @@ struct Pair {
                 if (unsure) byte = fp4_scale_of<double>(amax, exact, &border);
             }
         }
-        const float scale = fp4_scale_value(byte), inv = byte != 0 ? 1.f / scale : 0.f;
+        const float scale = fp4_scale_value(byte), inv = byte != 0 ? inverse(scale) : 0.f;
         const float other_inv = __shfl_xor_sync(kAll, inv, 1);
         float other_e = 0.f, other_scale = 0.f;
         if constexpr (kTurned) other_e = __shfl_xor_sync(kAll, e, 1);
@@ -274,14 +281,15 @@ struct Pair {
             uint32_t out;
             if constexpr (kSnapped) {
                 // A bf16 element divided by a scale of 4 bits is a border of two codes or at least 2^-9 of it
-                // away; the product with the inverse is off by 2^-23, which rounding to 16 bits takes back.
+                // away; the product with the inverse is off by 2^-22, which rounding to multiples of 2^-16
+                // (the last place of numbers from 128 to 256) takes back.
 #pragma unroll
-                for (int i = 0; i < 8; ++i) lo[i] = __uint_as_float((__float_as_uint(y[u][i] * f) + 0x80u) & 0xffffff00u);
+                for (int i = 0; i < 8; ++i) lo[i] = fmaf(y[u][i], f, 192.f) - 192.f;
                 out = f32x8_to_e2m1x8(lo);
             } else {
                 // The codes of the value less and more its error: where they differ (in more than the sign of a
                 // zero) the code comes from 64 bits.  A quotient is at most 6.4 near a border (larger ones saturate).
-                const float eq = (own ? e : other_e) * f + 0x1p-20f;
+                const float eq = (own ? e : other_e) * f + 0x1p-18f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) lo[i] = fmaf(y[u][i], f, -eq);
                 out = f32x8_to_e2m1x8(lo);
@@ -413,8 +421,10 @@ __global__ void __launch_bounds__(kRopeThreads, kMode == kAny ? 3 : 4) pa_rope_w
     extern __shared__ __align__(16) float2 s_table[];
     grid_dependency_wait();
     grid_dependents_launch();
-    if ((int)blockIdx.x < a.tile_ctas) encode_tokens<T, kMode>(a, blockIdx.x, s_table);
-    else turn_rows<T>(a, blockIdx.x - a.tile_ctas, s_table, false);
+    // the two kinds spread evenly over the grid
+    const int before = (int)((uint64_t)blockIdx.x * a.tile_ctas / gridDim.x);
+    if ((int)((uint64_t)(blockIdx.x + 1) * a.tile_ctas / gridDim.x) > before) encode_tokens<T, kMode>(a, before, s_table);
+    else turn_rows<T>(a, blockIdx.x - before, s_table, false);
 }
 
 template <typename T>
