@@ -13,8 +13,12 @@
 // lies so near a border of two codes that its error could cross it (or the largest
 // magnitude so near one of two scales) it is computed again in 64 bits.
 //
-// Read.  Blocks of the contexts become blocks of bf16 or f32 rows: eight elements a
-// thread, 4 bytes of codes in, 16 or 32 bytes out.
+// Read.  Blocks of the contexts become blocks of bf16 or f32 rows, a warp a tile.  It is
+// bound by memory, four fifths of it the rows that are written: 65536 tokens of 8 KV heads
+// of 128 to bf16, 312 MB, 51 us (6.1 TB/s, 0.91 of a copy); 777 tokens to f32 3.9 us.  Up to 8
+// tiles a CTA: 4, 16 and 32 of them 52, 53 and 58 us; four units ahead of a lane's eight 53; tiles
+// brought and taken by bulk copies through shared memory 51 and 4.5, and the kernels before and
+// after such a one waited for its share of the L1 (write and read of 8192 tokens 79 us, 67 so).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -460,7 +464,9 @@ pa_status launch_write(RopeArgs &a, cudaStream_t stream) {
 // ---------------------------------------------------------------------------
 // Reading back
 // ---------------------------------------------------------------------------
-constexpr int kReadThreads = 256;
+constexpr int kReadWarps = 4;
+constexpr int kMostTiles = 8;                    // of a CTA
+constexpr int kReadAhead = 8;                    // units of a lane on their way
 
 struct ReadArgs {
     void *key_out, *value_out;       // [num_seqs * width][num_kv_heads][16][head_dim]
@@ -474,7 +480,7 @@ struct ReadArgs {
     int num_seqs, num_kv_heads, head_dim;
     int max_blocks, num_blocks, width, window;
     int num_rows;                    // of the query
-    int splits;                      // CTAs of a block
+    int tiles, groups;               // tiles of a CTA; CTAs of a sequence
 };
 
 // f16 pair times f16 pair, exact, as two floats
@@ -483,83 +489,99 @@ __device__ __forceinline__ float2 product_of(uint32_t codes, uint32_t scale) {
     return make_float2(f16lo(v), f16hi(v));
 }
 
-// One CTA (or `splits`) a block of a context.  kDim: head_dim, or 0 where it is none of the
-// usual ones.
-template <typename T, int kDim>
-__global__ void __launch_bounds__(kReadThreads) pa_read_fp4_kernel(const ReadArgs a) {
+// A CTA widens up to kMostTiles tiles of a sequence: of its table's entries in order, of
+// an entry the keys' by KV head, then the values'.  Each warp takes every kReadWarps-th
+// one.  A lane's unit is 16 bytes of rows; codes, scales and rows of a tile follow one
+// another in the same order, so that its number is its place in each.
+template <typename T>
+__global__ void __launch_bounds__(32 * kReadWarps) pa_read_fp4_kernel(const ReadArgs a) {
+    constexpr int kUnit = 16 / (int)sizeof(T);           // elements
     grid_dependency_wait();
     grid_dependents_launch();
-    const int D = kDim > 0 ? kDim : a.head_dim;
-    const int at = blockIdx.x / a.splits, split = blockIdx.x - at * a.splits;
-    const int b = at / a.width, j = at - b * a.width;
+    const int D = a.head_dim, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.x / a.groups, group = blockIdx.x - b * a.groups, per_block = 2 * a.num_kv_heads;
+    int64_t i0 = (int64_t)group * a.tiles, i1 = min(i0 + a.tiles, (int64_t)a.width * per_block);
+    const int j0 = (int)(i0 / per_block);                // the CTA's first entry; lane k holds entry j0 + k
     int len = a.context_lens[b];
-    const int phys_ahead = a.block_tables[(int64_t)b * a.max_blocks + j];
-    const bool first_thread = threadIdx.x == 0 && split == 0;
+    const bool mine = (int64_t)(j0 + lane) * per_block < i1;
+    int phys = mine ? a.block_tables[(int64_t)b * a.max_blocks + j0 + lane] : 0;
     if (len < 0 || len > a.width * kBlockSize) {
-        if (first_thread && j == 0) report(a.status, PA_DEV_BAD_CONTEXT_LEN);
+        if (threadIdx.x == 0 && group == 0) report(a.status, PA_DEV_BAD_CONTEXT_LEN);
         len = len < 0 ? 0 : a.width * kBlockSize;
     }
-    if (first_thread && a.tables_out != nullptr) a.tables_out[at] = at;
+    if (warp == 0 && mine && a.tables_out != nullptr) a.tables_out[b * a.width + j0 + lane] = b * a.width + j0 + lane;
     int64_t chunk = 1;
     if (a.query_start != nullptr) {
         const int64_t from = a.query_start[b], end = a.query_start[b + 1];
         const bool outside = from < 0 || end < from || end > a.num_rows;
         chunk = end - from;
-        if (first_thread && j == 0) a.lens_out[b] = outside ? -1 : a.context_lens[b];
+        if (threadIdx.x == 0 && group == 0) a.lens_out[b] = outside ? -1 : a.context_lens[b];
         if (outside || chunk == 0) return;               // no row attends to the context
     }
     // a chunk's first row is the one that looks farthest back
-    const int64_t start = a.window > 0 ? len - chunk + 1 - a.window : 0;
-    const int rows = min(len - j * kBlockSize, kBlockSize);      // of the block
-    if (rows <= 0 || (int64_t)(j + 1) * kBlockSize <= start) return;
-    int phys = phys_ahead;
-    if ((unsigned)phys >= (unsigned)a.num_blocks) {
-        if (first_thread) report(a.status, PA_DEV_BAD_BLOCK_ID);
+    const int64_t start = a.window > 0 ? max(len - chunk + 1 - a.window, (int64_t)0) : 0;
+    const int first = (int)(start / kBlockSize), last = (len + kBlockSize - 1) / kBlockSize;     // entries that are read
+    i0 = max(i0, (int64_t)first * per_block);
+    i1 = min(i1, (int64_t)last * per_block);
+    if (i0 >= i1) return;
+    if (mine && j0 + lane >= first && j0 + lane < last && (unsigned)phys >= (unsigned)a.num_blocks) {
+        if (warp == 0) report(a.status, PA_DEV_BAD_BLOCK_ID);
         phys = 0;
     }
-    const int chunks = D / 8, per_tile = kBlockSize * chunks, all = 2 * a.num_kv_heads * per_tile;
-    const int64_t in = (int64_t)phys * a.num_kv_heads, out = (int64_t)at * a.num_kv_heads;
-#pragma unroll 4
-    for (int u = threadIdx.x + split * kReadThreads; u < all; u += a.splits * kReadThreads) {
-        int tile = u / per_tile;
-        const int rest = u - tile * per_tile, row = rest / chunks, c = rest - row * chunks;
+    const int skip = (int)(i0 - (int64_t)j0 * per_block), all = skip + (int)(i1 - i0);     // tiles of the first entry that are not read
+    for (int i = skip + warp; i < all; i += kReadWarps) {
+        const int entry = i / per_block, tile = i - entry * per_block, j = j0 + entry;
+        const int at = __shfl_sync(kAll, phys, entry);
         const bool value = tile >= a.num_kv_heads;
-        if (value) tile -= a.num_kv_heads;
-        const uint8_t *src = (value ? a.value_cache : a.key_cache) + (in + tile) * fp4_tile_bytes(D);
-        T *dst = static_cast<T *>(value ? a.value_out : a.key_out) + (out + tile) * kBlockSize * D + rest * 8;
-        float2 v[4];
-        if (row < rows) {
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(src + rest * 4);
-            const uint32_t s = fp4_scale_pair<0>(src[fp4_scales_at(D) + row * (D / 16) + c / 2]);
-            uint32_t x[4];
-            e2m1x8_to_f16x2x4(w, x);
+        const int h = value ? tile - a.num_kv_heads : tile;
+        const uint8_t *codes = (value ? a.value_cache : a.key_cache) + ((int64_t)at * a.num_kv_heads + h) * fp4_tile_bytes(D);
+        const uint8_t *scales = codes + fp4_scales_at(D);
+        uint4 *rows = reinterpret_cast<uint4 *>(static_cast<T *>(value ? a.value_out : a.key_out) +
+                                                ((int64_t)(b * a.width + j) * a.num_kv_heads + h) * kBlockSize * D);
+        const int held = min(len - j * kBlockSize, kBlockSize) * (D / kUnit);    // units of rows of the context
+        // (a tile is 32 units or a multiple of it)
+        for (int u0 = lane; u0 < kBlockSize * D / kUnit; u0 += 32 * kReadAhead) {
+            uint32_t c[kReadAhead], s[kReadAhead];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = product_of(x[i], s);
-        } else {
+            for (int k = 0; k < kReadAhead; ++k) {
+                const int u = u0 + 32 * k;
+                if (u >= kBlockSize * D / kUnit) break;
+                if constexpr (kUnit == 8) c[k] = reinterpret_cast<const uint32_t *>(codes)[u];
+                else c[k] = reinterpret_cast<const uint16_t *>(codes)[u];
+                s[k] = scales[u / (16 / kUnit)];
+            }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = make_float2(0.f, 0.f);
-        }
-        if constexpr (sizeof(T) == 4) {
-            reinterpret_cast<float4 *>(dst)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-            reinterpret_cast<float4 *>(dst)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
-        } else {
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
-                                                         pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+            for (int k = 0; k < kReadAhead; ++k) {
+                const int u = u0 + 32 * k;
+                if (u >= kBlockSize * D / kUnit) break;
+                uint32_t x[4];
+                e2m1x8_to_f16x2x4(c[k], x);
+                const uint32_t sc = fp4_scale_pair<0>(s[k]);
+                float2 v[kUnit / 2];
+#pragma unroll
+                for (int i = 0; i < kUnit / 2; ++i) v[i] = product_of(x[i], sc);
+                uint4 w;
+                if constexpr (kUnit == 4)
+                    w = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
+                else
+                    w = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
+                                   pack_bf16x2(v[3].x, v[3].y));
+                rows[u] = u < held ? w : make_uint4(0u, 0u, 0u, 0u);
+            }
         }
     }
 }
 
 template <typename T>
 pa_status launch_read(ReadArgs &a, cudaStream_t stream) {
-    const int64_t blocks = (int64_t)a.num_seqs * a.width;
-    const int64_t passes = ((int64_t)2 * a.num_kv_heads * kBlockSize * (a.head_dim / 8) + kReadThreads - 1) / kReadThreads;
-    a.splits = (int)std::max<int64_t>(1, std::min<int64_t>(passes, 8LL * device_sms() / blocks));
-    if (blocks * a.splits >= ((int64_t)1 << 31)) return PA_ERR_UNSUPPORTED;
-    const auto kernel = a.head_dim == 64    ? pa_read_fp4_kernel<T, 64>
-                        : a.head_dim == 128 ? pa_read_fp4_kernel<T, 128>
-                        : a.head_dim == 256 ? pa_read_fp4_kernel<T, 256>
-                                            : pa_read_fp4_kernel<T, 0>;
-    cudaError_t e = launch_chained(kernel, dim3((unsigned)(blocks * a.splits)), dim3(kReadThreads), 0, stream, a);
+    // a CTA has as many tiles as leave sixteen CTAs an SM, one a warp at least
+    const int64_t per_seq = (int64_t)a.width * 2 * a.num_kv_heads;
+    a.tiles = (int)std::max<int64_t>(kReadWarps, std::min<int64_t>(kMostTiles, a.num_seqs * per_seq / (16LL * device_sms())));
+    const int64_t groups = (per_seq + a.tiles - 1) / a.tiles, grid = a.num_seqs * groups;
+    if (grid >= ((int64_t)1 << 31)) return PA_ERR_UNSUPPORTED;
+    a.groups = (int)groups;
+    const auto kernel = pa_read_fp4_kernel<T>;
+    cudaError_t e = launch_chained(kernel, dim3((unsigned)grid), dim3(32 * kReadWarps), 0, stream, a);
     if (e != cudaSuccess) return cuda_failure(e, "pa_read_fp4_kernel launch");
     count_launches(1);
     return PA_OK;
