@@ -167,6 +167,13 @@ __device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) {
     return d;
 }
 
+// mma_f16_16816 that a compiler may move
+__device__ __forceinline__ void mma_pure(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 // A tile, whole and contiguous in its pool, into shared memory.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar, uint64_t policy) {
     asm volatile(
@@ -261,44 +268,52 @@ struct Warp4 {
         l0 = l1 = 0.f;
     }
 
-    // S^T of a tile in this lane's fragment, times the scales of the query's heads and the softmax.
-    __device__ __forceinline__ void scores(uint32_t ktile, float (&s)[4]) const {
-        s[0] = s[1] = s[2] = s[3] = 0.f;
+    // S^T of two tiles in this lane's fragment, times the scales of the query's heads and the
+    // softmax.  The tiles' products alternate, each tile's in two sums: a product waits for the fourth one before.
+    __device__ __forceinline__ void scores(uint32_t ktile, uint32_t stride, float (&s)[2][4]) const {
+        float part[2][2][4];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) part[i >> 3][(i >> 2) & 1][i & 3] = 0.f;
 #pragma unroll
         for (int c = 0; c < kKWords / kLoad; ++c) {
-            uint32_t r0[kLoad], r1[kLoad];
-            lds_words<kLoad>(ktile + kcode + 64 * c, r0);
-            lds_words<kLoad>(ktile + kcode + 64 * c + 8 * kRow, r1);
-            uint32_t c0, c1;
-            if constexpr (D == 64) {
-                c0 = lds8(ktile + kscale);
-                c1 = lds8(ktile + kscale + 8 * kScales);
-            } else {
-                c0 = lds16(ktile + kscale + 8 * c);
-                c1 = lds16(ktile + kscale + 8 * c + 8 * kScales);
-            }
-            const uint32_t s0[2] = {fp4_scale_pair<0>(c0), fp4_scale_pair<1>(c0)};
-            const uint32_t s1[2] = {fp4_scale_pair<0>(c1), fp4_scale_pair<1>(c1)};
+            uint32_t r[2][2][kLoad], sc[2][2][2];        // [tile][row g, g + 8]
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    lds_words<kLoad>(ktile + u * stride + kcode + 64 * c + 8 * i * kRow, r[u][i]);
+                    const uint32_t at = ktile + u * stride + kscale + 8 * c + 8 * i * kScales;
+                    const uint32_t w = D == 64 ? lds8(at) : lds16(at);
+                    sc[u][i][0] = fp4_scale_pair<0>(w);
+                    sc[u][i][1] = fp4_scale_pair<1>(w);
+                }
 #pragma unroll
             for (int w = 0; w < kLoad; ++w) {
-                uint32_t x[4], y[4];
-                e2m1x8_to_f16x2x4(r0[w], x);
-                e2m1x8_to_f16x2x4(r1[w], y);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[i] = mul_f16x2(x[i], s0[w / 2]);
-                    y[i] = mul_f16x2(y[i], s1[w / 2]);
-                }
                 const int k = 2 * (c * kLoad + w);
-                const uint32_t first[4] = {x[0], y[0], x[1], y[1]}, second[4] = {x[2], y[2], x[3], y[3]};
-                mma_f16_16816(s, first, qb[k][0], qb[k][1]);
-                mma_f16_16816(s, second, qb[k + 1][0], qb[k + 1][1]);
+                uint32_t x[2][4], y[2][4];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    e2m1x8_to_f16x2x4(r[u][0][w], x[u]);
+                    e2m1x8_to_f16x2x4(r[u][1][w], y[u]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[u][i] = mul_f16x2(x[u][i], sc[u][0][w / 2]);
+                        y[u][i] = mul_f16x2(y[u][i], sc[u][1][w / 2]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t f[4] = {x[u][2 * e], y[u][2 * e], x[u][2 * e + 1], y[u][2 * e + 1]};
+                        mma_pure(part[u][e], f, qb[k + e][0], qb[k + e][1]);
+                    }
             }
         }
-        s[0] *= qs0;
-        s[1] *= qs1;
-        s[2] *= qs0;
-        s[3] *= qs1;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[u][i] = (part[u][0][i] + part[u][1][i]) * (i & 1 ? qs1 : qs0);
     }
 
     // O^T += V^T P^T of a tile.
@@ -324,7 +339,7 @@ struct Warp4 {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t x[4] = {mul_f16x2(ea[k], sa), mul_f16x2(oa[k], sa), mul_f16x2(eb[k], sb), mul_f16x2(ob[k], sb)};
-                    mma_f16_16816(o[4 * (c * kWords + v) + k], x, b0, b1);
+                    mma_pure(o[4 * (c * kWords + v) + k], x, b0, b1);
                 }
             }
         }
@@ -336,8 +351,7 @@ struct Warp4 {
     __device__ __forceinline__ void blocks(uint32_t tiles, int nlo, int nvalid) {
         constexpr uint32_t kTile = fp4_tile_bytes(D);
         float s[2][4];
-        scores(tiles, s[0]);
-        scores(tiles + 2 * kTile, s[1]);
+        scores(tiles, 2 * kTile, s);
         if (nlo > 0 || nvalid < 2 * kBlockSize) {
             // rows that are not attended may hold any scale, NaN among them, and would reach the sum as 0 * NaN
             if (lane < nlo || lane >= nvalid) {
@@ -382,6 +396,7 @@ struct Warp4 {
                 o[i][3] *= a1;
             }
         }
+        uint32_t p[2][2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const float w0 = ex2_fast(s[u][0] - m0), w1 = ex2_fast(s[u][1] - m1);
@@ -391,10 +406,11 @@ struct Warp4 {
             // the weights enter the second product as f16, rounded once: 11 bits
             // move an output by at most 2^-11 of the largest value it weighs, where
             // bf16's 8 bits would be as coarse as the output's own rounding
-            const uint32_t b0 = movmatrix_trans(pack_f16x2(w0, w1));
-            const uint32_t b1 = movmatrix_trans(pack_f16x2(w2, w3));
-            values(tiles + (2 * u + 1) * kTile, b0, b1);
+            p[u][0] = movmatrix_trans(pack_f16x2(w0, w1));
+            p[u][1] = movmatrix_trans(pack_f16x2(w2, w3));
         }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) values(tiles + (2 * u + 1) * kTile, p[u][0], p[u][1]);
     }
 
     // The state as acc[heads][D], m[heads], l[heads].
@@ -755,36 +771,62 @@ struct Plan {
     bool ordered;                // longest sequences first
 };
 
-bool plan_of(int num_seqs, int axis, int max_blocks, int window, int partition_size, Plan *p) {
+// Estimated microseconds of a call whose CTAs take `pairs` pairs of blocks a warp, `ctas` of them at a time.
+// A warp alone on its scheduler takes 0.8 us a pair (of 128 elements; its products wait for one
+// another), and the SM 0.44 us for each CTA's where many share it.
+double pair_time(double ctas, int head_dim) {
+    const double k = ctas / device_sms(), f = head_dim == 64 ? 0.68 : head_dim == 256 ? 1.5 : 1.0;
+    return f * (k <= 1 ? 0.8 : k <= 2 ? 1.05 : std::max(1.65, 0.44 * k));
+}
+
+// How contexts are cut, by the table's width, as only the GPU knows the lengths.  Compared are
+// whole contexts (3.5 us and their pairs), clusters of 2, 4 or 8 CTAs that fit the GPU at once
+// (4.6 us, and 2.5 ns a CTA more) and parts enough to fill the GPU with a merge behind them (5 us
+// and 5.8 ns a CTA, up to a thousand).  Parts have 8 blocks at least, 40 where the sequences alone
+// make a CTA an SM, and 128 at most, or 256 where there are CTAs enough; a number of CTAs that
+// is short of filling the GPU by an eighth is left.
+// Contexts between half of and all of 1024 tokens, 8 KV heads of 128: 16 of them whole 10.1 us, in
+// clusters of 2 9.9, of 4 9.9, of 8 14.8; 32 whole 12.9, of 2 13.7; of 2048: 16 whole 16.5, of 2 13.8,
+// of 4 13.6, in 5 parts 14.8; 32 whole 21.4, of 2 20.6, in 3 parts 24.4; of 8192: one in clusters of
+// 8 11.4, in 64 parts 10.4; 32 whole 70.8, of 2 60.4, in 3 parts 59.2.
+//
+// Where there are more than five CTAs per SM and their parts short, CTAs have one warp, 16
+// of which an SM holds: a short part's time is its start and its end.  Contexts between half of
+// and all of 32 tokens: 800 CTAs 5.8 us against 9.8, 2048 7.8 / 21.0; of 128: 9.3 / 11.3, 13.7 / 23.6;
+// of 512: 800 CTAs 21.2 / 18.3.  (Those of 512 CTAs or fewer gain nothing: 128 tokens 7.7 / 6.3.)
+bool plan_of(int num_seqs, int axis, int max_blocks, int window, int partition_size, int head_dim, Plan *p) {
     if (partition_size != 0 && (partition_size < kBlockSize || partition_size > kMaxPartition || partition_size % kBlockSize))
         return false;
     int span = max_blocks;
     if (window > 0) span = std::min(span, (window - 1) / kBlockSize + 2);
     p->cluster = 1;
-    p->narrow = p->ordered = false;
-    const int64_t ctas = std::max<int64_t>(1, (int64_t)num_seqs * axis), target = 4LL * device_sms();
+    // what the GPU holds at once: four CTAs of four warps an SM, two with heads of 256
+    const int64_t sms = device_sms(), ctas = std::max<int64_t>(1, (int64_t)num_seqs * axis), target = (head_dim == 256 ? 2 : 4) * sms;
     if (partition_size != 0) {
         p->part_blocks = partition_size / kBlockSize;
     } else {
-        const int most = ctas >= target ? 256 : 128;
+        const int most = ctas >= target ? 256 : 128, largest = kMaxPartition / kBlockSize;
         int64_t parts = std::max<int64_t>((target - ctas / 8 + ctas - 1) / ctas, (span + most - 1) / most);
         parts = std::max<int64_t>(1, std::min<int64_t>(parts, 4 * ctas > target ? span / 40 : (span + 7) / 8));
-        const int cluster = parts <= 2 ? 2 : parts <= 4 ? 4 : 8;
-        if (parts > 1 && parts <= 8 && ctas * cluster <= target) {
-            p->cluster = cluster;
-            p->max_parts = 1;
-            p->part_blocks = (span + p->cluster - 1) / p->cluster + 1;
-            return true;
-        }
-        const int largest = kMaxPartition / kBlockSize;
+        // a grid beyond 32 CTAs an SM is made of the largest parts only: a wide table's last ones are often empty
         parts = std::min(parts, std::max<int64_t>(std::max<int64_t>((target + ctas - 1) / ctas, 8 * target / ctas),
                                                   (span + largest - 1) / largest));
-        p->part_blocks = std::max(1, (int)((span + parts - 1) / parts));
+        auto pairs = [&](int64_t n) { return (double)((span + 8 * n - 1) / (8 * n)); };          // of a warp, in n parts
+        auto cost = [&](int64_t n, double base) { return base + pairs(n) * pair_time((double)ctas * n, head_dim); };
+        double best = parts > 1 ? cost(parts, 5.0 + 0.0058 * std::min((double)ctas * parts, 1024.0)) : INFINITY;
+        if (span <= largest && cost(1, 3.5) <= best) best = cost(1, 3.5), parts = 1;
+        for (int c = 2; c <= 8 && ctas * c <= target; c *= 2)
+            if ((span + c - 1) / c < largest && c <= span && cost(c, 4.6 + 0.0025 * ctas * c) < best) {
+                best = cost(c, 4.6 + 0.0025 * ctas * c);
+                p->cluster = c;
+            }
+        p->part_blocks = p->cluster > 1 ? (span + p->cluster - 1) / p->cluster + 1 : std::max(1, (int)((span + parts - 1) / parts));
     }
-    p->max_parts = std::max(1, (span + p->part_blocks - 1) / p->part_blocks);
+    p->max_parts = p->cluster > 1 ? 1 : std::max(1, (span + p->part_blocks - 1) / p->part_blocks);
     const int64_t all = ctas * p->max_parts;
-    p->ordered = p->max_parts == 1 && num_seqs > 1 && num_seqs <= kOrdered && ctas > target;
-    p->narrow = p->part_blocks <= (all > 10LL * device_sms() ? 24 : all > 5LL * device_sms() ? 16 : 0);
+    p->narrow = p->cluster == 1 && p->part_blocks <= (all > 10 * sms ? 24 : all > 5 * sms ? 16 : 0);
+    // (not where CTAs are short: 2048 of one warp on 32 tokens 9.1 us in order of length, 7.8 in theirs)
+    p->ordered = !p->narrow && p->cluster == 1 && p->max_parts == 1 && num_seqs > 1 && num_seqs <= kOrdered && ctas > target;
     return true;
 }
 
@@ -850,7 +892,7 @@ extern "C" size_t pa_decode_fp4_workspace_bytes(int num_seqs, int num_q_heads, i
         return (size_t)-1;
     const int group = num_q_heads / num_kv_heads;
     Plan p;
-    if (!plan_of(num_seqs, num_kv_heads * (group / heads_per_cta(group)), max_blocks_per_seq, window, partition_size, &p))
+    if (!plan_of(num_seqs, num_kv_heads * (group / heads_per_cta(group)), max_blocks_per_seq, window, partition_size, head_dim, &p))
         return (size_t)-1;
     return workspace_of(num_seqs, num_q_heads, head_dim, p.max_parts);
 }
@@ -867,7 +909,7 @@ extern "C" pa_status pa_decode_fp4(void *out, const void *query, const void *key
         return PA_ERR_INVALID_ARG;
     const int group = num_q_heads / num_kv_heads, heads = heads_per_cta(group), splits = group / heads;
     Plan p;
-    if (!plan_of(num_seqs, num_kv_heads * splits, max_blocks_per_seq, window, partition_size, &p))
+    if (!plan_of(num_seqs, num_kv_heads * splits, max_blocks_per_seq, window, partition_size, head_dim, &p))
         return PA_ERR_INVALID_ARG;
     if (!head_dim_ok(head_dim)) return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0 || num_query_tokens == 0) return PA_OK;
