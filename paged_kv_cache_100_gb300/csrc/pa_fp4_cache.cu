@@ -44,13 +44,6 @@ __device__ __forceinline__ float inverse(float x) {
     return y;
 }
 
-// The code of d / scale in 64 bits (0 where the scale is 0).
-__device__ __noinline__ uint32_t exact_e2m1(double d, float scale) {
-    const double q = scale > 0.f ? fabs(d) / (double)scale : 0.0;
-    const uint32_t m = (q > 0.25) + (q >= 0.75) + (q > 1.25) + (q >= 1.75) + (q > 2.5) + (q >= 3.5) + (q > 5.0);
-    return m | (d < 0.0 ? 8u : 0u);
-}
-
 // Element d of a row of token `tok` in 64 bits.
 template <typename T>
 __device__ __forceinline__ double exact_of(const RopeArgs &a, const T *row, int64_t tok, int d) {
@@ -69,19 +62,33 @@ __device__ __noinline__ double exact_top(const RopeArgs &a, const T *row, int64_
     return top;
 }
 
+// Midway between the magnitudes of codes c and c + 1, c at most 6.
+__device__ __forceinline__ float code_border(uint32_t c) {
+    return c < 4 ? 0.25f + 0.5f * (float)c : c == 4 ? 2.5f : c == 5 ? 3.5f : 5.f;
+}
+
 // Eight codes, of which `below` and `above` differ in some, from element d on of a row: those in 64 bits.
 template <typename T, bool kTurned>
 __device__ __noinline__ uint32_t exact_codes(const RopeArgs &a, const T *row, int64_t tok, int d, uint32_t below, uint32_t above,
                                              float scale) {
+    uint32_t out = below;
     for (int i = 0; i < 8; ++i) {
-        if ((((below ^ above) >> (4 * i)) & 15u) == 0) continue;
+        const uint32_t p = (below >> (4 * i)) & 15u, q = (above >> (4 * i)) & 15u;
+        if (p == q) continue;
         uint32_t c = 0;                                  // a zero of either sign
-        if ((((below | above) >> (4 * i)) & 7u) != 0)
-            c = exact_e2m1(kTurned ? exact_of<T>(a, row, tok, d + i) : (double)to_float(row[d + i]), scale);
-        below = (below & ~(15u << (4 * i))) | (c << (4 * i));
-        above = (above & ~(15u << (4 * i))) | (c << (4 * i));
+        if (((p | q) & 7u) != 0) {
+            const uint32_t most = max(p & 7u, q & 7u);
+            const double x = kTurned ? exact_of<T>(a, row, tok, d + i) : (double)to_float(row[d + i]);
+            c = ((p ^ q) & 8u) != 0 ? 0u : min(p & 7u, q & 7u);
+            for (; c < most; ++c) {
+                const double border = (double)(code_border(c) * scale);          // exact: 3 bits times 4
+                if (!(fabs(x) > border || (fabs(x) == border && (c & 1u) != 0))) break;
+            }
+            c |= x < 0.0 ? 8u : 0u;
+        }
+        out = (out & ~(15u << (4 * i))) | (c << (4 * i));
     }
-    return below;
+    return out;
 }
 
 // Encodes a unit, elements y of token tok's row from element d0 on.  most: the largest

@@ -767,28 +767,30 @@ int heads_per_cta(int group) {
 struct Plan {
     int part_blocks, max_parts;
     int cluster;                 // CTAs of a cluster; > 1: max_parts is 1
-    bool narrow;                 // CTAs of one warp
+    int warps;                   // of a CTA: 4, or without clusters 1, 8 or 16
     bool ordered;                // longest sequences first
 };
 
-// Estimated microseconds of a call whose CTAs take `pairs` pairs of blocks a warp, `ctas` of them at a time.
-// A warp alone on its scheduler takes 0.8 us a pair (of 128 elements; its products wait for one
-// another), and the SM 0.44 us for each CTA's where many share it.
-double pair_time(double ctas, int head_dim) {
-    const double k = ctas / device_sms(), f = head_dim == 64 ? 0.68 : head_dim == 256 ? 1.5 : 1.0;
+// Microseconds that each warp's pair of blocks takes with `ctas` CTAs of `warps` warps on the GPU.  A
+// warp alone on its scheduler takes 0.8 us a pair (of 128 elements; its products wait for one
+// another), and the SM 0.44 us for every four warps where many share it.
+double pair_time(double ctas, int warps, int head_dim) {
+    const double k = warps / 4.0 * std::max(1.0, ctas / device_sms()), f = head_dim == 64 ? 0.68 : head_dim == 256 ? 1.5 : 1.0;
     return f * (k <= 1 ? 0.8 : k <= 2 ? 1.05 : std::max(1.65, 0.44 * k));
 }
 
 // How contexts are cut, by the table's width, as only the GPU knows the lengths.  Compared are
-// whole contexts (3.5 us and their pairs), clusters of 2, 4 or 8 CTAs that fit the GPU at once
+// whole contexts (3.5 us and their pairs) by CTAs of 4, 8 or 16 warps, clusters of 2, 4 or 8 CTAs that fit the GPU at once
 // (4.6 us, and 2.5 ns a CTA more) and parts enough to fill the GPU with a merge behind them (5 us
 // and 5.8 ns a CTA, up to a thousand).  Parts have 8 blocks at least, 40 where the sequences alone
 // make a CTA an SM, and 128 at most, or 256 where there are CTAs enough; a number of CTAs that
 // is short of filling the GPU by an eighth is left.
-// Contexts between half of and all of 1024 tokens, 8 KV heads of 128: 16 of them whole 10.1 us, in
-// clusters of 2 9.9, of 4 9.9, of 8 14.8; 32 whole 12.9, of 2 13.7; of 2048: 16 whole 16.5, of 2 13.8,
-// of 4 13.6, in 5 parts 14.8; 32 whole 21.4, of 2 20.6, in 3 parts 24.4; of 8192: one in clusters of
-// 8 11.4, in 64 parts 10.4; 32 whole 70.8, of 2 60.4, in 3 parts 59.2.
+// A few CTAs have more warps: the SM then has as much to do as in clusters, and less to merge.
+// Contexts between half of and all of 1024 tokens, 8 KV heads of 128: 16 of them by 4 warps 10.1 us, by
+// 16 8.5, in clusters of 2 or 4 9.9, of 8 14.8; 32 by 4 warps 12.9, by 8 12.3; of 2048: 8 by 4 warps
+// 16.1, in clusters of 4 9.7; 16 by 4 warps 16.5, by 16 12.4, in clusters of 4 13.6, in 5 parts 14.8; 32 by 4
+// warps 21.4, by 8 19.2, in clusters of 2 20.6, in 3 parts 24.4; of 8192: one in clusters of 8 11.4, in 64 parts
+// 10.4; 32 by 4 warps 70.8, in clusters of 2 60.4, in 3 parts 59.2.
 //
 // Where there are more than five CTAs per SM and their parts short, CTAs have one warp, 16
 // of which an SM holds: a short part's time is its start and its end.  Contexts between half of
@@ -800,6 +802,7 @@ bool plan_of(int num_seqs, int axis, int max_blocks, int window, int partition_s
     int span = max_blocks;
     if (window > 0) span = std::min(span, (window - 1) / kBlockSize + 2);
     p->cluster = 1;
+    p->warps = 4;
     // what the GPU holds at once: four CTAs of four warps an SM, two with heads of 256
     const int64_t sms = device_sms(), ctas = std::max<int64_t>(1, (int64_t)num_seqs * axis), target = (head_dim == 256 ? 2 : 4) * sms;
     if (partition_size != 0) {
@@ -811,22 +814,29 @@ bool plan_of(int num_seqs, int axis, int max_blocks, int window, int partition_s
         // a grid beyond 32 CTAs an SM is made of the largest parts only: a wide table's last ones are often empty
         parts = std::min(parts, std::max<int64_t>(std::max<int64_t>((target + ctas - 1) / ctas, 8 * target / ctas),
                                                   (span + largest - 1) / largest));
-        auto pairs = [&](int64_t n) { return (double)((span + 8 * n - 1) / (8 * n)); };          // of a warp, in n parts
-        auto cost = [&](int64_t n, double base) { return base + pairs(n) * pair_time((double)ctas * n, head_dim); };
-        double best = parts > 1 ? cost(parts, 5.0 + 0.0058 * std::min((double)ctas * parts, 1024.0)) : INFINITY;
-        if (span <= largest && cost(1, 3.5) <= best) best = cost(1, 3.5), parts = 1;
+        auto cost = [&](int64_t n, int warps, double base) {             // in n parts, by CTAs of `warps` warps
+            return base + (double)((span + 2 * warps * n - 1) / (2 * warps * n)) * pair_time((double)ctas * n, warps, head_dim);
+        };
+        double best = parts > 1 ? cost(parts, 4, 5.0 + 0.0058 * std::min((double)ctas * parts, 1024.0)) : INFINITY;
+        for (int w = 4; w <= (head_dim == 256 ? 8 : 16); w *= 2)
+            if (span <= largest && (w == 4 || ctas * w <= 4 * target) && cost(1, w, 3.5 + 0.02 * (w - 4)) <= best) {
+                best = cost(1, w, 3.5 + 0.02 * (w - 4));
+                parts = 1;
+                p->warps = w;
+            }
         for (int c = 2; c <= 8 && ctas * c <= target; c *= 2)
-            if ((span + c - 1) / c < largest && c <= span && cost(c, 4.6 + 0.0025 * ctas * c) < best) {
-                best = cost(c, 4.6 + 0.0025 * ctas * c);
+            if ((span + c - 1) / c < largest && c <= span && cost(c, 4, 4.6 + 0.0025 * ctas * c) < best) {
+                best = cost(c, 4, 4.6 + 0.0025 * ctas * c);
                 p->cluster = c;
             }
+        if (p->cluster > 1) p->warps = 4;
         p->part_blocks = p->cluster > 1 ? (span + p->cluster - 1) / p->cluster + 1 : std::max(1, (int)((span + parts - 1) / parts));
     }
     p->max_parts = p->cluster > 1 ? 1 : std::max(1, (span + p->part_blocks - 1) / p->part_blocks);
     const int64_t all = ctas * p->max_parts;
-    p->narrow = p->cluster == 1 && p->part_blocks <= (all > 10 * sms ? 24 : all > 5 * sms ? 16 : 0);
+    if (p->cluster == 1 && p->part_blocks <= (2 * all > 5 * target ? 24 : 4 * all > 5 * target ? 16 : 0)) p->warps = 1;
     // (not where CTAs are short: 2048 of one warp on 32 tokens 9.1 us in order of length, 7.8 in theirs)
-    p->ordered = !p->narrow && p->cluster == 1 && p->max_parts == 1 && num_seqs > 1 && num_seqs <= kOrdered && ctas > target;
+    p->ordered = p->warps == 4 && p->cluster == 1 && p->max_parts == 1 && num_seqs > 1 && num_seqs <= kOrdered && ctas > target;
     return true;
 }
 
@@ -867,10 +877,14 @@ pa_status launch_decode(const Fp4Args &a, cudaStream_t st) {
 
 template <int D>
 pa_status launch_all(const Fp4Args &a, const Plan &p, cudaStream_t st) {
-    const auto launch = p.cluster == 1   ? p.narrow ? launch_decode<D, 1, 2, 1> : launch_decode<D, 4, 2, 1>
-                        : p.cluster == 2 ? launch_decode<D, 4, 2, 2>
-                        : p.cluster == 4 ? launch_decode<D, 4, 2, 4>
-                                         : launch_decode<D, 4, 2, 8>;
+    pa_status (*launch)(const Fp4Args &, cudaStream_t) = launch_decode<D, 4, 2, 1>;
+    if (p.cluster == 2) launch = launch_decode<D, 4, 2, 2>;
+    if (p.cluster == 4) launch = launch_decode<D, 4, 2, 4>;
+    if (p.cluster == 8) launch = launch_decode<D, 4, 2, 8>;
+    if (p.warps == 1) launch = launch_decode<D, 1, 2, 1>;
+    if (p.warps == 8) launch = launch_decode<D, 8, 2, 1>;
+    if constexpr (D < 256)
+        if (p.warps == 16) launch = launch_decode<D, 16, 2, 1>;
     const pa_status s = launch(a, st);
     if (s != PA_OK || p.max_parts <= 1) return s;
     const cudaError_t e = launch_chained(pa_merge_fp4_kernel<D>, dim3((unsigned)(a.num_seqs * a.num_q_heads)),
