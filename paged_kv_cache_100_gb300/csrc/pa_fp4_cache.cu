@@ -500,7 +500,8 @@ __device__ __forceinline__ float2 product_of(uint32_t codes, uint32_t scale) {
 // an entry the keys' by KV head, then the values'.  Each warp takes every kReadWarps-th
 // one.  A lane's unit is 16 bytes of rows; codes, scales and rows of a tile follow one
 // another in the same order, so that its number is its place in each.
-template <typename T>
+// kHalfValues: values become f16, which is what prefill's second product takes.
+template <typename T, bool kHalfValues>
 __global__ void __launch_bounds__(32 * kReadWarps) pa_read_fp4_kernel(const ReadArgs a) {
     constexpr int kUnit = 16 / (int)sizeof(T);           // elements
     grid_dependency_wait();
@@ -568,7 +569,9 @@ __global__ void __launch_bounds__(32 * kReadWarps) pa_read_fp4_kernel(const Read
 #pragma unroll
                 for (int i = 0; i < kUnit / 2; ++i) v[i] = product_of(x[i], sc);
                 uint4 w;
-                if constexpr (kUnit == 4)
+                if (kHalfValues && value)
+                    w = make_uint4(mul_f16x2(x[0], sc), mul_f16x2(x[1], sc), mul_f16x2(x[2], sc), mul_f16x2(x[3], sc));
+                else if constexpr (kUnit == 4)
                     w = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
                 else
                     w = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
@@ -579,7 +582,7 @@ __global__ void __launch_bounds__(32 * kReadWarps) pa_read_fp4_kernel(const Read
     }
 }
 
-template <typename T>
+template <typename T, bool kHalfValues = false>
 pa_status launch_read(ReadArgs &a, cudaStream_t stream) {
     // a CTA has as many tiles as leave sixteen CTAs an SM, one a warp at least
     const int64_t per_seq = (int64_t)a.width * 2 * a.num_kv_heads;
@@ -587,7 +590,7 @@ pa_status launch_read(ReadArgs &a, cudaStream_t stream) {
     const int64_t groups = (per_seq + a.tiles - 1) / a.tiles, grid = a.num_seqs * groups;
     if (grid >= ((int64_t)1 << 31)) return PA_ERR_UNSUPPORTED;
     a.groups = (int)groups;
-    const auto kernel = pa_read_fp4_kernel<T>;
+    const auto kernel = pa_read_fp4_kernel<T, kHalfValues>;
     cudaError_t e = launch_chained(kernel, dim3((unsigned)grid), dim3(32 * kReadWarps), 0, stream, a);
     if (e != cudaSuccess) return cuda_failure(e, "pa_read_fp4_kernel launch");
     count_launches(1);
@@ -794,9 +797,9 @@ extern "C" pa_status pa_prefill_fp4(void *out, const void *query, const void *ke
     a.num_blocks = num_blocks;
     a.width = width;
     a.window = window;
-    const pa_status rc = launch_read<__nv_bfloat16>(a, static_cast<cudaStream_t>(stream));
+    const pa_status rc = launch_read<__nv_bfloat16, true>(a, static_cast<cudaStream_t>(stream));
     if (rc != PA_OK) return rc;
-    return pa_prefill(out, query, a.key_out, a.value_out, a.tables_out, a.lens_out, query_start, num_seqs, num_q_heads,
-                      num_kv_heads, head_dim, block_size, width, (int)staged, num_query_tokens, max_query_len, scale,
-                      PA_DTYPE_BF16, window, w, s.tables, device_status, stream);
+    return prefill_f16_values(out, query, a.key_out, a.value_out, a.tables_out, a.lens_out, query_start, num_seqs, num_q_heads,
+                              num_kv_heads, head_dim, width, (int)staged, num_query_tokens, max_query_len, scale, window, w,
+                              s.tables, device_status, stream);
 }

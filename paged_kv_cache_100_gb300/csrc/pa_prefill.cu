@@ -407,7 +407,8 @@ __device__ __forceinline__ bool group_all(int x, bool v) {
 // every barrier phase is counted across items, so the next item's Q and K/V
 // loads and its first QK^T products start while the last P.V products and the
 // output of the item before are still in flight.
-template <bool kPrefix>
+// kHalfValues: the pool's value rows are f16 already (prefill_f16_values).
+template <bool kPrefix, bool kHalfValues>
 __global__ void __launch_bounds__(kThreads, 1)
     pa_attn_tc_kernel(const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ CUtensorMap kmap,
@@ -774,6 +775,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int k0_tile = (d.blk_lo + 8 * j) * kBlockSize;
                 const bool edge = k0_tile < d.kv_lo || k0_tile + kKv > d.kv_hi;
                 uint4 *vt = reinterpret_cast<uint4 *>(sV + st * kTile);
+                if constexpr (kHalfValues) {
+                    for (int c = ct; edge && c < kTile / 16; c += kConvThreads) {
+                        const int kp = k0_tile + (c % (kHalf / 16)) / 8;
+                        if (kp < d.kv_lo || kp >= d.kv_hi) vt[c] = make_uint4(0, 0, 0, 0);
+                    }
+                } else {
 #pragma unroll 8
                 for (int i = 0; i < kTile / 16 / kConvThreads; ++i) {
                     const int c = ct + i * kConvThreads;
@@ -784,6 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     vt[c] = h;
                     vmax = __hmax2(__hmax2(vmax, abs_f16x2(h.x)),
                                    __hmax2(__hmax2(abs_f16x2(h.y), abs_f16x2(h.z)), abs_f16x2(h.w)));
+                }
                 }
                 // Group 1 keeps no phase of an item without a tile B in step but the drain, which
                 // it waits for by parity: no item drains before the group has left the one
@@ -1154,10 +1162,10 @@ pa_status encode_maps(const void *query, int query_rows, int num_q_heads, int nu
     return PA_OK;
 }
 
-template <bool kPrefix>
+template <bool kPrefix, bool kHalfValues = false>
 pa_status launch_tc(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
                     const PrefillArgs &a, dim3 grid, cudaStream_t stream) {
-    auto kernel = pa_attn_tc_kernel<kPrefix>;
+    auto kernel = pa_attn_tc_kernel<kPrefix, kHalfValues>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kSmemBytes);
     if (e != cudaSuccess) return cuda_failure(e, "cudaFuncSetAttribute(tensor-core attention)");
@@ -1258,14 +1266,14 @@ using namespace pa;
 
 extern "C" size_t pa_prefill_workspace_bytes(void) { return kPrefillWorkspaceBytes; }
 
-extern "C" pa_status pa_prefill(void *out, const void *query, const void *key_cache,
-                                const void *value_cache, const int32_t *block_tables,
-                                const int32_t *context_lens, const int32_t *query_start,
-                                int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
-                                int block_size, int max_blocks_per_seq, int num_blocks,
-                                int num_query_tokens, int max_query_len, float scale,
-                                pa_dtype dtype, int window, void *workspace, size_t workspace_bytes,
-                                int32_t *device_status, void *stream) {
+namespace pa {
+namespace {
+
+pa_status run_prefill(void *out, const void *query, const void *key_cache, const void *value_cache, const int32_t *block_tables,
+                      const int32_t *context_lens, const int32_t *query_start, int num_seqs, int num_q_heads,
+                      int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
+                      int num_query_tokens, int max_query_len, float scale, pa_dtype dtype, int window, bool f16_values,
+                      void *workspace, size_t workspace_bytes, int32_t *device_status, void *stream) {
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || block_size != kBlockSize ||
         max_blocks_per_seq < 0 || num_blocks <= 0 || num_q_heads % num_kv_heads != 0 ||
         num_query_tokens < 0 || max_query_len < 0 || window < 0 || !(scale == scale))
@@ -1314,5 +1322,33 @@ extern "C" pa_status pa_prefill(void *out, const void *query, const void *key_ca
     if (e != cudaSuccess) return cuda_failure(e, "cudaMemsetAsync(prefill ticket)");
     // persistent: one CTA per SM (each holds a whole SM), at most one per item
     const int64_t grid = std::min<int64_t>(items, prefill_sm_count());
-    return launch_tc<false>(qmap, kmap, vmap, a, dim3((unsigned)grid), cs);
+    return f16_values ? launch_tc<false, true>(qmap, kmap, vmap, a, dim3((unsigned)grid), cs)
+                      : launch_tc<false>(qmap, kmap, vmap, a, dim3((unsigned)grid), cs);
+}
+
+}  // namespace
+
+pa_status prefill_f16_values(void *out, const void *query, const void *keys, const void *values, const int32_t *block_tables,
+                             const int32_t *context_lens, const int32_t *query_start, int num_seqs, int num_q_heads,
+                             int num_kv_heads, int head_dim, int max_blocks_per_seq, int num_blocks, int num_query_tokens,
+                             int max_query_len, float scale, int window, void *workspace, size_t workspace_bytes,
+                             int32_t *device_status, void *stream) {
+    return run_prefill(out, query, keys, values, block_tables, context_lens, query_start, num_seqs, num_q_heads, num_kv_heads,
+                       head_dim, kBlockSize, max_blocks_per_seq, num_blocks, num_query_tokens, max_query_len, scale,
+                       PA_DTYPE_BF16, window, true, workspace, workspace_bytes, device_status, stream);
+}
+
+}  // namespace pa
+
+extern "C" pa_status pa_prefill(void *out, const void *query, const void *key_cache,
+                                const void *value_cache, const int32_t *block_tables,
+                                const int32_t *context_lens, const int32_t *query_start,
+                                int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                int block_size, int max_blocks_per_seq, int num_blocks,
+                                int num_query_tokens, int max_query_len, float scale,
+                                pa_dtype dtype, int window, void *workspace, size_t workspace_bytes,
+                                int32_t *device_status, void *stream) {
+    return run_prefill(out, query, key_cache, value_cache, block_tables, context_lens, query_start, num_seqs, num_q_heads,
+                       num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_blocks, num_query_tokens, max_query_len,
+                       scale, dtype, window, false, workspace, workspace_bytes, device_status, stream);
 }
