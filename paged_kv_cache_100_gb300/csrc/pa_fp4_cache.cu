@@ -49,6 +49,9 @@ template <typename T>
 __device__ __forceinline__ double exact_of(const RopeArgs &a, const T *row, int64_t tok, int d) {
     int first, second, pair;
     if (!pair_of(a, d, &first, &second, &pair)) return (double)to_float(row[d]);
+    // At position 0 nothing turns, and bf16 elements often are borders: one such token takes 8 us without sines, 13 to 21 with.
+    if (a.positions[tok] == 0 && isfinite(to_float(row[first])) && isfinite(to_float(row[second])))
+        return (double)to_float(row[d]) * a.factor;
     return exact_turn(to_float(row[first]), to_float(row[second]), d == second, a.positions[tok], a.turns[pair], a.factor);
 }
 
@@ -159,8 +162,8 @@ __device__ __forceinline__ const T *new_row(const RopeArgs &a, bool value, int64
 
 // Two lanes' part of two units, A and B, of a row that is read in whole vectors: the
 // even lane has the first eight elements of each and finds A's scale, the odd one the
-// others and B's.  With halves the units lie head_dim / 2 apart, all of it turned, else
-// they follow one another.  (Half the registers of a thread with both units: 64 leave
+// others and B's.  With halves the units lie rotary_dim / 2 apart, else (and behind
+// rotary_dim) they follow one another.  (Half the registers of a thread with both units: 64 leave
 // the query rows' CTAs of the same kernel 32 warps on an SM.)
 template <typename T, int kMode>
 struct Pair {
@@ -191,8 +194,10 @@ struct Pair {
                 for (int i = 0; i < N; ++i) y[u][v * N + i] = w[i];
             }
         if constexpr (kMode == kHalves) {
-            // (a value's lane that goes along has elements past the table)
-            const float4 *c = reinterpret_cast<const float4 *>(cs + skewed(on ? d[0] : 0));
+            // (elements past rotary_dim and a value's lane that goes along lie past the table)
+            const bool r = on && d[0] < a.rotary_dim / 2;
+            const float4 *c = reinterpret_cast<const float4 *>(cs + skewed(r ? d[0] : 0));
+            turns[0] = turns[1] = r;
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
                 const float4 w = c[i / 2];
@@ -200,8 +205,8 @@ struct Pair {
                 for (int k = 0; k < 2; ++k) {
                     const float p = y[0][i + k], q = y[1][i + k], cosine = k ? w.z : w.x, sine = k ? w.w : w.y;
                     most[0] = max(most[0], __float_as_uint(fabsf(p) + fabsf(q)));
-                    y[0][i + k] = p * cosine - q * sine;
-                    y[1][i + k] = q * cosine + p * sine;
+                    y[0][i + k] = r ? p * cosine - q * sine : p;
+                    y[1][i + k] = r ? q * cosine + p * sine : q;
                 }
             }
             most[1] = most[0];
@@ -241,7 +246,7 @@ struct Pair {
                     for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(y[u][i]));
                     top[u] = __float_as_uint(m);
                 }
-                if (!kTurned || most[u] >= 0x7f800000u) {
+                if (!kTurned || !(__uint_as_float(most[u]) * (float)a.factor < INFINITY)) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) top[u] = max(top[u], __float_as_uint(y[u][i]) & 0x7fffffffu);
                 }
@@ -300,12 +305,17 @@ struct Pair {
             } else {
                 // The codes of the value less and more its error: where they differ (in more than the sign of a
                 // zero) the code comes from 64 bits.  A quotient is at most 6.4 near a border (larger ones saturate).
-                const float eq = (own ? e : other_e) * f + 0x1p-18f;
+                // bf16 elements that are not turned are rounded as above instead: they often are borders.
+                const bool snap = sizeof(T) == 2 && !turns[u];
+                const float eq = snap ? 0.f : (own ? e : other_e) * f + 0x1p-18f, round = snap ? 192.f : 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) lo[i] = fmaf(y[u][i], f, -eq);
+                for (int i = 0; i < 8; ++i) {
+                    y[u][i] = sizeof(T) == 2 ? fmaf(y[u][i], f, round) - round : y[u][i] * f;
+                    lo[i] = y[u][i] - eq;
+                }
                 out = f32x8_to_e2m1x8(lo);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) lo[i] = fmaf(y[u][i], f, eq);
+                for (int i = 0; i < 8; ++i) lo[i] = y[u][i] + eq;
                 const uint32_t above = f32x8_to_e2m1x8(lo);
                 if (out != above)
                     out = exact_codes<T, kTurned>(a, new_row<T>(a, !kTurned, tok, h), tok, d[u], out, above, own ? scale : other_scale);
@@ -391,7 +401,7 @@ __device__ __forceinline__ void encode_tokens(const RopeArgs &a, int cta, float2
             const bool value = row >= a.num_kv_heads;
             const T *src = new_row<T>(a, value, t0 + t, value ? row - a.num_kv_heads : row);
             uint8_t *codes = tile + off * (D / 2), *scales = tile + fp4_scales_at(D) + off * per_row;
-            if (value || half == 0) encode_any<T, false>(a, src, t0 + t, 16 * item, nullptr, codes, scales);
+            if (value || 16 * item >= a.rotary_dim) encode_any<T, false>(a, src, t0 + t, 16 * item, nullptr, codes, scales);
             else encode_any<T, true>(a, src, t0 + t, 16 * item, table + t * table_row, codes, scales);
         }
     } else {
@@ -405,7 +415,7 @@ __device__ __forceinline__ void encode_tokens(const RopeArgs &a, int cta, float2
             at = min(t, nt - 1);
             value = row >= a.num_kv_heads;
             h = value ? row - a.num_kv_heads : row;
-            const bool apart = kMode == kHalves && !value;
+            const bool apart = kMode == kHalves && !value && 32 * (item >> 1) < a.rotary_dim;
             d[0] = (apart ? 16 : 32) * (item >> 1) + 8 * (item & 1);
             d[1] = d[0] + (apart ? half : 16);
             tile = tile_of(&off);
@@ -427,6 +437,74 @@ __device__ __forceinline__ void encode_tokens(const RopeArgs &a, int cta, float2
     }
 }
 
+// The query rows of a CTA's tokens where halves are no whole vectors: a lane keeps up to
+// kPairs pairs, those of its number and every 32nd behind it, and goes through the rows; it
+// alone touches their elements, so that rows may be turned in place.  (8192 tokens of 64 heads of
+// 128 of which 94 elements turn: 121 us, by vectors whose partners are read one by one 171.)
+template <typename T, int kPairs>
+__device__ __forceinline__ void turn_pair_rows(const RopeArgs &a, int cta, float2 *table) {
+    constexpr int kRows = 16 / kPairs;                   // of a warp on their way
+    const int half = a.rotary_dim / 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = cta / a.row_splits, split = cta - group * a.row_splits;
+    const int64_t t0 = (int64_t)group * a.row_tokens;
+    const int nt = (int)min((int64_t)a.row_tokens, a.num_tokens - t0);
+    for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
+        const int t = i / half;
+        table[t * a.table_row + i - t * half] = turn_of(a.positions[t0 + t], a.turns[i - t * half], (float)a.factor);
+    }
+    __syncthreads();
+    const int step = kRopeWarps * a.row_splits;
+    // behind rotary_dim: elements up to a whole vector, then vectors
+    constexpr int N = Vec<T>::N;
+    const int edge = (a.rotary_dim + N - 1) / N * N, odd = edge - a.rotary_dim, vectors = (a.head_dim - edge) / N;
+    const bool copies = a.query != a.query_out;
+    for (int t = 0; t < nt; ++t) {
+        const T *from = static_cast<const T *>(a.query) + (t0 + t) * a.q_stride;
+        T *to = static_cast<T *>(a.query_out) + (t0 + t) * a.q_out_stride;
+        float2 cs[kPairs];
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i)
+            if (lane + 32 * i < half) cs[i] = table[t * a.table_row + lane + 32 * i];
+        for (int r = warp + split * kRopeWarps; r < a.num_q_heads; r += kRows * step) {
+            T x[kRows][kPairs], y[kRows][kPairs], z[kRows];
+#pragma unroll
+            for (int u = 0; u < kRows; ++u)
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i) {
+                    const int p = lane + 32 * i;
+                    if (p >= half || r + u * step >= a.num_q_heads) continue;
+                    const T *row = from + (int64_t)(r + u * step) * a.head_dim;
+                    x[u][i] = row[p];
+                    y[u][i] = row[p + half];
+                }
+#pragma unroll
+            for (int u = 0; u < kRows; ++u)
+                if (copies && lane < odd && r + u * step < a.num_q_heads)
+                    z[u] = from[(int64_t)(r + u * step) * a.head_dim + a.rotary_dim + lane];
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                if (r + u * step >= a.num_q_heads) break;
+                T *out = to + (int64_t)(r + u * step) * a.head_dim;
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i) {
+                    const int p = lane + 32 * i;
+                    if (p >= half) break;
+                    const float x0 = to_float(x[u][i]), x1 = to_float(y[u][i]);
+                    out[p] = from_float<T>(x0 * cs[i].x - x1 * cs[i].y);
+                    out[p + half] = from_float<T>(x1 * cs[i].x + x0 * cs[i].y);
+                }
+                if (copies && lane < odd) out[a.rotary_dim + lane] = z[u];
+            }
+        }
+        if (copies)
+            for (int i = threadIdx.x + split * kRopeThreads; i < a.num_q_heads * vectors; i += kRopeThreads * a.row_splits) {
+                const int r = i / vectors, d = edge + (i - r * vectors) * N;
+                *reinterpret_cast<uint4 *>(to + (int64_t)r * a.head_dim + d) =
+                    *reinterpret_cast<const uint4 *>(from + (int64_t)r * a.head_dim + d);
+            }
+    }
+}
+
 template <typename T, int kMode>
 __global__ void __launch_bounds__(kRopeThreads, kMode == kAny ? 3 : 4) pa_rope_write_fp4_kernel(const __grid_constant__ RopeArgs a) {
     extern __shared__ __align__(16) float2 s_table[];
@@ -435,7 +513,9 @@ __global__ void __launch_bounds__(kRopeThreads, kMode == kAny ? 3 : 4) pa_rope_w
     // the two kinds spread evenly over the grid
     const int before = (int)((uint64_t)blockIdx.x * a.tile_ctas / gridDim.x);
     if ((int)((uint64_t)(blockIdx.x + 1) * a.tile_ctas / gridDim.x) > before) encode_tokens<T, kMode>(a, before, s_table);
-    else turn_rows<T>(a, blockIdx.x - before, s_table, false);
+    else if (a.whole) turn_rows<T>(a, blockIdx.x - before, s_table, false);
+    else if (a.rotary_dim <= 128) turn_pair_rows<T, 2>(a, blockIdx.x - before, s_table);
+    else turn_pair_rows<T, 4>(a, blockIdx.x - before, s_table);
 }
 
 template <typename T>
@@ -446,7 +526,7 @@ pa_status launch_write(RopeArgs &a, cudaStream_t stream) {
     a.tile_tokens = 1;
     while (a.tile_tokens < kMostEncodeTokens && n / (2 * a.tile_tokens) >= 4 * sms) a.tile_tokens *= 2;
     // units in pairs where rows are whole pairs of them and halves are whole units
-    const bool pairs = a.head_dim % 32 == 0 && (half == 0 || a.interleaved || a.rotary_dim == a.head_dim);
+    const bool pairs = a.head_dim % 32 == 0 && (half == 0 || a.interleaved || a.rotary_dim % 32 == 0);
     const int per_pass = kRopeThreads / (a.head_dim / 16);
     const int64_t passes = ((int64_t)a.tile_tokens * 2 * a.num_kv_heads + per_pass - 1) / per_pass;
     a.tile_splits = (int)std::max<int64_t>(1, std::min<int64_t>(passes, 4 * sms * a.tile_tokens / n));

@@ -143,6 +143,28 @@ def test_write_of_many_turned_keys(pkv, dtype, interleaved):
     _same(kc, _written(zero, ref, slots.tolist()), "keys")
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,rot,interleaved", [(128, 64, False), (128, 64, True), (128, 94, True), (128, 94, False), (256, 96, False),
+                                               (160, 32, False), (64, 64, False), (224, 224, True)])
+@pytest.mark.parametrize("scaling,factor", [("none", 1.0), ("by_parts", 32.0)])
+def test_write_of_partly_turned_keys_and_at_position_zero(pkv, D, rot, interleaved, dtype, scaling, factor):
+    """Units that are turned beside units that are not; tokens at position 0, where bf16 elements are borders of codes."""
+    g = torch.Generator().manual_seed(D + rot)
+    T, H = 300, 3
+    k = (torch.randn(T, H, D, generator=g) * torch.exp2(3 * torch.randn(T, H, 1, generator=g))).to(dtype)
+    pos = torch.randint(0, 3000, (T,), generator=g, dtype=torch.int32)
+    pos[::5] = 0
+    rope = pkv.rotary_plan(rot, interleaved=interleaved, scaling=scaling, factor=factor)
+    blocks = 20
+    kc, vc = pkv.fp4_pool(blocks, H, D), pkv.fp4_pool(blocks, H, D)
+    slots = torch.randperm(blocks * 16, generator=g)[:T]
+    pkv.rope_cache_write_fp4(None, k.cuda(), k.cuda(), pos.cuda(), rope, kc, vc, slots.cuda())
+    ref, _ = R.rotate(k.double().numpy(), *_angles(rope, pos.tolist()), interleaved)
+    zero = torch.zeros(kc.shape, dtype=torch.uint8)
+    _same(vc, _written(zero, k.double().numpy(), slots.tolist()), "values")
+    _same(kc, _written(zero, ref, slots.tolist()), "keys")
+
+
 def test_write_of_nan_and_infinity(pkv):
     D = 128
     x = torch.randn(4, 2, D, generator=torch.Generator().manual_seed(3))
