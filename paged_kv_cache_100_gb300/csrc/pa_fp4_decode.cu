@@ -771,11 +771,11 @@ struct Plan {
     bool ordered;                // longest sequences first
 };
 
-// Microseconds that each warp's pair of blocks takes with `ctas` CTAs of `warps` warps on the GPU.  A
+// Microseconds that each warp's pair of blocks takes with `ctas_per_sm` CTAs of `warps` warps on an SM.  A
 // warp alone on its scheduler takes 0.8 us a pair (of 128 elements; its products wait for one
 // another), and the SM 0.44 us for every four warps where many share it.
-double pair_time(double ctas, int warps, int head_dim) {
-    const double k = warps / 4.0 * std::max(1.0, ctas / device_sms()), f = head_dim == 64 ? 0.68 : head_dim == 256 ? 1.5 : 1.0;
+double pair_time(double ctas_per_sm, int warps, int head_dim) {
+    const double k = warps / 4.0 * std::max(1.0, ctas_per_sm), f = head_dim == 64 ? 0.68 : head_dim == 256 ? 1.5 : 1.0;
     return f * (k <= 1 ? 0.8 : k <= 2 ? 1.05 : std::max(1.65, 0.44 * k));
 }
 
@@ -815,7 +815,7 @@ bool plan_of(int num_seqs, int axis, int max_blocks, int window, int partition_s
         parts = std::min(parts, std::max<int64_t>(std::max<int64_t>((target + ctas - 1) / ctas, 8 * target / ctas),
                                                   (span + largest - 1) / largest));
         auto cost = [&](int64_t n, int warps, double base) {             // in n parts, by CTAs of `warps` warps
-            return base + (double)((span + 2 * warps * n - 1) / (2 * warps * n)) * pair_time((double)ctas * n, warps, head_dim);
+            return base + (double)((span + 2 * warps * n - 1) / (2 * warps * n)) * pair_time((double)ctas * n / sms, warps, head_dim);
         };
         double best = parts > 1 ? cost(parts, 4, 5.0 + 0.0058 * std::min((double)ctas * parts, 1024.0)) : INFINITY;
         for (int w = 4; w <= (head_dim == 256 ? 8 : 16); w *= 2)

@@ -166,13 +166,13 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// `count` elements of `type` that begin at byte `at` of a byte tensor, sharing its
+// A tensor of `type` that begins at byte `at` of a byte tensor, sharing its
 // storage (one allocation for several outputs).
-at::Tensor part_of(const at::Tensor &whole, int64_t at, int64_t count, at::ScalarType type) {
+at::Tensor part_of(const at::Tensor &whole, int64_t at, at::IntArrayRef sizes, at::ScalarType type) {
     at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(),
                                                             c10::scalarTypeToTypeMeta(type));
     t.unsafeGetTensorImpl()->set_storage_offset(at / (int64_t)c10::elementSize(type));
-    t.unsafeGetTensorImpl()->set_sizes_contiguous({count});
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
     return t;
 }
 
@@ -219,7 +219,7 @@ PyObject *plan_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
             const at::ScalarType type = i == 2 ? at::kLong : at::kInt;
             const int64_t size = i == 2 ? 8 : 4;
             if (a[7] == Py_None) {
-                out[i] = part_of(whole, at, sizes[i], type);
+                out[i] = part_of(whole, at, {sizes[i]}, type);
                 at = (at + sizes[i] * size + 15) & ~int64_t(15);
             } else if (i == 4 ? out[i].numel() != 1 : out[i].sizes() != at::IntArrayRef{sizes[i]})
                 {
@@ -429,10 +429,15 @@ PyObject *cache_read_fp4(PyObject *, PyObject *const *a, Py_ssize_t n) {
         Place place(dev, a[10]);
         at::Tensor out[2];
         static const char *names[2] = {"key_out", "value_out"};
+        const int64_t sizes[4] = {B * W, pools.hkv, kBlock, pools.head_dim};
+        const int64_t bytes = B * W * pools.hkv * kBlock * pools.head_dim * (type == at::kFloat ? 4 : 2);
+        at::Tensor whole;                // of the new outputs
+        if (a[7] == Py_None || a[8] == Py_None)
+            whole = at::empty({bytes * ((a[7] == Py_None) + (a[8] == Py_None))}, kc.options().dtype(at::kByte));
         for (int i = 0; i < 2; ++i) {
             PyObject *given = a[7 + i];
             if (given == Py_None) {
-                out[i] = at::empty({B * W, pools.hkv, kBlock, pools.head_dim}, kc.options().dtype(type));
+                out[i] = part_of(whole, i == 1 && a[7] == Py_None ? bytes : 0, sizes, type);
                 continue;
             }
             out[i] = tensor(given, names[i]);
