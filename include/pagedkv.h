@@ -734,17 +734,18 @@ pa_status pa_decode_fp4(void *out, const void *query, const void *key_cache,
 
 /*
  * Chunked prefill over 4-bit pools: pa_prefill's semantics, shapes and
- * arithmetic.  The blocks that the chunks attend to are read back once as bf16
- * (exact) into the workspace, where the tensor-core kernel finds them; every tile
- * of 256 query rows and every query head of a group would widen them again.
+ * arithmetic.  The blocks that the chunks attend to are read back once, keys as
+ * bf16 and values as f16 (exact), into the workspace, where the tensor-core kernel
+ * finds them; otherwise every tile of 256 query rows would widen them again.
  *  max_context_len   as in pa_cache_read_fp4: it sizes the workspace
  *  workspace         at least pa_prefill_fp4_workspace_bytes(...) bytes, 16-byte
- *                    aligned (num_seqs * W blocks of bf16 keys and values; calls
+ *                    aligned (num_seqs * W blocks of 16-bit keys and values; calls
  *                    that run at the same time need their own)
  * A sequence whose query_start entries fall, leave [0, num_query_tokens] or
  * exceed its context length, or whose context is longer than max_context_len or its
  * table, is not computed and flagged PA_DEV_BAD_CONTEXT_LEN.
- * A memset and two kernel launches.
+ * A NaN value that a chunk reads may reach all of the chunk's rows.
+ * Two kernel launches.
  */
 size_t pa_prefill_fp4_workspace_bytes(int num_seqs, int num_kv_heads, int head_dim,
                                       int max_blocks_per_seq, int max_context_len);

@@ -561,6 +561,7 @@ struct ReadArgs {
     const int32_t *context_lens;
     const int32_t *query_start;      // nullptr, or chunks whose rows each have their window
     int32_t *tables_out;             // nullptr, or [num_seqs][width]: where each block went
+    uint32_t *ticket;                // nullptr, or a word to be zeroed
     int32_t *lens_out;               // with query_start: the lengths, -1 where a sequence's rows leave the query's
     int32_t *status;
     int num_seqs, num_kv_heads, head_dim;
@@ -596,6 +597,7 @@ __global__ void __launch_bounds__(32 * kReadWarps) pa_read_fp4_kernel(const Read
         if (threadIdx.x == 0 && group == 0) report(a.status, PA_DEV_BAD_CONTEXT_LEN);
         len = len < 0 ? 0 : a.width * kBlockSize;
     }
+    if (blockIdx.x == 0 && threadIdx.x == 0 && a.ticket != nullptr) *a.ticket = 0;
     if (warp == 0 && mine && a.tables_out != nullptr) a.tables_out[b * a.width + j0 + lane] = b * a.width + j0 + lane;
     int64_t chunk = 1;
     if (a.query_start != nullptr) {
@@ -867,6 +869,7 @@ extern "C" pa_status pa_prefill_fp4(void *out, const void *query, const void *ke
     a.query_start = query_start;
     a.tables_out = reinterpret_cast<int32_t *>(w + s.tables);
     a.lens_out = reinterpret_cast<int32_t *>(w + s.lens);
+    a.ticket = reinterpret_cast<uint32_t *>(w);
     a.num_rows = num_query_tokens;
     a.status = device_status;
     a.num_seqs = num_seqs;

@@ -83,7 +83,8 @@ pa_status launch_prefix_tc(const void *query, const void *key_cache, const void 
                            cudaStream_t stream);
 
 // pa_prefill over pools whose keys are bf16 and whose values are f16, as its second
-// product takes them (pa_prefill.cu): what pa_prefill_fp4 stages.
+// product takes them (pa_prefill.cu): what pa_prefill_fp4 stages.  The first word of the
+// workspace is zero when the kernel before on the stream ends.
 pa_status prefill_f16_values(void *out, const void *query, const void *keys, const void *values, const int32_t *block_tables,
                              const int32_t *context_lens, const int32_t *query_start, int num_seqs, int num_q_heads,
                              int num_kv_heads, int head_dim, int max_blocks_per_seq, int num_blocks, int num_query_tokens,

@@ -1317,8 +1317,8 @@ pa_status run_prefill(void *out, const void *query, const void *key_cache, const
     a.num_items = (int)items;
     a.work_counter = static_cast<unsigned int *>(workspace);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    // the ticket counter starts at zero on every call
-    cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(unsigned int), cs);
+    // the ticket counter starts at zero on every call (the kernel that stages f16 values zeroes it)
+    cudaError_t e = f16_values ? cudaSuccess : cudaMemsetAsync(workspace, 0, sizeof(unsigned int), cs);
     if (e != cudaSuccess) return cuda_failure(e, "cudaMemsetAsync(prefill ticket)");
     // persistent: one CTA per SM (each holds a whole SM), at most one per item
     const int64_t grid = std::min<int64_t>(items, prefill_sm_count());
