@@ -12,7 +12,9 @@ library's CUDA kernels.  There is no CPU fallback.
 
 A whole step on the GPU, over E4M3 pools with one scale per block and KV head:
 ``plan_step``, ``rope_cache_write`` (with a ``rotary_plan``), ``decode_block_fp8`` and
-``prefill_block_fp8``; these go through a compiled binding.
+``prefill_block_fp8``; these go through a compiled binding.  Over pools held in 4 bits
+(``fp4_pool``: codes and scales in one tensor): ``rope_cache_write_fp4``, ``decode_fp4``,
+``prefill_fp4``, and ``cache_read_fp4`` to read them back.
 
 Layouts: pools [num_blocks][num_kv_heads][16][head_dim]; query/out
 [num_seqs][num_q_heads][head_dim]; block_tables int32 [num_seqs][max_blocks];

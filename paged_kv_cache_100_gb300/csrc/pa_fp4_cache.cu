@@ -8,7 +8,10 @@
 // else, so a token's row is written without a look at the rest of its block.  Two lanes
 // take two units of a row (a thread one, where rows are not made of pairs of them):
 // they turn the elements, find the scales and the codes, and store 8 bytes of codes and
-// one of scale a unit.  Other CTAs of the launch turn the queries' rows.
+// one of scale a unit.  Other CTAs of the launch turn the queries' rows.  8192 tokens of
+// 64 query and 8 KV heads of 128, 321 MB, 57 us (5.6 TB/s, 0.83 of a copy): the query rows take 48
+// alone and the keys and values 25, mostly arithmetic (440 instructions for the 16 elements of each
+// of 32 lanes), which the rows' traffic hides but for some 10.  64 tokens of 32 KV heads 6 us.
 //   A key's codes and scale are those of its exact rotation: where a 32-bit value
 // lies so near a border of two codes that its error could cross it (or the largest
 // magnitude so near one of two scales) it is computed again in 64 bits.

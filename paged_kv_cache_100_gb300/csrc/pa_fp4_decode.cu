@@ -12,9 +12,19 @@
 // CTAs that follow one another and find the tiles in L2.  Codes times scales are
 // exact in f16.
 //
-// Few sequences: a context is cut into parts so that the GPU is full.  Up to eight
-// parts form a thread-block cluster that merges through distributed shared memory;
-// more parts leave partials in the workspace for a second kernel.
+// Few sequences: a context goes to a CTA of 8 or 16 warps, or is cut into parts so that
+// the GPU is full.  Up to eight parts form a thread-block cluster that merges through
+// distributed shared memory; more leave partials in the workspace for a second kernel.
+// Many ragged ones: CTAs take the longest first.
+//
+// 64 contexts of up to 2048 tokens with 32 KV heads, 315 MB, 62 us (5.1 TB/s, 0.75 of a
+// copy); 256 of up to 4096 with 64 query heads on 8, 701 MB, 132 us (0.79); eight of 32768, 1.21
+// GB, 200 us (0.89).  Bound by instructions before memory: a pair of blocks takes a warp
+// 588, of which 128 conversions and 128 products with scales run at half the issue rate (ALU
+// pipe 0.57 busy, issue slots 0.65).  Four warps with rings of two pairs each were the best
+// shape: 2 and 8 warps 61, 132, 203 and 74, 154, 226 us, rings of three pairs 62, 132, 199, three
+// and five CTAs an SM 66, 140, 208 and 62, 132, 202.  One block at a time took 77, 166 and 232 us,
+// masks in every block's path 72, 150 and 210, sequences in the table's order 65, 140 and 196.
 #include <cuda_runtime.h>
 #include <math.h>
 
