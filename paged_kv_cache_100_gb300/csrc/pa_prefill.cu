@@ -307,6 +307,58 @@ __device__ __forceinline__ void pair_sync(int x, int quarter) {
     asm volatile("bar.sync %0, 64;" ::"r"(5 + 4 * x + quarter) : "memory");
 }
 
+// The same, with the OR of `v` over their threads.
+__device__ __forceinline__ bool pair_any(int x, int quarter, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(5 + 4 * x + quarter)
+        : "memory");
+    return r != 0;
+}
+
+// A thread's columns of O times alpha (a whole warp).
+__device__ __noinline__ void scale_output(uint32_t taddr, float alpha) {
+    const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll 1
+    for (int c = 0; c < kCols; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(taddr + c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            float r0, r1;
+            f2_unpack(f2_mul(f2_pack(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), a2), r0, r1);
+            o[i] = __float_as_uint(r0);
+            o[i + 1] = __float_as_uint(r1);
+        }
+        tmem_st32(taddr + c, o);
+    }
+    tmem_wait_st();
+}
+
+// Four lanes with four rows' chunks q of 16 bytes each, a[4 q ..]: afterwards lane
+// p holds chunk p of the four rows, a[4 i ..] that of row i.
+__device__ __forceinline__ void quad_transpose(uint32_t (&a)[16], int lane) {
+#pragma unroll
+    for (int s = 1; s <= 2; s <<= 1) {
+        const bool up = (lane & s) != 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (q & s) continue;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t send = up ? a[4 * q + k] : a[4 * (q + s) + k];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, send, s);
+                if (up) a[4 * q + k] = got;
+                else a[4 * (q + s) + k] = got;
+            }
+        }
+    }
+}
+
 // The work of one CTA step ("item"): two 128-row Q tiles of one KV head
 // against a range of positions.
 struct Item {
@@ -948,6 +1000,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tmem_wait_st();
                     }
+                    if constexpr (kHalfValues) {
+                        // A reference that rose anywhere in the 32 rows (rare after the first
+                        // steps): the two threads of each row agree on the larger one.
+                        const uint32_t my_sc = sc++;
+                        float psum = csum0 + csum1;
+                        if (pair_any(x, quarter, mref != m_used)) {
+                            const int rp = ex & 1;
+                            ++ex;
+                            red[(rp * kSplit + part) * kRows + r] = mref;
+                            pair_sync(x, quarter);
+                            const float rref = fmaxf(mref, red[(rp * kSplit + (part ^ 1)) * kRows + r]);
+                            if (got) {
+                                // chunks written against a smaller reference are scaled by the exact power
+                                // of two between them; O and l follow, once every P.V of this tile issued
+                                // so far has landed
+                                const float f0 = pow2_diff(cref0, rref), f1 = pow2_diff(cref1, rref);
+                                if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) scale_chunk_weights(s_base, f0, f1);
+                                psum = csum0 * f0 + csum1 * f1;
+                                const float alpha = rref > m_used ? pow2_diff(m_used, rref) : 1.f;
+                                if (j >= 1) {
+                                    if (!warp_wait(&bars[kPvDone + x], (my_sc - 1) & 1, fail, a.status)) ok = false;
+                                    tc_fence_after();
+                                    if (ok) scale_output(o_base, alpha);
+                                }
+                                l *= alpha;
+                                m_used = rref > m_used ? rref : m_used;
+                            }
+                        }
+                        if (!got || !ok) {
+                            ok = false;
+                            continue;
+                        }
+                        l += psum;
+                        tc_fence_before();
+                        mbar_arrive(&bars[kPFull + x]);
+                        continue;
+                    }
                     // the two threads of the row agree on the larger reference
                     const int rp = ex & 1;
                     ++ex;
@@ -1059,6 +1148,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                             reinterpret_cast<float4 *>(a.part_o + prow * kD)[lane] =
                                 stage[(size_t)rr * (kD / 4) + (lane ^ (rr & 31))];
                         }
+                    }
+                } else if (kHalfValues && __all_sync(0xffffffffu, ok) && drained) {
+                    tc_fence_after();
+                    const float inv = l_row == 0.f ? 0.f : 1.f / l_row;
+                    // four lanes exchange their rows' chunks, so that they write 64 bytes of one row
+                    // together: a lane's own row would be written in half sectors, 32 rows at a time
+                    const int64_t out_row =
+                        real ? (int64_t)(d.q0 + tx0 + tr) * a.num_q_heads + d.kvh * g + (r % g) : -1;
+                    int64_t row[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) row[i] = __shfl_sync(0xffffffffu, out_row, (lane & ~3) + i);
+                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + part * kCols + 8 * (lane & 3);
+#pragma unroll 1
+                    for (int c = 0; c < kCols; c += 32) {
+                        uint32_t o[32], w[16];
+                        tmem_ld32(o_base + c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            w[k] = pack2_bf16(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+                        quad_transpose(w, lane);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (row[i] >= 0)
+                                *reinterpret_cast<uint4 *>(out + row[i] * kD + c) =
+                                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                     }
                 } else if (__all_sync(0xffffffffu, ok) && drained) {
                     tc_fence_after();
