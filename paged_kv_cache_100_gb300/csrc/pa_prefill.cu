@@ -698,7 +698,94 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
-        if (lane == 0) {
+        if constexpr (kHalfValues) {
+            // The whole warp runs the loop and one elected lane issues: descriptors then
+            // stay in uniform registers.  (From a one-lane branch, as below, the 70B-shaped
+            // chunked mix took 1175 us, so 1159.)
+            constexpr uint32_t idS = idesc_bf16_f32(kRows, kKv, false);
+            constexpr uint32_t idPV = idesc_f16_f32(kRows, kD, true);
+            const uint64_t q_desc = sw128_desc(smem_u32(sQ), 16, 1024), k_desc = sw128_desc(smem_u32(sK), 16, 1024),
+                           v_desc = sw128_desc(smem_u32(sV), kHalf, 1024);
+            uint32_t gstep = 0;
+            uint32_t pcount[kQT] = {0, 0};
+            bool ok = true;
+            auto issue_s = [&](int x, uint32_t gs) {
+                tc_fence_after();
+                const uint64_t qd = q_desc + (uint64_t)(x * (kTile / 16)), kd = k_desc + (uint64_t)((gs % kStages) * (kTile / 16));
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint64_t o = (uint64_t)((k >> 2) * (kHalf / 16) + (k & 3) * 2);
+                        umma_bf16(tmem + col_s(x), qd + o, kd + o, idS, k > 0 ? 1u : 0u);
+                    }
+                    umma_commit(&bars[kSFull + x]);
+                }
+                __syncwarp();
+            };
+            auto issue_pv = [&](int x, uint32_t gs, int j, int it) -> bool {
+                if (!warp_wait(&bars[kPFull + x], pcount[x] & 1, fail, a.status)) return false;
+                ++pcount[x];
+                // the first P.V of an item overwrites O: the item before must have read it out
+                if (j == 0 && it >= 1 && !warp_wait(&bars[kOFree + x], (it - 1) & 1, fail, a.status)) return false;
+                tc_fence_after();
+                const uint64_t vd = v_desc + (uint64_t)((gs % kStages) * (kTile / 16));
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        umma_bf16_tmem_a(tmem + col_o(x), tmem + col_s(x) + 32 * (k >> 1) + 8 * (k & 1),
+                                         vd + (uint64_t)(k * (2048 / 16)), idPV, (j > 0 || k > 0) ? 1u : 0u);
+                    umma_commit(&bars[kPvDone + x]);
+                }
+                __syncwarp();
+                return true;
+            };
+            auto commit = [&](int bar) {
+                if (elect_one()) umma_commit(&bars[bar]);
+                __syncwarp();
+            };
+            for (int it = 0; ok; ++it) {
+                const int slot = it & 1;
+                const int item = warp_wait(&bars[kItemFull + slot], (it >> 1) & 1, fail, a.status) ? s_item[slot] : -1;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[kItemEmpty + slot]);
+                if (item < 0) break;
+                Item d;
+                describe_item<kPrefix>(a, item, kv_hi_cap, false, d, perm);
+                const int n = d.n_tiles;
+                if (!warp_wait(&bars[kQFull], it & 1, fail, a.status) ||
+                    !warp_wait(&bars[kKFull + gstep % kStages], (gstep / kStages) & 1, fail, a.status))
+                    break;
+                issue_s(0, gstep);
+                if (d.has_b) issue_s(1, gstep);
+                commit(kKEmpty + gstep % kStages);
+                if (n == 1) commit(kQFree);
+                for (int j = 0; j < n; ++j) {
+                    const uint32_t gs = gstep + j, gk = gs + 1;
+                    const bool more = j + 1 < n;
+                    // what is usually there already first: these waits run beside the
+                    // products in flight, the one for P does not
+                    if (!warp_wait(&bars[kVConv + gs % kStages], (gs / kStages) & 1, fail, a.status) ||
+                        (more && !warp_wait(&bars[kKFull + gk % kStages], (gk / kStages) & 1, fail, a.status)) ||
+                        !issue_pv(0, gs, j, it)) {
+                        ok = false;
+                        break;
+                    }
+                    if (more) issue_s(0, gk);
+                    if (d.has_b && !issue_pv(1, gs, j, it)) {
+                        ok = false;
+                        break;
+                    }
+                    commit(kVEmpty + gs % kStages);
+                    if (more) {
+                        if (d.has_b) issue_s(1, gk);
+                        commit(kKEmpty + gk % kStages);
+                        if (j + 2 == n) commit(kQFree);      // the item's last Q K^T is issued
+                    }
+                }
+                commit(kDrain);                              // every MMA of the item has completed once it flips
+                gstep += n;
+            }
+        } else if (lane == 0) {
             constexpr uint32_t idS = idesc_bf16_f32(kRows, kKv, false);
             constexpr uint32_t idPV = idesc_f16_f32(kRows, kD, true);
             const uint32_t q_u = smem_u32(sQ), k_u = smem_u32(sK), v_u = smem_u32(sV);
@@ -1215,7 +1302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) {
         // after a wait that gave up products may still be running: the CTA's memory is
         // theirs until they are done
-        if (lane == 0) {
+        if (kHalfValues ? elect_one() : lane == 0) {
             umma_commit(&bars[kEnd]);
             if (!mbar_wait_bounded(&bars[kEnd], 0)) report(a.status, PA_DEV_TIMEOUT);
         }

@@ -38,6 +38,15 @@ __device__ __forceinline__ void tc_fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // Shared-memory matrix descriptor of a 128-byte-swizzled operand tile (tiles
 // 1024-byte aligned).  K-major: sbo = stride of 8-row groups, lbo unused.
 // MN-major: lbo = stride between 64-element (128-byte) atoms along M/N,
