@@ -260,6 +260,43 @@ __device__ __noinline__ float2 chunk_weights_again(uint32_t taddr, float sl2k, f
     return make_float2(sum, ref);
 }
 
+// The same where some row sees only part of the chunk, or a first attempt summed past the
+// limit: the reference rises where the largest score leaves it 2^10 behind.
+__device__ __noinline__ float2 chunk_weights_general(uint32_t taddr, float sl2k, float ref, int kc, int qpos, int wlo) {
+    const int lo = wlo - kc, hi = qpos - kc;         // attended columns
+    if (__all_sync(0xffffffffu, hi < 0 || lo > 31)) {
+        // past the diagonal (or before the window) for all of the warp's rows
+        uint32_t zero[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) zero[i] = 0u;
+        tmem_st16(taddr, zero);
+        return make_float2(0.f, ref);
+    }
+    uint32_t v[32];
+    tmem_ld32(taddr, v);
+    tmem_wait_ld();
+    float rmax = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const float x = i >= lo && i <= hi ? __uint_as_float(v[i]) * sl2k : -INFINITY;
+        v[i] = __float_as_uint(x);
+        rmax = fmaxf(rmax, x);
+    }
+    if (rmax > ref + 10.f) ref = ceilf(rmax);
+    // before a row has seen anything its weights are 0: any finite reference does
+    const float r = ref == -INFINITY ? 0.f : ref;
+    uint32_t pp[16];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        const float p0 = ex2_approx(__uint_as_float(v[i]) - r), p1 = ex2_approx(__uint_as_float(v[i + 1]) - r);
+        sum += p0 + p1;
+        pp[i >> 1] = pack2_f16(p0, p1);
+    }
+    tmem_st16(taddr, pp);
+    return make_float2(sum, ref);
+}
+
 // Scales the f16 weights of this thread's two 32-column chunks (first 16
 // columns of each, from taddr) by f0 and f1.
 __device__ __noinline__ void scale_chunk_weights(uint32_t taddr, float f0, float f1) {
@@ -1036,6 +1073,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int c = 0; c < kCols; c += 32) {
                             const int kc = k0 + c;
                             const bool masked = chunk_masked(kc);
+                            if constexpr (kHalfValues) {
+                                bool general = masked;
+                                float sum;
+                                if (!general) {
+                                    uint32_t v[32], pp[16];
+                                    tmem_ld32(s_base + c, v);
+                                    tmem_wait_ld();
+                                    const uint64_t nm2 = f2_pack(-mref, -mref);
+                                    uint64_t ps2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+                                    for (int i = 0; i < 32; i += 2) {
+                                        float x0, x1;
+                                        f2_unpack(f2_fma(f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), k2, nm2), x0, x1);
+                                        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                                        ps2[(i >> 1) & 1] = f2_add(ps2[(i >> 1) & 1], f2_pack(p0, p1));
+                                        pp[i >> 1] = pack2_f16(p0, p1);
+                                    }
+                                    float a0, a1, b0, b1;
+                                    f2_unpack(ps2[0], a0, a1);
+                                    f2_unpack(ps2[1], b0, b1);
+                                    sum = (a0 + b0) + (a1 + b1);
+                                    general = __any_sync(0xffffffffu, !(sum <= kChunkSumMax));
+                                    if (!general) tmem_st16(s_base + c, pp);
+                                }
+                                if (general) {           // the whole warp; S is still in place
+                                    const float2 r2 = chunk_weights_general(s_base + c, sl2k, mref, kc, qpos, max(wlo, 0));
+                                    sum = r2.x;
+                                    mref = r2.y;
+                                }
+                                if (c == 0) {
+                                    cref0 = mref;
+                                    csum0 = sum;
+                                } else {
+                                    cref1 = mref;
+                                    csum1 = sum;
+                                }
+                                continue;
+                            }
                             uint32_t pp[16];
                             float sum;
                             {
