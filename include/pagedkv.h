@@ -733,22 +733,26 @@ pa_status pa_decode_fp4(void *out, const void *query, const void *key_cache,
                         int32_t *device_status, void *stream);
 
 /*
- * Chunked prefill over 4-bit pools: pa_prefill's semantics, shapes and
- * arithmetic.  The blocks that the chunks attend to are read back once, keys as
- * bf16 and values as f16 (exact), into the workspace, where the tensor-core kernel
- * finds them; otherwise every tile of 256 query rows would widen them again.
+ * Chunked prefill over 4-bit pools: pa_prefill's semantics and shapes.  Long
+ * chunks: the blocks that they attend to are read back once, keys as bf16 and
+ * values as f16 (exact), into the workspace, where the tensor-core kernel finds
+ * them; otherwise every tile of 256 query rows would widen them again.  Weights are
+ * rounded to f16.  A few rows on long contexts (by estimated time; at most 4096
+ * rows): every row is a row of pa_decode_fp4, with its arithmetic.
  *  max_context_len   as in pa_cache_read_fp4: it sizes the workspace
- *  workspace         at least pa_prefill_fp4_workspace_bytes(...) bytes, 16-byte
- *                    aligned (num_seqs * W blocks of 16-bit keys and values; calls
+ *  workspace         at least pa_prefill_fp4_workspace_bytes(...) bytes for the
+ *                    call's own sizes, 16-byte aligned (num_seqs * W blocks of
+ *                    16-bit keys and values, or decode's partial results; calls
  *                    that run at the same time need their own)
  * A sequence whose query_start entries fall, leave [0, num_query_tokens] or
  * exceed its context length, or whose context is longer than max_context_len or its
  * table, is not computed and flagged PA_DEV_BAD_CONTEXT_LEN.
  * A NaN value that a chunk reads may reach all of the chunk's rows.
- * Two kernel launches.
+ * Two or three kernel launches.
  */
-size_t pa_prefill_fp4_workspace_bytes(int num_seqs, int num_kv_heads, int head_dim,
-                                      int max_blocks_per_seq, int max_context_len);
+size_t pa_prefill_fp4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                      int max_blocks_per_seq, int num_query_tokens,
+                                      int max_query_len, int max_context_len, int window);
 pa_status pa_prefill_fp4(void *out, const void *query, const void *key_cache,
                          const void *value_cache, const int32_t *block_tables,
                          const int32_t *context_lens, const int32_t *query_start, int num_seqs,

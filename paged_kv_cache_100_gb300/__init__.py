@@ -662,9 +662,11 @@ def decode_fp4(query, key_cache, value_cache, block_tables, context_lens, scale=
     return r if out is None else out
 
 
-def prefill_fp4_workspace_bytes(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, max_context_len=None) -> int:
+def prefill_fp4_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, num_query_tokens,
+                                max_query_len, max_context_len=None, window=0) -> int:
     """Scratch ``prefill_fp4`` needs for these sizes."""
-    n = lib().pa_prefill_fp4_workspace_bytes(num_seqs, num_kv_heads, head_dim, max_blocks_per_seq, max_context_len or 0)
+    n = lib().pa_prefill_fp4_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                                             num_query_tokens, max_query_len, max_context_len or 0, window)
     if n == ctypes.c_size_t(-1).value:
         raise ValueError("invalid arguments for pa_prefill_fp4_workspace_bytes")
     return int(n)
@@ -674,8 +676,9 @@ def prefill_fp4(query, key_cache, value_cache, block_tables, context_lens, query
                 max_context_len=None, window=0, out=None, workspace=None, status=None, stream=None):
     """Chunked prefill over pools held in 4 bits (``pa_prefill_fp4``); arguments as ``prefill``.
 
-    The contexts' blocks are read back once into the workspace, of the tables' width or, smaller, that of
-    contexts of ``max_context_len`` tokens.  Returns ``out`` (bf16)."""
+    Long chunks: the contexts' blocks are read back once into the workspace, of the tables' width or, smaller,
+    that of contexts of ``max_context_len`` tokens.  A few rows on long contexts run as rows of ``decode_fp4``.
+    Returns ``out`` (bf16)."""
     if max_query_len is None:
         max_query_len = int((query_start[1:] - query_start[:-1]).max().item()) if query_start.numel() > 1 else 0
     r = _lib.binding().prefill_fp4(query, key_cache, value_cache, block_tables, context_lens, query_start, max_query_len,

@@ -74,7 +74,7 @@ SIGNATURES = {
     "pa_decode_fp4_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32, i32, i32]),
     "pa_decode_fp4": (i32, [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, f32, i32, i32, vp, sz, vp,
                             vp]),
-    "pa_prefill_fp4_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
+    "pa_prefill_fp4_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32, i32, i32, i32]),
     "pa_prefill_fp4": (i32, [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32, i32, f32, i32, vp, sz,
                              vp, vp]),
     "pa_block_copy_scaled": (i32, [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp]),

@@ -692,14 +692,44 @@ bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 // Sizes of head_dim that a pool's rows may have.
 bool pool_head_dim(int head_dim) { return head_dim > 0 && head_dim <= 256 && head_dim % 16 == 0; }
 
-// What prefill stages: the prefill's own workspace, tables, then the blocks.
+// What prefill keeps in its workspace.  By tiles: the tensor-core kernel's own, tables,
+// lengths, then the staged blocks.  By rows: which sequence each row is of and its
+// length, then decode's.
 struct Stage {
+    bool by_rows;
     size_t tables, lens, keys, values, bytes;
 };
-Stage stage_of(int num_seqs, int num_kv_heads, int head_dim, int width) {
+
+// Chunks of a few rows are rows of a decode, each of which reads its context again (from L2):
+// a tile of 256 rows takes a step of 128 positions 1.75 us however few rows it has, on one SM.
+// The estimates that are compared: 12 us, a wave's steps and the staging at 5.5 TB/s;
+// decode's own and 3 us.  Of 63 shapes measured both ways it takes the faster one or is
+// within 2 us of it (us, rows against tiles, 64 query and 8 KV heads): one chunk on 8192
+// tokens of 2 rows 21 : 158, of 64 126 : 166, of 256 404 : 164; 64 chunks on 2048 of
+// 4 rows 125 : 264, of 16 428 : 266.
+constexpr int kMostRows = 4096;
+Stage stage_of(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int width, int num_rows, int max_query_len,
+               int window) {
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    Stage s = {};
+    if (num_rows <= kMostRows) {
+        const int group = num_q_heads / num_kv_heads;
+        const int64_t items = std::min(((int64_t)max_query_len * group + 255) / 256 * num_seqs,
+                                       (int64_t)num_rows * group / 256 + num_seqs) * num_kv_heads;
+        const int64_t seen = window > 0 ? std::min<int64_t>(width, ((int64_t)window + max_query_len) / kBlockSize + 2) : width;
+        const double waves = (double)((items + device_sms() - 1) / device_sms());
+        const double staged = (double)num_seqs * seen * num_kv_heads * 2 * (fp4_tile_bytes(head_dim) + 32.0 * head_dim) / 5.5e6;
+        size_t partials;
+        const double rows = 3.0 + decode_fp4_rows_time(num_rows, num_q_heads, num_kv_heads, head_dim, width, window, &partials);
+        if (rows < 12.0 + staged + waves * (double)((seen + 7) / 8) * 1.75) {
+            s.by_rows = true;
+            s.lens = up((size_t)num_rows * sizeof(int32_t));
+            s.keys = 2 * s.lens;
+            s.bytes = s.keys + partials;
+            return s;
+        }
+    }
     const size_t pool = up((size_t)num_seqs * width * num_kv_heads * kBlockSize * head_dim * 2);
-    Stage s;
     s.tables = up(pa_prefill_workspace_bytes());
     s.lens = s.tables + up((size_t)num_seqs * width * sizeof(int32_t));
     s.keys = s.lens + up((size_t)num_seqs * sizeof(int32_t));
@@ -707,6 +737,36 @@ Stage stage_of(int num_seqs, int num_kv_heads, int head_dim, int width) {
     s.bytes = s.values + pool;
     return s;
 }
+
+// For every row of the query the sequence it is of (-1: none that is computed) and how many
+// positions it attends to.  One CTA; a warp a sequence.
+constexpr int kRowsThreads = 512;
+__global__ void __launch_bounds__(kRowsThreads)
+    pa_rows_fp4_kernel(const int32_t *query_start, const int32_t *context_lens, int32_t *seq_of, int32_t *row_lens, int num_seqs,
+                       int num_rows, int max_query_len, int most, int32_t *status) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    for (int i = threadIdx.x; i < num_rows; i += kRowsThreads) {
+        seq_of[i] = -1;
+        row_lens[i] = 0;
+    }
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    for (int b = threadIdx.x >> 5; b < num_seqs; b += kRowsThreads / 32) {
+        const int from = query_start[b], end = query_start[b + 1], len = context_lens[b];
+        if (from < 0 || end < from || end > num_rows || end - from > len || len > most) {
+            if (lane == 0) report(status, PA_DEV_BAD_CONTEXT_LEN);
+            continue;
+        }
+        const int rows = end - from;
+        if (rows > max_query_len && lane == 0) report(status, PA_DEV_BAD_QUERY_LEN);
+        for (int i = lane; i < min(rows, max_query_len); i += 32) {
+            seq_of[from + i] = b;
+            row_lens[from + i] = len - rows + i + 1;
+        }
+    }
+}
+
 // Blocks of a sequence that are read: max_context_len's, or the table's where it is 0.
 int width_of(int max_blocks_per_seq, int max_context_len) {
     if (max_context_len == 0) return max_blocks_per_seq;
@@ -829,12 +889,15 @@ extern "C" pa_status pa_cache_read_fp4(void *key_out, void *value_out, const voi
     return dtype == PA_DTYPE_F32 ? launch_read<float>(a, st) : launch_read<__nv_bfloat16>(a, st);
 }
 
-extern "C" size_t pa_prefill_fp4_workspace_bytes(int num_seqs, int num_kv_heads, int head_dim, int max_blocks_per_seq,
-                                                 int max_context_len) {
-    if (num_seqs < 0 || num_kv_heads <= 0 || head_dim <= 0 || max_blocks_per_seq < 0 ||
-        max_blocks_per_seq > 0x7fffffff / kBlockSize || max_context_len < 0)
+extern "C" size_t pa_prefill_fp4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                                 int max_blocks_per_seq, int num_query_tokens, int max_query_len,
+                                                 int max_context_len, int window) {
+    if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 || head_dim != 128 ||
+        max_blocks_per_seq < 0 || max_blocks_per_seq > 0x7fffffff / kBlockSize || num_query_tokens < 0 || max_query_len < 0 ||
+        max_context_len < 0 || window < 0)
         return (size_t)-1;
-    return stage_of(num_seqs, num_kv_heads, head_dim, width_of(max_blocks_per_seq, max_context_len)).bytes;
+    return stage_of(num_seqs, num_q_heads, num_kv_heads, head_dim, width_of(max_blocks_per_seq, max_context_len),
+                    num_query_tokens, max_query_len, window).bytes;
 }
 
 extern "C" pa_status pa_prefill_fp4(void *out, const void *query, const void *key_cache, const void *value_cache,
@@ -859,9 +922,20 @@ extern "C" pa_status pa_prefill_fp4(void *out, const void *query, const void *ke
     const int64_t staged = (int64_t)num_seqs * width;
     if ((int64_t)num_kv_heads * 4 * head_dim >= ((int64_t)1 << 30) || staged * num_kv_heads * kBlockSize >= ((int64_t)1 << 31))
         return PA_ERR_UNSUPPORTED;
-    const Stage s = stage_of(num_seqs, num_kv_heads, head_dim, width);
+    const Stage s = stage_of(num_seqs, num_q_heads, num_kv_heads, head_dim, width, num_query_tokens, max_query_len, window);
     if (workspace == nullptr || workspace_bytes < s.bytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
     uint8_t *w = static_cast<uint8_t *>(workspace);
+    if (s.by_rows) {
+        int32_t *seq_of = reinterpret_cast<int32_t *>(w), *row_lens = reinterpret_cast<int32_t *>(w + s.lens);
+        const cudaError_t e = launch_chained(pa_rows_fp4_kernel, dim3(1), dim3(kRowsThreads), 0, static_cast<cudaStream_t>(stream),
+                                             query_start, context_lens, seq_of, row_lens, num_seqs, num_query_tokens,
+                                             max_query_len, width * kBlockSize, device_status);
+        if (e != cudaSuccess) return cuda_failure(e, "pa_rows_fp4_kernel launch");
+        count_launches(1);
+        return decode_fp4_rows(out, query, key_cache, value_cache, block_tables, row_lens, seq_of, num_query_tokens, num_q_heads,
+                               num_kv_heads, head_dim, max_blocks_per_seq, width, num_blocks, scale, window, w + s.keys,
+                               s.bytes - s.keys, device_status, stream);
+    }
     ReadArgs a = {};
     a.key_out = w + s.keys;
     a.value_out = w + s.values;

@@ -50,6 +50,7 @@ struct Fp4Args {
     const int32_t *block_tables;
     const int32_t *context_lens;
     const int32_t *query_start;  // sequence b's row is query_start[b]; nullptr: row b
+    const int32_t *seq_of;       // nullptr, or rows in place of sequences: row b's table is seq_of[b]'s (-1: none)
     float *part_o;               // [(b * Hq + h) * max_parts + part][head_dim]
     float2 *part_ml;             // (reference, sum)
     int32_t *status;
@@ -106,6 +107,7 @@ __device__ __forceinline__ bool span_of(const Fp4Args &a, int len, int part, boo
 // The row of query and output that is sequence b's, or -1: it brings none, or more
 // than the one that a decode step has.
 __device__ __forceinline__ int row_of(const Fp4Args &a, int b, bool say) {
+    if (a.seq_of != nullptr) return a.seq_of[b] < 0 ? -1 : b;
     if (a.query_start == nullptr) return b;
     const int at = a.query_start[b], end = a.query_start[b + 1];
     if (end == at) return -1;
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 1 : 16 / NW) pa_decode_fp4
     // then the table follows it) and the query.  All of it is the warp's own business:
     // no barrier before the merge.
     const int len = a.context_lens[b];
-    const int32_t *row_table = a.block_tables + (int64_t)b * a.max_blocks;
+    const int32_t *row_table = a.block_tables + (int64_t)(a.seq_of != nullptr ? max(a.seq_of[b], 0) : b) * a.max_blocks;
     const bool early = kParts == 1 && a.window == 0;     // the partition does not move with the length
     const int in_part = 2 * (warp + NW * (lane >> 1)) + (lane & 1), ahead = part * a.part_blocks + in_part;
     int first_phys = early && in_part < a.part_blocks && ahead < a.max_blocks ? row_table[ahead] : -1;
@@ -779,6 +781,7 @@ struct Plan {
     int cluster;                 // CTAs of a cluster; > 1: max_parts is 1
     int warps;                   // of a CTA: 4, or without clusters 1, 8 or 16
     bool ordered;                // longest sequences first
+    double time;                 // estimated, in microseconds (partition_size 0)
 };
 
 // Microseconds that each warp's pair of blocks takes with `ctas_per_sm` CTAs of `warps` warps on an SM.  A
@@ -840,6 +843,7 @@ bool plan_of(int num_seqs, int axis, int max_blocks, int window, int partition_s
                 p->cluster = c;
             }
         if (p->cluster > 1) p->warps = 4;
+        p->time = best;
         p->part_blocks = p->cluster > 1 ? (span + p->cluster - 1) / p->cluster + 1 : std::max(1, (int)((span + parts - 1) / parts));
     }
     p->max_parts = p->cluster > 1 ? 1 : std::max(1, (span + p->part_blocks - 1) / p->part_blocks);
@@ -921,19 +925,22 @@ extern "C" size_t pa_decode_fp4_workspace_bytes(int num_seqs, int num_q_heads, i
     return workspace_of(num_seqs, num_q_heads, head_dim, p.max_parts);
 }
 
-extern "C" pa_status pa_decode_fp4(void *out, const void *query, const void *key_cache, const void *value_cache,
-                                   const int32_t *block_tables, const int32_t *context_lens, const int32_t *query_start,
-                                   int num_seqs, int num_query_tokens, int num_q_heads, int num_kv_heads, int head_dim,
-                                   int block_size, int max_blocks_per_seq, int num_blocks, float scale, int window,
-                                   int partition_size, void *workspace, size_t workspace_bytes, int32_t *device_status,
-                                   void *stream) {
+namespace pa {
+namespace {
+
+// max_blocks: entries of a table's row; width: of them, those that contexts reach.
+pa_status run_decode(void *out, const void *query, const void *key_cache, const void *value_cache, const int32_t *block_tables,
+                     const int32_t *context_lens, const int32_t *query_start, const int32_t *seq_of, int num_seqs,
+                     int num_query_tokens, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                     int max_blocks_per_seq, int width, int num_blocks, float scale, int window, int partition_size,
+                     void *workspace, size_t workspace_bytes, int32_t *device_status, void *stream) {
     if (num_seqs < 0 || num_query_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
         block_size != kBlockSize || max_blocks_per_seq < 0 || max_blocks_per_seq > 0x7fffffff / kBlockSize ||
         num_blocks <= 0 || window < 0 || !(scale == scale) || (query_start == nullptr && num_query_tokens != num_seqs))
         return PA_ERR_INVALID_ARG;
     const int group = num_q_heads / num_kv_heads, heads = heads_per_cta(group), splits = group / heads;
     Plan p;
-    if (!plan_of(num_seqs, num_kv_heads * splits, max_blocks_per_seq, window, partition_size, head_dim, &p))
+    if (!plan_of(num_seqs, num_kv_heads * splits, width, window, partition_size, head_dim, &p))
         return PA_ERR_INVALID_ARG;
     if (!head_dim_ok(head_dim)) return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0 || num_query_tokens == 0) return PA_OK;
@@ -954,6 +961,7 @@ extern "C" pa_status pa_decode_fp4(void *out, const void *query, const void *key
     a.block_tables = block_tables;
     a.context_lens = context_lens;
     a.query_start = query_start;
+    a.seq_of = seq_of;
     if (need > 0) {
         a.part_o = static_cast<float *>(workspace);
         a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) +
@@ -975,4 +983,38 @@ extern "C" pa_status pa_decode_fp4(void *out, const void *query, const void *key
     a.scale_log2 = scale * 1.4426950408889634f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return head_dim == 64 ? launch_all<64>(a, p, st) : head_dim == 128 ? launch_all<128>(a, p, st) : launch_all<256>(a, p, st);
+}
+
+}  // namespace
+
+double decode_fp4_rows_time(int num_rows, int num_q_heads, int num_kv_heads, int head_dim, int width, int window,
+                            size_t *workspace_bytes) {
+    const int group = num_q_heads / num_kv_heads;
+    Plan p;
+    plan_of(num_rows, num_kv_heads * (group / heads_per_cta(group)), width, window, 0, head_dim, &p);
+    *workspace_bytes = workspace_of(num_rows, num_q_heads, head_dim, p.max_parts);
+    return p.time;
+}
+
+pa_status decode_fp4_rows(void *out, const void *query, const void *key_cache, const void *value_cache,
+                          const int32_t *block_tables, const int32_t *row_lens, const int32_t *seq_of, int num_rows,
+                          int num_q_heads, int num_kv_heads, int head_dim, int max_blocks_per_seq, int width, int num_blocks,
+                          float scale, int window, void *workspace, size_t workspace_bytes, int32_t *device_status, void *stream) {
+    return run_decode(out, query, key_cache, value_cache, block_tables, row_lens, nullptr, seq_of, num_rows, num_rows,
+                      num_q_heads, num_kv_heads, head_dim, kBlockSize, max_blocks_per_seq, width, num_blocks, scale, window, 0,
+                      workspace, workspace_bytes, device_status, stream);
+}
+
+}  // namespace pa
+
+extern "C" pa_status pa_decode_fp4(void *out, const void *query, const void *key_cache, const void *value_cache,
+                                   const int32_t *block_tables, const int32_t *context_lens, const int32_t *query_start,
+                                   int num_seqs, int num_query_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                   int block_size, int max_blocks_per_seq, int num_blocks, float scale, int window,
+                                   int partition_size, void *workspace, size_t workspace_bytes, int32_t *device_status,
+                                   void *stream) {
+    return run_decode(out, query, key_cache, value_cache, block_tables, context_lens, query_start, nullptr, num_seqs,
+                      num_query_tokens, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
+                      max_blocks_per_seq, num_blocks, scale, window, partition_size, workspace, workspace_bytes,
+                      device_status, stream);
 }

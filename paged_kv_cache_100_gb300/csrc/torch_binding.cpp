@@ -642,7 +642,9 @@ PyObject *prefill_fp4(PyObject *, PyObject *const *a, Py_ssize_t n) {
         Place place(p.dev, a[13]);
         at::Tensor out = output_of(a[10], q, p.dev);
         const size_t need =
-            a[11] != Py_None ? 0 : f_prefill4_bytes(p.num_seqs, p.hkv, p.head_dim, p.max_blocks, longest);
+            a[11] != Py_None ? 0
+                             : f_prefill4_bytes(p.num_seqs, p.hq, p.hkv, p.head_dim, p.max_blocks, int_of(q.size(0), "query"),
+                                                longest_chunk, longest, window);
         at::Tensor w = workspace_of(a[11], need, q, p);
         const pa_status rc = call(f_prefill4, out.data_ptr(), (const void *)p.query, (const void *)p.kc, (const void *)p.vc,
                                   p.tables, p.lens, p_start, p.num_seqs, p.hq, p.hkv, p.head_dim, (int)kBlock, p.max_blocks,

@@ -106,7 +106,7 @@ PREFILL = dict(out=A, query=2 * A, key_cache=3 * A, value_cache=4 * A, tables=7 
     (dict(max_blocks=0), BAD), (dict(max_blocks=1 << 28), BAD), (dict(out=None), BAD), (dict(start=None), BAD),
     (dict(tables=None), BAD), (dict(lens=8 * A + 1), BAD), (dict(query=2 * A + 8), BAD), (dict(dim=64), UNSUPPORTED),
     (dict(hq=6), UNSUPPORTED), (dict(hq=64), UNSUPPORTED), (dict(workspace=None), WORKSPACE),
-    (dict(workspace_bytes=1000), WORKSPACE), (dict(workspace=10 * A + 4), WORKSPACE),
+    (dict(workspace_bytes=500), WORKSPACE), (dict(workspace=10 * A + 4), WORKSPACE),
     (dict(num_seqs=1 << 16, max_blocks=1 << 12), UNSUPPORTED), (dict(num_seqs=0, out=None), OK), (dict(tokens=0, out=None), OK),
     (dict(longest_chunk=0, out=None), OK)])
 def test_prefill_refuses(lib, over, expect):
@@ -115,16 +115,20 @@ def test_prefill_refuses(lib, over, expect):
 
 def test_prefill_workspace(lib):
     f, bad = lib.pa_prefill_fp4_workspace_bytes, ctypes.c_size_t(-1).value
-    block = 2 * 2 * 16 * 128 * 2                                     # keys and values of two heads
-    assert f(3, 2, 128, 10, 0) >= 30 * block and f(3, 2, 128, 10, 33) < 10 * block
-    assert f(3, 2, 128, 10, 33) >= 9 * block and f(3, 2, 128, 10, 1000) == f(3, 2, 128, 10, 0)
-    assert f(1 << 20, 8, 128, 1 << 10, 0) > 1 << 45                  # counted in 64 bits
-    for args in ((-1, 2, 128, 10, 0), (3, 0, 128, 10, 0), (3, 2, 0, 10, 0), (3, 2, 128, -1, 0), (3, 2, 128, 10, -1)):
+    block = 2 * 2 * 16 * 128 * 2                                     # keys and values of two heads, staged
+    long = (4000, 4000)                                              # rows, and of the longest chunk: staged
+    assert f(3, 8, 2, 128, 10, *long, 0, 0) >= 30 * block and f(3, 8, 2, 128, 10, *long, 33, 0) < 10 * block
+    assert f(3, 8, 2, 128, 10, *long, 33, 0) >= 9 * block and f(3, 8, 2, 128, 10, *long, 1000, 0) == f(3, 8, 2, 128, 10, *long, 0, 0)
+    assert f(1 << 20, 8, 8, 128, 1 << 10, 1 << 20, 100, 0, 0) > 1 << 45      # counted in 64 bits
+    assert f(1, 8, 2, 128, 512, 1, 1, 0, 0) < 512 * block            # a few rows: as a decode
+    for args in ((-1, 8, 2, 128, 10, 1, 1, 0, 0), (3, 7, 2, 128, 10, 1, 1, 0, 0), (3, 8, 0, 128, 10, 1, 1, 0, 0),
+                 (3, 8, 2, 64, 10, 1, 1, 0, 0), (3, 8, 2, 128, -1, 1, 1, 0, 0), (3, 8, 2, 128, 10, -1, 1, 0, 0),
+                 (3, 8, 2, 128, 10, 1, -1, 0, 0), (3, 8, 2, 128, 10, 1, 1, -1, 0), (3, 8, 2, 128, 10, 1, 1, 0, -1)):
         assert f(*args) == bad
-    assert pkv.prefill_fp4_workspace_bytes(3, 2, 128, 10, 33) == f(3, 2, 128, 10, 33)
+    assert pkv.prefill_fp4_workspace_bytes(3, 8, 2, 128, 10, *long, 33) == f(3, 8, 2, 128, 10, *long, 33, 0)
     assert pkv.decode_fp4_workspace_bytes(4, 8, 2, 128, 64, 512) == lib.pa_decode_fp4_workspace_bytes(4, 8, 2, 128, 64, 16, 0, 512)
     with pytest.raises(ValueError):
-        pkv.prefill_fp4_workspace_bytes(3, 2, 128, -1)
+        pkv.prefill_fp4_workspace_bytes(3, 8, 2, 128, -1, 1, 1)
     with pytest.raises(ValueError):
         pkv.decode_fp4_workspace_bytes(3, 2, 2, 96, 1)
 

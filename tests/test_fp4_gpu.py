@@ -427,12 +427,14 @@ def _rows(lens, new):
 
 
 @pytest.mark.parametrize("hq,hkv", [(4, 4), (4, 2), (8, 2), (16, 2), (16, 1)])
+@pytest.mark.parametrize("behind", [2, 4096], ids=["rows", "tiles"])     # of more than 4096 rows every chunk is tiles
 @pytest.mark.parametrize("window", [0, 1, 37, 300])
-def test_prefill_matches(pkv, hq, hkv, window):
+def test_prefill_matches(pkv, hq, hkv, window, behind):
     lens, new = [1, 17, 130, 300, 64, 0, 33], [1, 17, 100, 3, 0, 0, 16]
     p = F.Batch(hq + window, lens, hkv, 128)
     dev = p.device()
-    q, status = p.query(sum(new) + 2, hq), _status()
+    q, status = p.query(sum(new) + behind, hq), _status()
+    assert _by_rows(pkv, 7, hq, hkv, 128, 19, len(q), 100, 300, window) == (behind == 2)
     start = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
     if window:
         for b, (n, t) in enumerate(zip(lens, new)):
@@ -446,19 +448,21 @@ def test_prefill_matches(pkv, hq, hkv, window):
     assert (out[n:] == 5).all()
     # blocks of the longest context only
     again = pkv.prefill_fp4(q.cuda(), *dev, start, 100, window=window, max_context_len=300,
-                            workspace=torch.full((pkv.prefill_fp4_workspace_bytes(7, hkv, 128, 19, 300),), 0xFF,
+                            workspace=torch.full((pkv.prefill_fp4_workspace_bytes(7, hq, hkv, 128, 19, n + behind, 100, 300, window),), 0xFF,
                                                  dtype=torch.uint8, device="cuda"))
     assert torch.equal(again[:n], out[:n])
 
 
-def test_prefill_refuses_rows_on_the_device(pkv):
+@pytest.mark.parametrize("behind", [0, 4096], ids=["rows", "tiles"])
+def test_prefill_refuses_rows_on_the_device(pkv, behind):
     """Sequences whose rows leave the query, or whose context is too long, are left out and flagged."""
     lens, new = [40, 40, 40], [10, 10, 10]
     p = F.Batch(1, lens, 1, 128)
     q, dev, status = p.query(30, 4), p.device(), _status()
     ref, bound = p.reference(q.double().numpy(), _rows(lens, new), floor=4.0)
+    q = torch.cat([q, p.query(behind, 4)])
     # (in the last one rows 5 .. 9 are both the first's and the third's)
-    for start, ok, rows in (([0, 10, 20, 31], [0, 1], 10), ([-1, 10, 20, 30], [1, 2], 10), ([0, 10, 5, 15], [0], 5)):
+    for start, ok, rows in (([0, 10, 20, 31 + behind], [0, 1], 10), ([-1, 10, 20, 30], [1, 2], 10), ([0, 10, 5, 15], [0], 5)):
         status.zero_()
         out = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
         pkv.prefill_fp4(q.cuda(), *dev, torch.tensor(start, dtype=torch.int32, device="cuda"), 10, out=out, status=status)
@@ -471,6 +475,67 @@ def test_prefill_refuses_rows_on_the_device(pkv):
     pkv.prefill_fp4(q.cuda(), *dev, torch.tensor([0, 10, 20, 30], dtype=torch.int32, device="cuda"), 10, max_context_len=30,
                     out=out, status=status)
     assert int(status.item()) == 2 and (out == 5).all()
+
+
+def _by_rows(pkv, *args):
+    """Whether these sizes are computed a row at a time: then no block is staged."""
+    return pkv.prefill_fp4_workspace_bytes(*args) < args[0] * args[4] * args[2] * 2 * 16 * 128 * 2
+
+
+@pytest.mark.parametrize("hq,hkv", [(16, 2), (2, 2), (16, 1)])
+@pytest.mark.parametrize("window", [0, 1, 40, 1000])
+def test_prefill_of_few_rows(pkv, hq, hkv, window):
+    """Short chunks on long contexts, as rows of a decode: against the formula and against tiles."""
+    lens, new = [2000, 5, 0, 777, 16, 1600], [3, 5, 0, 1, 4, 8]
+    p = F.Batch(hq + window, lens, hkv, 128)
+    n, dev, status = sum(new), p.device(), _status()
+    assert _by_rows(pkv, 6, hq, hkv, 128, p.tables.shape[1], n + 3, 8, None, window)
+    if window:
+        for b, (m, t) in enumerate(zip(lens, new)):
+            dev[2][b, :max(0, m - t + 1 - window) // 16] = -1
+    q = p.query(n + 4096, hq)
+    start = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    out = torch.full((n + 3, hq, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    few = q[:n + 3].cuda()
+    pkv.prefill_fp4(few, *dev, start, 8, window=window, out=out, status=status)
+    assert int(status.item()) == 0 and (out[n:] == 5).all()
+    ref, bound = p.reference(q[:n].double().numpy(), _rows(lens, new), window=window, floor=4.0)
+    F.check(out[:n], ref, bound, f"{hq}/{hkv} W={window} rows")
+    tiles = pkv.prefill_fp4(q.cuda(), *dev, start, 8, window=window)
+    F.check(tiles[:n], ref, bound, f"{hq}/{hkv} W={window} tiles")
+
+    # captured, replayed, with other lengths behind the same addresses
+    work = torch.full((pkv.prefill_fp4_workspace_bytes(6, hq, hkv, 128, p.tables.shape[1], n + 3, 8, None, window),), 0xFF,
+                      dtype=torch.uint8, device="cuda")
+    graph, held = torch.cuda.CUDAGraph(), torch.zeros_like(out)
+    with torch.cuda.graph(graph):
+        pkv.prefill_fp4(few, *dev, start, 8, window=window, out=held, workspace=work)
+    for _ in range(2):
+        held.fill_(5)
+        work.fill_(0xFF)
+        graph.replay()
+        assert torch.equal(held, out)
+    dev[3][0] = 1990                                                 # rows 0 .. 2 end at 1990 now
+    dev[2][0, :] = dev[2][0, :].clamp(min=0)                         # (the window reaches back further)
+    held.fill_(5)
+    graph.replay()
+    if not window:
+        ref, bound = p.reference(q[:3].double().numpy(), [(0, m) for m in (1987, 1988, 1989)], floor=4.0)
+        F.check(held[:3], ref, bound, "shorter")
+    assert torch.equal(held[3:], out[3:])
+
+
+def test_prefill_of_few_rows_longer_than_said(pkv):
+    """Rows behind max_query_len are flagged and left as they were."""
+    p = F.Batch(3, [900, 900], 2, 128)
+    q, dev, status = p.query(12, 4), p.device(), _status()
+    start = torch.tensor([0, 4, 12], dtype=torch.int32, device="cuda")
+    out = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+    assert _by_rows(pkv, 2, 4, 2, 128, p.tables.shape[1], 12, 6)
+    pkv.prefill_fp4(q.cuda(), *dev, start, 6, out=out, status=status)
+    assert int(status.item()) == 64 and (out[10:] == 5).all()
+    ref, bound = p.reference(q[:10].double().numpy(), _rows([900, 900], [4, 8])[:10], floor=4.0)
+    F.check(out[:10], ref, bound)
 
 
 # ---------------------------------------------------------------------------------------------
