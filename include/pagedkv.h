@@ -716,8 +716,9 @@ pa_status pa_cache_read_fp4(void *key_out, void *value_out, const void *key_cach
  * and stream as in pa_decode_block_fp8.  bfloat16 query and out; head_dim 64, 128
  * or 256; any group (one of more than 8 query heads is split into parts of its
  * largest divisor up to 8, which read the same tiles).
- * Arithmetic: codes times scales are exact; query rows and weights are rounded
- * to f16 as in pa_decode_block_fp8; sums are fp32.  A row that attends to a NaN
+ * Arithmetic: codes times scales are exact; a query row is brought into f16's range
+ * by a power of two (elements below 2^-29 of its largest are off by up to 2^-39 of
+ * it); weights are rounded to f16 as in pa_decode_block_fp8; sums are fp32.  A row that attends to a NaN
  * becomes NaN: in the elements that a NaN value stands for, or whole where a key
  * holds one.  Rows that are not attended may hold anything.
  */

@@ -250,19 +250,12 @@ struct Warp4 {
 #pragma unroll
             for (uint32_t x : {w[c].x, w[c].y, w[c].z, w[c].w})
                 amax = max(amax, max((x << 16) & 0x7fffffffu, x & 0x7fff0000u));
-        if (amax >= 0x47800000u) {                       // 65536 or more: looked at again, as NaN is none of them
-            bool beyond = false;
-#pragma unroll
-            for (int c = 0; c < kKWords; ++c)
-                beyond |= bf16x2_beyond_f16(w[c].x) | bf16x2_beyond_f16(w[c].y) | bf16x2_beyond_f16(w[c].z) | bf16x2_beyond_f16(w[c].w);
-            if (beyond) report(a.status, PA_DEV_RANGE);  // the f16 query is not the query
-        }
         amax = max(amax, __shfl_xor_sync(kFull, amax, 1));
         amax = max(amax, __shfl_xor_sync(kFull, amax, 2));
-        // A row is brought up by a power of two so that its largest magnitude lies in
+        // A row is brought up or down by a power of two so that its largest magnitude lies in
         // [2^14, 2^15): f16 then holds every element exactly but those below 2^-29 of it,
         // which are off by at most 2^-39 of it.
-        const int up = min(max(14 + 127 - (int)(amax >> 23), 0), 126);
+        const int up = min(14 + 127 - (int)(amax >> 23), 126);
         const float f = __uint_as_float((uint32_t)(127 + up) << 23);
         const int down = (127 - up) << 23;               // 2^-up, of row g
         qs0 = __int_as_float(__shfl_sync(kFull, down, 8 * t)) * a.scale_log2;

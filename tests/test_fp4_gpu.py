@@ -371,9 +371,9 @@ def test_decode_status_and_bounds(pkv):
     assert int(status.item()) == 2 and torch.equal(out[0], good[0]) and (out[1] == 0).all()
     status.zero_()
     big = q.clone()
-    big[1, 2, 5] = 65536.0
-    pkv.decode_fp4(big.cuda(), *dev, status=status)
-    assert int(status.item()) == 256
+    big[1, 2, 5] = 65536.0                                           # beyond f16, not beyond a query
+    out = pkv.decode_fp4(big.cuda(), *dev, status=status)
+    assert int(status.item()) == 0 and torch.equal(out[0], good[0]) and bool(torch.isfinite(out).all())
 
 
 @pytest.mark.parametrize("partition", [0, 16])
@@ -523,6 +523,20 @@ def test_prefill_of_few_rows(pkv, hq, hkv, window):
         ref, bound = p.reference(q[:3].double().numpy(), [(0, m) for m in (1987, 1988, 1989)], floor=4.0)
         F.check(held[:3], ref, bound, "shorter")
     assert torch.equal(held[3:], out[3:])
+
+
+@pytest.mark.parametrize("power", [-60, 20, 40, 100])
+def test_queries_of_any_magnitude(pkv, power):
+    """A power of two taken from the scale and given to the query changes no bit, beyond f16's range too."""
+    lens = [300, 33, 700]
+    p = F.Batch(5, lens, 2, 128)
+    dev, q, status = p.device(), p.query(12, 8).cuda(), _status()
+    far = (q.float() * 2.0 ** power).to(torch.bfloat16)
+    for f in (lambda x, scale: pkv.decode_fp4(x[:3], *dev, scale, status=status),
+              lambda x, scale: pkv.prefill_fp4(x, *dev, start, 4, scale, status=status)):
+        start = torch.tensor([0, 4, 8, 12], dtype=torch.int32, device="cuda")
+        assert torch.equal(f(far, 2.0 ** -(4 + power)), f(q, 2.0 ** -4))
+    assert int(status.item()) == 0
 
 
 def test_prefill_of_few_rows_longer_than_said(pkv):
