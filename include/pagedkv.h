@@ -739,7 +739,7 @@ pa_status pa_decode_fp4(void *out, const void *query, const void *key_cache,
  * values as f16 (exact), into the workspace, where the tensor-core kernel finds
  * them; otherwise every tile of 256 query rows would widen them again.  Weights are
  * rounded to f16.  A few rows on long contexts (by estimated time; at most 4096
- * rows): every row is a row of pa_decode_fp4, with its arithmetic.
+ * rows): they are rows of pa_decode_fp4, with its arithmetic, of few heads several at a time.
  *  max_context_len   as in pa_cache_read_fp4: it sizes the workspace
  *  workspace         at least pa_prefill_fp4_workspace_bytes(...) bytes for the
  *                    call's own sizes, 16-byte aligned (num_seqs * W blocks of

@@ -693,20 +693,22 @@ bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 bool pool_head_dim(int head_dim) { return head_dim > 0 && head_dim <= 256 && head_dim % 16 == 0; }
 
 // What prefill keeps in its workspace.  By tiles: the tensor-core kernel's own, tables,
-// lengths, then the staged blocks.  By rows: which sequence each row is of and its
-// length, then decode's.
+// lengths, then the staged blocks.  By rows: chunks of a few rows and their lengths, then
+// decode's.
 struct Stage {
     bool by_rows;
+    int chunks;
     size_t tables, lens, keys, values, bytes;
 };
 
-// Chunks of a few rows are rows of a decode, each of which reads its context again (from L2):
-// a tile of 256 rows takes a step of 128 positions 1.75 us however few rows it has, on one SM.
+// Chunks of a few rows are rows of a decode, each of which (up to eight together, where a group has
+// few heads) reads its context again, from L2: a tile of 256 rows takes a step of 128 positions
+// 1.75 us however few rows it has, on one SM.
 // The estimates that are compared: 12 us, a wave's steps and the staging at 5.5 TB/s;
 // decode's own and 3 us.  Of 63 shapes measured both ways it takes the faster one or is
-// within 2 us of it (us, rows against tiles, 64 query and 8 KV heads): one chunk on 8192
-// tokens of 2 rows 21 : 158, of 64 126 : 166, of 256 404 : 164; 64 chunks on 2048 of
-// 4 rows 125 : 264, of 16 428 : 266.
+// within 10% of it (us, rows against tiles): one chunk on 8192 tokens, 64 query and 8 KV heads,
+// of 2 rows 21 : 156, of 64 128 : 166, of 256 404 : 164; 32 and 8 heads, of 16 29 : 156, of 64 70 : 166;
+// 64 chunks on 2048 of 4 rows, 64 and 8 heads 127 : 264, 32 and 8 70 : 264, 8 and 8 47 : 264.
 constexpr int kMostRows = 4096;
 Stage stage_of(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int width, int num_rows, int max_query_len,
                int window) {
@@ -719,12 +721,15 @@ Stage stage_of(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, in
         const int64_t seen = window > 0 ? std::min<int64_t>(width, ((int64_t)window + max_query_len) / kBlockSize + 2) : width;
         const double waves = (double)((items + device_sms() - 1) / device_sms());
         const double staged = (double)num_seqs * seen * num_kv_heads * 2 * (fp4_tile_bytes(head_dim) + 32.0 * head_dim) / 5.5e6;
+        // a sequence's last chunk may be short
+        const int each = decode_fp4_chunk_rows(num_q_heads, num_kv_heads);
+        s.chunks = (int)std::min<int64_t>(num_rows, (int64_t)num_rows / each + num_seqs);
         size_t partials;
-        const double rows = 3.0 + decode_fp4_rows_time(num_rows, num_q_heads, num_kv_heads, head_dim, width, window, &partials);
+        const double rows = 3.0 + decode_fp4_chunks_time(s.chunks, num_q_heads, num_kv_heads, head_dim, width, window, &partials);
         if (rows < 12.0 + staged + waves * (double)((seen + 7) / 8) * 1.75) {
             s.by_rows = true;
-            s.lens = up((size_t)num_rows * sizeof(int32_t));
-            s.keys = 2 * s.lens;
+            s.lens = up((size_t)s.chunks * sizeof(int4));
+            s.keys = s.lens + up((size_t)s.chunks * sizeof(int32_t));
             s.bytes = s.keys + partials;
             return s;
         }
@@ -738,32 +743,74 @@ Stage stage_of(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, in
     return s;
 }
 
-// For every row of the query the sequence it is of (-1: none that is computed) and how many
-// positions it attends to.  One CTA; a warp a sequence.
+// The chunks, of `each` rows at most, that the sequences' rows are cut into, and how many positions
+// the last row of each attends to; entries of no chunk have -1.  One CTA.
 constexpr int kRowsThreads = 512;
 __global__ void __launch_bounds__(kRowsThreads)
-    pa_rows_fp4_kernel(const int32_t *query_start, const int32_t *context_lens, int32_t *seq_of, int32_t *row_lens, int num_seqs,
-                       int num_rows, int max_query_len, int most, int32_t *status) {
+    pa_rows_fp4_kernel(const int32_t *query_start, const int32_t *context_lens, int4 *chunks, int32_t *chunk_lens, int num_chunks,
+                       int each, int num_seqs, int num_rows, int max_query_len, int most, int32_t *status) {
+    __shared__ int s_sum[kRowsThreads / 32];
     grid_dependency_wait();
     grid_dependents_launch();
-    for (int i = threadIdx.x; i < num_rows; i += kRowsThreads) {
-        seq_of[i] = -1;
-        row_lens[i] = 0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int done = 0;                                        // chunks of the sequences before
+    for (int b0 = 0; b0 < num_seqs; b0 += kRowsThreads) {
+        const int b = b0 + threadIdx.x;
+        int from = 0, rows = 0, len = 0, taken = 0;
+        if (b < num_seqs) {
+            from = query_start[b];
+            len = context_lens[b];
+            const int end = query_start[b + 1];
+            if (from < 0 || end < from || end > num_rows || end - from > len || len > most) {
+                report(status, PA_DEV_BAD_CONTEXT_LEN);
+            } else {
+                rows = end - from;
+                if (rows > max_query_len) report(status, PA_DEV_BAD_QUERY_LEN);
+                taken = min(rows, max_query_len);
+            }
+        }
+        const int n = (taken + each - 1) / each;
+        int before = n;                                  // this sequence's and those of the warp before it
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const int x = __shfl_up_sync(kAll, before, k);
+            before += lane >= k ? x : 0;
+        }
+        if (lane == 31) s_sum[warp] = before;
+        __syncthreads();
+        int all = 0, ahead = 0;
+#pragma unroll
+        for (int w = 0; w < kRowsThreads / 32; ++w) {
+            ahead += w < warp ? s_sum[w] : 0;
+            all += s_sum[w];
+        }
+        const int at = done + ahead + before - n;
+        // chunk c of the sequence that has its first one at `to`
+        auto put = [&](int c, int to, int seq, int first_row, int of_all, int seen) {
+            const int first = c * each, here = min(each, of_all - first);
+            // (more chunks than entries: rows that several sequences claim)
+            if (to + c >= num_chunks) {
+                report(status, PA_DEV_BAD_CONTEXT_LEN);
+                return;
+            }
+            chunks[to + c] = make_int4(seq, first_row + first, here, 0);
+            chunk_lens[to + c] = seen + first + here;
+        };
+        // a few chunks by the sequence's own thread, the others by its warp (64 sequences by the warp alone 6 us
+        // longer, one of 64 chunks by its thread alone 2)
+        constexpr int kOwn = 8;
+        for (int c = 0; c < min(n, kOwn); ++c) put(c, at, b, from, taken, len - rows);
+        for (unsigned left = __ballot_sync(kAll, n > kOwn); left != 0; left &= left - 1) {
+            const int s = __ffs((int)left) - 1, count = __shfl_sync(kAll, n, s), to = __shfl_sync(kAll, at, s);
+            const int s_from = __shfl_sync(kAll, from, s), s_taken = __shfl_sync(kAll, taken, s), seen = __shfl_sync(kAll, len - rows, s);
+            for (int c = kOwn + lane; c < count; c += 32) put(c, to, b - lane + s, s_from, s_taken, seen);
+        }
+        done = min(done + all, num_chunks);
+        __syncthreads();
     }
-    __syncthreads();
-    const int lane = threadIdx.x & 31;
-    for (int b = threadIdx.x >> 5; b < num_seqs; b += kRowsThreads / 32) {
-        const int from = query_start[b], end = query_start[b + 1], len = context_lens[b];
-        if (from < 0 || end < from || end > num_rows || end - from > len || len > most) {
-            if (lane == 0) report(status, PA_DEV_BAD_CONTEXT_LEN);
-            continue;
-        }
-        const int rows = end - from;
-        if (rows > max_query_len && lane == 0) report(status, PA_DEV_BAD_QUERY_LEN);
-        for (int i = lane; i < min(rows, max_query_len); i += 32) {
-            seq_of[from + i] = b;
-            row_lens[from + i] = len - rows + i + 1;
-        }
+    for (int c = done + threadIdx.x; c < num_chunks; c += kRowsThreads) {
+        chunks[c] = make_int4(-1, 0, 0, 0);
+        chunk_lens[c] = 0;
     }
 }
 
@@ -926,15 +973,17 @@ extern "C" pa_status pa_prefill_fp4(void *out, const void *query, const void *ke
     if (workspace == nullptr || workspace_bytes < s.bytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
     uint8_t *w = static_cast<uint8_t *>(workspace);
     if (s.by_rows) {
-        int32_t *seq_of = reinterpret_cast<int32_t *>(w), *row_lens = reinterpret_cast<int32_t *>(w + s.lens);
+        int4 *chunks = reinterpret_cast<int4 *>(w);
+        int32_t *chunk_lens = reinterpret_cast<int32_t *>(w + s.lens);
         const cudaError_t e = launch_chained(pa_rows_fp4_kernel, dim3(1), dim3(kRowsThreads), 0, static_cast<cudaStream_t>(stream),
-                                             query_start, context_lens, seq_of, row_lens, num_seqs, num_query_tokens,
+                                             query_start, context_lens, chunks, chunk_lens, s.chunks,
+                                             decode_fp4_chunk_rows(num_q_heads, num_kv_heads), num_seqs, num_query_tokens,
                                              max_query_len, width * kBlockSize, device_status);
         if (e != cudaSuccess) return cuda_failure(e, "pa_rows_fp4_kernel launch");
         count_launches(1);
-        return decode_fp4_rows(out, query, key_cache, value_cache, block_tables, row_lens, seq_of, num_query_tokens, num_q_heads,
-                               num_kv_heads, head_dim, max_blocks_per_seq, width, num_blocks, scale, window, w + s.keys,
-                               s.bytes - s.keys, device_status, stream);
+        return decode_fp4_chunks(out, query, key_cache, value_cache, block_tables, chunk_lens, chunks, s.chunks,
+                                 num_query_tokens, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, width, num_blocks,
+                                 scale, window, w + s.keys, s.bytes - s.keys, device_status, stream);
     }
     ReadArgs a = {};
     a.key_out = w + s.keys;

@@ -17,6 +17,9 @@
 // distributed shared memory; more leave partials in the workspace for a second kernel.
 // Many ragged ones: CTAs take the longest first.
 //
+// A prefill of short chunks runs here too: where a group has few heads the columns are those of up
+// to eight rows that follow one another, each of which ends a position later.
+//
 // 64 contexts of up to 2048 tokens with 32 KV heads, 315 MB, 62 us (5.1 TB/s, 0.75 of a
 // copy); 256 of up to 4096 with 64 query heads on 8, 701 MB, 132 us (0.79); eight of 32768, 1.21
 // GB, 200 us (0.89).  Bound by instructions before memory: a pair of blocks takes a warp
@@ -26,9 +29,11 @@
 // and five CTAs an SM 66, 140, 208 and 62, 132, 202.  One block at a time took 77, 166 and 232 us,
 // masks in every block's path 72, 150 and 210, sequences in the table's order 65, 140 and 196.
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "pa_device.cuh"
 #include "pa_fp4.cuh"
@@ -50,16 +55,18 @@ struct Fp4Args {
     const int32_t *block_tables;
     const int32_t *context_lens;
     const int32_t *query_start;  // sequence b's row is query_start[b]; nullptr: row b
-    const int32_t *seq_of;       // nullptr, or rows in place of sequences: row b's table is seq_of[b]'s (-1: none)
-    float *part_o;               // [(b * Hq + h) * max_parts + part][head_dim]
+    const int4 *chunks;          // nullptr, or chunks of rows in place of sequences: table's row (-1: none), first row, rows
+    float *part_o;               // [((b * axis + kvh * splits + split) * cols + col) * max_parts + part][head_dim]
     float2 *part_ml;             // (reference, sum)
     int32_t *status;
     int num_seqs, num_rows, num_q_heads, num_kv_heads;
     int heads;                   // query heads of a CTA
+    int cols;                    // its columns: those of up to eight heads, or heads of several rows (a power of two each)
     int splits;                  // CTAs of a (sequence, KV head, partition)
     int max_blocks, num_blocks;
     int part_blocks, max_parts;
     int window;
+    int reach;                   // positions that a row attends to at most
     int ordered;                 // CTAs take sequences longest first
     float scale_log2;
 };
@@ -68,9 +75,9 @@ struct Span {
     int L, start, blk0, nblk, nparts;
 };
 
-// Blocks of a context of `len` tokens: [*first, *blocks), the first position
-// attended in *start; *L the length, clamped.
-__device__ __forceinline__ void range_of(const Fp4Args &a, int len, bool say, int *L, int *start, int *first,
+// Blocks of a context of `len` tokens that its last `rows` tokens attend to: [*first, *blocks),
+// the first position attended in *start; *L the length, clamped.
+__device__ __forceinline__ void range_of(const Fp4Args &a, int len, int rows, bool say, int *L, int *start, int *first,
                                          int *blocks) {
     const int lmax = a.max_blocks * kBlockSize;
     if (len < 0 || len > lmax) {
@@ -78,15 +85,15 @@ __device__ __forceinline__ void range_of(const Fp4Args &a, int len, bool say, in
         len = len < 0 ? 0 : lmax;
     }
     *L = len;
-    *start = a.window > 0 && len > a.window ? len - a.window : 0;
+    *start = max(len - (rows - 1) - a.reach, 0);
     *first = *start / kBlockSize;
     *blocks = (len + kBlockSize - 1) / kBlockSize;
 }
 
 // Part `part` of `parts` of a context, cut evenly.
-__device__ __forceinline__ void even_span(const Fp4Args &a, int len, int part, int parts, bool say, Span &w) {
+__device__ __forceinline__ void even_span(const Fp4Args &a, int len, int rows, int part, int parts, bool say, Span &w) {
     int first, blocks;
-    range_of(a, len, say, &w.L, &w.start, &first, &blocks);
+    range_of(a, len, rows, say, &w.L, &w.start, &first, &blocks);
     const int n = max(blocks - first, 0);
     w.blk0 = first + (int)((int64_t)part * n / parts);
     w.nblk = first + (int)((int64_t)(part + 1) * n / parts) - w.blk0;
@@ -94,9 +101,9 @@ __device__ __forceinline__ void even_span(const Fp4Args &a, int len, int part, i
 }
 
 // Partition `part` of a context of `len` tokens; false when it lies past the end.
-__device__ __forceinline__ bool span_of(const Fp4Args &a, int len, int part, bool say, Span &w) {
+__device__ __forceinline__ bool span_of(const Fp4Args &a, int len, int rows, int part, bool say, Span &w) {
     int first, blocks;
-    range_of(a, len, say, &w.L, &w.start, &first, &blocks);
+    range_of(a, len, rows, say, &w.L, &w.start, &first, &blocks);
     w.nparts = blocks <= first ? 1 : (blocks - first + a.part_blocks - 1) / a.part_blocks;
     if (part >= w.nparts) return false;
     w.blk0 = first + part * a.part_blocks;
@@ -107,7 +114,6 @@ __device__ __forceinline__ bool span_of(const Fp4Args &a, int len, int part, boo
 // The row of query and output that is sequence b's, or -1: it brings none, or more
 // than the one that a decode step has.
 __device__ __forceinline__ int row_of(const Fp4Args &a, int b, bool say) {
-    if (a.seq_of != nullptr) return a.seq_of[b] < 0 ? -1 : b;
     if (a.query_start == nullptr) return b;
     const int at = a.query_start[b], end = a.query_start[b + 1];
     if (end == at) return -1;
@@ -195,6 +201,14 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
         : "memory");
 }
 
+// Column `col`'s (row, head) in query and output, as a number of heads: the heads of the
+// CTA's first row, then of those behind it.
+template <bool kChunks>
+__device__ __forceinline__ int64_t at_of(const Fp4Args &a, int row, int first_head, int col) {
+    const int r = kChunks ? col / a.heads : 0;
+    return (int64_t)(row + r) * a.num_q_heads + first_head + col - r * a.heads;
+}
+
 // One warp's attention state over its blocks: 8 query heads (columns; those past
 // the group have a zero query and are not stored).  Lane (g, t) = (lane / 4, lane %
 // 4) holds scores of tile rows g and g + 8 for heads 2t and 2t + 1.
@@ -207,7 +221,8 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 //  * Tile row r stands for token r, but rows 4, 5 and 6, 7 (and 12 to 15) are
 //    swapped: the four tokens that lanes t = 0 to 3 read together are then two even
 //    and two odd ones, which meet in each bank twice instead of four times.
-template <int D>
+// kChunks: the columns are those of several rows.
+template <int D, bool kChunks>
 struct Warp4 {
     static constexpr int kRow = D / 2;           // bytes of a row's codes
     static constexpr int kScales = D / 16;       // of a row
@@ -225,14 +240,14 @@ struct Warp4 {
     __device__ __forceinline__ int k_at(int w) const { return D == 64 ? 16 * t + 8 * w : 128 * (w / 4) + 32 * t + 8 * (w % 4); }
     __device__ __forceinline__ int v_at(int v) const { return D == 64 ? 8 * g : 128 * (v / 2) + 16 * g + 8 * (v % 2); }
 
-    __device__ __forceinline__ void load(const Fp4Args &a, int row, int first_head, int lane_, uint4 (&w)[kKWords]) {
+    __device__ __forceinline__ void load(const Fp4Args &a, int row, int rows, int first_head, int lane_, uint4 (&w)[kKWords]) {
         lane = lane_;
         g = lane >> 2;
         t = lane & 3;
-        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.query) + ((int64_t)row * a.num_q_heads + first_head + g) * D;
+        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.query) + at_of<kChunks>(a, row, first_head, g) * D;
 #pragma unroll
         for (int c = 0; c < kKWords; ++c)
-            w[c] = g < a.heads ? *reinterpret_cast<const uint4 *>(q + k_at(c)) : make_uint4(0u, 0u, 0u, 0u);
+            w[c] = g < a.heads * rows ? *reinterpret_cast<const uint4 *>(q + k_at(c)) : make_uint4(0u, 0u, 0u, 0u);
     }
 
     __device__ __forceinline__ void init(const Fp4Args &a, const uint4 (&w)[kKWords]) {
@@ -269,7 +284,9 @@ struct Warp4 {
         }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        m0 = m1 = -INFINITY;
+        // (of several rows one may attend to nothing of the first blocks: the least number lets its
+        // weights there, of scores of -infinity, be zero)
+        m0 = m1 = kChunks ? -FLT_MAX : -INFINITY;
         l0 = l1 = 0.f;
     }
 
@@ -350,15 +367,16 @@ struct Warp4 {
         }
     }
 
-    // Two blocks side by side in shared memory (K, V, K, V), of whose 32 rows [nlo, nvalid) are
-    // attended (at least one; nvalid at most 16: the second block is not there, and what its
-    // place holds does not matter).
-    __device__ __forceinline__ void blocks(uint32_t tiles, int nlo, int nvalid) {
+    // Two blocks side by side in shared memory (K, V, K, V), of whose 32 rows the first `limit` are there
+    // (16: what the second block's place holds does not matter), and the last query row of `rows` attends to
+    // `reach` ones before the one numbered `end`, each earlier one to a place less.  (At least one of them attends to one.)
+    __device__ __forceinline__ void blocks(const Fp4Args &a, uint32_t tiles, int end, int limit, int rows) {
         constexpr uint32_t kTile = fp4_tile_bytes(D);
         float s[2][4];
         scores(tiles, 2 * kTile, s);
-        if (nlo > 0 || nvalid < 2 * kBlockSize) {
+        if (end > a.reach || min(limit, end - rows + 1) < 2 * kBlockSize) {
             // rows that are not attended may hold any scale, NaN among them, and would reach the sum as 0 * NaN
+            const int nlo = end - rows + 1 - a.reach, nvalid = min(limit, end);
             if (lane < nlo || lane >= nvalid) {
                 const uint32_t at = tiles + (2 * (lane / kBlockSize) + 1) * kTile + fp4_scales_at(D) + lane % kBlockSize * kScales;
 #pragma unroll
@@ -367,14 +385,14 @@ struct Warp4 {
             fence_proxy_async_smem();
             __syncwarp();
             const int token = g < 4 ? g : g ^ 1;
+            // the rows behind those of columns 2t and 2t + 1
+            const int cut0 = kChunks ? max(rows - 1 - 2 * t / a.heads, 0) : 0, cut1 = kChunks ? max(rows - 1 - (2 * t + 1) / a.heads, 0) : 0;
+            auto outside = [&](int r, int cut) { return r >= min(limit, end - cut) || r < end - cut - a.reach; };
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int r0 = token + u * kBlockSize, r1 = r0 + 8;
-                const bool v0 = r0 >= nlo && r0 < nvalid, v1 = r1 >= nlo && r1 < nvalid;
-                s[u][0] = v0 ? s[u][0] : -INFINITY;
-                s[u][1] = v0 ? s[u][1] : -INFINITY;
-                s[u][2] = v1 ? s[u][2] : -INFINITY;
-                s[u][3] = v1 ? s[u][3] : -INFINITY;
+            for (int i = 0; i < 4; ++i) {                // row token + 8 i
+                float *x = &s[i >> 1][2 * (i & 1)];
+                x[0] = outside(token + 8 * i, cut0) ? -INFINITY : x[0];
+                x[1] = outside(token + 8 * i, cut1) ? -INFINITY : x[1];
             }
         }
         // every lane looks at its own scores; the column's maximum is only found where one rises
@@ -469,7 +487,9 @@ __device__ __forceinline__ float remote_f32(const float *mine, uint32_t rank) {
 }
 
 // kParts > 1: the grid's clusters of kParts CTAs each work on one (sequence, KV head).
-template <int D, int NW, int STAGES, int kParts>
+// kChunks: on chunks of rows (an instance of its own: looking at them cost a single context 1.5 us of
+// 5.4, 256 of them 2 of 132).
+template <int D, int NW, int STAGES, int kParts, bool kChunks>
 __global__ void __launch_bounds__(NW * 32, D == 256 ? 1 : 16 / NW) pa_decode_fp4_kernel(const Fp4Args a) {
     using S = Shape<D, NW, STAGES>;
     constexpr uint32_t kTile = fp4_tile_bytes(D);
@@ -498,19 +518,25 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 1 : 16 / NW) pa_decode_fp4
     // then the table follows it) and the query.  All of it is the warp's own business:
     // no barrier before the merge.
     const int len = a.context_lens[b];
-    const int32_t *row_table = a.block_tables + (int64_t)(a.seq_of != nullptr ? max(a.seq_of[b], 0) : b) * a.max_blocks;
+    int4 chunk = make_int4(b, 0, 1, 0);
+    if constexpr (kChunks) {
+        chunk = a.chunks[b];
+        if (chunk.x < 0) return;                         // (a cluster's CTAs all leave)
+    }
+    const int rows = kChunks ? chunk.z : 1;
+    const int32_t *row_table = a.block_tables + (int64_t)chunk.x * a.max_blocks;
     const bool early = kParts == 1 && a.window == 0;     // the partition does not move with the length
     const int in_part = 2 * (warp + NW * (lane >> 1)) + (lane & 1), ahead = part * a.part_blocks + in_part;
     int first_phys = early && in_part < a.part_blocks && ahead < a.max_blocks ? row_table[ahead] : -1;
     const bool say = threadIdx.x == 0 && part == 0 && idx == 0;
-    const int row = row_of(a, b, say);
+    const int row = kChunks ? chunk.y : row_of(a, b, say);
     if (row < 0) return;                                 // (a cluster's CTAs all leave)
-    Warp4<D> state;
-    uint4 query[Warp4<D>::kKWords];
-    state.load(a, row, first_head, lane, query);
+    Warp4<D, kChunks> state;
+    uint4 query[Warp4<D, kChunks>::kKWords];
+    state.load(a, row, rows, first_head, lane, query);
     Span w;
-    if constexpr (kParts > 1) even_span(a, len, part, kParts, say, w);
-    else if (!span_of(a, len, part, say, w)) return;
+    if constexpr (kParts > 1) even_span(a, len, rows, part, kParts, say, w);
+    else if (!span_of(a, len, rows, part, say, w)) return;
 
     extern __shared__ __align__(128) uint8_t ring[];
     int *entries = reinterpret_cast<int *>(ring + S::kRing);     // physical blocks of the partition
@@ -568,7 +594,7 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 1 : 16 / NW) pa_decode_fp4
             break;
         }
         const int place = place_of(2 * it), tok = (w.blk0 + place) * kBlockSize;
-        state.blocks(smem_u32(my_ring + s * S::kStage), max(0, w.start - tok), min(kBlockSize * min(2, w.nblk - place), w.L - tok));
+        state.blocks(a, smem_u32(my_ring + s * S::kStage), w.L - tok, kBlockSize * min(2, w.nblk - place), rows);
         __syncwarp();
         if (it + STAGES < count) {
             if (lane < 4) fence_proxy_async_smem();
@@ -586,7 +612,8 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 1 : 16 / NW) pa_decode_fp4
     }
     // the ring is idle: the warps' states are merged over it
     float *acc = reinterpret_cast<float *>(my_ring);
-    state.finish(a.heads, acc, s_m + warp * kHeads, s_l + warp * kHeads);
+    const int cols = a.heads * rows;
+    state.finish(cols, acc, s_m + warp * kHeads, s_l + warp * kHeads);
     __syncthreads();
     bool failed = false;
 #pragma unroll
@@ -610,8 +637,13 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 1 : 16 / NW) pa_decode_fp4
         if (failed) sum = __int_as_float(0x7fffffff);
         return O;
     };
-    const int64_t head0 = (int64_t)b * a.num_q_heads + first_head;
+    // the CTA's first column, among the partials and in the output
+    const int64_t col0 = kChunks ? ((int64_t)b * axis + idx) * a.cols : (int64_t)b * a.num_q_heads + first_head;
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + ((int64_t)row * a.num_q_heads + first_head) * D;
+    auto put = [&](int i, float x) {                     // element i of the CTA's columns
+        const int skipped = kChunks ? i / D / a.heads * (a.num_q_heads - a.heads) * D : 0;
+        out[i + skipped] = __float2bfloat16_rn(x);
+    };
     if constexpr (kParts > 1) {
         // The parts' states side by side in the cluster's shared memory: each CTA
         // merges its share of the elements.  A part that gave up keeps its place at
@@ -621,14 +653,14 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 1 : 16 / NW) pa_decode_fp4
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
             const int i = threadIdx.x + e * NW * 32;
-            if (i < a.heads * D) O[e] = merged(i, M[e], sum[e]);
+            if (i < cols * D) O[e] = merged(i, M[e], sum[e]);
         }
         __syncthreads();                                 // the warps' states are read
         float *state_o = reinterpret_cast<float *>(ring), *state_m = s_m, *state_l = s_l;
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
             const int i = threadIdx.x + e * NW * 32;
-            if (i >= a.heads * D) continue;
+            if (i >= cols * D) continue;
             state_o[i] = O[e];
             if (i % D == 0) {
                 state_m[i / D] = M[e];
@@ -636,7 +668,7 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 1 : 16 / NW) pa_decode_fp4
             }
         }
         cluster_sync();
-        for (int i = (int)threadIdx.x + part * NW * 32; i < a.heads * D; i += kParts * NW * 32) {
+        for (int i = (int)threadIdx.x + part * NW * 32; i < cols * D; i += kParts * NW * 32) {
             const int h = i / D;
             float pm[kParts], pl[kParts], po[kParts], top = -INFINITY;
 #pragma unroll
@@ -654,19 +686,19 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 1 : 16 / NW) pa_decode_fp4
                 l = fmaf(f, pl[r], l);
                 o = fmaf(f, po[r], o);
             }
-            out[i] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
+            put(i, l == 0.f ? 0.f : o / l);
         }
         cluster_sync();                                  // no CTA leaves while its state is read
     } else {
         const bool whole = w.nparts == 1;
-        for (int i = threadIdx.x; i < a.heads * D; i += NW * 32) {
+        for (int i = threadIdx.x; i < cols * D; i += NW * 32) {
             float M, sum;
             const float O = merged(i, M, sum);
             if (whole) {
                 // a NaN sum stays NaN; an empty context gives zeros
-                out[i] = __float2bfloat16_rn(sum == 0.f ? 0.f : O / sum);
+                put(i, sum == 0.f ? 0.f : O / sum);
             } else {
-                const int64_t at = (head0 + i / D) * a.max_parts + part;
+                const int64_t at = (col0 + i / D) * a.max_parts + part;
                 a.part_o[at * D + i % D] = O;
                 if (i % D == 0) a.part_ml[at] = make_float2(M, sum);
             }
@@ -674,11 +706,11 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 1 : 16 / NW) pa_decode_fp4
     }
 }
 
-// Merges the partitions of a (sequence, query head) row, one CTA a row: warp w
+// Merges the partitions of a column, one CTA a column: warp w
 // takes partials w, w + kMergeWarps, ..., a lane four of 128 columns, four partials on
 // their way at a time; the warps' sums meet in shared memory.
 constexpr int kMergeWarps = 4;
-template <int D>
+template <int D, bool kChunks>
 __global__ void __launch_bounds__(32 * kMergeWarps) pa_merge_fp4_kernel(const Fp4Args a) {
     constexpr int kVec = D / 4, kPer = (kVec + 31) / 32;         // 16-byte pieces of a row, and of a lane
     __shared__ float4 s_acc[kMergeWarps][kVec];
@@ -688,8 +720,18 @@ __global__ void __launch_bounds__(32 * kMergeWarps) pa_merge_fp4_kernel(const Fp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t row = blockIdx.x;
     Span w;
-    const int b = (int)(row / a.num_q_heads), out_row = row_of(a, b, false);
-    span_of(a, a.context_lens[b], 0, false, w);
+    const int per_seq = kChunks ? a.num_kv_heads * a.splits * a.cols : a.num_q_heads, b = (int)(row / per_seq);
+    const int in_seq = (int)(row - (int64_t)b * per_seq), col = kChunks ? in_seq % a.cols : 0;
+    int rows = 1, out_row;
+    if constexpr (kChunks) {
+        const int4 c = a.chunks[b];
+        out_row = c.x < 0 ? -1 : c.y;
+        rows = c.z;
+        if (col >= a.heads * rows) return;
+    } else {
+        out_row = row_of(a, b, false);
+    }
+    span_of(a, a.context_lens[b], rows, 0, false, w);
     if (w.nparts <= 1 || out_row < 0) return;
     const float2 *ml = a.part_ml + row * a.max_parts;
     const float4 *po = reinterpret_cast<const float4 *>(a.part_o + row * a.max_parts * D);
@@ -754,7 +796,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) pa_merge_fp4_kernel(const Fp
         o.w = fmaf(f, v.w, o.w);
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int64_t out_head = (int64_t)out_row * a.num_q_heads + (row - (int64_t)b * a.num_q_heads);
+    const int64_t out_head = kChunks ? at_of<true>(a, out_row, in_seq / a.cols * a.heads, col) : (int64_t)out_row * a.num_q_heads + in_seq;
     *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + out_head * D + 4 * threadIdx.x) =
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
@@ -860,7 +902,9 @@ size_t workspace_of(int num_seqs, int num_q_heads, int head_dim, int max_parts) 
 template <int D, int NW, int STAGES, int kParts>
 pa_status launch_decode(const Fp4Args &a, cudaStream_t st) {
     using S = Shape<D, NW, STAGES>;
-    auto kernel = pa_decode_fp4_kernel<D, NW, STAGES, kParts>;
+    auto kernel = pa_decode_fp4_kernel<D, NW, STAGES, kParts, false>;
+    if constexpr (D == 128)                              // what prefill takes
+        if (a.chunks != nullptr) kernel = pa_decode_fp4_kernel<D, NW, STAGES, kParts, true>;
     cudaError_t e = allow_smem(kernel, S::smem(kMaxPartition / kBlockSize));
     if (e != cudaSuccess) return cuda_failure(e, "cudaFuncSetAttribute(4-bit decode)");
     cudaLaunchConfig_t cfg = {};
@@ -894,7 +938,10 @@ pa_status launch_all(const Fp4Args &a, const Plan &p, cudaStream_t st) {
         if (p.warps == 16) launch = launch_decode<D, 16, 2, 1>;
     const pa_status s = launch(a, st);
     if (s != PA_OK || p.max_parts <= 1) return s;
-    const cudaError_t e = launch_chained(pa_merge_fp4_kernel<D>, dim3((unsigned)(a.num_seqs * a.num_q_heads)),
+    auto merge = pa_merge_fp4_kernel<D, false>;
+    if constexpr (D == 128)
+        if (a.chunks != nullptr) merge = pa_merge_fp4_kernel<D, true>;
+    const cudaError_t e = launch_chained(merge, dim3((unsigned)(a.num_seqs * a.num_kv_heads * a.splits * a.cols)),
                                          dim3(32 * kMergeWarps), 0, st, a);
     if (e != cudaSuccess) return cuda_failure(e, "pa_merge_fp4_kernel launch");
     count_launches(1);
@@ -921,19 +968,24 @@ extern "C" size_t pa_decode_fp4_workspace_bytes(int num_seqs, int num_q_heads, i
 namespace pa {
 namespace {
 
+// The window that `rows` rows one after another have together.
+int window_of(int window, int rows) { return window > 0 ? std::min(window, INT_MAX - rows) + rows - 1 : 0; }
+
 // max_blocks: entries of a table's row; width: of them, those that contexts reach.
 pa_status run_decode(void *out, const void *query, const void *key_cache, const void *value_cache, const int32_t *block_tables,
-                     const int32_t *context_lens, const int32_t *query_start, const int32_t *seq_of, int num_seqs,
+                     const int32_t *context_lens, const int32_t *query_start, const int4 *chunks, int num_seqs,
                      int num_query_tokens, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                      int max_blocks_per_seq, int width, int num_blocks, float scale, int window, int partition_size,
                      void *workspace, size_t workspace_bytes, int32_t *device_status, void *stream) {
     if (num_seqs < 0 || num_query_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
         block_size != kBlockSize || max_blocks_per_seq < 0 || max_blocks_per_seq > 0x7fffffff / kBlockSize ||
-        num_blocks <= 0 || window < 0 || !(scale == scale) || (query_start == nullptr && num_query_tokens != num_seqs))
+        num_blocks <= 0 || window < 0 || !(scale == scale) ||
+        (query_start == nullptr && chunks == nullptr && num_query_tokens != num_seqs))
         return PA_ERR_INVALID_ARG;
     const int group = num_q_heads / num_kv_heads, heads = heads_per_cta(group), splits = group / heads;
     Plan p;
-    if (!plan_of(num_seqs, num_kv_heads * splits, width, window, partition_size, head_dim, &p))
+    const int rows = chunks != nullptr ? kHeads / heads : 1;     // of a CTA at most
+    if (!plan_of(num_seqs, num_kv_heads * splits, width, window_of(window, rows), partition_size, head_dim, &p))
         return PA_ERR_INVALID_ARG;
     if (!head_dim_ok(head_dim)) return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0 || num_query_tokens == 0) return PA_OK;
@@ -943,8 +995,8 @@ pa_status run_decode(void *out, const void *query, const void *key_cache, const 
         ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens) |
           reinterpret_cast<uintptr_t>(query_start)) & 3u))
         return PA_ERR_INVALID_ARG;
-    if ((int64_t)num_seqs * num_q_heads * p.max_parts * p.cluster >= ((int64_t)1 << 31)) return PA_ERR_UNSUPPORTED;
-    const size_t need = workspace_of(num_seqs, num_q_heads, head_dim, p.max_parts);
+    if ((int64_t)num_seqs * num_q_heads * rows * p.max_parts * p.cluster >= ((int64_t)1 << 31)) return PA_ERR_UNSUPPORTED;
+    const size_t need = workspace_of(num_seqs, num_q_heads * rows, head_dim, p.max_parts);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace))) return PA_ERR_WORKSPACE;
     Fp4Args a = {};
     a.out = out;
@@ -954,11 +1006,11 @@ pa_status run_decode(void *out, const void *query, const void *key_cache, const 
     a.block_tables = block_tables;
     a.context_lens = context_lens;
     a.query_start = query_start;
-    a.seq_of = seq_of;
+    a.chunks = chunks;
     if (need > 0) {
         a.part_o = static_cast<float *>(workspace);
         a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) +
-                                               rows_bytes((int64_t)num_seqs * num_q_heads * p.max_parts, head_dim));
+                                               rows_bytes((int64_t)num_seqs * num_q_heads * rows * p.max_parts, head_dim));
     }
     a.status = device_status;
     a.num_seqs = num_seqs;
@@ -966,12 +1018,14 @@ pa_status run_decode(void *out, const void *query, const void *key_cache, const 
     a.num_q_heads = num_q_heads;
     a.num_kv_heads = num_kv_heads;
     a.heads = heads;
+    a.cols = heads * rows;
     a.splits = splits;
     a.max_blocks = max_blocks_per_seq;
     a.num_blocks = num_blocks;
     a.part_blocks = p.part_blocks;
     a.max_parts = p.max_parts;
     a.window = window;
+    a.reach = window > 0 ? std::min(window, INT_MAX - kHeads) : INT_MAX - kHeads;    // (with a CTA's rows taken off it is an int)
     a.ordered = p.ordered;
     a.scale_log2 = scale * 1.4426950408889634f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -980,22 +1034,25 @@ pa_status run_decode(void *out, const void *query, const void *key_cache, const 
 
 }  // namespace
 
-double decode_fp4_rows_time(int num_rows, int num_q_heads, int num_kv_heads, int head_dim, int width, int window,
-                            size_t *workspace_bytes) {
-    const int group = num_q_heads / num_kv_heads;
+int decode_fp4_chunk_rows(int num_q_heads, int num_kv_heads) { return kHeads / heads_per_cta(num_q_heads / num_kv_heads); }
+
+double decode_fp4_chunks_time(int num_chunks, int num_q_heads, int num_kv_heads, int head_dim, int width, int window,
+                              size_t *workspace_bytes) {
+    const int group = num_q_heads / num_kv_heads, heads = heads_per_cta(group), rows = kHeads / heads;
     Plan p;
-    plan_of(num_rows, num_kv_heads * (group / heads_per_cta(group)), width, window, 0, head_dim, &p);
-    *workspace_bytes = workspace_of(num_rows, num_q_heads, head_dim, p.max_parts);
+    plan_of(num_chunks, num_kv_heads * (group / heads), width, window_of(window, rows), 0, head_dim, &p);
+    *workspace_bytes = workspace_of(num_chunks, num_q_heads * rows, head_dim, p.max_parts);
     return p.time;
 }
 
-pa_status decode_fp4_rows(void *out, const void *query, const void *key_cache, const void *value_cache,
-                          const int32_t *block_tables, const int32_t *row_lens, const int32_t *seq_of, int num_rows,
-                          int num_q_heads, int num_kv_heads, int head_dim, int max_blocks_per_seq, int width, int num_blocks,
-                          float scale, int window, void *workspace, size_t workspace_bytes, int32_t *device_status, void *stream) {
-    return run_decode(out, query, key_cache, value_cache, block_tables, row_lens, nullptr, seq_of, num_rows, num_rows,
-                      num_q_heads, num_kv_heads, head_dim, kBlockSize, max_blocks_per_seq, width, num_blocks, scale, window, 0,
-                      workspace, workspace_bytes, device_status, stream);
+pa_status decode_fp4_chunks(void *out, const void *query, const void *key_cache, const void *value_cache,
+                            const int32_t *block_tables, const int32_t *chunk_lens, const int4 *chunks, int num_chunks,
+                            int num_query_tokens, int num_q_heads, int num_kv_heads, int head_dim, int max_blocks_per_seq,
+                            int width, int num_blocks, float scale, int window, void *workspace, size_t workspace_bytes,
+                            int32_t *device_status, void *stream) {
+    return run_decode(out, query, key_cache, value_cache, block_tables, chunk_lens, nullptr, chunks, num_chunks,
+                      num_query_tokens, num_q_heads, num_kv_heads, head_dim, kBlockSize, max_blocks_per_seq, width, num_blocks,
+                      scale, window, 0, workspace, workspace_bytes, device_status, stream);
 }
 
 }  // namespace pa

@@ -91,14 +91,17 @@ pa_status prefill_f16_values(void *out, const void *query, const void *keys, con
                              int max_query_len, float scale, int window, void *workspace, size_t workspace_bytes,
                              int32_t *device_status, void *stream);
 
-// pa_decode_fp4 for rows of chunks (pa_fp4_decode.cu): row r attends to the first row_lens[r]
-// positions of sequence seq_of[r] (-1: the row is left as it was).  width: table entries
-// that contexts reach.  The first one: its estimated microseconds, and its workspace.
-double decode_fp4_rows_time(int num_rows, int num_q_heads, int num_kv_heads, int head_dim, int width, int window,
-                            size_t *workspace_bytes);
-pa_status decode_fp4_rows(void *out, const void *query, const void *key_cache, const void *value_cache,
-                          const int32_t *block_tables, const int32_t *row_lens, const int32_t *seq_of, int num_rows,
-                          int num_q_heads, int num_kv_heads, int head_dim, int max_blocks_per_seq, int width, int num_blocks,
-                          float scale, int window, void *workspace, size_t workspace_bytes, int32_t *device_status, void *stream);
+// pa_decode_fp4 on chunks of rows in place of sequences: chunk c is chunks[c] = (its table's row or -1: none, its
+// first row of query and output, its rows), of at most decode_fp4_chunk_rows rows that follow one another in their
+// sequence, the last of which attends to chunk_lens[c] tokens; width: the entries of a table's row that contexts
+// reach.  The second one: its estimated microseconds, and its workspace.
+int decode_fp4_chunk_rows(int num_q_heads, int num_kv_heads);
+double decode_fp4_chunks_time(int num_chunks, int num_q_heads, int num_kv_heads, int head_dim, int width, int window,
+                              size_t *workspace_bytes);
+pa_status decode_fp4_chunks(void *out, const void *query, const void *key_cache, const void *value_cache,
+                            const int32_t *block_tables, const int32_t *chunk_lens, const int4 *chunks, int num_chunks,
+                            int num_query_tokens, int num_q_heads, int num_kv_heads, int head_dim, int max_blocks_per_seq,
+                            int width, int num_blocks, float scale, int window, void *workspace, size_t workspace_bytes,
+                            int32_t *device_status, void *stream);
 
 }  // namespace pa

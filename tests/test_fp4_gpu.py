@@ -482,7 +482,7 @@ def _by_rows(pkv, *args):
     return pkv.prefill_fp4_workspace_bytes(*args) < args[0] * args[4] * args[2] * 2 * 16 * 128 * 2
 
 
-@pytest.mark.parametrize("hq,hkv", [(16, 2), (2, 2), (16, 1)])
+@pytest.mark.parametrize("hq,hkv", [(16, 2), (8, 2), (4, 2), (2, 2), (16, 1)])
 @pytest.mark.parametrize("window", [0, 1, 40, 1000])
 def test_prefill_of_few_rows(pkv, hq, hkv, window):
     """Short chunks on long contexts, as rows of a decode: against the formula and against tiles."""
@@ -523,6 +523,35 @@ def test_prefill_of_few_rows(pkv, hq, hkv, window):
         ref, bound = p.reference(q[:3].double().numpy(), [(0, m) for m in (1987, 1988, 1989)], floor=4.0)
         F.check(held[:3], ref, bound, "shorter")
     assert torch.equal(held[3:], out[3:])
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (2, 1), (8, 1)])
+def test_prefill_of_few_rows_in_any_order(pkv, hq, hkv):
+    """Sequences whose rows do not lie in the sequences' order, one of which is refused; and more
+    sequences than a pass of the kernel that cuts the rows takes."""
+    p = F.Batch(8, [600, 40, 90, 333], hkv, 128)
+    q, dev, status = p.query(40, hq), p.device(), _status()
+    start = torch.tensor([20, 33, 0, 17, 19], dtype=torch.int32, device="cuda")     # the second one falls
+    assert _by_rows(pkv, 4, hq, hkv, 128, p.tables.shape[1], 40, 17)
+    out = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+    pkv.prefill_fp4(q.cuda(), *dev, start, 17, out=out, status=status)
+    assert int(status.item()) == 2
+    rows = {20 + i: (0, 587 + i) for i in range(13)} | {i: (2, 73 + i) for i in range(17)} | {17 + i: (3, 331 + i) for i in range(2)}
+    at = sorted(rows)
+    ref, bound = p.reference(q[at].double().numpy(), [rows[i] for i in at], floor=4.0)
+    F.check(out[at], ref, bound)
+    assert (out[[i for i in range(40) if i not in rows]] == 5).all()
+
+    lens = [1 + (7 * i) % 37 for i in range(1100)]
+    new = [min(n, i % 4) for i, n in enumerate(lens)]
+    p = F.Batch(9, lens, hkv, 128)
+    n, dev = sum(new), p.device()
+    q = p.query(n, hq)
+    start = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    assert _by_rows(pkv, 1100, hq, hkv, 128, p.tables.shape[1], n, 3)
+    out = pkv.prefill_fp4(q.cuda(), *dev, start, 3)
+    ref, bound = p.reference(q.double().numpy(), _rows(lens, new), floor=4.0)
+    F.check(out, ref, bound)
 
 
 @pytest.mark.parametrize("power", [-60, 20, 40, 100])
