@@ -747,7 +747,8 @@ pa_status pa_decode_fp4(void *out, const void *query, const void *key_cache,
  *                    that run at the same time need their own)
  * A sequence whose query_start entries fall, leave [0, num_query_tokens] or
  * exceed its context length, or whose context is longer than max_context_len or its
- * table, is not computed and flagged PA_DEV_BAD_CONTEXT_LEN.
+ * table, is not computed and flagged PA_DEV_BAD_CONTEXT_LEN.  Of a chunk longer than
+ * max_query_len (flagged PA_DEV_BAD_QUERY_LEN) the rows behind it may be left out.
  * A NaN value that a chunk reads may reach all of the chunk's rows.
  * Two or three kernel launches.
  */
