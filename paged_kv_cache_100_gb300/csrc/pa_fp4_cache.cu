@@ -181,7 +181,9 @@ struct Pair {
 #pragma unroll
             for (int v = 0; v < V; ++v) raw[u][v] = reinterpret_cast<const uint4 *>(row + (u ? d1 : d0))[v];
     }
-    // tile: where the row's block goes; nullptr: nothing is written.  cs: the token's row of the table.  Whole warps.
+    // tile: where the row's block goes; nullptr: nothing is written.  cs: the token's row of the table.  kValue: the
+    // rows are values.  Whole warps.
+    template <bool kValue>
     __device__ __forceinline__ void encode(const RopeArgs &a, int64_t tok, int h, const int (&d)[2], const float2 *cs, uint8_t *tile,
                                            int off) const {
         const bool odd = (threadIdx.x & 1) != 0, on = tile != nullptr;
@@ -322,7 +324,7 @@ struct Pair {
                 for (int i = 0; i < 8; ++i) lo[i] = y[u][i] + eq;
                 const uint32_t above = f32x8_to_e2m1x8(lo);
                 if (out != above)
-                    out = exact_codes<T, kTurned>(a, new_row<T>(a, !kTurned, tok, h), tok, d[u], out, above, own ? scale : other_scale);
+                    out = exact_codes<T, kTurned>(a, new_row<T>(a, kValue, tok, h), tok, d[u], out, above, own ? scale : other_scale);
             }
             *reinterpret_cast<uint32_t *>(codes + d[u] / 2) = isnan(f) ? 0u : out;
             if (own) tile[fp4_scales_at(D) + off * (D / 16) + d[u] / 16] = (uint8_t)byte;
@@ -430,9 +432,9 @@ __device__ __forceinline__ void encode_tokens(const RopeArgs &a, int cta, float2
         for (;;) {
             const bool any_key = __any_sync(kAll, tile != nullptr && !value), any_value = __any_sync(kAll, tile != nullptr && value);
             if (any_value)
-                reinterpret_cast<const Pair<T, kPlain> &>(x).encode(a, t0 + at, h, d, nullptr, value ? tile : nullptr, off);
+                reinterpret_cast<const Pair<T, kPlain> &>(x).template encode<true>(a, t0 + at, h, d, nullptr, value ? tile : nullptr, off);
             __syncwarp();
-            if (any_key) x.encode(a, t0 + at, h, d, table + at * table_row, value ? nullptr : tile, off);
+            if (any_key) x.template encode<false>(a, t0 + at, h, d, table + at * table_row, value ? nullptr : tile, off);
             __syncwarp();
             next();
             if (!__any_sync(kAll, place < per_pass && t < nt)) break;

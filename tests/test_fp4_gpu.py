@@ -165,6 +165,27 @@ def test_write_of_partly_turned_keys_and_at_position_zero(pkv, D, rot, interleav
     _same(kc, _written(zero, ref, slots.tolist()), "keys")
 
 
+def test_write_of_unturned_f32_keys_beside_other_values(pkv):
+    """Elements on and beside the borders of codes, in keys that are not the values: each row's codes are its own."""
+    g = torch.Generator().manual_seed(21)
+    T, H, D = 200, 3, 64
+    tie = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    scale = torch.from_numpy(F.SCALES[8:0xE2])[torch.randint(0, 0xE2 - 8, (T, H, D // 16, 1), generator=g)].float()
+    k = tie[torch.randint(0, 7, (T, H, D // 16, 16), generator=g)] * scale
+    k *= torch.randint(0, 2, k.shape, generator=g) * 2 - 1
+    beside = torch.randint(0, 3, k.shape, generator=g)
+    k = torch.where(beside == 0, torch.nextafter(k, k * 2), torch.where(beside == 1, torch.nextafter(k, k * 0), k))
+    k[..., 0] = 6 * scale[..., 0]
+    k = k.reshape(T, H, D)
+    v = torch.randn(T, H, D, generator=g)
+    blocks = -(-T // 16)
+    kc, vc = pkv.fp4_pool(blocks, H, D), pkv.fp4_pool(blocks, H, D)
+    pkv.rope_cache_write_fp4(None, k.cuda(), v.cuda(), None, None, kc, vc, torch.arange(T).cuda())
+    zero = torch.zeros(kc.shape, dtype=torch.uint8)
+    _same(vc, _written(zero, v.double().numpy(), range(T)), "values")
+    _same(kc, _written(zero, k.double().numpy(), range(T)), "keys")
+
+
 def test_write_of_nan_and_infinity(pkv):
     D = 128
     x = torch.randn(4, 2, D, generator=torch.Generator().manual_seed(3))
