@@ -57,20 +57,33 @@ __device__ __forceinline__ double exact_of(const RopeArgs &a, const T *row, int6
     return exact_turn(to_float(row[first]), to_float(row[second]), d == second, a.positions[tok], a.turns[pair], a.factor);
 }
 
-// The largest magnitude in 64 bits of those elements from d0 on that `which` has, which the
-// unit's others do not reach.  (An element takes more than a microsecond: 64-bit units are few.  With all
+// The larger of two magnitudes; NaN where one is.
+__device__ __forceinline__ double larger(double a, double b) { return isnan(a) ? a : isnan(b) ? b : fmax(a, b); }
+
+// The largest magnitude in 64 bits (NaN where one of them is) of those elements from d0 on that
+// `which` has, which the unit's others do not reach.  (An element takes more than a microsecond: 64-bit units are few.  With all
 // 16 of a unit 8192 tokens of 8 KV heads took 43 us, as one CTA had such a unit; with these 24.)
 template <typename T>
 __device__ __noinline__ double exact_top(const RopeArgs &a, const T *row, int64_t tok, int d0, uint32_t which) {
     double top = 0.0;
-    for (; which != 0; which &= which - 1) top = fmax(top, fabs(exact_of<T>(a, row, tok, d0 + __ffs((int)which) - 1)));
+    for (; which != 0; which &= which - 1) top = larger(top, fabs(exact_of<T>(a, row, tok, d0 + __ffs((int)which) - 1)));
     return top;
+}
+
+// Error of elements turned in 32 bits from pairs of |x0| + |x1| up to `most`: infinite where one of them
+// may leave f32's range on the way, so that the whole unit is found in 64 bits, which no f32 pair leaves.
+__device__ __forceinline__ float turn_error(const RopeArgs &a, float most) {
+    const float f = (float)a.factor;
+    return most * f >= 0x1p127f ? INFINITY : most * (kTurnError * f);
 }
 
 // Midway between the magnitudes of codes c and c + 1, c at most 6.
 __device__ __forceinline__ float code_border(uint32_t c) {
     return c < 4 ? 0.25f + 0.5f * (float)c : c == 4 ? 2.5f : c == 5 ? 3.5f : 5.f;
 }
+
+// Eight codes of -6 and of 6: `below` and `above` where nothing is known.
+constexpr uint32_t kAllLow = 0xffffffffu, kAllHigh = 0x77777777u;
 
 // Eight codes, of which `below` and `above` differ in some, from element d on of a row: those in 64 bits.
 template <typename T, bool kTurned>
@@ -105,17 +118,25 @@ __device__ __forceinline__ void encode16(const RopeArgs &a, const T *row, int64_
     uint32_t top = 0;                                    // as bits: magnitudes compare like integers, NaN above all
 #pragma unroll
     for (int k = 0; k < 16; ++k) top = max(top, __float_as_uint(y[k]) & 0x7fffffffu);
-    if (top > 0x7f800000u) {
+    const float amax = __uint_as_float(top), e = kTurned ? turn_error(a, most) : 0.f;     // error of an element
+    const bool wild = kTurned && e == INFINITY;
+    bool nan = top > 0x7f800000u;
+    float border = 0.f;
+    uint32_t byte = fp4_scale_of(amax, amax, &border);
+    if (wild) {
+        const double exact = exact_top<T>(a, row, tok, d0, 0xffffu);
+        nan = isnan(exact);
+        byte = fp4_scale_of<double>((float)exact, exact, &border);
+        if (exact > (double)kFp4Top) report(a.status, PA_DEV_RANGE);
+    } else if (!nan && amax > kFp4Top) {
+        report(a.status, PA_DEV_RANGE);
+    }
+    if (nan) {
         *reinterpret_cast<uint2 *>(codes) = make_uint2(0u, 0u);
         *scale_at = (uint8_t)kFp4NanScale;
         return;
     }
-    const float amax = __uint_as_float(top);
-    if (amax > kFp4Top) report(a.status, PA_DEV_RANGE);
-    float border;
-    uint32_t byte = fp4_scale_of(amax, amax, &border);
-    const float e = kTurned ? most * (kTurnError * (float)a.factor) : 0.f;       // error of an element
-    if (kTurned && most > 0.f && (fabsf(amax - border) <= e || amax <= e)) {
+    if (kTurned && !wild && most > 0.f && (fabsf(amax - border) <= e || amax <= e)) {
         uint32_t which = 0;
 #pragma unroll
         for (int k = 0; k < 16; ++k) which |= fabsf(y[k]) >= amax - 2.f * e ? 1u << k : 0u;
@@ -144,7 +165,8 @@ __device__ __forceinline__ void encode16(const RopeArgs &a, const T *row, int64_
         if constexpr (!kSnapped) {
             // The codes of the value less and more its error: where they differ (in more than the
             // sign of a zero) the code comes from 64 bits.
-            const uint32_t above = f32x8_to_e2m1x8(hi);
+            uint32_t above = f32x8_to_e2m1x8(hi);
+            if (wild) out[p] = kAllLow, above = kAllHigh;
             if (out[p] != above) out[p] = exact_codes<T, kTurned>(a, row, tok, d0 + 8 * p, out[p], above, scale);
         }
     }
@@ -263,28 +285,34 @@ struct Pair {
         float e = 0.f;                                   // error of an element of the lane's own unit
         if constexpr (kTurned) {
             const uint32_t m0 = turns[0] ? most[0] : 0u, m1 = turns[1] ? most[1] : 0u;
-            e = __uint_as_float(max(odd ? m1 : m0, __shfl_xor_sync(kAll, odd ? m0 : m1, 1))) * (kTurnError * (float)a.factor);
+            e = turn_error(a, __uint_as_float(max(odd ? m1 : m0, __shfl_xor_sync(kAll, odd ? m0 : m1, 1))));
         }
         const float amax = __uint_as_float(mine);
-        const bool nan = mine > 0x7f800000u;
-        float border;
+        const bool nan = mine > 0x7f800000u, wild = kTurned && e == INFINITY;
+        float border = 0.f;
         uint32_t byte = nan ? kFp4NanScale : fp4_scale_of(amax, amax, &border);
-        if (!nan && amax > kFp4Top && on) report(a.status, PA_DEV_RANGE);
+        if (!nan && amax > kFp4Top && on && !wild) report(a.status, PA_DEV_RANGE);
         if constexpr (kTurned) {
-            const bool unsure = !nan && e > 0.f && on && (fabsf(amax - border) <= e || amax <= e);
+            const bool unsure = on && (wild || (!nan && e > 0.f && (fabsf(amax - border) <= e || amax <= e)));
             if (__any_sync(kAll, unsure)) {
-                // both lanes' elements that may be the largest, in 64 bits
-                const float floor = unsure ? amax - 2.f * e : INFINITY, other_floor = __shfl_xor_sync(kAll, floor, 1);
+                // both lanes' elements that may be the largest, in 64 bits: all of them where 32 say nothing
+                const float floor = !unsure ? INFINITY : wild ? -INFINITY : amax - 2.f * e;
+                const float other_floor = __shfl_xor_sync(kAll, floor, 1);
                 uint32_t which[2] = {0, 0};
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) which[u] |= fabsf(y[u][i]) >= (odd == (u == 1) ? floor : other_floor) ? 1u << i : 0u;
+                    for (int i = 0; i < 8; ++i) which[u] |= fabsf(y[u][i]) < (odd == (u == 1) ? floor : other_floor) ? 0u : 1u << i;
                 const T *row = new_row<T>(a, false, tok, h);
                 const double a0 = exact_top<T>(a, row, tok, d[0], which[0]), a1 = exact_top<T>(a, row, tok, d[1], which[1]);
                 __syncwarp();
-                const double exact = fmax(odd ? a1 : a0, __shfl_xor_sync(kAll, odd ? a0 : a1, 1));
-                if (unsure) byte = fp4_scale_of<double>(amax, exact, &border);
+                const double exact = larger(odd ? a1 : a0, __shfl_xor_sync(kAll, odd ? a0 : a1, 1));
+                if (wild) {
+                    byte = isnan(exact) ? kFp4NanScale : fp4_scale_of<double>((float)exact, exact, &border);
+                    if (exact > (double)kFp4Top && on) report(a.status, PA_DEV_RANGE);
+                } else if (unsure) {
+                    byte = fp4_scale_of<double>(amax, exact, &border);
+                }
             }
         }
         const float scale = fp4_scale_value(byte), inv = byte != 0 ? inverse(scale) : 0.f;
@@ -313,7 +341,7 @@ struct Pair {
                 // zero) the code comes from 64 bits.  A quotient is at most 6.4 near a border (larger ones saturate).
                 // bf16 elements that are not turned are rounded as above instead: they often are borders.
                 const bool snap = sizeof(T) == 2 && kMode != kHalves && !turns[u];
-                const float eq = snap ? 0.f : (own ? e : other_e) * f + 0x1p-18f, round = snap ? 192.f : 0.f;
+                const float of_y = own ? e : other_e, eq = snap ? 0.f : of_y * f + 0x1p-18f, round = snap ? 192.f : 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     y[u][i] = sizeof(T) == 2 && kMode != kHalves ? fmaf(y[u][i], f, round) - round : y[u][i] * f;
@@ -322,7 +350,8 @@ struct Pair {
                 out = f32x8_to_e2m1x8(lo);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) lo[i] = y[u][i] + eq;
-                const uint32_t above = f32x8_to_e2m1x8(lo);
+                uint32_t above = f32x8_to_e2m1x8(lo);
+                if (kTurned && of_y == INFINITY) out = kAllLow, above = kAllHigh;
                 if (out != above)
                     out = exact_codes<T, kTurned>(a, new_row<T>(a, kValue, tok, h), tok, d[u], out, above, own ? scale : other_scale);
             }

@@ -208,6 +208,38 @@ def test_write_of_nan_and_infinity(pkv):
     assert not np.isnan(v[0, 1, 16:64]).any() and not np.isnan(v[0, 0]).any() and not np.isnan(v[0, 3]).any()
 
 
+@pytest.mark.parametrize("scaling,factor", [("none", 1.0), ("by_parts", 32.0)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,rot", [(128, 128), (128, 64), (128, 20), (48, 48), (256, 96)])
+def test_write_of_turned_keys_beyond_f32(pkv, D, rot, dtype, interleaved, scaling, factor):
+    """Infinities that are turned, and finite pairs whose rotation leaves f32's range: saturated, with the sign of the exact
+    rotation, in their own unit and in their partner's; a NaN only where the rotation is one."""
+    g = torch.Generator().manual_seed(D + rot)
+    T, H, half = 64, 2, rot // 2
+    k = torch.randn(T, H, D, generator=g).to(dtype)
+    top = torch.finfo(dtype).max
+    inf = float("inf")
+    odd = [(inf, 1.0), (-2.0, -inf), (top, top), (top, -top), (0.9 * top, 0.01 * top), (-top, 0.0), (0.0, top), (inf, inf),
+           (inf, float("nan")), (0.75 * top, 0.7 * top), (1e30, -1e30)]
+    for t in range(1, T):                                            # (the first token is ordinary)
+        p = int(torch.randint(0, half, (1,), generator=g))
+        i, j = (2 * p, 2 * p + 1) if interleaved else (p, p + half)
+        k[t, t % H, i], k[t, t % H, j] = odd[t % len(odd)]
+    k[5, 1, rot - 2:] = 0
+    pos = torch.randint(0, 3000, (T,), generator=g, dtype=torch.int32)
+    pos[40:52] = 0                                                   # where nothing turns
+    rope = pkv.rotary_plan(rot, interleaved=interleaved, scaling=scaling, factor=factor)
+    kc, vc, status = pkv.fp4_pool(4, H, D), pkv.fp4_pool(4, H, D), _status()
+    pkv.rope_cache_write_fp4(None, k.cuda(), k.cuda(), pos.cuda(), rope, kc, vc, torch.arange(T).cuda(), status=status)
+    with np.errstate(invalid="ignore"):
+        ref, _ = R.rotate(k.double().numpy(), *_angles(rope, pos.tolist()), interleaved)
+    zero = torch.zeros(kc.shape, dtype=torch.uint8)
+    _same(vc, _written(zero, k.double().numpy(), range(T)), "values")
+    _same(kc, _written(zero, ref, range(T)), "keys")
+    assert int(status.item()) == 256
+
+
 def test_write_slots(pkv):
     """Slots past the pool are skipped and flagged, negative ones skipped; the query is turned all the same."""
     g = torch.Generator().manual_seed(8)
