@@ -68,8 +68,9 @@ __device__ __forceinline__ float fp4_scale_value(uint32_t byte) {
 
 // The scale of 16 elements of which the largest magnitude is amax: amax / 6 to
 // nearest, ties to even, at least the smallest scale and at most kFp4TopScale; 0 for
-// 0.  `near` is amax to 2^-20; the decision compares amax itself with *border, six times
-// the number midway between the two scales in question, which is exact.
+// 0.  `near` is amax to 2^-20 (not a value that may be further off: of an exact amax, that rounded); the
+// decision compares amax itself with *border, six times the number midway between the two scales in
+// question, which is exact.
 template <typename F>
 __device__ __forceinline__ uint32_t fp4_scale_of(float near, F amax, float *border) {
     const float low = fminf(near, 2.f * kFp4Top) * ((1.f - 0x1p-18f) / 6.f);

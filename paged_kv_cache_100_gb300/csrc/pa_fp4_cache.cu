@@ -77,6 +77,13 @@ __device__ __forceinline__ float turn_error(const RopeArgs &a, float most) {
     return most * f >= 0x1p127f ? INFINITY : most * (kTurnError * f);
 }
 
+// Whether the scale of a unit of largest magnitude amax, off by e, is asked for in 64 bits: the border
+// that the 32-bit value was compared with lies within e, or another one may (the nearest lies amax / 32
+// away, below the first scale of a binade).
+__device__ __forceinline__ bool scale_unsure(float amax, float border, float e) {
+    return e > 0.f && (fabsf(amax - border) <= e || amax <= 64.f * e);
+}
+
 // Midway between the magnitudes of codes c and c + 1, c at most 6.
 __device__ __forceinline__ float code_border(uint32_t c) {
     return c < 4 ? 0.25f + 0.5f * (float)c : c == 4 ? 2.5f : c == 5 ? 3.5f : 5.f;
@@ -136,11 +143,12 @@ __device__ __forceinline__ void encode16(const RopeArgs &a, const T *row, int64_
         *scale_at = (uint8_t)kFp4NanScale;
         return;
     }
-    if (kTurned && !wild && most > 0.f && (fabsf(amax - border) <= e || amax <= e)) {
+    if (kTurned && !wild && scale_unsure(amax, border, e)) {
         uint32_t which = 0;
 #pragma unroll
         for (int k = 0; k < 16; ++k) which |= fabsf(y[k]) >= amax - 2.f * e ? 1u << k : 0u;
-        byte = fp4_scale_of<double>(amax, exact_top<T>(a, row, tok, d0, which), &border);
+        const double exact = exact_top<T>(a, row, tok, d0, which);
+        byte = fp4_scale_of<double>((float)exact, exact, &border);
     }
     const float scale = fp4_scale_value(byte), inv = byte != 0 ? 1.f / scale : 0.f;
     // of a quotient, which is at most 6.4 near a border (larger ones saturate)
@@ -293,7 +301,7 @@ struct Pair {
         uint32_t byte = nan ? kFp4NanScale : fp4_scale_of(amax, amax, &border);
         if (!nan && amax > kFp4Top && on && !wild) report(a.status, PA_DEV_RANGE);
         if constexpr (kTurned) {
-            const bool unsure = on && (wild || (!nan && e > 0.f && (fabsf(amax - border) <= e || amax <= e)));
+            const bool unsure = on && (wild || (!nan && scale_unsure(amax, border, e)));
             if (__any_sync(kAll, unsure)) {
                 // both lanes' elements that may be the largest, in 64 bits: all of them where 32 say nothing
                 const float floor = !unsure ? INFINITY : wild ? -INFINITY : amax - 2.f * e;
@@ -307,12 +315,8 @@ struct Pair {
                 const double a0 = exact_top<T>(a, row, tok, d[0], which[0]), a1 = exact_top<T>(a, row, tok, d[1], which[1]);
                 __syncwarp();
                 const double exact = larger(odd ? a1 : a0, __shfl_xor_sync(kAll, odd ? a0 : a1, 1));
-                if (wild) {
-                    byte = isnan(exact) ? kFp4NanScale : fp4_scale_of<double>((float)exact, exact, &border);
-                    if (exact > (double)kFp4Top && on) report(a.status, PA_DEV_RANGE);
-                } else if (unsure) {
-                    byte = fp4_scale_of<double>(amax, exact, &border);
-                }
+                if (unsure) byte = isnan(exact) ? kFp4NanScale : fp4_scale_of<double>((float)exact, exact, &border);
+                if (wild && on && exact > (double)kFp4Top) report(a.status, PA_DEV_RANGE);
             }
         }
         const float scale = fp4_scale_value(byte), inv = byte != 0 ? inverse(scale) : 0.f;

@@ -240,6 +240,31 @@ def test_write_of_turned_keys_beyond_f32(pkv, D, rot, dtype, interleaved, scalin
     assert int(status.item()) == 256
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,rot", [(128, 128), (128, 64), (64, 64), (256, 96), (128, 36), (80, 80)])
+def test_write_of_units_that_nearly_cancel(pkv, D, rot, dtype):
+    """Units of which every element is turned into next to nothing: scales and codes of what is left, exactly."""
+    g = torch.Generator().manual_seed(D + rot)
+    T, H, half = 600, 2, rot // 2
+    pos = torch.randint(1, 3000, (T,), generator=g, dtype=torch.int32)
+    rope = pkv.rotary_plan(rot)
+    cos, sin = (torch.from_numpy(x)[:, None] for x in _angles(rope, pos.tolist()))
+    k = torch.randn(T, H, D, generator=g).to(dtype)
+    # the pair's second element at random, of one size in a row; its first one nearest to what cancels
+    second = (torch.randn(T, H, half, generator=g) * torch.exp2(20 * torch.rand(T, H, 1, generator=g))).to(dtype)
+    k[..., half:rot] = second
+    k[..., :half] = (second.double() * sin / torch.where(cos.abs() < 0.01, 1.0, cos)).to(dtype)
+    blocks = -(-T // 16)
+    kc, vc = pkv.fp4_pool(blocks, H, D), pkv.fp4_pool(blocks, H, D)
+    pkv.rope_cache_write_fp4(None, k.cuda(), k.cuda(), pos.cuda(), rope, kc, vc, torch.arange(T).cuda())
+    ref, mass = R.rotate(k.double().numpy(), cos[:, 0].numpy(), sin[:, 0].numpy(), False)
+    if dtype == torch.float32:                                       # what is meant to be tested is there
+        unit = slice(0, 16)
+        assert (np.abs(ref[..., unit]).max(-1) < 2.0 ** -20 * mass[..., unit].max(-1)).mean() > 0.5
+    zero = torch.zeros(kc.shape, dtype=torch.uint8)
+    _same(kc, _written(zero, ref, range(T)), "keys")
+
+
 def test_write_slots(pkv):
     """Slots past the pool are skipped and flagged, negative ones skipped; the query is turned all the same."""
     g = torch.Generator().manual_seed(8)
