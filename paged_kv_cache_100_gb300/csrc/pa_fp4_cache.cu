@@ -78,10 +78,10 @@ __device__ __forceinline__ float turn_error(const RopeArgs &a, float most) {
 }
 
 // Whether the scale of a unit of largest magnitude amax, off by e, is asked for in 64 bits: the border
-// that the 32-bit value was compared with lies within e, or another one may (the nearest lies amax / 32
-// away, below the first scale of a binade).
+// that the 32-bit value was compared with lies within e, or the range's end, or another border may (the
+// nearest lies amax / 32 away, below the first scale of a binade).
 __device__ __forceinline__ bool scale_unsure(float amax, float border, float e) {
-    return e > 0.f && (fabsf(amax - border) <= e || amax <= 64.f * e);
+    return e > 0.f && (fabsf(amax - border) <= e || fabsf(amax - kFp4Top) <= e || amax <= 64.f * e);
 }
 
 // Midway between the magnitudes of codes c and c + 1, c at most 6.
@@ -127,28 +127,23 @@ __device__ __forceinline__ void encode16(const RopeArgs &a, const T *row, int64_
     for (int k = 0; k < 16; ++k) top = max(top, __float_as_uint(y[k]) & 0x7fffffffu);
     const float amax = __uint_as_float(top), e = kTurned ? turn_error(a, most) : 0.f;     // error of an element
     const bool wild = kTurned && e == INFINITY;
-    bool nan = top > 0x7f800000u;
+    bool nan = top > 0x7f800000u, beyond = amax > kFp4Top;
     float border = 0.f;
     uint32_t byte = fp4_scale_of(amax, amax, &border);
-    if (wild) {
-        const double exact = exact_top<T>(a, row, tok, d0, 0xffffu);
+    if (kTurned && (wild || (!nan && scale_unsure(amax, border, e)))) {
+        uint32_t which = 0;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) which |= wild || fabsf(y[k]) >= amax - 2.f * e ? 1u << k : 0u;
+        const double exact = exact_top<T>(a, row, tok, d0, which);
         nan = isnan(exact);
+        beyond = exact > (double)kFp4Top;
         byte = fp4_scale_of<double>((float)exact, exact, &border);
-        if (exact > (double)kFp4Top) report(a.status, PA_DEV_RANGE);
-    } else if (!nan && amax > kFp4Top) {
-        report(a.status, PA_DEV_RANGE);
     }
+    if (!nan && beyond) report(a.status, PA_DEV_RANGE);
     if (nan) {
         *reinterpret_cast<uint2 *>(codes) = make_uint2(0u, 0u);
         *scale_at = (uint8_t)kFp4NanScale;
         return;
-    }
-    if (kTurned && !wild && scale_unsure(amax, border, e)) {
-        uint32_t which = 0;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) which |= fabsf(y[k]) >= amax - 2.f * e ? 1u << k : 0u;
-        const double exact = exact_top<T>(a, row, tok, d0, which);
-        byte = fp4_scale_of<double>((float)exact, exact, &border);
     }
     const float scale = fp4_scale_value(byte), inv = byte != 0 ? 1.f / scale : 0.f;
     // of a quotient, which is at most 6.4 near a border (larger ones saturate)
@@ -299,7 +294,7 @@ struct Pair {
         const bool nan = mine > 0x7f800000u, wild = kTurned && e == INFINITY;
         float border = 0.f;
         uint32_t byte = nan ? kFp4NanScale : fp4_scale_of(amax, amax, &border);
-        if (!nan && amax > kFp4Top && on && !wild) report(a.status, PA_DEV_RANGE);
+        bool beyond = !nan && amax > kFp4Top;
         if constexpr (kTurned) {
             const bool unsure = on && (wild || (!nan && scale_unsure(amax, border, e)));
             if (__any_sync(kAll, unsure)) {
@@ -315,10 +310,13 @@ struct Pair {
                 const double a0 = exact_top<T>(a, row, tok, d[0], which[0]), a1 = exact_top<T>(a, row, tok, d[1], which[1]);
                 __syncwarp();
                 const double exact = larger(odd ? a1 : a0, __shfl_xor_sync(kAll, odd ? a0 : a1, 1));
-                if (unsure) byte = isnan(exact) ? kFp4NanScale : fp4_scale_of<double>((float)exact, exact, &border);
-                if (wild && on && exact > (double)kFp4Top) report(a.status, PA_DEV_RANGE);
+                if (unsure) {
+                    byte = isnan(exact) ? kFp4NanScale : fp4_scale_of<double>((float)exact, exact, &border);
+                    beyond = exact > (double)kFp4Top;
+                }
             }
         }
+        if (beyond && on) report(a.status, PA_DEV_RANGE);
         const float scale = fp4_scale_value(byte), inv = byte != 0 ? inverse(scale) : 0.f;
         const float other_inv = __shfl_xor_sync(kAll, inv, 1);
         float other_e = 0.f, other_scale = 0.f;

@@ -265,6 +265,30 @@ def test_write_of_units_that_nearly_cancel(pkv, D, rot, dtype):
     _same(kc, _written(zero, ref, range(T)), "keys")
 
 
+@pytest.mark.parametrize("dim,rot,interleaved", [(64, 64, False), (64, 64, True), (64, 20, False)])
+def test_write_flags_the_exact_range(pkv, dim, rot, interleaved):
+    """Elements turned into 61440 and a little more or less: flagged where the exact one is beyond it."""
+    g = np.random.default_rng(rot)
+    rope, T, half = pkv.rotary_plan(rot, interleaved=interleaved), 48, rot // 2
+    pos = g.integers(1, 3000, T)
+    cos, sin = _angles(rope, pos.tolist())
+    k = np.zeros((T, 1, dim))
+    for t in range(T):
+        p = int(np.argmax(np.abs(cos[t])))                           # a pair that turns by little
+        i, j = (2 * p, 2 * p + 1) if interleaved else (p, p + half)
+        k[t, 0, j] = np.float32(g.uniform(-500, 500))
+        k[t, 0, i] = np.float32((61440.0 + k[t, 0, j] * sin[t, p]) / cos[t, p])
+    ref, _ = R.rotate(k, cos, sin, interleaved)
+    beyond = np.abs(ref).reshape(T, -1).max(-1) > 61440.0
+    assert 10 < beyond.sum() < T - 10
+    x, where = torch.from_numpy(k).float().cuda(), torch.from_numpy(pos).to(torch.int32).cuda()
+    kc, vc, status = pkv.fp4_pool(T, 1, dim), pkv.fp4_pool(T, 1, dim), torch.zeros(T, dtype=torch.int32, device="cuda")
+    zero = torch.zeros(1, 1, dim, device="cuda")
+    for t in range(T):
+        pkv.rope_cache_write_fp4(None, x[t:t + 1], zero, where[t:t + 1], rope, kc, vc, torch.tensor([t]).cuda(), status=status[t:t + 1])
+    assert np.array_equal(status.cpu().numpy() == 256, beyond) and not (status.cpu().numpy() & ~256).any()
+
+
 def test_write_slots(pkv):
     """Slots past the pool are skipped and flagged, negative ones skipped; the query is turned all the same."""
     g = torch.Generator().manual_seed(8)
