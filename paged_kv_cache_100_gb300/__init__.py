@@ -435,6 +435,15 @@ def block_copy(key_cache, value_cache, src_dst, *, k_scales=None, v_scales=None,
     check(rc, "pa_block_copy")
 
 
+def _longest_chunk(query_start, stream):
+    """The longest of the chunks that begin at ``query_start``, read where the given stream (None: the current
+    one) has come to: it may be what that stream computes."""
+    if query_start.numel() < 2:
+        return 0
+    with _torch().cuda.stream(stream):
+        return int((query_start[1:] - query_start[:-1]).max().item())
+
+
 def prefill(query, key_cache, value_cache, block_tables, context_lens, query_start,
             max_query_len=None, scale=None, *, window=0, out=None, workspace=None, status=None,
             stream=None):
@@ -456,7 +465,7 @@ def prefill(query, key_cache, value_cache, block_tables, context_lens, query_sta
             value_cache.dtype != torch.bfloat16:
         raise TypeError("pa_prefill takes bfloat16 query and pools")
     if max_query_len is None:
-        max_query_len = int((query_start[1:] - query_start[:-1]).max().item()) if B else 0
+        max_query_len = _longest_chunk(query_start, stream)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
@@ -584,7 +593,7 @@ def prefill_block_fp8(query, key_cache, value_cache, k_scales, v_scales, block_t
     """Chunked prefill over E4M3 pools with one scale per block and KV head
     (``pa_prefill_block_fp8``); arguments as ``prefill``.  Returns ``out`` (bf16)."""
     if max_query_len is None:
-        max_query_len = int((query_start[1:] - query_start[:-1]).max().item()) if query_start.numel() > 1 else 0
+        max_query_len = _longest_chunk(query_start, stream)
     r = _lib.binding().prefill_block_fp8(query, key_cache, value_cache, k_scales, v_scales, block_tables,
                                          context_lens, query_start, max_query_len, scale, window, out, workspace,
                                          status, _given(stream, query))
@@ -680,7 +689,7 @@ def prefill_fp4(query, key_cache, value_cache, block_tables, context_lens, query
     that of contexts of ``max_context_len`` tokens.  A few rows on long contexts run as rows of ``decode_fp4``.
     Returns ``out`` (bf16)."""
     if max_query_len is None:
-        max_query_len = int((query_start[1:] - query_start[:-1]).max().item()) if query_start.numel() > 1 else 0
+        max_query_len = _longest_chunk(query_start, stream)
     r = _lib.binding().prefill_fp4(query, key_cache, value_cache, block_tables, context_lens, query_start, max_query_len,
                                    scale, max_context_len, window, out, workspace, status, _given(stream, query))
     if type(r) is int:

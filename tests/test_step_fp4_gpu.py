@@ -192,6 +192,34 @@ def test_given_streams(pkv):
     assert torch.equal(ko, want_k) and torch.equal(vo, want_v)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "block_fp8", "fp4"])
+def test_longest_chunk_is_read_on_the_given_stream(pkv, kind):
+    """max_query_len omitted: query_start may be what the given stream has yet to write."""
+    p = F.Batch(7, [500, 77], HKV, D, poison=False)
+    kc, vc, tables, lens = p.device()
+    args = (kc, vc, tables, lens)
+    call = pkv.prefill_fp4
+    if kind != "fp4":
+        k, v = (torch.from_numpy(F.unpack(t)[2]).to(torch.bfloat16).cuda() for t in (p.kc, p.vc))
+        args, call = (k, v, tables, lens), pkv.prefill
+    if kind == "block_fp8":
+        one = torch.ones(p.blocks, HKV, device="cuda")
+        args, call = (k.to(torch.float8_e4m3fn), v.to(torch.float8_e4m3fn), one, one, tables, lens), pkv.prefill_block_fp8
+    q = p.query(25, HQ).cuda()
+    start = torch.tensor([0, 20, 25], dtype=torch.int32, device="cuda")
+    want = call(q, *args, start)                                     # (loads every kernel that the second call takes)
+    late = torch.zeros_like(start)
+    out = torch.full_like(want, 5.0)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+        late.copy_(start)
+    call(q, *args, late, out=out, stream=side)
+    side.synchronize()
+    assert torch.equal(out, want)
+
+
 def test_calls_from_several_threads(pkv):
     """Calls of different sizes from threads with streams of their own."""
     import threading
