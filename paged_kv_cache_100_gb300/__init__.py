@@ -24,6 +24,7 @@ slot_mapping int64 [num_tokens]; copy pairs int32 [num_pairs][2].
 from __future__ import annotations
 
 import collections
+import contextlib
 import ctypes
 import math
 
@@ -92,6 +93,12 @@ def _stream(stream, t):
     return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
 
 
+def _on(stream):
+    """Where a call allocates its output and workspace: the given stream, which uses them, owns them, so that
+    memory given back with work in flight goes to no other one (None: the current stream)."""
+    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+
+
 def _status_ptr(status):
     torch = _torch()
     if status is None:
@@ -151,7 +158,8 @@ def decode(query, key_cache, value_cache, block_tables, context_lens, scale=None
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty_like(query)
+        with _on(stream):
+            out = torch.empty_like(query)
     elif out.shape != query.shape or out.dtype != query.dtype:
         raise ValueError("out must match query")
     max_blocks = block_tables.shape[1]
@@ -160,7 +168,8 @@ def decode(query, key_cache, value_cache, block_tables, context_lens, scale=None
         # caller's workspace is passed as given and sized by the library
         need = decode_workspace_bytes(B, Hq, Hkv, D, max_blocks, partition_size, query.dtype)
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+            with _on(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
         ws_ptr = _dev(workspace, "workspace")
@@ -191,7 +200,8 @@ def decode_shared_prefix(query, key_cache, value_cache, block_tables, context_le
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty_like(query)
+        with _on(stream):
+            out = torch.empty_like(query)
     max_blocks = block_tables.shape[1]
     if workspace is None:
         need = lib().pa_decode_shared_prefix_workspace_bytes(B, Hq, Hkv, D, max_blocks,
@@ -199,7 +209,8 @@ def decode_shared_prefix(query, key_cache, value_cache, block_tables, context_le
                                                                 int(partition_size))
         if need == ctypes.c_size_t(-1).value:
             raise ValueError("invalid arguments for pa_decode_shared_prefix_workspace_bytes")
-        workspace = torch.empty(max(int(need), 16), dtype=torch.uint8, device=query.device)
+        with _on(stream):
+            workspace = torch.empty(max(int(need), 16), dtype=torch.uint8, device=query.device)
     rc = lib().pa_decode_shared_prefix(
         _dev(out, "out"), _dev(query, "query"), _dev(key_cache, "key_cache"),
         _dev(value_cache, "value_cache"), _dev(block_tables, "block_tables", torch.int32),
@@ -231,7 +242,8 @@ def decode_shared_prefix_fp8(query, key_cache, value_cache, k_scales, v_scales, 
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty_like(query)
+        with _on(stream):
+            out = torch.empty_like(query)
     max_blocks = block_tables.shape[1]
     if workspace is None:
         need = lib().pa_decode_shared_prefix_fp8_workspace_bytes(B, Hq, Hkv, D, max_blocks,
@@ -239,7 +251,8 @@ def decode_shared_prefix_fp8(query, key_cache, value_cache, k_scales, v_scales, 
                                                                     int(partition_size))
         if need == ctypes.c_size_t(-1).value:
             raise ValueError("invalid arguments for pa_decode_shared_prefix_fp8_workspace_bytes")
-        workspace = torch.empty(max(int(need), 16), dtype=torch.uint8, device=query.device)
+        with _on(stream):
+            workspace = torch.empty(max(int(need), 16), dtype=torch.uint8, device=query.device)
     rc = lib().pa_decode_shared_prefix_fp8(
         _dev(out, "out"), _dev(query, "query"), _dev(key_cache, "key_cache"),
         _dev(value_cache, "value_cache"), _dev(k_scales, "k_scales", torch.float32),
@@ -281,14 +294,16 @@ def decode_fp8(query, key_cache, value_cache, k_scales, v_scales, block_tables, 
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty_like(query)
+        with _on(stream):
+            out = torch.empty_like(query)
     max_blocks = block_tables.shape[1]
     if workspace is None:
         # the library's scratch size for this call (0: none needed); a
         # caller's workspace is passed as given and sized by the library
         need = decode_workspace_bytes(B, Hq, Hkv, D, max_blocks, partition_size, "fp8")
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+            with _on(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
         ws_ptr = _dev(workspace, "workspace")
@@ -338,7 +353,8 @@ def decode_sliding_window(query, key_cache, value_cache, block_tables, context_l
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty_like(query)
+        with _on(stream):
+            out = torch.empty_like(query)
     elif out.shape != query.shape or out.dtype != query.dtype:
         raise ValueError("out must match query")
     max_blocks = block_tables.shape[1]
@@ -349,7 +365,8 @@ def decode_sliding_window(query, key_cache, value_cache, block_tables, context_l
         if need == ctypes.c_size_t(-1).value:
             raise ValueError("invalid arguments for pa_decode_sliding_window_workspace_bytes")
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+            with _on(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
         ws_ptr = _dev(workspace, "workspace")
@@ -469,12 +486,14 @@ def prefill(query, key_cache, value_cache, block_tables, context_lens, query_sta
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty_like(query)
+        with _on(stream):
+            out = torch.empty_like(query)
     elif out.shape != query.shape or out.dtype != query.dtype:
         raise ValueError("out must match query")
     need = int(lib().pa_prefill_workspace_bytes())
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+        with _on(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
     rc = lib().pa_prefill(
         _dev(out, "out"), _dev(query, "query"), _dev(key_cache, "key_cache"),
         _dev(value_cache, "value_cache"), _dev(block_tables, "block_tables", torch.int32),

@@ -109,3 +109,42 @@ def test_rotary_writes_of_different_sizes(pkv):
     assert not errors
     for pools, want in checks:
         assert all(torch.equal(a, b) for a, b in zip(pools, want))
+
+
+@pytest.mark.parametrize("kind", ["decode", "decode_fp8", "window", "window_fp8", "prefix", "prefix_fp8", "prefill"])
+def test_a_given_streams_workspace_is_that_streams(pkv, kind):
+    """Memory that the current stream takes while a given one has yet to run its call is none of that call's."""
+    g = torch.Generator().manual_seed(4)
+    B, H, lens = 4, 4, [3000, 2900, 2048, 2050]
+    blocks, width = 4 * 188, 188
+    rows = torch.randn(blocks, H, 16, D, generator=g).to(torch.bfloat16).cuda()
+    codes, one = rows.to(torch.float8_e4m3fn), torch.ones(H, device="cuda")
+    table = torch.arange(blocks, dtype=torch.int32).reshape(B, width).cuda()
+    table[:, :64] = table[0, :64]
+    length, q = torch.tensor(lens, dtype=torch.int32).cuda(), torch.randn(B, H, D, generator=g).to(torch.bfloat16).cuda()
+    start = torch.arange(B + 1, dtype=torch.int32).cuda()
+    calls = {"decode": lambda **o: pkv.decode(q, rows, rows, table, length, partition_size=64, **o),
+             "decode_fp8": lambda **o: pkv.decode_fp8(q, codes, codes, one, one, table, length, partition_size=64, **o),
+             "window": lambda **o: pkv.decode_sliding_window(q, rows, rows, table, length, 2000, partition_size=64, **o),
+             "window_fp8": lambda **o: pkv.decode_sliding_window(q, codes, codes, table, length, 2000, k_scales=one, v_scales=one,
+                                                                 partition_size=64, **o),
+             "prefix": lambda **o: pkv.decode_shared_prefix(q, rows, rows, table, length, 64, partition_size=64, **o),
+             "prefix_fp8": lambda **o: pkv.decode_shared_prefix_fp8(q, codes, codes, one, one, table, length, 64, partition_size=64, **o),
+             "prefill": lambda **o: pkv.prefill(q, rows, rows, table, length, start, 1, **o)}
+    call = calls[kind]
+    want = call()
+    assert bool((torch.full((8,), 7, dtype=torch.uint8, device="cuda") == 7).all())      # (loads its kernels)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    # (the output is dropped at once too: its memory is the side stream's as well)
+    call(stream=side)
+    taken = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in (256, 1024, 4096, 1 << 14, 1 << 17, 1 << 19, 1 << 20) for _ in range(8)]
+    got = call(stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    for t in taken:
+        assert bool((t == 7).all()), t.numel()
