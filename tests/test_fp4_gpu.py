@@ -441,6 +441,91 @@ def test_decode_values_of_any_size(pkv, D):
     F.check(out, ref, bound + 2 * size * np.abs(F.unpack(p.vc)[2]).max())
 
 
+@pytest.mark.parametrize("seqs,hq,hkv,D,longest,window,plan", [
+    (100, 8, 8, 128, 400, 0, False), (256, 8, 8, 128, 400, 0, False), (255, 8, 8, 128, 416, 0, True), (131, 16, 8, 64, 400, 0, True),
+    (77, 8, 8, 256, 640, 0, False), (200, 16, 4, 128, 480, 300, False), (33, 32, 32, 128, 512, 0, False)])
+def test_decode_longest_first(pkv, seqs, hq, hkv, D, longest, window, plan):
+    """More than four CTAs an SM, a part each and too long for CTAs of one warp: CTAs take the longest sequences
+    first.  Ragged ones, equal ones, empty ones and lengths out of range, each computed once."""
+    assert pkv.decode_fp4_workspace_bytes(seqs, hq, hkv, D, longest // 16, window=window) == 0
+    rng = np.random.default_rng(seqs)
+    lens = rng.integers(0, longest + 1, seqs)
+    lens[5:25] = 48                                                  # of one length
+    lens[[2, 3, 30]] = 0
+    lens[[0, 31]] = longest
+    p = F.Batch(seqs, lens, hkv, D, width=longest // 16)
+    kc, vc, tables, given = p.device()
+    given[0], given[2], given[31] = longest + 1, -7, 1 << 30         # clamped to what they are
+    for b, n in enumerate(lens):
+        if window:
+            tables[b, :max(0, n - window) // 16] = -1                # released blocks before the window
+    brings = [b for b in range(seqs) if not plan or b % 5 != 1]
+    q = p.query(len(brings) + 3, hq)
+    start = np.cumsum([0] + [int(b in brings) for b in range(seqs)])
+    status, out = _status(), torch.full(q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+    if plan:
+        pkv.decode_fp4(q.cuda(), kc, vc, tables, given, query_start=torch.tensor(start, dtype=torch.int32, device="cuda"), window=window,
+                       out=out, status=status)
+    else:
+        pkv.decode_fp4(q[:seqs].cuda(), kc, vc, tables, given, window=window, out=out[:seqs], status=status)
+    ref, bound = p.reference(q[:len(brings)].double().numpy(), [(b, int(lens[b]) - 1) for b in brings], window=window)
+    F.check(out[:len(brings)], ref, bound, f"{seqs}")
+    assert (out[len(brings):] == 5).all() and int(status.item()) == 2
+
+
+def _growing(p, size):
+    """Keys of p grow along the contexts: those of position i of sequence b by size(b, i)."""
+    x = torch.randn(p.blocks, p.hkv, 16, p.dim, generator=p.g, dtype=torch.float64)
+    for b, n in enumerate(p.lens):
+        for i in range(int(n)):
+            x[p.tables[b, i // 16], :, i % 16] *= size(b, i)
+    p.kc = F.pack(*F.encode(x.numpy()))
+    p.scales(p.kc)[torch.from_numpy(~p.live)[:, None].expand(-1, p.hkv, -1)] = 0xFF
+
+
+def _large_scores(p, q, rows, window=0, floor=1.0):
+    """Batch.reference where scores are large: what f32 sums of a score change a weight by comes on top.
+
+    Products are exact; each of D / 16 steps of 16 products adds at most 2^-22 of the sum of magnitudes A, and three
+    roundings of the scaled score 3 times 2^-24 of it: a score is off by e = (D 2^-26 + 2^-22) scale A.  A weight
+    p is then off by a factor of 1 + d, d = exp(e) - 1, and the output by at most sum p d |v - out| / (1 - sum p d)."""
+    out, bound = p.reference(q, rows, window=window, floor=floor)
+    group, scale = q.shape[1] // p.hkv, p.dim ** -0.5
+    kv, vv = F.unpack(p.kc)[2], F.unpack(p.vc)[2]
+    for i, (b, last) in enumerate(rows):
+        pos = np.arange(max(0, last + 1 - window) if window else 0, last + 1)
+        blk, off = p.tables[b][pos // 16], pos % 16
+        for h in range(p.hkv):
+            j = slice(h * group, (h + 1) * group)
+            k, v = kv[blk, h, off], vv[blk, h, off]
+            x = q[i, j] @ k.T * scale
+            w = np.exp(x - x.max(-1, keepdims=True))
+            w /= w.sum(-1, keepdims=True)
+            d = np.expm1((p.dim * 2.0 ** -26 + 2.0 ** -22) * scale * (np.abs(q[i, j]) @ np.abs(k).T))
+            far = np.einsum("gp,gpd->gd", w * d, np.abs(v[None] - out[i, j][:, None]))
+            bound[i, j] += far / (1 - (w * d).sum(-1, keepdims=True))
+    return out, bound
+
+
+GROWTH = {"rising": lambda b, i: 0.5 + 24 * i / 700, "late": lambda b, i: 24.0 if i > 600 else 0.5,
+          "halves": lambda b, i: (0.5 + 24 * i / 700) if (i // 64 + b) % 2 else 0.5, "falling": lambda b, i: 24.5 - 24 * i / 700,
+          "steps": lambda b, i: 2.0 ** (i // 128)}
+
+
+@pytest.mark.parametrize("growth", GROWTH)
+@pytest.mark.parametrize("D,hq,hkv", [(64, 4, 2), (128, 8, 1), (128, 2, 2), (256, 4, 2)])
+@pytest.mark.parametrize("partition", [0, 64])
+def test_decode_references_that_rise(pkv, growth, D, hq, hkv, partition):
+    """Scores that leave the reference behind again and again along a context: every output element within
+    what its own weights are off by."""
+    lens = [700, 655, 300, 40]
+    p = F.Batch(3, lens, hkv, D)
+    _growing(p, GROWTH[growth])
+    q = p.query(4, hq)
+    out = pkv.decode_fp4(q.cuda(), *p.device(), partition_size=partition)
+    F.check(out, *_large_scores(p, q.double().numpy(), [(b, n - 1) for b, n in enumerate(lens)]), growth)
+
+
 def test_decode_nan(pkv):
     """A NaN that is attended reaches its row and no other; NaN and infinite scales elsewhere reach none."""
     p = F.Batch(9, [50, 50, 50], 1, 128)
@@ -681,6 +766,103 @@ def test_prefill_of_few_rows_longer_than_said(pkv):
     assert int(status.item()) == 64 and (out[10:] == 5).all()
     ref, bound = p.reference(q[:10].double().numpy(), _rows([900, 900], [4, 8])[:10], floor=4.0)
     F.check(out[:10], ref, bound)
+
+
+def _in_parts(pkv, seqs, hq, hkv, width, rows, longest, window=0):
+    """Whether these sizes are computed by rows whose contexts are cut into parts: partial results need room
+    beside the chunks (16 bytes each) and their lengths (4)."""
+    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    heads = max(h for h in range(1, 9) if (hq // hkv) % h == 0)
+    chunks = min(rows, rows // (8 // heads) + seqs)
+    return pkv.prefill_fp4_workspace_bytes(seqs, hq, hkv, 128, width, rows, longest, None, window) > up(16 * chunks) + up(4 * chunks)
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (2, 1), (4, 1), (8, 1), (16, 1), (16, 2), (4, 4)])
+@pytest.mark.parametrize("lens,new,window", [
+    ([6147], [5], 0), ([6144 + 8], [8], 0), ([6400], [2], 4500), ([6147], [5], 4500),       # (rows that end before the last part)
+    ([6147, 1, 300, 6400, 5], [3, 2, 1, 4, 2], 0)])                                        # (the second one is refused)
+def test_prefill_of_few_rows_in_parts(pkv, hq, hkv, lens, new, window):
+    """Chunks whose contexts are cut into parts: partial results of several rows in a CTA's columns, merged."""
+    p = F.Batch(hq + len(lens), lens, hkv, 128, width=400)
+    n, dev, status = sum(new), p.device(), _status()
+    assert _by_rows(pkv, len(lens), hq, hkv, 128, 400, n, max(new), None, window)
+    assert _in_parts(pkv, len(lens), hq, hkv, 400, n, max(new), window) == (hq < 16 or new != [8])       # (those: clusters)
+    if window:
+        for b, (m, t) in enumerate(zip(lens, new)):
+            dev[2][b, :max(0, m - t + 1 - window) // 16] = -1
+    q = p.query(n, hq)
+    start = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    rows, ok = _rows(lens, new), [i for b, t in enumerate(new) for i in range(sum(new[:b]), sum(new[:b]) + t) if t <= lens[b]]
+    ref, bound = p.reference(q[ok].double().numpy(), [rows[i] for i in ok], window=window, floor=4.0)
+    need = pkv.prefill_fp4_workspace_bytes(len(lens), hq, hkv, 128, 400, n, max(new), None, window)
+    for fill in (0xFF, 0):                                           # what an earlier call left there does not matter
+        work = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        out = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+        pkv.prefill_fp4(q.cuda(), *dev, start, max(new), window=window, out=out, workspace=work, status=status)
+        F.check(out[ok], ref, bound, f"{hq}/{hkv} {lens} W={window}")
+        assert (out[[i for i in range(n) if i not in ok]] == 5).all()
+    assert int(status.item()) == (2 if len(ok) < n else 0)
+
+
+@pytest.mark.parametrize("hq,hkv,seqs", [(64, 8, 64), (32, 8, 64), (8, 8, 64), (16, 8, 90)])
+def test_prefill_of_few_rows_longest_first(pkv, hq, hkv, seqs):
+    """More chunks than fit the GPU at once, a part each: taken longest first, entries without a chunk among them."""
+    rng = np.random.default_rng(hq)
+    lens = rng.integers(4, 801, seqs).tolist()
+    lens[0], lens[1], lens[2] = 800, 4, 0
+    new = [min(n, 1 + int(rng.integers(0, 4))) for n in lens]
+    p = F.Batch(hq, lens, hkv, 128, width=50)
+    n, status = sum(new), _status()
+    assert _by_rows(pkv, seqs, hq, hkv, 128, 50, n, 4) and not _in_parts(pkv, seqs, hq, hkv, 50, n, 4)
+    q = p.query(n, hq)
+    start = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    out = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+    pkv.prefill_fp4(q.cuda(), *p.device(), start, 4, out=out, status=status)
+    ref, bound = p.reference(q.double().numpy(), _rows(lens, new), floor=4.0)
+    F.check(out, ref, bound, f"{hq}/{hkv}")
+    assert int(status.item()) == 0
+
+
+@pytest.mark.parametrize("growth", GROWTH)
+@pytest.mark.parametrize("hq,hkv,window", [(4, 4, 0), (8, 2, 0), (16, 1, 0), (4, 4, 200), (8, 2, 100)])
+@pytest.mark.parametrize("behind", [0, 4096], ids=["rows", "tiles"])
+def test_prefill_references_that_rise(pkv, growth, hq, hkv, window, behind):
+    """The same in prefill, in one half of a step's columns too and beside a window's end."""
+    lens, new = [700, 300], [300 if behind else 30, 40 if behind else 5]
+    p = F.Batch(window + hq, lens, hkv, 128)
+    _growing(p, GROWTH[growth])
+    n = sum(new)
+    q = p.query(n + behind, hq)
+    assert _by_rows(pkv, 2, hq, hkv, 128, p.tables.shape[1], len(q), max(new), None, window) == (behind == 0)
+    start = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    out = pkv.prefill_fp4(q.cuda(), *p.device(), start, window=window)
+    F.check(out[:n], *_large_scores(p, q[:n].double().numpy(), _rows(lens, new), window, floor=4.0), growth)
+
+
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (8, 2), (16, 1)])
+@pytest.mark.parametrize("window", [0, 150])
+def test_prefill_nan(pkv, hq, hkv, window):
+    """Tiles: a NaN key makes the rows that attend to it NaN and no other, a NaN value its elements of
+    those rows (and perhaps of others of the chunk); another sequence's, head's or unit's nothing."""
+    lens, new = [500, 333, 260], [300, 100, 260]
+    p = F.Batch(hq, lens, hkv, 128)
+    n, group, t = sum(new), hq // hkv, p.tables
+    q = p.query(n + 4096, hq)
+    start = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    ref, bound = p.reference(q[:n].double().numpy(), _rows(lens, new), window=window, floor=4.0)
+    p.scales(p.kc)[t[0, 270 // 16], 0, 270 % 16, 3] = 0xFF           # position 270, seen by the rows from 70 on
+    p.scales(p.vc)[t[1, 300 // 16], hkv - 1, 300 % 16, 5] = 0xFF     # elements 80 .. 95 of position 300
+    out = pkv.prefill_fp4(q.cuda(), *p.device(), start, window=window)[:n].double().cpu().numpy()
+    rows = np.array(_rows(lens, new))
+    sees = (rows[:, 0] == 0) & (rows[:, 1] >= 270) & (rows[:, 1] < (270 + window if window else 10 ** 6))
+    assert np.isnan(out[sees][:, :group]).all() and 100 < sees.sum() < 300
+    reads = (rows[:, 0] == 1) & (rows[:, 1] >= 300) & (rows[:, 1] < (300 + window if window else 10 ** 6))
+    assert np.isnan(out[reads][:, hq - group:, 80:96]).all() and reads.sum() == 33
+    clean = np.ones(out.shape, bool)
+    clean[sees, :group] = False
+    clean[300:400, hq - group:, 80:96] = False
+    assert not np.isnan(out[clean]).any()
+    F.check(torch.from_numpy(np.where(clean, out, ref)), ref, bound)
 
 
 # ---------------------------------------------------------------------------------------------
