@@ -125,6 +125,9 @@ __device__ __forceinline__ int row_of(const Fp4Args &a, int b, bool say) {
 
 // The sequence of rank `rank` by length, longest first, in kClasses classes of length (within one,
 // in order).  A warp's work; every warp of the grid that asks agrees.
+// A lane holds the lengths of eight sequences.  (With room for 1024: 320 sequences of 8 KV heads of up to 4096
+// tokens 156 us against 163 in the table's order, 384 177 / 179, 512 245 / 242; 256 of 32 KV heads of up to 2048 245
+// against 229 with room for 256.)
 constexpr int kOrdered = 256;                    // sequences at most
 constexpr int kClasses = 8;
 __device__ __forceinline__ int ranked(const Fp4Args &a, int rank) {
@@ -884,8 +887,14 @@ bool plan_of(int num_seqs, int axis, int max_blocks, int window, int partition_s
     p->max_parts = p->cluster > 1 ? 1 : std::max(1, (span + p->part_blocks - 1) / p->part_blocks);
     const int64_t all = ctas * p->max_parts;
     if (p->cluster == 1 && p->part_blocks <= (2 * all > 5 * target ? 24 : 4 * all > 5 * target ? 16 : 0)) p->warps = 1;
-    // (not where CTAs are short: 2048 of one warp on 32 tokens 9.1 us in order of length, 7.8 in theirs)
-    p->ordered = p->warps == 4 && p->cluster == 1 && p->max_parts == 1 && num_seqs > 1 && num_seqs <= kOrdered && ctas > target;
+    // Longest first saves a share of the longest CTA's time, which grows with the span, and costs each CTA 1.4 us of
+    // ranking, which adds up with the waves.  In order of length against the table's: 32 heads of their own,
+    // contexts of up to 512 tokens, 128 sequences 52.6 us against 47.1, 256 107.7 / 87.4; of up to 2048, 64
+    // 68.9 / 75.1, 128 121.0 / 122.9, 192 170.7 / 167.3, 256 228.9 / 215.3; of up to 16384, 64 373 / 443; 8 KV
+    // heads, of up to 1024, 128 26.6 / 28.4, 256 51.1 / 49.6, of up to 4096, 256 121.9 / 133.1.
+    // (Nor where CTAs are short: 2048 of one warp on 32 tokens 9.1 us in order of length, 7.8 in theirs.)
+    p->ordered = p->warps == 4 && p->cluster == 1 && p->max_parts == 1 && num_seqs > 1 && num_seqs <= kOrdered && ctas > target &&
+                 span * target > 20 * ctas;
     return true;
 }
 

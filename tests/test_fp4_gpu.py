@@ -442,11 +442,11 @@ def test_decode_values_of_any_size(pkv, D):
 
 
 @pytest.mark.parametrize("seqs,hq,hkv,D,longest,window,plan", [
-    (100, 8, 8, 128, 400, 0, False), (256, 8, 8, 128, 400, 0, False), (255, 8, 8, 128, 416, 0, True), (131, 16, 8, 64, 400, 0, True),
-    (77, 8, 8, 256, 640, 0, False), (200, 16, 4, 128, 480, 300, False), (33, 32, 32, 128, 512, 0, False)])
+    (100, 8, 8, 128, 480, 0, False), (256, 4, 4, 128, 576, 0, False), (255, 8, 4, 128, 592, 0, True), (131, 16, 8, 64, 624, 0, True),
+    (77, 8, 8, 256, 656, 0, False), (200, 16, 4, 128, 800, 480, False), (33, 32, 32, 128, 608, 0, False)])
 def test_decode_longest_first(pkv, seqs, hq, hkv, D, longest, window, plan):
-    """More than four CTAs an SM, a part each and too long for CTAs of one warp: CTAs take the longest sequences
-    first.  Ragged ones, equal ones, empty ones and lengths out of range, each computed once."""
+    """More than four CTAs an SM (two with heads of 256), a part each, and long for their number: CTAs take the longest
+    sequences first.  Ragged ones, equal ones, empty ones and lengths out of range, each computed once."""
     assert pkv.decode_fp4_workspace_bytes(seqs, hq, hkv, D, longest // 16, window=window) == 0
     rng = np.random.default_rng(seqs)
     lens = rng.integers(0, longest + 1, seqs)
