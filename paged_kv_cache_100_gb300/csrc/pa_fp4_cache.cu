@@ -737,11 +737,13 @@ struct Stage {
 // Chunks of a few rows are rows of a decode, each of which (up to eight together, where a group has
 // few heads) reads its context again, from L2: a tile of 256 rows takes a step of 128 positions
 // 1.75 us however few rows it has, on one SM.
-// The estimates that are compared: 12 us, a wave's steps and the staging at 5.5 TB/s;
-// decode's own and 3 us.  Of 63 shapes measured both ways it takes the faster one or is
-// within 10% of it (us, rows against tiles): one chunk on 8192 tokens, 64 query and 8 KV heads,
-// of 2 rows 21 : 156, of 64 128 : 166, of 256 404 : 164; 32 and 8 heads, of 16 29 : 156, of 64 70 : 166;
-// 64 chunks on 2048 of 4 rows, 64 and 8 heads 127 : 264, 32 and 8 70 : 264, 8 and 8 47 : 264.
+// The estimates that are compared: 12 us, a wave's steps and the staging at 5.5 TB/s, and a twentieth
+// (tiles take up to a fifth more than that); decode's own, its waves' starts and 3 us.  Of 975 shapes measured
+// both ways (1 to 256 chunks of 1 to 256 rows on 256 to 65536 tokens, groups of 8, 4 and 1: profiles/
+// prefill_fp4_ways.csv) it takes the faster one or is within 12% of it (us, rows against tiles): one chunk on 8192
+// tokens, 64 query and 8 KV heads, of 2 rows 16 : 150, of 64 123 : 160, of 256 408 : 160; 32 and 8 heads, of 16
+// 24 : 150, of 64 65 : 160; 64 chunks on 2048 of 4 rows, 64 and 8 heads 126 : 259, 32 and 8 68 : 258, 8 and 8
+// 40 : 258; 16 chunks of 16 on 256 30 : 19.
 constexpr int kMostRows = 4096;
 Stage stage_of(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int width, int num_rows, int max_query_len,
                int window) {
@@ -759,7 +761,7 @@ Stage stage_of(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, in
         s.chunks = (int)std::min<int64_t>(num_rows, (int64_t)num_rows / each + num_seqs);
         size_t partials;
         const double rows = 3.0 + decode_fp4_chunks_time(s.chunks, num_q_heads, num_kv_heads, head_dim, width, window, &partials);
-        if (rows < 12.0 + staged + waves * (double)((seen + 7) / 8) * 1.75) {
+        if (rows < 1.05 * (12.0 + staged + waves * (double)((seen + 7) / 8) * 1.75)) {
             s.by_rows = true;
             s.lens = up((size_t)s.chunks * sizeof(int4));
             s.keys = s.lens + up((size_t)s.chunks * sizeof(int32_t));

@@ -1051,7 +1051,8 @@ double decode_fp4_chunks_time(int num_chunks, int num_q_heads, int num_kv_heads,
     Plan p;
     plan_of(num_chunks, num_kv_heads * (group / heads), width, window_of(window, rows), 0, head_dim, &p);
     *workspace_bytes = workspace_of(num_chunks, num_q_heads * rows, head_dim, p.max_parts);
-    return p.time;
+    // and 4 us for the start and the end of each wave of CTAs, which the choice among cuts does not need
+    return p.time + 4.0 * num_chunks * num_kv_heads * (group / heads) / (4.0 * device_sms());
 }
 
 pa_status decode_fp4_chunks(void *out, const void *query, const void *key_cache, const void *value_cache,
