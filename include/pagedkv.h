@@ -750,7 +750,8 @@ pa_status pa_decode_fp4(void *out, const void *query, const void *key_cache,
  * table, is not computed and flagged PA_DEV_BAD_CONTEXT_LEN.  Of a chunk longer than
  * max_query_len (flagged PA_DEV_BAD_QUERY_LEN) the rows behind it may be left out.
  * A NaN value that a chunk reads may reach all of the chunk's rows.
- * Two or three kernel launches.
+ * num_seqs * W * num_kv_heads * 16 is below 2^31, in either way (PA_ERR_UNSUPPORTED): max_context_len
+ * keeps a wide table's W small.  Two or three kernel launches.
  */
 size_t pa_prefill_fp4_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                       int max_blocks_per_seq, int num_query_tokens,

@@ -9,12 +9,14 @@
 // take two units of a row (a thread one, where rows are not made of pairs of them):
 // they turn the elements, find the scales and the codes, and store 8 bytes of codes and
 // one of scale a unit.  Other CTAs of the launch turn the queries' rows.  8192 tokens of
-// 64 query and 8 KV heads of 128, 321 MB, 57 us (5.6 TB/s, 0.83 of a copy): the query rows take 48
-// alone and the keys and values 25, mostly arithmetic (440 instructions for the 16 elements of each
-// of 32 lanes), which the rows' traffic hides but for some 10.  64 tokens of 32 KV heads 6 us.
+// 64 query and 8 KV heads of 128, 311 MB in bf16, 59 us (5.3 TB/s, 0.78 of a copy): the query rows take 48
+// alone and the keys and values 24, mostly arithmetic (440 instructions for the 16 elements of each
+// of 32 lanes), which the rows' traffic hides but for some 11.  In f32, 613 MB, 99 us (0.92), as neighbours or
+// half of the elements turned 117, not turned 108.  64 tokens of 32 KV heads 6 us.
 //   A key's codes and scale are those of its exact rotation: where a 32-bit value
 // lies so near a border of two codes that its error could cross it (or the largest
-// magnitude so near one of two scales) it is computed again in 64 bits.
+// magnitude so near one of two scales) it is computed again in 64 bits, and so is a whole unit whose
+// pairs could leave f32's range on the way (8192 tokens of 8 KV heads of nothing but infinities: 1.5 ms).
 //
 // Read.  Blocks of the contexts become blocks of bf16 or f32 rows, a warp a tile.  It is
 // bound by memory, four fifths of it the rows that are written: 65536 tokens of 8 KV heads
@@ -193,7 +195,9 @@ __device__ __forceinline__ const T *new_row(const RopeArgs &a, bool value, int64
 // even lane has the first eight elements of each and finds A's scale, the odd one the
 // others and B's.  With halves the units lie rotary_dim / 2 apart, else (and behind
 // rotary_dim) they follow one another.  (Half the registers of a thread with both units: 64 leave
-// the query rows' CTAs of the same kernel 32 warps on an SM.)
+// the query rows' CTAs of the same kernel 32 warps on an SM.  They do not hold everything: by -Xptxas -v the turned
+// kinds keep 172 to 188 bytes a thread in local memory in bf16, 100 to 116 in f32, rows that are not turned 92 and 36;
+// 80 registers and no such bytes took 69 us for the 8192 tokens.)
 template <typename T, int kMode>
 struct Pair {
     static constexpr int N = Vec<T>::N, V = 8 / N;
@@ -477,7 +481,7 @@ __device__ __forceinline__ void encode_tokens(const RopeArgs &a, int cta, float2
 // The query rows of a CTA's tokens where halves are no whole vectors: a lane keeps up to
 // kPairs pairs, those of its number and every 32nd behind it, and goes through the rows; it
 // alone touches their elements, so that rows may be turned in place.  (8192 tokens of 64 heads of
-// 128 of which 94 elements turn: 121 us, by vectors whose partners are read one by one 171.)
+// 128 of which 94 elements turn: 119 us, by vectors whose partners are read one by one 171.)
 template <typename T, int kPairs>
 __device__ __forceinline__ void turn_pair_rows(const RopeArgs &a, int cta, float2 *table) {
     constexpr int kRows = 16 / kPairs;                   // of a warp on their way

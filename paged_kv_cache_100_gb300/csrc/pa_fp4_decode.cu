@@ -15,7 +15,7 @@
 // Few sequences: a context goes to a CTA of 8 or 16 warps, or is cut into parts so that
 // the GPU is full.  Up to eight parts form a thread-block cluster that merges through
 // distributed shared memory; more leave partials in the workspace for a second kernel.
-// Many ragged ones: CTAs take the longest first.
+// Many ragged ones, long for their number: CTAs take the longest first.
 //
 // A prefill of short chunks runs here too: where a group has few heads the columns are those of up
 // to eight rows that follow one another, each of which ends a position later.
@@ -891,7 +891,8 @@ bool plan_of(int num_seqs, int axis, int max_blocks, int window, int partition_s
     // ranking, which adds up with the waves.  In order of length against the table's: 32 heads of their own,
     // contexts of up to 512 tokens, 128 sequences 52.6 us against 47.1, 256 107.7 / 87.4; of up to 2048, 64
     // 68.9 / 75.1, 128 121.0 / 122.9, 192 170.7 / 167.3, 256 228.9 / 215.3; of up to 16384, 64 373 / 443; 8 KV
-    // heads, of up to 1024, 128 26.6 / 28.4, 256 51.1 / 49.6, of up to 4096, 256 121.9 / 133.1.
+    // heads, of up to 1024, 128 26.6 / 28.4, 256 51.1 / 49.6, of up to 4096, 256 121.9 / 133.1.  With heads of 64 and
+    // 256 (25 shapes) it takes the faster order or is within 7% of it.
     // (Nor where CTAs are short: 2048 of one warp on 32 tokens 9.1 us in order of length, 7.8 in theirs.)
     p->ordered = p->warps == 4 && p->cluster == 1 && p->max_parts == 1 && num_seqs > 1 && num_seqs <= kOrdered && ctas > target &&
                  span * target > 20 * ctas;
