@@ -74,9 +74,10 @@ __device__ __noinline__ double exact_top(const RopeArgs &a, const T *row, int64_
 
 // Error of elements turned in 32 bits from pairs of |x0| + |x1| up to `most`: infinite where one of them
 // may leave f32's range on the way, so that the whole unit is found in 64 bits, which no f32 pair leaves.
+// (At least the smallest normal number: products below it round by up to 2^-150, to zero too.)
 __device__ __forceinline__ float turn_error(const RopeArgs &a, float most) {
-    const float f = (float)a.factor;
-    return most * f >= 0x1p127f ? INFINITY : most * (kTurnError * f);
+    const float f = (float)a.factor, e = most * f >= 0x1p127f ? INFINITY : most * (kTurnError * f);
+    return most > 0.f ? fmaxf(e, 0x1p-126f) : e;
 }
 
 // Whether the scale of a unit of largest magnitude amax, off by e, is asked for in 64 bits: the border

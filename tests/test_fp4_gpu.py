@@ -289,6 +289,26 @@ def test_write_flags_the_exact_range(pkv, dim, rot, interleaved):
     assert np.array_equal(status.cpu().numpy() == 256, beyond) and not (status.cpu().numpy() & ~256).any()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,rot,interleaved", [(64, 64, False), (64, 64, True), (64, 20, False)])
+def test_write_of_turned_subnormal_keys(pkv, D, rot, interleaved, dtype):
+    """Keys down to f32's last bit: a unit that is turned into anything but zero has a scale, as one of zeros has none."""
+    g = torch.Generator().manual_seed(rot)
+    T = 200
+    size = torch.exp2(torch.randint(-150, -100, (T, 1, 1), generator=g).double())
+    k = (torch.randn(T, 1, D, generator=g, dtype=torch.float64) * size * (torch.rand(T, 1, D, generator=g) < 0.1)).to(dtype)
+    pos = torch.randint(0, 3000, (T,), generator=g, dtype=torch.int32)
+    rope = pkv.rotary_plan(rot, interleaved=interleaved)
+    blocks = -(-T // 16)
+    kc, vc, status = pkv.fp4_pool(blocks, 1, D), pkv.fp4_pool(blocks, 1, D), _status()
+    pkv.rope_cache_write_fp4(None, k.cuda(), k.cuda(), pos.cuda(), rope, kc, vc, torch.arange(T).cuda(), status=status)
+    ref, _ = R.rotate(k.double().numpy(), *_angles(rope, pos.tolist()), interleaved)
+    zero = torch.zeros(kc.shape, dtype=torch.uint8)
+    _same(vc, _written(zero, k.double().numpy(), range(T)), "values")
+    _same(kc, _written(zero, ref, range(T)), "keys")
+    assert int(status.item()) == 0
+
+
 def test_write_slots(pkv):
     """Slots past the pool are skipped and flagged, negative ones skipped; the query is turned all the same."""
     g = torch.Generator().manual_seed(8)
